@@ -1,6 +1,7 @@
 """Python binding of libbeam_boundary.so: the Beam sublayer-boundary path on one GB300 (sm_103a).
 
-Thin ctypes wrappers with the same names as the C ABI in ``include/beam_boundary.h``.  They only
+Thin ctypes wrappers with the same names as the C ABI in ``include/beam_boundary.h`` (and, in
+``decode.py``, ``include/beam_decode.h``).  They only
 marshal arguments (torch CUDA tensors -> device pointers, shapes, strides, the current stream)
 and raise ``BeamError`` on a non-zero status; every step of the computation runs in the CUDA
 kernels of the library.  There is no CPU fallback: if the library is missing, importing the
@@ -16,7 +17,9 @@ import threading
 
 import torch
 
-from . import _build
+from . import _build, decode
+from .decode import (beam_attn_prefix_fwd, beam_attn_prefix_workspace, beam_kv_evict_fwd,
+                     beam_w4_matvec_fwd)
 
 __all__ = ["BeamError", "build", "lib", "beam_abi_version", "beam_status_str",
            "beam_residual_scales", "beam_rope_cos_sin", "beam_residual_operand",
@@ -25,9 +28,10 @@ __all__ = ["BeamError", "build", "lib", "beam_abi_version", "beam_status_str",
            "beam_boundary_fwd", "beam_moe_combine_boundary_fwd", "beam_allreduce_boundary_fwd",
            "beam_qk_norm_rope_fwd", "beam_qk_norm_ssmax_fwd", "beam_qk_norm_rope_kv_fwd",
            "beam_qk_norm_ssmax_kv_fwd", "beam_grouped_topk_fwd", "beam_attn_gate_fwd",
-           "HEAD_DIM"]
+           "beam_attn_prefix_fwd", "beam_attn_prefix_workspace", "beam_kv_evict_fwd",
+           "beam_w4_matvec_fwd", "HEAD_DIM"]
 
-HEAD_DIM = 128
+HEAD_DIM = decode.HEAD_DIM
 LIB_PATH = _build.LIB_PATH
 
 _lock = threading.Lock()
@@ -94,6 +98,7 @@ def lib() -> ctypes.CDLL:
                        "beam_qk_norm_ssmax_kv_fwd", "beam_grouped_topk_fwd",
                        "beam_attn_gate_fwd"):
                 getattr(so, fn).restype = ctypes.c_int
+            decode.declare(so)
             _lib = so
     return _lib
 
@@ -344,7 +349,7 @@ def beam_qk_norm_ssmax_fwd(q, k, wq, wk, pos, eps: float = 1e-6, ssmax_base: flo
               T, nq, nk, HEAD_DIM, eps, ssmax_base, ssmax_exp, _stream(stream))
 
 
-CACHE_BF16, CACHE_FP8_E4M3 = 0, 1
+CACHE_BF16, CACHE_FP8_E4M3 = decode.CACHE_BF16, decode.CACHE_FP8_E4M3
 
 
 def _kv_common(k, v, slot_mapping, k_cache, v_cache, cache_dtype):

@@ -1,0 +1,318 @@
+"""Attention over the slot cache with a shared prefix against a plain 64-bit computation (needs a
+GB300).  The bounds count half a step of BF16 for the output, half a step of the weights' type for
+each weight, and FP32 sums elsewhere."""
+import math
+
+import pytest
+import torch
+
+import residual_stream_norm_gb300 as rsn
+from tests import _decode_ref as ref
+from tests._gpu import CANARY, Guarded, lib
+
+pytestmark = pytest.mark.gpu
+D = 128
+
+
+def make(B, q_len, n_q, n_kv, P, N, lens, fp8=False, seed=0, extra=7, q_pad=0, spread=1.0):
+    """A case on the CPU: caches with distinct random slots, NaN in every slot that is not listed."""
+    g = torch.Generator().manual_seed(seed)
+    lens = [int(n) for n in lens]
+    inside = [min(max(n, 0), N) for n in lens]
+    total = P + sum(inside)
+    S = total + extra
+    perm = torch.randperm(S, generator=g)
+    prefix = perm[:P].clone()
+    table = torch.full((B, N), -1, dtype=torch.int64)
+    at = P
+    for b, n in enumerate(inside):
+        table[b, :n] = perm[at:at + n]
+        table[b, n:] = perm[total] if extra else -1  # what lies behind a length is never read
+        at += n
+    k = torch.randn((S, n_kv, D), generator=g) * spread
+    v = torch.randn((S, n_kv, D), generator=g)
+    ks, vs = 1.0, 1.0
+    if fp8:
+        ks, vs = 0.05, 0.03
+        k = (k / ks).clamp(-448, 448).to(torch.float8_e4m3fn).view(torch.uint8)
+        v = (v / vs).clamp(-448, 448).to(torch.float8_e4m3fn).view(torch.uint8)
+        k[perm[total:]] = 0x7f
+        v[perm[total:]] = 0xff
+    else:
+        k, v = k.bfloat16(), v.bfloat16()
+        k[perm[total:]] = math.nan
+        v[perm[total:]] = math.nan
+    q = torch.randn((B * q_len, n_q + q_pad, D), generator=g).bfloat16()[:, :n_q]
+    return dict(q=q, k=k, v=v, prefix=prefix, table=table,
+                lens=torch.tensor(lens, dtype=torch.int32), q_len=q_len, ks=ks, vs=vs, fp8=fp8)
+
+
+def run(c, window=0, weights=False, weight_in=None, sm_scale=None, out=None):
+    B, N = c["table"].shape
+    T, n_q, _ = c["q"].shape
+    n_kv, P = c["k"].shape[1], c["prefix"].numel()
+    dev = {x: c[x].cuda() for x in ("k", "v", "prefix", "table", "lens")}
+    q = torch.empty_strided(c["q"].shape, c["q"].stride(), dtype=torch.bfloat16, device="cuda")
+    q.copy_(c["q"])
+    if out is None:
+        out = Guarded((T, n_q, D))
+    lse = Guarded((T, n_q), dtype=torch.float32)
+    w = Guarded((B, N), dtype=torch.float32) if weights else None
+    w_in = None if weight_in is None else weight_in.cuda()
+    n = rsn.beam_attn_prefix_workspace(B, c["q_len"], n_q, n_kv, P, N, window, weights)
+    # a workspace that holds NaN: nothing in it may be taken for data
+    workspace = torch.full((n // 4 + 64,), math.nan, dtype=torch.float32, device="cuda")
+    workspace[n // 4:] = CANARY
+    used = workspace[:n // 4].view(torch.uint8)
+    rsn.beam_attn_prefix_fwd(
+        out.view, q, dev["k"], dev["v"], dev["prefix"], dev["table"], dev["lens"], used,
+        cache_dtype=rsn.CACHE_FP8_E4M3 if c["fp8"] else rsn.CACHE_BF16, k_scale=c["ks"],
+        v_scale=c["vs"], sm_scale=sm_scale, window=window, lse_out=lse.view,
+        key_weight_out=None if w is None else w.view, key_weight_in=w_in)
+    torch.cuda.synchronize()
+    for x in (out, lse, w):
+        if x is not None:
+            x.check()
+    assert bool((workspace[n // 4:] == CANARY).all()), "workspace overrun"
+    return out.view.cpu(), lse.view.cpu(), None if w is None else w.view.cpu()
+
+
+def check(c, window=0, weights=False, weight_in=None, sm_scale=None):
+    got = run(c, window, weights, weight_in, sm_scale)
+    want, tol = ref.attention(c["q"], c["k"], c["v"], c["prefix"], c["table"], c["lens"],
+                              c["q_len"], c["ks"], c["vs"], sm_scale, window, weight_in, c["fp8"])
+    for name, x, y, e in zip(("out", "lse", "weights"), got, want, tol):
+        if x is None:
+            continue
+        x = x.double()
+        inf = torch.isinf(y)
+        assert bool((x[inf] == y[inf]).all()), name
+        d = (x - y).abs()[~inf]
+        bad = d > e[~inf]
+        assert not bool(bad.any()) and bool(torch.isfinite(d).all()), \
+            f"{name}: {int(bad.sum())} of {bad.numel()} off, worst {float(d.max()):.3g}"
+    return got
+
+
+CASES = [
+    # B, q_len, n_q, n_kv, P, N, lens
+    (1, 1, 1, 1, 0, 1, [1]),                      # one key
+    (1, 1, 6, 1, 0, 15, [15]),
+    (1, 1, 48, 8, 0, 17, [17]),
+    (2, 1, 6, 1, 1, 64, [64, 63]),
+    (3, 1, 12, 2, 63, 65, [65, 1, 33]),
+    (2, 1, 8, 8, 64, 130, [130, 127]),            # a KV head of its own for each query head
+    (2, 1, 16, 1, 65, 200, [200, 77]),            # 16 rows a unit
+    (1, 1, 40, 2, 129, 300, [300]),               # 20 query heads share a KV head
+    (4, 1, 6, 1, 1000, 90, [0, 5, -3, 90]),       # padded sequences: rows that see nothing
+    (2, 2, 6, 1, 0, 40, [1, 40]),                 # the first of two queries sees nothing
+    (3, 4, 6, 1, 100, 70, [70, 4, 3]),
+    (2, 7, 10, 2, 33, 50, [50, 8]),
+    (1, 17, 6, 2, 40, 80, [80]),
+    (2, 1, 6, 1, 50, 20, [25, 7]),                # a length past the table is limited to it
+    (2, 1, 6, 1, 50, 0, [0, 0]),                  # no table at all
+    (40, 1, 6, 1, 200, 9, list(range(1, 10)) * 4 + [9] * 4),  # many rows on the prefix
+    (1, 1, 6, 1, 0, 3000, [2999]),                # many parts of one list
+]
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("case", CASES)
+def test_sizes(case, fp8):
+    lib()
+    B, q_len, n_q, n_kv, P, N, lens = case
+    check(make(B, q_len, n_q, n_kv, P, N, lens, fp8=fp8, seed=B + N), weights=N > 0)
+
+
+@pytest.mark.parametrize("window", [1, 2, 16, 63, 64, 65, 200, 10 ** 12])
+@pytest.mark.parametrize("P", [0, 100])
+def test_windows(P, window):
+    lib()
+    check(make(3, 3, 6, 1, P, 150, [150, 70, 2], seed=window % 1000), window=window, weights=True)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_bad_slots_are_not_seen(fp8):
+    lib()
+    c = make(3, 1, 6, 2, 70, 100, [100, 40, 30], fp8=fp8, seed=3)
+    S = c["k"].shape[0]
+    c["prefix"][::7] = -1
+    c["prefix"][3] = S
+    c["table"][0, ::3] = -1
+    c["table"][1, :40] = S + 5              # a sequence that sees prefix keys only
+    c["table"][2, 5] = 2 ** 40
+    c["table"][2, 6] = -2 ** 62
+    check(c, weights=True)
+    c["prefix"][:] = -1                     # and one that sees nothing at all
+    out, lse, w = check(c, weights=True)
+    assert bool((out[1] == 0).all()) and bool((lse[1] == -math.inf).all())
+
+
+def test_accumulates_weights_in_place_and_strided():
+    lib()
+    c = make(2, 1, 12, 2, 30, 50, [50, 20], seed=5)
+    w0 = torch.rand((2, 50))
+    want, tol = ref.attention(c["q"], c["k"], c["v"], c["prefix"], c["table"], c["lens"], 1,
+                              weight_in=w0)
+    _, _, w = check(c, weights=True, weight_in=w0)
+    assert torch.equal(w[1, 20:], w0[1, 20:])          # what lies behind a length is only copied
+    wide = torch.zeros((2, 80), device="cuda")
+    wide[:, :50] = w0.cuda()
+    table = torch.full((2, 64), 2 ** 50, dtype=torch.int64, device="cuda")
+    table[:, :50] = c["table"].cuda()
+    n = rsn.beam_attn_prefix_workspace(2, 1, 12, 2, 30, 50, 0, True)
+    out = torch.empty_like(c["q"], device="cuda")
+    rsn.beam_attn_prefix_fwd(out, c["q"].cuda(), c["k"].cuda(), c["v"].cuda(), c["prefix"].cuda(),
+                             table[:, :50], c["lens"].cuda(),
+                             torch.empty(n, dtype=torch.uint8, device="cuda"),
+                             key_weight_in=wide[:, :50], key_weight_out=wide[:, :50])
+    torch.cuda.synchronize()
+    assert torch.equal(wide[:, :50].cpu(), w)
+    assert bool((wide[:, 50:] == 0).all())
+
+
+def test_strided_query_and_output_rows():
+    lib()
+    c = make(3, 2, 6, 1, 40, 60, [60, 33, 2], seed=6, q_pad=3)
+    assert not c["q"].is_contiguous()
+    plain = check(c)[0]
+    wide = Guarded((6, 9, D))
+    view = wide.view
+    wide.view = view[:, 1:7]
+    got = run(c, out=wide)[0]
+    assert torch.equal(got, plain)
+    assert bool((view[:, 0] == CANARY).all()) and bool((view[:, 7:] == CANARY).all())
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_peaked_scores_and_scales(fp8):
+    # scores up to several hundred: one key takes nearly all the weight
+    lib()
+    c = make(2, 1, 12, 2, 130, 140, [140, 90], fp8=fp8, seed=8, spread=8.0)
+    check(c, weights=True, sm_scale=1.0)
+    check(c, sm_scale=-0.3)
+    check(c, sm_scale=0.0)
+
+
+def test_fp8_query_range():
+    # rows of very large, very small and zero queries: the FP16 scaling is by row
+    lib()
+    c = make(4, 1, 6, 1, 20, 30, [30, 30, 12, 1], fp8=True, seed=9)
+    c["q"][0] *= 2.0 ** 100
+    c["q"][1] *= 2.0 ** -100
+    c["q"][2] = 0
+    check(c, sm_scale=2.0 ** -100)
+    c["q"][0] *= 2.0 ** -100
+    check(c, sm_scale=0.1)
+
+
+def test_non_finite_inputs_stay_in_their_rows():
+    lib()
+    c = make(3, 1, 6, 1, 40, 50, [50, 50, 50], seed=10)
+    clean = run(c)[0]
+    c["k"][c["table"][0, 3], 0, 5] = math.nan
+    c["v"][c["table"][1, 7], 0, 9] = math.inf
+    out, lse, _ = run(c)
+    assert bool(torch.isnan(out[0]).all()) and bool(torch.isnan(lse[0]).all())
+    assert bool((out[1, :, 9] == math.inf).all())
+    assert torch.equal(out[1, :, :9], clean[1, :, :9]) and torch.equal(out[2], clean[2])
+
+
+def test_values_of_unseen_keys_do_not_matter():
+    # a later token's or an out-of-window key's value may be NaN or infinite
+    lib()
+    c = make(2, 4, 6, 1, 30, 60, [60, 45], seed=11)
+    clean = run(c, window=20)[0]
+    for b, n in ((0, 60), (1, 45)):
+        c["v"][c["table"][b, n - 1], 0] = math.nan   # the last token: seen by the last query only
+        c["v"][c["table"][b, n - 2], 0, 3] = -math.inf
+        c["v"][c["table"][b, n - 23], 0] = math.nan  # out of the window of the last query only
+    out = run(c, window=20)[0].view(2, 4, 6, D)
+    clean = clean.view(2, 4, 6, D)
+    assert torch.equal(out[:, 1], clean[:, 1])
+    assert bool(torch.isnan(out[:, 3]).all()) and bool(torch.isnan(out[:, 0]).all())
+    assert bool((out[:, 2, :, 3] == -math.inf).all())
+    assert torch.equal(out[:, 2, :, 4:], clean[:, 2, :, 4:])
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_many_rows_on_a_long_prefix(fp8):
+    # above the switch to the kernel for many prefix rows, with ragged row and key tiles
+    lib()
+    for B, q_len, n_q, n_kv, P, window in ((43, 1, 6, 1, 1000, 0), (90, 1, 6, 1, 517, 0),
+                                           (13, 5, 12, 2, 700, 0), (30, 2, 6, 1, 300, 150)):
+        lens = [1 + (7 * b) % 11 for b in range(B)]
+        check(make(B, q_len, n_q, n_kv, P, 11, lens, fp8=fp8, seed=P), window=window, weights=True)
+
+
+def test_same_bits_every_time_and_on_another_stream():
+    lib()
+    c = make(20, 1, 48, 8, 500, 200, [200 - 9 * b for b in range(20)], seed=13)
+    first = run(c, weights=True)
+    for _ in range(3):
+        again = run(c, weights=True)
+        assert all(torch.equal(x, y) for x, y in zip(first, again))
+    s = torch.cuda.Stream()
+    with torch.cuda.stream(s):
+        again = run(c, weights=True)
+    assert all(torch.equal(x, y) for x, y in zip(first, again))
+
+
+def test_graph_replay_reads_the_lengths_anew():
+    lib()
+    c = make(4, 1, 6, 1, 100, 80, [80, 80, 80, 80], seed=14)
+    want_full = run(c)[0]
+    dev = {x: c[x].cuda() for x in ("q", "k", "v", "prefix", "table", "lens")}
+    out = torch.zeros_like(dev["q"])
+    n = rsn.beam_attn_prefix_workspace(4, 1, 6, 1, 100, 80)
+    ws = torch.empty(n, dtype=torch.uint8, device="cuda")
+
+    def call():
+        rsn.beam_attn_prefix_fwd(out, dev["q"], dev["k"], dev["v"], dev["prefix"], dev["table"],
+                                 dev["lens"], ws)
+    call()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call()
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out.cpu(), want_full)
+    c["lens"] = torch.tensor([1, 17, 0, 64], dtype=torch.int32)
+    want = run(c)[0]
+    dev["lens"].copy_(c["lens"])
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out.cpu(), want)
+
+
+def test_cache_offsets_past_32_bits():
+    lib()
+    S = 2_200_000                                     # 4.5 GB a cache
+    k = torch.zeros((S, 8, D), dtype=torch.bfloat16, device="cuda")
+    v = torch.zeros_like(k)
+    c = make(2, 1, 48, 8, 50, 40, [40, 23], seed=15, extra=1)
+    n = c["k"].shape[0]
+    k[-n:] = c["k"].cuda()
+    v[-n:] = c["v"].cuda()
+    want = run(c)[0]
+    out = torch.empty_like(want, device="cuda")
+    ws = torch.empty(rsn.beam_attn_prefix_workspace(2, 1, 48, 8, 50, 40), dtype=torch.uint8,
+                     device="cuda")
+    rsn.beam_attn_prefix_fwd(out, c["q"].cuda(), k, v, (c["prefix"] + S - n).cuda(),
+                             (c["table"] + S - n).cuda(), c["lens"].cuda(), ws)
+    torch.cuda.synchronize()
+    assert torch.equal(out.cpu(), want)
+
+
+def test_zero_sequences():
+    lib()
+    e = torch.empty
+    rsn.beam_attn_prefix_fwd(
+        e((0, 6, D), dtype=torch.bfloat16, device="cuda"),
+        e((0, 6, D), dtype=torch.bfloat16, device="cuda"),
+        e((3, 1, D), dtype=torch.bfloat16, device="cuda"),
+        e((3, 1, D), dtype=torch.bfloat16, device="cuda"), None,
+        e((0, 4), dtype=torch.int64, device="cuda"), e((0,), dtype=torch.int32, device="cuda"),
+        e((1,), dtype=torch.uint8, device="cuda"))
+    torch.cuda.synchronize()
