@@ -7,11 +7,12 @@
 //
 // Rows kernel: a warp works on 16 keys at a time for 8 or 16 query rows of one KV head.  It computes
 // the transposed products S^T = K Q^T and O^T = V^T P^T, so that the keys fill the 16 rows of the
-// matrix instruction and the few query rows its 8 columns.  Each warp copies its own keys (cp.async,
-// a gather by slot) into its own stages, so warps meet only when their parts are joined.
+// matrix instruction and the few query rows its 8 columns.  Each warp copies its own keys into its own
+// stages (TMA gathers of four slots' rows each), so warps meet only when their parts are joined.
 
 #include "decode_kernels.h"
 #include "decode_mma.cuh"
+#include "decode_tma.cuh"
 
 namespace beam {
 namespace {
@@ -19,30 +20,38 @@ namespace {
 constexpr int kD = 128;
 constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
-constexpr int kWarpKeys = 16;
-constexpr int kTileKeys = kWarps * kWarpKeys;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
+// A stage holds the keys and values of one step of a warp: rows of 128 bytes with their 16-byte chunks
+// exchanged by the copy (chunk c of row r at c ^ (r % 8)), so that ldmatrix finds eight rows' same
+// chunk in eight different bank groups.  BF16: 16 keys, the two halves of a head one after the other;
+// FP8: 32 keys.
 template <bool FP8>
 struct RowsConfig {
-    static constexpr int kRow = FP8 ? 128 : 256;          // bytes of a cache row of one head
-    static constexpr int kChunks = kRow / 16;
-    static constexpr int kStages = FP8 ? 4 : 3;
-    static constexpr int kTileBytes = kWarpKeys * kRow;   // keys or values of a stage
-    static constexpr int kWarpBytes = kStages * 2 * kTileBytes;
-    static constexpr int kCtasPerSm = FP8 ? 3 : 2;
-    static constexpr int kSmem = kWarps * kWarpBytes;
+    static constexpr int kMt = FP8 ? 2 : 1;       // 16-key tiles of a step
+    static constexpr int kKeys = 16 * kMt;
+    static constexpr int kTileKeys = kWarps * kKeys;
+    static constexpr int kHalf = 16 * 128;        // BF16: bytes of 16 keys' half heads
+    static constexpr int kValues = 4096;          // where the stage's values start
+    static constexpr int kStageBytes = 8192;
+    static constexpr int kStages = 3;
+    static constexpr int kWarpBytes = kStages * kStageBytes;
 };
 
-// Where the 16-byte chunk of a key lies in its row of shared memory: eight keys' same chunk fall into
-// eight different bank groups (ldmatrix); for FP8 an even and an odd key's chunks 0..3 do as well
-// (the 16-byte loads of the keys).
-template <bool FP8>
-__device__ __forceinline__ int swizzle(int key, int chunk)
-{
-    return FP8 ? chunk ^ (((key & 1) << 2) | ((key >> 1) & 3)) : chunk ^ (key & 7);
-}
+// Shared memory of the rows kernel: the stages, two join buffers, then the small arrays.
+template <int NT>
+struct RowsSmem {
+    static constexpr int kStagesEnd = kWarps * RowsConfig<false>::kWarpBytes;
+    static constexpr int kJoinBytes = 8 * NT * kD * 4;
+    static constexpr int kMl = kStagesEnd + 2 * kJoinBytes;          // float2 [kWarps][8 NT]
+    static constexpr int kBars = kMl + kWarps * 8 * NT * 8;          // uint64_t [kWarps][kStages]
+    static constexpr int kScan = kBars + kWarps * RowsConfig<false>::kStages * 8;  // int64_t [kWarps + 2]
+    static constexpr int kFail = kScan + (kWarps + 2) * 8;           // int
+    static constexpr int kBytes = kFail + 8;
+};
+
+__device__ unsigned int g_decode_fault_word = 0u;
 
 // The block whose share [c tot / C, (c + 1) tot / C) contains tile x (C <= tot).
 __device__ __forceinline__ int64_t owner(int64_t x, int64_t tot, int64_t ctas)
@@ -63,10 +72,10 @@ __device__ __forceinline__ int64_t seq_len(const AttnArgs &a, int64_t b)
     return n < 0 ? 0 : (n > a.width ? a.width : n);
 }
 
-__device__ __forceinline__ int64_t seq_tiles(const AttnArgs &a, int64_t b)
+__device__ __forceinline__ int64_t seq_tiles(const AttnArgs &a, const AttnPlan &p, int64_t b)
 {
     const int64_t n = seq_len(a, b);
-    return (n - first_key(n, a.q_len, a.window) + kTileKeys - 1) / kTileKeys;
+    return (n - first_key(n, a.q_len, a.window) + p.tile_keys - 1) / p.tile_keys;
 }
 
 // Factor 2^k that brings a row of largest magnitude bits `mx` (FP32) to [2^14, 2^15), and its
@@ -80,35 +89,39 @@ __device__ __forceinline__ void f16_row_factor(uint32_t mx, float &f, float &inv
     inv = __uint_as_float((uint32_t)(127 - k) << 23);
 }
 
-// The A fragment of V^T for 16 elements d (tile mt) and the 16 keys of a stage.  FP8: 16-bit units of
-// the transposed load are pairs (d, d + 1); after the split, matrix row g is element 2g of the 16
-// and row g + 8 element 2g + 1.
-template <bool FP8>
-__device__ __forceinline__ void load_values(uint32_t (&af)[4], uint32_t vt, int mt, int lane)
+// The A fragments of V^T for 16 elements d and 16 keys.  BF16 (`mt`: which 16 elements): matrix row is
+// d.  FP8: one load gives two fragments (mt, mt + 1; mt even), whose 16-bit units are pairs (d, d + 1);
+// after the split, matrix row g is element 2g of the 16 and row g + 8 element 2g + 1.
+__device__ __forceinline__ void load_values_bf16(uint32_t (&af)[4], uint32_t vt, int mt, int lane)
 {
-    using C = RowsConfig<FP8>;
-    if constexpr (!FP8) {
-        const int key = (lane >> 4) * 8 + (lane & 7), ch = 2 * mt + ((lane >> 3) & 1);
-        ldmatrix_x4_trans(af, vt + key * C::kRow + 16 * swizzle<FP8>(key, ch));
-    } else {
-        uint32_t r[4];
-        const int key = lane & 15, ch = (mt & ~1) + (lane >> 4);
-        ldmatrix_x4_trans(r, vt + key * C::kRow + 16 * swizzle<FP8>(key, ch));
-        const uint32_t r0 = mt & 1 ? r[2] : r[0], r1 = mt & 1 ? r[3] : r[1];
-        const uint32_t x0 = e4m3x2_to_f16x2(r0), x1 = e4m3x2_to_f16x2(r0 >> 16);
-        const uint32_t y0 = e4m3x2_to_f16x2(r1), y1 = e4m3x2_to_f16x2(r1 >> 16);
-        af[0] = __byte_perm(x0, x1, 0x5410), af[1] = __byte_perm(x0, x1, 0x7632);
-        af[2] = __byte_perm(y0, y1, 0x5410), af[3] = __byte_perm(y0, y1, 0x7632);
-    }
+    const int key = (lane >> 4) * 8 + (lane & 7), ch = 2 * mt + ((lane >> 3) & 1);
+    ldmatrix_x4_trans(af, vt + (ch >> 3) * RowsConfig<false>::kHalf + key * 128 +
+                              16 * ((ch & 7) ^ (key & 7)));
+}
+
+__device__ __forceinline__ void load_values_fp8(uint32_t (&a0)[4], uint32_t (&a1)[4], uint32_t vt,
+                                                int mt, int lane)
+{
+    uint32_t r[4];
+    const int key = lane & 15, ch = mt + (lane >> 4);
+    ldmatrix_x4_trans(r, vt + key * 128 + 16 * (ch ^ (key & 7)));
+    uint32_t x0 = e4m3x2_to_f16x2(r[0]), x1 = e4m3x2_to_f16x2(r[0] >> 16);
+    uint32_t y0 = e4m3x2_to_f16x2(r[1]), y1 = e4m3x2_to_f16x2(r[1] >> 16);
+    a0[0] = __byte_perm(x0, x1, 0x5410), a0[1] = __byte_perm(x0, x1, 0x7632);
+    a0[2] = __byte_perm(y0, y1, 0x5410), a0[3] = __byte_perm(y0, y1, 0x7632);
+    x0 = e4m3x2_to_f16x2(r[2]), x1 = e4m3x2_to_f16x2(r[2] >> 16);
+    y0 = e4m3x2_to_f16x2(r[3]), y1 = e4m3x2_to_f16x2(r[3] >> 16);
+    a1[0] = __byte_perm(x0, x1, 0x5410), a1[1] = __byte_perm(x0, x1, 0x7632);
+    a1[2] = __byte_perm(y0, y1, 0x5410), a1[3] = __byte_perm(y0, y1, 0x7632);
 }
 
 // Whether a stage's values hold an infinity or NaN (E4M3 has NaN only: all bits but the sign set).
 template <bool FP8>
-__device__ __forceinline__ bool tile_has_nonfinite(uint32_t vt, int lane)
+__device__ __forceinline__ bool stage_has_nonfinite(uint32_t vt, int lane)
 {
     bool bad = false;
 #pragma unroll 1
-    for (int i = lane; i < RowsConfig<FP8>::kTileBytes / 16; i += 32) {
+    for (int i = lane; i < 256; i += 32) {
         const uint4 v = lds128(vt + 16 * i);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
@@ -122,7 +135,7 @@ __device__ __forceinline__ bool tile_has_nonfinite(uint32_t vt, int lane)
     return __any_sync(0xffffffffu, bad);
 }
 
-// Row rr (of `rows`, per KV head): token and head of it.
+// Row rr (of `rows`, per KV head): its token; the query's index and the head within the group.
 __device__ __forceinline__ int64_t row_token(const AttnArgs &a, const AttnPlan &p, int64_t rr,
                                              int &i, int &hg)
 {
@@ -133,31 +146,80 @@ __device__ __forceinline__ int64_t row_token(const AttnArgs &a, const AttnPlan &
     return (int64_t)b * a.q_len + i;
 }
 
-template <int NT, bool FP8>
-__global__ void __launch_bounds__(kThreads, RowsConfig<FP8>::kCtasPerSm)
-    attn_rows_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ AttnPlan p)
-{
-    using C = RowsConfig<FP8>;
-    constexpr int M = 8 * NT;
-    extern __shared__ __align__(128) char smem[];
-    __shared__ int64_t s_start[3];  // sequence of the first tile, its first tile, all tiles
-    __shared__ float2 s_ml[kWarps][M];
-    __shared__ int64_t s_scan[kWarps + 1];
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int g = lane >> 2, t = lane & 3;
-    const uint32_t wbuf = smem_addr(smem) + warp * C::kWarpBytes;
-    pdl_launch_dependents();
-    pdl_wait();
+// Position in the units' sequence of key tiles.
+struct Cursor {
+    int64_t tile, end;    // the next tile of the share, and the share's end
+    int64_t b, b_start;   // sequence of `tile` (past the prefix), its first tile
+};
 
-    // ---- the share of this block ---------------------------------------------------------------
-    const int64_t p_units = a.n_kv * p.p_rtiles;
-    const int64_t p_total = p_units * p.p_tiles;
+// A unit's part that lies in the share.
+struct Unit {
+    const int64_t *list;
+    int64_t unit;
+    int32_t kvh;
+    int32_t row0, row_end;
+    int32_t k0, k1;       // keys of the part
+    int32_t key_end;      // of the list
+    bool prefix, whole;
+};
+
+__device__ __forceinline__ Unit next_unit(const AttnArgs &a, const AttnPlan &p, int M, Cursor &c)
+{
+    Unit u;
+    const int64_t p_units = a.n_kv * p.p_rtiles, p_total = p_units * p.p_tiles;
     const int64_t per_seq = (int64_t)a.n_kv * p.s_rtiles;
-    int64_t *cum = reinterpret_cast<int64_t *>(a.workspace + p.cum_off);
-    int64_t total = p_total;
-    for (int64_t b0 = 0; b0 < a.B; b0 += kThreads) {  // the sum over the sequences
+    int64_t start, tiles;
+    int32_t key_first;
+    u.prefix = c.tile < p_total;
+    if (u.prefix) {
+        u.unit = c.tile / p.p_tiles;
+        tiles = p.p_tiles;
+        start = u.unit * tiles;
+        u.kvh = (int32_t)(u.unit / p.p_rtiles);
+        u.row0 = (int32_t)(u.unit - u.kvh * p.p_rtiles) * M;
+        u.row_end = (int32_t)p.rows;
+        u.list = a.prefix;
+        key_first = (int32_t)p.p_first;
+        u.key_end = (int32_t)a.n_prefix;
+    } else {
+        tiles = seq_tiles(a, p, c.b);
+        while (c.tile >= c.b_start + per_seq * tiles) {
+            c.b_start += per_seq * tiles;
+            tiles = seq_tiles(a, p, ++c.b);
+        }
+        const int64_t x = (c.tile - c.b_start) / tiles;
+        u.unit = p_units + c.b * per_seq + x;
+        start = c.b_start + x * tiles;
+        u.kvh = (int32_t)(x / p.s_rtiles);
+        u.row0 = (int32_t)(c.b * p.R + (x - (int64_t)u.kvh * p.s_rtiles) * M);
+        u.row_end = (int32_t)((c.b + 1) * p.R);
+        u.list = a.table + c.b * a.table_stride;
+        u.key_end = (int32_t)seq_len(a, c.b);
+        key_first = (int32_t)first_key(u.key_end, a.q_len, a.window);
+    }
+    const int64_t seg_end = min(c.end, start + tiles);
+    u.whole = c.tile == start && seg_end == start + tiles;
+    u.k0 = key_first + (int32_t)(c.tile - start) * p.tile_keys;
+    u.k1 = (int32_t)min((int64_t)u.key_end, key_first + (seg_end - start) * p.tile_keys);
+    c.tile = seg_end;
+    return u;
+}
+
+// The sum over the sequences of their units' tiles after `base`; every thread of the block takes
+// part.  find >= base: also finds the sequence that holds tile `find`.  cum (or nullptr) receives the
+// running sums.
+__device__ __forceinline__ int64_t scan_sequences(const AttnArgs &a, const AttnPlan &p, int64_t base,
+                                                  int64_t find, int64_t *cum, int64_t *s_scan)
+{
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int64_t per_seq = (int64_t)a.n_kv * p.s_rtiles;
+    int64_t total = base;
+    if (cum && tid == 0)
+        cum[0] = base;
+    for (int64_t b0 = 0; b0 < a.B; b0 += kThreads) {
         const int64_t b = b0 + tid;
-        int64_t v = b < a.B ? per_seq * seq_tiles(a, b) : 0;
+        const int64_t own = b < a.B ? per_seq * seq_tiles(a, p, b) : 0;
+        int64_t v = own;
 #pragma unroll
         for (int off = 1; off < 32; off <<= 1) {
             const int64_t o = __shfl_up_sync(0xffffffffu, v, off);
@@ -168,106 +230,145 @@ __global__ void __launch_bounds__(kThreads, RowsConfig<FP8>::kCtasPerSm)
             s_scan[warp] = v;
         __syncthreads();
         int64_t before = 0, sum = 0;
+#pragma unroll
         for (int w = 0; w < kWarps; ++w) {
             before += w < warp ? s_scan[w] : 0;
             sum += s_scan[w];
         }
-        if (blockIdx.x == 0 && b < a.B)
-            cum[b + 1] = total + before + v;
+        const int64_t end = total + before + v;
+        if (cum && b < a.B)
+            cum[b + 1] = end;
+        if (find >= end - own && find < end) {
+            s_scan[kWarps] = b;
+            s_scan[kWarps + 1] = end - own;
+        }
         total += sum;
         __syncthreads();
+        if (find >= base && find < total)
+            break;
     }
-    if (blockIdx.x == 0 && tid == 0)
-        cum[0] = p_total;
+    return total;
+}
+
+template <int NT, bool FP8, bool WEIGHTS>
+__global__ void __launch_bounds__(kThreads, 2)
+    attn_rows_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ AttnPlan p,
+                     const __grid_constant__ CacheMaps maps)
+{
+    using C = RowsConfig<FP8>;
+    using S = RowsSmem<NT>;
+    constexpr int M = 8 * NT, MT = C::kMt;
+    extern __shared__ __align__(1024) char smem[];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int g = lane >> 2, t = lane & 3;
+    const uint32_t wbuf = smem_addr(smem) + warp * C::kWarpBytes;
+    float2 *s_ml = reinterpret_cast<float2 *>(smem + S::kMl);
+    uint64_t *bars = reinterpret_cast<uint64_t *>(smem + S::kBars) + warp * C::kStages;
+    int64_t *s_scan = reinterpret_cast<int64_t *>(smem + S::kScan);
+    volatile int *s_fail = reinterpret_cast<int *>(smem + S::kFail);
+    if (tid == 0)
+        *s_fail = smem_addr(smem) % 1024 != 0;  // the copies' exchange of chunks goes by address
+    if (lane == 0) {
+        for (int i = 0; i < C::kStages; ++i)
+            mbar_init(&bars[i], 1);
+        fence_mbar_init();
+        prefetch_map(&maps.k);
+        prefetch_map(&maps.v);
+    }
+    __syncwarp();
+    pdl_launch_dependents();
+    pdl_wait();
+
+    // ---- the share of this block ---------------------------------------------------------------
+    const int64_t p_units = a.n_kv * p.p_rtiles;
+    const int64_t p_total = p_units * p.p_tiles;
+    int64_t *cum = reinterpret_cast<int64_t *>(a.workspace + p.cum_off);
+    const int64_t total =
+        scan_sequences(a, p, p_total, -1, blockIdx.x == 0 ? cum : nullptr, s_scan);
     const int64_t shares = min((int64_t)p.ctas, total);  // none of them empty
-    if (blockIdx.x >= shares)
+    __syncthreads();
+    if (blockIdx.x >= shares || *s_fail)
         return;
-    int64_t tile = total * blockIdx.x / shares;
-    const int64_t tile_end = total * (blockIdx.x + 1) / shares;
-    int64_t b = 0, b_start = p_total;  // sequence of `tile` (once past the prefix), its first tile
-    if (tile >= p_total) {
-        int64_t run = p_total;
-        for (int64_t b0 = 0; b0 < a.B; b0 += kThreads) {
-            const int64_t bb = b0 + tid;
-            const int64_t own = bb < a.B ? per_seq * seq_tiles(a, bb) : 0;
-            int64_t v = own;
-#pragma unroll
-            for (int off = 1; off < 32; off <<= 1) {
-                const int64_t o = __shfl_up_sync(0xffffffffu, v, off);
-                if (lane >= off)
-                    v += o;
-            }
-            if (lane == 31)
-                s_scan[warp] = v;
-            __syncthreads();
-            int64_t before = 0, sum = 0;
-            for (int w = 0; w < kWarps; ++w) {
-                before += w < warp ? s_scan[w] : 0;
-                sum += s_scan[w];
-            }
-            const int64_t end = run + before + v;
-            if (tile >= end - own && tile < end) {
-                s_start[0] = bb;
-                s_start[1] = end - own;
-            }
-            run += sum;
-            __syncthreads();
-            if (tile < run)
-                break;
-        }
-        b = s_start[0];
-        b_start = s_start[1];
+    Cursor at{total * blockIdx.x / shares, total * (blockIdx.x + 1) / shares, 0, p_total};
+    if (at.tile >= p_total) {
+        scan_sequences(a, p, p_total, at.tile, nullptr, s_scan);
+        at.b = s_scan[kWarps];
+        at.b_start = s_scan[kWarps + 1];
     }
+
+    // ---- the copies: this warp's steps of every unit of the share, ahead of the arithmetic -----------
+    Cursor ahead = at;
+    Unit lu;
+    int ls = 0, lsteps = 0, slot = -1;
+    auto steps_of = [&](const Unit &u) {
+        return (u.k1 - u.k0 - warp * C::kKeys + C::kTileKeys - 1) / C::kTileKeys;
+    };
+    auto fetch_slot = [&]() {  // lane i: slot of the next step's key i, or -1
+        while (ls >= lsteps && ahead.tile < ahead.end) {
+            lu = next_unit(a, p, M, ahead);
+            ls = 0;
+            lsteps = steps_of(lu);
+        }
+        slot = -1;
+        const int key = lu.k0 + ls * C::kTileKeys + warp * C::kKeys + lane;
+        if (ls < lsteps && lane < C::kKeys && key < lu.k1) {
+            const int64_t x = lu.list[key];
+            slot = x >= 0 && x < a.num_slots ? (int)x : -1;
+        }
+    };
+    uint32_t masks[C::kStages];  // which keys of the stages in flight exist; the newest first
+#pragma unroll
+    for (int i = 0; i < C::kStages; ++i)
+        masks[i] = 0;
+    int in_stage = 0;
+    bool failed = false;  // a wait of this warp ran out: it copies nothing more
+    auto issue = [&]() {
+        const bool have = ls < lsteps && !failed;
+#pragma unroll
+        for (int i = C::kStages - 1; i > 0; --i)
+            masks[i] = masks[i - 1];
+        masks[0] = __ballot_sync(0xffffffffu, slot >= 0);
+        if (have) {
+            const uint32_t dst = wbuf + in_stage * C::kStageBytes;
+            // lanes 0..15: four keys each of K or V; a slot of -1 is out of the map and gives zeros
+            const int grp = FP8 ? lane & 7 : lane & 3, half = FP8 ? 0 : (lane >> 2) & 1;
+            const int isv = (lane >> 3) & 1;
+            const int y0 = __shfl_sync(0xffffffffu, slot, 4 * grp);
+            const int y1 = __shfl_sync(0xffffffffu, slot, 4 * grp + 1);
+            const int y2 = __shfl_sync(0xffffffffu, slot, 4 * grp + 2);
+            const int y3 = __shfl_sync(0xffffffffu, slot, 4 * grp + 3);
+            if (lane == 0)
+                mbar_arrive_expect_tx(&bars[in_stage], C::kStageBytes);
+            __syncwarp();
+            if (lane < 16)
+                gather4(dst + isv * C::kValues + half * C::kHalf + grp * 512,
+                        isv ? &maps.v : &maps.k, lu.kvh * kD + half * 64, y0, y1, y2, y3,
+                        &bars[in_stage]);
+            ++ls;
+        }
+        in_stage = in_stage + 1 == C::kStages ? 0 : in_stage + 1;
+        fetch_slot();
+    };
+    fetch_slot();
+#pragma unroll
+    for (int i = 0; i < C::kStages - 1; ++i)
+        issue();
+    int out_stage = 0, phase = 0;
 
     // ---- the units of the share ----------------------------------------------------------------
-    while (tile < tile_end) {
-        int64_t unit, unit_start, unit_tiles, key_first, key_end, row0, row_end;
-        int kvh;
-        const int64_t *list;
-        const bool prefix = tile < p_total;
-        if (prefix) {
-            unit = tile / p.p_tiles;
-            unit_tiles = p.p_tiles;
-            unit_start = unit * unit_tiles;
-            kvh = (int)(unit / p.p_rtiles);
-            row0 = (unit - kvh * p.p_rtiles) * M;
-            row_end = p.rows;
-            list = a.prefix;
-            key_first = p.p_first;
-            key_end = a.n_prefix;
-        } else {
-            int64_t tb = seq_tiles(a, b);
-            while (tile >= b_start + per_seq * tb) {
-                b_start += per_seq * tb;
-                tb = seq_tiles(a, ++b);
-            }
-            const int64_t u = (tile - b_start) / tb;
-            unit = p_units + b * per_seq + u;
-            unit_tiles = tb;
-            unit_start = b_start + u * tb;
-            kvh = (int)(u / p.s_rtiles);
-            row0 = b * p.R + (u - (int64_t)kvh * p.s_rtiles) * M;
-            row_end = (b + 1) * p.R;
-            list = a.table + b * a.table_stride;
-            key_end = seq_len(a, b);
-            key_first = first_key(key_end, a.q_len, a.window);
-        }
-        const int64_t seg_end = min(tile_end, unit_start + unit_tiles);
-        const bool whole = tile == unit_start && seg_end == unit_start + unit_tiles;
-        const int64_t k0 = key_first + (tile - unit_start) * kTileKeys;
-        const int64_t k1 = min(key_end, key_first + (seg_end - unit_start) * kTileKeys);
-
-        // ---- query fragments (columns g), and the rows' scale and keys (columns 2t, 2t + 1) --------
+    while (at.tile < at.end) {
+        const Unit u = next_unit(a, p, M, at);
+        // query fragments (columns g), and the rows' scale and keys (columns 2t, 2t + 1)
         uint32_t qf[NT][8][2];
         float row_inv[NT];
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-            const int64_t rr = row0 + 8 * n + g;
-            const bool act = rr < row_end;
+            const int rr = u.row0 + 8 * n + g;
+            const bool act = rr < u.row_end;
             int i = 0, hg = 0;
             const int64_t tok = act ? row_token(a, p, rr, i, hg) : 0;
             const char *qp = (const char *)a.q +
-                             2 * (tok * a.q_stride + (int64_t)(kvh * p.group + hg) * kD);
+                             2 * (tok * a.q_stride + (int64_t)(u.kvh * p.group + hg) * kD);
             row_inv[n] = 1.0f;
             if constexpr (!FP8) {
 #pragma unroll
@@ -279,22 +380,14 @@ __global__ void __launch_bounds__(kThreads, RowsConfig<FP8>::kCtasPerSm)
             } else {
                 uint32_t mx = 0u;
 #pragma unroll
-                for (int s = 0; s < 2; ++s) {
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        const uint4 v = act ? ld_cached(qp + 128 * s + 32 * t + 16 * h)
-                                            : make_uint4(0u, 0u, 0u, 0u);
-                        qf[n][4 * s + 2 * h][0] = v.x, qf[n][4 * s + 2 * h][1] = v.y;
-                        qf[n][4 * s + 2 * h + 1][0] = v.z, qf[n][4 * s + 2 * h + 1][1] = v.w;
-                    }
+                for (int ks = 0; ks < 8; ++ks) {
+                    const uint2 w = act ? *reinterpret_cast<const uint2 *>(qp + 32 * ks + 8 * t)
+                                        : make_uint2(0u, 0u);
+                    qf[n][ks][0] = w.x;
+                    qf[n][ks][1] = w.y;
+                    mx = max(mx, max((w.x << 16) & 0x7fffffffu, w.x & 0x7fff0000u));
+                    mx = max(mx, max((w.y << 16) & 0x7fffffffu, w.y & 0x7fff0000u));
                 }
-#pragma unroll
-                for (int ks = 0; ks < 8; ++ks)
-#pragma unroll
-                    for (int j = 0; j < 2; ++j) {
-                        mx = max(mx, (qf[n][ks][j] << 16) & 0x7fffffffu);
-                        mx = max(mx, qf[n][ks][j] & 0x7fff0000u);
-                    }
                 mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
                 mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
                 float f;
@@ -308,33 +401,45 @@ __global__ void __launch_bounds__(kThreads, RowsConfig<FP8>::kCtasPerSm)
             }
         }
         float scale[NT][2];
-        int64_t lo[NT][2], hi[NT][2];  // keys of the list that the row sees
-        int64_t lo_all = 0, hi_all = key_end;
+        int lo[NT][2], hi[NT][2];  // keys of the list that the row sees
+        int lo_all = 0, hi_all = u.key_end;
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                const int64_t rr = row0 + 8 * n + 2 * t + e;
+                const int rr = u.row0 + 8 * n + 2 * t + e;
                 scale[n][e] = __fmul_rn(__fmul_rn(a.sm_scale * a.k_scale, kLog2e),
                                         __shfl_sync(0xffffffffu, row_inv[n], 4 * (2 * t + e)));
                 lo[n][e] = 0;
-                hi[n][e] = key_end;
-                if (rr < row_end) {
+                hi[n][e] = u.key_end;
+                if (rr < u.row_end) {
                     int i, hg;
                     row_token(a, p, rr, i, hg);
-                    const int64_t rb = rr / p.R;
-                    const int64_t pos = seq_len(a, rb) - a.q_len + i;  // index in the suffix
-                    const int64_t at = prefix ? a.n_prefix + pos : pos;  // index in the list
-                    lo[n][e] = a.window > 0 && at + 1 - a.window > 0 ? at + 1 - a.window : 0;
-                    hi[n][e] = pos < 0 ? 0 : (prefix ? a.n_prefix : pos + 1);
+                    const int64_t pos = seq_len(a, rr / p.R) - a.q_len + i;  // in the suffix
+                    const int64_t where = u.prefix ? a.n_prefix + pos : pos;  // in the list
+                    lo[n][e] = a.window > 0 && where + 1 - a.window > 0
+                                   ? (int)min((int64_t)u.key_end, where + 1 - a.window)
+                                   : 0;
+                    hi[n][e] = pos < 0 ? 0 : (u.prefix ? u.key_end : (int)pos + 1);
                 }
                 lo_all = max(lo_all, lo[n][e]);
                 hi_all = min(hi_all, hi[n][e]);
             }
+        lo_all = __reduce_max_sync(0xffffffffu, lo_all);
+        hi_all = __reduce_min_sync(0xffffffffu, hi_all);
+        float *score[NT][2];  // where the rows' scores are kept
+        if constexpr (WEIGHTS) {
 #pragma unroll
-        for (int off = 1; off < 4; off <<= 1) {
-            lo_all = max(lo_all, (int64_t)__shfl_xor_sync(0xffffffffu, lo_all, off));
-            hi_all = min(hi_all, (int64_t)__shfl_xor_sync(0xffffffffu, hi_all, off));
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const int rr = u.row0 + 8 * n + 2 * t + e, sb = rr / p.R;
+                    score[n][e] = u.prefix || rr >= u.row_end
+                                      ? nullptr
+                                      : reinterpret_cast<float *>(a.workspace + p.score_off) +
+                                            (((int64_t)sb * a.n_kv + u.kvh) * p.R + (rr - sb * p.R)) *
+                                                p.score_width;
+                }
         }
 
         float o[8][NT][4], m[NT][2], l[NT][2];
@@ -347,135 +452,131 @@ __global__ void __launch_bounds__(kThreads, RowsConfig<FP8>::kCtasPerSm)
                 o[mt][n][0] = o[mt][n][1] = o[mt][n][2] = o[mt][n][3] = 0.0f;
         }
 
-        // ---- the keys: 16 a step and warp ----------------------------------------------------------
-        const int steps = (int)((k1 - k0 - warp * kWarpKeys + kTileKeys - 1) / kTileKeys);
-        const int64_t pitch = (int64_t)a.n_kv * C::kRow;
-        const char *kbase = (const char *)a.k_cache + kvh * C::kRow;
-        const char *vbase = (const char *)a.v_cache + kvh * C::kRow;
-        auto load_slot = [&](int s) -> int {  // lane i < 16: slot of key i, or -1
-            const int64_t key = k0 + (int64_t)s * kTileKeys + warp * kWarpKeys + lane;
-            if (lane >= kWarpKeys || s >= steps || key >= k1)
-                return -1;
-            const int64_t slot = list[key];
-            return slot >= 0 && slot < a.num_slots ? (int)slot : -1;
-        };
-        uint64_t masks = 0;  // which keys of the stages in flight exist, 16 bits each
-        auto issue = [&](int s, int slot) {
-            masks = (masks << 16) | (__ballot_sync(0xffffffffu, slot >= 0) & 0xffffu);
-            if (s < steps) {
-                const uint32_t kdst = wbuf + (s % C::kStages) * 2 * C::kTileBytes;
-                constexpr int kRowsPer = 32 / C::kChunks;
-                const int ch = lane % C::kChunks, r0 = lane / C::kChunks;
-#pragma unroll
-                for (int j = 0; j < kWarpKeys / kRowsPer; ++j) {
-                    const int r = j * kRowsPer + r0;
-                    const int sl = __shfl_sync(0xffffffffu, slot, r);
-                    const int64_t off = (sl < 0 ? 0 : sl) * pitch + 16 * ch;
-                    const uint32_t dst = r * C::kRow + 16 * swizzle<FP8>(r, ch);
-                    const uint32_t bytes = sl < 0 ? 0u : 16u;
-                    cp_async16(kdst + dst, kbase + off, bytes);
-                    cp_async16(kdst + C::kTileBytes + dst, vbase + off, bytes);
-                }
-            }
-            cp_async_commit();
-        };
-#pragma unroll
-        for (int s = 0; s < C::kStages - 1; ++s)
-            issue(s, load_slot(s));
-        int next_slot = load_slot(C::kStages - 1);
+        const int steps = steps_of(u);
         for (int s = 0; s < steps; ++s) {
-            cp_async_wait<C::kStages - 2>();
-            __syncwarp();
-            issue(s + C::kStages - 1, next_slot);
-            next_slot = load_slot(s + C::kStages);
-            const uint32_t kt = wbuf + (s % C::kStages) * 2 * C::kTileBytes;
-            const uint32_t vt = kt + C::kTileBytes;
-            const uint32_t mask = (uint32_t)(masks >> (16 * (C::kStages - 1))) & 0xffffu;
-            const int64_t key0 = k0 + (int64_t)s * kTileKeys + warp * kWarpKeys;
-
-            float sc[NT][4];
-#pragma unroll
-            for (int n = 0; n < NT; ++n)
-                sc[n][0] = sc[n][1] = sc[n][2] = sc[n][3] = 0.0f;
-            if constexpr (!FP8) {
-#pragma unroll
-                for (int ks = 0; ks < 8; ++ks) {
-                    uint32_t af[4];
-                    const int key = lane & 15, ch = 2 * ks + (lane >> 4);
-                    ldmatrix_x4(af, kt + key * C::kRow + 16 * swizzle<FP8>(key, ch));
-#pragma unroll
-                    for (int n = 0; n < NT; ++n)
-                        mma16816<FP8>(sc[n], af, qf[n][ks][0], qf[n][ks][1]);
-                }
-            } else {
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const uint4 x = lds128(kt + g * C::kRow + 16 * swizzle<FP8>(g, 4 * h + t));
-                    const uint4 y =
-                        lds128(kt + (g + 8) * C::kRow + 16 * swizzle<FP8>(g + 8, 4 * h + t));
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const uint32_t xw = word(x, j), yw = word(y, j);
-                        const uint32_t af[4] = {e4m3x2_to_f16x2(xw), e4m3x2_to_f16x2(yw),
-                                                e4m3x2_to_f16x2(xw >> 16),
-                                                e4m3x2_to_f16x2(yw >> 16)};
-#pragma unroll
-                        for (int n = 0; n < NT; ++n)
-                            mma16816<FP8>(sc[n], af, qf[n][4 * h + j][0], qf[n][4 * h + j][1]);
-                    }
-                }
+            __syncwarp();  // every lane has read the stage that the next copy overwrites
+            issue();
+            if (!failed &&
+                __any_sync(0xffffffffu, !mbar_wait(&bars[out_stage], phase))) {
+                failed = true;
+                *s_fail = 1;
+                atomicOr(&g_decode_fault_word, kFaultCopyTimeout);
             }
-            // scores to base 2; keys that a row does not see get -inf
-            const bool all_seen = mask == 0xffffu && key0 >= lo_all && key0 + kWarpKeys <= hi_all;
+            const uint32_t kt = wbuf + out_stage * C::kStageBytes, vt = kt + C::kValues;
+            const uint32_t mask = masks[C::kStages - 1];
+            if (++out_stage == C::kStages)
+                out_stage = 0, phase ^= 1;
+            const int key0 = u.k0 + s * C::kTileKeys + warp * C::kKeys;
+
+            float sc[MT][NT][4];
 #pragma unroll
-            for (int n = 0; n < NT; ++n)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int row = g + 8 * (e >> 1), col = e & 1;
-                    const float v = __fmul_rn(sc[n][e], scale[n][col]);
-                    const int64_t key = key0 + row;
-                    const bool seen = all_seen || (((mask >> row) & 1u) && key >= lo[n][col] &&
-                                                   key < hi[n][col]);
-                    sc[n][e] = seen ? v : -INFINITY;
-                }
-            if (a.weight_out && !prefix) {
+            for (int mk = 0; mk < MT; ++mk) {
+                // two chains of products, joined at the end: half the latency
+                float odd[NT][4];
 #pragma unroll
                 for (int n = 0; n < NT; ++n)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const int64_t rr = row0 + 8 * n + 2 * t + (e & 1);
-                        const int64_t key = key0 + g + 8 * (e >> 1);
-                        if (rr < row_end && key < k1) {
-                            const int64_t sb = rr / p.R;
-                            float *dst = reinterpret_cast<float *>(a.workspace + p.score_off);
-                            dst[((sb * a.n_kv + kvh) * p.R + (rr - sb * p.R)) * p.score_width +
-                                key] = sc[n][e];
+                    for (int e = 0; e < 4; ++e)
+                        sc[mk][n][e] = odd[n][e] = 0.0f;
+                const int key = 16 * mk + (lane & 15);
+#pragma unroll
+                for (int ks = 0; ks < 8; ks += FP8 ? 2 : 1) {
+                    uint32_t r[4];
+                    if constexpr (!FP8) {
+                        const int ch = 2 * ks + (lane >> 4);
+                        ldmatrix_x4(r, kt + (ch >> 3) * C::kHalf + key * 128 +
+                                           16 * ((ch & 7) ^ (key & 7)));
+#pragma unroll
+                        for (int n = 0; n < NT; ++n)
+                            mma16816<FP8>(ks & 1 ? odd[n] : sc[mk][n], r, qf[n][ks][0],
+                                          qf[n][ks][1]);
+                    } else {
+                        const int ch = ks + (lane >> 4);
+                        ldmatrix_x4(r, kt + key * 128 + 16 * (ch ^ (key & 7)));
+                        const uint32_t a0[4] = {e4m3x2_to_f16x2(r[0]), e4m3x2_to_f16x2(r[1]),
+                                                e4m3x2_to_f16x2(r[0] >> 16),
+                                                e4m3x2_to_f16x2(r[1] >> 16)};
+                        const uint32_t a1[4] = {e4m3x2_to_f16x2(r[2]), e4m3x2_to_f16x2(r[3]),
+                                                e4m3x2_to_f16x2(r[2] >> 16),
+                                                e4m3x2_to_f16x2(r[3] >> 16)};
+#pragma unroll
+                        for (int n = 0; n < NT; ++n) {
+                            mma16816<FP8>(sc[mk][n], a0, qf[n][ks][0], qf[n][ks][1]);
+                            mma16816<FP8>(odd[n], a1, qf[n][ks + 1][0], qf[n][ks + 1][1]);
                         }
                     }
+                }
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        sc[mk][n][e] =
+                            __fmul_rn(__fadd_rn(sc[mk][n][e], odd[n][e]), scale[n][e & 1]);
             }
-            uint32_t pf[NT][2];
+            // keys that a row does not see get -inf
+            const bool all_seen = mask == (FP8 ? 0xffffffffu : 0xffffu) && key0 >= lo_all &&
+                                  key0 + C::kKeys <= hi_all;
+            if (!all_seen) {
+#pragma unroll
+                for (int mk = 0; mk < MT; ++mk)
+#pragma unroll
+                    for (int n = 0; n < NT; ++n)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const int row = 16 * mk + g + 8 * (e >> 1), key = key0 + row;
+                            const bool seen = ((mask >> row) & 1u) && key >= lo[n][e & 1] &&
+                                              key < hi[n][e & 1];
+                            sc[mk][n][e] = seen ? sc[mk][n][e] : -INFINITY;
+                        }
+            }
+            if constexpr (WEIGHTS) {
+#pragma unroll
+                for (int mk = 0; mk < MT; ++mk)
+#pragma unroll
+                    for (int n = 0; n < NT; ++n)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const int key = key0 + 16 * mk + g + 8 * (e >> 1);
+                            if (score[n][e & 1] && key < u.k1)
+                                score[n][e & 1][key] = sc[mk][n][e];
+                        }
+            }
+            uint32_t pf[MT][NT][2];
             bool grew = false;
             float alpha[NT][2];
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
-                float ps[4];
+                float ms[2];
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    float mx = fmaxf(sc[n][e], sc[n][e + 2]);
+                    float mx = fmaxf(sc[0][n][e], sc[0][n][e + 2]);
+#pragma unroll
+                    for (int mk = 1; mk < MT; ++mk)
+                        mx = fmaxf(mx, fmaxf(sc[mk][n][e], sc[mk][n][e + 2]));
                     mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
                     mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
                     mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
                     const float mn = fmaxf(m[n][e], mx);
-                    const float ms = mn == -INFINITY ? 0.0f : mn;
-                    alpha[n][e] = exp2_fast(__fsub_rn(m[n][e], ms));
+                    ms[e] = mn == -INFINITY ? 0.0f : mn;
+                    alpha[n][e] = exp2_fast(__fsub_rn(m[n][e], ms[e]));
                     grew = grew || mn != m[n][e];
                     m[n][e] = mn;
-                    ps[e] = exp2_fast(__fsub_rn(sc[n][e], ms));
-                    ps[e + 2] = exp2_fast(__fsub_rn(sc[n][e + 2], ms));
-                    l[n][e] = __fmaf_rn(l[n][e], alpha[n][e], __fadd_rn(ps[e], ps[e + 2]));
+                    l[n][e] = __fmul_rn(l[n][e], alpha[n][e]);
                 }
-                pf[n][0] = movmatrix_trans(FP8 ? pack_f16x2(ps[0], ps[1]) : pack_bf16x2(ps[0], ps[1]));
-                pf[n][1] = movmatrix_trans(FP8 ? pack_f16x2(ps[2], ps[3]) : pack_bf16x2(ps[2], ps[3]));
+#pragma unroll
+                for (int mk = 0; mk < MT; ++mk) {
+                    float ps[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        ps[e] = exp2_fast(__fsub_rn(sc[mk][n][e], ms[e & 1]));
+#pragma unroll
+                    for (int e = 0; e < 2; ++e)
+                        l[n][e] = __fadd_rn(l[n][e], __fadd_rn(ps[e], ps[e + 2]));
+                    pf[mk][n][0] = movmatrix_trans(FP8 ? pack_f16x2(ps[0], ps[1])
+                                                       : pack_bf16x2(ps[0], ps[1]));
+                    pf[mk][n][1] = movmatrix_trans(FP8 ? pack_f16x2(ps[2], ps[3])
+                                                       : pack_bf16x2(ps[2], ps[3]));
+                }
             }
             if (__any_sync(0xffffffffu, grew)) {
 #pragma unroll
@@ -487,81 +588,80 @@ __global__ void __launch_bounds__(kThreads, RowsConfig<FP8>::kCtasPerSm)
                             o[mt][n][e] = __fmul_rn(o[mt][n][e], alpha[n][e & 1]);
             }
             // A weight of zero does not hide an infinite or NaN value of a key that only other rows
-            // see, so such a tile (rare) goes column by column with those values left out.
-            if (!all_seen && tile_has_nonfinite<FP8>(vt, lane)) {
+            // see, so such a stage (rare) goes column by column with those values left out.
+            if (!all_seen && stage_has_nonfinite<FP8>(vt, lane)) {
 #pragma unroll
-                for (int n = 0; n < NT; ++n)
-#pragma unroll 1
-                    for (int c = 0; c < 8; ++c) {
-                        const uint32_t b0 = g == c ? pf[n][0] : 0u, b1 = g == c ? pf[n][1] : 0u;
-                        const float lo_s = c & 1 ? sc[n][1] : sc[n][0];
-                        const float hi_s = c & 1 ? sc[n][3] : sc[n][2];
-                        // bit k: the column sees key k (lanes 4 k + c / 2 hold keys k and k + 8)
-                        const uint32_t lb = __ballot_sync(0xffffffffu, lo_s != -INFINITY);
-                        const uint32_t hb = __ballot_sync(0xffffffffu, hi_s != -INFINITY);
-                        uint32_t keep[2] = {0u, 0u};
-#pragma unroll
-                        for (int j = 0; j < 2; ++j) {
-                            const int bit = 4 * (2 * t + j) + c / 2;
-                            keep[0] |= ((lb >> bit) & 1u) ? 0xffffu << (16 * j) : 0u;
-                            keep[1] |= ((hb >> bit) & 1u) ? 0xffffu << (16 * j) : 0u;
-                        }
-#pragma unroll
-                        for (int mt = 0; mt < 8; ++mt) {
-                            uint32_t af[4];
-                            load_values<FP8>(af, vt, mt, lane);
-                            af[0] &= keep[0], af[1] &= keep[0];
-                            af[2] &= keep[1], af[3] &= keep[1];
-                            float add[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-                            mma16816<FP8>(add, af, b0, b1);
-#pragma unroll
-                            for (int e = 0; e < 4; ++e)  // the other columns' zeros met them too
-                                if (2 * t + (e & 1) == c)
-                                    o[mt][n][e] = __fadd_rn(o[mt][n][e], add[e]);
-                        }
-                    }
-                continue;
-            }
-            if constexpr (!FP8) {
-#pragma unroll
-                for (int mt = 0; mt < 8; ++mt) {
-                    uint32_t af[4];
-                    load_values<FP8>(af, vt, mt, lane);
+                for (int mk = 0; mk < MT; ++mk)
 #pragma unroll
                     for (int n = 0; n < NT; ++n)
-                        mma16816<FP8>(o[mt][n], af, pf[n][0], pf[n][1]);
-                }
-            } else {
-                // 16-bit units of the transposed load are pairs (d, d + 1): after the split, matrix
-                // row g is element 2g of the 16, row g + 8 element 2g + 1
+#pragma unroll 1
+                        for (int c = 0; c < 8; ++c) {
+                            const uint32_t b0 = g == c ? pf[mk][n][0] : 0u;
+                            const uint32_t b1 = g == c ? pf[mk][n][1] : 0u;
+                            const float s_lo = c & 1 ? sc[mk][n][1] : sc[mk][n][0];
+                            const float s_hi = c & 1 ? sc[mk][n][3] : sc[mk][n][2];
+                            // the column's scores of keys k and k + 8 lie in lane 4 k + c / 2
+                            const uint32_t lb = __ballot_sync(0xffffffffu, s_lo != -INFINITY);
+                            const uint32_t hb = __ballot_sync(0xffffffffu, s_hi != -INFINITY);
+                            uint32_t keep[2] = {0u, 0u};
 #pragma unroll
-                for (int c2 = 0; c2 < 4; ++c2) {
-                    uint32_t r[4];
-                    const int key = lane & 15, ch = 2 * c2 + (lane >> 4);
-                    ldmatrix_x4_trans(r, vt + key * C::kRow + 16 * swizzle<FP8>(key, ch));
+                            for (int j = 0; j < 2; ++j) {
+                                const int bit = 4 * (2 * t + j) + c / 2;
+                                keep[0] |= ((lb >> bit) & 1u) ? 0xffffu << (16 * j) : 0u;
+                                keep[1] |= ((hb >> bit) & 1u) ? 0xffffu << (16 * j) : 0u;
+                            }
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        const uint32_t x0 = e4m3x2_to_f16x2(r[2 * h]);
-                        const uint32_t x1 = e4m3x2_to_f16x2(r[2 * h] >> 16);
-                        const uint32_t y0 = e4m3x2_to_f16x2(r[2 * h + 1]);
-                        const uint32_t y1 = e4m3x2_to_f16x2(r[2 * h + 1] >> 16);
-                        const uint32_t af[4] = {__byte_perm(x0, x1, 0x5410),
-                                                __byte_perm(x0, x1, 0x7632),
-                                                __byte_perm(y0, y1, 0x5410),
-                                                __byte_perm(y0, y1, 0x7632)};
+                            for (int mt = 0; mt < 8; ++mt) {
+                                uint32_t af[4];
+                                if constexpr (FP8) {
+                                    uint32_t other[4];
+                                    if (mt & 1)
+                                        load_values_fp8(other, af, vt + mk * 2048, mt - 1, lane);
+                                    else
+                                        load_values_fp8(af, other, vt + mk * 2048, mt, lane);
+                                } else {
+                                    load_values_bf16(af, vt, mt, lane);
+                                }
+                                af[0] &= keep[0], af[1] &= keep[0];
+                                af[2] &= keep[1], af[3] &= keep[1];
+                                float add[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                                mma16816<FP8>(add, af, b0, b1);
+#pragma unroll
+                                for (int e = 0; e < 4; ++e)  // the other columns' zeros met them too
+                                    if (2 * t + (e & 1) == c)
+                                        o[mt][n][e] = __fadd_rn(o[mt][n][e], add[e]);
+                            }
+                        }
+                continue;
+            }
+#pragma unroll
+            for (int mk = 0; mk < MT; ++mk) {
+                if constexpr (!FP8) {
+#pragma unroll
+                    for (int mt = 0; mt < 8; ++mt) {
+                        uint32_t af[4];
+                        load_values_bf16(af, vt, mt, lane);
 #pragma unroll
                         for (int n = 0; n < NT; ++n)
-                            mma16816<FP8>(o[2 * c2 + h][n], af, pf[n][0], pf[n][1]);
+                            mma16816<FP8>(o[mt][n], af, pf[mk][n][0], pf[mk][n][1]);
+                    }
+                } else {
+#pragma unroll
+                    for (int mt = 0; mt < 8; mt += 2) {
+                        uint32_t a0[4], a1[4];
+                        load_values_fp8(a0, a1, vt + mk * 2048, mt, lane);
+#pragma unroll
+                        for (int n = 0; n < NT; ++n) {
+                            mma16816<FP8>(o[mt][n], a0, pf[mk][n][0], pf[mk][n][1]);
+                            mma16816<FP8>(o[mt + 1][n], a1, pf[mk][n][0], pf[mk][n][1]);
+                        }
                     }
                 }
             }
         }
 
-        // ---- join the warps ------------------------------------------------------------------------
-        cp_async_wait<0>();
-        __syncthreads();
-        constexpr int kPitch = kD + 4;
-        float *so = reinterpret_cast<float *>(smem);
+        // ---- join the warps: 2 into 0 and 3 into 1, then 1 into 0 ------------------------------------
+        __syncthreads();  // the last unit's join has been read
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -569,68 +669,152 @@ __global__ void __launch_bounds__(kThreads, RowsConfig<FP8>::kCtasPerSm)
                 float v = l[n][e];
                 v = __fadd_rn(v, __shfl_xor_sync(0xffffffffu, v, 4));
                 v = __fadd_rn(v, __shfl_xor_sync(0xffffffffu, v, 8));
-                v = __fadd_rn(v, __shfl_xor_sync(0xffffffffu, v, 16));
+                l[n][e] = __fadd_rn(v, __shfl_xor_sync(0xffffffffu, v, 16));
                 if (g == 0)
-                    s_ml[warp][8 * n + 2 * t + e] = make_float2(m[n][e], v);
+                    s_ml[warp * M + 8 * n + 2 * t + e] = make_float2(m[n][e], l[n][e]);
             }
+        float *buf = reinterpret_cast<float *>(smem + S::kStagesEnd) + (warp & 1) * M * kD + lane;
+        auto put = [&]() {
 #pragma unroll
-        for (int mt = 0; mt < 8; ++mt)
+            for (int mt = 0; mt < 8; ++mt)
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        buf[((mt * NT + n) * 4 + e) * 32] = o[mt][n][e];
+        };
+        auto add = [&](int from) {
 #pragma unroll
             for (int n = 0; n < NT; ++n)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int r = 8 * n + 2 * t + (e & 1);
-                    const int d = FP8 ? 16 * mt + 2 * g + (e >> 1) : 16 * mt + g + 8 * (e >> 1);
-                    so[(warp * M + r) * kPitch + d] = o[mt][n][e];
+                for (int e = 0; e < 2; ++e) {
+                    const float2 x = s_ml[from * M + 8 * n + 2 * t + e];
+                    const float mn = fmaxf(m[n][e], x.x);
+                    const float ms = mn == -INFINITY ? 0.0f : mn;
+                    const float f0 = exp2_fast(__fsub_rn(m[n][e], ms));
+                    const float f1 = exp2_fast(__fsub_rn(x.x, ms));
+                    m[n][e] = mn;
+                    l[n][e] = __fmaf_rn(f1, x.y, __fmul_rn(f0, l[n][e]));
+#pragma unroll
+                    for (int mt = 0; mt < 8; ++mt)
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            float &v = o[mt][n][e + 2 * h];
+                            v = __fmaf_rn(f1, buf[((mt * NT + n) * 4 + e + 2 * h) * 32],
+                                          __fmul_rn(f0, v));
+                        }
                 }
+        };
+        if (warp >= 2)
+            put();
         __syncthreads();
-        const bool direct = whole && !prefix && p_units == 0;
-        const int64_t part = unit + blockIdx.x;
-        for (int x = tid; x < M * (kD / 2); x += kThreads) {
-            const int r = x / (kD / 2), d = 2 * (x % (kD / 2));
-            const int64_t rr = row0 + r;
-            if (rr >= row_end)
-                continue;
-            float mm = -INFINITY;
+        if (warp < 2)
+            add(warp + 2);
+        if (warp == 1) {
+            put();
 #pragma unroll
-            for (int w = 0; w < kWarps; ++w)
-                mm = fmaxf(mm, s_ml[w][r].x);
-            const float ms = mm == -INFINITY ? 0.0f : mm;
-            float ll = 0.0f, o0 = 0.0f, o1 = 0.0f;
+            for (int n = 0; n < NT; ++n)
 #pragma unroll
-            for (int w = 0; w < kWarps; ++w) {
-                const float f = exp2_fast(__fsub_rn(s_ml[w][r].x, ms));
-                const float2 v = *reinterpret_cast<const float2 *>(&so[(w * M + r) * kPitch + d]);
-                ll = __fmaf_rn(f, s_ml[w][r].y, ll);
-                o0 = __fmaf_rn(f, v.x, o0);
-                o1 = __fmaf_rn(f, v.y, o1);
-            }
+                for (int e = 0; e < 2; ++e)
+                    if (g == 0)
+                        s_ml[M + 8 * n + 2 * t + e] = make_float2(m[n][e], l[n][e]);
+        }
+        __syncthreads();
+        if (warp > 0 || *s_fail)  // after a wait that ran out nothing more is written
+            continue;
+        buf += M * kD;  // warp 1's
+        add(1);
+        const bool direct = u.whole && !u.prefix && p_units == 0;
+        const int64_t part = u.unit + blockIdx.x;
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
             if (direct) {
-                int i, hg;
-                const int64_t tok = row_token(a, p, rr, i, hg);
-                const int h = kvh * p.group + hg;
-                const float f = ll == 0.0f ? 0.0f : __fdiv_rn(a.v_scale, ll);
-                *reinterpret_cast<uint32_t *>((char *)a.out +
-                                              2 * (tok * a.out_stride + (int64_t)h * kD + d)) =
-                    ll == 0.0f ? 0u : pack_bf16x2(__fmul_rn(o0, f), __fmul_rn(o1, f));
-                if (d == 0) {
-                    const float lse2 = ll == 0.0f ? -INFINITY : __fadd_rn(mm, log2f(ll));
-                    if (a.lse)
-                        a.lse[tok * a.n_q + h] =
-                            ll == 0.0f ? -INFINITY : __fmaf_rn(mm, kLn2, logf(ll));
-                    if (a.weight_out)
-                        reinterpret_cast<float *>(a.workspace + p.lse_off)[kvh * p.rows + rr] = lse2;
+                float f[2];
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const float ll = l[n][e];
+                    const int rr = u.row0 + 8 * n + 2 * t + e;
+                    f[e] = ll == 0.0f ? 0.0f : __fdiv_rn(a.v_scale, ll);
+                    if (g == 0 && rr < u.row_end) {
+                        int i, hg;
+                        const int64_t tok = row_token(a, p, rr, i, hg);
+                        if (a.lse)
+                            a.lse[tok * a.n_q + u.kvh * p.group + hg] =
+                                ll == 0.0f ? -INFINITY : __fmaf_rn(m[n][e], kLn2, logf(ll));
+                        if (WEIGHTS)
+                            reinterpret_cast<float *>(a.workspace +
+                                                      p.lse_off)[u.kvh * p.rows + rr] =
+                                ll == 0.0f ? -INFINITY : __fadd_rn(m[n][e], log2f(ll));
+                    }
+                }
+                // FP8: a lane holds d = 16 mt + 2g, + 1 of rows 2t and 2t + 1; BF16: d = 16 mt + g and
+                // + 8, so that the lanes of an even and an odd g exchange one row each
+                const int own = FP8 ? 0 : g & 1;
+                const int rr = u.row0 + 8 * n + 2 * t + own;
+                int i = 0, hg = 0, i1 = 0, hg1 = 0;
+                const bool in0 = rr < u.row_end, in1 = FP8 && rr + 1 < u.row_end;
+                const int64_t tok = in0 ? row_token(a, p, rr, i, hg) : 0;
+                const int64_t tok1 = in1 ? row_token(a, p, rr + 1, i1, hg1) : 0;
+                char *dst = (char *)a.out +
+                            2 * (tok * a.out_stride + (int64_t)(u.kvh * p.group + hg) * kD);
+                char *dst1 = (char *)a.out +
+                             2 * (tok1 * a.out_stride + (int64_t)(u.kvh * p.group + hg1) * kD);
+#pragma unroll
+                for (int mt = 0; mt < 8; ++mt) {
+                    float v[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        v[e] = l[n][e & 1] == 0.0f ? 0.0f : __fmul_rn(o[mt][n][e], f[e & 1]);
+                    if constexpr (FP8) {
+                        if (in0)
+                            *reinterpret_cast<uint32_t *>(dst + 32 * mt + 4 * g) =
+                                pack_bf16x2(v[0], v[2]);
+                        if (in1)
+                            *reinterpret_cast<uint32_t *>(dst1 + 32 * mt + 4 * g) =
+                                pack_bf16x2(v[1], v[3]);
+                    } else {
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            const float give = own ? v[2 * h] : v[2 * h + 1];
+                            const float got = __shfl_xor_sync(0xffffffffu, give, 4);
+                            const uint32_t w = own ? pack_bf16x2(got, v[2 * h + 1])
+                                                   : pack_bf16x2(v[2 * h], got);
+                            if (in0)
+                                *reinterpret_cast<uint32_t *>(dst + 32 * mt + 16 * h +
+                                                              2 * (g & ~1)) = w;
+                        }
+                    }
                 }
             } else {
                 float *po = reinterpret_cast<float *>(a.workspace + p.o_off);
-                *reinterpret_cast<float2 *>(po + (part * M + r) * kD + d) = make_float2(o0, o1);
-                if (d == 0)
-                    reinterpret_cast<float2 *>(a.workspace + p.ml_off)[part * M + r] =
-                        make_float2(mm, ll);
+                float2 *pm = reinterpret_cast<float2 *>(a.workspace + p.ml_off);
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const int r = 8 * n + 2 * t + e;
+                    if (u.row0 + r >= u.row_end)
+                        continue;
+                    if (g == 0)
+                        pm[part * M + r] = make_float2(m[n][e], l[n][e]);
+                    float *dst = po + (part * M + r) * kD;
+#pragma unroll
+                    for (int mt = 0; mt < 8; ++mt) {
+                        if constexpr (FP8) {
+                            *reinterpret_cast<float2 *>(dst + 16 * mt + 2 * g) =
+                                make_float2(o[mt][n][e], o[mt][n][e + 2]);
+                        } else {
+                            dst[16 * mt + g] = o[mt][n][e];
+                            dst[16 * mt + g + 8] = o[mt][n][e + 2];
+                        }
+                    }
+                }
             }
         }
-        __syncthreads();
-        tile = seg_end;
+    }
+    // a wait that ran out: the copies still in flight end before the block does (a bounded wait)
+    if (failed) {
+        const unsigned long long t0 = global_ns();
+        while (global_ns() - t0 < kWaitLimitNs / 4) {
+        }
     }
 }
 
@@ -742,17 +926,42 @@ __global__ void __launch_bounds__(256) attn_weight_kernel(const __grid_constant_
     }
 }
 
-template <int NT, bool FP8>
-cudaError_t launch_rows(const AttnArgs &a, const AttnPlan &p, cudaStream_t stream)
+// The kernel may use all of the shared memory: set once per device.
+template <auto Kernel>
+cudaError_t allow_smem(int bytes)
 {
-    static_assert(RowsConfig<FP8>::kSmem >= kWarps * 8 * NT * (kD + 4) * 4, "join buffer");
-    const cudaError_t e =
-        cudaFuncSetAttribute(attn_rows_kernel<NT, FP8>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             RowsConfig<FP8>::kSmem);
+    static bool done[64] = {};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess || (dev < 64 && done[dev]))
+        return e;
+    e = cudaFuncSetAttribute(Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess && dev < 64)
+        done[dev] = true;
+    return e;
+}
+
+template <int NT, bool FP8, bool WEIGHTS>
+cudaError_t launch_rows(const AttnArgs &a, const AttnPlan &p, const CacheMaps &maps,
+                        cudaStream_t stream)
+{
+    constexpr int bytes = RowsSmem<NT>::kBytes;
+    const cudaError_t e = allow_smem<attn_rows_kernel<NT, FP8, WEIGHTS>>(bytes);
     if (e != cudaSuccess)
         return e;
-    return launch_pdl(attn_rows_kernel<NT, FP8>, dim3(p.ctas), dim3(kThreads),
-                      RowsConfig<FP8>::kSmem, stream, a, p);
+    return launch_pdl(attn_rows_kernel<NT, FP8, WEIGHTS>, dim3(p.ctas), dim3(kThreads), bytes,
+                      stream, a, p, maps);
+}
+
+template <int NT>
+cudaError_t launch_rows_type(const AttnArgs &a, const AttnPlan &p, const CacheMaps &maps,
+                             cudaStream_t stream)
+{
+    if (a.fp8)
+        return a.weight_out ? launch_rows<NT, true, true>(a, p, maps, stream)
+                            : launch_rows<NT, true, false>(a, p, maps, stream);
+    return a.weight_out ? launch_rows<NT, false, true>(a, p, maps, stream)
+                        : launch_rows<NT, false, false>(a, p, maps, stream);
 }
 
 inline int64_t align_up(int64_t x, int64_t a) { return (x + a - 1) / a * a; }
@@ -760,9 +969,10 @@ inline int64_t align_up(int64_t x, int64_t a) { return (x + a - 1) / a * a; }
 }  // namespace
 
 AttnPlan attn_plan(int32_t B, int32_t q_len, int32_t n_q, int32_t n_kv, int64_t n_prefix,
-                   int64_t width, int64_t window, bool weights)
+                   int64_t width, int64_t window, bool weights, bool fp8)
 {
     AttnPlan p{};
+    p.tile_keys = fp8 ? RowsConfig<true>::kTileKeys : RowsConfig<false>::kTileKeys;
     p.group = n_q / n_kv;
     p.R = q_len * p.group;
     p.rows = (int64_t)B * p.R;
@@ -774,15 +984,15 @@ AttnPlan attn_plan(int32_t B, int32_t q_len, int32_t n_q, int32_t n_kv, int64_t 
     const int M = 8 * p.nt;
     p.s_rtiles = (p.R + M - 1) / M;
     p.p_rtiles = p_keys > 0 ? (p.rows + M - 1) / M : 0;
-    p.p_tiles = (p_keys + kTileKeys - 1) / kTileKeys;
+    p.p_tiles = (p_keys + p.tile_keys - 1) / p.tile_keys;
     p.units = n_kv * (p.p_rtiles + (int64_t)B * p.s_rtiles);
     int64_t keys = width;
     if (window > 0 && window + q_len - 1 < keys)
         keys = window + q_len - 1;
     const int64_t tiles =
         n_kv * (p.p_rtiles * p.p_tiles +
-                (int64_t)B * p.s_rtiles * ((keys + kTileKeys - 1) / kTileKeys));
-    const int64_t most = kPlanSms * 3;
+                (int64_t)B * p.s_rtiles * ((keys + p.tile_keys - 1) / p.tile_keys));
+    const int64_t most = kPlanSms * 2;
     p.ctas = (int32_t)(tiles < 1 ? 1 : (tiles < most ? tiles : most));
     p.score_width = align_up(width, 8);
     int64_t at = 0;
@@ -792,8 +1002,8 @@ AttnPlan attn_plan(int32_t B, int32_t q_len, int32_t n_q, int32_t n_kv, int64_t 
         return here;
     };
     p.cum_off = take(8 * ((int64_t)B + 1));
-    p.o_off = take((p.units + p.ctas) * M * kD * 4);
-    p.ml_off = take((p.units + p.ctas) * M * 8);
+    p.o_off = take((p.units + most) * M * kD * 4);
+    p.ml_off = take((p.units + most) * M * 8);
     p.lse_off = take(weights ? n_kv * p.rows * 4 : 0);
     p.score_off = take(weights ? n_kv * p.rows * p.score_width * 4 : 0);
     p.bytes = at;
@@ -802,11 +1012,11 @@ AttnPlan attn_plan(int32_t B, int32_t q_len, int32_t n_q, int32_t n_kv, int64_t 
 
 cudaError_t launch_attn_prefix(const AttnArgs &a, const AttnPlan &p, cudaStream_t stream)
 {
-    cudaError_t e;
-    if (a.fp8)
-        e = p.nt == 1 ? launch_rows<1, true>(a, p, stream) : launch_rows<2, true>(a, p, stream);
-    else
-        e = p.nt == 1 ? launch_rows<1, false>(a, p, stream) : launch_rows<2, false>(a, p, stream);
+    CacheMaps maps;
+    cudaError_t e = make_cache_maps(maps, a);
+    if (e != cudaSuccess)
+        return e;
+    e = p.nt == 1 ? launch_rows_type<1>(a, p, maps, stream) : launch_rows_type<2>(a, p, maps, stream);
     if (e != cudaSuccess)
         return e;
     const int64_t rows = p.rows * a.n_kv;
@@ -816,6 +1026,16 @@ cudaError_t launch_attn_prefix(const AttnArgs &a, const AttnPlan &p, cudaStream_
     e = launch_pdl(attn_weight_kernel, dim3((unsigned)((a.width + 255) / 256), (unsigned)(a.B < 65535 ? a.B : 65535)),
                    dim3(256), 0, stream, a, p);
     return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+cudaError_t read_decode_fault_word(unsigned int *value, bool clear)
+{
+    cudaError_t e = cudaMemcpyFromSymbol(value, g_decode_fault_word, sizeof(unsigned int));
+    if (e == cudaSuccess && clear) {
+        const unsigned int zero = 0u;
+        e = cudaMemcpyToSymbol(g_decode_fault_word, &zero, sizeof(unsigned int));
+    }
+    return e;
 }
 
 }  // namespace beam

@@ -42,7 +42,7 @@ int64_t beam_attn_prefix_workspace(int32_t B, int32_t q_len, int32_t n_q_heads, 
     if (st != BEAM_OK || B == 0)
         return st;
     return beam::attn_plan(B, q_len, n_q_heads, n_kv_heads, n_prefix, table_width, window,
-                           key_weights != 0)
+                           key_weights != 0, false)
         .bytes;
 }
 
@@ -81,7 +81,8 @@ int beam_attn_prefix_fwd(void *out, int64_t out_row_stride, float *lse_out,
         !aligned(key_weight_in, 4) || !aligned(key_weight_out, 4) || !aligned(workspace, 16))
         return BEAM_ERR_MISALIGNED;
     const beam::AttnPlan p = beam::attn_plan(B, q_len, n_q_heads, n_kv_heads, n_prefix,
-                                             table_width, window, key_weight_out != nullptr);
+                                             table_width, window, key_weight_out != nullptr,
+                                             cache_dtype == 1);
     if (workspace_bytes < p.bytes)
         return BEAM_ERR_INVALID_ARG;
     beam::AttnArgs a{};

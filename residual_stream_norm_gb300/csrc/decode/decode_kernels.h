@@ -45,6 +45,7 @@ struct AttnArgs {
 // row tile).  The units' key tiles, one after the other, are shared out evenly among `ctas` blocks.
 struct AttnPlan {
     int32_t group, R;
+    int32_t tile_keys;    // keys of a tile of the rows kernel
     int64_t rows;         // B * R
     int32_t nt;           // 8-row tiles of a unit's rows: 1 or 2
     int32_t s_rtiles;     // row tiles of a sequence
@@ -59,8 +60,10 @@ struct AttnPlan {
 };
 
 AttnPlan attn_plan(int32_t B, int32_t q_len, int32_t n_q, int32_t n_kv, int64_t n_prefix,
-                   int64_t width, int64_t window, bool weights);
+                   int64_t width, int64_t window, bool weights, bool fp8);
 cudaError_t launch_attn_prefix(const AttnArgs &a, const AttnPlan &p, cudaStream_t stream);
+// The decode operators' fault word of the current device (as read_fault_word).
+cudaError_t read_decode_fault_word(unsigned int *value, bool clear);
 
 struct EvictArgs {
     int64_t *table_out;
