@@ -42,8 +42,8 @@ extern "C" {
  * A row that sees nothing gives out = 0 and lse = -inf.  Scores, maxima, sums and outputs are FP32;
  * the weights exp(s_j - max) are rounded to BF16 (BF16 cache) or FP16 (FP8 cache) where they
  * multiply the values, an error of at most 2^-8 (2^-11) of each.  For an FP8 cache the query row is
- * taken in FP16 after an exact scaling by a power of two that brings its largest element to
- * [2^14, 2^15), so that only elements 2^-28 below the largest lose bits.
+ * taken in FP16 after an exact scaling by a power of two (at most 2^60) that brings its largest
+ * element to [2^14, 2^15), so that only elements 2^-28 below the largest (or below 2^-74) lose bits.
  * If key_weight_out is given, the weight that each suffix key received is added up:
  *   key_weight_out[b, j] = key_weight_in[b, j] + sum over i, h of exp(s_j - lse)   for j < len_b,
  *   and key_weight_in[b, j] for the others    (key_weight_in NULL: 0)

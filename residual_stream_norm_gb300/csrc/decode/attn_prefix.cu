@@ -10,18 +10,15 @@
 // matrix instruction and the few query rows its 8 columns.  Each warp copies its own keys into its own
 // stages (TMA gathers of four slots' rows each), so warps meet only when their parts are joined.
 
-#include "decode_kernels.h"
+#include "attn_common.cuh"
 #include "decode_mma.cuh"
 #include "decode_tma.cuh"
 
 namespace beam {
 namespace {
 
-constexpr int kD = 128;
 constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
-constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kLn2 = 0.6931471805599453f;
 
 // A stage holds the keys and values of one step of a warp: rows of 128 bytes with their 16-byte chunks
 // exchanged by the copy (chunk c of row r at c ^ (r % 8)), so that ldmatrix finds eight rows' same
@@ -66,27 +63,10 @@ __device__ __forceinline__ int64_t first_key(int64_t n, int q_len, int64_t windo
     return window > 0 && lo > 0 ? lo : 0;
 }
 
-__device__ __forceinline__ int64_t seq_len(const AttnArgs &a, int64_t b)
-{
-    const int64_t n = a.len[b];
-    return n < 0 ? 0 : (n > a.width ? a.width : n);
-}
-
 __device__ __forceinline__ int64_t seq_tiles(const AttnArgs &a, const AttnPlan &p, int64_t b)
 {
     const int64_t n = seq_len(a, b);
     return (n - first_key(n, a.q_len, a.window) + p.tile_keys - 1) / p.tile_keys;
-}
-
-// Factor 2^k that brings a row of largest magnitude bits `mx` (FP32) to [2^14, 2^15), and its
-// inverse; 1 for zero, infinite and NaN rows.
-__device__ __forceinline__ void f16_row_factor(uint32_t mx, float &f, float &inv)
-{
-    const int e = (int)(mx >> 23);
-    int k = e == 255 || mx == 0u ? 0 : 141 - e;
-    k = min(k, 120);
-    f = __uint_as_float((uint32_t)(127 + k) << 23);
-    inv = __uint_as_float((uint32_t)(127 - k) << 23);
 }
 
 // The A fragments of V^T for 16 elements d and 16 keys.  BF16 (`mt`: which 16 elements): matrix row is
@@ -133,17 +113,6 @@ __device__ __forceinline__ bool stage_has_nonfinite(uint32_t vt, int lane)
         }
     }
     return __any_sync(0xffffffffu, bad);
-}
-
-// Row rr (of `rows`, per KV head): its token; the query's index and the head within the group.
-__device__ __forceinline__ int64_t row_token(const AttnArgs &a, const AttnPlan &p, int64_t rr,
-                                             int &i, int &hg)
-{
-    const uint32_t b = (uint32_t)rr / (uint32_t)p.R;  // B * q_len * n_q < 2^31
-    const uint32_t r = (uint32_t)rr - b * p.R;
-    i = (int)(r / (uint32_t)p.group);
-    hg = (int)r - i * p.group;
-    return (int64_t)b * a.q_len + i;
 }
 
 // Position in the units' sequence of key tiles.
@@ -277,7 +246,11 @@ __global__ void __launch_bounds__(kThreads, 2)
     }
     __syncwarp();
     pdl_launch_dependents();
-    pdl_wait();
+    // Behind the tensor-core kernel, whose blocks let this one start only after their own wait, and
+    // whose results it does not read, the wait moves to the end: the two overlap, and the join that
+    // follows still finds both complete.
+    if (p.tc_parts == 0)
+        pdl_wait();
 
     // ---- the share of this block ---------------------------------------------------------------
     const int64_t p_units = a.n_kv * p.p_rtiles;
@@ -287,8 +260,11 @@ __global__ void __launch_bounds__(kThreads, 2)
         scan_sequences(a, p, p_total, -1, blockIdx.x == 0 ? cum : nullptr, s_scan);
     const int64_t shares = min((int64_t)p.ctas, total);  // none of them empty
     __syncthreads();
-    if (blockIdx.x >= shares || *s_fail)
+    if (blockIdx.x >= shares || *s_fail) {
+        if (p.tc_parts > 0)
+            pdl_wait();
         return;
+    }
     Cursor at{total * blockIdx.x / shares, total * (blockIdx.x + 1) / shares, 0, p_total};
     if (at.tile >= p_total) {
         scan_sequences(a, p, p_total, at.tile, nullptr, s_scan);
@@ -724,7 +700,7 @@ __global__ void __launch_bounds__(kThreads, 2)
             continue;
         buf += M * kD;  // warp 1's
         add(1);
-        const bool direct = u.whole && !u.prefix && p_units == 0;
+        const bool direct = u.whole && !u.prefix && p_units == 0 && p.tc_parts == 0;
         const int64_t part = u.unit + blockIdx.x;
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
@@ -816,6 +792,8 @@ __global__ void __launch_bounds__(kThreads, 2)
         while (global_ns() - t0 < kWaitLimitNs / 4) {
         }
     }
+    if (p.tc_parts > 0)
+        pdl_wait();
 }
 
 // Joins a row's parts: one warp per row and KV head, four elements a lane.
@@ -837,8 +815,8 @@ __global__ void __launch_bounds__(128) attn_join_kernel(const __grid_constant__ 
     const int64_t rt = (rr - b * p.R) / M;
     const int64_t tb = (cum[b + 1] - cum[b]) / per_seq;
     // the parts of the prefix unit, then those of the suffix unit
-    int64_t first[2] = {0, 0}, at[2] = {0, 0};
-    int count[2] = {0, 0};
+    int64_t first[3] = {0, 0, 0}, at[3] = {0, 0, 0};  // rows of part c: (first + c) * step + at
+    int count[3] = {0, 0, 0};
     if (p.p_rtiles > 0) {
         const int64_t unit = kvh * p.p_rtiles + rr / M, s = unit * p.p_tiles;
         const int64_t c0 = owner(s, total, shares);
@@ -852,29 +830,38 @@ __global__ void __launch_bounds__(128) attn_join_kernel(const __grid_constant__ 
         first[1] = a.n_kv * p.p_rtiles + b * per_seq + u + c0;
         count[1] = (int)(owner(s + tb - 1, total, shares) - c0) + 1;
         at[1] = rr - b * p.R - rt * M;
-        if (p.p_rtiles == 0 && count[1] == 1)
+        if (p.p_rtiles == 0 && p.tc_parts == 0 && count[1] == 1)
             return;  // the rows kernel wrote it
     }
     const float2 *ml = reinterpret_cast<const float2 *>(a.workspace + p.ml_off);
     const float *po = reinterpret_cast<const float *>(a.workspace + p.o_off);
+    const float2 *tml = reinterpret_cast<const float2 *>(a.workspace + p.tc_ml_off);
+    const float *tpo = reinterpret_cast<const float *>(a.workspace + p.tc_o_off);
+    first[2] = x * p.tc_parts;
+    count[2] = p.tc_parts;
     float m = -INFINITY;
-    for (int k = 0; k < 2; ++k)
-        for (int c = lane; c < count[k]; c += 32)
-            m = fmaxf(m, ml[(first[k] + c) * M + at[k]].x);
+#pragma unroll
+    for (int k = 0; k < 3; ++k)
+        for (int c = lane; c < count[k]; c += 32) {
+            const float2 w = k == 2 ? tml[first[2] + c] : ml[(first[k] + c) * M + at[k]];
+            m = fmaxf(m, w.y == 0.0f ? -INFINITY : w.x);
+        }
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1)
         m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
     const float ms = m == -INFINITY ? 0.0f : m;
     float l = 0.0f;
     float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    for (int k = 0; k < 2; ++k)
+#pragma unroll
+    for (int k = 0; k < 3; ++k)
         for (int c = 0; c < count[k]; ++c) {
-            const int64_t r = (first[k] + c) * M + at[k];
-            const float2 w = ml[r];
+            const int64_t r = k == 2 ? first[2] + c : (first[k] + c) * M + at[k];
+            const float2 w = k == 2 ? tml[r] : ml[r];
             if (w.y == 0.0f)
                 continue;
             const float f = exp2_fast(__fsub_rn(w.x, ms));
-            const float4 v = *reinterpret_cast<const float4 *>(po + r * kD + 4 * lane);
+            const float4 v =
+                *reinterpret_cast<const float4 *>((k == 2 ? tpo : po) + r * kD + 4 * lane);
             l = __fmaf_rn(f, w.y, l);
             o.x = __fmaf_rn(f, v.x, o.x);
             o.y = __fmaf_rn(f, v.y, o.y);
@@ -926,21 +913,6 @@ __global__ void __launch_bounds__(256) attn_weight_kernel(const __grid_constant_
     }
 }
 
-// The kernel may use all of the shared memory: set once per device.
-template <auto Kernel>
-cudaError_t allow_smem(int bytes)
-{
-    static bool done[64] = {};
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess || (dev < 64 && done[dev]))
-        return e;
-    e = cudaFuncSetAttribute(Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-    if (e == cudaSuccess && dev < 64)
-        done[dev] = true;
-    return e;
-}
-
 template <int NT, bool FP8, bool WEIGHTS>
 cudaError_t launch_rows(const AttnArgs &a, const AttnPlan &p, const CacheMaps &maps,
                         cudaStream_t stream)
@@ -966,12 +938,40 @@ cudaError_t launch_rows_type(const AttnArgs &a, const AttnPlan &p, const CacheMa
 
 inline int64_t align_up(int64_t x, int64_t a) { return (x + a - 1) / a * a; }
 
+// From these many rows a KV head and prefix keys on, the prefix goes to the tensor-core kernel.
+constexpr int64_t kTcRows = 33, kTcKeys = 256;
+
+// Divides the prefix among the tensor-core kernel's blocks: tiles of 256 rows, or, up to 128 rows, of
+// 128 rows with every other key tile to each half of the block.  The number of parts is the one
+// that fills the SMs best; a part costs about three key tiles besides its own.
+void plan_tc(AttnPlan &p, int32_t n_kv, int64_t n_prefix)
+{
+    p.tc_split = p.rows <= 128;
+    p.tc_rtiles = (int32_t)((p.rows + 255) / 256);
+    const int64_t tiles = (n_prefix + 127) / 128;           // key tiles
+    const int64_t most = p.tc_split ? (tiles + 1) / 2 : tiles;  // steps of a block
+    const int64_t units = (int64_t)p.tc_rtiles * n_kv;
+    int64_t best = INT64_MAX;
+    for (int64_t parts = 1; parts <= most && parts <= 4 * kPlanSms; ++parts) {
+        const int64_t steps = (most + parts - 1) / parts;
+        const int64_t cost = (units * parts + kPlanSms - 1) / kPlanSms * (steps + 3);
+        if (cost < best) {
+            best = cost;
+            p.tc_steps = (int32_t)steps;
+        }
+    }
+    p.tc_blocks = (int32_t)((most + p.tc_steps - 1) / p.tc_steps);
+    p.tc_parts = p.tc_split ? 2 * p.tc_blocks : p.tc_blocks;
+}
+
 }  // namespace
 
 AttnPlan attn_plan(int32_t B, int32_t q_len, int32_t n_q, int32_t n_kv, int64_t n_prefix,
-                   int64_t width, int64_t window, bool weights, bool fp8)
+                   int64_t width, int64_t window, bool weights, bool fp8, bool tc)
 {
     AttnPlan p{};
+    if (window > n_prefix + width)
+        window = 0;  // longer than any list
     p.tile_keys = fp8 ? RowsConfig<true>::kTileKeys : RowsConfig<false>::kTileKeys;
     p.group = n_q / n_kv;
     p.R = q_len * p.group;
@@ -980,10 +980,13 @@ AttnPlan attn_plan(int32_t B, int32_t q_len, int32_t n_q, int32_t n_kv, int64_t 
     if (p.p_first > n_prefix)
         p.p_first = n_prefix;
     const int64_t p_keys = n_prefix - p.p_first;
-    p.nt = (p.R > 8 || (p_keys > 0 && p.rows > 8)) ? 2 : 1;
+    if (tc && window == 0 && p.rows >= kTcRows && n_prefix >= kTcKeys)
+        plan_tc(p, n_kv, n_prefix);
+    const bool with_prefix = p_keys > 0 && p.tc_parts == 0;
+    p.nt = (p.R > 8 || (with_prefix && p.rows > 8)) ? 2 : 1;
     const int M = 8 * p.nt;
     p.s_rtiles = (p.R + M - 1) / M;
-    p.p_rtiles = p_keys > 0 ? (p.rows + M - 1) / M : 0;
+    p.p_rtiles = with_prefix ? (p.rows + M - 1) / M : 0;
     p.p_tiles = (p_keys + p.tile_keys - 1) / p.tile_keys;
     p.units = n_kv * (p.p_rtiles + (int64_t)B * p.s_rtiles);
     int64_t keys = width;
@@ -1005,6 +1008,8 @@ AttnPlan attn_plan(int32_t B, int32_t q_len, int32_t n_q, int32_t n_kv, int64_t 
     p.o_off = take((p.units + most) * M * kD * 4);
     p.ml_off = take((p.units + most) * M * 8);
     p.lse_off = take(weights ? n_kv * p.rows * 4 : 0);
+    p.tc_o_off = take(n_kv * p.rows * p.tc_parts * kD * 4);
+    p.tc_ml_off = take(n_kv * p.rows * p.tc_parts * 8);
     p.score_off = take(weights ? n_kv * p.rows * p.score_width * 4 : 0);
     p.bytes = at;
     return p;
@@ -1016,6 +1021,11 @@ cudaError_t launch_attn_prefix(const AttnArgs &a, const AttnPlan &p, cudaStream_
     cudaError_t e = make_cache_maps(maps, a);
     if (e != cudaSuccess)
         return e;
+    if (p.tc_parts > 0) {
+        e = launch_attn_tc(a, p, maps, stream);
+        if (e != cudaSuccess)
+            return e;
+    }
     e = p.nt == 1 ? launch_rows_type<1>(a, p, maps, stream) : launch_rows_type<2>(a, p, maps, stream);
     if (e != cudaSuccess)
         return e;
@@ -1030,11 +1040,15 @@ cudaError_t launch_attn_prefix(const AttnArgs &a, const AttnPlan &p, cudaStream_
 
 cudaError_t read_decode_fault_word(unsigned int *value, bool clear)
 {
-    cudaError_t e = cudaMemcpyFromSymbol(value, g_decode_fault_word, sizeof(unsigned int));
+    unsigned int tc = 0u;
+    cudaError_t e = read_attn_tc_fault_word(&tc, clear);
+    if (e == cudaSuccess)
+        e = cudaMemcpyFromSymbol(value, g_decode_fault_word, sizeof(unsigned int));
     if (e == cudaSuccess && clear) {
         const unsigned int zero = 0u;
         e = cudaMemcpyToSymbol(g_decode_fault_word, &zero, sizeof(unsigned int));
     }
+    *value |= tc;
     return e;
 }
 

@@ -1,0 +1,563 @@
+// attn_prefix_tc.cu -- the shared prefix's part of the attention for many query rows (sm_103a).
+//
+// All query rows that share a KV head see the same keys, so S = Q K^T and O = P V are products of
+// 128 x 128 tiles: tcgen05, sums in tensor memory.  A block takes two tiles of 128 rows (or, when there
+// are no more than 128 rows, two streams of key tiles for the one tile) and works on them in turn:
+// while one half's four warps turn scores into weights, a row a thread, the tensor cores work for the
+// other.  The weights go back to tensor memory in the place of the scores' second half, in 16 bits,
+// as the A operand of the second product.
+//
+// The running maximum is raised (and O scaled, in tensor memory) only when a score exceeds it by more
+// than 2^8: the weights of a part stay below 2^8, which FP32 sums and both 16-bit types hold with
+// the same relative precision, and nearly all tiles then need no scaling.
+//
+// Roles: warps 0-7 softmax; 8 issues the products; 9 copies keys and values (TMA gathers by slot); for
+// an FP8 cache warps 10-13 expand the copied bytes to FP16 (exact) in the layout of the products.
+
+#include "attn_common.cuh"
+#include "beam_f32x2.cuh"
+#include "decode_mma.cuh"
+#include "decode_tc.cuh"
+#include "decode_tma.cuh"
+
+namespace beam {
+namespace {
+
+__device__ unsigned int g_tc_fault_word = 0u;
+
+constexpr int kTile = 128 * 128 * 2;  // bytes of a 128 x 128 tile of 16-bit values: two halves
+constexpr int kHalfTile = kTile / 2;  // 64 values of each row
+constexpr int kRawTile = 128 * 128;   // FP8
+constexpr float kRaise = 8.0f;
+
+template <bool FP8, bool SPLIT>
+struct TcConfig {
+    static constexpr int kThreads = FP8 ? 448 : 320;
+    static constexpr int kQTiles = SPLIT ? 1 : 2;
+    static constexpr int kRaw = FP8 ? (SPLIT ? 4 : 2) : 0;
+    static constexpr int kK = kQTiles * kTile;        // two stages
+    static constexpr int kV = kK + 2 * kTile;         // two stages
+    static constexpr int kRawAt = kV + 2 * kTile;
+    static constexpr int kMask = kRawAt + kRaw * kRawTile;  // uint32_t [8][4]
+    static constexpr int kBars = kMask + 128;
+    static constexpr int kNumBars = 1 + 8 + 8 + 2 + 2 + 1 + 8;
+    static constexpr int kMisc = kBars + 8 * kNumBars;      // tensor memory address, fail
+    static constexpr int kBytes = kMisc + 16;
+    static_assert(kBytes <= 232448, "shared memory of a block");
+};
+
+// 64 columns of this thread's row, complete on return.
+__device__ __forceinline__ void load64(uint32_t addr, float (&r)[64])
+{
+    uint32_t *u = reinterpret_cast<uint32_t *>(r);
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x64.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, "
+        "%32, %33, %34, %35, %36, %37, %38, %39, %40, %41, %42, %43, %44, %45, %46, %47, "
+        "%48, %49, %50, %51, %52, %53, %54, %55, %56, %57, %58, %59, %60, %61, %62, %63}, [%64];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]), "=r"(u[4]), "=r"(u[5]), "=r"(u[6]),
+          "=r"(u[7]), "=r"(u[8]), "=r"(u[9]), "=r"(u[10]), "=r"(u[11]), "=r"(u[12]), "=r"(u[13]),
+          "=r"(u[14]), "=r"(u[15]), "=r"(u[16]), "=r"(u[17]), "=r"(u[18]), "=r"(u[19]),
+          "=r"(u[20]), "=r"(u[21]), "=r"(u[22]), "=r"(u[23]), "=r"(u[24]), "=r"(u[25]),
+          "=r"(u[26]), "=r"(u[27]), "=r"(u[28]), "=r"(u[29]), "=r"(u[30]), "=r"(u[31]),
+          "=r"(u[32]), "=r"(u[33]), "=r"(u[34]), "=r"(u[35]), "=r"(u[36]), "=r"(u[37]),
+          "=r"(u[38]), "=r"(u[39]), "=r"(u[40]), "=r"(u[41]), "=r"(u[42]), "=r"(u[43]),
+          "=r"(u[44]), "=r"(u[45]), "=r"(u[46]), "=r"(u[47]), "=r"(u[48]), "=r"(u[49]),
+          "=r"(u[50]), "=r"(u[51]), "=r"(u[52]), "=r"(u[53]), "=r"(u[54]), "=r"(u[55]),
+          "=r"(u[56]), "=r"(u[57]), "=r"(u[58]), "=r"(u[59]), "=r"(u[60]), "=r"(u[61]),
+          "=r"(u[62]), "=r"(u[63])
+        : "r"(addr)
+        : "memory");
+}
+
+// One product of 128 x 128 x 128: eight steps of 16.
+__device__ __forceinline__ void scores_product(uint32_t d, uint32_t q, uint32_t k, uint32_t desc)
+{
+#pragma unroll
+    for (int ks = 0; ks < 8; ++ks) {
+        const uint32_t off = (ks >> 2) * kHalfTile + (ks & 3) * 32;
+        tc_mma_ss(d, operand_desc(q + off, 16), operand_desc(k + off, 16), desc, ks > 0);
+    }
+}
+
+__device__ __forceinline__ void values_product(uint32_t d, uint32_t p, uint32_t v, uint32_t desc,
+                                               bool add)
+{
+#pragma unroll
+    for (int ks = 0; ks < 8; ++ks)
+        tc_mma_ts(d, p + 8 * ks, operand_desc(v + ks * 2048, kHalfTile), desc, add || ks > 0);
+}
+
+template <bool FP8, bool SPLIT>
+__global__ void __launch_bounds__(TcConfig<FP8, SPLIT>::kThreads, 1)
+    attn_tc_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ AttnPlan p,
+                   const __grid_constant__ CacheMaps maps)
+{
+    using C = TcConfig<FP8, SPLIT>;
+    extern __shared__ __align__(1024) char smem[];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const uint32_t base = smem_addr(smem);
+    uint32_t *s_mask = reinterpret_cast<uint32_t *>(smem + C::kMask);
+    uint64_t *bars = reinterpret_cast<uint64_t *>(smem + C::kBars);
+    uint64_t *q_full = bars, *k_full = bars + 1, *k_empty = bars + 3, *v_full = bars + 5,
+             *v_empty = bars + 7, *m_full = bars + 9, *s_full = bars + 17, *p_full = bars + 19,
+             *o_full = bars + 21, *r_full = bars + 22, *r_empty = bars + 26;
+    uint32_t *s_tmem = reinterpret_cast<uint32_t *>(smem + C::kMisc);
+    volatile int *s_fail = reinterpret_cast<int *>(smem + C::kMisc + 4);
+
+    const int kvh = blockIdx.y;
+    const int64_t row0 = (int64_t)blockIdx.x * (SPLIT ? 128 : 256);
+    const int64_t key0 = (int64_t)blockIdx.z * p.tc_steps * (SPLIT ? 256 : 128);
+    const int64_t key_end = min(a.n_prefix, key0 + (int64_t)p.tc_steps * (SPLIT ? 256 : 128));
+    const int N = (int)((key_end - key0 + 127) / 128);          // key tiles
+    const int halves = SPLIT ? 2 : (p.rows - row0 > 128 ? 2 : 1);  // that have rows
+
+    if (tid == 0) {
+        *s_fail = base % 1024 != 0;
+        mbar_init(q_full, SPLIT ? 128 : 128 * halves);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&k_full[i], FP8 ? 128 : 1);
+            mbar_init(&k_empty[i], 1);
+            mbar_init(&v_full[i], FP8 ? 128 : 1);
+            mbar_init(&v_empty[i], 1);
+            mbar_init(&s_full[i], 1);
+            mbar_init(&p_full[i], 128);
+        }
+        mbar_init(o_full, 1);
+        for (int i = 0; i < 8; ++i)
+            mbar_init(&m_full[i], 1);
+        for (int i = 0; i < 4; ++i) {
+            mbar_init(&r_full[i], 1);
+            mbar_init(&r_empty[i], 128);
+        }
+        fence_mbar_init();
+    }
+    if (warp == 8)
+        tmem_alloc_all(s_tmem);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *s_tmem;
+    pdl_wait();
+    pdl_launch_dependents();  // after the wait: the next kernel then need not wait before it starts
+
+    if (warp < 8 && !*s_fail) {
+        // ---- softmax: a row a thread -------------------------------------------------------------
+        const int half = warp >> 2;
+        const int64_t rr = row0 + (SPLIT ? 0 : 128 * half) + (tid & 127);
+        const bool act = rr < p.rows;
+        bool seen = false;
+        float scale = 0.0f;
+        if (half < halves) {
+            int i = 0, hg = 0;
+            const int64_t tok = act ? row_token(a, p, rr, i, hg) : 0;
+            seen = act && seq_len(a, rr / p.R) - a.q_len + i >= 0;
+            const char *qp = (const char *)a.q +
+                             2 * (tok * a.q_stride + (int64_t)(kvh * p.group + hg) * kD);
+            float f = 1.0f, inv = 1.0f;
+            if constexpr (FP8) {
+                uint32_t mx = 0u;
+#pragma unroll 4
+                for (int c = 0; c < 16; ++c) {
+                    const uint4 v = act ? ld_cached(qp + 16 * c) : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const uint32_t w = word(v, j);
+                        mx = max(mx, max((w << 16) & 0x7fffffffu, w & 0x7fff0000u));
+                    }
+                }
+                f16_row_factor(mx, f, inv);
+            }
+            scale = __fmul_rn(__fmul_rn(a.sm_scale * a.k_scale, kLog2e), inv);
+            if (!SPLIT || half == 0) {
+                const int r = tid & 127;
+                const uint32_t dst = base + (SPLIT ? 0 : half) * kTile + r * 128;
+#pragma unroll 4
+                for (int c = 0; c < 16; ++c) {
+                    uint4 v = act ? ld_cached(qp + 16 * c) : make_uint4(0u, 0u, 0u, 0u);
+                    if constexpr (FP8) {
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            word(v, j) = pack_f16x2(__fmul_rn(bf_lo(word(v, j)), f),
+                                                    __fmul_rn(bf_hi(word(v, j)), f));
+                    }
+                    sts128(dst + (c >> 3) * kHalfTile + 16 * ((c & 7) ^ (r & 7)), v);
+                }
+                fence_async_shared();
+                mbar_arrive(q_full);
+            }
+        }
+        const int tiles = half >= halves ? 0 : (SPLIT ? (N + 1 - half) / 2 : N);
+        const uint32_t s_at = tmem + half * 128 + ((uint32_t)(warp & 3) << 21);
+        const uint32_t o_at = s_at - half * 128 + 256 + half * 128;
+        float m = -INFINITY, l = 0.0f;
+        bool ok = true;
+        for (int j = 0; j < tiles; ++j) {
+            const int i = SPLIT ? 2 * j + half : j;
+            ok = mbar_wait_or_fail(&m_full[i & 7], (i >> 3) & 1, s_fail) &&
+                 mbar_wait_or_fail(&s_full[half], j & 1, s_fail);
+            if (!__all_sync(0xffffffffu, ok)) {
+                ok = false;
+                break;
+            }
+            tc_fence_after();
+            uint32_t mask[4];
+#pragma unroll
+            for (int w = 0; w < 4; ++w)
+                mask[w] = s_mask[4 * (i & 7) + w];
+            const bool all = (mask[0] & mask[1] & mask[2] & mask[3]) == 0xffffffffu;
+            float r[64];
+            float mx0 = -INFINITY, mx1 = -INFINITY;
+            load64(s_at, r);
+            if (!all) {
+#pragma unroll
+                for (int c = 0; c < 64; ++c)
+                    r[c] = (mask[c >> 5] >> (c & 31)) & 1u ? r[c] : -INFINITY;
+            }
+#pragma unroll
+            for (int c = 0; c < 64; c += 2) {
+                mx0 = fmaxf(mx0, r[c]);
+                mx1 = fmaxf(mx1, r[c + 1]);
+            }
+            load64(s_at + 64, r);
+            if (!all) {
+#pragma unroll
+                for (int c = 0; c < 64; ++c)
+                    r[c] = (mask[2 + (c >> 5)] >> (c & 31)) & 1u ? r[c] : -INFINITY;
+            }
+#pragma unroll
+            for (int c = 0; c < 64; c += 2) {
+                mx0 = fmaxf(mx0, r[c]);
+                mx1 = fmaxf(mx1, r[c + 1]);
+            }
+            const float mx = __fmul_rn(fmaxf(mx0, mx1), scale);
+            const bool raise = mx > __fadd_rn(m, kRaise);
+            if (__any_sync(0xffffffffu, raise)) {
+                const float mn = raise ? mx : m;
+                const float f = m == mn ? 1.0f : exp2_fast(__fsub_rn(m, mn));
+                l = __fmul_rn(l, f);
+                m = mn;
+                if (j > 0) {  // the last product with the values is complete: s_full came after it
+                    float o[64];
+#pragma unroll 1
+                    for (int h = 0; h < 2; ++h) {
+                        // keep the scores in r: they are read again below
+                        load64(o_at + 64 * h, o);
+#pragma unroll
+                        for (int c = 0; c < 64; ++c)
+                            o[c] = __fmul_rn(o[c], f);
+                        tmem_st32(o_at + 64 * h, *reinterpret_cast<uint32_t(*)[32]>(&o[0]));
+                        tmem_st32(o_at + 64 * h + 32, *reinterpret_cast<uint32_t(*)[32]>(&o[32]));
+                    }
+                    load64(s_at + 64, r);
+                    if (!all) {
+#pragma unroll
+                        for (int c = 0; c < 64; ++c)
+                            r[c] = (mask[2 + (c >> 5)] >> (c & 31)) & 1u ? r[c] : -INFINITY;
+                    }
+                }
+            }
+            const float neg = m == -INFINITY ? 0.0f : -m;
+            f2 sum = 0ull;
+#pragma unroll
+            for (int h = 1; h >= 0; --h) {  // the second half is in registers and makes room first
+                if (h == 0) {
+                    load64(s_at, r);
+                    if (!all) {
+#pragma unroll
+                        for (int c = 0; c < 64; ++c)
+                            r[c] = (mask[c >> 5] >> (c & 31)) & 1u ? r[c] : -INFINITY;
+                    }
+                }
+                uint32_t w[32];
+#pragma unroll
+                for (int c = 0; c < 32; ++c) {
+                    const float e0 = exp2_fast(__fmaf_rn(r[2 * c], scale, neg));
+                    const float e1 = exp2_fast(__fmaf_rn(r[2 * c + 1], scale, neg));
+                    sum = add2(sum, make_f2(e0, e1));
+                    w[c] = FP8 ? pack_f16x2(e0, e1) : pack_bf16x2(e0, e1);
+                }
+                tmem_st32(s_at + 64 + 32 * h, w);
+            }
+            l = __fadd_rn(l, __fadd_rn(lo_of(sum), hi_of(sum)));
+            tmem_wait_st();
+            tc_fence_before();
+            mbar_arrive(&p_full[half]);
+        }
+        // ---- the part ----------------------------------------------------------------------------
+        if (half < halves && ok && mbar_wait_or_fail(o_full, 0, s_fail)) {
+            tc_fence_after();
+            const int part = SPLIT ? 2 * blockIdx.z + half : blockIdx.z;
+            const int64_t at = ((int64_t)kvh * p.rows + rr) * p.tc_parts + part;
+            float *po = reinterpret_cast<float *>(a.workspace + p.tc_o_off) + at * kD;
+            if (tiles > 0) {
+#pragma unroll 1
+                for (int h = 0; h < 2; ++h) {
+                    float r[64];
+                    load64(o_at + 64 * h, r);
+                    if (act) {
+#pragma unroll
+                        for (int c = 0; c < 64; c += 4)
+                            *reinterpret_cast<float4 *>(po + 64 * h + c) =
+                                make_float4(r[c], r[c + 1], r[c + 2], r[c + 3]);
+                    }
+                }
+            }
+            if (act)
+                reinterpret_cast<float2 *>(a.workspace + p.tc_ml_off)[at] =
+                    make_float2(seen ? m : -INFINITY, seen ? l : 0.0f);
+        }
+    } else if (warp == 8 && !*s_fail) {
+        // ---- the products ------------------------------------------------------------------------
+        if (lane == 0) {
+            constexpr uint32_t dqk = mma_desc(FP8, false), dpv = mma_desc(FP8, true);
+            const uint32_t kt = base + C::kK, vt = base + C::kV;
+            bool ok = mbar_wait_or_fail(q_full, 0, s_fail);
+            auto wait_k = [&](int i) {
+                ok = ok && mbar_wait_or_fail(&k_full[i & 1], (i >> 1) & 1, s_fail);
+            };
+            auto qk = [&](int half, int i) {
+                tc_fence_after();
+                scores_product(tmem + half * 128, base + (SPLIT ? 0 : half) * kTile,
+                               kt + (i & 1) * kTile, dqk);
+                tc_commit(&s_full[half]);
+            };
+            auto pv = [&](int half, int j, int i) {
+                tc_fence_after();
+                values_product(tmem + 256 + half * 128, tmem + half * 128 + 64,
+                               vt + (i & 1) * kTile, dpv, j > 0);
+            };
+            if constexpr (SPLIT) {
+                for (int i = 0; i < 2 && i < N && ok; ++i) {
+                    wait_k(i);
+                    if (!ok)
+                        break;
+                    qk(i, i);
+                    tc_commit(&k_empty[i]);
+                }
+                for (int i = 0; i < N && ok; ++i) {
+                    const int half = i & 1, j = i >> 1;
+                    ok = mbar_wait_or_fail(&v_full[i & 1], (i >> 1) & 1, s_fail) &&
+                         mbar_wait_or_fail(&p_full[half], j & 1, s_fail);
+                    if (!ok)
+                        break;
+                    pv(half, j, i);
+                    tc_commit(&v_empty[i & 1]);
+                    if (i + 2 < N) {
+                        wait_k(i + 2);
+                        if (!ok)
+                            break;
+                        qk(half, i + 2);
+                        tc_commit(&k_empty[i & 1]);
+                    }
+                }
+            } else {
+                wait_k(0);
+                if (ok) {
+                    for (int h = 0; h < halves; ++h)
+                        qk(h, 0);
+                    tc_commit(&k_empty[0]);
+                }
+                for (int i = 0; i < N && ok; ++i)
+                    for (int h = 0; h < halves && ok; ++h) {
+                        if (h == 0)
+                            ok = mbar_wait_or_fail(&v_full[i & 1], (i >> 1) & 1, s_fail);
+                        ok = ok && mbar_wait_or_fail(&p_full[h], i & 1, s_fail);
+                        if (!ok)
+                            break;
+                        pv(h, i, i);
+                        if (h == halves - 1)
+                            tc_commit(&v_empty[i & 1]);
+                        if (i + 1 < N) {
+                            if (h == 0)
+                                wait_k(i + 1);
+                            if (!ok)
+                                break;
+                            qk(h, i + 1);
+                            if (h == halves - 1)
+                                tc_commit(&k_empty[(i + 1) & 1]);
+                        }
+                    }
+            }
+            if (ok)
+                tc_commit(o_full);
+        }
+        __syncwarp();
+    } else if (warp == 9 && !*s_fail) {
+        // ---- copies: K(0), (K(1),) then V(i), K(i + ahead) in turn, as the products take them -------
+        constexpr int ahead = SPLIT ? 2 : 1;
+        int slot_k[4], slot_v[4];
+        auto slots = [&](int i, int (&s)[4]) {  // this lane's four keys of tile i
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int64_t key = key0 + (int64_t)i * 128 + 4 * lane + j;
+                const int64_t x = i < N && key < key_end ? a.prefix[key] : -1;
+                s[j] = x >= 0 && x < a.num_slots ? (int)x : -1;
+            }
+        };
+        int raw = 0;  // FP8: copies so far
+        bool ok = true;
+        auto copy = [&](bool v, int i, const int (&s)[4]) {
+            if constexpr (FP8) {
+                const int st = raw % C::kRaw;
+                ok = ok && mbar_wait_or_fail(&r_empty[st], ((raw / C::kRaw) & 1) ^ 1, s_fail);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok)
+                    return;
+                if (lane == 0)
+                    mbar_arrive_expect_tx(&r_full[st], kRawTile);
+                __syncwarp();
+                gather4(base + C::kRawAt + st * kRawTile + lane * 512, v ? &maps.v : &maps.k,
+                        kvh * kD, s[0], s[1], s[2], s[3], &r_full[st]);
+                ++raw;
+            } else {
+                uint64_t *full = v ? &v_full[i & 1] : &k_full[i & 1];
+                ok = ok && mbar_wait_or_fail(v ? &v_empty[i & 1] : &k_empty[i & 1],
+                                             ((i >> 1) & 1) ^ 1, s_fail);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok)
+                    return;
+                if (lane == 0)
+                    mbar_arrive_expect_tx(full, kTile);
+                __syncwarp();
+                const uint32_t dst = base + (v ? C::kV : C::kK) + (i & 1) * kTile + lane * 512;
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+                    gather4(dst + h * kHalfTile, v ? &maps.v : &maps.k, kvh * kD + 64 * h, s[0],
+                            s[1], s[2], s[3], full);
+            }
+        };
+        auto copy_k = [&](int i) {
+            if (i >= N)
+                return;
+            copy(false, i, slot_k);
+            // The tile's mask.  Its place was last used by tile i - 8: this copy waited for the scores
+            // of tile i - 4 or a later one to be complete, so the softmax warps have left tile i - 6.
+            uint32_t bits = 0;
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                bits |= slot_k[j] >= 0 ? 1u << (4 * (lane & 7) + j) : 0u;
+            bits |= __shfl_xor_sync(0xffffffffu, bits, 1);
+            bits |= __shfl_xor_sync(0xffffffffu, bits, 2);
+            bits |= __shfl_xor_sync(0xffffffffu, bits, 4);
+            if (!ok)
+                return;
+            if ((lane & 7) == 0)
+                s_mask[4 * (i & 7) + (lane >> 3)] = bits;
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(&m_full[i & 7]);
+        };
+        for (int i = 0; i < ahead && ok; ++i) {
+            slots(i, slot_k);
+            copy_k(i);
+        }
+        slots(0, slot_v);
+        slots(ahead, slot_k);
+        for (int i = 0; i < N && ok; ++i) {
+            int next_v[4], next_k[4];
+            slots(i + 1, next_v);
+            slots(i + 1 + ahead, next_k);
+            copy(true, i, slot_v);
+            if (ok)
+                copy_k(i + ahead);
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                slot_v[j] = next_v[j], slot_k[j] = next_k[j];
+        }
+    } else if (FP8 && warp >= 10 && !*s_fail) {
+        // ---- FP8 to FP16, tile by tile in the copies' order ---------------------------------------
+        constexpr int ahead = SPLIT ? 2 : 1;
+        const int ct = tid - 320;
+        int raw = 0;
+        bool ok = true;
+        auto expand = [&](bool v, int i) {
+            const int st = raw % (C::kRaw > 0 ? C::kRaw : 1);
+            ok = ok && mbar_wait_or_fail(&r_full[st], (raw / (C::kRaw > 0 ? C::kRaw : 1)) & 1, s_fail) &&
+                 mbar_wait_or_fail(v ? &v_empty[i & 1] : &k_empty[i & 1], ((i >> 1) & 1) ^ 1, s_fail);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok)
+                return;
+            const uint32_t src = base + C::kRawAt + st * kRawTile;
+            const uint32_t dst = base + (v ? C::kV : C::kK) + (i & 1) * kTile;
+#pragma unroll 4
+            for (int x = 0; x < 8; ++x) {
+                // eight lanes: four chunks of an even and of the next row (stores without conflicts)
+                const int idx = x * 128 + ct;
+                const int c = (idx & 3) + 4 * ((idx >> 9) & 1), r = (idx >> 2) & 127;
+                const uint4 b = lds128(src + r * 128 + 16 * (c ^ (r & 7)));
+                const uint4 lo = make_uint4(e4m3x2_to_f16x2(b.x), e4m3x2_to_f16x2(b.x >> 16),
+                                            e4m3x2_to_f16x2(b.y), e4m3x2_to_f16x2(b.y >> 16));
+                const uint4 hi = make_uint4(e4m3x2_to_f16x2(b.z), e4m3x2_to_f16x2(b.z >> 16),
+                                            e4m3x2_to_f16x2(b.w), e4m3x2_to_f16x2(b.w >> 16));
+                const uint32_t at = dst + (c >> 2) * kHalfTile + r * 128;
+                sts128(at + 16 * ((2 * (c & 3)) ^ (r & 7)), lo);
+                sts128(at + 16 * ((2 * (c & 3) + 1) ^ (r & 7)), hi);
+            }
+            fence_async_shared();
+            mbar_arrive(v ? &v_full[i & 1] : &k_full[i & 1]);
+            mbar_arrive(&r_empty[st]);
+            ++raw;
+        };
+        for (int i = 0; i < ahead && i < N && ok; ++i)
+            expand(false, i);
+        for (int i = 0; i < N && ok; ++i) {
+            expand(true, i);
+            if (i + ahead < N && ok)
+                expand(false, i + ahead);
+        }
+    }
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    if (*s_fail) {
+        // a wait ran out: what is in flight ends before the block does (a bounded wait)
+        const unsigned long long t0 = global_ns();
+        while (global_ns() - t0 < kWaitLimitNs / 4) {
+        }
+        if (tid == 0)
+            atomicOr(&g_tc_fault_word, kFaultCopyTimeout);
+        __syncthreads();
+    }
+    tc_fence_after();
+    if (warp == 8)
+        tmem_free_all(tmem);
+}
+
+template <bool FP8, bool SPLIT>
+cudaError_t launch(const AttnArgs &a, const AttnPlan &p, const CacheMaps &maps, cudaStream_t stream)
+{
+    constexpr int bytes = TcConfig<FP8, SPLIT>::kBytes;
+    const cudaError_t e = allow_smem<attn_tc_kernel<FP8, SPLIT>>(bytes);
+    if (e != cudaSuccess)
+        return e;
+    return launch_pdl(attn_tc_kernel<FP8, SPLIT>,
+                      dim3((unsigned)p.tc_rtiles, (unsigned)a.n_kv, (unsigned)p.tc_blocks),
+                      dim3(TcConfig<FP8, SPLIT>::kThreads), bytes, stream, a, p, maps);
+}
+
+}  // namespace
+
+cudaError_t launch_attn_tc(const AttnArgs &a, const AttnPlan &p, const CacheMaps &maps,
+                           cudaStream_t stream)
+{
+    if (a.fp8)
+        return p.tc_split ? launch<true, true>(a, p, maps, stream)
+                          : launch<true, false>(a, p, maps, stream);
+    return p.tc_split ? launch<false, true>(a, p, maps, stream)
+                      : launch<false, false>(a, p, maps, stream);
+}
+
+cudaError_t read_attn_tc_fault_word(unsigned int *value, bool clear)
+{
+    cudaError_t e = cudaMemcpyFromSymbol(value, g_tc_fault_word, sizeof(unsigned int));
+    if (e == cudaSuccess && clear) {
+        const unsigned int zero = 0u;
+        e = cudaMemcpyToSymbol(g_tc_fault_word, &zero, sizeof(unsigned int));
+    }
+    return e;
+}
+
+}  // namespace beam

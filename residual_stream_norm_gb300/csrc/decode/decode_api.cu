@@ -41,9 +41,15 @@ int64_t beam_attn_prefix_workspace(int32_t B, int32_t q_len, int32_t n_q_heads, 
         check_attn_sizes(B, q_len, n_q_heads, n_kv_heads, n_prefix, table_width, window);
     if (st != BEAM_OK || B == 0)
         return st;
-    return beam::attn_plan(B, q_len, n_q_heads, n_kv_heads, n_prefix, table_width, window,
-                           key_weights != 0, false)
-        .bytes;
+    // the larger of what the call takes with and without the tensor-core kernel
+    int64_t most = 0;
+    for (int tc = 0; tc < 2; ++tc) {
+        const int64_t bytes = beam::attn_plan(B, q_len, n_q_heads, n_kv_heads, n_prefix,
+                                              table_width, window, key_weights != 0, false, tc != 0)
+                                  .bytes;
+        most = bytes > most ? bytes : most;
+    }
+    return most;
 }
 
 int beam_attn_prefix_fwd(void *out, int64_t out_row_stride, float *lse_out,
@@ -80,11 +86,17 @@ int beam_attn_prefix_fwd(void *out, int64_t out_row_stride, float *lse_out,
         !aligned(slot_table, 8) || !aligned(suffix_len, 4) || !aligned(lse_out, 4) ||
         !aligned(key_weight_in, 4) || !aligned(key_weight_out, 4) || !aligned(workspace, 16))
         return BEAM_ERR_MISALIGNED;
+    if (workspace_bytes < beam_attn_prefix_workspace(B, q_len, n_q_heads, n_kv_heads, n_prefix,
+                                                     table_width, window, key_weight_out != nullptr))
+        return BEAM_ERR_INVALID_ARG;
+    // a longer window than any list is none
+    window = window > n_prefix + table_width ? 0 : window;
+    // the tensor-core kernel takes the largest score before the scale and scales masked scores of
+    // -inf: the scale must keep order and not underflow
+    const float scale = sm_scale * (cache_dtype == 1 ? k_scale : 1.0f);
     const beam::AttnPlan p = beam::attn_plan(B, q_len, n_q_heads, n_kv_heads, n_prefix,
                                              table_width, window, key_weight_out != nullptr,
-                                             cache_dtype == 1);
-    if (workspace_bytes < p.bytes)
-        return BEAM_ERR_INVALID_ARG;
+                                             cache_dtype == 1, scale > 1.0e-15f);
     beam::AttnArgs a{};
     a.out = out;
     a.out_stride = out_row_stride;
@@ -111,8 +123,7 @@ int beam_attn_prefix_fwd(void *out, int64_t out_row_stride, float *lse_out,
     a.n_q = n_q_heads;
     a.n_kv = n_kv_heads;
     a.sm_scale = sm_scale;
-    // a longer window than any list is none
-    a.window = window > n_prefix + table_width ? 0 : window;
+    a.window = window;
     a.workspace = (char *)workspace;
     return cuda_status(beam::launch_attn_prefix(a, p, stream));
 }

@@ -54,14 +54,22 @@ struct AttnPlan {
     int64_t p_tiles;      // key tiles of a prefix unit
     int64_t units;        // all units
     int32_t ctas;
+    // the tensor-core kernel (tc_parts 0: not used): tiles of rows, blocks along the keys, steps of a
+    // block (128 keys; 256 with tc_split), and parts that it leaves of each row
+    int32_t tc_rtiles, tc_blocks, tc_steps, tc_parts;
+    bool tc_split;
     int64_t score_width;  // padded width of the score rows (key weights only)
     // workspace, in bytes from its start
-    int64_t cum_off, o_off, ml_off, lse_off, score_off, bytes;
+    int64_t cum_off, o_off, ml_off, lse_off, tc_o_off, tc_ml_off, score_off, bytes;
 };
 
 AttnPlan attn_plan(int32_t B, int32_t q_len, int32_t n_q, int32_t n_kv, int64_t n_prefix,
-                   int64_t width, int64_t window, bool weights, bool fp8);
+                   int64_t width, int64_t window, bool weights, bool fp8, bool tc);
 cudaError_t launch_attn_prefix(const AttnArgs &a, const AttnPlan &p, cudaStream_t stream);
+struct CacheMaps;
+cudaError_t launch_attn_tc(const AttnArgs &a, const AttnPlan &p, const CacheMaps &maps,
+                           cudaStream_t stream);
+cudaError_t read_attn_tc_fault_word(unsigned int *value, bool clear);
 // The decode operators' fault word of the current device (as read_fault_word).
 cudaError_t read_decode_fault_word(unsigned int *value, bool clear);
 
