@@ -16,6 +16,19 @@ __device__ __forceinline__ int64_t seq_len(const AttnArgs &a, int64_t b)
     return n < 0 ? 0 : (n > a.width ? a.width : n);
 }
 
+// The keys that any row of a sequence of n entries sees: [first, n).
+__device__ __forceinline__ int64_t first_key(int64_t n, int q_len, int64_t window)
+{
+    const int64_t lo = n - q_len + 1 - window;
+    return window > 0 && lo > 0 ? lo : 0;
+}
+
+// The same from a multiple of 16 on, where runs of slots are taken to start.
+__device__ __forceinline__ int64_t first_tile_key(int64_t n, int q_len, int64_t window)
+{
+    return first_key(n, q_len, window) & ~(int64_t)15;
+}
+
 // Factor 2^k, k <= 60, that brings a row of largest magnitude bits `mx` (FP32) to [2^14, 2^15), and
 // its inverse; 1 for zero, infinite and NaN rows.
 __device__ __forceinline__ void f16_row_factor(uint32_t mx, float &f, float &inv)

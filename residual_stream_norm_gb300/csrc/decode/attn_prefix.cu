@@ -56,17 +56,10 @@ __device__ __forceinline__ int64_t owner(int64_t x, int64_t tot, int64_t ctas)
     return ((x + 1) * ctas - 1) / tot;
 }
 
-// The keys that any row of a sequence of n entries sees: [first, n).
-__device__ __forceinline__ int64_t first_key(int64_t n, int q_len, int64_t window)
-{
-    const int64_t lo = n - q_len + 1 - window;
-    return window > 0 && lo > 0 ? lo : 0;
-}
-
 __device__ __forceinline__ int64_t seq_tiles(const AttnArgs &a, const AttnPlan &p, int64_t b)
 {
     const int64_t n = seq_len(a, b);
-    return (n - first_key(n, a.q_len, a.window) + p.tile_keys - 1) / p.tile_keys;
+    return (n - first_tile_key(n, a.q_len, a.window) + p.tile_keys - 1) / p.tile_keys;
 }
 
 // The A fragments of V^T for 16 elements d and 16 keys.  BF16 (`mt`: which 16 elements): matrix row is
@@ -164,7 +157,7 @@ __device__ __forceinline__ Unit next_unit(const AttnArgs &a, const AttnPlan &p, 
         u.row_end = (int32_t)((c.b + 1) * p.R);
         u.list = a.table + c.b * a.table_stride;
         u.key_end = (int32_t)seq_len(a, c.b);
-        key_first = (int32_t)first_key(u.key_end, a.q_len, a.window);
+        key_first = (int32_t)first_tile_key(u.key_end, a.q_len, a.window);
     }
     const int64_t seg_end = min(c.end, start + tiles);
     u.whole = c.tile == start && seg_end == start + tiles;
@@ -243,6 +236,8 @@ __global__ void __launch_bounds__(kThreads, 2)
         fence_mbar_init();
         prefetch_map(&maps.k);
         prefetch_map(&maps.v);
+        prefetch_map(&maps.k_run);
+        prefetch_map(&maps.v_run);
     }
     __syncwarp();
     pdl_launch_dependents();
@@ -306,20 +301,37 @@ __global__ void __launch_bounds__(kThreads, 2)
         masks[0] = __ballot_sync(0xffffffffu, slot >= 0);
         if (have) {
             const uint32_t dst = wbuf + in_stage * C::kStageBytes;
-            // lanes 0..15: four keys each of K or V; a slot of -1 is out of the map and gives zeros
-            const int grp = FP8 ? lane & 7 : lane & 3, half = FP8 ? 0 : (lane >> 2) & 1;
-            const int isv = (lane >> 3) & 1;
-            const int y0 = __shfl_sync(0xffffffffu, slot, 4 * grp);
-            const int y1 = __shfl_sync(0xffffffffu, slot, 4 * grp + 1);
-            const int y2 = __shfl_sync(0xffffffffu, slot, 4 * grp + 2);
-            const int y3 = __shfl_sync(0xffffffffu, slot, 4 * grp + 3);
             if (lane == 0)
                 mbar_arrive_expect_tx(&bars[in_stage], C::kStageBytes);
-            __syncwarp();
-            if (lane < 16)
-                gather4(dst + isv * C::kValues + half * C::kHalf + grp * 512,
-                        isv ? &maps.v : &maps.k, lu.kvh * kD + half * 64, y0, y1, y2, y3,
-                        &bars[in_stage]);
+            // runs of 16 slots go as one copy, other slots four by four (one of -1 is out of the map
+            // and gives zeros)
+            const int s0 = __shfl_sync(0xffffffffu, slot, FP8 ? lane & 16 : 0);
+            const uint32_t in_run = __ballot_sync(
+                0xffffffffu, s0 >= 0 && slot == s0 + (FP8 ? lane & 15 : lane));
+            const uint32_t in_map = __ballot_sync(0xffffffffu, s0 >= 0 && s0 + 15 < a.num_slots);
+            const int x = lu.kvh * kD;
+            if (FP8 ? in_run == 0xffffffffu && in_map == 0xffffffffu
+                    : (in_run & 0xffffu) == 0xffffu && (in_map & 1u)) {
+                // lanes 0..3: K and V of the two halves of the head (BF16) or of the two runs (FP8)
+                const int sub = lane & 1, isv = lane >> 1;
+                const int y = __shfl_sync(0xffffffffu, slot, FP8 ? 16 * sub : 0);
+                if (lane < 4)
+                    copy_run(dst + isv * C::kValues + sub * C::kHalf,
+                             isv ? &maps.v_run : &maps.k_run, FP8 ? x : x + 64 * sub, y,
+                             &bars[in_stage]);
+            } else {
+                // lanes 0..15: four keys each of K or V
+                const int grp = FP8 ? lane & 7 : lane & 3, half = FP8 ? 0 : (lane >> 2) & 1;
+                const int isv = (lane >> 3) & 1;
+                const int y0 = __shfl_sync(0xffffffffu, slot, 4 * grp);
+                const int y1 = __shfl_sync(0xffffffffu, slot, 4 * grp + 1);
+                const int y2 = __shfl_sync(0xffffffffu, slot, 4 * grp + 2);
+                const int y3 = __shfl_sync(0xffffffffu, slot, 4 * grp + 3);
+                if (lane < 16)
+                    gather4(dst + isv * C::kValues + half * C::kHalf + grp * 512,
+                            isv ? &maps.v : &maps.k, x + half * 64, y0, y1, y2, y3,
+                            &bars[in_stage]);
+            }
             ++ls;
         }
         in_stage = in_stage + 1 == C::kStages ? 0 : in_stage + 1;
@@ -977,8 +989,7 @@ AttnPlan attn_plan(int32_t B, int32_t q_len, int32_t n_q, int32_t n_kv, int64_t 
     p.R = q_len * p.group;
     p.rows = (int64_t)B * p.R;
     p.p_first = window > 0 && n_prefix + 1 > window ? n_prefix + 1 - window : 0;
-    if (p.p_first > n_prefix)
-        p.p_first = n_prefix;
+    p.p_first = (p.p_first < n_prefix ? p.p_first : n_prefix) & ~(int64_t)15;
     const int64_t p_keys = n_prefix - p.p_first;
     if (tc && window == 0 && p.rows >= kTcRows && n_prefix >= kTcKeys)
         plan_tc(p, n_kv, n_prefix);
@@ -991,7 +1002,7 @@ AttnPlan attn_plan(int32_t B, int32_t q_len, int32_t n_q, int32_t n_kv, int64_t 
     p.units = n_kv * (p.p_rtiles + (int64_t)B * p.s_rtiles);
     int64_t keys = width;
     if (window > 0 && window + q_len - 1 < keys)
-        keys = window + q_len - 1;
+        keys = window + q_len - 1 + 15;
     const int64_t tiles =
         n_kv * (p.p_rtiles * p.p_tiles +
                 (int64_t)B * p.s_rtiles * ((keys + p.tile_keys - 1) / p.tile_keys));

@@ -388,13 +388,31 @@ __global__ void __launch_bounds__(TcConfig<FP8, SPLIT>::kThreads, 1)
     } else if (warp == 9 && !*s_fail) {
         // ---- copies: K(0), (K(1),) then V(i), K(i + ahead) in turn, as the products take them -------
         constexpr int ahead = SPLIT ? 2 : 1;
-        int slot_k[4], slot_v[4];
-        auto slots = [&](int i, int (&s)[4]) {  // this lane's four keys of tile i
+        int slot[ahead + 2][4];  // this lane's four keys of tiles i, i + 1, ...
+        auto fetch = [&](int i, int64_t (&x)[4]) {
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 const int64_t key = key0 + (int64_t)i * 128 + 4 * lane + j;
-                const int64_t x = i < N && key < key_end ? a.prefix[key] : -1;
-                s[j] = x >= 0 && x < a.num_slots ? (int)x : -1;
+                x[j] = i < N && key < key_end ? a.prefix[key] : -1;
+            }
+        };
+        auto check = [&](const int64_t (&x)[4], int (&s)[4]) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                s[j] = x[j] >= 0 && x[j] < a.num_slots ? (int)x[j] : -1;
+        };
+        // copies a tile of 128-byte rows: runs of 16 slots as one copy, others four by four
+        auto rows = [&](uint32_t dst, const CUtensorMap *run, const CUtensorMap *four, int x,
+                        const int (&s)[4], bool mine, uint64_t *bar) {
+            const int s0 = __shfl_sync(0xffffffffu, s[0], lane & ~3);
+            const bool in = s0 >= 0 && s0 + 15 < a.num_slots && s[0] == s0 + 4 * (lane & 3) &&
+                            s[1] == s[0] + 1 && s[2] == s[0] + 2 && s[3] == s[0] + 3;
+            const uint32_t all = __ballot_sync(0xffffffffu, in) >> (lane & ~3);
+            if ((all & 15u) == 15u) {
+                if (mine)
+                    copy_run(dst + (lane >> 2) * 2048, run, x, s0, bar);
+            } else {
+                gather4(dst + lane * 512, four, x, s[0], s[1], s[2], s[3], bar);
             }
         };
         int raw = 0;  // FP8: copies so far
@@ -409,8 +427,8 @@ __global__ void __launch_bounds__(TcConfig<FP8, SPLIT>::kThreads, 1)
                 if (lane == 0)
                     mbar_arrive_expect_tx(&r_full[st], kRawTile);
                 __syncwarp();
-                gather4(base + C::kRawAt + st * kRawTile + lane * 512, v ? &maps.v : &maps.k,
-                        kvh * kD, s[0], s[1], s[2], s[3], &r_full[st]);
+                rows(base + C::kRawAt + st * kRawTile, v ? &maps.v_run : &maps.k_run,
+                     v ? &maps.v : &maps.k, kvh * kD, s, (lane & 3) == 0, &r_full[st]);
                 ++raw;
             } else {
                 uint64_t *full = v ? &v_full[i & 1] : &k_full[i & 1];
@@ -422,23 +440,23 @@ __global__ void __launch_bounds__(TcConfig<FP8, SPLIT>::kThreads, 1)
                 if (lane == 0)
                     mbar_arrive_expect_tx(full, kTile);
                 __syncwarp();
-                const uint32_t dst = base + (v ? C::kV : C::kK) + (i & 1) * kTile + lane * 512;
+                const uint32_t dst = base + (v ? C::kV : C::kK) + (i & 1) * kTile;
 #pragma unroll
                 for (int h = 0; h < 2; ++h)
-                    gather4(dst + h * kHalfTile, v ? &maps.v : &maps.k, kvh * kD + 64 * h, s[0],
-                            s[1], s[2], s[3], full);
+                    rows(dst + h * kHalfTile, v ? &maps.v_run : &maps.k_run,
+                         v ? &maps.v : &maps.k, kvh * kD + 64 * h, s, (lane & 3) == h, full);
             }
         };
-        auto copy_k = [&](int i) {
+        auto copy_k = [&](int i, const int (&s)[4]) {
             if (i >= N)
                 return;
-            copy(false, i, slot_k);
+            copy(false, i, s);
             // The tile's mask.  Its place was last used by tile i - 8: this copy waited for the scores
             // of tile i - 4 or a later one to be complete, so the softmax warps have left tile i - 6.
             uint32_t bits = 0;
 #pragma unroll
             for (int j = 0; j < 4; ++j)
-                bits |= slot_k[j] >= 0 ? 1u << (4 * (lane & 7) + j) : 0u;
+                bits |= s[j] >= 0 ? 1u << (4 * (lane & 7) + j) : 0u;
             bits |= __shfl_xor_sync(0xffffffffu, bits, 1);
             bits |= __shfl_xor_sync(0xffffffffu, bits, 2);
             bits |= __shfl_xor_sync(0xffffffffu, bits, 4);
@@ -450,22 +468,27 @@ __global__ void __launch_bounds__(TcConfig<FP8, SPLIT>::kThreads, 1)
             if (lane == 0)
                 mbar_arrive(&m_full[i & 7]);
         };
-        for (int i = 0; i < ahead && ok; ++i) {
-            slots(i, slot_k);
-            copy_k(i);
-        }
-        slots(0, slot_v);
-        slots(ahead, slot_k);
-        for (int i = 0; i < N && ok; ++i) {
-            int next_v[4], next_k[4];
-            slots(i + 1, next_v);
-            slots(i + 1 + ahead, next_k);
-            copy(true, i, slot_v);
-            if (ok)
-                copy_k(i + ahead);
+        int64_t x[4];
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-                slot_v[j] = next_v[j], slot_k[j] = next_k[j];
+        for (int i = 0; i <= ahead; ++i) {
+            fetch(i, x);
+            check(x, slot[i]);
+        }
+#pragma unroll
+        for (int i = 0; i < ahead; ++i)
+            if (ok)
+                copy_k(i, slot[i]);
+        for (int i = 0; i < N && ok; ++i) {
+            fetch(i + ahead + 1, x);  // arrives while the copies are issued
+            copy(true, i, slot[0]);
+            if (ok)
+                copy_k(i + ahead, slot[ahead]);
+            check(x, slot[ahead + 1]);
+#pragma unroll
+            for (int k = 0; k <= ahead; ++k)
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    slot[k][j] = slot[k + 1][j];
         }
     } else if (FP8 && warp >= 10 && !*s_fail) {
         // ---- FP8 to FP16, tile by tile in the copies' order ---------------------------------------

@@ -11,9 +11,14 @@
 namespace beam {
 
 // Maps of the K and V caches as matrices [num_slots, n_kv * 128] for copies of 128 bytes of one
-// head's row (64 BF16 or 128 FP8 elements), 128-byte swizzle.
+// head's row (64 BF16 or 128 FP8 elements), 128-byte swizzle: of four rows by slot (k, v), and of
+// kRun rows of consecutive slots (k_run, v_run).  A gather takes the copy engine about 30 cycles, a
+// quarter more than four rows take to arrive at the memory's full rate, so runs of slots, which is
+// what a paged allocator hands out, go as one copy.
+constexpr int kRun = 16;
+
 struct CacheMaps {
-    CUtensorMap k, v;
+    CUtensorMap k, v, k_run, v_run;
 };
 
 __device__ __forceinline__ void prefetch_map(const CUtensorMap *map)
@@ -30,6 +35,18 @@ __device__ __forceinline__ void gather4(uint32_t dst, const CUtensorMap *map, in
         "cp.async.bulk.tensor.2d.shared::cta.global.tile::gather4.mbarrier::complete_tx::bytes "
         "[%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(dst),
         "l"(map), "r"(x), "r"(y0), "r"(y1), "r"(y2), "r"(y3), "r"(smem_addr(bar))
+        : "memory");
+}
+
+// kRun rows of consecutive slots from y on, to dst, a multiple of 1024:
+// kRun * 128 bytes of transactions.
+__device__ __forceinline__ void copy_run(uint32_t dst, const CUtensorMap *map, int x, int y,
+                                         uint64_t *bar)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cta.global.tile.mbarrier::complete_tx::bytes "
+        "[%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+        "l"(map), "r"(x), "r"(y), "r"(smem_addr(bar))
         : "memory");
 }
 
@@ -64,15 +81,18 @@ inline cudaError_t make_cache_maps(CacheMaps &maps, const AttnArgs &a)
     const cuuint64_t cols = (cuuint64_t)a.n_kv * 128;
     const cuuint64_t dims[2] = {cols, (cuuint64_t)(a.num_slots > 0 ? a.num_slots : 1)};
     const cuuint64_t strides[1] = {cols * (fp8 ? 1 : 2)};
-    const cuuint32_t box[2] = {fp8 ? 128u : 64u, 1u}, ones[2] = {1u, 1u};
-    for (int i = 0; i < 2; ++i)
-        if (encode(i ? &maps.v : &maps.k,
+    const cuuint32_t ones[2] = {1u, 1u};
+    CUtensorMap *all[4] = {&maps.k, &maps.v, &maps.k_run, &maps.v_run};
+    for (int i = 0; i < 4; ++i) {
+        const cuuint32_t box[2] = {fp8 ? 128u : 64u, i < 2 ? 1u : (cuuint32_t)kRun};
+        if (encode(all[i],
                    fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2,
-                   const_cast<void *>(i ? v : k), dims, strides, box, ones,
+                   const_cast<void *>(i & 1 ? v : k), dims, strides, box, ones,
                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                    CU_TENSOR_MAP_L2_PROMOTION_NONE,
                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
             return cudaErrorInvalidValue;
+    }
     return cudaSuccess;
 }
 
