@@ -270,23 +270,31 @@ __global__ void __launch_bounds__(kThreads, 2)
     // ---- the copies: this warp's steps of every unit of the share, ahead of the arithmetic -----------
     Cursor ahead = at;
     Unit lu;
-    int ls = 0, lsteps = 0, slot = -1;
+    int ls = 0, lsteps = 0;
     auto steps_of = [&](const Unit &u) {
         return (u.k1 - u.k0 - warp * C::kKeys + C::kTileKeys - 1) / C::kTileKeys;
     };
-    auto fetch_slot = [&]() {  // lane i: slot of the next step's key i, or -1
+    // The slots of a step are loaded two steps before its copies are issued, and only looked at
+    // then: a load that is waited for at once held every step up by its latency.
+    struct Fetched {
+        int64_t slot;  // lane i: of key i, or -1
+        int32_t kvh;
+        bool have;
+    };
+    auto fetch = [&]() {
         while (ls >= lsteps && ahead.tile < ahead.end) {
             lu = next_unit(a, p, M, ahead);
             ls = 0;
             lsteps = steps_of(lu);
         }
-        slot = -1;
         const int key = lu.k0 + ls * C::kTileKeys + warp * C::kKeys + lane;
-        if (ls < lsteps && lane < C::kKeys && key < lu.k1) {
-            const int64_t x = lu.list[key];
-            slot = x >= 0 && x < a.num_slots ? (int)x : -1;
-        }
+        Fetched f{-1, lu.kvh, ls < lsteps};
+        if (f.have && lane < C::kKeys && key < lu.k1)
+            f.slot = lu.list[key];
+        ++ls;
+        return f;
     };
+    Fetched next = fetch(), second = fetch();
     uint32_t masks[C::kStages];  // which keys of the stages in flight exist; the newest first
 #pragma unroll
     for (int i = 0; i < C::kStages; ++i)
@@ -294,7 +302,8 @@ __global__ void __launch_bounds__(kThreads, 2)
     int in_stage = 0;
     bool failed = false;  // a wait of this warp ran out: it copies nothing more
     auto issue = [&]() {
-        const bool have = ls < lsteps && !failed;
+        const bool have = next.have && !failed;
+        const int slot = next.slot >= 0 && next.slot < a.num_slots ? (int)next.slot : -1;
 #pragma unroll
         for (int i = C::kStages - 1; i > 0; --i)
             masks[i] = masks[i - 1];
@@ -309,7 +318,7 @@ __global__ void __launch_bounds__(kThreads, 2)
             const uint32_t in_run = __ballot_sync(
                 0xffffffffu, s0 >= 0 && slot == s0 + (FP8 ? lane & 15 : lane));
             const uint32_t in_map = __ballot_sync(0xffffffffu, s0 >= 0 && s0 + 15 < a.num_slots);
-            const int x = lu.kvh * kD;
+            const int x = next.kvh * kD;
             if (FP8 ? in_run == 0xffffffffu && in_map == 0xffffffffu
                     : (in_run & 0xffffu) == 0xffffu && (in_map & 1u)) {
                 // lanes 0..3: K and V of the two halves of the head (BF16) or of the two runs (FP8)
@@ -332,12 +341,11 @@ __global__ void __launch_bounds__(kThreads, 2)
                             isv ? &maps.v : &maps.k, x + half * 64, y0, y1, y2, y3,
                             &bars[in_stage]);
             }
-            ++ls;
         }
         in_stage = in_stage + 1 == C::kStages ? 0 : in_stage + 1;
-        fetch_slot();
+        next = second;
+        second = fetch();
     };
-    fetch_slot();
 #pragma unroll
     for (int i = 0; i < C::kStages - 1; ++i)
         issue();
