@@ -51,19 +51,4 @@ __device__ __forceinline__ int64_t row_token(const AttnArgs &a, const AttnPlan &
     return (int64_t)b * a.q_len + i;
 }
 
-// The kernel may use all of the shared memory: set once per device.
-template <auto Kernel>
-cudaError_t allow_smem(int bytes)
-{
-    static bool done[64] = {};
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess || (dev < 64 && done[dev]))
-        return e;
-    e = cudaFuncSetAttribute(Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-    if (e == cudaSuccess && dev < 64)
-        done[dev] = true;
-    return e;
-}
-
 }  // namespace beam

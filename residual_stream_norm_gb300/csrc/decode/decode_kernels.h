@@ -101,4 +101,19 @@ struct W4Args {
 
 cudaError_t launch_w4_matvec(const W4Args &a, cudaStream_t stream);
 
+// The kernel may use all of the shared memory: set once per device.
+template <auto Kernel>
+cudaError_t allow_smem(int bytes)
+{
+    static bool done[64] = {};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess || (dev < 64 && done[dev]))
+        return e;
+    e = cudaFuncSetAttribute(Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess && dev < 64)
+        done[dev] = true;
+    return e;
+}
+
 }  // namespace beam

@@ -1,9 +1,16 @@
 // w4_matvec.cu -- products of a few tokens with a matrix of 4-bit weights (sm_103a).
 //
 // y[t, n] = sum_g scale[n, g] * ( sum_{k in g} x[t, k] (w[n, k] - z[n, g]) ).  w - z is a whole number of
-// at most five bits, exact in BF16, so the inner sum is a BF16 matrix product with FP32 sums.  A warp
-// takes 16 rows of w as the 16 rows of the matrix instruction and eight tokens as its columns; the
-// warps of a block share out k and join their sums at the end, in order.
+// at most five bits, exact in BF16, so the inner sum is a BF16 matrix product with FP32 sums: 16 rows of
+// w are the 16 rows of the matrix instruction, eight tokens its columns.
+//
+// A block takes R rows and steps of 256 k through shared memory (cp.async, several stages); its warps
+// share out the rows (WN) and each step's k (8 / WN).  With few rows a cluster of blocks shares out k as
+// well and joins its sums through distributed shared memory, in order, so no workspace is needed and
+// results do not depend on timing.
+//
+// What bounds it: the weights' bytes from memory; beside them the x fragments (R rows share each
+// copy of x, and MTW row tiles each fragment) and, from 32 tokens on, the matrix pipe.
 
 #include "decode_kernels.h"
 #include "decode_mma.cuh"
@@ -11,13 +18,21 @@
 namespace beam {
 namespace {
 
-constexpr int kW4Warps = 4;
-constexpr int kW4Threads = 32 * kW4Warps;
-constexpr int kW4Step = 256;                    // k of a warp's step
-constexpr int kW4Pitch = kW4Step / 2 + 16;      // bytes of a row in shared memory: no bank conflicts
-constexpr int kW4Stages = 5;
-constexpr int kW4StageBytes = 16 * kW4Pitch;
-constexpr int kW4Smem = kW4Warps * kW4Stages * kW4StageBytes;
+constexpr int kW4Threads = 256;
+constexpr int kStep = 256;          // k of a stage: 128 bytes of each row
+constexpr int kWindow = 1024;       // k whose scales and zeros are held at a time
+
+template <int NT, int MTW, int WN>
+struct W4Config {
+    static constexpr int kTok = 8 * NT;
+    static constexpr int kRows = 16 * MTW * WN;
+    static constexpr int kWk = 8 / WN;
+    static constexpr int kStages = NT >= 4 ? 2 : 4;
+    static constexpr int kStageBytes = kRows * 128 + kTok * 512;
+    static constexpr int kRed = kWk * kTok * kRows * 4;
+    static constexpr int kMain = kStages * kStageBytes > kRed ? kStages * kStageBytes : kRed;
+    static constexpr int smem(int group) { return kMain + kRows * (kWindow / group + 1) * 4; }
+};
 
 // a - b of two BF16 pairs; exact here.
 __device__ __forceinline__ uint32_t sub_bf16x2(uint32_t a, uint32_t b)
@@ -27,143 +42,284 @@ __device__ __forceinline__ uint32_t sub_bf16x2(uint32_t a, uint32_t b)
     return d;
 }
 
-template <int NT>
-__global__ void __launch_bounds__(kW4Threads) w4_matvec_kernel(const W4Args a)
+__device__ __forceinline__ uint32_t lds32(uint32_t addr)
 {
-    extern __shared__ __align__(128) char smem[];
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int g = lane >> 2, t = lane & 3;
-    const int64_t row0 = (int64_t)blockIdx.x * 16, t0 = (int64_t)blockIdx.y * (8 * NT);
-    const uint32_t buf = smem_addr(smem) + warp * kW4Stages * kW4StageBytes;
-    const int64_t all = (a.K + kW4Step - 1) / kW4Step;
-    const int steps = (int)((all - warp + kW4Warps - 1) / kW4Warps);
-    const int64_t kbytes = a.K / 2, groups = a.K / a.group;
-    pdl_launch_dependents();
-    auto issue = [&](int s) {
-        if (s < steps) {
-            const int64_t b0 = (int64_t)(s * kW4Warps + warp) * (kW4Step / 2);
-            const uint32_t dst = buf + (s % kW4Stages) * kW4StageBytes;
-            const int ch = lane & 7;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int r = 4 * j + (lane >> 3);
-                const bool in = row0 + r < a.N && b0 + 16 * ch < kbytes;
-                const char *src =
-                    (const char *)a.w + (in ? (row0 + r) * kbytes + b0 + 16 * ch : 0);
-                cp_async16(dst + r * kW4Pitch + 16 * ch, src, in ? 16u : 0u);
-            }
-        }
-        cp_async_commit();
-    };
-#pragma unroll
-    for (int s = 0; s < kW4Stages - 1; ++s)
-        issue(s);
-    pdl_wait();  // the weights are parameters; x is not
-    float acc[NT][4];
-#pragma unroll
-    for (int n = 0; n < NT; ++n)
-        acc[n][0] = acc[n][1] = acc[n][2] = acc[n][3] = 0.0f;
-    const bool r0 = row0 + g < a.N, r1 = row0 + g + 8 < a.N;
-    const uint16_t *sc = (const uint16_t *)a.scales;
-    for (int s = 0; s < steps; ++s) {
-        cp_async_wait<kW4Stages - 2>();
-        __syncwarp();
-        issue(s + kW4Stages - 1);
-        const uint32_t st = buf + (s % kW4Stages) * kW4StageBytes;
-        const int64_t k0 = (int64_t)(s * kW4Warps + warp) * kW4Step;
-        const int blocks = (int)((a.K - k0 < kW4Step ? a.K - k0 : kW4Step) / 32);
-        float part[NT][4];
-#pragma unroll
-        for (int n = 0; n < NT; ++n)
-            part[n][0] = part[n][1] = part[n][2] = part[n][3] = 0.0f;
-        for (int j = 0; j < blocks; ++j) {
-            const int64_t k = k0 + 32 * j, grp = k / a.group;
-            const uint32_t z0 =
-                (128u + (a.zeros ? (r0 ? a.zeros[(row0 + g) * groups + grp] & 15u : 0u) : 8u));
-            const uint32_t z1 =
-                (128u + (a.zeros ? (r1 ? a.zeros[(row0 + g + 8) * groups + grp] & 15u : 0u) : 8u));
-            // 128 + z in BF16: 0x4300 + z
-            const uint32_t zz0 = (0x4280u + z0) * 0x10001u, zz1 = (0x4280u + z1) * 0x10001u;
-            uint32_t w0, w1;
-            asm volatile("ld.shared.u32 %0, [%1];" : "=r"(w0) : "r"(st + g * kW4Pitch + 16 * j + 4 * t));
-            asm volatile("ld.shared.u32 %0, [%1];"
-                         : "=r"(w1)
-                         : "r"(st + (g + 8) * kW4Pitch + 16 * j + 4 * t));
-            uint32_t f0[4], f1[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {  // nibbles i and i + 4
-                f0[i] = sub_bf16x2(((w0 >> (4 * i)) & 0x000f000fu) | 0x43004300u, zz0);
-                f1[i] = sub_bf16x2(((w1 >> (4 * i)) & 0x000f000fu) | 0x43004300u, zz1);
-            }
-            const uint32_t a0[4] = {f0[0], f1[0], f0[1], f1[1]};
-            const uint32_t a1[4] = {f0[2], f1[2], f0[3], f1[3]};
-#pragma unroll
-            for (int n = 0; n < NT; ++n) {
-                const int64_t tok = t0 + 8 * n + g;
-                const uint4 x = tok < a.T ? ld_cached((const char *)a.x +
-                                                      2 * (tok * a.x_stride + k + 8 * t))
-                                          : make_uint4(0u, 0u, 0u, 0u);
-                mma16816<false>(part[n], a0, __byte_perm(x.x, x.z, 0x5410),
-                                __byte_perm(x.x, x.z, 0x7632));
-                mma16816<false>(part[n], a1, __byte_perm(x.y, x.w, 0x5410),
-                                __byte_perm(x.y, x.w, 0x7632));
-            }
-            if ((k + 32) % a.group == 0 || j + 1 == blocks) {  // the group's end, or the step's
-                const float s0 = r0 ? bf_lo(sc[(row0 + g) * groups + grp]) : 0.0f;
-                const float s1 = r1 ? bf_lo(sc[(row0 + g + 8) * groups + grp]) : 0.0f;
-#pragma unroll
-                for (int n = 0; n < NT; ++n)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        acc[n][e] = __fmaf_rn(e < 2 ? s0 : s1, part[n][e], acc[n][e]);
-                        part[n][e] = 0.0f;
-                    }
-            }
-        }
-    }
-    cp_async_wait<0>();
-    __syncthreads();
-    float *red = reinterpret_cast<float *>(smem);  // [warp][token][16 rows]
-#pragma unroll
-    for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-            red[(warp * 8 * NT + 8 * n + 2 * t + (e & 1)) * 16 + g + 8 * (e >> 1)] = acc[n][e];
-    __syncthreads();
-    for (int x = tid; x < 8 * NT * 16; x += kW4Threads) {
-        const int64_t tok = t0 + x / 16, n = row0 + x % 16;
-        if (tok < a.T && n < a.N) {
-            float v = red[x];
-#pragma unroll
-            for (int w = 1; w < kW4Warps; ++w)
-                v = __fadd_rn(v, red[w * 8 * NT * 16 + x]);
-            reinterpret_cast<uint16_t *>(a.y)[tok * a.y_stride + n] =
-                (uint16_t)pack_bf16x2(v, 0.0f);
-        }
-    }
+    uint32_t v;
+    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+    return v;
 }
 
-template <int NT>
+__device__ __forceinline__ void cluster_sync()
+{
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::
+                     : "memory");
+}
+
+// A float of another block of the cluster, at this block's shared address.
+__device__ __forceinline__ float ld_cluster(uint32_t addr, int rank)
+{
+    float v;
+    asm volatile("{\n\t.reg .u32 a;\n\tmapa.shared::cluster.u32 a, %1, %2;\n\t"
+                 "ld.shared::cluster.f32 %0, [a];\n\t}"
+                 : "=f"(v)
+                 : "r"(addr), "r"(rank)
+                 : "memory");
+    return v;
+}
+
+// x: which 16-byte chunk of a token's 128 bytes a chunk is kept at.  A quarter of a warp reads four
+// neighbouring chunks of an even and of the next token: no bank conflicts.
+__device__ __forceinline__ int x_place(int tok, int chunk)
+{
+    return chunk ^ (((tok & 1) << 2) | ((tok >> 1) & 3));
+}
+
+template <int NT, int MTW, int WN, int GROUP>
+__global__ void __launch_bounds__(kW4Threads) w4_matvec_kernel(const W4Args a, int split)
+{
+    using C = W4Config<NT, MTW, WN>;
+    constexpr int R = C::kRows, kTok = C::kTok, WK = C::kWk, ST = C::kStages;
+    constexpr int kWin = kWindow / GROUP, kPitch = kWin + 1;
+    extern __shared__ __align__(128) char smem[];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int g = lane >> 2, t = lane & 3, wn = warp % WN, wk = warp / WN;
+    const int rank = blockIdx.x % split;
+    const int64_t row0 = (int64_t)(blockIdx.x / split) * R, t0 = (int64_t)blockIdx.y * kTok;
+    const int all = (int)((a.K + kStep - 1) / kStep);
+    const int s0 = (int)((int64_t)all * rank / split), s1 = (int)((int64_t)all * (rank + 1) / split);
+    const int64_t kbytes = a.K / 2, groups = a.K / GROUP;
+    const uint32_t base = smem_addr(smem);
+    uint32_t *params = reinterpret_cast<uint32_t *>(smem + C::kMain);  // [R][kPitch]: scale, zero
+    const int toks = (int)(a.T - t0 < kTok ? a.T - t0 : kTok);
+    pdl_launch_dependents();
+
+    // weights of step s: rows of 128 bytes, chunk c of row r at c ^ (r % 8)
+    auto copy_w = [&](int s) {
+        const uint32_t dst = base + (s - s0) % ST * C::kStageBytes;
+        const int ch = tid & 7;
+        const int64_t at = (int64_t)s * (kStep / 2) + 16 * ch;
+#pragma unroll
+        for (int j = 0; j < R / 32; ++j) {
+            const int r = 32 * j + (tid >> 3);
+            const bool in = row0 + r < a.N && at < kbytes;
+            cp_async16(dst + r * 128 + 16 * (ch ^ (r & 7)),
+                       (const char *)a.w + (in ? (row0 + r) * kbytes + at : 0), in ? 16u : 0u);
+        }
+    };
+    // x of step s: four blocks of 64 k, each of rows of 128 bytes
+    auto copy_x = [&](int s) {
+        const uint32_t dst = base + (s - s0) % ST * C::kStageBytes + R * 128;
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+            const int q = tid & 31, tok = 8 * j + (tid >> 5);
+            const int64_t k = (int64_t)s * kStep + 8 * q;
+            const bool in = tok < toks && k < a.K;
+            cp_async16(dst + (q >> 3) * kTok * 128 + tok * 128 + 16 * x_place(tok, q & 7),
+                       (const char *)a.x + (in ? 2 * ((t0 + tok) * a.x_stride + k) : 0),
+                       in ? 16u : 0u);
+        }
+    };
+    // scales and zeros of the window that starts with step s
+    auto load_params = [&](int s) {
+        const int64_t g0 = (int64_t)s * (kStep / GROUP);
+        const int gn = (int)(groups - g0 < kWin ? groups - g0 : kWin);
+#pragma unroll 4
+        for (int x = tid; x < R * kWin; x += kW4Threads) {
+            const int r = x / kWin, i = x % kWin;
+            uint32_t v = 0u;
+            if (i < gn && row0 + r < a.N) {
+                const int64_t at = (row0 + r) * groups + g0 + i;
+                v = (uint32_t)((const uint16_t *)a.scales)[at] << 16;
+                v |= a.zeros ? a.zeros[at] & 15u : 8u;
+            }
+            params[r * kPitch + i] = v;
+        }
+    };
+#pragma unroll
+    for (int s = 0; s < ST - 1; ++s)  // the weights are parameters: they need not wait
+        if (s0 + s < s1)
+            copy_w(s0 + s);
+    load_params(s0);
+    pdl_wait();
+#pragma unroll
+    for (int s = 0; s < ST - 1; ++s) {
+        if (s0 + s < s1)
+            copy_x(s0 + s);
+        cp_async_commit();  // the first group holds every weight copy so far too
+    }
+
+    float acc[MTW][NT][4];
+#pragma unroll
+    for (int m = 0; m < MTW; ++m)
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+            acc[m][n][0] = acc[m][n][1] = acc[m][n][2] = acc[m][n][3] = 0.0f;
+    int win = s0;
+    for (int s = s0; s < s1; ++s) {
+        cp_async_wait<ST - 2>();
+        __syncthreads();
+        if (s - win == kWindow / kStep) {
+            win = s;
+            load_params(s);
+            __syncthreads();
+        }
+        if (s + ST - 1 < s1) {
+            copy_w(s + ST - 1);
+            copy_x(s + ST - 1);
+        }
+        cp_async_commit();
+        const uint32_t ws = base + (s - s0) % ST * C::kStageBytes, xs = ws + R * 128;
+        float part[MTW][NT][4];
+#pragma unroll
+        for (int jj = 0; jj < 8 / WK; ++jj) {
+            const int j = wk * (8 / WK) + jj;  // 32 k
+            if (jj == 0 || (32 * jj) % GROUP == 0) {
+#pragma unroll
+                for (int m = 0; m < MTW; ++m)
+#pragma unroll
+                    for (int n = 0; n < NT; ++n)
+                        part[m][n][0] = part[m][n][1] = part[m][n][2] = part[m][n][3] = 0.0f;
+            }
+            uint32_t b[NT][4];
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                const uint4 x = lds128(xs + (j >> 1) * kTok * 128 + (8 * n + g) * 128 +
+                                       16 * x_place(g, 4 * (j & 1) + t));
+                b[n][0] = __byte_perm(x.x, x.z, 0x5410), b[n][1] = __byte_perm(x.x, x.z, 0x7632);
+                b[n][2] = __byte_perm(x.y, x.w, 0x5410), b[n][3] = __byte_perm(x.y, x.w, 0x7632);
+            }
+            const int gi = (s - win) * (kStep / GROUP) + 32 * j / GROUP;
+            const bool last = jj + 1 == 8 / WK || (32 * (jj + 1)) % GROUP == 0;
+#pragma unroll
+            for (int m = 0; m < MTW; ++m) {
+                const int r = (wn * MTW + m) * 16 + g;
+                const uint32_t p0 = params[r * kPitch + gi], p1 = params[(r + 8) * kPitch + gi];
+                // 128 + z in BF16 is 0x4300 + z
+                const uint32_t z0 = ((p0 & 15u) + 0x4300u) * 0x10001u;
+                const uint32_t z1 = ((p1 & 15u) + 0x4300u) * 0x10001u;
+                const uint32_t w0 = lds32(ws + r * 128 + 16 * (j ^ (r & 7)) + 4 * t);
+                const uint32_t w1 = lds32(ws + (r + 8) * 128 + 16 * (j ^ (r & 7)) + 4 * t);
+                uint32_t f0[4], f1[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {  // values i and i + 4 of the eight
+                    f0[i] = sub_bf16x2(((w0 >> (4 * i)) & 0x000f000fu) | 0x43004300u, z0);
+                    f1[i] = sub_bf16x2(((w1 >> (4 * i)) & 0x000f000fu) | 0x43004300u, z1);
+                }
+                const uint32_t a0[4] = {f0[0], f1[0], f0[1], f1[1]};
+                const uint32_t a1[4] = {f0[2], f1[2], f0[3], f1[3]};
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                    mma16816<false>(part[m][n], a0, b[n][0], b[n][1]);
+                    mma16816<false>(part[m][n], a1, b[n][2], b[n][3]);
+                }
+                if (last) {
+                    const float c0 = __uint_as_float(p0 & 0xffff0000u);
+                    const float c1 = __uint_as_float(p1 & 0xffff0000u);
+#pragma unroll
+                    for (int n = 0; n < NT; ++n)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            acc[m][n][e] = __fmaf_rn(e < 2 ? c0 : c1, part[m][n][e], acc[m][n][e]);
+                }
+            }
+        }
+    }
+    // ---- the warps' sums over k, then the cluster's, in order ------------------------------------------
+    cp_async_wait<0>();
+    __syncthreads();
+    float *red = reinterpret_cast<float *>(smem);  // [WK][kTok][R]
+#pragma unroll
+    for (int m = 0; m < MTW; ++m)
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                red[(wk * kTok + 8 * n + 2 * t + (e & 1)) * R + (wn * MTW + m) * 16 + g +
+                    8 * (e >> 1)] = acc[m][n][e];
+    __syncthreads();
+    constexpr int kOut = kTok * R;
+    const int first = kOut / split * rank, end = kOut / split * (rank + 1);
+    if (split > 1) {
+        for (int x = tid; x < toks * R; x += kW4Threads) {
+            float v = red[x];
+#pragma unroll
+            for (int w = 1; w < WK; ++w)
+                v = __fadd_rn(v, red[w * kOut + x]);
+            red[x] = v;
+        }
+        cluster_sync();
+    }
+    for (int x = first + tid; x < end; x += kW4Threads) {
+        const int64_t tok = x / R, n = row0 + x % R;
+        if (tok >= toks || n >= a.N)
+            continue;
+        float v;
+        if (split > 1) {
+            v = ld_cluster(base + 4 * x, 0);
+            for (int q = 1; q < split; ++q)
+                v = __fadd_rn(v, ld_cluster(base + 4 * x, q));
+        } else {
+            v = red[x];
+#pragma unroll
+            for (int w = 1; w < WK; ++w)
+                v = __fadd_rn(v, red[w * kOut + x]);
+        }
+        reinterpret_cast<uint16_t *>(a.y)[(t0 + tok) * a.y_stride + n] =
+            (uint16_t)pack_bf16x2(v, 0.0f);
+    }
+    if (split > 1)
+        cluster_sync();  // the others may still read this block's sums
+}
+
+template <int NT, int MTW, int WN, int GROUP>
 cudaError_t launch(const W4Args &a, cudaStream_t stream)
 {
-    const cudaError_t e = cudaFuncSetAttribute(
-        w4_matvec_kernel<NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, kW4Smem);
+    using C = W4Config<NT, MTW, WN>;
+    constexpr int bytes = C::smem(GROUP);
+    cudaError_t e = allow_smem<w4_matvec_kernel<NT, MTW, WN, GROUP>>(bytes);
     if (e != cudaSuccess)
         return e;
+    const int64_t tiles = (a.N + C::kRows - 1) / C::kRows;
+    const int64_t steps = (a.K + kStep - 1) / kStep;
+    const int64_t ttiles = (a.T + C::kTok - 1) / C::kTok;
+    // a cluster shares out k while there are fewer than three blocks for two SMs and each still gets
+    // two steps
+    int split = 1;
+    while (split < 8 && tiles * ttiles * split < kPlanSms * 3 / 2 && steps >= 4 * split)
+        split *= 2;
     W4Args b = a;
-    const int64_t tiles = (a.T + 8 * NT - 1) / (8 * NT);
-    for (int64_t at = 0; at < tiles; at += 65535) {
-        const int64_t here = tiles - at < 65535 ? tiles - at : 65535;
-        b.T = a.T - at * 8 * NT;
-        b.x = (const char *)a.x + 2 * at * 8 * NT * a.x_stride;
-        b.y = (char *)a.y + 2 * at * 8 * NT * a.y_stride;
-        const cudaError_t f =
-            launch_pdl(w4_matvec_kernel<NT>, dim3((unsigned)((a.N + 15) / 16), (unsigned)here),
-                       dim3(kW4Threads), kW4Smem, stream, b);
-        if (f != cudaSuccess)
-            return f;
+    for (int64_t at = 0; at < ttiles; at += 65535) {
+        const int64_t here = ttiles - at < 65535 ? ttiles - at : 65535;
+        b.T = a.T - at * C::kTok;
+        b.x = (const char *)a.x + 2 * at * C::kTok * a.x_stride;
+        b.y = (char *)a.y + 2 * at * C::kTok * a.y_stride;
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3((unsigned)(tiles * split), (unsigned)here);
+        cfg.blockDim = dim3(kW4Threads);
+        cfg.dynamicSmemBytes = bytes;
+        cfg.stream = stream;
+        cudaLaunchAttribute attr[2];
+        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[0].val.programmaticStreamSerializationAllowed = 1;
+        attr[1].id = cudaLaunchAttributeClusterDimension;
+        attr[1].val.clusterDim.x = (unsigned)split;
+        attr[1].val.clusterDim.y = 1;
+        attr[1].val.clusterDim.z = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = split > 1 ? 2 : 1;
+        e = cudaLaunchKernelEx(&cfg, w4_matvec_kernel<NT, MTW, WN, GROUP>, b, split);
+        if (e != cudaSuccess)
+            return e;
     }
     return cudaGetLastError();
+}
+
+template <int NT, int MTW, int WN>
+cudaError_t launch_group(const W4Args &a, cudaStream_t stream)
+{
+    return a.group == 32   ? launch<NT, MTW, WN, 32>(a, stream)
+           : a.group == 64 ? launch<NT, MTW, WN, 64>(a, stream)
+                           : launch<NT, MTW, WN, 128>(a, stream);
 }
 
 }  // namespace
@@ -171,10 +327,12 @@ cudaError_t launch(const W4Args &a, cudaStream_t stream)
 cudaError_t launch_w4_matvec(const W4Args &a, cudaStream_t stream)
 {
     if (a.T <= 8)
-        return launch<1>(a, stream);
+        return launch_group<1, 2, 2>(a, stream);
     if (a.T <= 16)
-        return launch<2>(a, stream);
-    return launch<4>(a, stream);
+        return launch_group<2, 2, 4>(a, stream);
+    if (a.T <= 32)
+        return launch_group<4, 4, 2>(a, stream);
+    return launch_group<8, 2, 4>(a, stream);
 }
 
 }  // namespace beam
