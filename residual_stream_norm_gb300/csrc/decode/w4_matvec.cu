@@ -12,6 +12,7 @@
 // What bounds it: the weights' bytes from memory; beside them the x fragments (R rows share each
 // copy of x, and MTW row tiles each fragment) and, from 32 tokens on, the matrix pipe.
 
+#include "beam_f32x2.cuh"
 #include "decode_kernels.h"
 #include "decode_mma.cuh"
 
@@ -67,6 +68,16 @@ __device__ __forceinline__ float ld_cluster(uint32_t addr, int rank)
     return v;
 }
 
+// C = A B, without a sum to start from.
+__device__ __forceinline__ void mma16816_first(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
+                                               uint32_t b1)
+{
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+        "{%8,%9}, {%10,%10,%10,%10};"
+        : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.0f));
+}
+
 // x: which 16-byte chunk of a token's 128 bytes a chunk is kept at.  A quarter of a warp reads four
 // neighbouring chunks of an even and of the next token: no bank conflicts.
 __device__ __forceinline__ int x_place(int tok, int chunk)
@@ -75,7 +86,8 @@ __device__ __forceinline__ int x_place(int tok, int chunk)
 }
 
 template <int NT, int MTW, int WN, int GROUP>
-__global__ void __launch_bounds__(kW4Threads) w4_matvec_kernel(const W4Args a, int split)
+__global__ void __launch_bounds__(kW4Threads, NT >= 4 ? 2 : 3)
+    w4_matvec_kernel(const W4Args a, int split)
 {
     using C = W4Config<NT, MTW, WN>;
     constexpr int R = C::kRows, kTok = C::kTok, WK = C::kWk, ST = C::kStages;
@@ -89,33 +101,36 @@ __global__ void __launch_bounds__(kW4Threads) w4_matvec_kernel(const W4Args a, i
     const int s0 = (int)((int64_t)all * rank / split), s1 = (int)((int64_t)all * (rank + 1) / split);
     const int64_t kbytes = a.K / 2, groups = a.K / GROUP;
     const uint32_t base = smem_addr(smem);
-    uint32_t *params = reinterpret_cast<uint32_t *>(smem + C::kMain);  // [R][kPitch]: scale, zero
+    uint32_t *params = reinterpret_cast<uint32_t *>(smem + C::kMain);  // [R][kPitch]: scale, 128 + zero
     const int toks = (int)(a.T - t0 < kTok ? a.T - t0 : kTok);
     pdl_launch_dependents();
 
     // weights of step s: rows of 128 bytes, chunk c of row r at c ^ (r % 8)
-    auto copy_w = [&](int s) {
-        const uint32_t dst = base + (s - s0) % ST * C::kStageBytes;
-        const int ch = tid & 7;
-        const int64_t at = (int64_t)s * (kStep / 2) + 16 * ch;
+    const char *w_src = (const char *)a.w + row0 * kbytes + (tid >> 3) * kbytes + 16 * (tid & 7);
+    const uint32_t w_dst = base + (tid >> 3) * 128 + 16 * ((tid & 7) ^ ((tid >> 3) & 7));
+    const int64_t w_left = kbytes - 16 * (tid & 7);  // > 0: this thread's chunk of step 0 exists
+    auto copy_w = [&](int s, int stage) {
+        const int64_t at = (int64_t)s * (kStep / 2);
+        const uint32_t dst = w_dst + stage * C::kStageBytes;
 #pragma unroll
         for (int j = 0; j < R / 32; ++j) {
-            const int r = 32 * j + (tid >> 3);
-            const bool in = row0 + r < a.N && at < kbytes;
-            cp_async16(dst + r * 128 + 16 * (ch ^ (r & 7)),
-                       (const char *)a.w + (in ? (row0 + r) * kbytes + at : 0), in ? 16u : 0u);
+            const bool in = row0 + 32 * j + (tid >> 3) < a.N && at < w_left;
+            cp_async16(dst + 32 * j * 128, in ? w_src + at + 32 * j * kbytes : (const char *)a.w,
+                       in ? 16u : 0u);
         }
     };
     // x of step s: four blocks of 64 k, each of rows of 128 bytes
-    auto copy_x = [&](int s) {
-        const uint32_t dst = base + (s - s0) % ST * C::kStageBytes + R * 128;
+    const char *x_src = (const char *)a.x + 2 * ((t0 + (tid >> 5)) * a.x_stride + 8 * (tid & 31));
+    const uint32_t x_dst = base + R * 128 + ((tid & 31) >> 3) * kTok * 128 + (tid >> 5) * 128 +
+                           16 * x_place(tid >> 5, tid & 7);
+    auto copy_x = [&](int s, int stage) {
+        const int64_t k = (int64_t)s * kStep;
+        const uint32_t dst = x_dst + stage * C::kStageBytes;
 #pragma unroll
         for (int j = 0; j < NT; ++j) {
-            const int q = tid & 31, tok = 8 * j + (tid >> 5);
-            const int64_t k = (int64_t)s * kStep + 8 * q;
-            const bool in = tok < toks && k < a.K;
-            cp_async16(dst + (q >> 3) * kTok * 128 + tok * 128 + 16 * x_place(tok, q & 7),
-                       (const char *)a.x + (in ? 2 * ((t0 + tok) * a.x_stride + k) : 0),
+            const bool in = 8 * j + (tid >> 5) < toks && k + 8 * (tid & 31) < a.K;
+            cp_async16(dst + 8 * j * 128,
+                       in ? x_src + 2 * (k + 8 * j * a.x_stride) : (const char *)a.x,
                        in ? 16u : 0u);
         }
     };
@@ -130,7 +145,7 @@ __global__ void __launch_bounds__(kW4Threads) w4_matvec_kernel(const W4Args a, i
             if (i < gn && row0 + r < a.N) {
                 const int64_t at = (row0 + r) * groups + g0 + i;
                 v = (uint32_t)((const uint16_t *)a.scales)[at] << 16;
-                v |= a.zeros ? a.zeros[at] & 15u : 8u;
+                v |= 0x4300u + (a.zeros ? a.zeros[at] & 15u : 8u);  // 128 + z in BF16
             }
             params[r * kPitch + i] = v;
         }
@@ -138,23 +153,23 @@ __global__ void __launch_bounds__(kW4Threads) w4_matvec_kernel(const W4Args a, i
 #pragma unroll
     for (int s = 0; s < ST - 1; ++s)  // the weights are parameters: they need not wait
         if (s0 + s < s1)
-            copy_w(s0 + s);
+            copy_w(s0 + s, s);
     load_params(s0);
     pdl_wait();
 #pragma unroll
     for (int s = 0; s < ST - 1; ++s) {
         if (s0 + s < s1)
-            copy_x(s0 + s);
+            copy_x(s0 + s, s);
         cp_async_commit();  // the first group holds every weight copy so far too
     }
 
-    float acc[MTW][NT][4];
+    f2 acc[MTW][NT][2];  // pairs of neighbouring tokens: rows g and g + 8
 #pragma unroll
     for (int m = 0; m < MTW; ++m)
 #pragma unroll
         for (int n = 0; n < NT; ++n)
-            acc[m][n][0] = acc[m][n][1] = acc[m][n][2] = acc[m][n][3] = 0.0f;
-    int win = s0;
+            acc[m][n][0] = acc[m][n][1] = 0ull;
+    int win = s0, stage = 0, ahead = ST - 1;
     for (int s = s0; s < s1; ++s) {
         cp_async_wait<ST - 2>();
         __syncthreads();
@@ -164,62 +179,66 @@ __global__ void __launch_bounds__(kW4Threads) w4_matvec_kernel(const W4Args a, i
             __syncthreads();
         }
         if (s + ST - 1 < s1) {
-            copy_w(s + ST - 1);
-            copy_x(s + ST - 1);
+            copy_w(s + ST - 1, ahead);
+            copy_x(s + ST - 1, ahead);
         }
+        ahead = ahead + 1 == ST ? 0 : ahead + 1;
         cp_async_commit();
-        const uint32_t ws = base + (s - s0) % ST * C::kStageBytes, xs = ws + R * 128;
-        float part[MTW][NT][4];
+        const uint32_t ws = base + stage * C::kStageBytes, xs = ws + R * 128;
+        stage = stage + 1 == ST ? 0 : stage + 1;
+        // this warp's part of the step, a group (or its part of one) at a time: BLK blocks of 32 k
+        constexpr int kMine = 8 / WK, BLK = GROUP / 32 < kMine ? GROUP / 32 : kMine;
 #pragma unroll
-        for (int jj = 0; jj < 8 / WK; ++jj) {
-            const int j = wk * (8 / WK) + jj;  // 32 k
-            if (jj == 0 || (32 * jj) % GROUP == 0) {
+        for (int jg = 0; jg < kMine / BLK; ++jg) {
+            const int j0 = wk * kMine + jg * BLK;
+            uint32_t b[BLK][NT][4];
 #pragma unroll
-                for (int m = 0; m < MTW; ++m)
-#pragma unroll
-                    for (int n = 0; n < NT; ++n)
-                        part[m][n][0] = part[m][n][1] = part[m][n][2] = part[m][n][3] = 0.0f;
-            }
-            uint32_t b[NT][4];
-#pragma unroll
-            for (int n = 0; n < NT; ++n) {
-                const uint4 x = lds128(xs + (j >> 1) * kTok * 128 + (8 * n + g) * 128 +
-                                       16 * x_place(g, 4 * (j & 1) + t));
-                b[n][0] = __byte_perm(x.x, x.z, 0x5410), b[n][1] = __byte_perm(x.x, x.z, 0x7632);
-                b[n][2] = __byte_perm(x.y, x.w, 0x5410), b[n][3] = __byte_perm(x.y, x.w, 0x7632);
-            }
-            const int gi = (s - win) * (kStep / GROUP) + 32 * j / GROUP;
-            const bool last = jj + 1 == 8 / WK || (32 * (jj + 1)) % GROUP == 0;
-#pragma unroll
-            for (int m = 0; m < MTW; ++m) {
-                const int r = (wn * MTW + m) * 16 + g;
-                const uint32_t p0 = params[r * kPitch + gi], p1 = params[(r + 8) * kPitch + gi];
-                // 128 + z in BF16 is 0x4300 + z
-                const uint32_t z0 = ((p0 & 15u) + 0x4300u) * 0x10001u;
-                const uint32_t z1 = ((p1 & 15u) + 0x4300u) * 0x10001u;
-                const uint32_t w0 = lds32(ws + r * 128 + 16 * (j ^ (r & 7)) + 4 * t);
-                const uint32_t w1 = lds32(ws + (r + 8) * 128 + 16 * (j ^ (r & 7)) + 4 * t);
-                uint32_t f0[4], f1[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {  // values i and i + 4 of the eight
-                    f0[i] = sub_bf16x2(((w0 >> (4 * i)) & 0x000f000fu) | 0x43004300u, z0);
-                    f1[i] = sub_bf16x2(((w1 >> (4 * i)) & 0x000f000fu) | 0x43004300u, z1);
-                }
-                const uint32_t a0[4] = {f0[0], f1[0], f0[1], f1[1]};
-                const uint32_t a1[4] = {f0[2], f1[2], f0[3], f1[3]};
+            for (int jj = 0; jj < BLK; ++jj)
 #pragma unroll
                 for (int n = 0; n < NT; ++n) {
-                    mma16816<false>(part[m][n], a0, b[n][0], b[n][1]);
-                    mma16816<false>(part[m][n], a1, b[n][2], b[n][3]);
+                    const int j = j0 + jj;
+                    const uint4 x = lds128(xs + (j >> 1) * kTok * 128 + (8 * n + g) * 128 +
+                                           16 * x_place(g, 4 * (j & 1) + t));
+                    b[jj][n][0] = __byte_perm(x.x, x.z, 0x5410);
+                    b[jj][n][1] = __byte_perm(x.x, x.z, 0x7632);
+                    b[jj][n][2] = __byte_perm(x.y, x.w, 0x5410);
+                    b[jj][n][3] = __byte_perm(x.y, x.w, 0x7632);
                 }
-                if (last) {
-                    const float c0 = __uint_as_float(p0 & 0xffff0000u);
-                    const float c1 = __uint_as_float(p1 & 0xffff0000u);
+            const uint32_t *pp = params + (wn * MTW * 16 + g) * kPitch +
+                                 (s - win) * (kStep / GROUP) + 32 * j0 / GROUP;
 #pragma unroll
-                    for (int n = 0; n < NT; ++n)
+            for (int m = 0; m < MTW; ++m) {
+                const uint32_t p0 = pp[16 * m * kPitch], p1 = pp[(16 * m + 8) * kPitch];
+                const uint32_t z0 = __byte_perm(p0, p0, 0x1010), z1 = __byte_perm(p1, p1, 0x1010);
+                float part[NT][4];
 #pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            acc[m][n][e] = __fmaf_rn(e < 2 ? c0 : c1, part[m][n][e], acc[m][n][e]);
+                for (int jj = 0; jj < BLK; ++jj) {
+                    const uint32_t at = ws + (wn * MTW * 16 + g) * 128 + 16 * ((j0 + jj) ^ g) + 4 * t;
+                    const uint32_t w0 = lds32(at + 16 * m * 128);
+                    const uint32_t w1 = lds32(at + (16 * m + 8) * 128);
+                    uint32_t f0[4], f1[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {  // values i and i + 4 of the eight
+                        f0[i] = sub_bf16x2(((w0 >> (4 * i)) & 0x000f000fu) | 0x43004300u, z0);
+                        f1[i] = sub_bf16x2(((w1 >> (4 * i)) & 0x000f000fu) | 0x43004300u, z1);
+                    }
+                    const uint32_t a0[4] = {f0[0], f1[0], f0[1], f1[1]};
+                    const uint32_t a1[4] = {f0[2], f1[2], f0[3], f1[3]};
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) {
+                        if (jj == 0)
+                            mma16816_first(part[n], a0, b[jj][n][0], b[jj][n][1]);
+                        else
+                            mma16816<false>(part[n], a0, b[jj][n][0], b[jj][n][1]);
+                        mma16816<false>(part[n], a1, b[jj][n][2], b[jj][n][3]);
+                    }
+                }
+                const f2 c0 = splat(__uint_as_float(p0 & 0xffff0000u));
+                const f2 c1 = splat(__uint_as_float(p1 & 0xffff0000u));
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                    acc[m][n][0] = fma2(c0, make_f2(part[n][0], part[n][1]), acc[m][n][0]);
+                    acc[m][n][1] = fma2(c1, make_f2(part[n][2], part[n][3]), acc[m][n][1]);
                 }
             }
         }
@@ -235,7 +254,7 @@ __global__ void __launch_bounds__(kW4Threads) w4_matvec_kernel(const W4Args a, i
 #pragma unroll
             for (int e = 0; e < 4; ++e)
                 red[(wk * kTok + 8 * n + 2 * t + (e & 1)) * R + (wn * MTW + m) * 16 + g +
-                    8 * (e >> 1)] = acc[m][n][e];
+                    8 * (e >> 1)] = e & 1 ? hi_of(acc[m][n][e >> 1]) : lo_of(acc[m][n][e >> 1]);
     __syncthreads();
     constexpr int kOut = kTok * R;
     const int first = kOut / split * rank, end = kOut / split * (rank + 1);
