@@ -101,8 +101,8 @@ BEAM_API int beam_kv_evict_fwd(int64_t *table_out, int32_t *len_out, float *weig
 
 /* Products of a few tokens with a matrix of 4-bit weights:
  *   y[t, n] = bf16( sum_k x[t, k] * (w[n, k] - z[n, k / group]) * scale[n, k / group] )
- * The products of a group are summed in FP32 from exact values x * (w - z), scaled in FP32, and the
- * groups added in FP32 in a fixed order; one rounding to BF16.
+ * The products of 32 to 128 consecutive k of a group are summed in FP32 from exact values
+ * x * (w - z), scaled in FP32, and these sums added in FP32 in a fixed order; one rounding to BF16.
  *
  *   y [T, N] bf16, row t at y + t*y_row_stride (elements, >= N; any alignment of 2 bytes)
  *   x [T, K] bf16, row t at x + t*x_row_stride (>= K, a multiple of 8; 16-byte aligned)

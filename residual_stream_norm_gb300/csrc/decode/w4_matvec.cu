@@ -23,7 +23,7 @@ constexpr int kW4Threads = 256;
 constexpr int kStep = 256;          // k of a stage: 128 bytes of each row
 constexpr int kWindow = 1024;       // k whose scales and zeros are held at a time
 
-template <int NT, int MTW, int WN>
+template <int NT, int MTW, int WN, int GROUP>
 struct W4Config {
     static constexpr int kTok = 8 * NT;
     static constexpr int kRows = 16 * MTW * WN;
@@ -32,7 +32,9 @@ struct W4Config {
     static constexpr int kStageBytes = kRows * 128 + kTok * 512;
     static constexpr int kRed = kWk * kTok * kRows * 4;
     static constexpr int kMain = kStages * kStageBytes > kRed ? kStages * kStageBytes : kRed;
-    static constexpr int smem(int group) { return kMain + kRows * (kWindow / group + 1) * 4; }
+    // then the window's scales and zeros: as copied, and as used (one word each)
+    static constexpr int kParams = kMain + kRows * (kWindow / GROUP) * 3;
+    static constexpr int kBytes = kParams + kRows * (kWindow / GROUP + 1) * 4;
 };
 
 // a - b of two BF16 pairs; exact here.
@@ -89,7 +91,7 @@ template <int NT, int MTW, int WN, int GROUP>
 __global__ void __launch_bounds__(kW4Threads, NT >= 4 ? 2 : 3)
     w4_matvec_kernel(const W4Args a, int split)
 {
-    using C = W4Config<NT, MTW, WN>;
+    using C = W4Config<NT, MTW, WN, GROUP>;
     constexpr int R = C::kRows, kTok = C::kTok, WK = C::kWk, ST = C::kStages;
     constexpr int kWin = kWindow / GROUP, kPitch = kWin + 1;
     extern __shared__ __align__(128) char smem[];
@@ -101,7 +103,7 @@ __global__ void __launch_bounds__(kW4Threads, NT >= 4 ? 2 : 3)
     const int s0 = (int)((int64_t)all * rank / split), s1 = (int)((int64_t)all * (rank + 1) / split);
     const int64_t kbytes = a.K / 2, groups = a.K / GROUP;
     const uint32_t base = smem_addr(smem);
-    uint32_t *params = reinterpret_cast<uint32_t *>(smem + C::kMain);  // [R][kPitch]: scale, 128 + zero
+    uint32_t *params = reinterpret_cast<uint32_t *>(smem + C::kParams);  // [R][kPitch]: scale, 128 + zero
     const int toks = (int)(a.T - t0 < kTok ? a.T - t0 : kTok);
     pdl_launch_dependents();
 
@@ -134,8 +136,44 @@ __global__ void __launch_bounds__(kW4Threads, NT >= 4 ? 2 : 3)
                        in ? 16u : 0u);
         }
     };
-    // scales and zeros of the window that starts with step s
+    // Scales and zeros of the window that starts with step s (a multiple of four).  Rows that start on 16 bytes are copied
+    // a window ahead and then unpacked; others are loaded when they are needed, which costs their
+    // latency once a window.
+    const bool ahead_ok = groups % 16 == 0 && (uint64_t)a.scales % 16 == 0 &&
+                          (!a.zeros || (uint64_t)a.zeros % 16 == 0);
+    const uint32_t raw_s = base + C::kMain, raw_z = raw_s + R * kWin * 2;
+    auto copy_params = [&](int s) {
+        constexpr int kChunksS = kWin * 2 / 16;           // of a row's scales: 16 bytes each
+        constexpr int kZ = kWin < 16 ? kWin : 16;         // bytes of a copy of zeros
+        const int64_t g0 = (int64_t)s * (kStep / GROUP);
+        for (int x = tid; x < R * kChunksS; x += kW4Threads) {
+            const int r = x / kChunksS, c = x % kChunksS;
+            const bool in = row0 + r < a.N && g0 + 8 * c < groups;
+            cp_async16(raw_s + 16 * x,
+                       (const char *)a.scales + (in ? 2 * ((row0 + r) * groups + g0 + 8 * c) : 0),
+                       in ? 16u : 0u);
+        }
+        if (a.zeros)
+            for (int x = tid; x < R * (kWin / kZ); x += kW4Threads) {
+                const int r = x / (kWin / kZ), c = x % (kWin / kZ);
+                const bool in = row0 + r < a.N && g0 + kZ * c < groups;
+                const uint8_t *src = a.zeros + (in ? (row0 + r) * groups + g0 + kZ * c : 0);
+                if constexpr (kZ == 16)
+                    cp_async16(raw_z + 16 * x, src, in ? 16u : 0u);
+                else
+                    cp_async8(raw_z + 8 * x, src, in ? 8u : 0u);
+            }
+    };
     auto load_params = [&](int s) {
+        if (ahead_ok) {
+            const uint16_t *rs = reinterpret_cast<const uint16_t *>(smem + C::kMain);
+            const uint8_t *rz = reinterpret_cast<const uint8_t *>(smem + C::kMain + R * kWin * 2);
+#pragma unroll 4
+            for (int x = tid; x < R * kWin; x += kW4Threads)
+                params[x / kWin * kPitch + x % kWin] =
+                    (uint32_t)rs[x] << 16 | (0x4300u + (a.zeros ? rz[x] & 15u : 8u));
+            return;
+        }
         const int64_t g0 = (int64_t)s * (kStep / GROUP);
         const int gn = (int)(groups - g0 < kWin ? groups - g0 : kWin);
 #pragma unroll 4
@@ -150,11 +188,15 @@ __global__ void __launch_bounds__(kW4Threads, NT >= 4 ? 2 : 3)
             params[r * kPitch + i] = v;
         }
     };
+    int win = s0 & ~(kWindow / kStep - 1);
+    if (ahead_ok)
+        copy_params(win);
 #pragma unroll
     for (int s = 0; s < ST - 1; ++s)  // the weights are parameters: they need not wait
         if (s0 + s < s1)
             copy_w(s0 + s, s);
-    load_params(s0);
+    if (!ahead_ok)
+        load_params(win);
     pdl_wait();
 #pragma unroll
     for (int s = 0; s < ST - 1; ++s) {
@@ -169,14 +211,19 @@ __global__ void __launch_bounds__(kW4Threads, NT >= 4 ? 2 : 3)
 #pragma unroll
         for (int n = 0; n < NT; ++n)
             acc[m][n][0] = acc[m][n][1] = 0ull;
-    int win = s0, stage = 0, ahead = ST - 1;
+    int stage = 0, ahead = ST - 1;
+    bool fresh = ahead_ok;  // the window's parameters are there, but not unpacked
     for (int s = s0; s < s1; ++s) {
         cp_async_wait<ST - 2>();
         __syncthreads();
-        if (s - win == kWindow / kStep) {
-            win = s;
-            load_params(s);
+        if (s - win == kWindow / kStep)
+            win = s, fresh = true;
+        if (fresh) {
+            load_params(win);
             __syncthreads();
+            if (ahead_ok && win + kWindow / kStep < s1)
+                copy_params(win + kWindow / kStep);
+            fresh = false;
         }
         if (s + ST - 1 < s1) {
             copy_w(s + ST - 1, ahead);
@@ -186,8 +233,10 @@ __global__ void __launch_bounds__(kW4Threads, NT >= 4 ? 2 : 3)
         cp_async_commit();
         const uint32_t ws = base + stage * C::kStageBytes, xs = ws + R * 128;
         stage = stage + 1 == ST ? 0 : stage + 1;
-        // this warp's part of the step, a group (or its part of one) at a time: BLK blocks of 32 k
-        constexpr int kMine = 8 / WK, BLK = GROUP / 32 < kMine ? GROUP / 32 : kMine;
+        // this warp's part of the step, a group or a part of one at a time: BLK blocks of 32 k
+        constexpr int kMine = 8 / WK, kMost = NT >= 8 ? 1 : (NT >= 4 ? 2 : 4);
+        constexpr int kInGroup = GROUP / 32 < kMine ? GROUP / 32 : kMine;
+        constexpr int BLK = kInGroup < kMost ? kInGroup : kMost;
 #pragma unroll
         for (int jg = 0; jg < kMine / BLK; ++jg) {
             const int j0 = wk * kMine + jg * BLK;
@@ -293,8 +342,8 @@ __global__ void __launch_bounds__(kW4Threads, NT >= 4 ? 2 : 3)
 template <int NT, int MTW, int WN, int GROUP>
 cudaError_t launch(const W4Args &a, cudaStream_t stream)
 {
-    using C = W4Config<NT, MTW, WN>;
-    constexpr int bytes = C::smem(GROUP);
+    using C = W4Config<NT, MTW, WN, GROUP>;
+    constexpr int bytes = C::kBytes;
     cudaError_t e = allow_smem<w4_matvec_kernel<NT, MTW, WN, GROUP>>(bytes);
     if (e != cudaSuccess)
         return e;
@@ -350,8 +399,8 @@ cudaError_t launch_w4_matvec(const W4Args &a, cudaStream_t stream)
     if (a.T <= 16)
         return launch_group<2, 2, 4>(a, stream);
     if (a.T <= 32)
-        return launch_group<4, 4, 2>(a, stream);
-    return launch_group<8, 2, 4>(a, stream);
+        return launch_group<4, 2, 4>(a, stream);
+    return launch_group<8, 1, 8>(a, stream);
 }
 
 }  // namespace beam

@@ -35,7 +35,7 @@ def check(x, w, s, z, group, y=None):
 
 @pytest.mark.parametrize("zeros", [False, True])
 @pytest.mark.parametrize("T,N,K,group", [
-    (1, 1, 32, 32), (1, 5, 64, 64), (1, 16, 128, 128), (1, 17, 160, 32), (2, 33, 320, 64),
+    (1, 1, 32, 32), (5, 70, 2560, 32), (20, 140, 4096, 64), (40, 130, 2048, 128), (3, 65, 6144, 128), (1, 5, 64, 64), (1, 16, 128, 128), (1, 17, 160, 32), (2, 33, 320, 64),
     (3, 100, 640, 128), (7, 31, 1056, 32), (8, 64, 4096, 128), (9, 65, 576, 64),
     (15, 40, 384, 128), (16, 257, 96, 32), (17, 16, 2048, 64), (31, 50, 1024, 128),
     (32, 48, 480, 32), (33, 90, 704, 64), (64, 130, 256, 128), (65, 24, 512, 32),
