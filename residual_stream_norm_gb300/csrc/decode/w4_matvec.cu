@@ -45,13 +45,6 @@ __device__ __forceinline__ uint32_t sub_bf16x2(uint32_t a, uint32_t b)
     return d;
 }
 
-__device__ __forceinline__ uint32_t lds32(uint32_t addr)
-{
-    uint32_t v;
-    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
-    return v;
-}
-
 __device__ __forceinline__ void cluster_sync()
 {
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::
@@ -169,9 +162,14 @@ __global__ void __launch_bounds__(kW4Threads, NT >= 4 ? 2 : 3)
             const uint16_t *rs = reinterpret_cast<const uint16_t *>(smem + C::kMain);
             const uint8_t *rz = reinterpret_cast<const uint8_t *>(smem + C::kMain + R * kWin * 2);
 #pragma unroll 4
-            for (int x = tid; x < R * kWin; x += kW4Threads)
-                params[x / kWin * kPitch + x % kWin] =
-                    (uint32_t)rs[x] << 16 | (0x4300u + (a.zeros ? rz[x] & 15u : 8u));
+            for (int x = 2 * tid; x < R * kWin; x += 2 * kW4Threads) {  // two groups at a time
+                const uint32_t sc = *reinterpret_cast<const uint32_t *>(rs + x);
+                const uint32_t z =
+                    a.zeros ? *reinterpret_cast<const uint16_t *>(rz + x) & 0x0f0fu : 0x0808u;
+                uint32_t *dst = params + x / kWin * kPitch + x % kWin;
+                dst[0] = sc << 16 | (0x4300u + (z & 15u));  // 128 + z in BF16
+                dst[1] = (sc & 0xffff0000u) | (0x4300u + (z >> 8));
+            }
             return;
         }
         const int64_t g0 = (int64_t)s * (kStep / GROUP);
@@ -231,7 +229,7 @@ __global__ void __launch_bounds__(kW4Threads, NT >= 4 ? 2 : 3)
         }
         ahead = ahead + 1 == ST ? 0 : ahead + 1;
         cp_async_commit();
-        const uint32_t ws = base + stage * C::kStageBytes, xs = ws + R * 128;
+        const char *ws = smem + stage * C::kStageBytes, *xs = ws + R * 128;
         stage = stage + 1 == ST ? 0 : stage + 1;
         // this warp's part of the step, a group or a part of one at a time: BLK blocks of 32 k
         constexpr int kMine = 8 / WK, kMost = NT >= 8 ? 1 : (NT >= 4 ? 2 : 4);
@@ -246,8 +244,9 @@ __global__ void __launch_bounds__(kW4Threads, NT >= 4 ? 2 : 3)
 #pragma unroll
                 for (int n = 0; n < NT; ++n) {
                     const int j = j0 + jj;
-                    const uint4 x = lds128(xs + (j >> 1) * kTok * 128 + (8 * n + g) * 128 +
-                                           16 * x_place(g, 4 * (j & 1) + t));
+                    const uint4 x = *reinterpret_cast<const uint4 *>(
+                        xs + (j >> 1) * kTok * 128 + (8 * n + g) * 128 +
+                        16 * x_place(g, 4 * (j & 1) + t));
                     b[jj][n][0] = __byte_perm(x.x, x.z, 0x5410);
                     b[jj][n][1] = __byte_perm(x.x, x.z, 0x7632);
                     b[jj][n][2] = __byte_perm(x.y, x.w, 0x5410);
@@ -262,9 +261,10 @@ __global__ void __launch_bounds__(kW4Threads, NT >= 4 ? 2 : 3)
                 float part[NT][4];
 #pragma unroll
                 for (int jj = 0; jj < BLK; ++jj) {
-                    const uint32_t at = ws + (wn * MTW * 16 + g) * 128 + 16 * ((j0 + jj) ^ g) + 4 * t;
-                    const uint32_t w0 = lds32(at + 16 * m * 128);
-                    const uint32_t w1 = lds32(at + (16 * m + 8) * 128);
+                    const char *at = ws + (wn * MTW * 16 + g) * 128 + 16 * ((j0 + jj) ^ g) + 4 * t;
+                    const uint32_t w0 = *reinterpret_cast<const uint32_t *>(at + 16 * m * 128);
+                    const uint32_t w1 =
+                        *reinterpret_cast<const uint32_t *>(at + (16 * m + 8) * 128);
                     uint32_t f0[4], f1[4];
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {  // values i and i + 4 of the eight
@@ -350,11 +350,17 @@ cudaError_t launch(const W4Args &a, cudaStream_t stream)
     const int64_t tiles = (a.N + C::kRows - 1) / C::kRows;
     const int64_t steps = (a.K + kStep - 1) / kStep;
     const int64_t ttiles = (a.T + C::kTok - 1) / C::kTok;
-    // a cluster shares out k while there are fewer than three blocks for two SMs and each still gets
-    // two steps
+    // How many blocks of a cluster share out k: what makes the rounds of blocks on the SMs shortest, a
+    // block costing about three steps besides its own.
+    const int64_t slots = kPlanSms * (NT >= 4 ? 2 : 3);
     int split = 1;
-    while (split < 8 && tiles * ttiles * split < kPlanSms * 3 / 2 && steps >= 4 * split)
-        split *= 2;
+    int64_t best = INT64_MAX;
+    for (int q = 1; q <= 8 && q <= steps; q *= 2) {
+        const int64_t cost =
+            (tiles * ttiles * q + slots - 1) / slots * ((steps + q - 1) / q + 3);
+        if (cost < best)
+            best = cost, split = q;
+    }
     W4Args b = a;
     for (int64_t at = 0; at < ttiles; at += 65535) {
         const int64_t here = ttiles - at < 65535 ? ttiles - at : 65535;
