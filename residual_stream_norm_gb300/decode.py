@@ -13,6 +13,7 @@ import torch
 
 HEAD_DIM = 128
 CACHE_BF16, CACHE_FP8_E4M3 = 0, 1
+_SM_SCALE = HEAD_DIM ** -0.5
 
 
 def declare(so: ctypes.CDLL) -> None:
@@ -30,46 +31,63 @@ def declare(so: ctypes.CDLL) -> None:
     so.beam_w4_matvec_fwd.restype = ctypes.c_int
 
 
-def _run(fn: str, device: torch.device, stream, *args) -> None:
-    from . import BeamError, lib
-    f = getattr(lib(), fn)
-    if stream is not None:
-        s = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+_fns: dict = {}
+
+
+def _run(fn: str, index: int, stream, *args) -> None:
+    f = _fns.get(fn)
+    if f is None:
+        from . import lib
+        f = _fns[fn] = getattr(lib(), fn)
+    if stream is None:
+        s = torch._C._cuda_getCurrentRawStream(index)
     else:
-        s = torch.cuda.current_stream(device).cuda_stream
-    if device.index == torch.cuda.current_device():
+        s = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+    if index == torch._C._cuda_getDevice():
         st = f(*args, s)
     else:
-        with torch.cuda.device(device):
+        with torch.cuda.device(index):
             st = f(*args, s)
     if st != 0:
+        from . import BeamError
         raise BeamError(fn, st)
 
 
-def _check(t, name: str, dtype, shape, device, inner_only: bool = False) -> None:
-    """A CUDA tensor of this type and shape on `device`: contiguous, or (inner_only) with
-    contiguous rows of its last dimension."""
+def _check(t, name: str, dtype, shape, index: int, rows: bool = False) -> None:
+    """A CUDA tensor of this type and shape on device `index`: contiguous, or (rows) with contiguous
+    rows of its last dimension.  The first test is all that a good argument costs."""
+    try:
+        if t.dtype is dtype and t.get_device() == index and t.shape == shape and \
+                (t.is_contiguous() or (rows and t.stride(-1) == 1)):
+            return
+    except AttributeError:
+        pass
     if not isinstance(t, torch.Tensor) or t.dtype != dtype or not t.is_cuda:
         raise TypeError(f"{name}: expected a CUDA {dtype} tensor")
     if t.shape != shape:
         raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
-    if t.device != device:
-        raise ValueError(f"{name}: must be on {device}")
-    if not t.is_contiguous() and not (inner_only and t.stride(-1) == 1):
-        raise ValueError(f"{name}: must be contiguous")
+    if t.get_device() != index:
+        raise ValueError(f"{name}: must be on cuda:{index}")
+    raise ValueError(f"{name}: must be contiguous")
 
 
 def _row_stride(t: torch.Tensor) -> int:
-    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), math.prod(t.shape[1:]))
+    if t.shape[0] > 1:
+        return t.stride(0)
+    return max(t.stride(0), math.prod(t.shape[1:]))
 
 
 def _head_rows(t, name: str):
-    """[T, heads, 128] bf16 with contiguous heads; the rows may be strided."""
-    if not isinstance(t, torch.Tensor) or t.dtype != torch.bfloat16 or not t.is_cuda:
+    """(T, heads, row stride, device) of a [T, heads, 128] bf16 CUDA tensor with contiguous heads; the
+    rows may be strided."""
+    if not isinstance(t, torch.Tensor) or t.dtype is not torch.bfloat16 or not t.is_cuda:
         raise TypeError(f"{name}: expected a CUDA bfloat16 tensor")
-    if t.dim() != 3 or t.shape[2] != HEAD_DIM or t.stride(2) != 1 or \
-            (t.shape[1] > 1 and t.stride(1) != HEAD_DIM):
-        raise ValueError(f"{name}: expected [T, heads, {HEAD_DIM}] with contiguous heads")
+    if t.dim() == 3:
+        T, n, d = t.shape
+        st = t.stride()
+        if d == HEAD_DIM and st[2] == 1 and (n <= 1 or st[1] == HEAD_DIM):
+            return T, n, st[0] if T > 1 else max(st[0], n * HEAD_DIM), t.get_device()
+    raise ValueError(f"{name}: expected [T, heads, {HEAD_DIM}] with contiguous heads")
 
 
 def beam_attn_prefix_workspace(B: int, q_len: int, n_q_heads: int, n_kv_heads: int,
@@ -96,60 +114,56 @@ def beam_attn_prefix_fwd(out, q, k_cache, v_cache, prefix_slots, slot_table, suf
     contiguous uint8 tensor of at least ``beam_attn_prefix_workspace`` bytes; lse_out
     [B*q_len, n_q] fp32; key_weight_in / key_weight_out [B, N] fp32 (may be one tensor).  sm_scale
     defaults to 1/sqrt(128).  The last q_len entries of a sequence's suffix are its query tokens."""
-    _head_rows(q, "q")
-    _head_rows(out, "out")
-    dev = q.device
-    if out.shape != q.shape or out.device != dev:
+    T, nq, q_stride, dev = _head_rows(q, "q")
+    oT, oq, out_stride, odev = _head_rows(out, "out")
+    if (oT, oq, odev) != (T, nq, dev):
         raise ValueError("out must have q's shape and device")
-    T, nq = q.shape[0], q.shape[1]
-    if not isinstance(suffix_len, torch.Tensor) or suffix_len.dim() != 1:
-        raise TypeError("suffix_len: expected a CUDA int32 tensor [B]")
-    B = suffix_len.shape[0]
+    if not isinstance(suffix_len, torch.Tensor) or not isinstance(slot_table, torch.Tensor) or \
+            slot_table.dim() != 2:
+        raise TypeError("suffix_len and slot_table: expected CUDA tensors [B] int32 and [B, N] int64")
+    B, N = slot_table.shape
     _check(suffix_len, "suffix_len", torch.int32, (B,), dev)
-    if (B == 0) != (T == 0) or (B and T % B):
+    _check(slot_table, "slot_table", torch.int64, (B, N), dev, rows=True)
+    if T % B if B else T:
         raise ValueError(f"q has {T} rows, not a multiple of the {B} sequences")
-    if not isinstance(slot_table, torch.Tensor) or slot_table.dim() != 2:
-        raise TypeError("slot_table: expected a CUDA int64 tensor [B, N]")
-    N = slot_table.shape[1]
-    _check(slot_table, "slot_table", torch.int64, (B, N), dev, inner_only=True)
     P = 0
     if prefix_slots is not None:
         P = prefix_slots.numel() if isinstance(prefix_slots, torch.Tensor) else -1
         _check(prefix_slots, "prefix_slots", torch.int64, (P,), dev)
     if cache_dtype not in (CACHE_BF16, CACHE_FP8_E4M3):
         raise ValueError(f"cache_dtype: {cache_dtype}")
-    for c, nm in ((k_cache, "k_cache"), (v_cache, "v_cache")):
-        if not (isinstance(c, torch.Tensor) and c.is_cuda and c.device == dev and c.dim() == 3 and
-                c.is_contiguous() and c.shape[2] == HEAD_DIM and
-                (c.dtype == torch.bfloat16 if cache_dtype == CACHE_BF16 else
-                 c.element_size() == 1)):
-            raise TypeError(f"{nm}: expected a contiguous CUDA [num_slots, n_kv, {HEAD_DIM}] tensor "
-                            + ("of bfloat16" if cache_dtype == CACHE_BF16 else "of bytes"))
-    if k_cache.shape != v_cache.shape:
-        raise ValueError("k_cache and v_cache must have the same shape")
-    if not (isinstance(workspace, torch.Tensor) and workspace.is_cuda and
-            workspace.device == dev and workspace.is_contiguous()):
-        raise TypeError("workspace: expected a contiguous CUDA tensor")
+    if not isinstance(k_cache, torch.Tensor) or k_cache.dim() != 3 or k_cache.shape[2] != HEAD_DIM \
+            or (k_cache.dtype is not torch.bfloat16 if cache_dtype == CACHE_BF16 else
+                k_cache.element_size() != 1):
+        raise TypeError(f"k_cache: expected a CUDA [num_slots, n_kv, {HEAD_DIM}] tensor of " +
+                        ("bfloat16" if cache_dtype == CACHE_BF16 else "bytes"))
+    S, n_kv, _ = k_cache.shape
+    _check(k_cache, "k_cache", k_cache.dtype, k_cache.shape, dev)
+    _check(v_cache, "v_cache", k_cache.dtype, k_cache.shape, dev)
+    if not (isinstance(workspace, torch.Tensor) and workspace.get_device() == dev and
+            workspace.is_contiguous()):
+        raise TypeError("workspace: expected a contiguous CUDA tensor on q's device")
+    lse = w_in = w_out = None
+    ws = 0
     if lse_out is not None:
         _check(lse_out, "lse_out", torch.float32, (T, nq), dev)
-    ws = 0
-    for w, nm in ((key_weight_out, "key_weight_out"), (key_weight_in, "key_weight_in")):
-        if w is not None:
-            _check(w, nm, torch.float32, (B, N), dev, inner_only=True)
-            if ws and _row_stride(w) != ws and B > 1:
+        lse = lse_out.data_ptr()
+    if key_weight_out is not None:
+        _check(key_weight_out, "key_weight_out", torch.float32, (B, N), dev, rows=True)
+        w_out, ws = key_weight_out.data_ptr(), _row_stride(key_weight_out)
+        if key_weight_in is not None:
+            _check(key_weight_in, "key_weight_in", torch.float32, (B, N), dev, rows=True)
+            w_in = key_weight_in.data_ptr()
+            if B > 1 and _row_stride(key_weight_in) != ws:
                 raise ValueError("key_weight_in and key_weight_out must have the same row stride")
-            ws = _row_stride(w)
-    if key_weight_in is not None and key_weight_out is None:
+    elif key_weight_in is not None:
         raise ValueError("key_weight_in without key_weight_out")
-    _run("beam_attn_prefix_fwd", dev, stream, out.data_ptr(), _row_stride(out),
-         None if lse_out is None else lse_out.data_ptr(),
-         None if key_weight_in is None else key_weight_in.data_ptr(),
-         None if key_weight_out is None else key_weight_out.data_ptr(), ws, q.data_ptr(),
-         _row_stride(q), k_cache.data_ptr(), v_cache.data_ptr(), k_cache.shape[0], cache_dtype,
-         k_scale, v_scale, prefix_slots.data_ptr() if P else None, P, slot_table.data_ptr(),
-         _row_stride(slot_table) if B else N, N, suffix_len.data_ptr(), B, T // B if B else 1, nq,
-         k_cache.shape[1], HEAD_DIM, HEAD_DIM ** -0.5 if sm_scale is None else sm_scale, window,
-         workspace.data_ptr(), workspace.numel() * workspace.element_size())
+    _run("beam_attn_prefix_fwd", dev, stream, out.data_ptr(), out_stride, lse, w_in, w_out, ws,
+         q.data_ptr(), q_stride, k_cache.data_ptr(), v_cache.data_ptr(), S, cache_dtype, k_scale,
+         v_scale, prefix_slots.data_ptr() if P else None, P, slot_table.data_ptr(),
+         slot_table.stride(0) if B > 1 else N, N, suffix_len.data_ptr(), B, T // B if B else 1, nq,
+         n_kv, HEAD_DIM, _SM_SCALE if sm_scale is None else sm_scale, window, workspace.data_ptr(),
+         workspace.nbytes)
 
 
 def beam_kv_evict_fwd(table_out, len_out, weight_out, freed_out, table_in, len_in, weight_in,
@@ -161,7 +175,7 @@ def beam_kv_evict_fwd(table_out, len_out, weight_out, freed_out, table_in, len_i
     budget: the slots that left, -1 behind them."""
     if not isinstance(table_in, torch.Tensor) or table_in.dim() != 2:
         raise TypeError("table_in: expected a CUDA int64 tensor [rows, width]")
-    dev = table_in.device
+    dev = table_in.get_device()
     rows, width = table_in.shape
     _check(table_in, "table_in", torch.int64, (rows, width), dev)
     _check(table_out, "table_out", torch.int64, (rows, width), dev)
@@ -185,11 +199,11 @@ def beam_w4_matvec_fwd(y, x, w, scales, zeros=None, group: int = 128, stream=Non
     if not isinstance(x, torch.Tensor) or x.dim() != 2 or not isinstance(w, torch.Tensor) or \
             w.dim() != 2:
         raise TypeError("x and w: expected CUDA tensors [T, K] and [N, K/2]")
-    dev = x.device
+    dev = x.get_device()
     T, K = x.shape
     N = w.shape[0]
-    _check(x, "x", torch.bfloat16, (T, K), dev, inner_only=True)
-    _check(y, "y", torch.bfloat16, (T, N), dev, inner_only=True)
+    _check(x, "x", torch.bfloat16, (T, K), dev, rows=True)
+    _check(y, "y", torch.bfloat16, (T, N), dev, rows=True)
     if K % 2:
         raise ValueError("x: K must be even")
     _check(w, "w", torch.uint8, (N, K // 2), dev)
