@@ -53,13 +53,21 @@ __device__ unsigned int g_decode_fault_word = 0u;
 // The block whose share [c tot / C, (c + 1) tot / C) contains tile x (C <= tot).
 __device__ __forceinline__ int64_t owner(int64_t x, int64_t tot, int64_t ctas)
 {
-    return ((x + 1) * ctas - 1) / tot;
+    const int64_t y = (x + 1) * ctas - 1;
+    return (uint64_t)(y | tot) >> 32 ? y / tot : (uint32_t)y / (uint32_t)tot;
+}
+
+// x / y, x >= 0, y > 0: most often both fit 32 bits, and the division is much shorter.
+__device__ __forceinline__ int64_t div32(int64_t x, int64_t y)
+{
+    return (uint64_t)(x | y) >> 32 ? x / y : (uint32_t)x / (uint32_t)y;
 }
 
 __device__ __forceinline__ int64_t seq_tiles(const AttnArgs &a, const AttnPlan &p, int64_t b)
 {
     const int64_t n = seq_len(a, b);
-    return (n - first_tile_key(n, a.q_len, a.window) + p.tile_keys - 1) / p.tile_keys;
+    // tile_keys is a power of two
+    return (n - first_tile_key(n, a.q_len, a.window) + p.tile_keys - 1) >> (31 - __clz(p.tile_keys));
 }
 
 // The A fragments of V^T for 16 elements d and 16 keys.  BF16 (`mt`: which 16 elements): matrix row is
@@ -134,10 +142,10 @@ __device__ __forceinline__ Unit next_unit(const AttnArgs &a, const AttnPlan &p, 
     int32_t key_first;
     u.prefix = c.tile < p_total;
     if (u.prefix) {
-        u.unit = c.tile / p.p_tiles;
+        u.unit = div32(c.tile, p.p_tiles);
         tiles = p.p_tiles;
         start = u.unit * tiles;
-        u.kvh = (int32_t)(u.unit / p.p_rtiles);
+        u.kvh = (int32_t)div32(u.unit, p.p_rtiles);
         u.row0 = (int32_t)(u.unit - u.kvh * p.p_rtiles) * M;
         u.row_end = (int32_t)p.rows;
         u.list = a.prefix;
@@ -149,10 +157,10 @@ __device__ __forceinline__ Unit next_unit(const AttnArgs &a, const AttnPlan &p, 
             c.b_start += per_seq * tiles;
             tiles = seq_tiles(a, p, ++c.b);
         }
-        const int64_t x = (c.tile - c.b_start) / tiles;
+        const int64_t x = div32(c.tile - c.b_start, tiles);
         u.unit = p_units + c.b * per_seq + x;
         start = c.b_start + x * tiles;
-        u.kvh = (int32_t)(x / p.s_rtiles);
+        u.kvh = (int32_t)div32(x, p.s_rtiles);
         u.row0 = (int32_t)(c.b * p.R + (x - (int64_t)u.kvh * p.s_rtiles) * M);
         u.row_end = (int32_t)((c.b + 1) * p.R);
         u.list = a.table + c.b * a.table_stride;
@@ -260,7 +268,7 @@ __global__ void __launch_bounds__(kThreads, 2)
             pdl_wait();
         return;
     }
-    Cursor at{total * blockIdx.x / shares, total * (blockIdx.x + 1) / shares, 0, p_total};
+    Cursor at{div32(total * blockIdx.x, shares), div32(total * (blockIdx.x + 1), shares), 0, p_total};
     if (at.tile >= p_total) {
         scan_sequences(a, p, p_total, at.tile, nullptr, s_scan);
         at.b = s_scan[kWarps];
@@ -816,40 +824,47 @@ __global__ void __launch_bounds__(kThreads, 2)
         pdl_wait();
 }
 
-// Joins a row's parts: one warp per row and KV head, four elements a lane.
+// Joins a row's parts: WARPS warps a row and KV head, which share out the parts; a lane has four
+// elements.  Many parts mean few rows: four warps then.  A warp looks at 32 parts' maxima and sums at
+// a time, a lane each, and its loads of the parts do not wait for one another.
+template <int WARPS>
 __global__ void __launch_bounds__(128) attn_join_kernel(const __grid_constant__ AttnArgs a,
                                                         const __grid_constant__ AttnPlan p)
 {
+    __shared__ float4 s_o[4][32];
+    __shared__ float2 s_ml[4];
     pdl_launch_dependents();
     pdl_wait();
-    const int lane = threadIdx.x & 31;
-    const int64_t x = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int sub = WARPS == 1 ? 0 : warp;
+    const int64_t x = WARPS == 1 ? (int64_t)blockIdx.x * 4 + warp : blockIdx.x;
     if (x >= p.rows * a.n_kv)  // B * q_len * n_q < 2^31
         return;
     const int M = 8 * p.nt;
-    const int kvh = (int)(x / p.rows);
-    const int64_t rr = x - kvh * p.rows, b = rr / p.R;
+    const int kvh = (int)((uint32_t)x / (uint32_t)p.rows);
+    const int64_t rr = x - kvh * p.rows, b = (uint32_t)rr / (uint32_t)p.R;
     const int64_t *cum = reinterpret_cast<const int64_t *>(a.workspace + p.cum_off);
     const int64_t total = cum[a.B], shares = min((int64_t)p.ctas, total);
+    const int64_t c0b = cum[b], c1b = cum[b + 1];
     const int64_t per_seq = (int64_t)a.n_kv * p.s_rtiles;
     const int64_t rt = (rr - b * p.R) / M;
-    const int64_t tb = (cum[b + 1] - cum[b]) / per_seq;
-    // the parts of the prefix unit, then those of the suffix unit
-    int64_t first[3] = {0, 0, 0}, at[3] = {0, 0, 0};  // rows of part c: (first + c) * step + at
-    int count[3] = {0, 0, 0};
+    const int64_t tb = div32(c1b - c0b, per_seq);
+    // the parts of the prefix unit, then those of the suffix unit, then the tensor-core kernel's
+    int64_t first[3] = {0, 0, 0};
+    int at[3] = {0, 0, 0}, count[3] = {0, 0, 0};  // row of part c: (first + c) * M + at
     if (p.p_rtiles > 0) {
         const int64_t unit = kvh * p.p_rtiles + rr / M, s = unit * p.p_tiles;
         const int64_t c0 = owner(s, total, shares);
         first[0] = unit + c0;
         count[0] = (int)(owner(s + p.p_tiles - 1, total, shares) - c0) + 1;
-        at[0] = rr % M;
+        at[0] = (int)(rr % M);
     }
     if (tb > 0) {
-        const int64_t u = (int64_t)kvh * p.s_rtiles + rt, s = cum[b] + u * tb;
+        const int64_t u = (int64_t)kvh * p.s_rtiles + rt, s = c0b + u * tb;
         const int64_t c0 = owner(s, total, shares);
         first[1] = a.n_kv * p.p_rtiles + b * per_seq + u + c0;
         count[1] = (int)(owner(s + tb - 1, total, shares) - c0) + 1;
-        at[1] = rr - b * p.R - rt * M;
+        at[1] = (int)(rr - b * p.R - rt * M);
         if (p.p_rtiles == 0 && p.tc_parts == 0 && count[1] == 1)
             return;  // the rows kernel wrote it
     }
@@ -859,35 +874,75 @@ __global__ void __launch_bounds__(128) attn_join_kernel(const __grid_constant__ 
     const float *tpo = reinterpret_cast<const float *>(a.workspace + p.tc_o_off);
     first[2] = x * p.tc_parts;
     count[2] = p.tc_parts;
-    float m = -INFINITY;
-#pragma unroll
-    for (int k = 0; k < 3; ++k)
-        for (int c = lane; c < count[k]; c += 32) {
-            const float2 w = k == 2 ? tml[first[2] + c] : ml[(first[k] + c) * M + at[k]];
-            m = fmaxf(m, w.y == 0.0f ? -INFINITY : w.x);
-        }
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1)
-        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
-    const float ms = m == -INFINITY ? 0.0f : m;
-    float l = 0.0f;
+    float m = -INFINITY, l = 0.0f;
     float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
-    for (int k = 0; k < 3; ++k)
-        for (int c = 0; c < count[k]; ++c) {
-            const int64_t r = k == 2 ? first[2] + c : (first[k] + c) * M + at[k];
-            const float2 w = k == 2 ? tml[r] : ml[r];
-            if (w.y == 0.0f)
-                continue;
-            const float f = exp2_fast(__fsub_rn(w.x, ms));
-            const float4 v =
-                *reinterpret_cast<const float4 *>((k == 2 ? tpo : po) + r * kD + 4 * lane);
-            l = __fmaf_rn(f, w.y, l);
-            o.x = __fmaf_rn(f, v.x, o.x);
-            o.y = __fmaf_rn(f, v.y, o.y);
-            o.z = __fmaf_rn(f, v.z, o.z);
-            o.w = __fmaf_rn(f, v.w, o.w);
+    for (int k = 0; k < 3; ++k) {
+        for (int c0 = 32 * sub; c0 < count[k]; c0 += 32 * WARPS) {
+            const int n = min(32, count[k] - c0);
+            const int64_t r0 = k == 2 ? first[2] + c0 : (first[k] + c0) * M + at[k];
+            const int step = k == 2 ? 1 : M;
+            float2 w = make_float2(-INFINITY, 0.0f);
+            if (lane < n)
+                w = (k == 2 ? tml : ml)[r0 + lane * step];
+            // a part that saw nothing adds nothing, whatever its sums hold
+            float mx = w.y == 0.0f ? -INFINITY : w.x;
+#pragma unroll
+            for (int off = 16; off > 0; off >>= 1)
+                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
+            const float mn = fmaxf(m, mx), ms = mn == -INFINITY ? 0.0f : mn;
+            const float f0 = exp2_fast(__fsub_rn(m, ms));
+            const float f = w.y == 0.0f ? 0.0f : exp2_fast(__fsub_rn(w.x, ms));
+            m = mn;
+            float ls = __fmul_rn(f, w.y);
+#pragma unroll
+            for (int off = 16; off > 0; off >>= 1)
+                ls = __fadd_rn(ls, __shfl_xor_sync(0xffffffffu, ls, off));
+            l = __fmaf_rn(l, f0, ls);
+            o.x = __fmul_rn(o.x, f0), o.y = __fmul_rn(o.y, f0);
+            o.z = __fmul_rn(o.z, f0), o.w = __fmul_rn(o.w, f0);
+            const uint32_t live = __ballot_sync(0xffffffffu, lane < n && w.y != 0.0f);
+            const float *src = (k == 2 ? tpo : po) + r0 * kD + 4 * lane;
+            for (int c = 0; c < n; c += 8) {
+                float4 v[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    v[j] = (live >> (c + j)) & 1u
+                               ? *reinterpret_cast<const float4 *>(src + (int64_t)(c + j) * step * kD)
+                               : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const float fj = __shfl_sync(0xffffffffu, f, (c + j) & 31);
+                    o.x = __fmaf_rn(fj, v[j].x, o.x);
+                    o.y = __fmaf_rn(fj, v[j].y, o.y);
+                    o.z = __fmaf_rn(fj, v[j].z, o.z);
+                    o.w = __fmaf_rn(fj, v[j].w, o.w);
+                }
+            }
         }
+    }
+    if constexpr (WARPS > 1) {
+        s_o[warp][lane] = o;
+        if (lane == 0)
+            s_ml[warp] = make_float2(m, l);
+        __syncthreads();
+        if (warp > 0)
+            return;
+#pragma unroll
+        for (int k = 1; k < WARPS; ++k)
+            m = fmaxf(m, s_ml[k].x);
+        const float ms = m == -INFINITY ? 0.0f : m;
+        l = 0.0f;
+        o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+        for (int k = 0; k < WARPS; ++k) {
+            const float f = exp2_fast(__fsub_rn(s_ml[k].x, ms));
+            const float4 v = s_o[k][lane];
+            l = __fmaf_rn(f, s_ml[k].y, l);
+            o.x = __fmaf_rn(f, v.x, o.x), o.y = __fmaf_rn(f, v.y, o.y);
+            o.z = __fmaf_rn(f, v.z, o.z), o.w = __fmaf_rn(f, v.w, o.w);
+        }
+    }
     int i, hg;
     const int64_t tok = row_token(a, p, rr, i, hg);
     const int h = kvh * p.group + hg;
@@ -1049,7 +1104,10 @@ cudaError_t launch_attn_prefix(const AttnArgs &a, const AttnPlan &p, cudaStream_
     if (e != cudaSuccess)
         return e;
     const int64_t rows = p.rows * a.n_kv;
-    e = launch_pdl(attn_join_kernel, dim3((unsigned)((rows + 3) / 4)), dim3(128), 0, stream, a, p);
+    e = rows < kPlanSms * 8
+            ? launch_pdl(attn_join_kernel<4>, dim3((unsigned)rows), dim3(128), 0, stream, a, p)
+            : launch_pdl(attn_join_kernel<1>, dim3((unsigned)((rows + 3) / 4)), dim3(128), 0, stream,
+                         a, p);
     if (e != cudaSuccess || !a.weight_out || a.width == 0)
         return e != cudaSuccess ? e : cudaGetLastError();
     e = launch_pdl(attn_weight_kernel, dim3((unsigned)((a.width + 255) / 256), (unsigned)(a.B < 65535 ? a.B : 65535)),
