@@ -93,7 +93,7 @@ BEAM_API int64_t beam_attn_prefix_workspace(int32_t B, int32_t q_len, int32_t n_
  *   len_in, len_out [rows] int32; freed_out [rows, freed_width] int64, freed_width >=
  *   max(0, width - budget) (may be NULL if that is 0).  All contiguous.  Each output may be the
  *   same buffer as its input; no other overlap.
- * rows in [0, 2^31), width in [0, 2^31); 0 <= recent <= budget. */
+ * rows in [0, 2^31), width in [0, 2^30); 0 <= recent <= budget. */
 BEAM_API int beam_kv_evict_fwd(int64_t *table_out, int32_t *len_out, float *weight_out,
                                int64_t *freed_out, int64_t freed_width, const int64_t *table_in,
                                const int32_t *len_in, const float *weight_in, int64_t rows,

@@ -133,7 +133,7 @@ int beam_kv_evict_fwd(int64_t *table_out, int32_t *len_out, float *weight_out, i
                       const float *weight_in, int64_t rows, int64_t width, int64_t budget,
                       int64_t recent, cudaStream_t stream)
 {
-    if (rows < 0 || rows >= kMost || width < 0 || width >= kMost || budget < 0 || recent < 0 ||
+    if (rows < 0 || rows >= kMost || width < 0 || width >= kMost / 2 || budget < 0 || recent < 0 ||
         recent > budget || freed_width < 0 || freed_width < width - budget)
         return BEAM_ERR_INVALID_ARG;
     if (rows == 0)

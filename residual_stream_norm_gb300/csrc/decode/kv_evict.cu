@@ -1,8 +1,14 @@
 // kv_evict.cu -- eviction from the slot cache by accumulated attention weight (sm_103a).
 //
-// The k-th largest weight of a row is found by radix selection on order-preserving integer keys: four
-// passes of eight bits, each a histogram of the keys that still match.  One ordered pass then moves
-// what stays to the row's front and lists what leaves.
+// The smallest weight that stays is found by radix selection on order-preserving integer keys: digits
+// of 11, 11 and 10 bits from the top, each a histogram of the keys that still match, until what is left
+// of the row is decided.  One ordered pass then moves what stays to the row's front and lists what
+// leaves.  A block reads its weights once, into shared memory; what bounds the operator is then the
+// move: 12 bytes read and 12 written for every entry.
+//
+// One block a row; a cluster shares out long rows when there are few (histograms and counts meet in
+// distributed shared memory).  A row that is compacted in place stays with one block: the ordered pass
+// writes only to places that it has read, but one block of a cluster would overrun its neighbour.
 
 #include "decode_kernels.h"
 #include "decode_mma.cuh"
@@ -12,6 +18,10 @@ namespace {
 
 constexpr int kEvictThreads = 1024;
 constexpr int kEvictWarps = kEvictThreads / 32;
+constexpr int kBins = 2048;
+constexpr int kPerThread = 4;                         // entries of a round
+constexpr int kRound = kPerThread * kEvictThreads;
+constexpr int kMostCached = 50 * 1024;                // weights in shared memory
 
 // Order-preserving key: larger weights, larger keys; -0 as +0; NaN below every number.
 __device__ __forceinline__ uint32_t weight_key(float w)
@@ -22,118 +32,288 @@ __device__ __forceinline__ uint32_t weight_key(float w)
     return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
 
-__global__ void __launch_bounds__(kEvictThreads) kv_evict_kernel(const EvictArgs a)
+__device__ __forceinline__ void cluster_sync()
 {
-    __shared__ uint32_t hist[256];
-    __shared__ uint32_t s_prefix, s_want;
-    __shared__ int s_cnt[2][kEvictWarps];
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::
+                     : "memory");
+}
+
+// A word of another block of the cluster, at this block's shared address.
+__device__ __forceinline__ uint32_t ld_cluster(const void *p, int rank)
+{
+    uint32_t v;
+    asm volatile("{\n\t.reg .u32 a;\n\tmapa.shared::cluster.u32 a, %1, %2;\n\t"
+                 "ld.shared::cluster.u32 %0, [a];\n\t}"
+                 : "=r"(v)
+                 : "r"(smem_addr(p)), "r"(rank)
+                 : "memory");
+    return v;
+}
+
+__device__ __forceinline__ uint32_t warp_scan(uint32_t v, int lane)  // inclusive
+{
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+        const uint32_t o = __shfl_up_sync(0xffffffffu, v, off);
+        v += lane >= off ? o : 0u;
+    }
+    return v;
+}
+
+__global__ void __launch_bounds__(kEvictThreads) kv_evict_kernel(const EvictArgs a, int split,
+                                                                 int cached)
+{
+    extern __shared__ float s_weight[];  // [cached]
+    __shared__ uint32_t s_hist[kBins];
+    __shared__ uint32_t s_warp[2][kPerThread * kEvictWarps];
+    __shared__ uint32_t s_pick[3];       // digit, still wanted of it, whether all of it stays
+    __shared__ uint32_t s_count[2];      // of this block's entries: above the smallest, equal to it
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int rank = blockIdx.x % split;
+    const int64_t row = blockIdx.x / split;
     pdl_launch_dependents();
     pdl_wait();
-    for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
-        int64_t n = a.len_in[row];
-        n = n < 0 ? 0 : (n > a.width ? a.width : n);
-        const float *win = a.weight_in + row * a.width;
-        const int64_t *tin = a.table_in + row * a.width;
-        float *wout = a.weight_out + row * a.width;
-        int64_t *tout = a.table_out + row * a.width;
-        int64_t *freed = a.freed_out + row * a.freed_width;
-        const bool over = n > a.budget;
-        const int64_t old = over ? n - a.recent : 0;  // entries that compete
-        const int64_t keep = over ? a.budget - a.recent : 0;
-        // ---- the smallest key that stays, and how many of the entries that have it -----------------
-        uint32_t thr = 0xffffffffu, ties = 0;
-        if (keep > 0) {
-            if (tid == 0) {
-                s_prefix = 0;
-                s_want = (uint32_t)keep;
-            }
-            for (int shift = 24; shift >= 0; shift -= 8) {
-                if (tid < 256)
-                    hist[tid] = 0;
-                __syncthreads();
-                const uint32_t prefix = s_prefix;
-                for (int64_t j = tid; j < old; j += kEvictThreads) {
-                    const uint32_t k = weight_key(win[j]);
-                    if (shift == 24 || (k >> (shift + 8)) == prefix)
-                        atomicAdd(&hist[(k >> shift) & 255u], 1u);
+    int64_t n64 = a.len_in[row];
+    n64 = n64 < 0 ? 0 : (n64 > a.width ? a.width : n64);
+    const int n = (int)n64;
+    const float *win = a.weight_in + row * a.width;
+    const int64_t *tin = a.table_in + row * a.width;
+    float *wout = a.weight_out + row * a.width;
+    int64_t *tout = a.table_out + row * a.width;
+    int64_t *freed = a.freed_out + row * a.freed_width;
+    const bool over = n > a.budget;
+    const int old = over ? n - (int)a.recent : 0;                   // entries that compete
+    const int keep = over ? (int)(a.budget - a.recent) : 0;         // and how many of them stay
+    const int per = (n + split - 1) / split;
+    const int begin = min(n, rank * per), end = min(n, begin + per);  // this block's entries
+    const int in_smem = min(end - begin, cached);
+    const int compete = max(0, min(end, old) - begin);              // of them, the first ones
+    for (int j = tid; j < in_smem; j += kEvictThreads)
+        s_weight[j] = win[begin + j];
+    auto weight = [&](int j) { return j < in_smem ? s_weight[j] : win[begin + j]; };
+
+    // ---- the key above which all stay, and how many of those equal to it -------------------------------
+    uint32_t thr = 0xffffffffu, ties = 0;
+    if (keep > 0) {
+        uint32_t prefix = 0, want = (uint32_t)keep;
+        int shift = 32;
+#pragma unroll 1
+        for (int pass = 0; pass < 3; ++pass) {
+            const int bits = pass < 2 ? 11 : 10;
+            for (int i = tid; i < kBins; i += kEvictThreads)
+                s_hist[i] = 0;
+            __syncthreads();
+            const int above = shift;
+            shift -= bits;
+            for (int j0 = 0; j0 < compete; j0 += kEvictThreads) {
+                const int j = j0 + tid;
+                bool match = j < compete;
+                uint32_t digit = 0;
+                if (match) {
+                    const uint32_t k = weight_key(weight(j));
+                    match = pass == 0 || (k >> above) == prefix;
+                    digit = (k >> shift) & ((1u << bits) - 1u);
                 }
-                __syncthreads();
-                if (tid == 0) {
-                    uint32_t want = s_want;
-                    int d = 255;
-                    while (hist[d] < want)
-                        want -= hist[d--];
-                    s_want = want;
-                    s_prefix = (prefix << 8) | (uint32_t)d;
+                const uint32_t who = __ballot_sync(0xffffffffu, match);
+                if (who == 0)
+                    continue;
+                // equal digits of a whole warp (equal weights, a narrow range) are one addition
+                const uint32_t d0 = __shfl_sync(0xffffffffu, digit, __ffs(who) - 1);
+                if (__all_sync(0xffffffffu, !match || digit == d0)) {
+                    if (lane == __ffs(who) - 1)
+                        atomicAdd(&s_hist[d0], (uint32_t)__popc(who));
+                } else if (match) {
+                    atomicAdd(&s_hist[digit], 1u);
                 }
-                __syncthreads();
             }
-            thr = s_prefix;
-            ties = s_want;
-        }
-        // ---- move ----------------------------------------------------------------------------------
-        int64_t kept_before = 0, eq_before = 0;
-        for (int64_t base = 0; base < n; base += kEvictThreads) {
-            const int64_t j = base + tid;
-            const bool in = j < n;
-            const float w = in ? win[j] : 0.0f;
-            const int64_t slot = in ? tin[j] : -1;
-            const uint32_t k = weight_key(w);
-            const bool compete = in && j < old;
-            const bool eq = compete && keep > 0 && k == thr;
-            const uint32_t eqb = __ballot_sync(0xffffffffu, eq);
-            if (lane == 0)
-                s_cnt[0][warp] = __popc(eqb);
             __syncthreads();
-            int before = 0, all = 0;
-            for (int x = 0; x < kEvictWarps; ++x) {
-                before += x < warp ? s_cnt[0][x] : 0;
-                all += s_cnt[0][x];
+            uint32_t h[2];  // the bins from the top: 2047 - 2 tid, 2046 - 2 tid
+            h[0] = s_hist[kBins - 1 - 2 * tid];
+            h[1] = s_hist[kBins - 2 - 2 * tid];
+            if (split > 1) {
+                cluster_sync();
+                h[0] = h[1] = 0;
+                for (int q = 0; q < split; ++q) {
+                    h[0] += ld_cluster(&s_hist[kBins - 1 - 2 * tid], q);
+                    h[1] += ld_cluster(&s_hist[kBins - 2 - 2 * tid], q);
+                }
             }
-            const int64_t eq_rank = eq_before + before + __popc(eqb & ((1u << lane) - 1u));
-            const bool stay =
-                in && (!compete || (keep > 0 && (k > thr || (eq && eq_rank < (int64_t)ties))));
-            eq_before += all;
-            const uint32_t sb = __ballot_sync(0xffffffffu, stay);
-            if (lane == 0)
-                s_cnt[1][warp] = __popc(sb);
+            const uint32_t inc = warp_scan(h[0] + h[1], lane);
+            if (lane == 31)
+                s_warp[0][warp] = inc;
             __syncthreads();
-            before = all = 0;
-            for (int x = 0; x < kEvictWarps; ++x) {
-                before += x < warp ? s_cnt[1][x] : 0;
-                all += s_cnt[1][x];
+            const uint32_t w = warp_scan(s_warp[0][lane], lane);
+            const uint32_t before =
+                (warp > 0 ? __shfl_sync(0xffffffffu, w, warp - 1) : 0u) + inc - h[0] - h[1];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const uint32_t b = before + (i ? h[0] : 0u);
+                if (b < want && want <= b + h[i]) {
+                    s_pick[0] = kBins - 1 - 2 * tid - i;
+                    s_pick[1] = want - b;
+                    s_pick[2] = want - b == h[i];
+                }
             }
-            const int64_t to = kept_before + before + __popc(sb & ((1u << lane) - 1u));
-            if (stay) {
-                wout[to] = w;
-                tout[to] = slot;
-            } else if (in) {
-                freed[j - to] = slot;
-            }
-            kept_before += all;
             __syncthreads();
+            prefix = (prefix << bits) | s_pick[0];
+            want = s_pick[1];
+            const bool decided = s_pick[2] != 0;
+            if (split > 1)
+                cluster_sync();  // the others have read this block's histogram
+            if (decided && pass < 2) {  // all of the digit stays: everything from its first key on
+                thr = (prefix << shift) - 1u;
+                want = 0;
+                break;
+            }
+            thr = prefix;
         }
-        for (int64_t j = kept_before + tid; j < a.width; j += kEvictThreads) {
-            wout[j] = 0.0f;
-            tout[j] = -1;
-        }
-        for (int64_t j = n - kept_before + tid; j < a.freed_width; j += kEvictThreads)
-            freed[j] = -1;
-        if (tid == 0)
-            a.len_out[row] = (int32_t)kept_before;
-        __syncthreads();
+        ties = want;
     }
+    __syncthreads();
+    // ---- where this block's entries go -------------------------------------------------------------
+    uint32_t gt_before = 0, eq_before = 0;  // of the competing entries in front
+    if (split > 1 && keep > 0) {
+        if (tid < 2)
+            s_count[tid] = 0;
+        __syncthreads();
+        uint32_t gt = 0, eq = 0;
+        for (int j = tid; j < compete; j += kEvictThreads) {
+            const uint32_t k = weight_key(weight(j));
+            gt += k > thr;
+            eq += k == thr;
+        }
+        gt = __reduce_add_sync(0xffffffffu, gt);
+        eq = __reduce_add_sync(0xffffffffu, eq);
+        if (lane == 0) {
+            atomicAdd(&s_count[0], gt);
+            atomicAdd(&s_count[1], eq);
+        }
+        cluster_sync();
+        for (int q = 0; q < rank; ++q) {
+            gt_before += ld_cluster(&s_count[0], q);
+            eq_before += ld_cluster(&s_count[1], q);
+        }
+        cluster_sync();
+    }
+    // ---- move: rounds in order; a round's reads are complete before its writes ---------------------------
+    const int64_t m = over ? a.budget : n;
+    int64_t slot[kPerThread];
+#pragma unroll
+    for (int k = 0; k < kPerThread; ++k) {
+        const int j = begin + k * kEvictThreads + tid;
+        slot[k] = j < end ? tin[j] : -1;
+    }
+    for (int base = begin, round = 0; base < end; base += kRound, round ^= 1) {
+        float w[kPerThread];
+        int64_t next[kPerThread];
+        uint32_t above[kPerThread], equal[kPerThread];
+#pragma unroll
+        for (int k = 0; k < kPerThread; ++k) {
+            const int j = base + k * kEvictThreads + tid;
+            w[k] = j < end ? weight(j - begin) : 0.0f;
+            const int jn = j + kRound;
+            next[k] = jn < end ? tin[jn] : -1;
+            const uint32_t key = weight_key(w[k]);
+            const bool c = j < old && j < end && keep > 0;
+            above[k] = __ballot_sync(0xffffffffu, c && key > thr);
+            equal[k] = __ballot_sync(0xffffffffu, c && key == thr);
+            if (lane == 0)
+                s_warp[round][k * kEvictWarps + warp] =
+                    (uint32_t)__popc(above[k]) | (uint32_t)__popc(equal[k]) << 16;
+        }
+        __syncthreads();
+        // running counts over the 128 (k, warp): four a lane
+        const uint4 c4 = *reinterpret_cast<const uint4 *>(&s_warp[round][4 * lane]);
+        const uint32_t sum = c4.x + c4.y + c4.z + c4.w, inc = warp_scan(sum, lane);
+        const uint32_t all = __shfl_sync(0xffffffffu, inc, 31);
+        uint32_t mine = inc - sum;  // exclusive, at this warp's place among the lane's four
+        mine += (warp & 3) > 0 ? c4.x : 0u;
+        mine += (warp & 3) > 1 ? c4.y : 0u;
+        mine += (warp & 3) > 2 ? c4.z : 0u;
+#pragma unroll
+        for (int k = 0; k < kPerThread; ++k) {
+            const int j = base + k * kEvictThreads + tid;
+            const uint32_t front = __shfl_sync(0xffffffffu, mine, 8 * k + warp / 4);
+            const uint32_t low = (1u << lane) - 1u;
+            const uint32_t gt = gt_before + (front & 0xffffu) + __popc(above[k] & low);
+            const uint32_t eq = eq_before + (front >> 16) + __popc(equal[k] & low);
+            if (j < end) {
+                const bool is_gt = (above[k] >> lane) & 1u, is_eq = (equal[k] >> lane) & 1u;
+                const bool stay = j >= old || is_gt || (is_eq && eq < ties);
+                // entries in front that stay
+                const int to = j >= old ? (over ? keep + j - old : j) : (int)(gt + min(eq, ties));
+                if (stay) {
+                    wout[to] = w[k];
+                    tout[to] = slot[k];
+                } else {
+                    freed[j - to] = slot[k];
+                }
+            }
+            slot[k] = next[k];
+        }
+        gt_before += all & 0xffffu;
+        eq_before += all >> 16;
+    }
+    // ---- behind what stays -------------------------------------------------------------------------
+    const int64_t stride = (int64_t)split * kEvictThreads;
+    __syncthreads();  // in place: the last round's reads of the others are complete
+    for (int64_t j = m + rank * kEvictThreads + tid; j < a.width; j += stride) {
+        wout[j] = 0.0f;
+        tout[j] = -1;
+    }
+    for (int64_t j = n - m + rank * kEvictThreads + tid; j < a.freed_width; j += stride)
+        freed[j] = -1;
+    if (tid == 0 && rank == 0)
+        a.len_out[row] = (int32_t)m;
 }
 
 }  // namespace
 
 cudaError_t launch_kv_evict(const EvictArgs &a, cudaStream_t stream)
 {
-    const unsigned grid = (unsigned)(a.rows < (1 << 20) ? a.rows : (1 << 20));
-    const cudaError_t e =
-        launch_pdl(kv_evict_kernel, dim3(grid), dim3(kEvictThreads), 0, stream, a);
-    return e != cudaSuccess ? e : cudaGetLastError();
+    const bool in_place = (a.width > 0) && (a.table_in == a.table_out || a.weight_in == a.weight_out ||
+                                            a.len_in == a.len_out);
+    // a cluster per row while that leaves SMs over and gives each block a round of its own
+    int split = 1;
+    while (!in_place && split < 8 && a.rows * split * 2 <= kPlanSms + 8 &&
+           a.width >= (int64_t)split * 2 * kRound / 2)
+        split *= 2;
+    const int64_t per = (a.width + split - 1) / split;
+    const int cached = (int)(per < kMostCached ? per : kMostCached);
+    cudaError_t e = allow_smem<kv_evict_kernel>(kMostCached * 4);
+    if (e != cudaSuccess)
+        return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.blockDim = dim3(kEvictThreads);
+    cfg.dynamicSmemBytes = (size_t)cached * 4;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = (unsigned)split;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = split > 1 ? 2 : 1;
+    // at most 2^30 blocks a launch
+    const int64_t most = ((int64_t)1 << 30) / split;
+    for (int64_t r = 0; r < a.rows; r += most) {
+        EvictArgs b = a;
+        b.rows = a.rows - r < most ? a.rows - r : most;
+        b.table_out = a.table_out + r * a.width;
+        b.table_in = a.table_in + r * a.width;
+        b.weight_out = a.weight_out + r * a.width;
+        b.weight_in = a.weight_in + r * a.width;
+        b.freed_out = a.freed_out + r * a.freed_width;
+        b.len_in = a.len_in + r;
+        b.len_out = a.len_out + r;
+        cfg.gridDim = dim3((unsigned)(b.rows * split));
+        e = cudaLaunchKernelEx(&cfg, kv_evict_kernel, b, split, cached);
+        if (e != cudaSuccess)
+            return e;
+    }
+    return cudaGetLastError();
 }
 
 }  // namespace beam

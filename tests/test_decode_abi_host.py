@@ -84,7 +84,8 @@ def evict(lib, t_out=A, n_out=A, w_out=A, freed=A, fw=64, t_in=A, n_in=A, w_in=A
 
 
 @pytest.mark.parametrize("kw,want", [
-    (dict(rows=-1), INVALID), (dict(width=-1), INVALID), (dict(budget=-1), INVALID),
+    (dict(rows=-1), INVALID), (dict(width=-1), INVALID), (dict(width=1 << 30, fw=1 << 30), INVALID),
+    (dict(budget=-1), INVALID),
     (dict(recent=-1), INVALID), (dict(recent=65), INVALID), (dict(fw=63), INVALID),
     (dict(freed=None), INVALID), (dict(t_out=None), INVALID), (dict(n_out=None), INVALID),
     (dict(w_out=None), INVALID), (dict(t_in=None), INVALID), (dict(n_in=None), INVALID),

@@ -93,6 +93,7 @@ def test_long_rows(kind):
                                         (131072, 131000, 64, [131072, 131001])):
         table, weight = case(2, width, width, kind)
         check(table, np.array(lens, np.int32), weight, budget, recent)
+        check(table, np.array(lens, np.int32), weight, budget, recent, in_place=True)
 
 
 def test_many_rows():
