@@ -7,8 +7,10 @@
 // move: 12 bytes read and 12 written for every entry.
 //
 // One block a row; a cluster shares out long rows when there are few (histograms and counts meet in
-// distributed shared memory).  A row that is compacted in place stays with one block: the ordered pass
-// writes only to places that it has read, but one block of a cluster would overrun its neighbour.
+// distributed shared memory).  Each warp counts what stays of a stretch of its own, and from the sums
+// in front of it moves that stretch by itself.  A row that is compacted in place takes one block and
+// goes in rounds instead, all of a round's reads before its writes: a stretch's front end is moved
+// into the back of the stretch before it.
 
 #include "decode_kernels.h"
 #include "decode_mma.cuh"
@@ -19,8 +21,9 @@ namespace {
 constexpr int kEvictThreads = 1024;
 constexpr int kEvictWarps = kEvictThreads / 32;
 constexpr int kBins = 2048;
-constexpr int kPerThread = 4;                         // entries of a round
+constexpr int kPerThread = 4;                         // entries of a round, in place
 constexpr int kRound = kPerThread * kEvictThreads;
+constexpr int kList = 4096;                           // keys that the last digits are looked up in
 constexpr int kMostCached = 50 * 1024;                // weights in shared memory
 
 // Order-preserving key: larger weights, larger keys; -0 as +0; NaN below every number.
@@ -60,14 +63,17 @@ __device__ __forceinline__ uint32_t warp_scan(uint32_t v, int lane)  // inclusiv
     return v;
 }
 
+template <bool IN_PLACE>
 __global__ void __launch_bounds__(kEvictThreads) kv_evict_kernel(const EvictArgs a, int split,
                                                                  int cached)
 {
     extern __shared__ float s_weight[];  // [cached]
     __shared__ uint32_t s_hist[kBins];
+    __shared__ uint32_t s_list[kList];
     __shared__ uint32_t s_warp[2][kPerThread * kEvictWarps];
     __shared__ uint32_t s_pick[3];       // digit, still wanted of it, whether all of it stays
     __shared__ uint32_t s_count[2];      // of this block's entries: above the smallest, equal to it
+    __shared__ uint32_t s_listed;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int rank = blockIdx.x % split;
     const int64_t row = blockIdx.x / split;
@@ -88,45 +94,71 @@ __global__ void __launch_bounds__(kEvictThreads) kv_evict_kernel(const EvictArgs
     const int begin = min(n, rank * per), end = min(n, begin + per);  // this block's entries
     const int in_smem = min(end - begin, cached);
     const int compete = max(0, min(end, old) - begin);              // of them, the first ones
-    for (int j = tid; j < in_smem; j += kEvictThreads)
-        s_weight[j] = win[begin + j];
-    auto weight = [&](int j) { return j < in_smem ? s_weight[j] : win[begin + j]; };
+    if (IN_PLACE || keep > 0) {  // in place a round's weights may be overwritten by its neighbours
+#pragma unroll 8
+        for (int j = tid; j < in_smem; j += kEvictThreads)
+            s_weight[j] = win[begin + j];
+    }
+    const int have = IN_PLACE || keep > 0 ? in_smem : 0;
+    auto weight = [&](int j) { return j < have ? s_weight[j] : win[begin + j]; };
 
     // ---- the key above which all stay, and how many of those equal to it -------------------------------
     uint32_t thr = 0xffffffffu, ties = 0;
     if (keep > 0) {
         uint32_t prefix = 0, want = (uint32_t)keep;
         int shift = 32;
+        bool listed = false;  // the keys that still match are in s_list
 #pragma unroll 1
         for (int pass = 0; pass < 3; ++pass) {
             const int bits = pass < 2 ? 11 : 10;
             for (int i = tid; i < kBins; i += kEvictThreads)
                 s_hist[i] = 0;
+            if (tid == 0 && pass == 1)
+                s_listed = 0;
             __syncthreads();
             const int above = shift;
             shift -= bits;
-            for (int j0 = 0; j0 < compete; j0 += kEvictThreads) {
-                const int j = j0 + tid;
-                bool match = j < compete;
-                uint32_t digit = 0;
-                if (match) {
-                    const uint32_t k = weight_key(weight(j));
-                    match = pass == 0 || (k >> above) == prefix;
-                    digit = (k >> shift) & ((1u << bits) - 1u);
+            const uint32_t digits = (1u << bits) - 1u;
+            if (pass == 0) {
+#pragma unroll 4
+                for (int j0 = 0; j0 < compete; j0 += kEvictThreads) {
+                    const int j = j0 + tid;
+                    const bool in = j < compete;
+                    const uint32_t digit = in ? weight_key(weight(j)) >> 21 : 0u;
+                    // equal digits of a whole warp (equal weights) are one addition
+                    const uint32_t who = __ballot_sync(0xffffffffu, in);
+                    const uint32_t d0 = __shfl_sync(0xffffffffu, digit, 0);
+                    if (__all_sync(0xffffffffu, !in || digit == d0)) {
+                        if (lane == 0 && who)
+                            atomicAdd(&s_hist[d0], (uint32_t)__popc(who));
+                    } else if (in) {
+                        atomicAdd(&s_hist[digit], 1u);
+                    }
                 }
-                const uint32_t who = __ballot_sync(0xffffffffu, match);
-                if (who == 0)
-                    continue;
-                // equal digits of a whole warp (equal weights, a narrow range) are one addition
-                const uint32_t d0 = __shfl_sync(0xffffffffu, digit, __ffs(who) - 1);
-                if (__all_sync(0xffffffffu, !match || digit == d0)) {
-                    if (lane == __ffs(who) - 1)
-                        atomicAdd(&s_hist[d0], (uint32_t)__popc(who));
-                } else if (match) {
-                    atomicAdd(&s_hist[digit], 1u);
+            } else if (!listed) {
+                // pass 1 keeps the keys that match the first digit, if they fit
+#pragma unroll 4
+                for (int j = tid; j < compete; j += kEvictThreads) {
+                    const uint32_t k = weight_key(weight(j));
+                    if (k >> above == prefix) {
+                        atomicAdd(&s_hist[(k >> shift) & digits], 1u);
+                        if (pass == 1) {
+                            const uint32_t at = atomicAdd(&s_listed, 1u);
+                            if (at < kList)
+                                s_list[at] = k;
+                        }
+                    }
+                }
+            } else {
+                const int m = (int)s_listed;
+                for (int j = tid; j < m; j += kEvictThreads) {
+                    const uint32_t k = s_list[j];
+                    if (k >> above == prefix)
+                        atomicAdd(&s_hist[(k >> shift) & digits], 1u);
                 }
             }
             __syncthreads();
+            listed = pass == 1 && s_listed <= kList;
             uint32_t h[2];  // the bins from the top: 2047 - 2 tid, 2046 - 2 tid
             h[0] = s_hist[kBins - 1 - 2 * tid];
             h[1] = s_hist[kBins - 2 - 2 * tid];
@@ -169,34 +201,92 @@ __global__ void __launch_bounds__(kEvictThreads) kv_evict_kernel(const EvictArgs
         }
         ties = want;
     }
-    __syncthreads();
-    // ---- where this block's entries go -------------------------------------------------------------
-    uint32_t gt_before = 0, eq_before = 0;  // of the competing entries in front
-    if (split > 1 && keep > 0) {
-        if (tid < 2)
-            s_count[tid] = 0;
-        __syncthreads();
-        uint32_t gt = 0, eq = 0;
-        for (int j = tid; j < compete; j += kEvictThreads) {
-            const uint32_t k = weight_key(weight(j));
-            gt += k > thr;
-            eq += k == thr;
-        }
-        gt = __reduce_add_sync(0xffffffffu, gt);
-        eq = __reduce_add_sync(0xffffffffu, eq);
-        if (lane == 0) {
-            atomicAdd(&s_count[0], gt);
-            atomicAdd(&s_count[1], eq);
-        }
-        cluster_sync();
-        for (int q = 0; q < rank; ++q) {
-            gt_before += ld_cluster(&s_count[0], q);
-            eq_before += ld_cluster(&s_count[1], q);
-        }
-        cluster_sync();
-    }
-    // ---- move: rounds in order; a round's reads are complete before its writes ---------------------------
     const int64_t m = over ? a.budget : n;
+    uint32_t gt_before = 0, eq_before = 0;  // of the competing entries in front
+    if constexpr (!IN_PLACE) {
+        // ---- each warp's stretch: count, sums in front, move ---------------------------------------
+        const int len = ((end - begin + kEvictWarps - 1) / kEvictWarps + 31) & ~31;
+        const int s0 = min(end - begin, warp * len), s1 = min(end - begin, s0 + len);
+        if (keep > 0) {
+            uint32_t gt = 0, eq = 0;
+            const int c1 = min(s1, compete);
+#pragma unroll 4
+            for (int j = s0 + lane; j < c1; j += 32) {
+                const uint32_t k = weight_key(weight(j));
+                gt += k > thr;
+                eq += k == thr;
+            }
+            gt = __reduce_add_sync(0xffffffffu, gt);
+            eq = __reduce_add_sync(0xffffffffu, eq);
+            __syncthreads();  // s_warp is free
+            if (lane == 0) {
+                s_warp[0][warp] = gt;
+                s_warp[1][warp] = eq;
+            }
+            __syncthreads();
+            const uint32_t g = warp_scan(s_warp[0][lane], lane), e = warp_scan(s_warp[1][lane], lane);
+            gt_before = warp > 0 ? __shfl_sync(0xffffffffu, g, warp - 1) : 0u;
+            eq_before = warp > 0 ? __shfl_sync(0xffffffffu, e, warp - 1) : 0u;
+            if (split > 1) {
+                if (tid == 31) {
+                    s_count[0] = g;
+                    s_count[1] = e;
+                }
+                cluster_sync();
+                for (int q = 0; q < rank; ++q) {
+                    gt_before += ld_cluster(&s_count[0], q);
+                    eq_before += ld_cluster(&s_count[1], q);
+                }
+                cluster_sync();
+            }
+        }
+        constexpr int kAhead = 4;
+        const uint32_t low = (1u << lane) - 1u;
+        int64_t slot[kAhead];
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+            const int j = s0 + 32 * k + lane;
+            slot[k] = j < s1 ? tin[begin + j] : -1;
+        }
+        for (int base = s0; base < s1; base += 32 * kAhead) {
+            float w[kAhead];
+            int64_t next[kAhead];
+#pragma unroll
+            for (int k = 0; k < kAhead; ++k) {
+                const int j = base + 32 * k + lane, jn = j + 32 * kAhead;
+                w[k] = j < s1 ? weight(j) : 0.0f;
+                next[k] = jn < s1 ? tin[begin + jn] : -1;
+            }
+#pragma unroll
+            for (int k = 0; k < kAhead; ++k) {
+                const int j = base + 32 * k + lane;
+                const uint32_t key = weight_key(w[k]);
+                const bool c = j < compete && keep > 0;
+                const uint32_t above = __ballot_sync(0xffffffffu, c && key > thr);
+                const uint32_t equal = __ballot_sync(0xffffffffu, c && key == thr);
+                const uint32_t gt = gt_before + __popc(above & low);
+                const uint32_t eq = eq_before + __popc(equal & low);
+                if (j < s1) {
+                    const int at = begin + j;
+                    const bool stay =
+                        at >= old || (c && (key > thr || (key == thr && eq < ties)));
+                    // entries in front that stay
+                    const int to = at >= old ? at - old + keep : (int)(gt + min(eq, ties));
+                    if (stay) {
+                        wout[to] = w[k];
+                        tout[to] = slot[k];
+                    } else {
+                        freed[at - to] = slot[k];
+                    }
+                }
+                gt_before += __popc(above);
+                eq_before += __popc(equal);
+                slot[k] = next[k];
+            }
+        }
+    } else {
+    __syncthreads();
+    // ---- move: rounds in order; a round's reads are complete before its writes ---------------------------
     int64_t slot[kPerThread];
 #pragma unroll
     for (int k = 0; k < kPerThread; ++k) {
@@ -254,9 +344,10 @@ __global__ void __launch_bounds__(kEvictThreads) kv_evict_kernel(const EvictArgs
         gt_before += all & 0xffffu;
         eq_before += all >> 16;
     }
+    }
     // ---- behind what stays -------------------------------------------------------------------------
     const int64_t stride = (int64_t)split * kEvictThreads;
-    __syncthreads();  // in place: the last round's reads of the others are complete
+    __syncthreads();  // in place: the others' reads are complete
     for (int64_t j = m + rank * kEvictThreads + tid; j < a.width; j += stride) {
         wout[j] = 0.0f;
         tout[j] = -1;
@@ -280,7 +371,8 @@ cudaError_t launch_kv_evict(const EvictArgs &a, cudaStream_t stream)
         split *= 2;
     const int64_t per = (a.width + split - 1) / split;
     const int cached = (int)(per < kMostCached ? per : kMostCached);
-    cudaError_t e = allow_smem<kv_evict_kernel>(kMostCached * 4);
+    cudaError_t e = in_place ? allow_smem<kv_evict_kernel<true>>(kMostCached * 4)
+                             : allow_smem<kv_evict_kernel<false>>(kMostCached * 4);
     if (e != cudaSuccess)
         return e;
     cudaLaunchConfig_t cfg = {};
@@ -309,7 +401,8 @@ cudaError_t launch_kv_evict(const EvictArgs &a, cudaStream_t stream)
         b.len_in = a.len_in + r;
         b.len_out = a.len_out + r;
         cfg.gridDim = dim3((unsigned)(b.rows * split));
-        e = cudaLaunchKernelEx(&cfg, kv_evict_kernel, b, split, cached);
+        e = cudaLaunchKernelEx(&cfg, in_place ? kv_evict_kernel<true> : kv_evict_kernel<false>, b,
+                               split, cached);
         if (e != cudaSuccess)
             return e;
     }
