@@ -26,6 +26,8 @@ constexpr int kRound = kPerThread * kEvictThreads;
 constexpr int kList = 4096;                           // keys that the last digits are looked up in
 constexpr int kMostCached = 50 * 1024;                // weights in shared memory
 
+constexpr uint32_t kZeroKey = 0x80000000u;
+
 // Order-preserving key: larger weights, larger keys; -0 as +0; NaN below every number.
 __device__ __forceinline__ uint32_t weight_key(float w)
 {
@@ -53,6 +55,17 @@ __device__ __forceinline__ uint32_t ld_cluster(const void *p, int rank)
     return v;
 }
 
+__device__ __forceinline__ uint2 ld_cluster2(const void *p, int rank)
+{
+    uint2 v;
+    asm volatile("{\n\t.reg .u32 a;\n\tmapa.shared::cluster.u32 a, %2, %3;\n\t"
+                 "ld.shared::cluster.v2.u32 {%0, %1}, [a];\n\t}"
+                 : "=r"(v.x), "=r"(v.y)
+                 : "r"(smem_addr(p)), "r"(rank)
+                 : "memory");
+    return v;
+}
+
 __device__ __forceinline__ uint32_t warp_scan(uint32_t v, int lane)  // inclusive
 {
 #pragma unroll
@@ -68,12 +81,12 @@ __global__ void __launch_bounds__(kEvictThreads) kv_evict_kernel(const EvictArgs
                                                                  int cached)
 {
     extern __shared__ float s_weight[];  // [cached]
-    __shared__ uint32_t s_hist[kBins];
+    __shared__ __align__(8) uint32_t s_hist[kBins];
     __shared__ uint32_t s_list[kList];
     __shared__ uint32_t s_warp[2][kPerThread * kEvictWarps];
     __shared__ uint32_t s_pick[3];       // digit, still wanted of it, whether all of it stays
     __shared__ uint32_t s_count[2];      // of this block's entries: above the smallest, equal to it
-    __shared__ uint32_t s_listed;
+    __shared__ uint32_t s_listed, s_zeros;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int rank = blockIdx.x % split;
     const int64_t row = blockIdx.x / split;
@@ -94,11 +107,7 @@ __global__ void __launch_bounds__(kEvictThreads) kv_evict_kernel(const EvictArgs
     const int begin = min(n, rank * per), end = min(n, begin + per);  // this block's entries
     const int in_smem = min(end - begin, cached);
     const int compete = max(0, min(end, old) - begin);              // of them, the first ones
-    if (IN_PLACE || keep > 0) {  // in place a round's weights may be overwritten by its neighbours
-#pragma unroll 8
-        for (int j = tid; j < in_smem; j += kEvictThreads)
-            s_weight[j] = win[begin + j];
-    }
+    // In place all weights that fit come first: a round's may be overwritten by the one before it.
     const int have = IN_PLACE || keep > 0 ? in_smem : 0;
     auto weight = [&](int j) { return j < have ? s_weight[j] : win[begin + j]; };
 
@@ -113,34 +122,57 @@ __global__ void __launch_bounds__(kEvictThreads) kv_evict_kernel(const EvictArgs
             const int bits = pass < 2 ? 11 : 10;
             for (int i = tid; i < kBins; i += kEvictThreads)
                 s_hist[i] = 0;
-            if (tid == 0 && pass == 1)
-                s_listed = 0;
+            if (tid == 0 && pass == 0)
+                s_listed = s_zeros = 0;
             __syncthreads();
             const int above = shift;
             shift -= bits;
             const uint32_t digits = (1u << bits) - 1u;
             if (pass == 0) {
-#pragma unroll 4
-                for (int j0 = 0; j0 < compete; j0 += kEvictThreads) {
-                    const int j = j0 + tid;
-                    const bool in = j < compete;
-                    const uint32_t digit = in ? weight_key(weight(j)) >> 21 : 0u;
-                    // equal digits of a whole warp (equal weights) are one addition
-                    const uint32_t who = __ballot_sync(0xffffffffu, in);
-                    const uint32_t d0 = __shfl_sync(0xffffffffu, digit, 0);
-                    if (__all_sync(0xffffffffu, !in || digit == d0)) {
-                        if (lane == 0 && who)
-                            atomicAdd(&s_hist[d0], (uint32_t)__popc(who));
-                    } else if (in) {
-                        atomicAdd(&s_hist[digit], 1u);
+                // the weights arrive here; zeros, often many, are counted apart
+                uint32_t zeros = 0;
+#pragma unroll 1
+                for (int j0 = tid; j0 < in_smem; j0 += 8 * kEvictThreads) {
+                    float w[8];
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) {
+                        const int j = j0 + k * kEvictThreads;
+                        w[k] = j < in_smem ? win[begin + j] : 0.0f;
                     }
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) {
+                        const int j = j0 + k * kEvictThreads;
+                        if (j < in_smem)
+                            s_weight[j] = w[k];
+                        if (j < compete) {
+                            if (w[k] == 0.0f)
+                                ++zeros;
+                            else
+                                atomicAdd(&s_hist[weight_key(w[k]) >> 21], 1u);
+                        }
+                    }
+                }
+                for (int j = in_smem + tid; j < compete; j += kEvictThreads) {
+                    const float w = win[begin + j];
+                    if (w == 0.0f)
+                        ++zeros;
+                    else
+                        atomicAdd(&s_hist[weight_key(w) >> 21], 1u);
+                }
+                zeros = __reduce_add_sync(0xffffffffu, zeros);
+                if (lane == 0 && zeros) {
+                    atomicAdd(&s_zeros, zeros);
+                    atomicAdd(&s_hist[kZeroKey >> 21], zeros);
                 }
             } else if (!listed) {
                 // pass 1 keeps the keys that match the first digit, if they fit
+                if (tid == 0 && kZeroKey >> above == prefix)
+                    atomicAdd(&s_hist[(kZeroKey >> shift) & digits], s_zeros);
+                const float *from = compete <= have ? s_weight : win + begin;
 #pragma unroll 4
                 for (int j = tid; j < compete; j += kEvictThreads) {
-                    const uint32_t k = weight_key(weight(j));
-                    if (k >> above == prefix) {
+                    const uint32_t k = weight_key(from[j]);
+                    if (k >> above == prefix && k != kZeroKey) {
                         atomicAdd(&s_hist[(k >> shift) & digits], 1u);
                         if (pass == 1) {
                             const uint32_t at = atomicAdd(&s_listed, 1u);
@@ -150,6 +182,8 @@ __global__ void __launch_bounds__(kEvictThreads) kv_evict_kernel(const EvictArgs
                     }
                 }
             } else {
+                if (tid == 0 && kZeroKey >> above == prefix)
+                    atomicAdd(&s_hist[(kZeroKey >> shift) & digits], s_zeros);
                 const int m = (int)s_listed;
                 for (int j = tid; j < m; j += kEvictThreads) {
                     const uint32_t k = s_list[j];
@@ -166,8 +200,9 @@ __global__ void __launch_bounds__(kEvictThreads) kv_evict_kernel(const EvictArgs
                 cluster_sync();
                 h[0] = h[1] = 0;
                 for (int q = 0; q < split; ++q) {
-                    h[0] += ld_cluster(&s_hist[kBins - 1 - 2 * tid], q);
-                    h[1] += ld_cluster(&s_hist[kBins - 2 - 2 * tid], q);
+                    const uint2 v = ld_cluster2(&s_hist[kBins - 2 - 2 * tid], q);
+                    h[0] += v.y;
+                    h[1] += v.x;
                 }
             }
             const uint32_t inc = warp_scan(h[0] + h[1], lane);
@@ -200,6 +235,9 @@ __global__ void __launch_bounds__(kEvictThreads) kv_evict_kernel(const EvictArgs
             thr = prefix;
         }
         ties = want;
+    } else if (IN_PLACE) {
+        for (int j = tid; j < in_smem; j += kEvictThreads)
+            s_weight[j] = win[begin + j];
     }
     const int64_t m = over ? a.budget : n;
     uint32_t gt_before = 0, eq_before = 0;  // of the competing entries in front
@@ -207,12 +245,13 @@ __global__ void __launch_bounds__(kEvictThreads) kv_evict_kernel(const EvictArgs
         // ---- each warp's stretch: count, sums in front, move ---------------------------------------
         const int len = ((end - begin + kEvictWarps - 1) / kEvictWarps + 31) & ~31;
         const int s0 = min(end - begin, warp * len), s1 = min(end - begin, s0 + len);
+        const float *from = s1 <= have ? s_weight : win + begin;
         if (keep > 0) {
             uint32_t gt = 0, eq = 0;
             const int c1 = min(s1, compete);
 #pragma unroll 4
             for (int j = s0 + lane; j < c1; j += 32) {
-                const uint32_t k = weight_key(weight(j));
+                const uint32_t k = weight_key(from[j]);
                 gt += k > thr;
                 eq += k == thr;
             }
@@ -254,7 +293,7 @@ __global__ void __launch_bounds__(kEvictThreads) kv_evict_kernel(const EvictArgs
 #pragma unroll
             for (int k = 0; k < kAhead; ++k) {
                 const int j = base + 32 * k + lane, jn = j + 32 * kAhead;
-                w[k] = j < s1 ? weight(j) : 0.0f;
+                w[k] = j < s1 ? from[j] : 0.0f;
                 next[k] = jn < s1 ? tin[begin + jn] : -1;
             }
 #pragma unroll
