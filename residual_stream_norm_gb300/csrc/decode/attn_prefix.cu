@@ -50,6 +50,12 @@ struct RowsSmem {
 
 __device__ unsigned int g_decode_fault_word = 0u;
 
+// What a unit costs a block besides its key tiles (queries, joining the warps, results), in tiles:
+// shares are dealt out over the tiles and this, so that a block of many short units has fewer tiles.
+// The first kUnitCost places of a unit's stretch stand for it; a share that ends among them has no
+// tile of the unit.
+constexpr int kUnitCost = 2;
+
 // The block whose share [c tot / C, (c + 1) tot / C) contains tile x (C <= tot).
 __device__ __forceinline__ int64_t owner(int64_t x, int64_t tot, int64_t ctas)
 {
@@ -116,7 +122,14 @@ __device__ __forceinline__ bool stage_has_nonfinite(uint32_t vt, int lane)
     return __any_sync(0xffffffffu, bad);
 }
 
-// Position in the units' sequence of key tiles.
+// Places of each of a sequence's units: its tiles and what it costs besides; none without a key.
+__device__ __forceinline__ int64_t seq_places(const AttnArgs &a, const AttnPlan &p, int64_t b)
+{
+    const int64_t t = seq_tiles(a, p, b);
+    return t > 0 ? t + kUnitCost : 0;
+}
+
+// Position in the units' sequence of places.
 struct Cursor {
     int64_t tile, end;    // the next tile of the share, and the share's end
     int64_t b, b_start;   // sequence of `tile` (past the prefix), its first tile
@@ -128,6 +141,7 @@ struct Unit {
     int64_t unit;
     int32_t kvh;
     int32_t row0, row_end;
+    int32_t row_base;     // the sequence's first row (suffix)
     int32_t k0, k1;       // keys of the part
     int32_t key_end;      // of the list
     bool prefix, whole;
@@ -136,46 +150,50 @@ struct Unit {
 __device__ __forceinline__ Unit next_unit(const AttnArgs &a, const AttnPlan &p, int M, Cursor &c)
 {
     Unit u;
-    const int64_t p_units = a.n_kv * p.p_rtiles, p_total = p_units * p.p_tiles;
+    const int64_t p_units = a.n_kv * p.p_rtiles, p_places = p.p_tiles + kUnitCost;
+    const int64_t p_total = p_units * p_places;
     const int64_t per_seq = (int64_t)a.n_kv * p.s_rtiles;
     int64_t start, tiles;
     int32_t key_first;
     u.prefix = c.tile < p_total;
     if (u.prefix) {
-        u.unit = div32(c.tile, p.p_tiles);
+        u.unit = div32(c.tile, p_places);
         tiles = p.p_tiles;
-        start = u.unit * tiles;
+        start = u.unit * p_places + kUnitCost;
         u.kvh = (int32_t)div32(u.unit, p.p_rtiles);
         u.row0 = (int32_t)(u.unit - u.kvh * p.p_rtiles) * M;
         u.row_end = (int32_t)p.rows;
+        u.row_base = 0;
         u.list = a.prefix;
         key_first = (int32_t)p.p_first;
         u.key_end = (int32_t)a.n_prefix;
     } else {
-        tiles = seq_tiles(a, p, c.b);
-        while (c.tile >= c.b_start + per_seq * tiles) {
-            c.b_start += per_seq * tiles;
-            tiles = seq_tiles(a, p, ++c.b);
+        int64_t places = seq_places(a, p, c.b);
+        while (c.tile >= c.b_start + per_seq * places) {
+            c.b_start += per_seq * places;
+            places = seq_places(a, p, ++c.b);
         }
-        const int64_t x = div32(c.tile - c.b_start, tiles);
+        const int64_t x = div32(c.tile - c.b_start, places);
+        tiles = places - kUnitCost;
         u.unit = p_units + c.b * per_seq + x;
-        start = c.b_start + x * tiles;
+        start = c.b_start + x * places + kUnitCost;
         u.kvh = (int32_t)div32(x, p.s_rtiles);
         u.row0 = (int32_t)(c.b * p.R + (x - (int64_t)u.kvh * p.s_rtiles) * M);
         u.row_end = (int32_t)((c.b + 1) * p.R);
+        u.row_base = u.row_end - p.R;
         u.list = a.table + c.b * a.table_stride;
         u.key_end = (int32_t)seq_len(a, c.b);
         key_first = (int32_t)first_tile_key(u.key_end, a.q_len, a.window);
     }
-    const int64_t seg_end = min(c.end, start + tiles);
-    u.whole = c.tile == start && seg_end == start + tiles;
-    u.k0 = key_first + (int32_t)(c.tile - start) * p.tile_keys;
+    const int64_t seg_end = min(c.end, start + tiles), first = max(c.tile, start);
+    u.whole = first == start && seg_end == start + tiles;
+    u.k0 = key_first + (int32_t)(first - start) * p.tile_keys;
     u.k1 = (int32_t)min((int64_t)u.key_end, key_first + (seg_end - start) * p.tile_keys);
     c.tile = seg_end;
-    return u;
+    return u;  // k1 <= k0: none of its tiles
 }
 
-// The sum over the sequences of their units' tiles after `base`; every thread of the block takes
+// The sum over the sequences of their units' places after `base`; every thread of the block takes
 // part.  find >= base: also finds the sequence that holds tile `find`.  cum (or nullptr) receives the
 // running sums.
 __device__ __forceinline__ int64_t scan_sequences(const AttnArgs &a, const AttnPlan &p, int64_t base,
@@ -188,7 +206,7 @@ __device__ __forceinline__ int64_t scan_sequences(const AttnArgs &a, const AttnP
         cum[0] = base;
     for (int64_t b0 = 0; b0 < a.B; b0 += kThreads) {
         const int64_t b = b0 + tid;
-        const int64_t own = b < a.B ? per_seq * seq_tiles(a, p, b) : 0;
+        const int64_t own = b < a.B ? per_seq * seq_places(a, p, b) : 0;
         int64_t v = own;
 #pragma unroll
         for (int off = 1; off < 32; off <<= 1) {
@@ -257,7 +275,7 @@ __global__ void __launch_bounds__(kThreads, 2)
 
     // ---- the share of this block ---------------------------------------------------------------
     const int64_t p_units = a.n_kv * p.p_rtiles;
-    const int64_t p_total = p_units * p.p_tiles;
+    const int64_t p_total = p_units * (p.p_tiles + kUnitCost);
     int64_t *cum = reinterpret_cast<int64_t *>(a.workspace + p.cum_off);
     const int64_t total =
         scan_sequences(a, p, p_total, -1, blockIdx.x == 0 ? cum : nullptr, s_scan);
@@ -280,7 +298,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     Unit lu;
     int ls = 0, lsteps = 0;
     auto steps_of = [&](const Unit &u) {
-        return (u.k1 - u.k0 - warp * C::kKeys + C::kTileKeys - 1) / C::kTileKeys;
+        return (max(u.k1 - u.k0, 0) - warp * C::kKeys + C::kTileKeys - 1) / C::kTileKeys;
     };
     // The slots of a step are loaded two steps before its copies are issued, and only looked at
     // then: a load that is waited for at once held every step up by its latency.
@@ -362,6 +380,8 @@ __global__ void __launch_bounds__(kThreads, 2)
     // ---- the units of the share ----------------------------------------------------------------
     while (at.tile < at.end) {
         const Unit u = next_unit(a, p, M, at);
+        if (u.k1 <= u.k0)
+            continue;
         // query fragments (columns g), and the rows' scale and keys (columns 2t, 2t + 1)
         uint32_t qf[NT][8][2];
         float row_inv[NT];
@@ -417,9 +437,16 @@ __global__ void __launch_bounds__(kThreads, 2)
                 lo[n][e] = 0;
                 hi[n][e] = u.key_end;
                 if (rr < u.row_end) {
-                    int i, hg;
-                    row_token(a, p, rr, i, hg);
-                    const int64_t pos = seq_len(a, rr / p.R) - a.q_len + i;  // in the suffix
+                    int64_t pos;  // in the suffix
+                    if (!u.prefix) {
+                        pos = (int64_t)u.key_end - 1;
+                        if (a.q_len > 1)
+                            pos += (rr - u.row_base) / p.group - (a.q_len - 1);
+                    } else {
+                        int i, hg;
+                        row_token(a, p, rr, i, hg);
+                        pos = seq_len(a, (uint32_t)rr / (uint32_t)p.R) - a.q_len + i;
+                    }
                     const int64_t where = u.prefix ? a.n_prefix + pos : pos;  // in the list
                     lo[n][e] = a.window > 0 && where + 1 - a.window > 0
                                    ? (int)min((int64_t)u.key_end, where + 1 - a.window)
@@ -848,19 +875,20 @@ __global__ void __launch_bounds__(128) attn_join_kernel(const __grid_constant__ 
     const int64_t c0b = cum[b], c1b = cum[b + 1];
     const int64_t per_seq = (int64_t)a.n_kv * p.s_rtiles;
     const int64_t rt = (rr - b * p.R) / M;
-    const int64_t tb = div32(c1b - c0b, per_seq);
+    const int64_t places = div32(c1b - c0b, per_seq), tb = places - kUnitCost;
     // the parts of the prefix unit, then those of the suffix unit, then the tensor-core kernel's
     int64_t first[3] = {0, 0, 0};
     int at[3] = {0, 0, 0}, count[3] = {0, 0, 0};  // row of part c: (first + c) * M + at
     if (p.p_rtiles > 0) {
-        const int64_t unit = kvh * p.p_rtiles + rr / M, s = unit * p.p_tiles;
+        const int64_t unit = kvh * p.p_rtiles + rr / M;
+        const int64_t s = unit * (p.p_tiles + kUnitCost) + kUnitCost;
         const int64_t c0 = owner(s, total, shares);
         first[0] = unit + c0;
         count[0] = (int)(owner(s + p.p_tiles - 1, total, shares) - c0) + 1;
         at[0] = (int)(rr % M);
     }
     if (tb > 0) {
-        const int64_t u = (int64_t)kvh * p.s_rtiles + rt, s = c0b + u * tb;
+        const int64_t u = (int64_t)kvh * p.s_rtiles + rt, s = c0b + u * places + kUnitCost;
         const int64_t c0 = owner(s, total, shares);
         first[1] = a.n_kv * p.p_rtiles + b * per_seq + u + c0;
         count[1] = (int)(owner(s + tb - 1, total, shares) - c0) + 1;
@@ -1066,7 +1094,7 @@ AttnPlan attn_plan(int32_t B, int32_t q_len, int32_t n_q, int32_t n_kv, int64_t 
     int64_t keys = width;
     if (window > 0 && window + q_len - 1 < keys)
         keys = window + q_len - 1 + 15;
-    const int64_t tiles =
+    const int64_t tiles =  // the most there can be
         n_kv * (p.p_rtiles * p.p_tiles +
                 (int64_t)B * p.s_rtiles * ((keys + p.tile_keys - 1) / p.tile_keys));
     const int64_t most = kPlanSms * 2;
