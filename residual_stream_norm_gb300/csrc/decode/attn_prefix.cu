@@ -54,7 +54,7 @@ __device__ unsigned int g_decode_fault_word = 0u;
 // shares are dealt out over the tiles and this, so that a block of many short units has fewer tiles.
 // The first kUnitCost places of a unit's stretch stand for it; a share that ends among them has no
 // tile of the unit.
-constexpr int kUnitCost = 2;
+constexpr int kUnitCost = 3;
 
 // The block whose share [c tot / C, (c + 1) tot / C) contains tile x (C <= tot).
 __device__ __forceinline__ int64_t owner(int64_t x, int64_t tot, int64_t ctas)
@@ -1094,9 +1094,10 @@ AttnPlan attn_plan(int32_t B, int32_t q_len, int32_t n_q, int32_t n_kv, int64_t 
     int64_t keys = width;
     if (window > 0 && window + q_len - 1 < keys)
         keys = window + q_len - 1 + 15;
-    const int64_t tiles =  // the most there can be
-        n_kv * (p.p_rtiles * p.p_tiles +
-                (int64_t)B * p.s_rtiles * ((keys + p.tile_keys - 1) / p.tile_keys));
+    // the most places there can be: no block is worth less than one
+    const int64_t tiles =
+        n_kv * (p.p_rtiles * (p.p_tiles + kUnitCost) +
+                (int64_t)B * p.s_rtiles * ((keys + p.tile_keys - 1) / p.tile_keys + kUnitCost));
     const int64_t most = kPlanSms * 2;
     p.ctas = (int32_t)(tiles < 1 ? 1 : (tiles < most ? tiles : most));
     p.score_width = align_up(width, 8);
