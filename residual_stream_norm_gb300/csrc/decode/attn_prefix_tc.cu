@@ -310,24 +310,38 @@ __global__ void __launch_bounds__(TcConfig<FP8, SPLIT>::kThreads, 1)
                     make_float2(seen ? m : -INFINITY, seen ? l : 0.0f);
         }
     } else if (warp == 8 && !*s_fail) {
-        // ---- the products ------------------------------------------------------------------------
-        if (lane == 0) {
+        // ---- the products: the whole warp waits, one lane issues (descriptors then stay uniform) -------
+        {
+            const bool one = elect_one();
             constexpr uint32_t dqk = mma_desc(FP8, false), dpv = mma_desc(FP8, true);
             const uint32_t kt = base + C::kK, vt = base + C::kV;
-            bool ok = mbar_wait_or_fail(q_full, 0, s_fail);
-            auto wait_k = [&](int i) {
-                ok = ok && mbar_wait_or_fail(&k_full[i & 1], (i >> 1) & 1, s_fail);
+            bool ok = true;
+            auto wait = [&](uint64_t *bar, uint32_t parity) {
+                ok = ok && __all_sync(0xffffffffu, mbar_wait_or_fail(bar, parity, s_fail));
+                return ok;
             };
+            wait(q_full, 0);
+            auto wait_k = [&](int i) { wait(&k_full[i & 1], (i >> 1) & 1); };
             auto qk = [&](int half, int i) {
                 tc_fence_after();
-                scores_product(tmem + half * 128, base + (SPLIT ? 0 : half) * kTile,
-                               kt + (i & 1) * kTile, dqk);
-                tc_commit(&s_full[half]);
+                if (one) {
+                    scores_product(tmem + half * 128, base + (SPLIT ? 0 : half) * kTile,
+                                   kt + (i & 1) * kTile, dqk);
+                    tc_commit(&s_full[half]);
+                }
+                __syncwarp();
             };
             auto pv = [&](int half, int j, int i) {
                 tc_fence_after();
-                values_product(tmem + 256 + half * 128, tmem + half * 128 + 64,
-                               vt + (i & 1) * kTile, dpv, j > 0);
+                if (one)
+                    values_product(tmem + 256 + half * 128, tmem + half * 128 + 64,
+                                   vt + (i & 1) * kTile, dpv, j > 0);
+                __syncwarp();
+            };
+            auto commit = [&](uint64_t *bar) {
+                if (one)
+                    tc_commit(bar);
+                __syncwarp();
             };
             if constexpr (SPLIT) {
                 for (int i = 0; i < 2 && i < N && ok; ++i) {
@@ -335,22 +349,20 @@ __global__ void __launch_bounds__(TcConfig<FP8, SPLIT>::kThreads, 1)
                     if (!ok)
                         break;
                     qk(i, i);
-                    tc_commit(&k_empty[i]);
+                    commit(&k_empty[i]);
                 }
                 for (int i = 0; i < N && ok; ++i) {
                     const int half = i & 1, j = i >> 1;
-                    ok = mbar_wait_or_fail(&v_full[i & 1], (i >> 1) & 1, s_fail) &&
-                         mbar_wait_or_fail(&p_full[half], j & 1, s_fail);
-                    if (!ok)
+                    if (!wait(&v_full[i & 1], (i >> 1) & 1) || !wait(&p_full[half], j & 1))
                         break;
                     pv(half, j, i);
-                    tc_commit(&v_empty[i & 1]);
+                    commit(&v_empty[i & 1]);
                     if (i + 2 < N) {
                         wait_k(i + 2);
                         if (!ok)
                             break;
                         qk(half, i + 2);
-                        tc_commit(&k_empty[i & 1]);
+                        commit(&k_empty[i & 1]);
                     }
                 }
             } else {
@@ -358,18 +370,17 @@ __global__ void __launch_bounds__(TcConfig<FP8, SPLIT>::kThreads, 1)
                 if (ok) {
                     for (int h = 0; h < halves; ++h)
                         qk(h, 0);
-                    tc_commit(&k_empty[0]);
+                    commit(&k_empty[0]);
                 }
                 for (int i = 0; i < N && ok; ++i)
                     for (int h = 0; h < halves && ok; ++h) {
                         if (h == 0)
-                            ok = mbar_wait_or_fail(&v_full[i & 1], (i >> 1) & 1, s_fail);
-                        ok = ok && mbar_wait_or_fail(&p_full[h], i & 1, s_fail);
-                        if (!ok)
+                            wait(&v_full[i & 1], (i >> 1) & 1);
+                        if (!wait(&p_full[h], i & 1))
                             break;
                         pv(h, i, i);
                         if (h == halves - 1)
-                            tc_commit(&v_empty[i & 1]);
+                            commit(&v_empty[i & 1]);
                         if (i + 1 < N) {
                             if (h == 0)
                                 wait_k(i + 1);
@@ -377,12 +388,12 @@ __global__ void __launch_bounds__(TcConfig<FP8, SPLIT>::kThreads, 1)
                                 break;
                             qk(h, i + 1);
                             if (h == halves - 1)
-                                tc_commit(&k_empty[(i + 1) & 1]);
+                                commit(&k_empty[(i + 1) & 1]);
                         }
                     }
             }
             if (ok)
-                tc_commit(o_full);
+                commit(o_full);
         }
         __syncwarp();
     } else if (warp == 9 && !*s_fail) {

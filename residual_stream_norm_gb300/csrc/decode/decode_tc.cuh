@@ -41,6 +41,15 @@ __host__ __device__ constexpr uint32_t mma_desc(bool f16, bool b_rows_k)
            ((b_rows_k ? 1u : 0u) << 16) | ((128u >> 3) << 17) | ((128u >> 4) << 24);
 }
 
+// One lane of a converged warp.
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+                 : "=r"(r));
+    return r != 0;
+}
+
 // D[128 x 128] (+)= A[128 x 16] B[16 x 128]: A from shared memory or from tensor memory.
 __device__ __forceinline__ void tc_mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t desc,
                                           bool add)
