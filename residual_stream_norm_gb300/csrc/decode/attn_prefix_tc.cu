@@ -11,8 +11,9 @@
 // than 2^8: the weights of a part stay below 2^8, which FP32 sums and both 16-bit types hold with
 // the same relative precision, and nearly all tiles then need no scaling.
 //
-// Roles: warps 0-7 softmax; 8 issues the products; 9 copies keys and values (TMA gathers by slot); for
-// an FP8 cache warps 10-13 expand the copied bytes to FP16 (exact) in the layout of the products.
+// Roles: warps 0-7 softmax; 8 issues the products; 9 copies keys and 10 values (TMA, by slot; one warp
+// for both took longer to issue a tile's copies than the products took); for an FP8 cache warps 11-14
+// expand the copied bytes to FP16 (exact) in the layout of the products.
 
 #include "attn_common.cuh"
 #include "beam_f32x2.cuh"
@@ -32,9 +33,10 @@ constexpr float kRaise = 8.0f;
 
 template <bool FP8, bool SPLIT>
 struct TcConfig {
-    static constexpr int kThreads = FP8 ? 448 : 320;
+    static constexpr int kThreads = FP8 ? 480 : 352;
     static constexpr int kQTiles = SPLIT ? 1 : 2;
-    static constexpr int kRaw = FP8 ? (SPLIT ? 4 : 2) : 0;
+    static constexpr int kRaw = FP8 ? (SPLIT ? 4 : 2) : 0;  // half of them keys, half values
+    static constexpr int kRing = kRaw > 0 ? kRaw / 2 : 1;
     static constexpr int kK = kQTiles * kTile;        // two stages
     static constexpr int kV = kK + 2 * kTile;         // two stages
     static constexpr int kRawAt = kV + 2 * kTile;
@@ -396,125 +398,96 @@ __global__ void __launch_bounds__(TcConfig<FP8, SPLIT>::kThreads, 1)
                 commit(o_full);
         }
         __syncwarp();
-    } else if (warp == 9 && !*s_fail) {
-        // ---- copies: K(0), (K(1),) then V(i), K(i + ahead) in turn, as the products take them -------
-        constexpr int ahead = SPLIT ? 2 : 1;
-        int slot[ahead + 2][4];  // this lane's four keys of tiles i, i + 1, ...
-        auto fetch = [&](int i, int64_t (&x)[4]) {
+    } else if ((warp == 9 || warp == 10) && !*s_fail) {
+        // ---- copies: keys (warp 9, with the masks of which exist) or values (warp 10) -----------------
+        const bool v = warp == 10;
+        const CUtensorMap *run = v ? &maps.v_run : &maps.k_run, *four = v ? &maps.v : &maps.k;
+        auto fetch = [&](int i, int64_t (&x)[4]) {  // this lane's four keys of tile i
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 const int64_t key = key0 + (int64_t)i * 128 + 4 * lane + j;
                 x[j] = i < N && key < key_end ? a.prefix[key] : -1;
             }
         };
-        auto check = [&](const int64_t (&x)[4], int (&s)[4]) {
+        bool ok = true;
+        int64_t x[4], ahead[4];
+        fetch(0, x);
+        for (int i = 0; i < N; ++i) {
+            fetch(i + 1, ahead);  // arrives while this tile's copies wait and are issued
+            int s[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j)
                 s[j] = x[j] >= 0 && x[j] < a.num_slots ? (int)x[j] : -1;
-        };
-        // copies a tile of 128-byte rows: runs of 16 slots as one copy, others four by four
-        auto rows = [&](uint32_t dst, const CUtensorMap *run, const CUtensorMap *four, int x,
-                        const int (&s)[4], bool mine, uint64_t *bar) {
+            // runs of 16 slots go as one copy, others four by four
             const int s0 = __shfl_sync(0xffffffffu, s[0], lane & ~3);
             const bool in = s0 >= 0 && s0 + 15 < a.num_slots && s[0] == s0 + 4 * (lane & 3) &&
                             s[1] == s[0] + 1 && s[2] == s[0] + 2 && s[3] == s[0] + 3;
-            const uint32_t all = __ballot_sync(0xffffffffu, in) >> (lane & ~3);
-            if ((all & 15u) == 15u) {
-                if (mine)
-                    copy_run(dst + (lane >> 2) * 2048, run, x, s0, bar);
-            } else {
-                gather4(dst + lane * 512, four, x, s[0], s[1], s[2], s[3], bar);
-            }
-        };
-        int raw = 0;  // FP8: copies so far
-        bool ok = true;
-        auto copy = [&](bool v, int i, const int (&s)[4]) {
+            const bool whole =
+                ((__ballot_sync(0xffffffffu, in) >> (lane & ~3)) & 15u) == 15u;
+            uint64_t *full, *empty;
+            uint32_t dst, parity;
             if constexpr (FP8) {
-                const int st = raw % C::kRaw;
-                ok = ok && mbar_wait_or_fail(&r_empty[st], ((raw / C::kRaw) & 1) ^ 1, s_fail);
-                ok = __all_sync(0xffffffffu, ok);
-                if (!ok)
-                    return;
-                if (lane == 0)
-                    mbar_arrive_expect_tx(&r_full[st], kRawTile);
-                __syncwarp();
-                rows(base + C::kRawAt + st * kRawTile, v ? &maps.v_run : &maps.k_run,
-                     v ? &maps.v : &maps.k, kvh * kD, s, (lane & 3) == 0, &r_full[st]);
-                ++raw;
+                const int st = i % C::kRing;
+                full = &r_full[2 * v + st];
+                empty = &r_empty[2 * v + st];
+                parity = ((i / C::kRing) & 1) ^ 1;
+                dst = base + C::kRawAt + (v * C::kRing + st) * kRawTile;
             } else {
-                uint64_t *full = v ? &v_full[i & 1] : &k_full[i & 1];
-                ok = ok && mbar_wait_or_fail(v ? &v_empty[i & 1] : &k_empty[i & 1],
-                                             ((i >> 1) & 1) ^ 1, s_fail);
-                ok = __all_sync(0xffffffffu, ok);
-                if (!ok)
-                    return;
-                if (lane == 0)
-                    mbar_arrive_expect_tx(full, kTile);
-                __syncwarp();
-                const uint32_t dst = base + (v ? C::kV : C::kK) + (i & 1) * kTile;
-#pragma unroll
-                for (int h = 0; h < 2; ++h)
-                    rows(dst + h * kHalfTile, v ? &maps.v_run : &maps.k_run,
-                         v ? &maps.v : &maps.k, kvh * kD + 64 * h, s, (lane & 3) == h, full);
+                full = v ? &v_full[i & 1] : &k_full[i & 1];
+                empty = v ? &v_empty[i & 1] : &k_empty[i & 1];
+                parity = ((i >> 1) & 1) ^ 1;
+                dst = base + (v ? C::kV : C::kK) + (i & 1) * kTile;
             }
-        };
-        auto copy_k = [&](int i, const int (&s)[4]) {
-            if (i >= N)
-                return;
-            copy(false, i, s);
-            // The tile's mask.  Its place was last used by tile i - 8: this copy waited for the scores
-            // of tile i - 4 or a later one to be complete, so the softmax warps have left tile i - 6.
-            uint32_t bits = 0;
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-                bits |= s[j] >= 0 ? 1u << (4 * (lane & 7) + j) : 0u;
-            bits |= __shfl_xor_sync(0xffffffffu, bits, 1);
-            bits |= __shfl_xor_sync(0xffffffffu, bits, 2);
-            bits |= __shfl_xor_sync(0xffffffffu, bits, 4);
+            ok = __all_sync(0xffffffffu, mbar_wait_or_fail(empty, parity, s_fail));
             if (!ok)
-                return;
-            if ((lane & 7) == 0)
-                s_mask[4 * (i & 7) + (lane >> 3)] = bits;
-            __syncwarp();
+                break;
             if (lane == 0)
-                mbar_arrive(&m_full[i & 7]);
-        };
-        int64_t x[4];
-#pragma unroll
-        for (int i = 0; i <= ahead; ++i) {
-            fetch(i, x);
-            check(x, slot[i]);
-        }
-#pragma unroll
-        for (int i = 0; i < ahead; ++i)
-            if (ok)
-                copy_k(i, slot[i]);
-        for (int i = 0; i < N && ok; ++i) {
-            fetch(i + ahead + 1, x);  // arrives while the copies are issued
-            copy(true, i, slot[0]);
-            if (ok)
-                copy_k(i + ahead, slot[ahead]);
-            check(x, slot[ahead + 1]);
-#pragma unroll
-            for (int k = 0; k <= ahead; ++k)
+                mbar_arrive_expect_tx(full, FP8 ? kRawTile : kTile);
+            __syncwarp();
+            if (whole) {
+                // a lane of each four for each half of the head
+                if ((lane & 3) < (FP8 ? 1 : 2))
+                    copy_run(dst + (lane & 3) * kHalfTile + (lane >> 2) * 2048, run,
+                             kvh * kD + 64 * (lane & 3), s0, full);
+            } else {
+                gather4(dst + lane * 512, four, kvh * kD, s[0], s[1], s[2], s[3], full);
+                if (!FP8)
+                    gather4(dst + kHalfTile + lane * 512, four, kvh * kD + 64, s[0], s[1], s[2],
+                            s[3], full);
+            }
+            if (!v) {
+                // The tile's mask.  Its place was last used by tile i - 8: this copy waited for the
+                // scores of tile i - 4 or a later one, so the softmax warps have left tile i - 6.
+                uint32_t bits = 0;
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
-                    slot[k][j] = slot[k + 1][j];
+                    bits |= s[j] >= 0 ? 1u << (4 * (lane & 7) + j) : 0u;
+                bits |= __shfl_xor_sync(0xffffffffu, bits, 1);
+                bits |= __shfl_xor_sync(0xffffffffu, bits, 2);
+                bits |= __shfl_xor_sync(0xffffffffu, bits, 4);
+                if ((lane & 7) == 0)
+                    s_mask[4 * (i & 7) + (lane >> 3)] = bits;
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(&m_full[i & 7]);
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                x[j] = ahead[j];
         }
-    } else if (FP8 && warp >= 10 && !*s_fail) {
-        // ---- FP8 to FP16, tile by tile in the copies' order ---------------------------------------
+    } else if (FP8 && warp >= 11 && !*s_fail) {
+        // ---- FP8 to FP16, in the products' order ----------------------------------------------------
         constexpr int ahead = SPLIT ? 2 : 1;
-        const int ct = tid - 320;
-        int raw = 0;
+        const int ct = tid - 352;
         bool ok = true;
         auto expand = [&](bool v, int i) {
-            const int st = raw % (C::kRaw > 0 ? C::kRaw : 1);
-            ok = ok && mbar_wait_or_fail(&r_full[st], (raw / (C::kRaw > 0 ? C::kRaw : 1)) & 1, s_fail) &&
+            const int st = i % C::kRing;
+            ok = ok && mbar_wait_or_fail(&r_full[2 * v + st], (i / C::kRing) & 1, s_fail) &&
                  mbar_wait_or_fail(v ? &v_empty[i & 1] : &k_empty[i & 1], ((i >> 1) & 1) ^ 1, s_fail);
             ok = __all_sync(0xffffffffu, ok);
             if (!ok)
                 return;
-            const uint32_t src = base + C::kRawAt + st * kRawTile;
+            const uint32_t src = base + C::kRawAt + (v * C::kRing + st) * kRawTile;
             const uint32_t dst = base + (v ? C::kV : C::kK) + (i & 1) * kTile;
 #pragma unroll 4
             for (int x = 0; x < 8; ++x) {
@@ -532,8 +505,7 @@ __global__ void __launch_bounds__(TcConfig<FP8, SPLIT>::kThreads, 1)
             }
             fence_async_shared();
             mbar_arrive(v ? &v_full[i & 1] : &k_full[i & 1]);
-            mbar_arrive(&r_empty[st]);
-            ++raw;
+            mbar_arrive(&r_empty[2 * v + st]);
         };
         for (int i = 0; i < ahead && i < N && ok; ++i)
             expand(false, i);

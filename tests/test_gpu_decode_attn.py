@@ -14,14 +14,19 @@ pytestmark = pytest.mark.gpu
 D = 128
 
 
-def make(B, q_len, n_q, n_kv, P, N, lens, fp8=False, seed=0, extra=7, q_pad=0, spread=1.0):
-    """A case on the CPU: caches with distinct random slots, NaN in every slot that is not listed."""
+def make(B, q_len, n_q, n_kv, P, N, lens, fp8=False, seed=0, extra=7, q_pad=0, spread=1.0,
+         page=0):
+    """A case on the CPU: caches with distinct random slots (or pages of `page` consecutive ones), NaN in
+    every slot that is not listed."""
     g = torch.Generator().manual_seed(seed)
     lens = [int(n) for n in lens]
     inside = [min(max(n, 0), N) for n in lens]
     total = P + sum(inside)
     S = total + extra
     perm = torch.randperm(S, generator=g)
+    if page:
+        S = -(-S // page) * page
+        perm = (torch.randperm(S // page, generator=g)[:, None] * page + torch.arange(page)).view(-1)
     prefix = perm[:P].clone()
     table = torch.full((B, N), -1, dtype=torch.int64)
     at = P
@@ -122,6 +127,18 @@ def test_sizes(case, fp8):
     lib()
     B, q_len, n_q, n_kv, P, N, lens = case
     check(make(B, q_len, n_q, n_kv, P, N, lens, fp8=fp8, seed=B + N), weights=N > 0)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("page", [1, 8, 16, 24, 64, 10 ** 4])
+def test_pages(page, fp8):
+    # slots in runs of all lengths, which start and end inside the tiles; few and many prefix rows
+    lib()
+    check(make(3, 2, 12, 2, 300, 150, [150, 61, 16], fp8=fp8, seed=page, page=page), weights=True)
+    check(make(3, 2, 6, 1, 300, 150, [150, 61, 16], fp8=fp8, seed=page, page=page), window=70)
+    check(make(40, 1, 6, 1, 1000, 33, [1 + b % 33 for b in range(40)], fp8=fp8, seed=page,
+               page=page))
+    check(make(25, 1, 6, 1, 520, 9, [9] * 25, fp8=fp8, seed=page, page=page))
 
 
 @pytest.mark.parametrize("window", [1, 2, 16, 63, 64, 65, 200, 10 ** 12])
