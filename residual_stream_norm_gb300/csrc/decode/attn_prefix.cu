@@ -36,13 +36,11 @@ struct RowsConfig {
     static constexpr int kWarpBytes = kStages * kStageBytes;
 };
 
-// Shared memory of the rows kernel: the stages, two join buffers, then the small arrays.
-template <int NT>
+// Shared memory of the rows kernel: the stages, the join's buffer, then the small arrays.
 struct RowsSmem {
     static constexpr int kStagesEnd = kWarps * RowsConfig<false>::kWarpBytes;
-    static constexpr int kJoinBytes = 8 * NT * kD * 4;
-    static constexpr int kMl = kStagesEnd + 2 * kJoinBytes;          // float2 [kWarps][8 NT]
-    static constexpr int kBars = kMl + kWarps * 8 * NT * 8;          // uint64_t [kWarps][kStages]
+    static constexpr int kMl = kStagesEnd + kWarps * 8 * kD * 4;     // float2 [kWarps][8]
+    static constexpr int kBars = kMl + kWarps * 8 * 8;               // uint64_t [kWarps][kStages]
     static constexpr int kScan = kBars + kWarps * RowsConfig<false>::kStages * 8;  // int64_t [kWarps + 2]
     static constexpr int kFail = kScan + (kWarps + 2) * 8;           // int
     static constexpr int kBytes = kFail + 8;
@@ -129,10 +127,14 @@ __device__ __forceinline__ int64_t seq_places(const AttnArgs &a, const AttnPlan 
     return t > 0 ? t + kUnitCost : 0;
 }
 
-// Position in the units' sequence of places.
+// A place in the units' sequence, and the unit that holds it: from unit to unit it only counts on.
 struct Cursor {
-    int64_t tile, end;    // the next tile of the share, and the share's end
-    int64_t b, b_start;   // sequence of `tile` (past the prefix), its first tile
+    int64_t tile, end;    // the next place of the share, and the share's end
+    int64_t start;        // the unit's first place
+    int64_t unit, rt;     // the unit, and its tile of rows
+    int32_t places;       // of the unit
+    int32_t b, kvh;       // sequence (b < 0: the prefix) and KV head
+    int32_t key_first, key_end;
 };
 
 // A unit's part that lies in the share.
@@ -142,55 +144,78 @@ struct Unit {
     int32_t kvh;
     int32_t row0, row_end;
     int32_t row_base;     // the sequence's first row (suffix)
-    int32_t k0, k1;       // keys of the part
+    int32_t k0, k1;       // keys of the part; k1 <= k0: none
     int32_t key_end;      // of the list
     bool prefix, whole;
 };
 
+__device__ __forceinline__ void cursor_keys(const AttnArgs &a, const AttnPlan &p, Cursor &c)
+{
+    if (c.b < 0) {
+        c.key_first = (int32_t)p.p_first;
+        c.key_end = (int32_t)a.n_prefix;
+        c.places = (int32_t)p.p_tiles + kUnitCost;
+    } else {
+        c.key_end = (int32_t)seq_len(a, c.b);
+        c.key_first = (int32_t)first_tile_key(c.key_end, a.q_len, a.window);
+        c.places = (int32_t)seq_places(a, p, c.b);
+    }
+}
+
+// The cursor of a share that starts at place `tile`: sequence b (its first place b_start) holds it, or
+// the prefix (b < 0, b_start 0).
+__device__ __forceinline__ Cursor first_cursor(const AttnArgs &a, const AttnPlan &p, int64_t tile,
+                                               int64_t end, int64_t b, int64_t b_start)
+{
+    Cursor c;
+    c.tile = tile;
+    c.end = end;
+    c.b = (int32_t)b;
+    cursor_keys(a, p, c);
+    const int64_t rtiles = b < 0 ? p.p_rtiles : p.s_rtiles;
+    const int64_t x = div32(tile - b_start, c.places);
+    c.start = b_start + x * c.places;
+    c.kvh = (int32_t)div32(x, rtiles);
+    c.rt = x - c.kvh * rtiles;
+    c.unit = x + (b < 0 ? 0 : a.n_kv * (p.p_rtiles + b * p.s_rtiles));
+    return c;
+}
+
 __device__ __forceinline__ Unit next_unit(const AttnArgs &a, const AttnPlan &p, int M, Cursor &c)
 {
-    Unit u;
-    const int64_t p_units = a.n_kv * p.p_rtiles, p_places = p.p_tiles + kUnitCost;
-    const int64_t p_total = p_units * p_places;
-    const int64_t per_seq = (int64_t)a.n_kv * p.s_rtiles;
-    int64_t start, tiles;
-    int32_t key_first;
-    u.prefix = c.tile < p_total;
-    if (u.prefix) {
-        u.unit = div32(c.tile, p_places);
-        tiles = p.p_tiles;
-        start = u.unit * p_places + kUnitCost;
-        u.kvh = (int32_t)div32(u.unit, p.p_rtiles);
-        u.row0 = (int32_t)(u.unit - u.kvh * p.p_rtiles) * M;
-        u.row_end = (int32_t)p.rows;
-        u.row_base = 0;
-        u.list = a.prefix;
-        key_first = (int32_t)p.p_first;
-        u.key_end = (int32_t)a.n_prefix;
-    } else {
-        int64_t places = seq_places(a, p, c.b);
-        while (c.tile >= c.b_start + per_seq * places) {
-            c.b_start += per_seq * places;
-            places = seq_places(a, p, ++c.b);
+    if (c.tile >= c.start + c.places) {  // on to the unit that follows
+        c.start += c.places;
+        ++c.unit;
+        if (++c.rt == (c.b < 0 ? p.p_rtiles : p.s_rtiles)) {
+            c.rt = 0;
+            if (++c.kvh == a.n_kv) {
+                c.kvh = 0;
+                c.b = c.b < 0 ? 0 : c.b + 1;
+                cursor_keys(a, p, c);
+                while (c.places == 0) {  // sequences without a key have no places
+                    c.unit += (int64_t)a.n_kv * p.s_rtiles;
+                    ++c.b;
+                    cursor_keys(a, p, c);
+                }
+            }
         }
-        const int64_t x = div32(c.tile - c.b_start, places);
-        tiles = places - kUnitCost;
-        u.unit = p_units + c.b * per_seq + x;
-        start = c.b_start + x * places + kUnitCost;
-        u.kvh = (int32_t)div32(x, p.s_rtiles);
-        u.row0 = (int32_t)(c.b * p.R + (x - (int64_t)u.kvh * p.s_rtiles) * M);
-        u.row_end = (int32_t)((c.b + 1) * p.R);
-        u.row_base = u.row_end - p.R;
-        u.list = a.table + c.b * a.table_stride;
-        u.key_end = (int32_t)seq_len(a, c.b);
-        key_first = (int32_t)first_tile_key(u.key_end, a.q_len, a.window);
     }
-    const int64_t seg_end = min(c.end, start + tiles), first = max(c.tile, start);
-    u.whole = first == start && seg_end == start + tiles;
-    u.k0 = key_first + (int32_t)(first - start) * p.tile_keys;
-    u.k1 = (int32_t)min((int64_t)u.key_end, key_first + (seg_end - start) * p.tile_keys);
+    Unit u;
+    u.prefix = c.b < 0;
+    u.unit = c.unit;
+    u.kvh = c.kvh;
+    u.key_end = c.key_end;
+    u.row_base = u.prefix ? 0 : c.b * p.R;
+    u.row0 = u.row_base + (int32_t)c.rt * M;
+    u.row_end = u.prefix ? (int32_t)p.rows : u.row_base + p.R;
+    u.list = u.prefix ? a.prefix : a.table + c.b * a.table_stride;
+    const int64_t start = c.start + kUnitCost, stop = c.start + c.places;
+    const int64_t seg_end = min(c.end, stop), first = max(c.tile, start);
+    u.whole = first == start && seg_end == stop;
+    u.k0 = c.key_first + (int32_t)(first - start) * p.tile_keys;
+    u.k1 = (int32_t)min((int64_t)u.key_end, c.key_first + (seg_end - start) * p.tile_keys);
     c.tile = seg_end;
-    return u;  // k1 <= k0: none of its tiles
+    return u;
 }
 
 // The sum over the sequences of their units' places after `base`; every thread of the block takes
@@ -244,7 +269,7 @@ __global__ void __launch_bounds__(kThreads, 2)
                      const __grid_constant__ CacheMaps maps)
 {
     using C = RowsConfig<FP8>;
-    using S = RowsSmem<NT>;
+    using S = RowsSmem;
     constexpr int M = 8 * NT, MT = C::kMt;
     extern __shared__ __align__(1024) char smem[];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -286,12 +311,14 @@ __global__ void __launch_bounds__(kThreads, 2)
             pdl_wait();
         return;
     }
-    Cursor at{div32(total * blockIdx.x, shares), div32(total * (blockIdx.x + 1), shares), 0, p_total};
-    if (at.tile >= p_total) {
-        scan_sequences(a, p, p_total, at.tile, nullptr, s_scan);
-        at.b = s_scan[kWarps];
-        at.b_start = s_scan[kWarps + 1];
+    const int64_t tile0 = div32(total * blockIdx.x, shares);
+    int64_t b0 = -1, b0_start = 0;
+    if (tile0 >= p_total) {
+        scan_sequences(a, p, p_total, tile0, nullptr, s_scan);
+        b0 = s_scan[kWarps];
+        b0_start = s_scan[kWarps + 1];
     }
+    Cursor at = first_cursor(a, p, tile0, div32(total * (blockIdx.x + 1), shares), b0, b0_start);
 
     // ---- the copies: this warp's steps of every unit of the share, ahead of the arithmetic -----------
     Cursor ahead = at;
@@ -691,150 +718,138 @@ __global__ void __launch_bounds__(kThreads, 2)
             }
         }
 
-        // ---- join the warps: 2 into 0 and 3 into 1, then 1 into 0 ------------------------------------
-        __syncthreads();  // the last unit's join has been read
+        // ---- join the warps: each adds up a quarter of the head's elements for all four ------------------
+        const bool direct = u.whole && !u.prefix && p_units == 0 && p.tc_parts == 0;
+        const int64_t part = u.unit + blockIdx.x;
+        float4 *buf = reinterpret_cast<float4 *>(smem + S::kStagesEnd);  // [warp][mt][lane]
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
+        for (int n = 0; n < NT; ++n) {
+            __syncthreads();  // the last join has been read
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 float v = l[n][e];
                 v = __fadd_rn(v, __shfl_xor_sync(0xffffffffu, v, 4));
                 v = __fadd_rn(v, __shfl_xor_sync(0xffffffffu, v, 8));
-                l[n][e] = __fadd_rn(v, __shfl_xor_sync(0xffffffffu, v, 16));
+                v = __fadd_rn(v, __shfl_xor_sync(0xffffffffu, v, 16));
                 if (g == 0)
-                    s_ml[warp * M + 8 * n + 2 * t + e] = make_float2(m[n][e], l[n][e]);
+                    s_ml[warp * 8 + 2 * t + e] = make_float2(m[n][e], v);
             }
-        float *buf = reinterpret_cast<float *>(smem + S::kStagesEnd) + (warp & 1) * M * kD + lane;
-        auto put = [&]() {
 #pragma unroll
             for (int mt = 0; mt < 8; ++mt)
+                buf[(warp * 8 + mt) * 32 + lane] =
+                    make_float4(o[mt][n][0], o[mt][n][1], o[mt][n][2], o[mt][n][3]);
+            __syncthreads();
+            if (*s_fail)  // after a wait that ran out nothing more is written
+                continue;
+            float mm[2], ll[2], f[kWarps][2];
 #pragma unroll
-                for (int n = 0; n < NT; ++n)
+            for (int e = 0; e < 2; ++e) {
+                float2 x[kWarps];
+                mm[e] = -INFINITY;
 #pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        buf[((mt * NT + n) * 4 + e) * 32] = o[mt][n][e];
-        };
-        auto add = [&](int from) {
-#pragma unroll
-            for (int n = 0; n < NT; ++n)
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const float2 x = s_ml[from * M + 8 * n + 2 * t + e];
-                    const float mn = fmaxf(m[n][e], x.x);
-                    const float ms = mn == -INFINITY ? 0.0f : mn;
-                    const float f0 = exp2_fast(__fsub_rn(m[n][e], ms));
-                    const float f1 = exp2_fast(__fsub_rn(x.x, ms));
-                    m[n][e] = mn;
-                    l[n][e] = __fmaf_rn(f1, x.y, __fmul_rn(f0, l[n][e]));
-#pragma unroll
-                    for (int mt = 0; mt < 8; ++mt)
-#pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            float &v = o[mt][n][e + 2 * h];
-                            v = __fmaf_rn(f1, buf[((mt * NT + n) * 4 + e + 2 * h) * 32],
-                                          __fmul_rn(f0, v));
-                        }
+                for (int w = 0; w < kWarps; ++w) {
+                    x[w] = s_ml[w * 8 + 2 * t + e];
+                    mm[e] = fmaxf(mm[e], x[w].x);
                 }
-        };
-        if (warp >= 2)
-            put();
-        __syncthreads();
-        if (warp < 2)
-            add(warp + 2);
-        if (warp == 1) {
-            put();
+                const float ms = mm[e] == -INFINITY ? 0.0f : mm[e];
+                ll[e] = 0.0f;
 #pragma unroll
-            for (int n = 0; n < NT; ++n)
+                for (int w = 0; w < kWarps; ++w) {
+                    f[w][e] = exp2_fast(__fsub_rn(x[w].x, ms));
+                    ll[e] = __fmaf_rn(f[w][e], x[w].y, ll[e]);
+                }
+            }
+            float v[2][4];  // this warp's two tiles of 16 elements
 #pragma unroll
-                for (int e = 0; e < 2; ++e)
-                    if (g == 0)
-                        s_ml[M + 8 * n + 2 * t + e] = make_float2(m[n][e], l[n][e]);
-        }
-        __syncthreads();
-        if (warp > 0 || *s_fail)  // after a wait that ran out nothing more is written
-            continue;
-        buf += M * kD;  // warp 1's
-        add(1);
-        const bool direct = u.whole && !u.prefix && p_units == 0 && p.tc_parts == 0;
-        const int64_t part = u.unit + blockIdx.x;
+            for (int h = 0; h < 2; ++h) {
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
+                for (int e = 0; e < 4; ++e)
+                    v[h][e] = 0.0f;
+#pragma unroll
+                for (int w = 0; w < kWarps; ++w) {
+                    const float4 x = buf[(w * 8 + 2 * warp + h) * 32 + lane];
+                    v[h][0] = __fmaf_rn(f[w][0], x.x, v[h][0]);
+                    v[h][1] = __fmaf_rn(f[w][1], x.y, v[h][1]);
+                    v[h][2] = __fmaf_rn(f[w][0], x.z, v[h][2]);
+                    v[h][3] = __fmaf_rn(f[w][1], x.w, v[h][3]);
+                }
+            }
+            const int r0 = 8 * n + 2 * t;  // this lane's rows: r0, r0 + 1
             if (direct) {
-                float f[2];
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    const float ll = l[n][e];
-                    const int rr = u.row0 + 8 * n + 2 * t + e;
-                    f[e] = ll == 0.0f ? 0.0f : __fdiv_rn(a.v_scale, ll);
-                    if (g == 0 && rr < u.row_end) {
+                    const int rr = u.row0 + r0 + e;
+                    const float c = ll[e] == 0.0f ? 0.0f : __fdiv_rn(a.v_scale, ll[e]);
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        v[h][e] = ll[e] == 0.0f ? 0.0f : __fmul_rn(v[h][e], c);
+                        v[h][e + 2] = ll[e] == 0.0f ? 0.0f : __fmul_rn(v[h][e + 2], c);
+                    }
+                    if (warp == 0 && g == 0 && rr < u.row_end) {
                         int i, hg;
                         const int64_t tok = row_token(a, p, rr, i, hg);
                         if (a.lse)
                             a.lse[tok * a.n_q + u.kvh * p.group + hg] =
-                                ll == 0.0f ? -INFINITY : __fmaf_rn(m[n][e], kLn2, logf(ll));
+                                ll[e] == 0.0f ? -INFINITY : __fmaf_rn(mm[e], kLn2, logf(ll[e]));
                         if (WEIGHTS)
                             reinterpret_cast<float *>(a.workspace +
                                                       p.lse_off)[u.kvh * p.rows + rr] =
-                                ll == 0.0f ? -INFINITY : __fadd_rn(m[n][e], log2f(ll));
+                                ll[e] == 0.0f ? -INFINITY : __fadd_rn(mm[e], log2f(ll[e]));
                     }
                 }
-                // FP8: a lane holds d = 16 mt + 2g, + 1 of rows 2t and 2t + 1; BF16: d = 16 mt + g and
-                // + 8, so that the lanes of an even and an odd g exchange one row each
+                // FP8: a lane holds d = 16 mt + 2g, + 1 of both rows; BF16: d = 16 mt + g and + 8, so the
+                // lanes of an even and an odd g exchange a row each
                 const int own = FP8 ? 0 : g & 1;
-                const int rr = u.row0 + 8 * n + 2 * t + own;
-                int i = 0, hg = 0, i1 = 0, hg1 = 0;
+                const int rr = u.row0 + r0 + own;
                 const bool in0 = rr < u.row_end, in1 = FP8 && rr + 1 < u.row_end;
+                int i = 0, hg = 0, hg1 = 0;
                 const int64_t tok = in0 ? row_token(a, p, rr, i, hg) : 0;
-                const int64_t tok1 = in1 ? row_token(a, p, rr + 1, i1, hg1) : 0;
-                char *dst = (char *)a.out +
+                const int64_t tok1 = in1 ? row_token(a, p, rr + 1, i, hg1) : 0;
+                char *dst = (char *)a.out + 64 * warp +
                             2 * (tok * a.out_stride + (int64_t)(u.kvh * p.group + hg) * kD);
-                char *dst1 = (char *)a.out +
+                char *dst1 = (char *)a.out + 64 * warp +
                              2 * (tok1 * a.out_stride + (int64_t)(u.kvh * p.group + hg1) * kD);
 #pragma unroll
-                for (int mt = 0; mt < 8; ++mt) {
-                    float v[4];
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        v[e] = l[n][e & 1] == 0.0f ? 0.0f : __fmul_rn(o[mt][n][e], f[e & 1]);
+                for (int h = 0; h < 2; ++h) {
                     if constexpr (FP8) {
                         if (in0)
-                            *reinterpret_cast<uint32_t *>(dst + 32 * mt + 4 * g) =
-                                pack_bf16x2(v[0], v[2]);
+                            *reinterpret_cast<uint32_t *>(dst + 32 * h + 4 * g) =
+                                pack_bf16x2(v[h][0], v[h][2]);
                         if (in1)
-                            *reinterpret_cast<uint32_t *>(dst1 + 32 * mt + 4 * g) =
-                                pack_bf16x2(v[1], v[3]);
+                            *reinterpret_cast<uint32_t *>(dst1 + 32 * h + 4 * g) =
+                                pack_bf16x2(v[h][1], v[h][3]);
                     } else {
 #pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            const float give = own ? v[2 * h] : v[2 * h + 1];
+                        for (int k = 0; k < 2; ++k) {
+                            const float give = own ? v[h][2 * k] : v[h][2 * k + 1];
                             const float got = __shfl_xor_sync(0xffffffffu, give, 4);
-                            const uint32_t w = own ? pack_bf16x2(got, v[2 * h + 1])
-                                                   : pack_bf16x2(v[2 * h], got);
+                            const uint32_t w = own ? pack_bf16x2(got, v[h][2 * k + 1])
+                                                   : pack_bf16x2(v[h][2 * k], got);
                             if (in0)
-                                *reinterpret_cast<uint32_t *>(dst + 32 * mt + 16 * h +
+                                *reinterpret_cast<uint32_t *>(dst + 32 * h + 16 * k +
                                                               2 * (g & ~1)) = w;
                         }
                     }
                 }
             } else {
-                float *po = reinterpret_cast<float *>(a.workspace + p.o_off);
-                float2 *pm = reinterpret_cast<float2 *>(a.workspace + p.ml_off);
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    const int r = 8 * n + 2 * t + e;
+                    const int r = r0 + e;
                     if (u.row0 + r >= u.row_end)
                         continue;
-                    if (g == 0)
-                        pm[part * M + r] = make_float2(m[n][e], l[n][e]);
-                    float *dst = po + (part * M + r) * kD;
+                    if (warp == 0 && g == 0)
+                        reinterpret_cast<float2 *>(a.workspace + p.ml_off)[part * M + r] =
+                            make_float2(mm[e], ll[e]);
+                    float *dst = reinterpret_cast<float *>(a.workspace + p.o_off) +
+                                 (part * M + r) * kD + 32 * warp;
 #pragma unroll
-                    for (int mt = 0; mt < 8; ++mt) {
+                    for (int h = 0; h < 2; ++h) {
                         if constexpr (FP8) {
-                            *reinterpret_cast<float2 *>(dst + 16 * mt + 2 * g) =
-                                make_float2(o[mt][n][e], o[mt][n][e + 2]);
+                            *reinterpret_cast<float2 *>(dst + 16 * h + 2 * g) =
+                                make_float2(v[h][e], v[h][e + 2]);
                         } else {
-                            dst[16 * mt + g] = o[mt][n][e];
-                            dst[16 * mt + g + 8] = o[mt][n][e + 2];
+                            dst[16 * h + g] = v[h][e];
+                            dst[16 * h + g + 8] = v[h][e + 2];
                         }
                     }
                 }
@@ -1020,7 +1035,7 @@ template <int NT, bool FP8, bool WEIGHTS>
 cudaError_t launch_rows(const AttnArgs &a, const AttnPlan &p, const CacheMaps &maps,
                         cudaStream_t stream)
 {
-    constexpr int bytes = RowsSmem<NT>::kBytes;
+    constexpr int bytes = RowsSmem::kBytes;
     const cudaError_t e = allow_smem<attn_rows_kernel<NT, FP8, WEIGHTS>>(bytes);
     if (e != cudaSuccess)
         return e;
