@@ -1062,11 +1062,11 @@ constexpr int64_t kTcRows = 33, kTcKeys = 256;
 // Divides the prefix among the tensor-core kernel's blocks: tiles of 256 rows, or, up to 128 rows, of
 // 128 rows with every other key tile to each half of the block.  The number of parts is the one
 // that fills the SMs best; a part costs about three key tiles besides its own.
-void plan_tc(AttnPlan &p, int32_t n_kv, int64_t n_prefix)
+void plan_tc(AttnPlan &p, int32_t n_kv, int64_t keys)
 {
     p.tc_split = p.rows <= 128;
     p.tc_rtiles = (int32_t)((p.rows + 255) / 256);
-    const int64_t tiles = (n_prefix + 127) / 128;           // key tiles
+    const int64_t tiles = (keys + 127) / 128;               // key tiles
     const int64_t most = p.tc_split ? (tiles + 1) / 2 : tiles;  // steps of a block
     const int64_t units = (int64_t)p.tc_rtiles * n_kv;
     int64_t best = INT64_MAX;
@@ -1097,8 +1097,8 @@ AttnPlan attn_plan(int32_t B, int32_t q_len, int32_t n_q, int32_t n_kv, int64_t 
     p.p_first = window > 0 && n_prefix + 1 > window ? n_prefix + 1 - window : 0;
     p.p_first = (p.p_first < n_prefix ? p.p_first : n_prefix) & ~(int64_t)15;
     const int64_t p_keys = n_prefix - p.p_first;
-    if (tc && window == 0 && p.rows >= kTcRows && n_prefix >= kTcKeys)
-        plan_tc(p, n_kv, n_prefix);
+    if (tc && p.rows >= kTcRows && p_keys >= kTcKeys)
+        plan_tc(p, n_kv, p_keys);
     const bool with_prefix = p_keys > 0 && p.tc_parts == 0;
     p.nt = (p.R > 8 || (with_prefix && p.rows > 8)) ? 2 : 1;
     const int M = 8 * p.nt;

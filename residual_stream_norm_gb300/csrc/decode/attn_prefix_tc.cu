@@ -11,6 +11,11 @@
 // than 2^8: the weights of a part stay below 2^8, which FP32 sums and both 16-bit types hold with
 // the same relative precision, and nearly all tiles then need no scaling.
 //
+// A window cuts the prefix row by row.  A weight of zero does not hide an infinite or NaN value from the
+// matrix product, so where some row does not see a key of a tile the softmax warps first look the
+// tile's values over, and put zeros in the place of such values; the rows that do see them get them
+// back at the end.
+//
 // Roles: warps 0-7 softmax; 8 issues the products; 9 copies keys and 10 values (TMA, by slot; one warp
 // for both took longer to issue a tile's copies than the products took); for an FP8 cache warps 11-14
 // expand the copied bytes to FP16 (exact) in the layout of the products.
@@ -44,7 +49,7 @@ struct TcConfig {
     static constexpr int kBars = kMask + 128;
     static constexpr int kNumBars = 1 + 8 + 8 + 2 + 2 + 1 + 8;
     static constexpr int kMisc = kBars + 8 * kNumBars;      // tensor memory address, fail
-    static constexpr int kBytes = kMisc + 16;
+    static constexpr int kBytes = kMisc + 16;                // + largest first key, values left out
     static_assert(kBytes <= 232448, "shared memory of a block");
 };
 
@@ -74,6 +79,56 @@ __device__ __forceinline__ void load64(uint32_t addr, float (&r)[64])
         : "memory");
 }
 
+// Puts zeros in the place of the infinite and NaN values of a tile; 128 threads.  Whether this thread
+// found one.
+template <bool F16>
+__device__ __forceinline__ bool leave_out(uint32_t tile, int t)
+{
+    constexpr uint32_t kExp = F16 ? 0x7c007c00u : 0x7f807f80u;
+    bool found = false;
+#pragma unroll 4
+    for (int i = 0; i < kTile / 16 / 128; ++i) {
+        const uint32_t at = tile + (i * 128 + t) * 16;
+        uint4 v = lds128(at);
+        uint32_t bad = 0;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const uint32_t x = __vcmpeq2(word(v, k) & kExp, kExp);
+            word(v, k) &= ~x;
+            bad |= x;
+        }
+        if (bad) {
+            sts128(at, v);
+            found = true;
+        }
+    }
+    return found;
+}
+
+// Adds to 64 elements (from d0 on) of a row's sum the infinite and NaN values of the keys it sees.
+template <bool FP8>
+__device__ __noinline__ void put_back(const AttnArgs &a, float (&o)[64], int kvh, int d0,
+                                      int64_t key, int64_t key_end)
+{
+    for (; key < key_end; ++key) {
+        const int64_t slot = a.prefix[key];
+        if (slot < 0 || slot >= a.num_slots)
+            continue;
+        const int64_t at = (slot * a.n_kv + kvh) * kD + d0;
+        for (int c = 0; c < 64; ++c) {
+            float v;
+            if constexpr (FP8)
+                v = (((const uint8_t *)a.v_cache)[at + c] & 0x7fu) == 0x7fu
+                        ? __uint_as_float(0x7fc00000u)
+                        : 0.0f;
+            else
+                v = __uint_as_float((uint32_t)((const uint16_t *)a.v_cache)[at + c] << 16);
+            if (!isfinite(v))
+                o[c] = __fadd_rn(o[c], v);
+        }
+    }
+}
+
 // One product of 128 x 128 x 128: eight steps of 16.
 __device__ __forceinline__ void scores_product(uint32_t d, uint32_t q, uint32_t k, uint32_t desc)
 {
@@ -92,7 +147,7 @@ __device__ __forceinline__ void values_product(uint32_t d, uint32_t p, uint32_t 
         tc_mma_ts(d, p + 8 * ks, operand_desc(v + ks * 2048, kHalfTile), desc, add || ks > 0);
 }
 
-template <bool FP8, bool SPLIT>
+template <bool FP8, bool SPLIT, bool WINDOW>
 __global__ void __launch_bounds__(TcConfig<FP8, SPLIT>::kThreads, 1)
     attn_tc_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ AttnPlan p,
                    const __grid_constant__ CacheMaps maps)
@@ -108,16 +163,20 @@ __global__ void __launch_bounds__(TcConfig<FP8, SPLIT>::kThreads, 1)
              *o_full = bars + 21, *r_full = bars + 22, *r_empty = bars + 26;
     uint32_t *s_tmem = reinterpret_cast<uint32_t *>(smem + C::kMisc);
     volatile int *s_fail = reinterpret_cast<int *>(smem + C::kMisc + 4);
+    int *s_first = reinterpret_cast<int *>(smem + C::kMisc + 8);
+    volatile int *s_left_out = reinterpret_cast<int *>(smem + C::kMisc + 12);
 
     const int kvh = blockIdx.y;
     const int64_t row0 = (int64_t)blockIdx.x * (SPLIT ? 128 : 256);
-    const int64_t key0 = (int64_t)blockIdx.z * p.tc_steps * (SPLIT ? 256 : 128);
+    const int64_t key0 = p.p_first + (int64_t)blockIdx.z * p.tc_steps * (SPLIT ? 256 : 128);
     const int64_t key_end = min(a.n_prefix, key0 + (int64_t)p.tc_steps * (SPLIT ? 256 : 128));
     const int N = (int)((key_end - key0 + 127) / 128);          // key tiles
     const int halves = SPLIT ? 2 : (p.rows - row0 > 128 ? 2 : 1);  // that have rows
 
     if (tid == 0) {
         *s_fail = base % 1024 != 0;
+        *s_first = 0;
+        *s_left_out = 0;
         mbar_init(q_full, SPLIT ? 128 : 128 * halves);
         for (int i = 0; i < 2; ++i) {
             mbar_init(&k_full[i], FP8 ? 128 : 1);
@@ -151,11 +210,23 @@ __global__ void __launch_bounds__(TcConfig<FP8, SPLIT>::kThreads, 1)
         const int64_t rr = row0 + (SPLIT ? 0 : 128 * half) + (tid & 127);
         const bool act = rr < p.rows;
         bool seen = false;
+        int first = 0;  // first key that the row sees, counted from key0
         float scale = 0.0f;
         if (half < halves) {
             int i = 0, hg = 0;
             const int64_t tok = act ? row_token(a, p, rr, i, hg) : 0;
-            seen = act && seq_len(a, rr / p.R) - a.q_len + i >= 0;
+            if (act) {
+                const int64_t pos = seq_len(a, (uint32_t)rr / (uint32_t)p.R) - a.q_len + i;
+                seen = pos >= 0;
+                if (WINDOW && seen)
+                    first = (int)max((int64_t)0, min(key_end, a.n_prefix + pos + 1 - a.window) - key0);
+            }
+            if constexpr (WINDOW) {
+                const int most = __reduce_max_sync(0xffffffffu, first);
+                if (lane == 0)
+                    atomicMax(s_first, most);
+                named_sync(1, 128 * (SPLIT ? 2 : halves));
+            }
             const char *qp = (const char *)a.q +
                              2 * (tok * a.q_stride + (int64_t)(kvh * p.group + hg) * kD);
             float f = 1.0f, inv = 1.0f;
@@ -196,6 +267,15 @@ __global__ void __launch_bounds__(TcConfig<FP8, SPLIT>::kThreads, 1)
         const uint32_t o_at = s_at - half * 128 + 256 + half * 128;
         float m = -INFINITY, l = 0.0f;
         bool ok = true;
+        const int most_first = WINDOW ? *s_first : 0;
+        // scores of 64 columns from c0 on: -inf where there is no key or the row does not see it
+        auto hide = [&](float (&r)[64], const uint32_t *mask, int c0, int from) {
+#pragma unroll
+            for (int c = 0; c < 64; ++c)
+                r[c] = ((mask[c >> 5] >> (c & 31)) & 1u) && (!WINDOW || c0 + c >= from)
+                           ? r[c]
+                           : -INFINITY;
+        };
         for (int j = 0; j < tiles; ++j) {
             const int i = SPLIT ? 2 * j + half : j;
             ok = mbar_wait_or_fail(&m_full[i & 7], (i >> 3) & 1, s_fail) &&
@@ -209,26 +289,22 @@ __global__ void __launch_bounds__(TcConfig<FP8, SPLIT>::kThreads, 1)
 #pragma unroll
             for (int w = 0; w < 4; ++w)
                 mask[w] = s_mask[4 * (i & 7) + w];
-            const bool all = (mask[0] & mask[1] & mask[2] & mask[3]) == 0xffffffffu;
+            const int from = first - 128 * i;  // the row's first column
+            const bool all = (mask[0] & mask[1] & mask[2] & mask[3]) == 0xffffffffu &&
+                             (!WINDOW || most_first <= 128 * i);
             float r[64];
             float mx0 = -INFINITY, mx1 = -INFINITY;
             load64(s_at, r);
-            if (!all) {
-#pragma unroll
-                for (int c = 0; c < 64; ++c)
-                    r[c] = (mask[c >> 5] >> (c & 31)) & 1u ? r[c] : -INFINITY;
-            }
+            if (!all)
+                hide(r, mask, 0, from);
 #pragma unroll
             for (int c = 0; c < 64; c += 2) {
                 mx0 = fmaxf(mx0, r[c]);
                 mx1 = fmaxf(mx1, r[c + 1]);
             }
             load64(s_at + 64, r);
-            if (!all) {
-#pragma unroll
-                for (int c = 0; c < 64; ++c)
-                    r[c] = (mask[2 + (c >> 5)] >> (c & 31)) & 1u ? r[c] : -INFINITY;
-            }
+            if (!all)
+                hide(r, mask + 2, 64, from);
 #pragma unroll
             for (int c = 0; c < 64; c += 2) {
                 mx0 = fmaxf(mx0, r[c]);
@@ -254,11 +330,8 @@ __global__ void __launch_bounds__(TcConfig<FP8, SPLIT>::kThreads, 1)
                         tmem_st32(o_at + 64 * h + 32, *reinterpret_cast<uint32_t(*)[32]>(&o[32]));
                     }
                     load64(s_at + 64, r);
-                    if (!all) {
-#pragma unroll
-                        for (int c = 0; c < 64; ++c)
-                            r[c] = (mask[2 + (c >> 5)] >> (c & 31)) & 1u ? r[c] : -INFINITY;
-                    }
+                    if (!all)
+                        hide(r, mask + 2, 64, from);
                 }
             }
             const float neg = m == -INFINITY ? 0.0f : -m;
@@ -267,11 +340,8 @@ __global__ void __launch_bounds__(TcConfig<FP8, SPLIT>::kThreads, 1)
             for (int h = 1; h >= 0; --h) {  // the second half is in registers and makes room first
                 if (h == 0) {
                     load64(s_at, r);
-                    if (!all) {
-#pragma unroll
-                        for (int c = 0; c < 64; ++c)
-                            r[c] = (mask[c >> 5] >> (c & 31)) & 1u ? r[c] : -INFINITY;
-                    }
+                    if (!all)
+                        hide(r, mask, 0, from);
                 }
                 uint32_t w[32];
 #pragma unroll
@@ -284,6 +354,12 @@ __global__ void __launch_bounds__(TcConfig<FP8, SPLIT>::kThreads, 1)
                 tmem_st32(s_at + 64 + 32 * h, w);
             }
             l = __fadd_rn(l, __fadd_rn(lo_of(sum), hi_of(sum)));
+            if (WINDOW && most_first > 128 * i) {
+                ok = mbar_wait_or_fail(&v_full[i & 1], (i >> 1) & 1, s_fail);
+                if (ok && leave_out<FP8>(base + C::kV + (i & 1) * kTile, tid & 127))
+                    *s_left_out = 1;
+                fence_async_shared();
+            }
             tmem_wait_st();
             tc_fence_before();
             mbar_arrive(&p_full[half]);
@@ -299,6 +375,10 @@ __global__ void __launch_bounds__(TcConfig<FP8, SPLIT>::kThreads, 1)
                 for (int h = 0; h < 2; ++h) {
                     float r[64];
                     load64(o_at + 64 * h, r);
+                    if constexpr (WINDOW) {
+                        if (act && *s_left_out)
+                            put_back<FP8>(a, r, kvh, 64 * h, key0 + first, key_end);
+                    }
                     if (act) {
 #pragma unroll
                         for (int c = 0; c < 64; c += 4)
@@ -532,16 +612,24 @@ __global__ void __launch_bounds__(TcConfig<FP8, SPLIT>::kThreads, 1)
         tmem_free_all(tmem);
 }
 
-template <bool FP8, bool SPLIT>
+template <bool FP8, bool SPLIT, bool WINDOW>
 cudaError_t launch(const AttnArgs &a, const AttnPlan &p, const CacheMaps &maps, cudaStream_t stream)
 {
     constexpr int bytes = TcConfig<FP8, SPLIT>::kBytes;
-    const cudaError_t e = allow_smem<attn_tc_kernel<FP8, SPLIT>>(bytes);
+    const cudaError_t e = allow_smem<attn_tc_kernel<FP8, SPLIT, WINDOW>>(bytes);
     if (e != cudaSuccess)
         return e;
-    return launch_pdl(attn_tc_kernel<FP8, SPLIT>,
+    return launch_pdl(attn_tc_kernel<FP8, SPLIT, WINDOW>,
                       dim3((unsigned)p.tc_rtiles, (unsigned)a.n_kv, (unsigned)p.tc_blocks),
                       dim3(TcConfig<FP8, SPLIT>::kThreads), bytes, stream, a, p, maps);
+}
+
+template <bool FP8, bool SPLIT>
+cudaError_t launch_window(const AttnArgs &a, const AttnPlan &p, const CacheMaps &maps,
+                          cudaStream_t stream)
+{
+    return a.window > 0 ? launch<FP8, SPLIT, true>(a, p, maps, stream)
+                        : launch<FP8, SPLIT, false>(a, p, maps, stream);
 }
 
 }  // namespace
@@ -550,10 +638,10 @@ cudaError_t launch_attn_tc(const AttnArgs &a, const AttnPlan &p, const CacheMaps
                            cudaStream_t stream)
 {
     if (a.fp8)
-        return p.tc_split ? launch<true, true>(a, p, maps, stream)
-                          : launch<true, false>(a, p, maps, stream);
-    return p.tc_split ? launch<false, true>(a, p, maps, stream)
-                      : launch<false, false>(a, p, maps, stream);
+        return p.tc_split ? launch_window<true, true>(a, p, maps, stream)
+                          : launch_window<true, false>(a, p, maps, stream);
+    return p.tc_split ? launch_window<false, true>(a, p, maps, stream)
+                      : launch_window<false, false>(a, p, maps, stream);
 }
 
 cudaError_t read_attn_tc_fault_word(unsigned int *value, bool clear)

@@ -253,11 +253,34 @@ def test_values_of_unseen_keys_do_not_matter():
 
 
 @pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("B,P,window", [(50, 600, 400), (25, 900, 600), (50, 600, 300)])
+def test_values_that_a_window_hides_from_some_rows(B, P, window, fp8):
+    # prefix values that are not finite: rows that see them show it, the others do not change
+    lib()
+    lens = [1 + 3 * b for b in range(B)]
+    c = make(B, 1, 6, 1, P, 3 * B, lens, fp8=fp8, seed=B)
+    clean = run(c, window=window)[0]
+    j = P - window + 60                        # out of the window of the longer sequences
+    c["v"][c["prefix"][j], 0, 9] = 0x7f if fp8 else math.nan
+    if not fp8:
+        c["v"][c["prefix"][j + 1], 0, 5] = -math.inf
+    out = run(c, window=window)[0]
+    for b, n in enumerate(lens):
+        sees, sees1 = n - 1 < window - P + j, n - 1 < window - P + j + 1
+        assert bool(torch.isnan(out[b, :, 9]).all()) == sees, b
+        if not fp8:
+            assert bool((out[b, :, 5] == -math.inf).all()) == sees1, b
+        keep = [d for d in range(D) if d not in (5, 9)]
+        assert torch.equal(out[b][:, keep], clean[b][:, keep]), b
+
+
+@pytest.mark.parametrize("fp8", [False, True])
 def test_many_rows_on_a_long_prefix(fp8):
     # above the switch to the kernel for many prefix rows, with ragged row and key tiles
     lib()
     for B, q_len, n_q, n_kv, P, window in ((43, 1, 6, 1, 1000, 0), (90, 1, 6, 1, 517, 0),
-                                           (13, 5, 12, 2, 700, 0), (30, 2, 6, 1, 300, 150)):
+                                           (13, 5, 12, 2, 700, 0), (30, 2, 6, 1, 300, 150),
+                                           (40, 1, 6, 1, 800, 270), (20, 3, 6, 1, 900, 512)):
         lens = [1 + (7 * b) % 11 for b in range(B)]
         check(make(B, q_len, n_q, n_kv, P, 11, lens, fp8=fp8, seed=P), window=window, weights=True)
 
