@@ -220,9 +220,10 @@ __device__ __forceinline__ Unit next_unit(const AttnArgs &a, const AttnPlan &p, 
 
 // The sum over the sequences of their units' places after `base`; every thread of the block takes
 // part.  find >= base: also finds the sequence that holds tile `find`.  cum (or nullptr) receives the
-// running sums.
+// running sums; last_own, last_end: this thread's last sequence's places and their running sum.
 __device__ __forceinline__ int64_t scan_sequences(const AttnArgs &a, const AttnPlan &p, int64_t base,
-                                                  int64_t find, int64_t *cum, int64_t *s_scan)
+                                                  int64_t find, int64_t *cum, int64_t *s_scan,
+                                                  int64_t &last_own, int64_t &last_end)
 {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int64_t per_seq = (int64_t)a.n_kv * p.s_rtiles;
@@ -257,6 +258,7 @@ __device__ __forceinline__ int64_t scan_sequences(const AttnArgs &a, const AttnP
         }
         total += sum;
         __syncthreads();
+        last_own = own, last_end = end;
         if (find >= base && find < total)
             break;
     }
@@ -302,8 +304,9 @@ __global__ void __launch_bounds__(kThreads, 2)
     const int64_t p_units = a.n_kv * p.p_rtiles;
     const int64_t p_total = p_units * (p.p_tiles + kUnitCost);
     int64_t *cum = reinterpret_cast<int64_t *>(a.workspace + p.cum_off);
-    const int64_t total =
-        scan_sequences(a, p, p_total, -1, blockIdx.x == 0 ? cum : nullptr, s_scan);
+    int64_t own = 0, own_end = 0;
+    const int64_t total = scan_sequences(a, p, p_total, -1, blockIdx.x == 0 ? cum : nullptr, s_scan,
+                                         own, own_end);
     const int64_t shares = min((int64_t)p.ctas, total);  // none of them empty
     __syncthreads();
     if (blockIdx.x >= shares || *s_fail) {
@@ -314,7 +317,15 @@ __global__ void __launch_bounds__(kThreads, 2)
     const int64_t tile0 = div32(total * blockIdx.x, shares);
     int64_t b0 = -1, b0_start = 0;
     if (tile0 >= p_total) {
-        scan_sequences(a, p, p_total, tile0, nullptr, s_scan);
+        if (a.B > kThreads) {
+            scan_sequences(a, p, p_total, tile0, nullptr, s_scan, own, own_end);
+        } else {  // the sums are at hand
+            if (tile0 >= own_end - own && tile0 < own_end) {
+                s_scan[kWarps] = tid;
+                s_scan[kWarps + 1] = own_end - own;
+            }
+            __syncthreads();
+        }
         b0 = s_scan[kWarps];
         b0_start = s_scan[kWarps + 1];
     }
@@ -647,7 +658,8 @@ __global__ void __launch_bounds__(kThreads, 2)
             }
             // A weight of zero does not hide an infinite or NaN value of a key that only other rows
             // see, so such a stage (rare) goes column by column with those values left out.
-            if (!all_seen && stage_has_nonfinite<FP8>(vt, lane)) {
+            const bool hidden = key0 < lo_all || hi_all < min(key0 + C::kKeys, u.key_end);
+            if (hidden && stage_has_nonfinite<FP8>(vt, lane)) {
 #pragma unroll
                 for (int mk = 0; mk < MT; ++mk)
 #pragma unroll

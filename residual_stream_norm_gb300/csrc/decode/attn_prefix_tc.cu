@@ -230,33 +230,34 @@ __global__ void __launch_bounds__(TcConfig<FP8, SPLIT>::kThreads, 1)
             const char *qp = (const char *)a.q +
                              2 * (tok * a.q_stride + (int64_t)(kvh * p.group + hg) * kD);
             float f = 1.0f, inv = 1.0f;
+            uint4 row[16];
+#pragma unroll
+            for (int c = 0; c < 16; ++c)
+                row[c] = act ? ld_cached(qp + 16 * c) : make_uint4(0u, 0u, 0u, 0u);
             if constexpr (FP8) {
                 uint32_t mx = 0u;
-#pragma unroll 4
-                for (int c = 0; c < 16; ++c) {
-                    const uint4 v = act ? ld_cached(qp + 16 * c) : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+                for (int c = 0; c < 16; ++c)
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
-                        const uint32_t w = word(v, j);
+                        const uint32_t w = word(row[c], j);
                         mx = max(mx, max((w << 16) & 0x7fffffffu, w & 0x7fff0000u));
                     }
-                }
                 f16_row_factor(mx, f, inv);
             }
             scale = __fmul_rn(__fmul_rn(a.sm_scale * a.k_scale, kLog2e), inv);
             if (!SPLIT || half == 0) {
                 const int r = tid & 127;
                 const uint32_t dst = base + (SPLIT ? 0 : half) * kTile + r * 128;
-#pragma unroll 4
+#pragma unroll
                 for (int c = 0; c < 16; ++c) {
-                    uint4 v = act ? ld_cached(qp + 16 * c) : make_uint4(0u, 0u, 0u, 0u);
                     if constexpr (FP8) {
 #pragma unroll
                         for (int j = 0; j < 4; ++j)
-                            word(v, j) = pack_f16x2(__fmul_rn(bf_lo(word(v, j)), f),
-                                                    __fmul_rn(bf_hi(word(v, j)), f));
+                            word(row[c], j) = pack_f16x2(__fmul_rn(bf_lo(word(row[c], j)), f),
+                                                         __fmul_rn(bf_hi(word(row[c], j)), f));
                     }
-                    sts128(dst + (c >> 3) * kHalfTile + 16 * ((c & 7) ^ (r & 7)), v);
+                    sts128(dst + (c >> 3) * kHalfTile + 16 * ((c & 7) ^ (r & 7)), row[c]);
                 }
                 fence_async_shared();
                 mbar_arrive(q_full);
@@ -369,8 +370,11 @@ __global__ void __launch_bounds__(TcConfig<FP8, SPLIT>::kThreads, 1)
             tc_fence_after();
             const int part = SPLIT ? 2 * blockIdx.z + half : blockIdx.z;
             const int64_t at = ((int64_t)kvh * p.rows + rr) * p.tc_parts + part;
-            float *po = reinterpret_cast<float *>(a.workspace + p.tc_o_off) + at * kD;
             if (tiles > 0) {
+                // The stages are free now (every copy has arrived, every product is complete): a warp's
+                // 32 rows go through them, so that rows are written whole.  Chunk c of row r lies at
+                // c ^ (r % 8).
+                const uint32_t stage = base + (half ? C::kV : C::kK) + (warp & 3) * 16384;
 #pragma unroll 1
                 for (int h = 0; h < 2; ++h) {
                     float r[64];
@@ -379,13 +383,22 @@ __global__ void __launch_bounds__(TcConfig<FP8, SPLIT>::kThreads, 1)
                         if (act && *s_left_out)
                             put_back<FP8>(a, r, kvh, 64 * h, key0 + first, key_end);
                     }
-                    if (act) {
 #pragma unroll
-                        for (int c = 0; c < 64; c += 4)
-                            *reinterpret_cast<float4 *>(po + 64 * h + c) =
-                                make_float4(r[c], r[c + 1], r[c + 2], r[c + 3]);
-                    }
+                    for (int c = 0; c < 16; ++c)
+                        sts128(stage + lane * 512 + 16 * ((16 * h + c) ^ (lane & 7)),
+                               make_uint4(__float_as_uint(r[4 * c]), __float_as_uint(r[4 * c + 1]),
+                                          __float_as_uint(r[4 * c + 2]),
+                                          __float_as_uint(r[4 * c + 3])));
                 }
+                __syncwarp();
+                float *po = reinterpret_cast<float *>(a.workspace + p.tc_o_off);
+                const int64_t rr0 = rr - lane;
+                const int rows = (int)min((int64_t)32, p.rows - rr0);
+#pragma unroll 4
+                for (int x = 0; x < rows; ++x)
+                    st_global(po + (((int64_t)kvh * p.rows + rr0 + x) * p.tc_parts + part) * kD +
+                                  4 * lane,
+                              lds128(stage + x * 512 + 16 * (lane ^ (x & 7))));
             }
             if (act)
                 reinterpret_cast<float2 *>(a.workspace + p.tc_ml_off)[at] =
