@@ -105,26 +105,31 @@ __device__ __forceinline__ bool leave_out(uint32_t tile, int t)
     return found;
 }
 
-// Adds to 64 elements (from d0 on) of a row's sum the infinite and NaN values of the keys it sees.
+// Adds to a row's sums, in shared memory (chunk c at c ^ (lane % 8)), the infinite and NaN values of the
+// keys it sees.
 template <bool FP8>
-__device__ __noinline__ void put_back(const AttnArgs &a, float (&o)[64], int kvh, int d0,
-                                      int64_t key, int64_t key_end)
+__device__ __noinline__ void put_back(const AttnArgs &a, uint32_t row, int lane, int kvh, int64_t key,
+                                      int64_t key_end)
 {
     for (; key < key_end; ++key) {
         const int64_t slot = a.prefix[key];
         if (slot < 0 || slot >= a.num_slots)
             continue;
-        const int64_t at = (slot * a.n_kv + kvh) * kD + d0;
-        for (int c = 0; c < 64; ++c) {
+        const int64_t at = (slot * a.n_kv + kvh) * kD;
+        for (int d = 0; d < kD; ++d) {
             float v;
             if constexpr (FP8)
-                v = (((const uint8_t *)a.v_cache)[at + c] & 0x7fu) == 0x7fu
+                v = (((const uint8_t *)a.v_cache)[at + d] & 0x7fu) == 0x7fu
                         ? __uint_as_float(0x7fc00000u)
                         : 0.0f;
             else
-                v = __uint_as_float((uint32_t)((const uint16_t *)a.v_cache)[at + c] << 16);
-            if (!isfinite(v))
-                o[c] = __fadd_rn(o[c], v);
+                v = __uint_as_float((uint32_t)((const uint16_t *)a.v_cache)[at + d] << 16);
+            if (!isfinite(v)) {
+                const uint32_t p = row + 16 * ((d >> 2) ^ (lane & 7)) + 4 * (d & 3);
+                float o;
+                asm volatile("ld.shared.f32 %0, [%1];" : "=f"(o) : "r"(p) : "memory");
+                asm volatile("st.shared.f32 [%0], %1;" ::"r"(p), "f"(__fadd_rn(o, v)) : "memory");
+            }
         }
     }
 }
@@ -227,37 +232,47 @@ __global__ void __launch_bounds__(TcConfig<FP8, SPLIT>::kThreads, 1)
                     atomicMax(s_first, most);
                 named_sync(1, 128 * (SPLIT ? 2 : halves));
             }
-            const char *qp = (const char *)a.q +
-                             2 * (tok * a.q_stride + (int64_t)(kvh * p.group + hg) * kD);
-            float f = 1.0f, inv = 1.0f;
+            // The warp loads its 32 rows two at a time, half a warp a row, all of them in flight;
+            // FP8: a row's largest magnitude gives the factor that takes it to FP16.
+            const int64_t off =
+                act ? 2 * (tok * a.q_stride + (int64_t)(kvh * p.group + hg) * kD) : -1;
             uint4 row[16];
 #pragma unroll
-            for (int c = 0; c < 16; ++c)
-                row[c] = act ? ld_cached(qp + 16 * c) : make_uint4(0u, 0u, 0u, 0u);
+            for (int k = 0; k < 16; ++k) {
+                const int64_t o = __shfl_sync(0xffffffffu, off, 2 * k + (lane >> 4));
+                row[k] = o >= 0 ? ld_cached((const char *)a.q + o + 16 * (lane & 15))
+                                : make_uint4(0u, 0u, 0u, 0u);
+            }
+            float inv = 1.0f;
             if constexpr (FP8) {
-                uint32_t mx = 0u;
 #pragma unroll
-                for (int c = 0; c < 16; ++c)
+                for (int k = 0; k < 16; ++k) {
+                    uint32_t mx = 0u;
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
-                        const uint32_t w = word(row[c], j);
+                        const uint32_t w = word(row[k], j);
                         mx = max(mx, max((w << 16) & 0x7fffffffu, w & 0x7fff0000u));
                     }
-                f16_row_factor(mx, f, inv);
+#pragma unroll
+                    for (int x = 1; x < 16; x <<= 1)
+                        mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, x));
+                    float f, back;
+                    f16_row_factor(mx, f, back);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        word(row[k], j) = pack_f16x2(__fmul_rn(bf_lo(word(row[k], j)), f),
+                                                     __fmul_rn(bf_hi(word(row[k], j)), f));
+                    back = __shfl_sync(0xffffffffu, back, 16 * (lane & 1));
+                    inv = lane >> 1 == k ? back : inv;  // of this thread's row
+                }
             }
             scale = __fmul_rn(__fmul_rn(a.sm_scale * a.k_scale, kLog2e), inv);
             if (!SPLIT || half == 0) {
-                const int r = tid & 127;
-                const uint32_t dst = base + (SPLIT ? 0 : half) * kTile + r * 128;
+                const uint32_t dst = base + (SPLIT ? 0 : half) * kTile + (lane >> 3 & 1) * kHalfTile;
 #pragma unroll
-                for (int c = 0; c < 16; ++c) {
-                    if constexpr (FP8) {
-#pragma unroll
-                        for (int j = 0; j < 4; ++j)
-                            word(row[c], j) = pack_f16x2(__fmul_rn(bf_lo(word(row[c], j)), f),
-                                                         __fmul_rn(bf_hi(word(row[c], j)), f));
-                    }
-                    sts128(dst + (c >> 3) * kHalfTile + 16 * ((c & 7) ^ (r & 7)), row[c]);
+                for (int k = 0; k < 16; ++k) {
+                    const int r = 32 * (warp & 3) + 2 * k + (lane >> 4);
+                    sts128(dst + r * 128 + 16 * ((lane & 7) ^ (r & 7)), row[k]);
                 }
                 fence_async_shared();
                 mbar_arrive(q_full);
@@ -270,12 +285,18 @@ __global__ void __launch_bounds__(TcConfig<FP8, SPLIT>::kThreads, 1)
         bool ok = true;
         const int most_first = WINDOW ? *s_first : 0;
         // scores of 64 columns from c0 on: -inf where there is no key or the row does not see it
-        auto hide = [&](float (&r)[64], const uint32_t *mask, int c0, int from) {
+        bool all = true, cut = false;  // whether the tile has all keys; whether the window cuts it
+        auto hide = [&](float (&r)[64], uint32_t m0, uint32_t m1, int c0, int from) {
+            if (!all) {
 #pragma unroll
-            for (int c = 0; c < 64; ++c)
-                r[c] = ((mask[c >> 5] >> (c & 31)) & 1u) && (!WINDOW || c0 + c >= from)
-                           ? r[c]
-                           : -INFINITY;
+                for (int c = 0; c < 64; ++c)
+                    r[c] = ((c < 32 ? m0 : m1) >> (c & 31)) & 1u ? r[c] : -INFINITY;
+            }
+            if (WINDOW && cut) {
+#pragma unroll
+                for (int c = 0; c < 64; ++c)
+                    r[c] = c0 + c >= from ? r[c] : -INFINITY;
+            }
         };
         for (int j = 0; j < tiles; ++j) {
             const int i = SPLIT ? 2 * j + half : j;
@@ -291,21 +312,19 @@ __global__ void __launch_bounds__(TcConfig<FP8, SPLIT>::kThreads, 1)
             for (int w = 0; w < 4; ++w)
                 mask[w] = s_mask[4 * (i & 7) + w];
             const int from = first - 128 * i;  // the row's first column
-            const bool all = (mask[0] & mask[1] & mask[2] & mask[3]) == 0xffffffffu &&
-                             (!WINDOW || most_first <= 128 * i);
+            all = (mask[0] & mask[1] & mask[2] & mask[3]) == 0xffffffffu;
+            cut = WINDOW && most_first > 128 * i;
             float r[64];
             float mx0 = -INFINITY, mx1 = -INFINITY;
             load64(s_at, r);
-            if (!all)
-                hide(r, mask, 0, from);
+            hide(r, mask[0], mask[1], 0, from);
 #pragma unroll
             for (int c = 0; c < 64; c += 2) {
                 mx0 = fmaxf(mx0, r[c]);
                 mx1 = fmaxf(mx1, r[c + 1]);
             }
             load64(s_at + 64, r);
-            if (!all)
-                hide(r, mask + 2, 64, from);
+            hide(r, mask[2], mask[3], 64, from);
 #pragma unroll
             for (int c = 0; c < 64; c += 2) {
                 mx0 = fmaxf(mx0, r[c]);
@@ -331,8 +350,7 @@ __global__ void __launch_bounds__(TcConfig<FP8, SPLIT>::kThreads, 1)
                         tmem_st32(o_at + 64 * h + 32, *reinterpret_cast<uint32_t(*)[32]>(&o[32]));
                     }
                     load64(s_at + 64, r);
-                    if (!all)
-                        hide(r, mask + 2, 64, from);
+                    hide(r, mask[2], mask[3], 64, from);
                 }
             }
             const float neg = m == -INFINITY ? 0.0f : -m;
@@ -341,8 +359,7 @@ __global__ void __launch_bounds__(TcConfig<FP8, SPLIT>::kThreads, 1)
             for (int h = 1; h >= 0; --h) {  // the second half is in registers and makes room first
                 if (h == 0) {
                     load64(s_at, r);
-                    if (!all)
-                        hide(r, mask, 0, from);
+                    hide(r, mask[0], mask[1], 0, from);
                 }
                 uint32_t w[32];
 #pragma unroll
@@ -355,7 +372,7 @@ __global__ void __launch_bounds__(TcConfig<FP8, SPLIT>::kThreads, 1)
                 tmem_st32(s_at + 64 + 32 * h, w);
             }
             l = __fadd_rn(l, __fadd_rn(lo_of(sum), hi_of(sum)));
-            if (WINDOW && most_first > 128 * i) {
+            if (cut) {
                 ok = mbar_wait_or_fail(&v_full[i & 1], (i >> 1) & 1, s_fail);
                 if (ok && leave_out<FP8>(base + C::kV + (i & 1) * kTile, tid & 127))
                     *s_left_out = 1;
@@ -379,10 +396,6 @@ __global__ void __launch_bounds__(TcConfig<FP8, SPLIT>::kThreads, 1)
                 for (int h = 0; h < 2; ++h) {
                     float r[64];
                     load64(o_at + 64 * h, r);
-                    if constexpr (WINDOW) {
-                        if (act && *s_left_out)
-                            put_back<FP8>(a, r, kvh, 64 * h, key0 + first, key_end);
-                    }
 #pragma unroll
                     for (int c = 0; c < 16; ++c)
                         sts128(stage + lane * 512 + 16 * ((16 * h + c) ^ (lane & 7)),
@@ -390,15 +403,27 @@ __global__ void __launch_bounds__(TcConfig<FP8, SPLIT>::kThreads, 1)
                                           __float_as_uint(r[4 * c + 2]),
                                           __float_as_uint(r[4 * c + 3])));
                 }
+                if constexpr (WINDOW) {
+                    if (act && *s_left_out)
+                        put_back<FP8>(a, stage + lane * 512, lane, kvh, key0 + first, key_end);
+                }
                 __syncwarp();
-                float *po = reinterpret_cast<float *>(a.workspace + p.tc_o_off);
                 const int64_t rr0 = rr - lane;
                 const int rows = (int)min((int64_t)32, p.rows - rr0);
-#pragma unroll 4
-                for (int x = 0; x < rows; ++x)
-                    st_global(po + (((int64_t)kvh * p.rows + rr0 + x) * p.tc_parts + part) * kD +
-                                  4 * lane,
-                              lds128(stage + x * 512 + 16 * (lane ^ (x & 7))));
+                const int64_t step = (int64_t)p.tc_parts * kD;
+                float *po = reinterpret_cast<float *>(a.workspace + p.tc_o_off) +
+                            ((int64_t)kvh * p.rows + rr0) * step + part * kD + 4 * lane;
+#pragma unroll
+                for (int x0 = 0; x0 < 32; x0 += 8) {
+                    uint4 v[8];
+#pragma unroll
+                    for (int x = 0; x < 8; ++x)
+                        v[x] = lds128(stage + (x0 + x) * 512 + 16 * (lane ^ x));
+#pragma unroll
+                    for (int x = 0; x < 8; ++x)
+                        if (x0 + x < rows)
+                            st_global(po + (x0 + x) * step, v[x]);
+                }
             }
             if (act)
                 reinterpret_cast<float2 *>(a.workspace + p.tc_ml_off)[at] =
