@@ -1068,8 +1068,18 @@ cudaError_t launch_rows_type(const AttnArgs &a, const AttnPlan &p, const CacheMa
 
 inline int64_t align_up(int64_t x, int64_t a) { return (x + a - 1) / a * a; }
 
-// From these many rows a KV head and prefix keys on, the prefix goes to the tensor-core kernel.
-constexpr int64_t kTcRows = 33, kTcKeys = 256;
+// The prefix goes to the tensor-core kernel where that is expected to take less time, in tenths of a
+// microsecond: it costs 11 us to set up and write out and 1.8 us a step (bench of 1 to 43 steps); the
+// rows kernel 1.3 us a tile of 64 keys for 16 rows, or a unit's cost of kUnitCost of them, on each
+// of its blocks.  (128 rows behind 512 keys: 7 against 13 us; 384 rows behind 5001: 69 against 22 us.)
+bool prefer_tc(const AttnPlan &p, int32_t n_kv, int64_t keys)
+{
+    const int64_t places = n_kv * ((p.rows + 15) / 16) * ((keys + 63) / 64 + kUnitCost);
+    const int64_t rows = 13 * ((places + 2 * kPlanSms - 1) / (2 * kPlanSms));
+    const int64_t blocks = (int64_t)p.tc_rtiles * n_kv * p.tc_blocks;
+    const int64_t tc = 110 + 18 * p.tc_steps * ((blocks + kPlanSms - 1) / kPlanSms);
+    return tc < rows;
+}
 
 // Divides the prefix among the tensor-core kernel's blocks: tiles of 256 rows, or, up to 128 rows, of
 // 128 rows with every other key tile to each half of the block.  The number of parts is the one
@@ -1091,7 +1101,8 @@ void plan_tc(AttnPlan &p, int32_t n_kv, int64_t keys)
         }
     }
     p.tc_blocks = (int32_t)((most + p.tc_steps - 1) / p.tc_steps);
-    p.tc_parts = p.tc_split ? 2 * p.tc_blocks : p.tc_blocks;
+    if (prefer_tc(p, n_kv, keys))
+        p.tc_parts = p.tc_split ? 2 * p.tc_blocks : p.tc_blocks;
 }
 
 }  // namespace
@@ -1109,7 +1120,7 @@ AttnPlan attn_plan(int32_t B, int32_t q_len, int32_t n_q, int32_t n_kv, int64_t 
     p.p_first = window > 0 && n_prefix + 1 > window ? n_prefix + 1 - window : 0;
     p.p_first = (p.p_first < n_prefix ? p.p_first : n_prefix) & ~(int64_t)15;
     const int64_t p_keys = n_prefix - p.p_first;
-    if (tc && p.rows >= kTcRows && p_keys >= kTcKeys)
+    if (tc && p_keys > 0)
         plan_tc(p, n_kv, p_keys);
     const bool with_prefix = p_keys > 0 && p.tc_parts == 0;
     p.nt = (p.R > 8 || (with_prefix && p.rows > 8)) ? 2 : 1;

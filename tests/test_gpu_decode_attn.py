@@ -138,7 +138,13 @@ def test_pages(page, fp8):
     check(make(3, 2, 6, 1, 300, 150, [150, 61, 16], fp8=fp8, seed=page, page=page), window=70)
     check(make(40, 1, 6, 1, 1000, 33, [1 + b % 33 for b in range(40)], fp8=fp8, seed=page,
                page=page))
-    check(make(25, 1, 6, 1, 520, 9, [9] * 25, fp8=fp8, seed=page, page=page))
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("page", [1, 16, 24])
+def test_pages_on_a_long_prefix(page, fp8):
+    lib()
+    check(make(30, 1, 48, 8, 2500, 9, [1 + b % 9 for b in range(30)], fp8=fp8, seed=page, page=page))
 
 
 @pytest.mark.parametrize("window", [1, 2, 16, 63, 64, 65, 200, 10 ** 12])
@@ -253,36 +259,48 @@ def test_values_of_unseen_keys_do_not_matter():
 
 
 @pytest.mark.parametrize("fp8", [False, True])
-@pytest.mark.parametrize("B,P,window", [(50, 600, 400), (25, 900, 600), (50, 600, 300)])
+@pytest.mark.parametrize("B,P,window", [(30, 3000, 2700), (20, 4600, 4200)])
 def test_values_that_a_window_hides_from_some_rows(B, P, window, fp8):
     # prefix values that are not finite: rows that see them show it, the others do not change
     lib()
-    lens = [1 + 3 * b for b in range(B)]
-    c = make(B, 1, 6, 1, P, 3 * B, lens, fp8=fp8, seed=B)
+    lens = [1 + 7 * b for b in range(B)]
+    c = make(B, 1, 48, 8, P, 7 * B, lens, fp8=fp8, seed=B)
     clean = run(c, window=window)[0]
     j = P - window + 60                        # out of the window of the longer sequences
-    c["v"][c["prefix"][j], 0, 9] = 0x7f if fp8 else math.nan
+    c["v"][c["prefix"][j], 3, 9] = 0x7f if fp8 else math.nan
     if not fp8:
-        c["v"][c["prefix"][j + 1], 0, 5] = -math.inf
+        c["v"][c["prefix"][j + 1], 3, 5] = -math.inf
     out = run(c, window=window)[0]
     for b, n in enumerate(lens):
         sees, sees1 = n - 1 < window - P + j, n - 1 < window - P + j + 1
-        assert bool(torch.isnan(out[b, :, 9]).all()) == sees, b
+        assert bool(torch.isnan(out[b, 18:24, 9]).all()) == sees, b
         if not fp8:
-            assert bool((out[b, :, 5] == -math.inf).all()) == sees1, b
+            assert bool((out[b, 18:24, 5] == -math.inf).all()) == sees1, b
         keep = [d for d in range(D) if d not in (5, 9)]
         assert torch.equal(out[b][:, keep], clean[b][:, keep]), b
+        assert torch.equal(out[b, :18], clean[b, :18]) and torch.equal(out[b, 24:], clean[b, 24:]), b
 
 
 @pytest.mark.parametrize("fp8", [False, True])
-def test_many_rows_on_a_long_prefix(fp8):
-    # above the switch to the kernel for many prefix rows, with ragged row and key tiles
+@pytest.mark.parametrize("B,q_len,n_q,n_kv,P,window", [
+    (43, 1, 48, 8, 2000, 0), (20, 1, 48, 8, 4001, 0), (13, 5, 48, 8, 2500, 0),
+    (25, 2, 48, 8, 2600, 1800), (20, 1, 48, 8, 4000, 3900), (3, 1, 48, 8, 20000, 0),
+    (60, 1, 40, 8, 1300, 0)])
+def test_many_rows_on_a_long_prefix(B, q_len, n_q, n_kv, P, window, fp8):
+    # enough work for the kernel for many prefix rows, with ragged row and key tiles and padded rows
     lib()
-    for B, q_len, n_q, n_kv, P, window in ((43, 1, 6, 1, 1000, 0), (90, 1, 6, 1, 517, 0),
-                                           (13, 5, 12, 2, 700, 0), (30, 2, 6, 1, 300, 150),
-                                           (40, 1, 6, 1, 800, 270), (20, 3, 6, 1, 900, 512)):
-        lens = [1 + (7 * b) % 11 for b in range(B)]
-        check(make(B, q_len, n_q, n_kv, P, 11, lens, fp8=fp8, seed=P), window=window, weights=True)
+    lens = [(7 * b) % 12 for b in range(B)]
+    check(make(B, q_len, n_q, n_kv, P, 11, lens, fp8=fp8, seed=P), window=window, weights=True)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_long_prefix_with_bad_slots(fp8):
+    lib()
+    c = make(25, 1, 48, 8, 3000, 5, [5] * 25, fp8=fp8, seed=4)
+    c["prefix"][::9] = -1
+    c["prefix"][1:2500:250] = c["k"].shape[0]
+    c["prefix"][700:1100] = 2 ** 45
+    check(c)
 
 
 def test_same_bits_every_time_and_on_another_stream():
