@@ -67,9 +67,17 @@ __device__ __forceinline__ int64_t div32(int64_t x, int64_t y)
     return (uint64_t)(x | y) >> 32 ? x / y : (uint32_t)x / (uint32_t)y;
 }
 
-__device__ __forceinline__ int64_t seq_tiles(const AttnArgs &a, const AttnPlan &p, int64_t b)
+// Keys of a sequence's units: its own, behind the prefix's where that is in line with them.  A sequence
+// without a key of its own has no row that sees any.
+__device__ __forceinline__ int64_t line_len(const AttnArgs &a, const AttnPlan &p, int64_t b)
 {
     const int64_t n = seq_len(a, b);
+    return n > 0 ? p.in_line + n : 0;
+}
+
+__device__ __forceinline__ int64_t seq_tiles(const AttnArgs &a, const AttnPlan &p, int64_t b)
+{
+    const int64_t n = line_len(a, p, b);
     // tile_keys is a power of two
     return (n - first_tile_key(n, a.q_len, a.window) + p.tile_keys - 1) >> (31 - __clz(p.tile_keys));
 }
@@ -139,7 +147,8 @@ struct Cursor {
 
 // A unit's part that lies in the share.
 struct Unit {
-    const int64_t *list;
+    const int64_t *list;  // of the keys from `split` on; those before are the prefix's
+    int32_t split;
     int64_t unit;
     int32_t kvh;
     int32_t row0, row_end;
@@ -156,7 +165,7 @@ __device__ __forceinline__ void cursor_keys(const AttnArgs &a, const AttnPlan &p
         c.key_end = (int32_t)a.n_prefix;
         c.places = (int32_t)p.p_tiles + kUnitCost;
     } else {
-        c.key_end = (int32_t)seq_len(a, c.b);
+        c.key_end = (int32_t)line_len(a, p, c.b);
         c.key_first = (int32_t)first_tile_key(c.key_end, a.q_len, a.window);
         c.places = (int32_t)seq_places(a, p, c.b);
     }
@@ -208,7 +217,8 @@ __device__ __forceinline__ Unit next_unit(const AttnArgs &a, const AttnPlan &p, 
     u.row_base = u.prefix ? 0 : c.b * p.R;
     u.row0 = u.row_base + (int32_t)c.rt * M;
     u.row_end = u.prefix ? (int32_t)p.rows : u.row_base + p.R;
-    u.list = u.prefix ? a.prefix : a.table + c.b * a.table_stride;
+    u.split = u.prefix ? 0 : (int32_t)p.in_line;
+    u.list = u.prefix ? a.prefix : a.table + c.b * a.table_stride - u.split;
     const int64_t start = c.start + kUnitCost, stop = c.start + c.places;
     const int64_t seg_end = min(c.end, stop), first = max(c.tile, start);
     u.whole = first == start && seg_end == stop;
@@ -354,7 +364,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         const int key = lu.k0 + ls * C::kTileKeys + warp * C::kKeys + lane;
         Fetched f{-1, lu.kvh, ls < lsteps};
         if (f.have && lane < C::kKeys && key < lu.k1)
-            f.slot = lu.list[key];
+            f.slot = key < lu.split ? a.prefix[key] : lu.list[key];
         ++ls;
         return f;
     };
@@ -475,9 +485,9 @@ __global__ void __launch_bounds__(kThreads, 2)
                 lo[n][e] = 0;
                 hi[n][e] = u.key_end;
                 if (rr < u.row_end) {
-                    int64_t pos;  // in the suffix
+                    int64_t pos;  // in the suffix (a suffix unit: in the line, split + that)
                     if (!u.prefix) {
-                        pos = (int64_t)u.key_end - 1;
+                        pos = (int64_t)u.key_end - 1;  // in the line
                         if (a.q_len > 1)
                             pos += (rr - u.row_base) / p.group - (a.q_len - 1);
                     } else {
@@ -489,7 +499,7 @@ __global__ void __launch_bounds__(kThreads, 2)
                     lo[n][e] = a.window > 0 && where + 1 - a.window > 0
                                    ? (int)min((int64_t)u.key_end, where + 1 - a.window)
                                    : 0;
-                    hi[n][e] = pos < 0 ? 0 : (u.prefix ? u.key_end : (int)pos + 1);
+                    hi[n][e] = pos < u.split ? 0 : (u.prefix ? u.key_end : (int)pos + 1);
                 }
                 lo_all = max(lo_all, lo[n][e]);
                 hi_all = min(hi_all, hi[n][e]);
@@ -507,7 +517,7 @@ __global__ void __launch_bounds__(kThreads, 2)
                                       ? nullptr
                                       : reinterpret_cast<float *>(a.workspace + p.score_off) +
                                             (((int64_t)sb * a.n_kv + u.kvh) * p.R + (rr - sb * p.R)) *
-                                                p.score_width;
+                                                p.score_width - u.split;
                 }
         }
 
@@ -606,7 +616,7 @@ __global__ void __launch_bounds__(kThreads, 2)
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
                             const int key = key0 + 16 * mk + g + 8 * (e >> 1);
-                            if (score[n][e & 1] && key < u.k1)
+                            if (score[n][e & 1] && key < u.k1 && key >= u.split)
                                 score[n][e & 1][key] = sc[mk][n][e];
                         }
             }
@@ -1014,32 +1024,63 @@ __global__ void __launch_bounds__(128) attn_join_kernel(const __grid_constant__ 
     }
 }
 
-// The weight each suffix key received: one thread per key, over the scores that the rows kernel kept.
+// The weight each suffix key received, out of the scores that the rows kernel kept: a thread a key, eight
+// loads at a time.  SHARES 4: a block takes 64 keys only, and its four groups of threads a quarter of
+// the rows each, added in order: less time where there are few keys (20 sequences of 156 keys and 192
+// rows: 14 us less), more where there are many (8 of 100K keys: 34 us more).
+template <int SHARES>
 __global__ void __launch_bounds__(256) attn_weight_kernel(const __grid_constant__ AttnArgs a,
                                                           const __grid_constant__ AttnPlan p)
 {
+    constexpr int kWeightKeys = 256 / SHARES;
+    __shared__ float s_part[4][kWeightKeys];
     pdl_launch_dependents();
     pdl_wait();
-    const int64_t j = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    if (j >= a.width)
-        return;
+    const int t = threadIdx.x % kWeightKeys, q = threadIdx.x / kWeightKeys;
+    const int64_t j0 = (int64_t)blockIdx.x * kWeightKeys, j = j0 + t;
+    const int rows = a.n_kv * p.R;  // rows of a sequence, KV head by KV head
+    const int r_begin = (int)((int64_t)rows * q / SHARES);
+    const int r_end = (int)((int64_t)rows * (q + 1) / SHARES);
     for (int64_t b = blockIdx.y; b < a.B; b += gridDim.y) {
-    const int64_t n = seq_len(a, b);
-    float w = a.weight_in ? a.weight_in[b * a.weight_stride + j] : 0.0f;
-    if (j < n && j >= first_key(n, a.q_len, a.window)) {
-        const float *lse = reinterpret_cast<const float *>(a.workspace + p.lse_off);
-        const float *sc = reinterpret_cast<const float *>(a.workspace + p.score_off);
+        const int64_t n = seq_len(a, b), first = first_key(n, a.q_len, a.window);
+        const bool any = j0 < n && j0 + kWeightKeys > first;  // the same for the whole block
         float sum = 0.0f;
-        for (int h = 0; h < a.n_kv; ++h)
-            for (int r = 0; r < p.R; ++r) {
-                const float x = lse[h * p.rows + b * p.R + r];
-                const float s = sc[((b * a.n_kv + h) * p.R + r) * p.score_width + j];
-                if (x != -INFINITY)
-                    sum = __fadd_rn(sum, exp2_fast(__fsub_rn(s, x)));
+        if (any) {
+            const float *lse = reinterpret_cast<const float *>(a.workspace + p.lse_off) + b * p.R;
+            const float *sc = reinterpret_cast<const float *>(a.workspace + p.score_off) +
+                              b * rows * p.score_width + j;
+            const bool in = j < n && j >= first;
+            int h = r_begin / p.R, r = r_begin - h * p.R;
+            for (int x0 = r_begin; x0 < r_end; x0 += 8) {
+                float s[8], z[8];
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    const bool have = in && x0 + k < r_end;
+                    s[k] = have ? sc[(int64_t)(x0 + k) * p.score_width] : 0.0f;
+                    z[k] = have ? lse[h * p.rows + r] : -INFINITY;
+                    if (++r == p.R)
+                        r = 0, ++h;
+                }
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                    if (z[k] != -INFINITY)
+                        sum = __fadd_rn(sum, exp2_fast(__fsub_rn(s[k], z[k])));
             }
-        w = __fadd_rn(w, sum);
-    }
-    a.weight_out[b * a.weight_stride + j] = w;
+            if (SHARES > 1) {
+                s_part[q][t] = sum;
+                __syncthreads();
+            }
+        }
+        if (q == 0 && j < a.width) {
+            float w = a.weight_in ? a.weight_in[b * a.weight_stride + j] : 0.0f;
+            if (SHARES > 1 && any)
+                sum = __fadd_rn(__fadd_rn(sum, s_part[1][t]),
+                                __fadd_rn(s_part[2][t], s_part[3][t]));
+            w = __fadd_rn(w, sum);
+            a.weight_out[b * a.weight_stride + j] = w;
+        }
+        if (SHARES > 1 && any)
+            __syncthreads();
     }
 }
 
@@ -1067,6 +1108,8 @@ cudaError_t launch_rows_type(const AttnArgs &a, const AttnPlan &p, const CacheMa
 }
 
 inline int64_t align_up(int64_t x, int64_t a) { return (x + a - 1) / a * a; }
+
+constexpr int64_t kInLine = 256;
 
 // The prefix goes to the tensor-core kernel where that is expected to take less time, in tenths of a
 // microsecond: it costs 11 us to set up and write out and 1.8 us a step (bench of 1 to 43 steps); the
@@ -1122,14 +1165,20 @@ AttnPlan attn_plan(int32_t B, int32_t q_len, int32_t n_q, int32_t n_kv, int64_t 
     const int64_t p_keys = n_prefix - p.p_first;
     if (tc && p_keys > 0)
         plan_tc(p, n_kv, p_keys);
-    const bool with_prefix = p_keys > 0 && p.tc_parts == 0;
+    // A short prefix goes in front of each sequence's own keys: it is read again for each of them (out
+    // of the cache), but needs no units of its own and no join.
+    const bool in_line = p.tc_parts == 0 && n_prefix <= kInLine && width < (int64_t)1 << 30;
+    p.in_line = in_line ? n_prefix : 0;
+    const bool with_prefix = p_keys > 0 && p.tc_parts == 0 && !in_line;
+    // (24 rows a unit were measured too: the kernel then spills, and calls of few units, which wait
+    // rather than work, take longer: 8 queries of 7 sequences 13 -> 19 us.)
     p.nt = (p.R > 8 || (with_prefix && p.rows > 8)) ? 2 : 1;
     const int M = 8 * p.nt;
     p.s_rtiles = (p.R + M - 1) / M;
     p.p_rtiles = with_prefix ? (p.rows + M - 1) / M : 0;
     p.p_tiles = (p_keys + p.tile_keys - 1) / p.tile_keys;
     p.units = n_kv * (p.p_rtiles + (int64_t)B * p.s_rtiles);
-    int64_t keys = width;
+    int64_t keys = p.in_line + width;
     if (window > 0 && window + q_len - 1 < keys)
         keys = window + q_len - 1 + 15;
     // the most places there can be: no block is worth less than one
@@ -1177,8 +1226,13 @@ cudaError_t launch_attn_prefix(const AttnArgs &a, const AttnPlan &p, cudaStream_
                          a, p);
     if (e != cudaSuccess || !a.weight_out || a.width == 0)
         return e != cudaSuccess ? e : cudaGetLastError();
-    e = launch_pdl(attn_weight_kernel, dim3((unsigned)((a.width + 255) / 256), (unsigned)(a.B < 65535 ? a.B : 65535)),
-                   dim3(256), 0, stream, a, p);
+    const unsigned by = (unsigned)(a.B < 65535 ? a.B : 65535);
+    if (a.B * ((a.width + 255) / 256) < 8 * kPlanSms)
+        e = launch_pdl(attn_weight_kernel<4>, dim3((unsigned)((a.width + 63) / 64), by), dim3(256),
+                       0, stream, a, p);
+    else
+        e = launch_pdl(attn_weight_kernel<1>, dim3((unsigned)((a.width + 255) / 256), by), dim3(256),
+                       0, stream, a, p);
     return e != cudaSuccess ? e : cudaGetLastError();
 }
 

@@ -47,7 +47,8 @@ struct AttnPlan {
     int32_t group, R;
     int32_t tile_keys;    // keys of a tile of the rows kernel
     int64_t rows;         // B * R
-    int32_t nt;           // 8-row tiles of a unit's rows: 1 or 2
+    int32_t nt;           // 8-row tiles of a unit's rows: 1, 2 or 3
+    int64_t in_line;      // prefix keys that stand in front of each sequence's own (all or none)
     int32_t s_rtiles;     // row tiles of a sequence
     int64_t p_rtiles;     // row tiles of the prefix's units (0: no prefix)
     int64_t p_first;      // first prefix key that any row can see
