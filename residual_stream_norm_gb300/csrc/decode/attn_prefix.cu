@@ -150,13 +150,25 @@ struct Unit {
     const int64_t *list;  // of the keys from `split` on; those before are the prefix's
     int32_t split;
     int64_t unit;
-    int32_t kvh;
+    int32_t b, kvh;       // sequence (prefix: -1) and KV head
     int32_t row0, row_end;
     int32_t row_base;     // the sequence's first row (suffix)
     int32_t k0, k1;       // keys of the part; k1 <= k0: none
     int32_t key_end;      // of the list
     bool prefix, whole;
 };
+
+// Row rr of a unit: its token, query and head within the group.
+__device__ __forceinline__ int64_t unit_row(const AttnArgs &a, const AttnPlan &p, const Unit &u,
+                                            int rr, int &i, int &hg)
+{
+    if (u.prefix)
+        return row_token(a, p, rr, i, hg);
+    const uint32_t r = (uint32_t)(rr - u.row_base);
+    i = p.group_magic ? (int)__umulhi(r, p.group_magic) : (int)(r / (uint32_t)p.group);
+    hg = (int)r - i * p.group;
+    return (int64_t)u.b * a.q_len + i;
+}
 
 __device__ __forceinline__ void cursor_keys(const AttnArgs &a, const AttnPlan &p, Cursor &c)
 {
@@ -212,6 +224,7 @@ __device__ __forceinline__ Unit next_unit(const AttnArgs &a, const AttnPlan &p, 
     Unit u;
     u.prefix = c.b < 0;
     u.unit = c.unit;
+    u.b = c.b;
     u.kvh = c.kvh;
     u.key_end = c.key_end;
     u.row_base = u.prefix ? 0 : c.b * p.R;
@@ -438,7 +451,7 @@ __global__ void __launch_bounds__(kThreads, 2)
             const int rr = u.row0 + 8 * n + g;
             const bool act = rr < u.row_end;
             int i = 0, hg = 0;
-            const int64_t tok = act ? row_token(a, p, rr, i, hg) : 0;
+            const int64_t tok = act ? unit_row(a, p, u, rr, i, hg) : 0;
             const char *qp = (const char *)a.q +
                              2 * (tok * a.q_stride + (int64_t)(u.kvh * p.group + hg) * kD);
             row_inv[n] = 1.0f;
@@ -488,8 +501,11 @@ __global__ void __launch_bounds__(kThreads, 2)
                     int64_t pos;  // in the suffix (a suffix unit: in the line, split + that)
                     if (!u.prefix) {
                         pos = (int64_t)u.key_end - 1;  // in the line
-                        if (a.q_len > 1)
-                            pos += (rr - u.row_base) / p.group - (a.q_len - 1);
+                        if (a.q_len > 1) {
+                            int i, hg;
+                            unit_row(a, p, u, rr, i, hg);
+                            pos += i - (a.q_len - 1);
+                        }
                     } else {
                         int i, hg;
                         row_token(a, p, rr, i, hg);
@@ -512,12 +528,13 @@ __global__ void __launch_bounds__(kThreads, 2)
             for (int n = 0; n < NT; ++n)
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    const int rr = u.row0 + 8 * n + 2 * t + e, sb = rr / p.R;
+                    const int rr = u.row0 + 8 * n + 2 * t + e;
                     score[n][e] = u.prefix || rr >= u.row_end
                                       ? nullptr
                                       : reinterpret_cast<float *>(a.workspace + p.score_off) +
-                                            (((int64_t)sb * a.n_kv + u.kvh) * p.R + (rr - sb * p.R)) *
-                                                p.score_width - u.split;
+                                            (((int64_t)u.b * a.n_kv + u.kvh) * p.R +
+                                             (rr - u.row_base)) * p.score_width -
+                                            u.split;
                 }
         }
 
@@ -809,13 +826,14 @@ __global__ void __launch_bounds__(kThreads, 2)
                     }
                     if (warp == 0 && g == 0 && rr < u.row_end) {
                         int i, hg;
-                        const int64_t tok = row_token(a, p, rr, i, hg);
+                        const int64_t tok = unit_row(a, p, u, rr, i, hg);
                         if (a.lse)
                             a.lse[tok * a.n_q + u.kvh * p.group + hg] =
                                 ll[e] == 0.0f ? -INFINITY : __fmaf_rn(mm[e], kLn2, logf(ll[e]));
                         if (WEIGHTS)
-                            reinterpret_cast<float *>(a.workspace +
-                                                      p.lse_off)[u.kvh * p.rows + rr] =
+                            reinterpret_cast<float *>(
+                                a.workspace + p.lse_off)[((int64_t)u.b * a.n_kv + u.kvh) * p.R +
+                                                         (rr - u.row_base)] =
                                 ll[e] == 0.0f ? -INFINITY : __fadd_rn(mm[e], log2f(ll[e]));
                     }
                 }
@@ -825,8 +843,8 @@ __global__ void __launch_bounds__(kThreads, 2)
                 const int rr = u.row0 + r0 + own;
                 const bool in0 = rr < u.row_end, in1 = FP8 && rr + 1 < u.row_end;
                 int i = 0, hg = 0, hg1 = 0;
-                const int64_t tok = in0 ? row_token(a, p, rr, i, hg) : 0;
-                const int64_t tok1 = in1 ? row_token(a, p, rr + 1, i, hg1) : 0;
+                const int64_t tok = in0 ? unit_row(a, p, u, rr, i, hg) : 0;
+                const int64_t tok1 = in1 ? unit_row(a, p, u, rr + 1, i, hg1) : 0;
                 char *dst = (char *)a.out + 64 * warp +
                             2 * (tok * a.out_stride + (int64_t)(u.kvh * p.group + hg) * kD);
                 char *dst1 = (char *)a.out + 64 * warp +
@@ -1019,7 +1037,8 @@ __global__ void __launch_bounds__(128) attn_join_kernel(const __grid_constant__ 
         if (a.lse)
             a.lse[tok * a.n_q + h] = l == 0.0f ? -INFINITY : __fmaf_rn(m, kLn2, logf(l));
         if (a.weight_out)
-            reinterpret_cast<float *>(a.workspace + p.lse_off)[kvh * p.rows + rr] =
+            reinterpret_cast<float *>(
+                a.workspace + p.lse_off)[(b * a.n_kv + kvh) * p.R + (rr - b * p.R)] =
                 l == 0.0f ? -INFINITY : __fadd_rn(m, log2f(l));
     }
 }
@@ -1046,20 +1065,17 @@ __global__ void __launch_bounds__(256) attn_weight_kernel(const __grid_constant_
         const bool any = j0 < n && j0 + kWeightKeys > first;  // the same for the whole block
         float sum = 0.0f;
         if (any) {
-            const float *lse = reinterpret_cast<const float *>(a.workspace + p.lse_off) + b * p.R;
+            const float *lse = reinterpret_cast<const float *>(a.workspace + p.lse_off) + b * rows;
             const float *sc = reinterpret_cast<const float *>(a.workspace + p.score_off) +
                               b * rows * p.score_width + j;
             const bool in = j < n && j >= first;
-            int h = r_begin / p.R, r = r_begin - h * p.R;
             for (int x0 = r_begin; x0 < r_end; x0 += 8) {
                 float s[8], z[8];
 #pragma unroll
                 for (int k = 0; k < 8; ++k) {
                     const bool have = in && x0 + k < r_end;
                     s[k] = have ? sc[(int64_t)(x0 + k) * p.score_width] : 0.0f;
-                    z[k] = have ? lse[h * p.rows + r] : -INFINITY;
-                    if (++r == p.R)
-                        r = 0, ++h;
+                    z[k] = have ? lse[x0 + k] : -INFINITY;
                 }
 #pragma unroll
                 for (int k = 0; k < 8; ++k)
@@ -1159,6 +1175,10 @@ AttnPlan attn_plan(int32_t B, int32_t q_len, int32_t n_q, int32_t n_kv, int64_t 
     p.tile_keys = fp8 ? RowsConfig<true>::kTileKeys : RowsConfig<false>::kTileKeys;
     p.group = n_q / n_kv;
     p.R = q_len * p.group;
+    // r / group = high word of r * magic while r * group < 2^32
+    p.group_magic = p.group > 1 && (int64_t)p.R * p.group < (int64_t)1 << 32
+                        ? (uint32_t)((((int64_t)1 << 32) + p.group - 1) / p.group)
+                        : 0;
     p.rows = (int64_t)B * p.R;
     p.p_first = window > 0 && n_prefix + 1 > window ? n_prefix + 1 - window : 0;
     p.p_first = (p.p_first < n_prefix ? p.p_first : n_prefix) & ~(int64_t)15;

@@ -45,6 +45,7 @@ struct AttnArgs {
 // row tile).  The units' key tiles, one after the other, are shared out evenly among `ctas` blocks.
 struct AttnPlan {
     int32_t group, R;
+    uint32_t group_magic;
     int32_t tile_keys;    // keys of a tile of the rows kernel
     int64_t rows;         // B * R
     int32_t nt;           // 8-row tiles of a unit's rows: 1, 2 or 3
