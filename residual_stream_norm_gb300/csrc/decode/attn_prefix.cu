@@ -128,11 +128,12 @@ __device__ __forceinline__ bool stage_has_nonfinite(uint32_t vt, int lane)
     return __any_sync(0xffffffffu, bad);
 }
 
-// Places of each of a sequence's units: its tiles and what it costs besides; none without a key.
+// Places of each of a sequence's units: its tiles and what it costs besides; none without a key (but
+// with whole units these write their rows' zeros).
 __device__ __forceinline__ int64_t seq_places(const AttnArgs &a, const AttnPlan &p, int64_t b)
 {
     const int64_t t = seq_tiles(a, p, b);
-    return t > 0 ? t + kUnitCost : 0;
+    return t > 0 || p.whole ? t + kUnitCost : 0;
 }
 
 // A place in the units' sequence, and the unit that holds it: from unit to unit it only counts on.
@@ -199,6 +200,8 @@ __device__ __forceinline__ Cursor first_cursor(const AttnArgs &a, const AttnPlan
     c.kvh = (int32_t)div32(x, rtiles);
     c.rt = x - c.kvh * rtiles;
     c.unit = x + (b < 0 ? 0 : a.n_kv * (p.p_rtiles + b * p.s_rtiles));
+    if (p.whole && tile > c.start)  // the unit belongs to the share that has its first place
+        c.tile = c.start + c.places;
     return c;
 }
 
@@ -233,7 +236,7 @@ __device__ __forceinline__ Unit next_unit(const AttnArgs &a, const AttnPlan &p, 
     u.split = u.prefix ? 0 : (int32_t)p.in_line;
     u.list = u.prefix ? a.prefix : a.table + c.b * a.table_stride - u.split;
     const int64_t start = c.start + kUnitCost, stop = c.start + c.places;
-    const int64_t seg_end = min(c.end, stop), first = max(c.tile, start);
+    const int64_t seg_end = p.whole ? stop : min(c.end, stop), first = max(c.tile, start);
     u.whole = first == start && seg_end == stop;
     u.k0 = c.key_first + (int32_t)(first - start) * p.tile_keys;
     u.k1 = (int32_t)min((int64_t)u.key_end, c.key_first + (seg_end - start) * p.tile_keys);
@@ -441,7 +444,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     // ---- the units of the share ----------------------------------------------------------------
     while (at.tile < at.end) {
         const Unit u = next_unit(a, p, M, at);
-        if (u.k1 <= u.k0)
+        if (u.k1 <= u.k0 && !p.whole)
             continue;
         // query fragments (columns g), and the rows' scale and keys (columns 2t, 2t + 1)
         uint32_t qf[NT][8][2];
@@ -1201,6 +1204,10 @@ AttnPlan attn_plan(int32_t B, int32_t q_len, int32_t n_q, int32_t n_kv, int64_t 
     int64_t keys = p.in_line + width;
     if (window > 0 && window + q_len - 1 < keys)
         keys = window + q_len - 1 + 15;
+    // Units that are not split need no join: where none has more than one tile, or where there are so
+    // many that shares of whole units are even enough.
+    p.whole = p.p_rtiles == 0 && p.tc_parts == 0 &&
+              (keys + 15 <= p.tile_keys || p.units >= 12 * kPlanSms);
     // the most places there can be: no block is worth less than one
     const int64_t tiles =
         n_kv * (p.p_rtiles * (p.p_tiles + kUnitCost) +
@@ -1240,7 +1247,10 @@ cudaError_t launch_attn_prefix(const AttnArgs &a, const AttnPlan &p, cudaStream_
     if (e != cudaSuccess)
         return e;
     const int64_t rows = p.rows * a.n_kv;
-    e = rows < kPlanSms * 8
+    if (p.whole)
+        e = cudaSuccess;
+    else
+        e = rows < kPlanSms * 8
             ? launch_pdl(attn_join_kernel<4>, dim3((unsigned)rows), dim3(128), 0, stream, a, p)
             : launch_pdl(attn_join_kernel<1>, dim3((unsigned)((rows + 3) / 4)), dim3(128), 0, stream,
                          a, p);

@@ -79,6 +79,13 @@ __device__ __forceinline__ void load64(uint32_t addr, float (&r)[64])
         : "memory");
 }
 
+__device__ __forceinline__ float max3(float a, float b, float c)
+{
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+
 // Puts zeros in the place of the infinite and NaN values of a tile; 128 threads.  Whether this thread
 // found one.
 template <bool F16>
@@ -319,16 +326,16 @@ __global__ void __launch_bounds__(TcConfig<FP8, SPLIT>::kThreads, 1)
             load64(s_at, r);
             hide(r, mask[0], mask[1], 0, from);
 #pragma unroll
-            for (int c = 0; c < 64; c += 2) {
-                mx0 = fmaxf(mx0, r[c]);
-                mx1 = fmaxf(mx1, r[c + 1]);
+            for (int c = 0; c < 64; c += 4) {
+                mx0 = max3(mx0, r[c], r[c + 1]);
+                mx1 = max3(mx1, r[c + 2], r[c + 3]);
             }
             load64(s_at + 64, r);
             hide(r, mask[2], mask[3], 64, from);
 #pragma unroll
-            for (int c = 0; c < 64; c += 2) {
-                mx0 = fmaxf(mx0, r[c]);
-                mx1 = fmaxf(mx1, r[c + 1]);
+            for (int c = 0; c < 64; c += 4) {
+                mx0 = max3(mx0, r[c], r[c + 1]);
+                mx1 = max3(mx1, r[c + 2], r[c + 3]);
             }
             const float mx = __fmul_rn(fmaxf(mx0, mx1), scale);
             const bool raise = mx > __fadd_rn(m, kRaise);
@@ -354,6 +361,7 @@ __global__ void __launch_bounds__(TcConfig<FP8, SPLIT>::kThreads, 1)
                 }
             }
             const float neg = m == -INFINITY ? 0.0f : -m;
+            const f2 scale2 = splat(scale), neg2 = splat(neg);
             f2 sum = 0ull;
 #pragma unroll
             for (int h = 1; h >= 0; --h) {  // the second half is in registers and makes room first
@@ -364,8 +372,8 @@ __global__ void __launch_bounds__(TcConfig<FP8, SPLIT>::kThreads, 1)
                 uint32_t w[32];
 #pragma unroll
                 for (int c = 0; c < 32; ++c) {
-                    const float e0 = exp2_fast(__fmaf_rn(r[2 * c], scale, neg));
-                    const float e1 = exp2_fast(__fmaf_rn(r[2 * c + 1], scale, neg));
+                    const f2 x = fma2(make_f2(r[2 * c], r[2 * c + 1]), scale2, neg2);
+                    const float e0 = exp2_fast(lo_of(x)), e1 = exp2_fast(hi_of(x));
                     sum = add2(sum, make_f2(e0, e1));
                     w[c] = FP8 ? pack_f16x2(e0, e1) : pack_bf16x2(e0, e1);
                 }

@@ -56,6 +56,7 @@ struct AttnPlan {
     int64_t p_tiles;      // key tiles of a prefix unit
     int64_t units;        // all units
     int32_t ctas;
+    bool whole;           // shares are of whole units: the rows kernel writes every result itself
     // the tensor-core kernel (tc_parts 0: not used): tiles of rows, blocks along the keys, steps of a
     // block (128 keys; 256 with tc_split), and parts that it leaves of each row
     int32_t tc_rtiles, tc_blocks, tc_steps, tc_parts;
