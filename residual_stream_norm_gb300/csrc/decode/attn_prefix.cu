@@ -936,7 +936,7 @@ __global__ void __launch_bounds__(128) attn_join_kernel(const __grid_constant__ 
     const int64_t places = div32(c1b - c0b, per_seq), tb = places - kUnitCost;
     // the parts of the prefix unit, then those of the suffix unit, then the tensor-core kernel's
     int64_t first[3] = {0, 0, 0};
-    int at[3] = {0, 0, 0}, count[3] = {0, 0, 0};  // row of part c: (first + c) * M + at
+    int at[2] = {0, 0}, count[3] = {0, 0, 0};
     if (p.p_rtiles > 0) {
         const int64_t unit = kvh * p.p_rtiles + rr / M;
         const int64_t s = unit * (p.p_tiles + kUnitCost) + kUnitCost;
@@ -960,50 +960,54 @@ __global__ void __launch_bounds__(128) attn_join_kernel(const __grid_constant__ 
     const float *tpo = reinterpret_cast<const float *>(a.workspace + p.tc_o_off);
     first[2] = x * p.tc_parts;
     count[2] = p.tc_parts;
+    const int c01 = count[0] + count[1], parts = c01 + count[2];
+    // where part c's row lies among its kernel's parts
+    auto row_of = [&](int c) {
+        return c < count[0] ? (first[0] + c) * M + at[0]
+               : c < c01    ? (first[1] + c - count[0]) * M + at[1]
+                            : first[2] + c - c01;
+    };
     float m = -INFINITY, l = 0.0f;
     float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    constexpr int kLoads = WARPS == 1 ? 4 : 8;  // at a time
+    const int begin = parts * sub / WARPS, end = parts * (sub + 1) / WARPS;  // this warp's parts
+    for (int c0 = begin; c0 < end; c0 += 32) {
+        const int n = min(32, end - c0);
+        float2 w = make_float2(-INFINITY, 0.0f);
+        if (lane < n)
+            w = (c0 + lane < c01 ? ml : tml)[row_of(c0 + lane)];
+        // a part that saw nothing adds nothing, whatever its sums hold
+        float mx = w.y == 0.0f ? -INFINITY : w.x;
 #pragma unroll
-    for (int k = 0; k < 3; ++k) {
-        for (int c0 = 32 * sub; c0 < count[k]; c0 += 32 * WARPS) {
-            const int n = min(32, count[k] - c0);
-            const int64_t r0 = k == 2 ? first[2] + c0 : (first[k] + c0) * M + at[k];
-            const int step = k == 2 ? 1 : M;
-            float2 w = make_float2(-INFINITY, 0.0f);
-            if (lane < n)
-                w = (k == 2 ? tml : ml)[r0 + lane * step];
-            // a part that saw nothing adds nothing, whatever its sums hold
-            float mx = w.y == 0.0f ? -INFINITY : w.x;
+        for (int off = 16; off > 0; off >>= 1)
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
+        const float mn = fmaxf(m, mx), ms = mn == -INFINITY ? 0.0f : mn;
+        const float f0 = exp2_fast(__fsub_rn(m, ms));
+        const float f = w.y == 0.0f ? 0.0f : exp2_fast(__fsub_rn(w.x, ms));
+        m = mn;
+        float ls = __fmul_rn(f, w.y);
 #pragma unroll
-            for (int off = 16; off > 0; off >>= 1)
-                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
-            const float mn = fmaxf(m, mx), ms = mn == -INFINITY ? 0.0f : mn;
-            const float f0 = exp2_fast(__fsub_rn(m, ms));
-            const float f = w.y == 0.0f ? 0.0f : exp2_fast(__fsub_rn(w.x, ms));
-            m = mn;
-            float ls = __fmul_rn(f, w.y);
+        for (int off = 16; off > 0; off >>= 1)
+            ls = __fadd_rn(ls, __shfl_xor_sync(0xffffffffu, ls, off));
+        l = __fmaf_rn(l, f0, ls);
+        o.x = __fmul_rn(o.x, f0), o.y = __fmul_rn(o.y, f0);
+        o.z = __fmul_rn(o.z, f0), o.w = __fmul_rn(o.w, f0);
+        const uint32_t live = __ballot_sync(0xffffffffu, lane < n && w.y != 0.0f);
+        for (int c = 0; c < n; c += kLoads) {
+            float4 v[kLoads];
 #pragma unroll
-            for (int off = 16; off > 0; off >>= 1)
-                ls = __fadd_rn(ls, __shfl_xor_sync(0xffffffffu, ls, off));
-            l = __fmaf_rn(l, f0, ls);
-            o.x = __fmul_rn(o.x, f0), o.y = __fmul_rn(o.y, f0);
-            o.z = __fmul_rn(o.z, f0), o.w = __fmul_rn(o.w, f0);
-            const uint32_t live = __ballot_sync(0xffffffffu, lane < n && w.y != 0.0f);
-            const float *src = (k == 2 ? tpo : po) + r0 * kD + 4 * lane;
-            for (int c = 0; c < n; c += 8) {
-                float4 v[8];
+            for (int j = 0; j < kLoads; ++j)
+                v[j] = (live >> (c + j)) & 1u
+                           ? *reinterpret_cast<const float4 *>(
+                                 (c0 + c + j < c01 ? po : tpo) + row_of(c0 + c + j) * kD + 4 * lane)
+                           : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    v[j] = (live >> (c + j)) & 1u
-                               ? *reinterpret_cast<const float4 *>(src + (int64_t)(c + j) * step * kD)
-                               : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const float fj = __shfl_sync(0xffffffffu, f, (c + j) & 31);
-                    o.x = __fmaf_rn(fj, v[j].x, o.x);
-                    o.y = __fmaf_rn(fj, v[j].y, o.y);
-                    o.z = __fmaf_rn(fj, v[j].z, o.z);
-                    o.w = __fmaf_rn(fj, v[j].w, o.w);
-                }
+            for (int j = 0; j < kLoads; ++j) {
+                const float fj = __shfl_sync(0xffffffffu, f, (c + j) & 31);
+                o.x = __fmaf_rn(fj, v[j].x, o.x);
+                o.y = __fmaf_rn(fj, v[j].y, o.y);
+                o.z = __fmaf_rn(fj, v[j].z, o.z);
+                o.w = __fmaf_rn(fj, v[j].w, o.w);
             }
         }
     }
