@@ -5,10 +5,18 @@
 // by exp(m - m').  Parts of a list join by the same rule.  Exponents are taken to base 2, scores
 // carry the factor log2(e).
 //
-// Rows kernel: a warp works on 16 keys at a time for 8 or 16 query rows of one KV head.  It computes
-// the transposed products S^T = K Q^T and O^T = V^T P^T, so that the keys fill the 16 rows of the
-// matrix instruction and the few query rows its 8 columns.  Each warp copies its own keys into its own
-// stages (TMA gathers of four slots' rows each), so warps meet only when their parts are joined.
+// Rows kernel (every sequence's own keys; the prefix where that is little work): a warp works on 16 keys
+// (FP8: 32) at a time for 8 or 16 query rows of one KV head.  It computes the transposed products
+// S^T = K Q^T and O^T = V^T P^T, so that the keys fill the 16 rows of the matrix instruction and the few
+// query rows its 8 columns; the 128-row tiles of tcgen05 would stay nearly empty, and the matrix pipe
+// is 8 to 14% busy as it is.  Each warp copies its own keys into its own three stages (TMA, by slot),
+// two steps ahead and on across the units, so warps meet only when their parts are joined; one warp
+// copying for four took twice the time (106 -> 196 us below).
+//
+// What bounds it: the keys' and values' bytes.  8 sequences of 16-20K keys take 104 us for 586 MB
+// (5.6 TB/s, 0.83 of the copy rate), FP8 with twice the keys 110 us; where lists are short, what each
+// unit costs besides its keys.  Any order of lists is shared out evenly by the device itself: the
+// lengths are not known to the host, and one long list among short ones must not hold the call up.
 
 #include "attn_common.cuh"
 #include "decode_mma.cuh"
@@ -910,8 +918,9 @@ __global__ void __launch_bounds__(kThreads, 2)
 }
 
 // Joins a row's parts: WARPS warps a row and KV head, which share out the parts; a lane has four
-// elements.  Many parts mean few rows: four warps then.  A warp looks at 32 parts' maxima and sums at
-// a time, a lane each, and its loads of the parts do not wait for one another.
+// elements.  Few rows have many parts: four warps then (a sequence of 2047 keys in 32 parts: 10.2 us
+// for the call; part after part it took 15.5).  A warp looks at 32 parts' maxima and sums at a time, a
+// lane each, and its loads of the parts do not wait for one another.
 template <int WARPS>
 __global__ void __launch_bounds__(128) attn_join_kernel(const __grid_constant__ AttnArgs a,
                                                         const __grid_constant__ AttnPlan p)

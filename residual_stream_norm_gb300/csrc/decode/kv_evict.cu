@@ -3,8 +3,12 @@
 // The smallest weight that stays is found by radix selection on order-preserving integer keys: digits
 // of 11, 11 and 10 bits from the top, each a histogram of the keys that still match, until what is left
 // of the row is decided.  One ordered pass then moves what stays to the row's front and lists what
-// leaves.  A block reads its weights once, into shared memory; what bounds the operator is then the
-// move: 12 bytes read and 12 written for every entry.
+// leaves.  A block reads its weights once, into shared memory.
+//
+// What bounds it: 72 rows of ~100K entries take 57 us (3.1 TB/s; floor 26 us), about 22 us of them the
+// move at the memory's rate and the rest reading and the three digits' histograms, whose atomics and
+// instructions two blocks a row cannot hide behind the move; one row of 2K takes 7.1 us, a chain of
+// some fifteen block barriers.
 //
 // One block a row; a cluster shares out long rows when there are few (histograms and counts meet in
 // distributed shared memory).  Each warp counts what stays of a stretch of its own, and from the sums

@@ -9,8 +9,13 @@
 // well and joins its sums through distributed shared memory, in order, so no workspace is needed and
 // results do not depend on timing.
 //
-// What bounds it: the weights' bytes from memory; beside them the x fragments (R rows share each
-// copy of x, and MTW row tiles each fragment) and, from 32 tokens on, the matrix pipe.
+// Measured: 1 token, 6144 x 5120: 10.2 us (floor 2.4 us; six steps a block, then two cluster barriers:
+// latency); 8 tokens, 5120 x 14336: 15.1 us (2.7 TB/s); 32 tokens, 5120 x 40960, groups of 32: 78 us.
+// What bounds the larger ones is not the weights' bytes but the integer pipe: unpacking takes 2.75
+// instructions a pair of weights (shift, mask with the 128 that makes it a BF16 number, exact
+// subtraction of 128 + z), and 32 tokens add the fragments of x and the scaling of each group's sums.
+// Row tiles of 32 to 256 rows a block, 2 to 6 stages and other shares of rows and k between the warps
+// were measured: within 1% or slower.
 
 #include "beam_f32x2.cuh"
 #include "decode_kernels.h"
