@@ -9,7 +9,8 @@
  * is launched, calls asynchronous on `stream`, programmatic dependent launch.  Model parameters
  * (4-bit weights, scales, zeros) may be read before the preceding kernel of the stream has ended;
  * everything else is read, and every output written, only after it.  Calls on different streams
- * need workspaces of their own.
+ * need workspaces of their own.  Waits inside the kernels are bounded; beam_device_faults() also
+ * reports one that ran out, after which the call's outputs are not to be used.
  */
 #ifndef BEAM_DECODE_H
 #define BEAM_DECODE_H
@@ -30,7 +31,7 @@ extern "C" {
  * The keys of sequence b, in order, are the n_prefix slots prefix_slots[0..n_prefix) that all
  * sequences share and the suffix slots slot_table[b, 0..len_b), len_b = suffix_len[b] limited to
  * [0, table_width]: the sequence's own tokens, the q_len query tokens last.  Prefix keys and values
- * are read once for the whole batch.
+ * are read once for the whole batch (a prefix of up to 256 keys: once a sequence, out of the L2 cache).
  *
  * Query i of sequence b (row t = b*q_len + i) stands at suffix index p = len_b - q_len + i.  A row
  * with p < 0 is padding: it sees nothing.  Others see suffix keys j <= p with p - j < window and

@@ -11,7 +11,7 @@
 // query rows its 8 columns; the 128-row tiles of tcgen05 would stay nearly empty, and the matrix pipe
 // is 8 to 14% busy as it is.  Each warp copies its own keys into its own three stages (TMA, by slot),
 // two steps ahead and on across the units, so warps meet only when their parts are joined; one warp
-// copying for four took twice the time (106 -> 196 us below).
+// copying for four took twice the time (104 -> 196 us for the sequences below).
 //
 // What bounds it: the keys' and values' bytes.  8 sequences of 16-20K keys take 104 us for 586 MB
 // (5.6 TB/s, 0.83 of the copy rate), FP8 with twice the keys 110 us; where lists are short, what each
@@ -918,8 +918,8 @@ __global__ void __launch_bounds__(kThreads, 2)
 }
 
 // Joins a row's parts: WARPS warps a row and KV head, which share out the parts; a lane has four
-// elements.  Few rows have many parts: four warps then (a sequence of 2047 keys in 32 parts: 10.2 us
-// for the call; part after part it took 15.5).  A warp looks at 32 parts' maxima and sums at a time, a
+// elements.  Few rows have many parts: four warps then (a sequence of 2047 keys, the whole call:
+// 15.5 -> 11.9 us with these loads and four warps).  A warp looks at 32 parts' maxima and sums at a time, a
 // lane each, and its loads of the parts do not wait for one another.
 template <int WARPS>
 __global__ void __launch_bounds__(128) attn_join_kernel(const __grid_constant__ AttnArgs a,
@@ -1141,6 +1141,9 @@ cudaError_t launch_rows_type(const AttnArgs &a, const AttnPlan &p, const CacheMa
 
 inline int64_t align_up(int64_t x, int64_t a) { return (x + a - 1) / a * a; }
 
+// Up to so many prefix keys stand in line with each sequence's own and are read again for each, out of
+// the cache; more are units of their own, joined later.  In line: 96 sequences of 4 query rows behind 10
+// keys 58.7 -> 45.8 us, 57 of 2 behind 80 keys 18.9 -> 13.1.  The limit itself was not swept.
 constexpr int64_t kInLine = 256;
 
 // The prefix goes to the tensor-core kernel where that is expected to take less time, in tenths of a
@@ -1218,7 +1221,8 @@ AttnPlan attn_plan(int32_t B, int32_t q_len, int32_t n_q, int32_t n_kv, int64_t 
     if (window > 0 && window + q_len - 1 < keys)
         keys = window + q_len - 1 + 15;
     // Units that are not split need no join: where none has more than one tile, or where there are so
-    // many that shares of whole units are even enough.
+    // many that shares of whole units are even enough.  Against split units: 14 sequences of 3 tokens
+    // 13.2 -> 10.1 us, 21 of at most 53 keys with weights 12.7 -> 10.9.  The 12 was not swept.
     p.whole = p.p_rtiles == 0 && p.tc_parts == 0 &&
               (keys + 15 <= p.tile_keys || p.units >= 12 * kPlanSms);
     // the most places there can be: no block is worth less than one

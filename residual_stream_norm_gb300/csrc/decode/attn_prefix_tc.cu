@@ -9,8 +9,8 @@
 //
 // What bounds it: for 768 rows and 32K keys it takes 80 us (1.29 PFLOP/s, tensor pipe 52% busy).  A step
 // (two products of 128 x 128 x 128 for each half) takes about 3450 cycles, of which the products need
-// 2180 at the full rate.  Q K^T runs slower than that: its instructions read 8 KB of shared memory
-// each, which is the shared memory's full rate, while the copies write 64 KB a step beside them; and
+// 2180 at the full rate.  In a trace Q K^T's eight instructions take 890 of them and P V's 540; the likely
+// reason is that the former read both operands from shared memory, which the copies write as well; and
 // a half's next scores must wait until its weights, which lie in their place, have been used.  FP8: the
 // expansion to FP16 shares the shared memory too (3900 cycles a step).  Alone, a block costs about
 // 11 us to set up and write out, so few rows or keys go to the rows kernel.

@@ -10,12 +10,14 @@
 // results do not depend on timing.
 //
 // Measured: 1 token, 6144 x 5120: 10.2 us (floor 2.4 us; six steps a block, then two cluster barriers:
-// latency); 8 tokens, 5120 x 14336: 15.1 us (2.7 TB/s); 32 tokens, 5120 x 40960, groups of 32: 78 us.
-// What bounds the larger ones is not the weights' bytes but the integer pipe: unpacking takes 2.75
+// latency); 8 tokens, 5120 x 14336: 15.1 us with the weights in the L2
+// cache, 19.3 from memory; 32 tokens, 5120 x 40960, groups of 32: 78 us.
+// What bounds the larger ones is not the weights' bytes but instructions (53 to 58% of the issue slots,
+// warps held up by the arithmetic pipe): unpacking takes 2.75
 // instructions a pair of weights (shift, mask with the 128 that makes it a BF16 number, exact
 // subtraction of 128 + z), and 32 tokens add the fragments of x and the scaling of each group's sums.
-// Row tiles of 32 to 256 rows a block, 2 to 6 stages and other shares of rows and k between the warps
-// were measured: within 1% or slower.
+// Rows a block: 1 token 64: 10.2, 32: 11.4, 128: 11.2 us; 8 tokens 15.1, 16.4, 21.0; 32 tokens 128: 77.5,
+// 64: 85, 256: 118.  Copies further ahead: equal or slower.
 
 #include "beam_f32x2.cuh"
 #include "decode_kernels.h"
