@@ -1061,14 +1061,17 @@ __global__ void __launch_bounds__(128) attn_join_kernel(const __grid_constant__ 
 
 // The weight each suffix key received, out of the scores that the rows kernel kept: a thread a key, eight
 // loads at a time.  SHARES 4: a block takes 64 keys only, and its four groups of threads a quarter of
-// the rows each, added in order: less time where there are few keys (20 sequences of 156 keys and 192
-// rows: 14 us less), more where there are many (8 of 100K keys: 34 us more).
+// the rows each, added in order: less time where few keys can have a weight (20 sequences of 156 keys
+// and 192 rows: 14 us less; a window of 512 in 15 tables of 31,918: 90 -> 70 us for the call), more where
+// many can (8 of 100K keys: 34 us more).  SHARES 8, 32 keys a block, where the tables have few blocks: 10
+// of 3,407 keys 42.2 -> 38.6 us for the call, 15 of 1,410 keys 47.9 -> 43.9; for 32 of 4,096 keys 140.5 ->
+// 142.5, for 15 of 31,918 69.8 -> 71.7, so not there.
 template <int SHARES>
 __global__ void __launch_bounds__(256) attn_weight_kernel(const __grid_constant__ AttnArgs a,
                                                           const __grid_constant__ AttnPlan p)
 {
     constexpr int kWeightKeys = 256 / SHARES;
-    __shared__ float s_part[4][kWeightKeys];
+    __shared__ float s_part[SHARES][kWeightKeys];
     pdl_launch_dependents();
     pdl_wait();
     const int t = threadIdx.x % kWeightKeys, q = threadIdx.x / kWeightKeys;
@@ -1106,8 +1109,9 @@ __global__ void __launch_bounds__(256) attn_weight_kernel(const __grid_constant_
         if (q == 0 && j < a.width) {
             float w = a.weight_in ? a.weight_in[b * a.weight_stride + j] : 0.0f;
             if (SHARES > 1 && any)
-                sum = __fadd_rn(__fadd_rn(sum, s_part[1][t]),
-                                __fadd_rn(s_part[2][t], s_part[3][t]));
+#pragma unroll
+                for (int k = 1; k < SHARES; ++k)
+                    sum = __fadd_rn(sum, s_part[k][t]);
             w = __fadd_rn(w, sum);
             a.weight_out[b * a.weight_stride + j] = w;
         }
@@ -1274,7 +1278,13 @@ cudaError_t launch_attn_prefix(const AttnArgs &a, const AttnPlan &p, cudaStream_
     if (e != cudaSuccess || !a.weight_out || a.width == 0)
         return e != cudaSuccess ? e : cudaGetLastError();
     const unsigned by = (unsigned)(a.B < 65535 ? a.B : 65535);
-    if (a.B * ((a.width + 255) / 256) < 8 * kPlanSms)
+    int64_t keys = a.width;  // that can have a weight
+    if (a.window > 0 && (int64_t)a.window + a.q_len - 1 < keys)
+        keys = (int64_t)a.window + a.q_len - 1;
+    if (a.B * ((a.width + 255) / 256) < 2 * kPlanSms)
+        e = launch_pdl(attn_weight_kernel<8>, dim3((unsigned)((a.width + 31) / 32), by), dim3(256),
+                       0, stream, a, p);
+    else if (a.B * ((keys + 255) / 256) < 8 * kPlanSms)
         e = launch_pdl(attn_weight_kernel<4>, dim3((unsigned)((a.width + 63) / 64), by), dim3(256),
                        0, stream, a, p);
     else
