@@ -136,9 +136,9 @@ __global__ void __launch_bounds__(kW4Threads, NT >= 4 ? 2 : 3)
                        in ? 16u : 0u);
         }
     };
-    // Scales and zeros of the window that starts with step s (a multiple of four).  Rows that start on 16 bytes are copied
-    // a window ahead and then unpacked; others are loaded when they are needed, which costs their
-    // latency once a window.
+    // Scales and zeros of the window that starts with step s (a multiple of four).  Rows that start on 16
+    // bytes are copied while the window before is worked on and then unpacked; others are loaded when
+    // they are needed, which costs their latency once a window.
     const bool ahead_ok = groups % 16 == 0 && (uint64_t)a.scales % 16 == 0 &&
                           (!a.zeros || (uint64_t)a.zeros % 16 == 0);
     const uint32_t raw_s = base + C::kMain, raw_z = raw_s + R * kWin * 2;
@@ -219,7 +219,18 @@ __global__ void __launch_bounds__(kW4Threads, NT >= 4 ? 2 : 3)
     int stage = 0, ahead = ST - 1;
     bool fresh = ahead_ok;  // the window's parameters are there, but not unpacked
     for (int s = s0; s < s1; ++s) {
-        cp_async_wait<ST - 2>();
+        // Step i of the block (from 0) finds ST - 1 + i groups committed and needs the first i + 1, the
+        // weights' and x's of its own: all but the newest ST - 2.  The second window's scales and
+        // zeros are in group ST - 1 (from 0), with the copies that step 0 issues.  A block whose
+        // share starts on step s0 % 4 of a window needs them in step 4 - s0 % 4, which with four
+        // stages covers group 4 for s0 % 4 = 0 and 3 for 1, but only 2 for 2 and 1 for 3: there
+        // everything is waited for.  Later windows are copied four steps ahead.  (A second buffer
+        // instead of the wait: equal times, but 9 to 16 tokens in groups of 64 then fit one block an SM,
+        // 5120 -> 14336 25.6 -> 35.2 us.)
+        if (ST > 2 && s - win == kWindow / kStep && s - s0 < ST - 1)
+            cp_async_wait<0>();
+        else
+            cp_async_wait<ST - 2>();
         __syncthreads();
         if (s - win == kWindow / kStep)
             win = s, fresh = true;

@@ -103,3 +103,34 @@ def test_no_tokens():
                            torch.empty((0, 64), dtype=torch.bfloat16, device="cuda"), w.cuda(),
                            s.cuda(), group=32)
     torch.cuda.synchronize()
+
+
+# 10 to 44 steps of 256 columns shared out over clusters of 1, 2, 4 and 8 blocks, so that shares start on
+# every step of a window of 1024 columns
+@pytest.mark.parametrize("T", [1, 8, 16])
+@pytest.mark.parametrize("N,K,group,zeros", [
+    (5120, 6144, 128, False), (14336, 5120, 64, True), (3584, 5120, 64, True),
+    (7000, 5632, 32, True), (29000, 2560, 32, True), (130, 11264, 64, False)])
+def test_windows_of_scales_from_memory(N, K, group, zeros, T):
+    # Scales and zeros that differ from window to window: those of another window give another
+    # result.  Everything is read from memory, which a buffer larger than the L2 cache sees to.
+    lib()
+    x, w, s, z = make(T, N, K, group, zeros, seed=N + T)
+    window = torch.arange(K // group) * group // 1024
+    s = (s.float() * 2.0 ** (window % 5 * 2 - 4)[None]).bfloat16()
+    if zeros:
+        z = ((z + 5 * window[None]) % 16).to(torch.uint8)
+    want, tol = ref.w4_matvec(x, w, s, z, group)
+    xd, wd, sd = x.cuda(), w.cuda(), s.cuda()
+    zd = None if z is None else z.cuda()
+    flush = torch.empty(2 ** 28, dtype=torch.uint8, device="cuda")
+    first = None
+    for i in range(6):
+        y = torch.full((T, N), float("nan"), dtype=torch.bfloat16, device="cuda")
+        flush.fill_(i)
+        rsn.beam_w4_matvec_fwd(y, xd, wd, sd, zd, group=group)
+        if first is None:
+            first = y
+            d = (y.cpu().double() - want).abs()
+            assert bool((d <= tol).all()), f"worst {float((d - tol).max()):.3g} past the bound"
+        assert torch.equal(y, first)
