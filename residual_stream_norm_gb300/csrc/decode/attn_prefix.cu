@@ -328,11 +328,10 @@ __global__ void __launch_bounds__(kThreads, 2)
     }
     __syncwarp();
     pdl_launch_dependents();
-    // Behind the tensor-core kernel, whose blocks let this one start only after their own wait, and
-    // whose results it does not read, the wait moves to the end: the two overlap, and the join that
-    // follows still finds both complete.
-    if (p.tc_parts == 0)
-        pdl_wait();
+    // Behind the tensor-core kernel too, whose results it does not read: what earlier kernels wrote
+    // (lengths, table, queries, cache) is visible to the grid that waits, not to one that is merely
+    // started by a grid that has waited.
+    pdl_wait();
 
     // ---- the share of this block ---------------------------------------------------------------
     const int64_t p_units = a.n_kv * p.p_rtiles;
@@ -343,11 +342,8 @@ __global__ void __launch_bounds__(kThreads, 2)
                                          own, own_end);
     const int64_t shares = min((int64_t)p.ctas, total);  // none of them empty
     __syncthreads();
-    if (blockIdx.x >= shares || *s_fail) {
-        if (p.tc_parts > 0)
-            pdl_wait();
+    if (blockIdx.x >= shares || *s_fail)
         return;
-    }
     const int64_t tile0 = div32(total * blockIdx.x, shares);
     int64_t b0 = -1, b0_start = 0;
     if (tile0 >= p_total) {
@@ -913,8 +909,6 @@ __global__ void __launch_bounds__(kThreads, 2)
         while (global_ns() - t0 < kWaitLimitNs / 4) {
         }
     }
-    if (p.tc_parts > 0)
-        pdl_wait();
 }
 
 // Joins a row's parts: WARPS warps a row and KV head, which share out the parts; a lane has four

@@ -221,8 +221,8 @@ __global__ void __launch_bounds__(TcConfig<FP8, SPLIT>::kThreads, 1)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *s_tmem;
+    pdl_launch_dependents();
     pdl_wait();
-    pdl_launch_dependents();  // after the wait: the next kernel then need not wait before it starts
 
     if (warp < 8 && !*s_fail) {
         // ---- softmax: a row a thread -------------------------------------------------------------

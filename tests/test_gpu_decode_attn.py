@@ -374,3 +374,78 @@ def test_zero_sequences():
         e((0, 4), dtype=torch.int64, device="cuda"), e((0,), dtype=torch.int32, device="cuda"),
         e((1,), dtype=torch.uint8, device="cuda"))
     torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("graph", [False, True])
+def test_right_behind_the_kernels_that_write_its_inputs(graph, fp8):
+    # a long prefix for many rows; Q/K norm writes the queries and the newest keys and values, eviction the
+    # table, lengths and weights, and attention follows at once
+    lib()
+    B, n_q, n_kv, P, width, budget = 25, 48, 8, 3000, 9, 6
+    g = torch.Generator().manual_seed(16)
+    ks, vs = (0.05, 0.03) if fp8 else (1.0, 1.0)
+    S = P + B * width
+    perm = torch.randperm(S, generator=g)
+    prefix, own = perm[:P].cuda(), perm[P:].view(B, width).cuda()
+    caches = []
+    for scale in (ks, vs):
+        x = torch.randn((S, n_kv, D), generator=g)
+        x = (x / scale).to(torch.float8_e4m3fn).view(torch.uint8) if fp8 else x.bfloat16()
+        caches.append(x.cuda())
+    k, v = caches
+    wq, wk = (torch.ones(D, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    pos = torch.full((B,), P + width - 1, dtype=torch.int64, device="cuda")
+    tokens = torch.randn((4, B, n_q + 2 * n_kv, D), generator=g).bfloat16().cuda()
+    weights = torch.rand((4, B, width), generator=g).cuda()
+    qkv, w = torch.empty_like(tokens[0]), torch.empty_like(weights[0])
+    q, k_new, v_new = qkv[:, :n_q], qkv[:, n_q:n_q + n_kv], qkv[:, n_q + n_kv:]
+    slots = own[:, -1].contiguous()
+    table, lens = own.clone(), torch.full((B,), width, dtype=torch.int32, device="cuda")
+    freed = torch.empty((B, width - budget), dtype=torch.int64, device="cuda")
+    out = torch.empty((B, n_q, D), dtype=torch.bfloat16, device="cuda")
+    lse = torch.empty((B, n_q), dtype=torch.float32, device="cuda")
+    ws = torch.empty(rsn.beam_attn_prefix_workspace(B, 1, n_q, n_kv, P, width, key_weights=True),
+                     dtype=torch.uint8, device="cuda")
+    kind = rsn.CACHE_FP8_E4M3 if fp8 else rsn.CACHE_BF16
+
+    def attend(out, lse, w_in, w_out):
+        rsn.beam_attn_prefix_fwd(out, q, k, v, prefix, table, lens, ws, cache_dtype=kind, k_scale=ks,
+                                 v_scale=vs, lse_out=lse, key_weight_in=w_in, key_weight_out=w_out)
+
+    def steps():
+        rsn.beam_kv_evict_fwd(table, lens, w, freed, table, lens, w, budget, 2)
+        rsn.beam_qk_norm_ssmax_kv_fwd(q, k_new, v_new, wq, wk, pos, slots, k, v, cache_dtype=kind,
+                                      k_scale=ks, v_scale=vs)
+        attend(out, lse, w, w)
+
+    def inputs(i):
+        qkv.copy_(tokens[i])
+        w.copy_(weights[i])
+        table.copy_(own)
+        lens.fill_(width)
+
+    if graph:
+        inputs(0)
+        steps()
+        torch.cuda.synchronize()
+        captured = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(captured):
+            steps()
+    for i in range(4):
+        inputs(i)
+        captured.replay() if graph else steps()
+        torch.cuda.synchronize()
+        # what the writers left, and attention over it once more, by itself
+        kept, n, w0, _ = ref.evict(own.cpu().numpy(), [width] * B, weights[i].cpu().numpy(), budget, 2,
+                                   width - budget)
+        w0 = torch.from_numpy(w0)
+        assert torch.equal(table.cpu(), torch.from_numpy(kept)) and bool((lens == budget).all())
+        again = [torch.empty_like(x) for x in (out, lse, w)]
+        attend(again[0], again[1], w0.cuda(), again[2])
+        torch.cuda.synchronize()
+        assert all(torch.equal(x, y) for x, y in zip((out, lse, w), again))
+    want, tol = ref.attention(q.cpu(), k.cpu(), v.cpu(), prefix.cpu(), table.cpu(), lens.cpu(), 1, ks,
+                              vs, weight_in=w0, fp8=fp8)
+    for x, y, e in zip((out, lse, w), want, tol):
+        assert bool(((x.cpu().double() - y).abs() <= e).all())
