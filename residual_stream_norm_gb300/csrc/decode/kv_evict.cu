@@ -32,6 +32,13 @@ constexpr int kMostCached = 50 * 1024;                // weights in shared memor
 
 constexpr uint32_t kZeroKey = 0x80000000u;
 
+// Counts of a round's warps, read four at a time.
+struct alignas(16) WarpCounts {
+    uint32_t of[kPerThread * kEvictWarps];
+};
+static_assert(alignof(WarpCounts) >= alignof(uint4) && sizeof(WarpCounts) == 4 * 32 * sizeof(uint32_t),
+              "four counts a lane");
+
 // Order-preserving key: larger weights, larger keys; -0 as +0; NaN below every number.
 __device__ __forceinline__ uint32_t weight_key(float w)
 {
@@ -87,7 +94,7 @@ __global__ void __launch_bounds__(kEvictThreads) kv_evict_kernel(const EvictArgs
     extern __shared__ float s_weight[];  // [cached]
     __shared__ __align__(8) uint32_t s_hist[kBins];
     __shared__ uint32_t s_list[kList];
-    __shared__ uint32_t s_warp[2][kPerThread * kEvictWarps];
+    __shared__ WarpCounts s_warp[2];
     __shared__ uint32_t s_pick[3];       // digit, still wanted of it, whether all of it stays
     __shared__ uint32_t s_count[2];      // of this block's entries: above the smallest, equal to it
     __shared__ uint32_t s_listed, s_zeros;
@@ -211,9 +218,9 @@ __global__ void __launch_bounds__(kEvictThreads) kv_evict_kernel(const EvictArgs
             }
             const uint32_t inc = warp_scan(h[0] + h[1], lane);
             if (lane == 31)
-                s_warp[0][warp] = inc;
+                s_warp[0].of[warp] = inc;
             __syncthreads();
-            const uint32_t w = warp_scan(s_warp[0][lane], lane);
+            const uint32_t w = warp_scan(s_warp[0].of[lane], lane);
             const uint32_t before =
                 (warp > 0 ? __shfl_sync(0xffffffffu, w, warp - 1) : 0u) + inc - h[0] - h[1];
 #pragma unroll
@@ -263,11 +270,12 @@ __global__ void __launch_bounds__(kEvictThreads) kv_evict_kernel(const EvictArgs
             eq = __reduce_add_sync(0xffffffffu, eq);
             __syncthreads();  // s_warp is free
             if (lane == 0) {
-                s_warp[0][warp] = gt;
-                s_warp[1][warp] = eq;
+                s_warp[0].of[warp] = gt;
+                s_warp[1].of[warp] = eq;
             }
             __syncthreads();
-            const uint32_t g = warp_scan(s_warp[0][lane], lane), e = warp_scan(s_warp[1][lane], lane);
+            const uint32_t g = warp_scan(s_warp[0].of[lane], lane);
+            const uint32_t e = warp_scan(s_warp[1].of[lane], lane);
             gt_before = warp > 0 ? __shfl_sync(0xffffffffu, g, warp - 1) : 0u;
             eq_before = warp > 0 ? __shfl_sync(0xffffffffu, e, warp - 1) : 0u;
             if (split > 1) {
@@ -351,12 +359,12 @@ __global__ void __launch_bounds__(kEvictThreads) kv_evict_kernel(const EvictArgs
             above[k] = __ballot_sync(0xffffffffu, c && key > thr);
             equal[k] = __ballot_sync(0xffffffffu, c && key == thr);
             if (lane == 0)
-                s_warp[round][k * kEvictWarps + warp] =
+                s_warp[round].of[k * kEvictWarps + warp] =
                     (uint32_t)__popc(above[k]) | (uint32_t)__popc(equal[k]) << 16;
         }
         __syncthreads();
         // running counts over the 128 (k, warp): four a lane
-        const uint4 c4 = *reinterpret_cast<const uint4 *>(&s_warp[round][4 * lane]);
+        const uint4 c4 = *reinterpret_cast<const uint4 *>(&s_warp[round].of[4 * lane]);
         const uint32_t sum = c4.x + c4.y + c4.z + c4.w, inc = warp_scan(sum, lane);
         const uint32_t all = __shfl_sync(0xffffffffu, inc, 31);
         uint32_t mine = inc - sum;  // exclusive, at this warp's place among the lane's four
