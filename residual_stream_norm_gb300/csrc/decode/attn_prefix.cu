@@ -315,8 +315,11 @@ __global__ void __launch_bounds__(kThreads, 2)
     uint64_t *bars = reinterpret_cast<uint64_t *>(smem + S::kBars) + warp * C::kStages;
     int64_t *s_scan = reinterpret_cast<int64_t *>(smem + S::kScan);
     volatile int *s_fail = reinterpret_cast<int *>(smem + S::kFail);
-    if (tid == 0)
+    if (tid == 0) {
         *s_fail = smem_addr(smem) % 1024 != 0;  // the copies' exchange of chunks goes by address
+        if (*s_fail)
+            atomicOr(&g_decode_fault_word, kFaultCopyTimeout);
+    }
     if (lane == 0) {
         for (int i = 0; i < C::kStages; ++i)
             mbar_init(&bars[i], 1);
