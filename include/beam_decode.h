@@ -43,7 +43,8 @@ extern "C" {
  *   lse = log(sum_j exp(s_j))                 out = bf16(v_scale * sum_j exp(s_j - lse) v_j)
  * A row that sees nothing gives out = 0 and lse = -inf.  Scores, maxima, sums and outputs are FP32;
  * the weights exp(s_j - max) are rounded to BF16 (BF16 cache) or FP16 (FP8 cache) where they
- * multiply the values, an error of at most 2^-8 (2^-11) of each.  For an FP8 cache the query row is
+ * multiply the values: an error of at most 2^-8 of each (BF16), of 2^-11 of each and 2^-32 of the
+ * largest (FP16, scaled up by a power of two first).  For an FP8 cache the query row is
  * taken in FP16 after an exact scaling by a power of two (at most 2^60) that brings its largest
  * element to [2^14, 2^15), so that only elements 2^-28 below the largest (or below 2^-74) lose bits.
  * If key_weight_out is given, the weight that each suffix key received is added up:

@@ -5,6 +5,13 @@
 // by exp(m - m').  Parts of a list join by the same rule.  Exponents are taken to base 2, scores
 // carry the factor log2(e).
 //
+// The weights exp(s - m) meet the values in 16 bits, since a matrix instruction has both operands in one
+// type: BF16, at most 2^-8 of each weight off, for a BF16 cache; FP16, 2^-11, for an FP8 cache, whose values
+// it holds exactly.  The sum l takes them in FP32.  (Two BF16 parts of each weight would take the second
+// product twice.)  FP16 has only 2^-14 to 2^16 at full precision, so for an FP8 cache m stands kTop below the
+// maximum and the weights reach 2^kTop: 2^-11 of each then holds down to 2^-29 of the largest, and what lies
+// below errs by 2^-40 of it at most.
+//
 // Rows kernel (every sequence's own keys; the prefix where that is little work): a warp works on 16 keys
 // (FP8: 32) at a time for 8 or 16 query rows of one KV head.  It computes the transposed products
 // S^T = K Q^T and O^T = V^T P^T, so that the keys fill the 16 rows of the matrix instruction and the few
@@ -25,6 +32,7 @@
 namespace beam {
 namespace {
 
+constexpr float kTop = 15.0f;
 constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
 
@@ -662,6 +670,8 @@ __global__ void __launch_bounds__(kThreads, 2)
                     mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
                     mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
                     mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+                    if constexpr (FP8)
+                        mx = __fsub_ru(mx, kTop);  // upwards: no weight above 2^kTop
                     const float mn = fmaxf(m[n][e], mx);
                     ms[e] = mn == -INFINITY ? 0.0f : mn;
                     alpha[n][e] = exp2_fast(__fsub_rn(m[n][e], ms[e]));

@@ -15,9 +15,11 @@
 // expansion to FP16 shares the shared memory too (3900 cycles a step).  Alone, a block costs about
 // 11 us to set up and write out, so few rows or keys go to the rows kernel.
 //
-// The running maximum is raised (and O scaled, in tensor memory) only when a score exceeds it by more
-// than 2^8: the weights of a part stay below 2^8, which FP32 sums and both 16-bit types hold with
-// the same relative precision, and nearly all tiles then need no scaling.
+// The reference m of a row is raised (and O scaled, in tensor memory) only when a score exceeds what it was
+// raised to by more than 8, a published way to leave out nearly all scaling of an online softmax.  A BF16
+// cache's weights 2^(s - m) then stay below 2^8, which BF16 and FP32 hold as well as those below 1.  For an FP8
+// cache they are FP16, so m is raised to 7 below the largest score: they reach 2^7 at least and 2^15 at most,
+// are within 2^-11 of themselves down to 2^-21 of the largest, and below that within 2^-32 of it.
 //
 // A window cuts the prefix row by row.  A weight of zero does not hide an infinite or NaN value from the
 // matrix product, so where some row does not see a key of a tile the softmax warps first look the
@@ -43,6 +45,7 @@ constexpr int kTile = 128 * 128 * 2;  // bytes of a 128 x 128 tile of 16-bit val
 constexpr int kHalfTile = kTile / 2;  // 64 values of each row
 constexpr int kRawTile = 128 * 128;   // FP8
 constexpr float kRaise = 8.0f;
+constexpr float kBelow = 7.0f;  // FP8
 
 template <bool FP8, bool SPLIT>
 struct TcConfig {
@@ -345,10 +348,12 @@ __global__ void __launch_bounds__(TcConfig<FP8, SPLIT>::kThreads, 1)
                 mx0 = max3(mx0, r[c], r[c + 1]);
                 mx1 = max3(mx1, r[c + 2], r[c + 3]);
             }
-            const float mx = __fmul_rn(fmaxf(mx0, mx1), scale);
-            const bool raise = mx > __fadd_rn(m, kRaise);
+            // rounded so that no weight passes its bound
+            constexpr float below = FP8 ? kBelow : 0.0f;
+            const float mx = __fmul_ru(fmaxf(mx0, mx1), scale);
+            const bool raise = mx > __fadd_rd(m, below + kRaise);
             if (__any_sync(0xffffffffu, raise)) {
-                const float mn = raise ? mx : m;
+                const float mn = raise ? __fsub_ru(mx, below) : m;
                 const float f = m == mn ? 1.0f : exp2_fast(__fsub_rn(m, mn));
                 l = __fmul_rn(l, f);
                 m = mn;

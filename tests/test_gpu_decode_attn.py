@@ -449,3 +449,38 @@ def test_right_behind_the_kernels_that_write_its_inputs(graph, fp8):
                               vs, weight_in=w0, fp8=fp8)
     for x, y, e in zip((out, lse, w), want, tol):
         assert bool(((x.cpu().double() - y).abs() <= e).all())
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("B,P,N", [
+    (1, 0, 2001),        # a sequence's own keys
+    (2, 100, 2001),      # behind a prefix in line
+    (8, 40001, 1),       # a prefix for up to 128 rows on the tensor cores
+    (9, 50001, 1)])      # and for more
+def test_small_weights_beside_strong_keys(B, P, N, fp8):
+    # every sixteenth key takes nearly all of the weight and has no value: the output is what the others,
+    # each of 1.4 x 2^-24 of a strong key's weight, add up to
+    lib()
+    n_q, S = 16, P + B * N
+    strong = torch.arange(S) % 16 == 0
+    k = torch.zeros((S, 1, D))
+    k[strong, 0, 0] = 1.0
+    v = torch.ones((S, 1, D))
+    v[strong] = 0.0
+    q = torch.zeros((B, n_q, D), dtype=torch.bfloat16)
+    q[:, :, 0] = 1.0
+    cast = (lambda x: x.to(torch.float8_e4m3fn).view(torch.uint8)) if fp8 else (
+        lambda x: x.bfloat16())
+    c = dict(q=q, k=cast(k), v=cast(v), prefix=torch.arange(P), table=P + torch.arange(B * N).view(B, N),
+             lens=torch.full((B,), N, dtype=torch.int32), q_len=1, ks=1.0, vs=1.0, fp8=fp8)
+    sm = 24 * math.log(2.0) - math.log(1.4)
+    out, lse, w = run(c, weights=True, sm_scale=sm)
+    # a sequence's rows are alike: one of each in 64 bits
+    for b in range(B):
+        want, tol = ref.attention(q[:1, :1], c["k"], c["v"], c["prefix"], c["table"][b:b + 1],
+                                  c["lens"][:1], 1, sm_scale=sm, fp8=fp8)
+        assert float(tol[0].max()) < 0.02 * float(want[0].min())
+        assert bool(((out[b].double() - want[0][0]).abs() <= tol[0][0]).all()), \
+            f"{out[b].min():.4g} to {out[b].max():.4g} for {float(want[0].min()):.4g}"
+        assert bool(((lse[b].double() - want[1][0]).abs() <= tol[1][0]).all())
+        assert bool(((w[b].double() - n_q * want[2][0]).abs() <= n_q * tol[2][0]).all())
