@@ -1231,16 +1231,22 @@ AttnPlan attn_plan(int32_t B, int32_t q_len, int32_t n_q, int32_t n_kv, int64_t 
     int64_t keys = p.in_line + width;
     if (window > 0 && window + q_len - 1 < keys)
         keys = window + q_len - 1 + 15;
-    // Units that are not split need no join: where none has more than one tile, or where there are so
-    // many that shares of whole units are even enough.  Against split units: 14 sequences of 3 tokens
-    // 13.2 -> 10.1 us, 21 of at most 53 keys with weights 12.7 -> 10.9.  The 12 was not swept.
+    // Units that are not split need no join: where none has more than one tile, or where the longest that
+    // there can be takes no more places than an even share of the units' costs alone, so that whatever
+    // the lengths no block has more than twice an even share.  Against split units: 14 sequences of
+    // 3 tokens 13.2 -> 10.1 us, 21 of at most 53 keys with weights 12.7 -> 10.9; 8 KV heads, 512 sequences
+    // of 1-300 keys 104 -> 94, 256 of 1-300 56.6 -> 53.6, 256 behind a window of 512 94.5 -> 87.5, 256 of
+    // 1-1024 113 -> 121.  Without the bound, one list of 100K keys among 256 short ones held the
+    // call up (1859 us; split 141).
+    const int64_t most = kPlanSms * 2;
     p.whole = p.p_rtiles == 0 && p.tc_parts == 0 &&
-              (keys + 15 <= p.tile_keys || p.units >= 12 * kPlanSms);
+              (keys + 15 <= p.tile_keys ||
+               ((keys + 15 + p.tile_keys - 1) / p.tile_keys + kUnitCost) * most <=
+                   p.units * kUnitCost);
     // the most places there can be: no block is worth less than one
     const int64_t tiles =
         n_kv * (p.p_rtiles * (p.p_tiles + kUnitCost) +
                 (int64_t)B * p.s_rtiles * ((keys + p.tile_keys - 1) / p.tile_keys + kUnitCost));
-    const int64_t most = kPlanSms * 2;
     p.ctas = (int32_t)(tiles < 1 ? 1 : (tiles < most ? tiles : most));
     p.score_width = align_up(width, 8);
     int64_t at = 0;

@@ -484,3 +484,33 @@ def test_small_weights_beside_strong_keys(B, P, N, fp8):
             f"{out[b].min():.4g} to {out[b].max():.4g} for {float(want[0].min()):.4g}"
         assert bool(((lse[b].double() - want[1][0]).abs() <= tol[1][0]).all())
         assert bool(((w[b].double() - n_q * want[2][0]).abs() <= n_q * tol[2][0]).all())
+
+
+def test_one_long_list_among_many_short_ones():
+    # the long list is shared out: the call takes little more than its two parts by themselves (all of a head's
+    # 60,000 keys in one block would take some ten times as long)
+    lib()
+    B, n = 256, 60000
+    short = [1 + (37 * b) % 200 for b in range(B)]
+    times = []
+    for lens, N in ((short, n), ([n], n), (short[:90] + [n] + short[91:], n)):
+        c = make(len(lens), 1, 8, 8, 0, N, lens, seed=17)
+        dev = {x: c[x].cuda() for x in ("q", "k", "v", "table", "lens")}
+        ws = torch.empty(rsn.beam_attn_prefix_workspace(len(lens), 1, 8, 8, 0, N), dtype=torch.uint8,
+                         device="cuda")
+        out = torch.empty_like(dev["q"])
+        best = math.inf
+        for _ in range(8):
+            a, b = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+            a.record()
+            rsn.beam_attn_prefix_fwd(out, dev["q"], dev["k"], dev["v"], None, dev["table"], dev["lens"],
+                                     ws)
+            b.record()
+            torch.cuda.synchronize()
+            best = min(best, a.elapsed_time(b))
+        times.append(best)
+    assert times[2] < 3 * (times[0] + times[1]), times
+    pick = [0, 90, 200]
+    want, tol = ref.attention(c["q"][pick], c["k"], c["v"], c["prefix"], c["table"][pick],
+                              c["lens"][pick], 1)
+    assert bool(((out.cpu()[pick].double() - want[0]).abs() <= tol[0]).all())
