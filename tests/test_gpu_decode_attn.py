@@ -514,3 +514,22 @@ def test_one_long_list_among_many_short_ones():
     want, tol = ref.attention(c["q"][pick], c["k"], c["v"], c["prefix"], c["table"][pick],
                               c["lens"][pick], 1)
     assert bool(((out.cpu()[pick].double() - want[0]).abs() <= tol[0]).all())
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("B,n_q,n_kv,P,N", [
+    (129, 6, 1, 0, 150),    # the last sequence starts a second round of the sums over the sequences
+    (300, 6, 1, 0, 150),
+    (300, 4, 2, 300, 90),   # with a prefix in units of its own or on the tensor cores
+    (260, 8, 8, 0, 200)])   # whole units of several tiles
+def test_more_sequences_than_threads_of_a_block(B, n_q, n_kv, P, N, fp8):
+    lib()
+    lens = [(53 * b) % (N + 1) for b in range(B)]
+    for b in (0, 126, 127, 128, 255, 256, B - 1):       # without a key, around the rounds' ends
+        if b < B:
+            lens[b] = 0
+    lens[1], lens[125], lens[B - 2] = N, N, N
+    c = make(B, 1, n_q, n_kv, P, N, lens, fp8=fp8, seed=B + n_q)
+    plain = check(c, weights=True)
+    assert all(torch.equal(x, y) for x, y in zip(run(c), plain[:2]))  # with and without weights
+    check(c, window=77)

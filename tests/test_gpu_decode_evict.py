@@ -113,3 +113,37 @@ def test_no_rows_and_no_width():
         rsn.beam_kv_evict_fwd(t, n, w, None, t, n, w, 10, 2)
         torch.cuda.synchronize()
         assert bool((n == 0).all())
+
+
+def test_rows_past_the_shared_memory_of_a_block():
+    # more entries a block than it holds weights for, in too many rows for clusters
+    lib()
+    rows, width, budget, recent = 81, 53000, 52000, 500
+    g = np.random.default_rng(7)
+    table = g.integers(0, 2 ** 40, (rows, width))
+    weight = g.integers(0, 3000, (rows, width)).astype(np.float32)   # many ties
+    weight[1] = (g.random(width) ** 8 * 50).astype(np.float32)
+    lens = np.full(rows, width, np.int32)
+    lens[2], lens[3], lens[4] = budget + 1, budget, 51201
+    F = width - budget
+    want = [np.full((rows, width), -1, np.int64), np.minimum(lens, budget),
+            np.zeros((rows, width), np.float32), np.full((rows, F), -1, np.int64)]
+    for r in range(rows):
+        n = int(lens[r])
+        stay = np.ones(n, bool)
+        if n > budget:
+            old = n - recent
+            order = np.argsort(-weight[r, :old], kind="stable")
+            stay[:old] = False
+            stay[order[:budget - recent]] = True
+        m = int(stay.sum())
+        want[0][r, :m], want[2][r, :m] = table[r, :n][stay], weight[r, :n][stay]
+        want[3][r, :n - m] = table[r, :n][~stay]
+    for in_place in (False, True):
+        dt, dn, dw = (torch.from_numpy(x.copy()).cuda() for x in (table, lens, weight))
+        outs = [dt, dn, dw] if in_place else [torch.empty_like(x) for x in (dt, dn, dw)]
+        outs.append(torch.empty((rows, F), dtype=torch.int64, device="cuda"))
+        rsn.beam_kv_evict_fwd(*outs, dt, dn, dw, budget, recent)
+        torch.cuda.synchronize()
+        for name, got, exp in zip(("table", "len", "weight", "freed"), outs, want):
+            assert np.array_equal(got.cpu().numpy(), exp), (name, in_place)
