@@ -409,23 +409,61 @@ __global__ void __launch_bounds__(kEvictThreads) kv_evict_kernel(const EvictArgs
         a.len_out[row] = (int32_t)m;
 }
 
+// How many clusters of `split` blocks the device holds at a time (a cluster stays within one of its groups
+// of SMs, so fewer than the SMs would give); the same for all calls.
+int resident_clusters(int split)
+{
+    static int known[64][4] = {};
+    int dev = 0, n = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess)
+        return 0;
+    int *at = dev < 64 ? &known[dev][split / 4] : nullptr;
+    if (at && *at)
+        return *at;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)split);
+    cfg.blockDim = dim3(kEvictThreads);
+    cfg.dynamicSmemBytes = kMostCached * 4;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = (unsigned)split;
+    attr.val.clusterDim.y = 1;
+    attr.val.clusterDim.z = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    if (cudaOccupancyMaxActiveClusters(&n, kv_evict_kernel<false>, &cfg) != cudaSuccess)
+        return 0;
+    if (at)
+        *at = n;
+    return n;
+}
+
 }  // namespace
 
 cudaError_t launch_kv_evict(const EvictArgs &a, cudaStream_t stream)
 {
     const bool in_place = (a.width > 0) && (a.table_in == a.table_out || a.weight_in == a.weight_out ||
                                             a.len_in == a.len_out);
-    // a cluster per row while that leaves SMs over and gives each block a round of its own
-    int split = 1;
-    while (!in_place && split < 8 && a.rows * split * 2 <= kPlanSms + 8 &&
-           a.width >= (int64_t)split * 2 * kRound / 2)
-        split *= 2;
-    const int64_t per = (a.width + split - 1) / split;
-    const int cached = (int)(per < kMostCached ? per : kMostCached);
     cudaError_t e = in_place ? allow_smem<kv_evict_kernel<true>>(kMostCached * 4)
                              : allow_smem<kv_evict_kernel<false>>(kMostCached * 4);
     if (e != cudaSuccess)
         return e;
+    // Blocks of a cluster per row, as many as make long rows shorter, while all rows' clusters are resident at
+    // once.  1, 2, 4 and 8 blocks for 8 rows, us: of 9K 11.9, 12.8, 13.0, 17.6; of 12.5K 14.1, 13.5, 13.6, 17.9; of
+    // 16K 15.4, 14.5, 14.0, 18.3; of 80K 63, 33, 23.5, 23.2; of 200K 150, 85, 41, 32.  More clusters than fit
+    // take a second round: 15 and 16 rows of 100K in eights 25.5 and 47 (in fours 27), 36 and 37 in fours 29.5 and
+    // 54 (in pairs 45), 76 and 77 rows of 40K in pairs 22.7 and 42 (single blocks 31).
+    int split = 1;
+    if (!in_place) {
+        constexpr struct {
+            int split, width;
+        } kinds[] = {{8, 81920}, {4, 16384}, {2, 12288}};
+        for (const auto &k : kinds)
+            if (split == 1 && a.width >= k.width && a.rows <= resident_clusters(k.split))
+                split = k.split;
+    }
+    const int64_t per = (a.width + split - 1) / split;
+    const int cached = (int)(per < kMostCached ? per : kMostCached);
     cudaLaunchConfig_t cfg = {};
     cfg.blockDim = dim3(kEvictThreads);
     cfg.dynamicSmemBytes = (size_t)cached * 4;

@@ -147,3 +147,35 @@ def test_rows_past_the_shared_memory_of_a_block():
         torch.cuda.synchronize()
         for name, got, exp in zip(("table", "len", "weight", "freed"), outs, want):
             assert np.array_equal(got.cpu().numpy(), exp), (name, in_place)
+
+
+@pytest.mark.parametrize("rows,width", [(15, 100000), (36, 100000), (76, 40000)])
+def test_one_more_row_does_not_double_the_time(rows, width):
+    # around the numbers of clusters that are resident at once
+    lib()
+
+    def time(n):
+        table, weight = case(n, width, n)
+        dt, dw = torch.from_numpy(table).cuda(), torch.from_numpy(weight).cuda()
+        dn = torch.full((n,), width, dtype=torch.int32, device="cuda")
+        budget = width - 2000
+        outs = [torch.empty_like(x) for x in (dt, dn, dw)]
+        outs.append(torch.empty((n, 2000), dtype=torch.int64, device="cuda"))
+        graph = torch.cuda.CUDAGraph()
+        rsn.beam_kv_evict_fwd(*outs, dt, dn, dw, budget, 100)
+        torch.cuda.synchronize()
+        with torch.cuda.graph(graph):
+            for _ in range(10):
+                rsn.beam_kv_evict_fwd(*outs, dt, dn, dw, budget, 100)
+        times = []
+        for _ in range(8):
+            a, b = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+            a.record()
+            graph.replay()
+            b.record()
+            torch.cuda.synchronize()
+            times.append(a.elapsed_time(b))
+        return min(times)
+
+    few, more = time(rows), time(rows + 1)
+    assert more < 1.75 * few, (few, more)
