@@ -398,13 +398,16 @@ __global__ void __launch_bounds__(TcConfig<FP8, SPLIT>::kThreads, 1)
                 if (ok && leave_out<FP8>(base + C::kV + (i & 1) * kTile, tid & 127))
                     *s_left_out = 1;
                 fence_async_shared();
+                __syncwarp();  // the warp is whole again before its tensor-memory instructions
             }
             tmem_wait_st();
             tc_fence_before();
             mbar_arrive(&p_full[half]);
         }
         // ---- the part ----------------------------------------------------------------------------
-        if (half < halves && ok && mbar_wait_or_fail(o_full, 0, s_fail)) {
+        // (by whole warps, also where a wait runs out for some lanes only)
+        if (half < halves &&
+            __all_sync(0xffffffffu, ok && mbar_wait_or_fail(o_full, 0, s_fail))) {
             tc_fence_after();
             const int part = SPLIT ? 2 * blockIdx.z + half : blockIdx.z;
             const int64_t at = ((int64_t)kvh * p.rows + rr) * p.tc_parts + part;
