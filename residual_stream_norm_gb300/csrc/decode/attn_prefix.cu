@@ -1153,8 +1153,11 @@ cudaError_t launch_rows_type(const AttnArgs &a, const AttnPlan &p, const CacheMa
 inline int64_t align_up(int64_t x, int64_t a) { return (x + a - 1) / a * a; }
 
 // Up to so many prefix keys stand in line with each sequence's own and are read again for each, out of
-// the cache; more are units of their own, joined later.  In line: 96 sequences of 4 query rows behind 10
-// keys 58.7 -> 45.8 us, 57 of 2 behind 80 keys 18.9 -> 13.1.  The limit itself was not swept.
+// the cache; more are units of their own, joined later (the tensor-core kernel, where it is preferred, comes
+// first).  In units and in line, us, behind 16, 128 and 256 keys: 1 sequence 8.4, 8.6, 8.8 and 8.0, 8.2, 8.2; 32 of
+// 50-100 keys 15.8, 16.8, 17.5 and 11.5, 13.6, 15.4; 96 of 4 tokens and 30-60 keys 66, 71, 81 and 39, 50, 62; 128 of
+// 250-500 keys 62, 63, 66 and 48, 52, 58.  Behind 512 keys in line is ahead by up to a seventh but 3% behind for
+// 64 sequences, behind 768 it is slower for 32 to 128 (21.8 against 20.5, 80.7 against 77.8).
 constexpr int64_t kInLine = 256;
 
 // The prefix goes to the tensor-core kernel where that is expected to take less time, in tenths of a
