@@ -1163,7 +1163,10 @@ constexpr int64_t kInLine = 256;
 // The prefix goes to the tensor-core kernel where that is expected to take less time, in tenths of a
 // microsecond: it costs 11 us to set up and write out and 1.8 us a step (bench of 1 to 43 steps); the
 // rows kernel 1.3 us a tile of 64 keys for 16 rows, or a unit's cost of kUnitCost of them, on each
-// of its blocks.  (128 rows behind 512 keys: 7 against 13 us; 384 rows behind 5001: 69 against 22 us.)
+// of its blocks.  (128 rows behind 512 keys: 7 against 13 us; 384 rows behind 5001: 69 against 22 us.  Whole
+// calls, 6 rows of a KV head a sequence: 16 sequences behind 3000 keys 22.8 against 23.6 us, 8192 keys 35.9 against
+// 26.4; 128 sequences behind 300 keys 48.6 against 45.7, 1000 keys 65 against 49.  Over 80 such sizes the
+// choice was at most a sixth from the better side, most often within 3%.)
 bool prefer_tc(const AttnPlan &p, int32_t n_kv, int64_t keys)
 {
     const int64_t places = n_kv * ((p.rows + 15) / 16) * ((keys + 63) / 64 + kUnitCost);

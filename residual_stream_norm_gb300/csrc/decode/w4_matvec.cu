@@ -10,8 +10,8 @@
 // results do not depend on timing.
 //
 // Measured: 1 token, 6144 x 5120: 10.2 us (floor 2.4 us; six steps a block, then two cluster barriers:
-// latency); 8 tokens, 5120 x 14336: 15.1 us with the weights in the L2
-// cache, 19.3 from memory; 32 tokens, 5120 x 40960, groups of 32: 78 us.
+// latency); 8 tokens, 5120 x 14336: 15.2 us with the weights in the L2
+// cache, 19.0 from memory; 16 tokens 25.8; 32 tokens, 5120 x 40960, groups of 32: 77.5 us.
 // What bounds the larger ones is not the weights' bytes but instructions (53 to 58% of the issue slots,
 // warps held up by the arithmetic pipe): unpacking takes 2.75
 // instructions a pair of weights (shift, mask with the 128 that makes it a BF16 number, exact
