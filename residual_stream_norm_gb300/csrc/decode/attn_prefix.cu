@@ -33,6 +33,7 @@ namespace beam {
 namespace {
 
 constexpr float kTop = 15.0f;
+constexpr float kTopInv = 1.0f / 32768.0f;  // 2^-kTop
 constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
 
@@ -69,6 +70,20 @@ __device__ unsigned int g_decode_fault_word = 0u;
 // The first kUnitCost places of a unit's stretch stand for it; a share that ends among them has no
 // tile of the unit.
 constexpr int kUnitCost = 3;
+
+// A row's log-sum-exp, natural and to base 2, from its reference and sum.  FP8: with kTop moved back from the
+// sum to the reference first, since the sum of two numbers of opposite sign near kTop would cost bits.
+__device__ __forceinline__ float log_sum(bool fp8, float m, float l)
+{
+    return fp8 ? __fmaf_rn(__fadd_rn(m, kTop), kLn2, logf(__fmul_rn(l, kTopInv)))
+               : __fmaf_rn(m, kLn2, logf(l));
+}
+
+__device__ __forceinline__ float log2_sum(bool fp8, float m, float l)
+{
+    return fp8 ? __fadd_rn(__fadd_rn(m, kTop), log2f(__fmul_rn(l, kTopInv)))
+               : __fadd_rn(m, log2f(l));
+}
 
 // The block whose share [c tot / C, (c + 1) tot / C) contains tile x (C <= tot).
 __device__ __forceinline__ int64_t owner(int64_t x, int64_t tot, int64_t ctas)
@@ -849,12 +864,12 @@ __global__ void __launch_bounds__(kThreads, 2)
                         const int64_t tok = unit_row(a, p, u, rr, i, hg);
                         if (a.lse)
                             a.lse[tok * a.n_q + u.kvh * p.group + hg] =
-                                ll[e] == 0.0f ? -INFINITY : __fmaf_rn(mm[e], kLn2, logf(ll[e]));
+                                ll[e] == 0.0f ? -INFINITY : log_sum(FP8, mm[e], ll[e]);
                         if (WEIGHTS)
                             reinterpret_cast<float *>(
                                 a.workspace + p.lse_off)[((int64_t)u.b * a.n_kv + u.kvh) * p.R +
                                                          (rr - u.row_base)] =
-                                ll[e] == 0.0f ? -INFINITY : __fadd_rn(mm[e], log2f(ll[e]));
+                                ll[e] == 0.0f ? -INFINITY : log2_sum(FP8, mm[e], ll[e]);
                     }
                 }
                 // FP8: a lane holds d = 16 mt + 2g, + 1 of both rows; BF16: d = 16 mt + g and + 8, so the
@@ -1058,11 +1073,11 @@ __global__ void __launch_bounds__(128) attn_join_kernel(const __grid_constant__ 
                  pack_bf16x2(__fmul_rn(o.z, f), __fmul_rn(o.w, f)));
     if (lane == 0) {
         if (a.lse)
-            a.lse[tok * a.n_q + h] = l == 0.0f ? -INFINITY : __fmaf_rn(m, kLn2, logf(l));
+            a.lse[tok * a.n_q + h] = l == 0.0f ? -INFINITY : log_sum(a.fp8, m, l);
         if (a.weight_out)
             reinterpret_cast<float *>(
                 a.workspace + p.lse_off)[(b * a.n_kv + kvh) * p.R + (rr - b * p.R)] =
-                l == 0.0f ? -INFINITY : __fadd_rn(m, log2f(l));
+                l == 0.0f ? -INFINITY : log2_sum(a.fp8, m, l);
     }
 }
 

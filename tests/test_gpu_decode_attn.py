@@ -533,3 +533,30 @@ def test_more_sequences_than_threads_of_a_block(B, n_q, n_kv, P, N, fp8):
     plain = check(c, weights=True)
     assert all(torch.equal(x, y) for x, y in zip(run(c), plain[:2]))  # with and without weights
     check(c, window=77)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("B,P,N", [(7, 0, 1), (3, 0, 3000)])
+def test_log_sums_near_zero(B, P, N, fp8):
+    # sums next to 1 (one key, or a strong one among weak ones): a few steps of FP32 at 1, whatever the weights
+    # are scaled by
+    lib()
+    c = make(B, 1, 8, 8, P, N, [N] * B, fp8=fp8, seed=18)
+    c["q"] *= 0.125
+    c["k"][c["table"][:, 1:].flatten()] = 0
+    if N > 1:
+        c["q"][:] = 0
+        c["q"][:, :, 0] = 1.0
+        c["k"][c["table"][:, 1:].flatten(), :, 0] = 0xfe if fp8 else -448.0  # the lowest E4M3 number
+        c["k"][c["table"][:, 0]] = 0
+    sm = 0.0625
+    ks = c["ks"] if fp8 else 1.0
+    _, lse, _ = run(c, sm_scale=sm, weights=True)
+    for b in range(B):
+        kk = ref.cache_values(c["k"][c["table"][b]], ks).transpose(0, 1)          # [8, N, D]
+        s = torch.einsum("hd,hnd->hn", c["q"][b].double(), kk) * sm
+        want = torch.logsumexp(s, 1)
+        # the score's rounding (as in the reference), one of exp2 and two of the logarithm near 1, one of the sum
+        tol = (c["q"][b].double().abs()[:, None] * kk.abs()).sum(2).max() * sm * 128 * ref.U32 * 2 + \
+            (8 * s.abs().max(1).values.clamp(min=1.0)) * ref.U32
+        assert bool(((lse[b].double() - want).abs() <= tol).all()), (lse[b], want)
