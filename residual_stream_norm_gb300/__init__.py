@@ -1,7 +1,7 @@
 """Python binding of libbeam_boundary.so: the Beam sublayer-boundary path on one GB300 (sm_103a).
 
 Thin ctypes wrappers with the same names as the C ABI in ``include/beam_boundary.h`` (and, in
-``decode.py``, ``include/beam_decode.h``).  They only
+``decode.py`` and ``draft.py``, ``include/beam_decode.h`` and ``include/beam_draft.h``).  They only
 marshal arguments (torch CUDA tensors -> device pointers, shapes, strides, the current stream)
 and raise ``BeamError`` on a non-zero status; every step of the computation runs in the CUDA
 kernels of the library.  There is no CPU fallback: if the library is missing, importing the
@@ -17,9 +17,11 @@ import threading
 
 import torch
 
-from . import _build, decode
+from . import _build, decode, draft
 from .decode import (beam_attn_prefix_fwd, beam_attn_prefix_workspace, beam_kv_evict_fwd,
                      beam_w4_matvec_fwd)
+from .draft import (beam_attn_kv4_fwd, beam_attn_kv4_workspace, beam_draft_verify_fwd,
+                    beam_kv4_write_fwd, beam_moe_layer_fwd, beam_moe_layer_workspace)
 
 __all__ = ["BeamError", "build", "lib", "beam_abi_version", "beam_status_str",
            "beam_residual_scales", "beam_rope_cos_sin", "beam_residual_operand",
@@ -29,7 +31,9 @@ __all__ = ["BeamError", "build", "lib", "beam_abi_version", "beam_status_str",
            "beam_qk_norm_rope_fwd", "beam_qk_norm_ssmax_fwd", "beam_qk_norm_rope_kv_fwd",
            "beam_qk_norm_ssmax_kv_fwd", "beam_grouped_topk_fwd", "beam_attn_gate_fwd",
            "beam_attn_prefix_fwd", "beam_attn_prefix_workspace", "beam_kv_evict_fwd",
-           "beam_w4_matvec_fwd", "HEAD_DIM"]
+           "beam_w4_matvec_fwd", "beam_kv4_write_fwd", "beam_attn_kv4_fwd",
+           "beam_attn_kv4_workspace", "beam_moe_layer_fwd", "beam_moe_layer_workspace",
+           "beam_draft_verify_fwd", "HEAD_DIM"]
 
 HEAD_DIM = decode.HEAD_DIM
 LIB_PATH = _build.LIB_PATH
@@ -99,6 +103,7 @@ def lib() -> ctypes.CDLL:
                        "beam_attn_gate_fwd"):
                 getattr(so, fn).restype = ctypes.c_int
             decode.declare(so)
+            draft.declare(so)
             _lib = so
     return _lib
 
