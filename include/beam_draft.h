@@ -9,9 +9,8 @@
  * before anything is launched, calls asynchronous on `stream`, programmatic dependent launch.  The
  * router's weights may be read before the preceding kernel of the stream has ended; everything else is
  * read, and every output written, only after it.  Calls on different streams need workspaces of their
- * own; a workspace's contents need not be kept or cleared between calls.  Waits inside the kernels are
- * bounded; beam_device_faults() also reports one that ran out, after which the call's outputs are not
- * to be used.
+ * own; a workspace's contents need not be kept or cleared between calls.  No kernel here waits for anything but
+ * its own block's or cluster's threads and copies.
  */
 #ifndef BEAM_DRAFT_H
 #define BEAM_DRAFT_H
@@ -94,12 +93,12 @@ BEAM_API int64_t beam_attn_kv4_workspace(int32_t B, int32_t q_len, int32_t n_q_h
  *
  *   z[t, e] = <x[t], router_w[e]>                             (all 256 experts)
  *   ids, w  = beam_grouped_topk_fwd(z, router_bias)           (8 groups, 4 of them, 8 experts)
- *   g = w_gate_up[e, 0..F) x[t]    u = w_gate_up[e, F..2F) x[t]    a = bf16(g / (1 + exp(-g)) * u)
+ *   g = w_gate_up[e, 0..F) x[t]    u = w_gate_up[e, F..2F) x[t]    a = g / (1 + exp(-g)) * u
  *   out[t] = bf16( sum over k of (routed_scaling * w[t, k]) * w_down[ids[t, k]] a[t, k] )
  * The logits z are sums of the exact products in FP32 pairs, rounded once to FP32, so that the choice does
  * not hang on the order of a sum.  The experts' sums, g, u and the sum over k (in the order of the experts'
- * numbers) are FP32; a is rounded to BF16, the type of the down product's operands (an error of at most
- * 2^-8 of each).
+ * numbers) are FP32; a goes into the down product as the sum of two BF16 values, its
+ * rounding and the rounding of the rest (an error of at most 2^-16 of each).
  * The call computes the part of the experts [first_expert, first_expert + n_local), whose weights it gets
  * (the others are another rank's), with F their intermediate columns on this rank: for expert- and
  * tensor-parallel shares `out` is a partial sum for beam_allreduce_boundary_fwd, for the whole layer it
@@ -136,8 +135,9 @@ BEAM_API int64_t beam_moe_layer_workspace(int64_t T, int32_t H, int32_t F, int32
  * where P = rint(2^44 p), Q = rint(2^44 q) are the probabilities in units of 2^-44 (values outside [0, 1] are
  * limited to it, NaN counts as 0).  It is the smallest token v with
  *   sum of the weights up to v  >  floor(u * S),   S the sum of all, u = u_sample[b] limited to [0, 1)
- * (u in units of 2^-64), or -1 if all weights are zero.  All of it is whole-number arithmetic: results do
- * not depend on the order of any sum.  This draws from the target's distribution exactly, up to the units.
+ * and cut off to units of 2^-24 (NaN: 0), or -1 if all weights are zero.  All of it is whole-number arithmetic: results do
+ * not depend on the order of any sum.  Over random
+ * numbers this draws from the target's distribution, up to the units.
  *
  *   tokens_out [B, k + 1] int64: the accepted tokens, the drawn one, -1 behind them
  *   n_accepted_out [B] int32: a

@@ -18,7 +18,6 @@
 #include "beam_sincos.cuh"
 #include "beam_tma.cuh"
 #include "decode/decode_kernels.h"
-#include "draft/draft_kernels.h"
 
 namespace {
 
@@ -159,13 +158,11 @@ int beam_device_faults(uint32_t *flags, int clear)
 {
     if (!flags)
         return BEAM_ERR_INVALID_ARG;
-    unsigned int v = 0u, d = 0u, r = 0u;
+    unsigned int v = 0u, d = 0u;
     cudaError_t e = beam::read_fault_word(&v, clear != 0);
     if (e == cudaSuccess)
         e = beam::read_decode_fault_word(&d, clear != 0);
-    if (e == cudaSuccess)
-        e = beam::read_draft_fault_word(&r, clear != 0);
-    *flags = v | d | r;
+    *flags = v | d;
     return cuda_status(e);
 }
 

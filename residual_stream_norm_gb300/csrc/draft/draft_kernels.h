@@ -78,13 +78,11 @@ struct MoeArgs {
 
 // Byte offsets in the workspace.
 struct MoePlan {
-    int64_t logits, ids, weights, act, bytes;
+    int64_t logits, ids, weights, passes, act, bytes;
 };
 
 MoePlan moe_plan(int64_t T, int32_t H, int32_t F);
 cudaError_t launch_moe_layer(const MoeArgs &a, const MoePlan &p, cudaStream_t stream);
-// The fault word of the kernels of this folder (as read_fault_word).
-cudaError_t read_draft_fault_word(unsigned int *value, bool clear);
 
 struct VerifyArgs {
     int64_t *tokens_out;

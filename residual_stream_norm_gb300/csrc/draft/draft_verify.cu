@@ -5,9 +5,9 @@
 // place where the running sum passes u S.  Probabilities are whole numbers of 2^-44, so sums are 64-bit
 // integers, exact in any order, and V < 2^20 of them stay below 2^64.
 //
-// One cluster of up to 8 blocks takes a sequence: each warp sums a stretch of the row, the first block reads
-// all stretches' sums out of its peers' shared memory, picks the stretch that holds the border, and its
-// threads search it (it is in the L2 cache by then).  The row is read from memory once.
+// One cluster of up to 8 blocks takes a sequence: each warp sums a stretch of the row, every block reads all
+// stretches' sums out of its peers' shared memory, and the one whose stretch holds the border searches it (it
+// is in the L2 cache by then).  The row is read from memory once.
 
 #include <cooperative_groups.h>
 
@@ -32,35 +32,55 @@ __device__ __forceinline__ float prob(const void *row, int64_t v)
         return ((const float *)row)[v];
 }
 
-// rint(2^44 p), p limited to [0, 1]; NaN: 0.  The scaling is exact.
-__device__ __forceinline__ int64_t units(float p)
+// rint(2^44 p) = 2^22 hi + lo, p limited to [0, 1]; NaN: 0.  A conversion to 64 bits goes through the FP64
+// pipe, which is narrow here (124 us for 128 rows of 160,000 with it, 39 with this): two FP32 additions to 2^23
+// do it, which leave a whole number in the mantissa, the first one cut off, the second rounded to nearest even.
+// What the first cuts off is exact, and the halves' ties are those of the whole.
+struct Units {
+    int32_t hi, lo;
+};
+
+__device__ __forceinline__ Units units(float p)
 {
-    return __float2ll_rn(__fmul_rn(fminf(fmaxf(p, 0.0f), 1.0f), 17592186044416.0f));
+    constexpr float k22 = 4194304.0f, k23 = 8388608.0f;
+    const float x = __fmul_rn(fminf(fmaxf(p, 0.0f), 1.0f), k22);
+    const float h = __fadd_rz(x, k23);
+    const float l = __fadd_rn(__fmul_rn(__fsub_rn(x, __fsub_rn(h, k23)), k22), k23);
+    return Units{(int32_t)(__float_as_uint(h) - 0x4b000000u), (int32_t)(__float_as_uint(l) - 0x4b000000u)};
 }
+
+__device__ __forceinline__ int64_t whole(int32_t hi, int32_t lo) { return ((int64_t)hi << 22) + lo; }
 
 // The rows that a sequence's last token is drawn from.
 struct Rows {
     const void *target;
-    const void *draft;  // nullptr: none (or all on token `spike`)
-    int64_t spike;      // -1: none
+    const void *draft;  // nullptr: none
+    int64_t spike;      // the draft is all on this token (-1: not so)
 };
 
-// Weight of token v; `plain` its target's probability.
-template <bool BF16>
-__device__ __forceinline__ void weight_of(float p, float q, bool has_q, bool spike, int64_t &w,
-                                          int64_t &plain)
+// Weight of a token as 2^22 hi + lo.
+__device__ __forceinline__ Units weight_of(float p, float q, bool spike)
 {
-    plain = units(p);
-    w = plain - (has_q ? units(q) : 0);
-    w = w < 0 || spike ? 0 : w;
+    const Units a = units(p), b = units(q);
+    Units w{a.hi - b.hi, a.lo - b.lo};
+    // its sign is that of hi unless hi is 0, since |lo| <= 2^22
+    if (spike || w.hi < 0 || (w.hi == 0 && w.lo < 0))
+        w.hi = w.lo = 0;
+    return w;
 }
 
-// Sums of the weights and of the target's probabilities of tokens [v0, v1), one lane's share.
 template <bool BF16>
-__device__ __forceinline__ void sum_stretch(const Rows &r, int64_t v0, int64_t v1, int lane,
-                                            uint64_t &sw, uint64_t &sp)
+__device__ __forceinline__ Units weight_at(const Rows &r, int64_t v)
+{
+    return weight_of(prob<BF16>(r.target, v), r.draft ? prob<BF16>(r.draft, v) : 0.0f, v == r.spike);
+}
+
+// Sum of the weights of tokens [v0, v1), one lane's share.
+template <bool BF16>
+__device__ __forceinline__ uint64_t sum_stretch(const Rows &r, int64_t v0, int64_t v1, int lane)
 {
     constexpr int kEach = 8;
+    uint64_t sum = 0;
     for (int64_t v = v0 + lane; v < v1; v += 32 * kEach) {
         float p[kEach], q[kEach];
 #pragma unroll
@@ -69,14 +89,16 @@ __device__ __forceinline__ void sum_stretch(const Rows &r, int64_t v0, int64_t v
             p[i] = in ? prob<BF16>(r.target, v + 32 * i) : 0.0f;
             q[i] = in && r.draft ? prob<BF16>(r.draft, v + 32 * i) : 0.0f;
         }
+        int32_t hi = 0, lo = 0;  // of 8 tokens: well within 32 bits
 #pragma unroll
         for (int i = 0; i < kEach; ++i) {
-            int64_t w, plain;
-            weight_of<BF16>(p[i], q[i], r.draft != nullptr, v + 32 * i == r.spike, w, plain);
-            sw += (uint64_t)w;
-            sp += (uint64_t)plain;
+            const Units w = weight_of(p[i], q[i], v + 32 * i == r.spike);
+            hi += w.hi;
+            lo += w.lo;
         }
+        sum += (uint64_t)whole(hi, lo);
     }
+    return sum;
 }
 
 __device__ __forceinline__ uint64_t warp_sum64(uint64_t v)
@@ -104,7 +126,7 @@ __device__ __forceinline__ uint64_t warp_below64(uint64_t v, int lane, uint64_t 
 template <bool BF16>
 __global__ void __launch_bounds__(kThreads) draft_verify_kernel(const VerifyArgs a)
 {
-    __shared__ uint64_t s_w[kWarps], s_p[kWarps];  // the stretches' sums, read by the first block
+    __shared__ uint64_t s_w[2][kWarps];  // the stretches' sums, read by all blocks of the cluster
     __shared__ uint64_t s_scan[kWarps];
     __shared__ int s_found;
     const cg::cluster_group cluster = cg::this_cluster();
@@ -156,48 +178,34 @@ __global__ void __launch_bounds__(kThreads) draft_verify_kernel(const VerifyArgs
     const int64_t mine = (int64_t)rank * kWarps + warp;
     const int64_t v0 = mine * each < a.V ? mine * each : a.V;
     const int64_t v1 = v0 + each < a.V ? v0 + each : a.V;
-    uint64_t sw = 0, sp = 0;
-    sum_stretch<BF16>(r, v0, v1, lane, sw, sp);
-    sw = warp_sum64(sw);
-    sp = warp_sum64(sp);
-    if (lane == 0) {
-        s_w[warp] = sw;
-        s_p[warp] = sp;
-    }
-    cluster.sync();
-    if (rank == 0) {
-        // ---- every warp: all stretches' sums (at most 4 a lane, in order), the border, its stretch ----
-        uint64_t w[4], p[4], lw = 0, lp = 0;
-        const int per = (int)((stretches + 31) / 32);
+    uint64_t w[4], below = 0, total = 0;
+    const int per = (int)((stretches + 31) / 32);
+    for (int again = 0;; ++again) {
+        const uint64_t sum = warp_sum64(sum_stretch<BF16>(r, v0, v1, lane));
+        if (lane == 0)
+            s_w[again][warp] = sum;
+        cluster.sync();
+        // every warp of every block: all stretches' sums, at most 4 a lane, in order
+        uint64_t own = 0;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const int64_t s = (int64_t)lane * per + i;
-            w[i] = p[i] = 0;
-            if (i < per && s < stretches) {
-                w[i] = *cluster.map_shared_rank(&s_w[s % kWarps], (int)(s / kWarps));
-                p[i] = *cluster.map_shared_rank(&s_p[s % kWarps], (int)(s / kWarps));
-            }
-            lw += w[i];
-            lp += p[i];
+            const int s = lane * per + i;
+            w[i] = i < per && s < stretches
+                       ? *cluster.map_shared_rank(&s_w[again][s % kWarps], s / kWarps)
+                       : 0;
+            own += w[i];
         }
-        uint64_t total;
-        uint64_t below = warp_below64(lw, lane, total);
-        const bool plain = total == 0;  // no weight left: the target's own probabilities
-        if (plain) {
-            below = warp_below64(lp, lane, total);
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                w[i] = p[i];
-            r.draft = nullptr;
-            r.spike = -1;
-        }
+        below = warp_below64(own, lane, total);
+        if (total != 0 || again == 1 || (!r.draft && r.spike < 0))
+            break;
+        r.draft = nullptr;  // no weight left: the target's own probabilities
+        r.spike = -1;
+    }
+    {
         float u = a.u_sample[b];
         u = fminf(fmaxf(u, 0.0f), 0.99999994f);  // NaN: 0
-        // u in units of 2^-64, in two steps of 32 bits: its 24 bits stand anywhere
-        const double ud = (double)u * 4294967296.0;
-        const uint64_t u_hi = (uint64_t)ud;
-        const uint64_t u64 = (u_hi << 32) | (uint64_t)((ud - (double)u_hi) * 4294967296.0);
-        const uint64_t border = __umul64hi(u64, total);
+        // floor(floor(2^24 u) S / 2^24)
+        const uint64_t border = __umul64hi((uint64_t)(u * 16777216.0f) << 40, total);
         int at = -1;
         uint64_t start = 0;
 #pragma unroll
@@ -212,18 +220,17 @@ __global__ void __launch_bounds__(kThreads) draft_verify_kernel(const VerifyArgs
         const int owner = has ? __ffs((int)has) - 1 : 0;
         at = __shfl_sync(0xffffffffu, at, owner);
         start = __shfl_sync(0xffffffffu, start, owner);
-        // ---- the block searches the stretch: a thread takes consecutive tokens --------------------
+        // ---- the stretch's block searches it: a thread takes consecutive tokens -------------------
         int64_t token = -1;
-        if (at >= 0) {
+        const bool here = rank == (at >= 0 ? at / kWarps : 0);
+        if (here && at >= 0) {
             const int64_t f0 = at * each, f1 = f0 + each < a.V ? f0 + each : a.V;
             const int64_t few = (f1 - f0 + kThreads - 1) / kThreads;
             const int64_t t0 = f0 + threadIdx.x * few;
             uint64_t own = 0;
             for (int64_t v = t0; v < t0 + few && v < f1; ++v) {
-                int64_t x, y;
-                weight_of<BF16>(prob<BF16>(r.target, v), r.draft ? prob<BF16>(r.draft, v) : 0.0f,
-                                r.draft != nullptr, v == r.spike, x, y);
-                own += (uint64_t)x;
+                const Units x = weight_at<BF16>(r, v);
+                own += (uint64_t)whole(x.hi, x.lo);
             }
             uint64_t all;
             uint64_t run = warp_below64(own, lane, all);
@@ -237,26 +244,27 @@ __global__ void __launch_bounds__(kThreads) draft_verify_kernel(const VerifyArgs
                 run += s_scan[i];
             if (run <= border && border - run < own) {
                 for (int64_t v = t0; v < t0 + few && v < f1; ++v) {
-                    int64_t x, y;
-                    weight_of<BF16>(prob<BF16>(r.target, v),
-                                    r.draft ? prob<BF16>(r.draft, v) : 0.0f, r.draft != nullptr,
-                                    v == r.spike, x, y);
-                    if (border - run < (uint64_t)x) {
+                    const Units x = weight_at<BF16>(r, v);
+                    const uint64_t n1 = (uint64_t)whole(x.hi, x.lo);
+                    if (border - run < n1) {
                         s_found = (int)v;
                         break;
                     }
-                    run += (uint64_t)x;
+                    run += n1;
                 }
             }
             __syncthreads();
             token = s_found;
         }
-        for (int i = threadIdx.x; i <= k; i += kThreads)
-            a.tokens_out[b * (k + 1) + i] = i < acc ? a.tokens[b * k + i] : (i == acc ? token : -1);
-        if (threadIdx.x == 0)
-            a.accepted[b] = acc;
+        if (here) {
+            for (int i = threadIdx.x; i <= k; i += kThreads)
+                a.tokens_out[b * (k + 1) + i] =
+                    i < acc ? a.tokens[b * k + i] : (i == acc ? token : -1);
+            if (threadIdx.x == 0)
+                a.accepted[b] = acc;
+        }
     }
-    cluster.sync();  // the first block has read its peers' shared memory
+    cluster.sync();  // all have read their peers' shared memory
 }
 
 template <bool BF16>

@@ -2,7 +2,9 @@
 //
 // A group of 32, 64 or 128 columns is held as codes 0..15 on the line minimum + scale * code.  Half a warp
 // takes one row of a KV head: each lane 8 columns (16 bytes in, 4 bytes of codes out), the group's smallest
-// and largest value by shuffles among its 4, 8 or 16 lanes.
+// and largest value by shuffles of a BF16 pair (minimum, -maximum) among its 4, 8 or 16 lanes.  For a prefill
+// chunk the kernel is bound by its instructions rather than by memory, so a half-warp's place in a token is worked out
+// once, and codes are rounded and packed with FP32 additions and fused multiply-adds.
 
 #include "beam_device.cuh"
 #include "draft_kernels.h"
@@ -11,6 +13,44 @@ namespace beam {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int kHalves = kThreads / 16;
+constexpr int kAhead = 4;  // rows that a half-warp has in hand at a time
+
+__device__ __forceinline__ uint32_t min_nan_bf16x2(uint32_t a, uint32_t b)
+{
+    uint32_t d;
+    asm("min.NaN.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+}
+
+// The codes rint(d / scale) of 8 values x of one group, d = x - lo.  d times the reciprocal is within 2^-19 of
+// the quotient (which is at most 15.06: scale is span / 15 but for its rounding), so a code is the quotient's own
+// rounding unless the product stands nearer than 2^-18 to a half: then IEEE division decides.
+__device__ __forceinline__ uint32_t codes_of(const uint4 &v, float lo, float scale)
+{
+    constexpr float kMagic = 12582912.0f;  // 1.5 2^23: a sum with it is rounded to a whole number
+    const float inv = __frcp_rn(scale);
+    float n[8], off = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const float d = __fsub_rn(i & 1 ? bf_hi(word(v, i / 2)) : bf_lo(word(v, i / 2)), lo);
+        n[i] = __fsub_rn(__fmaf_rn(d, inv, kMagic), kMagic);
+        off = fmaxf(off, fabsf(__fmaf_rn(d, inv, -n[i])));
+    }
+    // a subnormal scale may be far from span / 15, and its reciprocal overflow
+    if (off > 0.5f - 3.814697265625e-06f || scale < 1.1754943508222875e-38f) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const float d = __fsub_rn(i & 1 ? bf_hi(word(v, i / 2)) : bf_lo(word(v, i / 2)), lo);
+            n[i] = fminf(rintf(__fdiv_rn(d, scale)), 15.0f);
+        }
+    }
+    // four codes a number below 2^16: exact
+    const float a = __fmaf_rn(__fmaf_rn(__fmaf_rn(n[3], 16.0f, n[2]), 16.0f, n[1]), 16.0f, n[0]);
+    const float b = __fmaf_rn(__fmaf_rn(__fmaf_rn(n[7], 16.0f, n[6]), 16.0f, n[5]), 16.0f, n[4]);
+    return __byte_perm(__float_as_uint(__fadd_rn(a, kMagic)), __float_as_uint(__fadd_rn(b, kMagic)),
+                       0x5410);
+}
 
 template <int Group>
 __global__ void __launch_bounds__(kThreads) kv4_write_kernel(const Kv4WriteArgs a)
@@ -18,64 +58,63 @@ __global__ void __launch_bounds__(kThreads) kv4_write_kernel(const Kv4WriteArgs 
     constexpr int kLanes = Group / 8;   // lanes of a group
     constexpr int kGroups = 128 / Group;
     pdl_launch_dependents();
+    const int lane = threadIdx.x & 15, half = threadIdx.x >> 4;
+    const int per = 2 * a.n_kv;                          // rows of a token: its K heads, then its V heads
+    const int at_once = per < kHalves ? kHalves / per : 1;  // tokens of a block
+    const int tt = per < kHalves ? half / per : 0;
+    const int64_t step = (int64_t)gridDim.x * at_once;
     pdl_wait();
-    const int lane = threadIdx.x & 15;
-    const int64_t rows = a.T * 2 * a.n_kv;  // of a token: its K heads, then its V heads
-    const int64_t step = (int64_t)gridDim.x * (kThreads / 16);
-    const uint32_t per = 2 * a.n_kv;
-    // both halves of a warp take part in every shuffle: the loop runs for as long as either has a row
-    for (int64_t r = (int64_t)blockIdx.x * (kThreads / 16) + (threadIdx.x >> 4);
-         (r & ~(int64_t)1) < rows; r += step) {
-        const int64_t t = r < rows ? r / per : 0;
-        const int j = (int)(r - t * per);
-        const int which = j >= a.n_kv;
-        const int head = which ? j - a.n_kv : j;
-        const int64_t slot = r < rows ? a.slot[t] : -1;
-        const bool on = slot >= 0 && slot < a.num_slots;
-        uint4 v = make_uint4(0, 0, 0, 0);
-        if (on)
-            v = ld_stream((const uint16_t *)(which ? a.src[1] : a.src[0]) +
-                          t * (which ? a.src_stride[1] : a.src_stride[0]) + head * 128 + lane * 8);
-        float x[8];
-        float lo = __uint_as_float(0x7f800000u), hi = -lo;
-        bool finite = true;
+    // every bound is the same for both halves of a warp, or a half without a row goes along: shuffles are the warp's
+    for (int j0 = 0; j0 < per; j0 += kHalves) {
+        const int j = per < kHalves ? half - tt * per : j0 + half;
+        const bool on = j < per && tt < at_once;
+        const bool value = j >= a.n_kv;
+        const int head = value ? j - a.n_kv : j;
+        const uint16_t *src = (const uint16_t *)(value ? a.src[1] : a.src[0]) + head * 128 + lane * 8;
+        const int64_t stride = value ? a.src_stride[1] : a.src_stride[0];
+        uint32_t *codes = reinterpret_cast<uint32_t *>(value ? a.cache[1] : a.cache[0]) + head * 16 + lane;
+        uint32_t *scales = reinterpret_cast<uint32_t *>(value ? a.scales[1] : a.scales[0]) +
+                           head * kGroups + lane / kLanes;
+        for (int64_t t0 = (int64_t)blockIdx.x * at_once; t0 < a.T; t0 += step * kAhead) {
+            uint4 v[kAhead];
+            int64_t slot[kAhead];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            x[2 * i] = bf_lo(word(v, i));
-            x[2 * i + 1] = bf_hi(word(v, i));
-        }
+            for (int i = 0; i < kAhead; ++i) {
+                const int64_t t = t0 + i * step + tt;
+                slot[i] = on && t < a.T ? a.slot[t] : -1;
+                if (slot[i] >= a.num_slots)
+                    slot[i] = -1;
+                v[i] = make_uint4(0, 0, 0, 0);
+                if (slot[i] >= 0)
+                    v[i] = ld_stream(src + t * stride);
+            }
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            lo = fminf(lo, x[i]);
-            hi = fmaxf(hi, x[i]);
-            finite = finite && isfinite(x[i]);
-        }
+            for (int i = 0; i < kAhead; ++i) {
+                if (i > 0 && t0 + i * step >= a.T)
+                    break;
+                constexpr uint32_t kSign = 0x80008000u;
+                const uint32_t lo2 = min_nan_bf16x2(min_nan_bf16x2(v[i].x, v[i].y),
+                                                    min_nan_bf16x2(v[i].z, v[i].w));
+                const uint32_t hi2 = min_nan_bf16x2(
+                    min_nan_bf16x2(v[i].x ^ kSign, v[i].y ^ kSign),
+                    min_nan_bf16x2(v[i].z ^ kSign, v[i].w ^ kSign));
+                // (minimum, -maximum)
+                uint32_t ends = min_nan_bf16x2(__byte_perm(lo2, hi2, 0x5410), __byte_perm(lo2, hi2, 0x7632));
 #pragma unroll
-        for (int off = 1; off < kLanes; off <<= 1) {
-            lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, off));
-            hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, off));
-            finite = __shfl_xor_sync(0xffffffffu, (int)finite, off) && finite;
-        }
-        const float span = __fsub_rn(hi, lo);
-        const uint32_t held = pack_bf16x2(__fdiv_rn(span, 15.0f), lo);
-        float scale = bf_lo(held);
-        const bool bad = !finite || !isfinite(span);
-        const bool flat = bad || !(scale > 0.0f);
-        if (flat)
-            scale = 1.0f;
-        uint32_t code = 0u;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const float q = fminf(rintf(__fdiv_rn(__fsub_rn(x[i], lo), scale)), 15.0f);
-            code |= (flat ? 0u : (uint32_t)q) << (4 * i);
-        }
-        if (on) {
-            const int64_t row = slot * a.n_kv + head;
-            reinterpret_cast<uint32_t *>((which ? a.cache[1] : a.cache[0]) + row * 64)[lane] = code;
-            if (lane % kLanes == 0)
-                reinterpret_cast<uint32_t *>(which ? a.scales[1]
-                                                     : a.scales[0])[row * kGroups + lane / kLanes] =
-                    bad ? 0x7fc0u : held;
+                for (int off = 1; off < kLanes; off <<= 1)
+                    ends = min_nan_bf16x2(ends, __shfl_xor_sync(0xffffffffu, ends, off));
+                const float lo = bf_lo(ends);
+                const float span = -__fadd_rn(bf_hi(ends), lo);  // NaN or infinite: as the values are
+                const uint32_t held = pack_bf16x2(__fdiv_rn(span, 15.0f), lo);
+                const float scale = bf_lo(held);
+                const bool bad = !isfinite(span) || !isfinite(lo);
+                const uint32_t code = bad || !(scale > 0.0f) ? 0u : codes_of(v[i], lo, scale);
+                if (slot[i] >= 0) {
+                    codes[slot[i] * a.n_kv * 16] = code;
+                    if (lane % kLanes == 0)
+                        scales[slot[i] * a.n_kv * kGroups] = bad ? 0x7fc0u : held;
+                }
+            }
         }
     }
 }
@@ -84,8 +123,8 @@ __global__ void __launch_bounds__(kThreads) kv4_write_kernel(const Kv4WriteArgs 
 
 cudaError_t launch_kv4_write(const Kv4WriteArgs &a, cudaStream_t stream)
 {
-    const int64_t rows = a.T * 2 * a.n_kv;
-    const int64_t blocks = (rows + kThreads / 16 - 1) / (kThreads / 16);
+    const int at_once = 2 * a.n_kv < kHalves ? kHalves / (2 * a.n_kv) : 1;
+    const int64_t blocks = (a.T + at_once - 1) / at_once;
     const unsigned grid = (unsigned)(blocks < 152 * 8 ? blocks : 152 * 8);
     cudaError_t e;
     if (a.group == 32)

@@ -1,22 +1,25 @@
 // moe_layer.cu -- a whole mixture-of-experts layer for a few tokens (sm_103a).
 //
 // With up to 256 tokens and 8 of 256 experts each, an expert has a handful of tokens: the layer is bound by
-// reading the chosen experts' weights, each once.  Four kernels:
-//  1. router: z = x router_w^T, one block an expert, in FP32 pairs;
-//  2. the grouped top-k of beam_grouped_topk_fwd;
+// reading the chosen experts' weights, each once.  Kernels:
+//  1. router: z = x router_w^T in FP32 pairs;
+//  2. the grouped top-k of beam_grouped_topk_fwd: for up to 16 tokens in every block of the next kernel, two
+//     tokens a warp at most, else as that kernel;
 //  3. up: g, u and a = silu(g) u for each (token, expert) pair;
 //  4. down: each block owns some of the H output columns and adds up all experts' shares of them.
 //
-// Kernels 3 and 4 stream weights through a ring of stages in shared memory: one warp copies rows of weights,
-// and the tokens' rows that they meet, by bulk copies; eight warps multiply, each its own columns of the
-// stage, with m16n8k16 instructions whose left operand is 16 rows of weights (for up: 8 of the gate and the
-// same 8 of the up projection, so that one thread holds g and u of the same place) and whose right one is up
-// to 8 tokens.  Both operands are read 16 bytes a thread: the instruction's columns are the row's in another
-// order, the same for both.  The warps' sums meet in shared memory, in order.  An expert with more than 8 tokens is
-// taken in several passes, the later ones out of the L2 cache.
+// Kernels 3 and 4 give each of a block's eight warps a stream of its own: 16 rows of weights by 64 columns at a
+// time, copied with cp.async some stages ahead into the warp's part of shared memory together with the tokens'
+// rows that they meet (bulk copies of a row's kilobyte, one instruction each, ran at 1.9 TB/s: 1.17 ms for 64 tokens of a
+// tensor-parallel eighth, 0.55 this way).  They are multiplied with m16n8k16 instructions whose left operand is
+// the weights (for up: 8 rows of the gate and the same 8 of the up projection, so that one thread holds g and u of the
+// same place) and whose right one is up to 8 tokens.  Both operands are read 16 bytes a thread: the
+// instruction's columns are the row's in another order, the same for both.  Warps take parts of the columns of
+// the same tile, or where rows are short tiles of their own; their sums meet in shared memory, in order.  An expert
+// with more than 8 tokens is taken in several passes, the later ones out of the L2 cache.
 
 #include "beam_device.cuh"
-#include "beam_tma.cuh"
+#include "beam_routing.cuh"
 #include "decode/decode_mma.cuh"
 #include "draft_kernels.h"
 
@@ -24,77 +27,142 @@ namespace beam {
 namespace {
 
 constexpr int kSms = 152;
-constexpr int kExperts = 256;
-constexpr int kTopK = 8;
 constexpr int kMaxTokens = 256;
 constexpr int kMaxPasses = kExperts + kMaxTokens;  // sum over experts of ceil(pairs / 8)
 constexpr int kPassTokens = 8;
-constexpr int kWarps = 8;                           // that multiply
-constexpr int kConsumers = kWarps * 32;
-constexpr int kThreads = kConsumers + 32;           // and one that copies
-constexpr int kMaxStages = 12;
-constexpr int kMaxStageBytes = 30 * 1024;
-constexpr int kSmem = 227 * 1024;
-
-__device__ unsigned int g_moe_fault_word = 0u;
+constexpr int kWarps = 8;
+constexpr int kThreads = kWarps * 32;
+constexpr int kFusedTokens = 16;   // tokens that the up kernel routes itself
+constexpr int kCols = 64;          // columns of a stage: 128 bytes of a row
+constexpr int kUpStages = 8;
+constexpr int kDownStages = 5;
+constexpr int kMaxSums = 36 * 1024;  // bytes of a slab's sums: 36 rows of 256 tokens
 
 // ---------------------------------------------------------------------------------------------
 // router
 // ---------------------------------------------------------------------------------------------
 
-constexpr int kRouterThreads = 128;
-constexpr int kRouterTokens = 4;  // at a time
+// A block takes two experts and up to 8 tokens; a thread the columns 4 i, i = its number modulo 256, of both.
+// A sum starts at a power of two times 1.5 that is larger than twice all of its terms together: each
+// addition rounds to a grid that the running sum never leaves, so that the part taken up, acc' - acc, is exact, and what is left of
+// the product, one fused multiply-add, goes into a second sum: four instructions a product, where pairs by
+// TwoSum take ten.
+constexpr int kRouterExperts = 2;
+constexpr int kRouterTokens = 8;
+constexpr int kRouterVecs = 5;    // float4s of an expert's row a thread holds: 5,120 columns at a time
+constexpr int kRouterSums = kRouterExperts * kRouterTokens;
 
-__global__ void __launch_bounds__(kRouterThreads)
+__device__ __forceinline__ Sum2 merge_across(Sum2 keep, Sum2 give, int off)
+{
+    Sum2 o;
+    o.hi = __shfl_xor_sync(0xffffffffu, give.hi, off);
+    o.lo = __shfl_xor_sync(0xffffffffu, give.lo, off);
+    return sum_merge(keep, o);
+}
+
+__global__ void __launch_bounds__(kThreads)
     moe_router_kernel(float *logits, const uint16_t *x, int64_t x_stride, const float *router_w,
                       int T, int H)
 {
-    __shared__ Sum2 s_part[kRouterThreads / 32][kRouterTokens];
-    const int e = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const float *w = router_w + (int64_t)e * H;
+    __shared__ Sum2 s_part[kWarps][kRouterSums];
+    const int e0 = blockIdx.x * kRouterExperts, t0 = blockIdx.y * kRouterTokens;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int n = T - t0 < kRouterTokens ? T - t0 : kRouterTokens;
     pdl_launch_dependents();
-    // a model parameter: on its way while the kernel before still runs
-    for (int i = threadIdx.x * 32; i < H; i += kRouterThreads * 32)
-        asm volatile("prefetch.global.L2 [%0];" ::"l"(w + i));
-    pdl_wait();
-    for (int t0 = 0; t0 < T; t0 += kRouterTokens) {
-        Sum2 acc[kRouterTokens];
+    Sum2 total[kRouterSums];  // [expert][token]
 #pragma unroll
-        for (int i = 0; i < kRouterTokens; ++i)
-            acc[i] = Sum2{0.0f, 0.0f};
-        for (int k = threadIdx.x * 4; k < H; k += kRouterThreads * 4) {
-            const float4 wv = *reinterpret_cast<const float4 *>(w + k);
-            const float ws[4] = {wv.x, wv.y, wv.z, wv.w};
+    for (int i = 0; i < kRouterSums; ++i)
+        total[i] = Sum2{0.0f, 0.0f};
+    for (int k0 = 0; k0 < H; k0 += kThreads * 4 * kRouterVecs) {
+        float4 w[kRouterExperts][kRouterVecs];
+        float mw[kRouterExperts];
 #pragma unroll
-            for (int i = 0; i < kRouterTokens; ++i) {
-                if (t0 + i >= T)
-                    continue;
-                const uint2 xv = *reinterpret_cast<const uint2 *>(x + (t0 + i) * x_stride + k);
-                const float xs[4] = {bf_lo(xv.x), bf_hi(xv.x), bf_lo(xv.y), bf_hi(xv.y)};
+        for (int e = 0; e < kRouterExperts; ++e) {
+            mw[e] = 0.0f;
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const float p = __fmul_rn(xs[j], ws[j]);
-                    const float low = __fmaf_rn(xs[j], ws[j], -p);  // exact
-                    float s, err;
-                    two_sum(acc[i].hi, p, s, err);
-                    acc[i] = Sum2{s, __fadd_rn(acc[i].lo, __fadd_rn(err, low))};
-                }
+            for (int v = 0; v < kRouterVecs; ++v) {
+                const int k = k0 + (v * kThreads + threadIdx.x) * 4;
+                w[e][v] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                if (k < H)  // a model parameter: read before waiting on the previous kernel
+                    w[e][v] = *reinterpret_cast<const float4 *>(router_w + (int64_t)(e0 + e) * H + k);
             }
         }
+        if (k0 == 0)
+            pdl_wait();
 #pragma unroll
-        for (int i = 0; i < kRouterTokens; ++i) {
-            const Sum2 v = warp_sum(acc[i]);
-            if (lane == 0)
-                s_part[warp][i] = v;
+        for (int e = 0; e < kRouterExperts; ++e)
+#pragma unroll
+            for (int v = 0; v < kRouterVecs; ++v)
+                mw[e] = fmaxf(fmaxf(fmaxf(mw[e], fabsf(w[e][v].x)), fabsf(w[e][v].y)),
+                              fmaxf(fabsf(w[e][v].z), fabsf(w[e][v].w)));
+#pragma unroll
+        for (int t = 0; t < kRouterTokens; ++t) {
+            if (t >= n)
+                continue;
+            uint2 xv[kRouterVecs];
+            float mx = 0.0f;
+#pragma unroll
+            for (int v = 0; v < kRouterVecs; ++v) {
+                const int k = k0 + (v * kThreads + threadIdx.x) * 4;
+                xv[v] = make_uint2(0u, 0u);
+                if (k < H)
+                    xv[v] = *reinterpret_cast<const uint2 *>(x + (t0 + t) * x_stride + k);
+            }
+            float xs[kRouterVecs][4];
+#pragma unroll
+            for (int v = 0; v < kRouterVecs; ++v) {
+                xs[v][0] = bf_lo(xv[v].x), xs[v][1] = bf_hi(xv[v].x);
+                xs[v][2] = bf_lo(xv[v].y), xs[v][3] = bf_hi(xv[v].y);
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    mx = fmaxf(mx, fabsf(xs[v][j]));
+            }
+#pragma unroll
+            for (int e = 0; e < kRouterExperts; ++e) {
+                // 20 terms of at most mx mw each are below 2^(E + 1), E the exponent of 32 mx mw; 1.5 2^(E + 2)
+                const float bound = __fmul_rn(__fmul_rn(mx, 32.0f), mw[e]);
+                const float seed = __fmul_rn(
+                    __uint_as_float(max(__float_as_uint(bound) & 0x7f800000u, 0x01000000u)), 6.0f);
+                float acc = seed, lo = 0.0f;
+#pragma unroll
+                for (int v = 0; v < kRouterVecs; ++v) {
+                    const float ws[4] = {w[e][v].x, w[e][v].y, w[e][v].z, w[e][v].w};
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const float next = __fmaf_rn(xs[v][j], ws[j], acc);
+                        lo = __fadd_rn(lo, __fmaf_rn(xs[v][j], ws[j], -__fsub_rn(next, acc)));
+                        acc = next;
+                    }
+                }
+                Sum2 &s = total[e * kRouterTokens + t];
+                // a NaN or infinite term: seed or sum is not finite, and the logit is NaN
+                s = sum_merge(s, Sum2{__fsub_rn(acc, seed), lo});
+            }
         }
-        __syncthreads();
-        if (threadIdx.x < kRouterTokens && t0 + (int)threadIdx.x < T) {
-            Sum2 v = s_part[0][threadIdx.x];
-            for (int i = 1; i < kRouterThreads / 32; ++i)
-                v = sum_merge(v, s_part[i][threadIdx.x]);
-            logits[(int64_t)(t0 + threadIdx.x) * kExperts + e] = sum_value(v);
+    }
+    // 16 sums over 32 lanes: each step hands half of the sums to the other half of the lanes
+#pragma unroll
+    for (int half = kRouterSums / 2; half > 0; half /= 2) {
+        const int off = half * 2;  // lanes 16, 8, 4, 2 apart
+        const bool upper = lane & off;
+#pragma unroll
+        for (int i = 0; i < half; ++i) {
+            const Sum2 a = total[i], b = total[i + half];
+            total[i] = merge_across(upper ? b : a, upper ? a : b, off);
         }
-        __syncthreads();
+    }
+    const Sum2 mine = merge_across(total[0], total[0], 1);
+    if ((lane & 1) == 0)
+        s_part[warp][lane >> 1] = mine;
+    __syncthreads();
+    if (threadIdx.x < kRouterSums) {
+        const int e = threadIdx.x / kRouterTokens, t = threadIdx.x % kRouterTokens;
+        Sum2 v = s_part[0][threadIdx.x];
+#pragma unroll
+        for (int i = 1; i < kWarps; ++i)
+            v = sum_merge(v, s_part[i][threadIdx.x]);
+        if (t < n)
+            logits[(int64_t)(t0 + t) * kExperts + e0 + e] = sum_value(v);
     }
 }
 
@@ -104,30 +172,68 @@ __global__ void __launch_bounds__(kRouterThreads)
 
 struct Passes {
     int count;
-    int16_t expert[kMaxPasses];
-    int16_t tokens[kMaxPasses];
-    int16_t pair[kMaxPasses][kPassTokens];  // token * 8 + k
+    int info[kMaxPasses];                   // expert, and the number of its tokens times 2^16
+    uint4 pairs[kMaxPasses];                // 8 16-bit numbers: token * 8 + k
+    __device__ __forceinline__ int expert(int p) const { return info[p] & 0xffff; }
+    __device__ __forceinline__ int tokens(int p) const { return info[p] >> 16; }
+    __device__ __forceinline__ int pair(int p, int j) const
+    {
+        return reinterpret_cast<const int16_t *>(&pairs[p])[j];
+    }
 };
 
-struct Ring {
-    uint64_t full[kMaxStages], empty[kMaxStages];
-    int fail;
+// What building them takes.
+struct PassScratch {
+    int scan[kWarps];
+    int16_t begin[kExperts];                // an expert's first pass
+    int16_t fill[kWarps][kExperts];         // its pairs, by the warp that counted them
+    int32_t ids[kFusedTokens * kTopK];      // of tokens that this block routed
 };
 
-// All threads; `scratch` holds an expert for each pair.  In the order of experts, then of tokens.
-__device__ __forceinline__ void build_passes(Passes &ps, int16_t *scratch, const int32_t *ids, int T,
+__host__ __device__ constexpr int most_passes(int T)
+{
+    return T * kTopK < kExperts + T ? T * kTopK : kExperts + T;
+}
+
+// All threads.  Passes are in the order of experts, an expert's pairs in their own: every block makes the same ones,
+// since blocks share a pass's places.  A warp takes T pairs and counts them by expert, 32 at a time.
+__device__ __forceinline__ void build_passes(Passes &list, PassScratch &ps, const int32_t *ids, int T,
                                              int first, int local)
 {
-    __shared__ int s_sum[kExperts / 32];
-    const int n = T * kTopK;
-    for (int i = threadIdx.x; i < n; i += kThreads)
-        scratch[i] = (int16_t)(ids[i] - first);
+    constexpr int kEach = kMaxTokens / 32;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    for (int i = threadIdx.x; i < kWarps * kExperts; i += kThreads)
+        ps.fill[i / kExperts][i % kExperts] = 0;
     __syncthreads();
-    const int e = threadIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    int mine = 0;
-    if (e < local)
-        for (int i = 0; i < n; ++i)
-            mine += scratch[i] == e;
+    int expert[kEach], place[kEach];
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+        expert[i] = -1;
+        if (i * 32 >= T)
+            continue;
+        const int at = i * 32 + lane;
+        const int e = at < T ? ids[warp * T + at] - first : -1;
+        const bool in = e >= 0 && e < local;
+        const uint32_t same = __match_any_sync(0xffffffffu, in ? e : -1);
+        const uint32_t before = same & ((1u << lane) - 1u);
+        const int had = in ? ps.fill[warp][e] : 0;
+        __syncwarp();
+        if (in) {
+            expert[i] = e;
+            place[i] = had + __popc(before);
+            if (before == 0u)
+                ps.fill[warp][e] = (int16_t)(had + __popc(same));
+        }
+        __syncwarp();
+    }
+    __syncthreads();
+    int mine = 0;  // of expert threadIdx.x; its counts become the pairs in front of each warp's
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+        const int n = ps.fill[w][threadIdx.x];
+        ps.fill[w][threadIdx.x] = (int16_t)mine;
+        mine += n;
+    }
     const int need = (mine + kPassTokens - 1) / kPassTokens;
     int at = need;
 #pragma unroll
@@ -136,230 +242,233 @@ __device__ __forceinline__ void build_passes(Passes &ps, int16_t *scratch, const
         if (lane >= off)
             at += o;
     }
-    if (lane == 31 && warp < kExperts / 32)
-        s_sum[warp] = at;
+    if (lane == 31)
+        ps.scan[warp] = at;
     __syncthreads();
     at -= need;
-    for (int i = 0; i < warp && i < kExperts / 32; ++i)
-        at += s_sum[i];
-    if (e < local && mine > 0) {
-        int put = 0;
-        for (int i = 0; i < n; ++i)
-            if (scratch[i] == e) {
-                ps.pair[at + put / kPassTokens][put % kPassTokens] = (int16_t)i;
-                ++put;
-            }
-        for (int i = 0; i < need; ++i) {
-            ps.expert[at + i] = (int16_t)e;
-            ps.tokens[at + i] =
-                (int16_t)(mine - i * kPassTokens < kPassTokens ? mine - i * kPassTokens : kPassTokens);
+    for (int i = 0; i < warp; ++i)
+        at += ps.scan[i];
+    ps.begin[threadIdx.x] = (int16_t)at;
+    for (int i = 0; i < need; ++i)
+        list.info[at + i] = (int)threadIdx.x | min(mine - i * kPassTokens, kPassTokens) << 16;
+    if (threadIdx.x == kThreads - 1)
+        list.count = at + need;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kEach; ++i)
+        if (expert[i] >= 0) {
+            const int n = ps.fill[warp][expert[i]] + place[i];
+            reinterpret_cast<int16_t *>(
+                &list.pairs[ps.begin[expert[i]] + n / kPassTokens])[n % kPassTokens] =
+                (int16_t)(warp * T + i * 32 + lane);
         }
-    }
-    if (threadIdx.x == kExperts - 1)
-        ps.count = at + need;
     __syncthreads();
 }
 
 // ---------------------------------------------------------------------------------------------
-// the ring
+// the warps' streams
 // ---------------------------------------------------------------------------------------------
 
-// How rows of K columns are cut: segments of `cols` columns (a multiple of 32), the last one shorter.
-struct Cut {
-    int32_t K, cols, segs;
-    int32_t rows;    // rows of weights of a stage
-    int32_t pitch;   // bytes from row to row of a stage: 64 modulo 128, so that eight threads that read
-                     // 16 bytes each of two rows meet all banks
-    int32_t stage_bytes, stages;
+// Where the 16 bytes `c` of row `row` of a stage stand: rows that eight neighbouring threads read together, 2r and
+// 2r + 1, take different halves of the 128 bytes that a row has.
+__device__ __forceinline__ uint32_t swizzled(int row, int c)
+{
+    return (uint32_t)(row * 128 + ((c ^ (((row & 1) << 2) | ((row >> 1) & 3))) << 4));
+}
+
+// Rows of a tile that a lane copies: rows lane / 8 + 4 i of the weights and of the tokens; nullptr: none.
+template <int XR>
+struct Rows {
+    const uint16_t *w[4];
+    const uint16_t *x[XR / 4];
 };
 
-Cut make_cut(int K, int rows, int other_bytes)
+// How a block's tiles are shared out: `parts` warps take a part of a tile's columns each.
+struct Cut {
+    int32_t K, steps, parts;  // columns, stages of a whole tile
+};
+
+Cut make_cut(int K)
 {
     Cut c;
     c.K = K;
-    c.rows = rows;
-    int most = kMaxStageBytes / (2 * (rows + kPassTokens)) / 32 * 32;
-    most = most > 512 ? 512 : most;
-    c.segs = (K + most - 1) / most;
-    c.cols = ((K + c.segs - 1) / c.segs + 31) / 32 * 32;
-    c.segs = (K + c.cols - 1) / c.cols;
-    c.pitch = (c.cols * 2 + 127) / 128 * 128 + 64;
-    c.stage_bytes = (rows + kPassTokens) * c.pitch;
-    c.stages = (kSmem - other_bytes) / c.stage_bytes;
-    c.stages = c.stages > kMaxStages ? kMaxStages : c.stages;
+    c.steps = (K + kCols - 1) / kCols;
+    c.parts = c.steps >= 32 ? 8 : (c.steps >= 16 ? 4 : (c.steps >= 8 ? 2 : 1));
     return c;
 }
 
-// Where copying or multiplying stands in the ring.
-struct Turn {
-    int stage = 0;
-    uint32_t phase = 0;
-    __device__ __forceinline__ void next(int stages)
-    {
-        if (++stage == stages) {
-            stage = 0;
-            phase ^= 1u;
-        }
-    }
-};
+__host__ __device__ constexpr int stage_bytes(int XR) { return (16 + XR) * 128; }
+constexpr int kAreaBytes = 2 * kWarps * 128 * 4;
 
-// The copying warp: all segments of a job, whose row i of weights is at row(i) and goes to the stage's row
-// place(i), and whose token j's row is at token(j).
-template <typename Row, typename Place, typename Token>
-__device__ __forceinline__ void copy_job(char *stages, Ring &ring, Turn &turn, const Cut &c, int rows,
-                                         int tokens, Row row, Place place, Token token)
-{
-    const int lane = threadIdx.x & 31;
-    for (int s = 0; s < c.segs; ++s) {
-        if (!mbar_wait_or_fail(&ring.empty[turn.stage], turn.phase ^ 1u, &ring.fail))
-            return;
-        const int cols = c.K - s * c.cols < c.cols ? c.K - s * c.cols : c.cols;
-        const uint32_t bytes = (uint32_t)cols * 2;
-        uint64_t *bar = &ring.full[turn.stage];
-        if (lane == 0)
-            mbar_arrive_expect_tx(bar, bytes * (uint32_t)(rows + tokens));
-        __syncwarp();
-        char *dst = stages + turn.stage * c.stage_bytes;
-        for (int i = lane; i < rows + tokens; i += 32) {
-            const uint16_t *src = i < rows ? row(i) : token(i - rows);
-            bulk_g2s(dst + (i < rows ? place(i) : c.rows + i - rows) * c.pitch, src + s * c.cols, bytes,
-                     bar);
-        }
-        __syncwarp();
-        turn.next(c.stages);
-    }
-}
-
-// A multiplying warp: its columns of all segments of a job.  Row i of the left operand's 16 MT is the stage's
-// row place(i); acc[m] are rows 16 m + g, 16 m + g + 8 of tokens 2t, 2t + 1.
-template <int MT, typename Place>
-__device__ __forceinline__ void multiply_job(float (&acc)[MT][4], const char *stages, Ring &ring, Turn &turn,
-                                             const Cut &c, int tokens, Place place)
+// All tiles of the block.  rows_of(tile) gives the rows that this lane copies, of which warps take steps;
+// done(round, area) is called by all threads behind a barrier, with the sums [warp][16 rows][8 tokens] of the
+// round's 8 / parts tiles; drained() once by each warp when its last copy is under way.  XR is 8, or 16: the tokens' rows
+// in two parts whose sum they are.
+template <int XR, int D, typename RowsOf, typename Done, typename Drained>
+__device__ __forceinline__ void run_tiles(char *smem, float *area, const Cut &c, int tiles, RowsOf rows_of,
+                                          Done done, Drained drained)
 {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int g = lane >> 2, t = lane & 3;
-    uint32_t at[MT][2];
+    const int at_once = kWarps / c.parts, rounds = (tiles + at_once - 1) / at_once;
+    const int first = warp / c.parts, part = warp % c.parts;
+    const int s0 = c.steps * part / c.parts, steps = c.steps * (part + 1) / c.parts - s0;
+    const int mine = tiles > first ? (tiles - first + at_once - 1) / at_once : 0;
+    const uint32_t base = smem_addr(smem) + warp * D * stage_bytes(XR);
+
+    // copying
+    Rows<XR> rows;
+    int tile = first, step = 0, left = mine * steps, put = 0;
+    const int chunk = lane & 7, row = lane >> 3;
+    auto open_tile = [&]() {
+        rows = rows_of(tile);
+        // past the last column nothing is read, and zeros take its place; rows that are not there are not
+        // copied: what stands in their places reaches only their own sums, which nobody takes
+        const int k = s0 * kCols + chunk * 8 < c.K ? s0 * kCols + chunk * 8 : 0;
 #pragma unroll
-    for (int m = 0; m < MT; ++m)
+        for (int i = 0; i < 4; ++i)
+            rows.w[i] = rows.w[i] ? rows.w[i] + k : nullptr;
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            at[m][h] = place(m * 16 + h * 8 + g) * c.pitch + t * 16;
-            acc[m][2 * h] = acc[m][2 * h + 1] = 0.0f;
-        }
-    const uint32_t xat = (c.rows + (g < tokens ? g : tokens - 1)) * c.pitch + t * 16;
-    for (int s = 0; s < c.segs; ++s) {
-        mbar_wait_or_fail(&ring.full[turn.stage], turn.phase, &ring.fail);
-        const int cols = c.K - s * c.cols < c.cols ? c.K - s * c.cols : c.cols;
-        const uint32_t base = smem_addr(stages + turn.stage * c.stage_bytes);
-        for (int k = warp * 32; k < cols; k += kWarps * 32) {
-            const bool in = k + t * 8 < cols;  // columns come by eights: all or none of a thread's
-            const uint4 none = make_uint4(0, 0, 0, 0);
-            const uint4 x = in ? lds128(base + xat + k * 2) : none;
+        for (int i = 0; i < XR / 4; ++i)
+            rows.x[i] = rows.x[i] ? rows.x[i] + k : nullptr;
+    };
+    auto copy_next = [&]() {
+        if (left > 0) {
+            if (step == 0)
+                open_tile();
+            const uint32_t to = base + put * stage_bytes(XR);
+            const bool in = (s0 + step) * kCols + chunk * 8 < c.K;
 #pragma unroll
-            for (int m = 0; m < MT; ++m) {
-                const uint4 lo = in ? lds128(base + at[m][0] + k * 2) : none;
-                const uint4 hi = in ? lds128(base + at[m][1] + k * 2) : none;
-                const uint32_t f0[4] = {lo.x, hi.x, lo.y, hi.y}, f1[4] = {lo.z, hi.z, lo.w, hi.w};
-                mma16816<false>(acc[m], f0, x.x, x.y);
-                mma16816<false>(acc[m], f1, x.z, x.w);
+            for (int i = 0; i < 4; ++i) {
+                if (rows.w[i])
+                    cp_async16(to + swizzled(i * 4 + row, chunk), rows.w[i] + (in ? step * kCols : 0),
+                               in ? 16u : 0u);
             }
-        }
-        __syncwarp();
-        if (lane == 0)
-            mbar_arrive(&ring.empty[turn.stage]);
-        turn.next(c.stages);
-    }
-}
-
-// This warp's sums to its place of the meeting area: [row][token].
-template <int MT>
-__device__ __forceinline__ void leave_sums(const float (&acc)[MT][4], float *mine)
-{
-    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
 #pragma unroll
-    for (int m = 0; m < MT; ++m) {
-        *reinterpret_cast<float2 *>(mine + (m * 16 + g) * 8 + 2 * t) = make_float2(acc[m][0], acc[m][1]);
-        *reinterpret_cast<float2 *>(mine + (m * 16 + 8 + g) * 8 + 2 * t) =
-            make_float2(acc[m][2], acc[m][3]);
-    }
-}
-
-__device__ __forceinline__ void init_ring(Ring &ring, int stages)
-{
-    if (threadIdx.x == 0) {
-        for (int i = 0; i < stages; ++i) {
-            mbar_init(&ring.full[i], 1);
-            mbar_init(&ring.empty[i], kWarps);
+            for (int i = 0; i < XR / 4; ++i) {
+                if (rows.x[i])
+                    cp_async16(to + 2048 + swizzled(i * 4 + row, chunk),
+                               rows.x[i] + (in ? step * kCols : 0), in ? 16u : 0u);
+            }
+            put = put + 1 == D ? 0 : put + 1;
+            if (++step == steps) {
+                step = 0;
+                tile += at_once;
+            }
+            if (--left == 0)
+                drained();
         }
-        ring.fail = 0;
-        fence_mbar_init();
-    }
-}
+        cp_async_commit();
+    };
+    if (mine == 0)
+        drained();
+    // not unrolled: code that runs once is bound by its fetching
+#pragma unroll 1
+    for (int i = 0; i < D - 1; ++i)
+        copy_next();
 
-// After a wait that ran out: the copies that are still under way end before the block's shared memory goes.
-__device__ __forceinline__ void end_ring(Ring &ring, int stages, Turn turn)
-{
-    if (threadIdx.x < kConsumers || !*(volatile int *)&ring.fail)
-        return;
-    for (int i = 0; i < stages; ++i) {  // the stages before `turn`, latest first
-        if (turn.stage == 0) {
-            turn.stage = stages;
-            turn.phase ^= 1u;
+    int get = 0;
+    for (int round = 0; round < rounds; ++round) {
+        float *sums = area + (round & 1) * kWarps * 128;
+        if (round * at_once + first < tiles) {
+            float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 1
+            for (int s = 0; s < steps; ++s) {
+                cp_async_wait<D - 2>();
+                __syncwarp();
+                copy_next();
+                const uint32_t from = base + get * stage_bytes(XR);
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const uint32_t a = from + swizzled(g, h * 4 + t);
+                    const uint4 lo = lds128(a), hi = lds128(a + 1024);
+                    const uint32_t f0[4] = {lo.x, hi.x, lo.y, hi.y}, f1[4] = {lo.z, hi.z, lo.w, hi.w};
+#pragma unroll
+                    for (int y = 0; y < XR / 8; ++y) {
+                        const uint4 x = lds128(a + 2048 + y * 1024);
+                        mma16816<false>(acc, f0, x.x, x.y);
+                        mma16816<false>(acc, f1, x.z, x.w);
+                    }
+                }
+                get = get + 1 == D ? 0 : get + 1;
+            }
+            float *to = sums + warp * 128;
+            *reinterpret_cast<float2 *>(to + g * 8 + 2 * t) = make_float2(acc[0], acc[1]);
+            *reinterpret_cast<float2 *>(to + (8 + g) * 8 + 2 * t) = make_float2(acc[2], acc[3]);
         }
-        --turn.stage;
-        mbar_wait(&ring.full[turn.stage], turn.phase, 20000000ull);
+        __syncthreads();
+        done(round, sums);
     }
-    if ((threadIdx.x & 31) == 0)
-        atomicOr(&g_moe_fault_word, kFaultCopyTimeout);
+    cp_async_wait<0>();
 }
-
-// ---------------------------------------------------------------------------------------------
-// up: a = bf16(silu(g) u)
-// ---------------------------------------------------------------------------------------------
-
-constexpr int kUpPlaces = 8;  // places (of F) of a job
-
-__host__ __device__ constexpr int meeting_bytes(int MT) { return 2 * kWarps * MT * 16 * 8 * 4; }
 
 struct ShareArgs {
     const uint16_t *x;
     int64_t x_stride;
     const uint16_t *w13, *w2;
-    uint16_t *act;             // [T * 8, F]
+    uint16_t *act;             // [2][T * 8, F]: the activations in two BF16 parts
     uint16_t *out;
     int64_t out_stride;
-    const int32_t *ids;
-    const float *weights;
+    const float *logits, *bias;
+    int32_t *ids;
+    float *weights;
+    Passes *passes;
     int32_t first, local, T, H, F;
     float scaling;
     Cut cut;
-    int32_t block_rows;        // down: most rows of a job
+    int32_t slab;              // down: most rows of a block at a time
 };
 
-// A block's share of the places of all passes: jobs of up to 8 places of one pass.
-struct UpJobs {
+// The block's rows of the down projection: [from, to).
+__device__ __forceinline__ void down_rows(const ShareArgs &a, int block, int blocks, int &from, int &to)
+{
+    from = (int)((int64_t)a.H * block / blocks);
+    to = (int)((int64_t)a.H * (block + 1) / blocks);
+}
+
+// ---------------------------------------------------------------------------------------------
+// up: a = silu(g) u
+// ---------------------------------------------------------------------------------------------
+
+// A block's share of the places (of F) of all passes, in tiles of up to 8 places of one pass: a first run that
+// may start inside a pass, whole passes, a last run.
+struct UpTiles {
     int64_t at, end;
-    int F;
-    int pass, f, n;  // the job at hand
-    int left, jobs;  // places and jobs left of this block's run in the pass
-    __device__ __forceinline__ bool next()
+    int F, first_pass, first_run, first_tiles, whole_tiles, count;
+    __device__ __forceinline__ UpTiles(int64_t from, int64_t to, int F_) : at(from), end(to), F(F_)
     {
-        if (jobs == 0) {
-            if (at >= end)
-                return false;
-            pass = (int)(at / F);
-            f = (int)(at - (int64_t)pass * F);
-            n = 0;
-            const int64_t stop = ((int64_t)pass + 1) * F < end ? ((int64_t)pass + 1) * F : end;
-            left = (int)(stop - at);
-            jobs = (left + kUpPlaces - 1) / kUpPlaces;
-            at = stop;
+        count = first_tiles = first_pass = first_run = 0;
+        whole_tiles = (F + 7) / 8;
+        if (from >= to)
+            return;
+        first_pass = (int)(from / F);
+        const int64_t stop = ((int64_t)first_pass + 1) * F;
+        first_run = (int)((stop < to ? stop : to) - from);
+        first_tiles = (first_run + 7) / 8;
+        const int64_t rest = to - from - first_run;
+        count = first_tiles + (int)(rest / F) * whole_tiles + (int)((rest % F + 7) / 8);
+    }
+    // its pass, first place and number of places
+    __device__ __forceinline__ void get(int i, int &pass, int &f, int &n) const
+    {
+        int run = first_run, tiles = first_tiles, f0;
+        pass = first_pass;
+        if (i < first_tiles) {
+            f0 = (int)(at - (int64_t)first_pass * F);
+        } else {
+            i -= first_tiles;
+            const int over = i / whole_tiles;
+            i -= over * whole_tiles;
+            pass += 1 + over;
+            f0 = 0;
+            const int64_t rest = end - (int64_t)pass * F;
+            run = rest < F ? (int)rest : F;
+            tiles = (run + 7) / 8;
         }
-        f += n;
-        n = (left + jobs - 1) / jobs;  // even: none much smaller than the others
-        left -= n;
-        --jobs;
-        return true;
+        // even: none much smaller than the others
+        f = run * i / tiles;
+        n = run * (i + 1) / tiles - f;
+        f += f0;
     }
 };
 
@@ -367,144 +476,215 @@ __global__ void __launch_bounds__(kThreads, 1) moe_up_kernel(const ShareArgs a)
 {
     extern __shared__ __align__(128) char smem[];
     __shared__ Passes ps;
-    __shared__ Ring ring;
-    char *stages = smem;
-    float *meet = reinterpret_cast<float *>(smem + a.cut.stages * a.cut.stage_bytes);
+    __shared__ PassScratch scratch;
+    float *area = reinterpret_cast<float *>(smem + kWarps * kUpStages * stage_bytes(8));
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     pdl_launch_dependents();
-    init_ring(ring, a.cut.stages);
     pdl_wait();
-    build_passes(ps, reinterpret_cast<int16_t *>(meet), a.ids, a.T, a.first, a.local);
-    const int64_t places = (int64_t)ps.count * a.F;
-    UpJobs jobs{};
-    jobs.F = a.F;
-    jobs.at = places * blockIdx.x / gridDim.x;
-    jobs.end = places * (blockIdx.x + 1) / gridDim.x;
-    Turn turn;
-    if (threadIdx.x >= kConsumers) {
-        while (jobs.next() && !*(volatile int *)&ring.fail) {
-            const uint16_t *w = a.w13 + (int64_t)ps.expert[jobs.pass] * 2 * a.F * a.H;
-            const int n = jobs.n, f = jobs.f, pass = jobs.pass;
-            copy_job(
-                stages, ring, turn, a.cut, 2 * n, ps.tokens[pass],
-                [&](int i) { return w + (int64_t)(i < n ? f + i : a.F + f + i - n) * a.H; },
-                [&](int i) { return i < n ? i : kUpPlaces + i - n; },
-                [&](int j) { return a.x + (ps.pair[pass][j] / kTopK) * a.x_stride; });
+    const bool fused = a.T <= kFusedTokens;
+    if (fused) {
+#pragma unroll 1
+        for (int t = warp; t < a.T; t += kWarps) {
+            const float4 z0 = ld_stream_f4(a.logits + t * kExperts + lane * kPerLane);
+            const float4 z1 = ld_stream_f4(a.logits + t * kExperts + lane * kPerLane + 4);
+            const float4 b0 = *reinterpret_cast<const float4 *>(a.bias + lane * kPerLane);
+            const float4 b1 = *reinterpret_cast<const float4 *>(a.bias + lane * kPerLane + 4);
+            const float z[kPerLane] = {z0.x, z0.y, z0.z, z0.w, z1.x, z1.y, z1.z, z1.w};
+            const float bias[kPerLane] = {b0.x, b0.y, b0.z, b0.w, b1.x, b1.y, b1.z, b1.w};
+            const int id = route_ids(z, bias, lane);
+            if (lane < kTopK)
+                scratch.ids[t * kTopK + lane] = id;
         }
-    } else {
-        const int warp = threadIdx.x >> 5;
-        int buf = 0;
-        while (jobs.next()) {
-            const int n = jobs.n, tokens = ps.tokens[jobs.pass];
-            float acc[1][4];
-            multiply_job<1>(acc, stages, ring, turn, a.cut, tokens, [&](int i) {
-                const int r = i & 7;
-                return (i & 8) + (r < n ? r : n - 1);
-            });
-            float *area = meet + buf * kWarps * 128;
-            leave_sums<1>(acc, area + warp * 128);
-            named_sync(1, kConsumers);
-            // places run fastest: neighbouring threads write neighbouring values
-            const int r = threadIdx.x & 7, j = threadIdx.x >> 3;
-            if (r < n && j < tokens) {
-                float g = 0.0f, u = 0.0f;
+        __syncthreads();
+    }
+    build_passes(ps, scratch, fused ? scratch.ids : a.ids, a.T, a.first, a.local);
+    if (blockIdx.x == 0) {  // for the next kernel
+        for (int i = threadIdx.x; i < ps.count; i += kThreads) {
+            a.passes->info[i] = ps.info[i];
+            a.passes->pairs[i] = ps.pairs[i];
+        }
+        if (threadIdx.x == 0)
+            a.passes->count = ps.count;
+    }
+    const int64_t places = (int64_t)ps.count * a.F;
+    const UpTiles tiles(places * blockIdx.x / gridDim.x, places * (blockIdx.x + 1) / gridDim.x, a.F);
+    const int64_t n_act = (int64_t)a.T * kTopK * a.F;
+    run_tiles<8, kUpStages>(
+        smem, area, a.cut, tiles.count,
+        [&](int i) {
+            int pass, f, n;
+            tiles.get(i, pass, f, n);
+            const uint16_t *w = a.w13 + ((int64_t)ps.expert(pass) * 2 * a.F + f) * a.H;
+            Rows<8> r;
 #pragma unroll
-                for (int w = 0; w < kWarps; ++w) {
-                    g += area[w * 128 + r * 8 + j];
-                    u += area[w * 128 + (8 + r) * 8 + j];
+            for (int j = 0; j < 4; ++j) {  // rows 0-7: gate; 8-15: up
+                const int row = (lane >> 3) + 4 * j;
+                r.w[j] = (row & 7) < n ? w + ((row & 7) + (row < 8 ? 0 : (int64_t)a.F)) * a.H : nullptr;
+            }
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const int row = (lane >> 3) + 4 * j;
+                r.x[j] = row < ps.tokens(pass) ? a.x + (ps.pair(pass, row) / kTopK) * a.x_stride : nullptr;
+            }
+            return r;
+        },
+        [&](int round, const float *sums) {
+            const int parts = a.cut.parts, at_once = kWarps / parts;
+            // places run fastest: neighbouring threads write neighbouring values
+            for (int i = threadIdx.x; i < at_once * 64; i += kThreads) {
+                const int tile = round * at_once + (i >> 6), r = i & 7, j = (i >> 3) & 7;
+                if (tile >= tiles.count)
+                    break;
+                int pass, f, n;
+                tiles.get(tile, pass, f, n);
+                if (r >= n || j >= ps.tokens(pass))
+                    continue;
+                const float *from = sums + (i >> 6) * parts * 128 + r * 8 + j;
+                float g = 0.0f, u = 0.0f;
+                for (int w = 0; w < parts; ++w) {
+                    g += from[w * 128];
+                    u += from[w * 128 + 64];
                 }
                 const float v = __fdiv_rn(g, 1.0f + expf(-g)) * u;
-                a.act[(int64_t)ps.pair[jobs.pass][j] * a.F + jobs.f + r] =
-                    (uint16_t)pack_bf16x2(v, 0.0f);
+                const uint32_t hi = pack_bf16x2(v, 0.0f);
+                uint16_t *to = a.act + (int64_t)ps.pair(pass, j) * a.F + f + r;
+                to[0] = (uint16_t)hi;
+                to[n_act] = (uint16_t)pack_bf16x2(__fsub_rn(v, bf_lo(hi)), 0.0f);
             }
-            buf ^= 1;
-        }
-    }
-    end_ring(ring, a.cut.stages, turn);
+        },
+        [&]() {
+            // This warp's last weights are on their way.  The choice's own weights are of use to the next kernel only.
+            if (fused && blockIdx.x == 0) {
+#pragma unroll 1
+                for (int t = warp; t < a.T; t += kWarps) {
+                    const int id = lane < kTopK ? scratch.ids[t * kTopK + lane] : 0;
+                    const float w = route_weight(lane < kTopK ? a.logits[t * kExperts + id] : 0.0f);
+                    if (lane < kTopK) {
+                        a.ids[t * kTopK + lane] = id;
+                        a.weights[t * kTopK + lane] = w;
+                    }
+                }
+            }
+            // The first weights that the next kernel's block here reads, up to 192 KB of them, are brought to the L2
+            // cache while that kernel starts.
+            if (warp != 0)
+                return;
+            int from, to;
+            down_rows(a, blockIdx.x, gridDim.x, from, to);
+            const uint32_t bytes = (uint32_t)(to - from) * (uint32_t)a.F * 2u;
+            for (int p = lane; p < ps.count && bytes > 0 && (p + 1) * (int64_t)bytes <= 192 * 1024; p += 32)
+                asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(
+                                 a.w2 + ((int64_t)ps.expert(p) * a.H + from) * a.F),
+                             "r"(bytes)
+                             : "memory");
+        });
 }
 
 // ---------------------------------------------------------------------------------------------
 // down: out = sum over the pairs of scaling * weight * w2 a
 // ---------------------------------------------------------------------------------------------
 
-template <int MT>
 __global__ void __launch_bounds__(kThreads, 1) moe_down_kernel(const ShareArgs a)
 {
     extern __shared__ __align__(128) char smem[];
     __shared__ Passes ps;
-    __shared__ Ring ring;
-    char *stages = smem;
-    float *meet = reinterpret_cast<float *>(smem + a.cut.stages * a.cut.stage_bytes);
-    float *sums = meet + meeting_bytes(MT) / 4;  // [token][row of the block's]
+    float *area = reinterpret_cast<float *>(smem + kWarps * kDownStages * stage_bytes(16));
+    float *sums = area + kAreaBytes / 4;  // [token][row of the block's]
+    const int lane = threadIdx.x & 31;
     pdl_launch_dependents();
-    init_ring(ring, a.cut.stages);
     pdl_wait();
-    build_passes(ps, reinterpret_cast<int16_t *>(meet), a.ids, a.T, a.first, a.local);
-    const int r_end = (int)((int64_t)a.H * (blockIdx.x + 1) / gridDim.x);
-    Turn turn;
-    int r0 = (int)((int64_t)a.H * blockIdx.x / gridDim.x);
-    if (threadIdx.x >= kConsumers) {
-        for (; r0 < r_end && !*(volatile int *)&ring.fail; r0 += a.block_rows) {
-            const int n = r_end - r0 < a.block_rows ? r_end - r0 : a.block_rows;
-            for (int p = 0; p < ps.count && !*(volatile int *)&ring.fail; ++p) {
-                const uint16_t *w = a.w2 + ((int64_t)ps.expert[p] * a.H + r0) * a.F;
-                copy_job(
-                    stages, ring, turn, a.cut, n, ps.tokens[p],
-                    [&](int i) { return w + (int64_t)i * a.F; }, [](int i) { return i; },
-                    [&](int j) { return a.act + (int64_t)ps.pair[p][j] * a.F; });
-            }
-        }
-    } else {
-        const int warp = threadIdx.x >> 5;
-        int buf = 0;
-        for (; r0 < r_end; r0 += a.block_rows) {
-            const int n = r_end - r0 < a.block_rows ? r_end - r0 : a.block_rows;
-            for (int i = threadIdx.x; i < a.T * a.block_rows; i += kConsumers)
-                sums[i] = 0.0f;
-            for (int p = 0; p < ps.count; ++p) {
-                const int tokens = ps.tokens[p];
-                float acc[MT][4];
-                multiply_job<MT>(acc, stages, ring, turn, a.cut, tokens,
-                                 [&](int i) { return i < n ? i : n - 1; });
-                float *area = meet + buf * kWarps * MT * 128;
-                leave_sums<MT>(acc, area + warp * MT * 128);
-                named_sync(1, kConsumers);
-                for (int i = threadIdx.x; i < n * 8; i += kConsumers) {
-                    const int j = i & 7;
-                    if (j < tokens) {
-                        float v = 0.0f;
+    const int most = most_passes(a.T);
+    for (int i = threadIdx.x; i < most; i += kThreads) {
+        ps.info[i] = a.passes->info[i];
+        ps.pairs[i] = ld_plain(&a.passes->pairs[i]);
+    }
+    if (threadIdx.x == 0)
+        ps.count = a.passes->count;
+    float *weight = sums + a.T * a.slab;  // [pair]
+    for (int i = threadIdx.x; i < a.T * kTopK; i += kThreads)
+        weight[i] = a.scaling * a.weights[i];
+    __syncthreads();
+    int r0, r1;
+    down_rows(a, blockIdx.x, gridDim.x, r0, r1);
+    const int64_t n_act = (int64_t)a.T * kTopK * a.F;
+    for (; r0 < r1; r0 += a.slab) {
+        const int rows = min(r1 - r0, a.slab), row_tiles = (rows + 15) / 16, tiles = row_tiles * ps.count;
+        for (int i = threadIdx.x; i < a.T * rows; i += kThreads)
+            sums[i] = 0.0f;
+        run_tiles<16, kDownStages>(
+            smem, area, a.cut, tiles,
+            [&](int i) {
+                const int rt = i / ps.count, pass = i - rt * ps.count;
+                const int from = rows * rt / row_tiles, n = rows * (rt + 1) / row_tiles - from;
+                const uint16_t *w = a.w2 + ((int64_t)ps.expert(pass) * a.H + r0 + from) * a.F;
+                Rows<16> r;
 #pragma unroll
-                        for (int w = 0; w < kWarps; ++w)
-                            v += area[w * MT * 128 + i];
-                        const int pair = ps.pair[p][j];
-                        float *s = sums + (pair / kTopK) * a.block_rows + (i >> 3);
-                        *s = __fmaf_rn(a.scaling * a.weights[pair], v, *s);
+                for (int j = 0; j < 4; ++j) {
+                    const int row = (lane >> 3) + 4 * j;
+                    r.w[j] = row < n ? w + (int64_t)row * a.F : nullptr;
+                }
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    const int row = (lane >> 3) + 4 * j;
+                    r.x[j] = r.x[j + 2] = nullptr;
+                    if (row < ps.tokens(pass)) {
+                        r.x[j] = a.act + (int64_t)ps.pair(pass, row) * a.F;
+                        r.x[j + 2] = r.x[j] + n_act;
                     }
                 }
-                buf ^= 1;
-            }
-            named_sync(1, kConsumers);
-            for (int i = threadIdx.x; i < a.T * n; i += kConsumers) {
-                const int t = i / n, r = i - t * n;
-                a.out[t * a.out_stride + r0 + r] =
-                    (uint16_t)pack_bf16x2(sums[t * a.block_rows + r], 0.0f);
-            }
-            named_sync(1, kConsumers);
+                return r;
+            },
+            [&](int round, const float *part_sums) {
+                const int parts = a.cut.parts, at_once = kWarps / parts;
+                // a thread owns a row of each tile and the tokens of its class: sums grow in the order of the
+                // tiles
+                const int r = threadIdx.x & 15, mine = threadIdx.x >> 4;
+                const int end = min(tiles, (round + 1) * at_once);
+                int rt = round * at_once / ps.count, pass = round * at_once - rt * ps.count;
+                for (int i = round * at_once; i < end; ++i) {
+                    const int from = rows * rt / row_tiles, n = rows * (rt + 1) / row_tiles - from;
+                    const uint4 pairs = ps.pairs[pass];
+                    const int tokens = ps.tokens(pass);
+                    const float *v0 = part_sums + (i - round * at_once) * parts * 128 + r * 8;
+#pragma unroll
+                    for (int j = 0; j < kPassTokens; ++j) {
+                        if (j >= tokens)
+                            break;
+                        const int pair = (word(pairs, j / 2) >> (16 * (j & 1))) & 0xffff, t = pair / kTopK;
+                        if ((t & 15) != mine || r >= n)
+                            continue;
+                        float v = 0.0f;
+                        for (int w = 0; w < parts; ++w)
+                            v += v0[w * 128 + j];
+                        float *s = sums + t * rows + from + r;
+                        *s = __fmaf_rn(weight[pair], v, *s);
+                    }
+                    if (++pass == ps.count) {
+                        pass = 0;
+                        ++rt;
+                    }
+                }
+            },
+            []() {});
+        __syncthreads();
+        for (int i = threadIdx.x; i < a.T * rows; i += kThreads) {
+            const int t = i / rows, r = i - t * rows;
+            a.out[t * a.out_stride + r0 + r] = (uint16_t)pack_bf16x2(sums[i], 0.0f);
         }
+        __syncthreads();
     }
-    end_ring(ring, a.cut.stages, turn);
 }
 
 template <auto Kernel>
 cudaError_t launch_share(const ShareArgs &s, int grid, int smem, cudaStream_t stream)
 {
-    static bool done[64] = {};
+    static int done[64] = {};  // the most shared memory that was asked for
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
-    if (e == cudaSuccess && (dev >= 64 || !done[dev])) {
-        e = cudaFuncSetAttribute(Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 kSmem - (int)(sizeof(Passes) + sizeof(Ring) + 64));
+    if (e == cudaSuccess && (dev >= 64 || done[dev] < smem)) {
+        e = cudaFuncSetAttribute(Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
         if (e == cudaSuccess && dev < 64)
-            done[dev] = true;
+            done[dev] = smem;
     }
     return e == cudaSuccess
                ? launch_pdl(Kernel, dim3((unsigned)grid), dim3(kThreads), (size_t)smem, stream, s)
@@ -519,8 +699,9 @@ MoePlan moe_plan(int64_t T, int32_t H, int32_t F)
     p.logits = 0;
     p.ids = T * kExperts * 4;
     p.weights = p.ids + T * kTopK * 4;
-    p.act = p.weights + T * kTopK * 4;
-    p.bytes = p.act + T * kTopK * F * 2;
+    p.passes = p.weights + T * kTopK * 4;
+    p.act = p.passes + (int64_t)sizeof(Passes);
+    p.bytes = p.act + 2 * T * kTopK * F * 2;
     return p;
 }
 
@@ -535,57 +716,46 @@ cudaError_t launch_moe_layer(const MoeArgs &a, const MoePlan &p, cudaStream_t st
     s.act = (uint16_t *)(a.workspace + p.act);
     s.out = (uint16_t *)a.out;
     s.out_stride = a.out_stride;
-    int32_t *ids = a.ids ? a.ids : (int32_t *)(a.workspace + p.ids);
-    float *weights = a.weights ? a.weights : (float *)(a.workspace + p.weights);
-    s.ids = ids;
-    s.weights = weights;
+    s.logits = logits;
+    s.bias = a.router_bias;
+    s.ids = a.ids ? a.ids : (int32_t *)(a.workspace + p.ids);
+    s.weights = a.weights ? a.weights : (float *)(a.workspace + p.weights);
+    s.passes = (Passes *)(a.workspace + p.passes);
     s.first = a.first;
     s.local = a.local;
     s.T = a.T;
     s.H = a.H;
     s.F = a.F;
     s.scaling = a.scaling;
-    cudaError_t e = launch_pdl(moe_router_kernel, dim3(kExperts), dim3(kRouterThreads), 0, stream, logits,
-                               s.x, s.x_stride, a.router_w, a.T, a.H);
-    if (e == cudaSuccess) {
+    cudaError_t e = launch_pdl(moe_router_kernel,
+                               dim3(kExperts / kRouterExperts, (a.T + kRouterTokens - 1) / kRouterTokens),
+                               dim3(kThreads), 0, stream, logits, s.x, s.x_stride, a.router_w, a.T, a.H);
+    if (e == cudaSuccess && a.T > kFusedTokens) {
         RouteArgs r{};
         r.logits = logits;
         r.bias = a.router_bias;
-        r.ids = ids;
-        r.weights = weights;
+        r.ids = s.ids;
+        r.weights = s.weights;
         r.T = a.T;
         e = launch_grouped_topk(r, stream);
     }
-    const int fixed = (int)(sizeof(Passes) + sizeof(Ring) + 64);
+    // both kernels have a block an SM: a block of the second finds its first weights in the L2 cache
+    const int down = a.H < kSms ? a.H : kSms;
     if (e == cudaSuccess) {
-        // the pairs' experts lie in the meeting area while the passes are made
-        const int other = meeting_bytes(1);
-        s.cut = make_cut(a.H, 2 * kUpPlaces, fixed + other);
-        e = launch_share<moe_up_kernel>(s, kSms, s.cut.stages * s.cut.stage_bytes + other, stream);
+        s.cut = make_cut(a.H);
+        e = launch_share<moe_up_kernel>(s, kSms, kWarps * kUpStages * stage_bytes(8) + kAreaBytes, stream);
     }
     if (e == cudaSuccess) {
-        const int grid = a.H < kSms ? a.H : kSms;
-        const int own = (a.H + grid - 1) / grid;
-        s.block_rows = (own + (own + 47) / 48 - 1) / ((own + 47) / 48);
-        const int MT = (s.block_rows + 15) / 16;
-        const int other = meeting_bytes(MT) + a.T * s.block_rows * 4;
-        s.cut = make_cut(a.F, s.block_rows, fixed + other);
-        const int smem = s.cut.stages * s.cut.stage_bytes + other;
-        e = MT == 1   ? launch_share<moe_down_kernel<1>>(s, grid, smem, stream)
-            : MT == 2 ? launch_share<moe_down_kernel<2>>(s, grid, smem, stream)
-                      : launch_share<moe_down_kernel<3>>(s, grid, smem, stream);
+        s.cut = make_cut(a.F);
+        const int own = (a.H + down - 1) / down, most = kMaxSums / (a.T * 4);
+        const int slabs = (own + most - 1) / most;
+        s.slab = (own + slabs - 1) / slabs;
+        e = launch_share<moe_down_kernel>(s, down,
+                                          kWarps * kDownStages * stage_bytes(16) + kAreaBytes +
+                                              a.T * (s.slab + kTopK) * 4,
+                                          stream);
     }
     return e != cudaSuccess ? e : cudaGetLastError();
-}
-
-cudaError_t read_draft_fault_word(unsigned int *value, bool clear)
-{
-    cudaError_t e = cudaMemcpyFromSymbol(value, g_moe_fault_word, sizeof(unsigned int));
-    if (e == cudaSuccess && clear) {
-        const unsigned int zero = 0u;
-        e = cudaMemcpyToSymbol(g_moe_fault_word, &zero, sizeof(unsigned int));
-    }
-    return e;
 }
 
 }  // namespace beam

@@ -114,8 +114,8 @@ def moe_layer(x, ids, weights, w13, w2, first, scaling):
             g, u = gu[:F], gu[F:]
             sig = torch.sigmoid(g)
             a = g * sig * u
-            # |silu'| <= 1.1; then BF16
-            da = 1.1 * d[:F] * u.abs() + (g * sig).abs() * d[F:] + (BF16 + 16 * U32) * a.abs()
+            # |silu'| <= 1.1; then two BF16 parts
+            da = 1.1 * d[:F] * u.abs() + (g * sig).abs() * d[F:] + (BF16 ** 2 + 16 * U32) * a.abs()
             da += 1.1 * d[:F] * d[F:]
             c = float(np.float32(scaling)) * float(weights[t, k])
             y = a2 @ a
@@ -158,7 +158,7 @@ def verify(tokens, target, draft, u_accept, u_sample, lens=None):
         S, run, token = sum(w), 0, -1
         u = float(u_sample[b])
         u = 0.0 if u != u else min(max(u, 0.0), float(np.float32(0.99999994)))
-        border = int(u * 2.0 ** 64) * S >> 64
+        border = int(u * 2.0 ** 24) * S >> 24
         for v, i in enumerate(w):
             run += i
             if run > border:
