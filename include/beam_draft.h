@@ -96,8 +96,8 @@ BEAM_API int64_t beam_attn_kv4_workspace(int32_t B, int32_t q_len, int32_t n_q_h
  *   g = w_gate_up[e, 0..F) x[t]    u = w_gate_up[e, F..2F) x[t]    a = g / (1 + exp(-g)) * u
  *   out[t] = bf16( sum over k of (routed_scaling * w[t, k]) * w_down[ids[t, k]] a[t, k] )
  * The logits z are sums of the exact products in FP32 pairs, rounded once to FP32, so that the choice does
- * not hang on the order of a sum.  The experts' sums, g, u and the sum over k (in the order of the experts'
- * numbers) are FP32; a goes into the down product as the sum of two BF16 values, its
+ * not hang on the order of a sum.  The experts' sums, g, u and the sum over k (in the order of k) are
+ * FP32; a goes into the down product as the sum of two BF16 values, its
  * rounding and the rounding of the rest (an error of at most 2^-16 of each).
  * The call computes the part of the experts [first_expert, first_expert + n_local), whose weights it gets
  * (the others are another rank's), with F their intermediate columns on this rank: for expert- and

@@ -78,7 +78,8 @@ struct MoeArgs {
 
 // Byte offsets in the workspace.
 struct MoePlan {
-    int64_t logits, ids, weights, passes, act, bytes;
+    int64_t logits, ids, weights, passes, act, sums, bytes;
+    int64_t sum_rows;
 };
 
 MoePlan moe_plan(int64_t T, int32_t H, int32_t F);

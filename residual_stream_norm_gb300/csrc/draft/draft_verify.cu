@@ -19,12 +19,12 @@ namespace cg = cooperative_groups;
 namespace beam {
 namespace {
 
-constexpr int kThreads = 512;
+constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kMaxCluster = 8;
 
 template <bool BF16>
-__device__ __forceinline__ float prob(const void *row, int64_t v)
+__device__ __forceinline__ float prob(const void *row, int v)
 {
     if constexpr (BF16)
         return __uint_as_float((uint32_t)((const uint16_t *)row)[v] << 16);
@@ -33,12 +33,13 @@ __device__ __forceinline__ float prob(const void *row, int64_t v)
 }
 
 // rint(2^44 p) = 2^22 hi + lo, p limited to [0, 1]; NaN: 0.  A conversion to 64 bits goes through the FP64
-// pipe, which is narrow here (124 us for 128 rows of 160,000 with it, 39 with this): two FP32 additions to 2^23
-// do it, which leave a whole number in the mantissa, the first one cut off, the second rounded to nearest even.
-// What the first cuts off is exact, and the halves' ties are those of the whole.
+// pipe, which is narrow here: two FP32 additions to 2^23 do it, which leave a whole number in the
+// mantissa's bits, the first one cut off, the second rounded to nearest even.  What the first cuts off is exact, and
+// the lower part's ties are those of the whole.  Both parts come with the bits of 2^23 on top.
 struct Units {
     int32_t hi, lo;
 };
+constexpr int32_t kNone = 0x4b000000;  // either part of 0
 
 __device__ __forceinline__ Units units(float p)
 {
@@ -46,57 +47,118 @@ __device__ __forceinline__ Units units(float p)
     const float x = __fmul_rn(fminf(fmaxf(p, 0.0f), 1.0f), k22);
     const float h = __fadd_rz(x, k23);
     const float l = __fadd_rn(__fmul_rn(__fsub_rn(x, __fsub_rn(h, k23)), k22), k23);
-    return Units{(int32_t)(__float_as_uint(h) - 0x4b000000u), (int32_t)(__float_as_uint(l) - 0x4b000000u)};
+    return Units{(int32_t)__float_as_uint(h), (int32_t)__float_as_uint(l)};
 }
 
-__device__ __forceinline__ int64_t whole(int32_t hi, int32_t lo) { return ((int64_t)hi << 22) + lo; }
+__device__ __forceinline__ uint64_t whole(int32_t hi, int32_t lo)
+{
+    return (uint64_t)(((int64_t)hi << 22) + lo);
+}
 
 // The rows that a sequence's last token is drawn from.
 struct Rows {
     const void *target;
     const void *draft;  // nullptr: none
-    int64_t spike;      // the draft is all on this token (-1: not so)
+    int32_t spike;      // the draft is all on this token (-1: not so)
 };
 
-// Weight of a token as 2^22 hi + lo.
-__device__ __forceinline__ Units weight_of(float p, float q, bool spike)
+// Weight of a token, 2^22 hi + lo.
+template <bool Draft>
+__device__ __forceinline__ Units weight_of(float p, float q)
 {
-    const Units a = units(p), b = units(q);
+    const Units a = units(p), b = Draft ? units(q) : Units{kNone, kNone};
     Units w{a.hi - b.hi, a.lo - b.lo};
     // its sign is that of hi unless hi is 0, since |lo| <= 2^22
-    if (spike || w.hi < 0 || (w.hi == 0 && w.lo < 0))
+    if (Draft && (w.hi < 0 || (w.hi == 0 && w.lo < 0)))
         w.hi = w.lo = 0;
     return w;
 }
 
 template <bool BF16>
-__device__ __forceinline__ Units weight_at(const Rows &r, int64_t v)
+__device__ __forceinline__ uint64_t weight_at(const Rows &r, int v)
 {
-    return weight_of(prob<BF16>(r.target, v), r.draft ? prob<BF16>(r.draft, v) : 0.0f, v == r.spike);
+    if (v == r.spike)
+        return 0;
+    const Units w = r.draft ? weight_of<true>(prob<BF16>(r.target, v), prob<BF16>(r.draft, v))
+                            : weight_of<false>(prob<BF16>(r.target, v), 0.0f);
+    return whole(w.hi, w.lo);
 }
 
-// Sum of the weights of tokens [v0, v1), one lane's share.
+// 16 bytes of probabilities.
 template <bool BF16>
-__device__ __forceinline__ uint64_t sum_stretch(const Rows &r, int64_t v0, int64_t v1, int lane)
+__device__ __forceinline__ void unpack(float (&p)[BF16 ? 8 : 4], const uint4 &v)
 {
-    constexpr int kEach = 8;
-    uint64_t sum = 0;
-    for (int64_t v = v0 + lane; v < v1; v += 32 * kEach) {
-        float p[kEach], q[kEach];
 #pragma unroll
-        for (int i = 0; i < kEach; ++i) {
-            const bool in = v + 32 * i < v1;
-            p[i] = in ? prob<BF16>(r.target, v + 32 * i) : 0.0f;
-            q[i] = in && r.draft ? prob<BF16>(r.draft, v + 32 * i) : 0.0f;
+    for (int i = 0; i < 4; ++i) {
+        if constexpr (BF16) {
+            p[2 * i] = bf_lo(word(v, i));
+            p[2 * i + 1] = bf_hi(word(v, i));
+        } else {
+            p[i] = __uint_as_float(word(v, i));
         }
-        int32_t hi = 0, lo = 0;  // of 8 tokens: well within 32 bits
+    }
+}
+
+// Sum of the weights of tokens [v0, v1), one lane's share, but for a spike.  Rows that start on 16 bytes are
+// read 16 bytes a lane (v0 and v1 are multiples of 8, but for the row's end), others token by token.
+template <bool BF16, bool Draft>
+__device__ __forceinline__ uint64_t sum_stretch(const Rows &r, int v0, int v1, int lane)
+{
+    uint64_t sum = 0;
+    int v = v0;
+    if (((uintptr_t)r.target | (uintptr_t)r.draft) % 16 == 0) {
+        constexpr int kVec = BF16 ? 8 : 4, kAhead = 4;
+        const uint4 *tp = reinterpret_cast<const uint4 *>(r.target);
+        const uint4 *dp = reinterpret_cast<const uint4 *>(r.draft);
+        const int end = v1 / kVec;
+#pragma unroll 1
+        for (int i0 = v0 / kVec; i0 < end; i0 += 32 * kAhead) {
+            uint4 p[kAhead], q[kAhead];
 #pragma unroll
-        for (int i = 0; i < kEach; ++i) {
-            const Units w = weight_of(p[i], q[i], v + 32 * i == r.spike);
+            for (int k = 0; k < kAhead; ++k) {
+                const int i = i0 + k * 32 + lane;
+                p[k] = q[k] = make_uint4(0, 0, 0, 0);
+                if (i < end) {
+                    p[k] = ld_cached(tp + i);
+                    if (Draft)
+                        q[k] = ld_cached(dp + i);
+                }
+            }
+            int32_t hi = 0, lo = 0;  // of at most 32 tokens: within 32 bits
+#pragma unroll
+            for (int k = 0; k < kAhead; ++k) {
+                float x[kVec], y[kVec];
+                unpack<BF16>(x, p[k]);
+                unpack<BF16>(y, q[k]);
+#pragma unroll
+                for (int j = 0; j < kVec; ++j) {
+                    const Units w = weight_of<Draft>(x[j], y[j]);
+                    hi += w.hi;
+                    lo += w.lo;
+                }
+            }
+            sum += whole(hi, lo);
+        }
+        v = max(v0, end * kVec);  // the row's end
+    }
+    constexpr int kAhead = 8;
+#pragma unroll 1
+    for (; v < v1; v += 32 * kAhead) {
+        float p[kAhead], q[kAhead];
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+            const int i = v + k * 32 + lane;
+            p[k] = i < v1 ? prob<BF16>(r.target, i) : 0.0f;
+            q[k] = Draft && i < v1 ? prob<BF16>(r.draft, i) : 0.0f;
+        }
+        int32_t hi = 0, lo = 0;
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+            const Units w = weight_of<Draft>(p[k], q[k]);
             hi += w.hi;
             lo += w.lo;
         }
-        sum += (uint64_t)whole(hi, lo);
+        sum += whole(hi, lo);
     }
     return sum;
 }
@@ -124,7 +186,7 @@ __device__ __forceinline__ uint64_t warp_below64(uint64_t v, int lane, uint64_t 
 }
 
 template <bool BF16>
-__global__ void __launch_bounds__(kThreads) draft_verify_kernel(const VerifyArgs a)
+__global__ void __launch_bounds__(kThreads, 4) draft_verify_kernel(const VerifyArgs a)
 {
     __shared__ uint64_t s_w[2][kWarps];  // the stretches' sums, read by all blocks of the cluster
     __shared__ uint64_t s_scan[kWarps];
@@ -149,9 +211,9 @@ __global__ void __launch_bounds__(kThreads) draft_verify_kernel(const VerifyArgs
         if (i < n) {
             const int64_t x = a.tokens[b * k + i];
             if (x >= 0 && x < a.V) {
-                const float p = prob<BF16>(target + i * a.target_pos * (BF16 ? 2 : 4), x);
+                const float p = prob<BF16>(target + i * a.target_pos * (BF16 ? 2 : 4), (int)x);
                 const float q =
-                    a.draft ? prob<BF16>(draft + i * a.draft_pos * (BF16 ? 2 : 4), x) : 1.0f;
+                    a.draft ? prob<BF16>(draft + i * a.draft_pos * (BF16 ? 2 : 4), (int)x) : 1.0f;
                 // the FP32 factors' product is exact in 64 bits
                 ok = (double)a.u_accept[b * k + i] * (double)q < (double)p;
             }
@@ -168,22 +230,28 @@ __global__ void __launch_bounds__(kThreads) draft_verify_kernel(const VerifyArgs
     if (acc < n) {
         if (a.draft)
             r.draft = draft + acc * a.draft_pos * (BF16 ? 2 : 4);
-        else
-            r.spike = a.tokens[b * k + acc];
+        else {
+            const int64_t x = a.tokens[b * k + acc];
+            r.spike = x >= 0 && x < a.V ? (int)x : -1;
+        }
     }
 
     // ---- sums of this warp's stretch --------------------------------------------------------------
-    const int64_t stretches = (int64_t)ranks * kWarps;
-    const int64_t each = (a.V + stretches - 1) / stretches;
-    const int64_t mine = (int64_t)rank * kWarps + warp;
-    const int64_t v0 = mine * each < a.V ? mine * each : a.V;
-    const int64_t v1 = v0 + each < a.V ? v0 + each : a.V;
+    const int V = (int)a.V, stretches = ranks * kWarps;
+    const int each = ((V + stretches - 1) / stretches + 7) & ~7;
+    const int v0 = min((rank * kWarps + warp) * each, V), v1 = min(v0 + each, V);
     uint64_t w[4], below = 0, total = 0;
     const int per = (int)((stretches + 31) / 32);
     for (int again = 0;; ++again) {
-        const uint64_t sum = warp_sum64(sum_stretch<BF16>(r, v0, v1, lane));
-        if (lane == 0)
+        uint64_t sum = warp_sum64(r.draft ? sum_stretch<BF16, true>(r, v0, v1, lane)
+                                          : sum_stretch<BF16, false>(r, v0, v1, lane));
+        if (lane == 0) {
+            if (r.spike >= v0 && r.spike < v1) {
+                const Units x = weight_of<false>(prob<BF16>(r.target, r.spike), 0.0f);
+                sum -= whole(x.hi, x.lo);
+            }
             s_w[again][warp] = sum;
+        }
         cluster.sync();
         // every warp of every block: all stretches' sums, at most 4 a lane, in order
         uint64_t own = 0;
@@ -221,17 +289,15 @@ __global__ void __launch_bounds__(kThreads) draft_verify_kernel(const VerifyArgs
         at = __shfl_sync(0xffffffffu, at, owner);
         start = __shfl_sync(0xffffffffu, start, owner);
         // ---- the stretch's block searches it: a thread takes consecutive tokens -------------------
-        int64_t token = -1;
+        int token = -1;
         const bool here = rank == (at >= 0 ? at / kWarps : 0);
         if (here && at >= 0) {
-            const int64_t f0 = at * each, f1 = f0 + each < a.V ? f0 + each : a.V;
-            const int64_t few = (f1 - f0 + kThreads - 1) / kThreads;
-            const int64_t t0 = f0 + threadIdx.x * few;
+            const int f0 = at * each, f1 = min(f0 + each, V);
+            const int few = (each + kThreads - 1) / kThreads;
+            const int t0 = f0 + threadIdx.x * few, t1 = min(t0 + few, f1);
             uint64_t own = 0;
-            for (int64_t v = t0; v < t0 + few && v < f1; ++v) {
-                const Units x = weight_at<BF16>(r, v);
-                own += (uint64_t)whole(x.hi, x.lo);
-            }
+            for (int v = t0; v < t1; ++v)
+                own += weight_at<BF16>(r, v);
             uint64_t all;
             uint64_t run = warp_below64(own, lane, all);
             if (lane == 0)
@@ -243,14 +309,13 @@ __global__ void __launch_bounds__(kThreads) draft_verify_kernel(const VerifyArgs
             for (int i = 0; i < warp; ++i)
                 run += s_scan[i];
             if (run <= border && border - run < own) {
-                for (int64_t v = t0; v < t0 + few && v < f1; ++v) {
-                    const Units x = weight_at<BF16>(r, v);
-                    const uint64_t n1 = (uint64_t)whole(x.hi, x.lo);
-                    if (border - run < n1) {
-                        s_found = (int)v;
+                for (int v = t0; v < t1; ++v) {
+                    const uint64_t x = weight_at<BF16>(r, v);
+                    if (border - run < x) {
+                        s_found = v;
                         break;
                     }
-                    run += n1;
+                    run += x;
                 }
             }
             __syncthreads();
@@ -270,7 +335,7 @@ __global__ void __launch_bounds__(kThreads) draft_verify_kernel(const VerifyArgs
 template <bool BF16>
 cudaError_t launch(const VerifyArgs &a, cudaStream_t stream)
 {
-    // Blocks of a sequence: 8 while each warp's stretch has some 128 tokens.
+    // Blocks of a sequence: 8 while each warp's stretch has 128 tokens.
     int ranks = kMaxCluster;
     while (ranks > 1 && a.V < (int64_t)ranks * kWarps * 128)
         ranks /= 2;

@@ -35,8 +35,8 @@ constexpr int kThreads = kWarps * 32;
 constexpr int kFusedTokens = 16;   // tokens that the up kernel routes itself
 constexpr int kCols = 64;          // columns of a stage: 128 bytes of a row
 constexpr int kUpStages = 8;
-constexpr int kDownStages = 5;
-constexpr int kMaxSums = 36 * 1024;  // bytes of a slab's sums: 36 rows of 256 tokens
+constexpr int kDownStages = 6;
+constexpr int kSumRows = 512;      // least rows of the down kernel's sums
 
 // ---------------------------------------------------------------------------------------------
 // router
@@ -300,11 +300,11 @@ Cut make_cut(int K)
 __host__ __device__ constexpr int stage_bytes(int XR) { return (16 + XR) * 128; }
 constexpr int kAreaBytes = 2 * kWarps * 128 * 4;
 
-// All tiles of the block.  rows_of(tile) gives the rows that this lane copies, of which warps take steps;
-// done(round, area) is called by all threads behind a barrier, with the sums [warp][16 rows][8 tokens] of the
-// round's 8 / parts tiles; drained() once by each warp when its last copy is under way.  XR is 8, or 16: the tokens' rows
-// in two parts whose sum they are.
-template <int XR, int D, typename RowsOf, typename Done, typename Drained>
+// All tiles of the block.  rows_of(tile) gives the rows that this lane copies; drained() is called once by each
+// warp when its last copy is under way.  Joint: done(round, area) is called by all threads behind a barrier, with the
+// sums [warp][16 rows][8 tokens] of the round's 8 / parts tiles.  Otherwise warps go on by themselves, and a warp calls
+// done(tile, part, its sums).  XR is 8, or 16: the tokens' rows in two parts whose sum they are.
+template <int XR, int D, bool Joint, typename RowsOf, typename Done, typename Drained>
 __device__ __forceinline__ void run_tiles(char *smem, float *area, const Cut &c, int tiles, RowsOf rows_of,
                                           Done done, Drained drained)
 {
@@ -392,12 +392,18 @@ __device__ __forceinline__ void run_tiles(char *smem, float *area, const Cut &c,
                 }
                 get = get + 1 == D ? 0 : get + 1;
             }
-            float *to = sums + warp * 128;
-            *reinterpret_cast<float2 *>(to + g * 8 + 2 * t) = make_float2(acc[0], acc[1]);
-            *reinterpret_cast<float2 *>(to + (8 + g) * 8 + 2 * t) = make_float2(acc[2], acc[3]);
+            if constexpr (Joint) {
+                float *to = sums + warp * 128;
+                *reinterpret_cast<float2 *>(to + g * 8 + 2 * t) = make_float2(acc[0], acc[1]);
+                *reinterpret_cast<float2 *>(to + (8 + g) * 8 + 2 * t) = make_float2(acc[2], acc[3]);
+            } else {
+                done(round * at_once + first, part, acc);
+            }
         }
-        __syncthreads();
-        done(round, sums);
+        if constexpr (Joint) {
+            __syncthreads();
+            done(round, sums);
+        }
     }
     cp_async_wait<0>();
 }
@@ -416,7 +422,8 @@ struct ShareArgs {
     int32_t first, local, T, H, F;
     float scaling;
     Cut cut;
-    int32_t slab;              // down: most rows of a block at a time
+    float *sums;               // [sum_rows][H]: a pair's share of the output, by part and pair
+    int32_t sum_rows;
 };
 
 // The block's rows of the down projection: [from, to).
@@ -509,7 +516,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_up_kernel(const ShareArgs a)
     const int64_t places = (int64_t)ps.count * a.F;
     const UpTiles tiles(places * blockIdx.x / gridDim.x, places * (blockIdx.x + 1) / gridDim.x, a.F);
     const int64_t n_act = (int64_t)a.T * kTopK * a.F;
-    run_tiles<8, kUpStages>(
+    run_tiles<8, kUpStages, true>(
         smem, area, a.cut, tiles.count,
         [&](int i) {
             int pass, f, n;
@@ -584,94 +591,102 @@ __global__ void __launch_bounds__(kThreads, 1) moe_up_kernel(const ShareArgs a)
 // down: out = sum over the pairs of scaling * weight * w2 a
 // ---------------------------------------------------------------------------------------------
 
+constexpr uint32_t kAbsent = 0xffffffffu;  // a NaN that no product gives
+
+// A block owns some output columns, so it can add up by itself what its warps leave for each pair: warps never
+// wait for one another until then.  Adding round by round in shared memory instead, in order behind barriers, took
+// half of the kernel's instructions (64 tokens of an eighth: 308 us, TODO).
 __global__ void __launch_bounds__(kThreads, 1) moe_down_kernel(const ShareArgs a)
 {
     extern __shared__ __align__(128) char smem[];
     __shared__ Passes ps;
-    float *area = reinterpret_cast<float *>(smem + kWarps * kDownStages * stage_bytes(16));
-    float *sums = area + kAreaBytes / 4;  // [token][row of the block's]
-    const int lane = threadIdx.x & 31;
+    __shared__ float weight[kMaxTokens * kTopK];  // scaled; kAbsent: the expert is not here
+    const int lane = threadIdx.x & 31, g = lane >> 2, t2 = 2 * (lane & 3);
     pdl_launch_dependents();
     pdl_wait();
     const int most = most_passes(a.T);
+#pragma unroll 1
     for (int i = threadIdx.x; i < most; i += kThreads) {
         ps.info[i] = a.passes->info[i];
         ps.pairs[i] = ld_plain(&a.passes->pairs[i]);
     }
     if (threadIdx.x == 0)
         ps.count = a.passes->count;
-    float *weight = sums + a.T * a.slab;  // [pair]
-    for (int i = threadIdx.x; i < a.T * kTopK; i += kThreads)
-        weight[i] = a.scaling * a.weights[i];
     __syncthreads();
     int r0, r1;
     down_rows(a, blockIdx.x, gridDim.x, r0, r1);
-    const int64_t n_act = (int64_t)a.T * kTopK * a.F;
-    for (; r0 < r1; r0 += a.slab) {
-        const int rows = min(r1 - r0, a.slab), row_tiles = (rows + 15) / 16, tiles = row_tiles * ps.count;
-        for (int i = threadIdx.x; i < a.T * rows; i += kThreads)
-            sums[i] = 0.0f;
-        run_tiles<16, kDownStages>(
-            smem, area, a.cut, tiles,
-            [&](int i) {
-                const int rt = i / ps.count, pass = i - rt * ps.count;
-                const int from = rows * rt / row_tiles, n = rows * (rt + 1) / row_tiles - from;
-                const uint16_t *w = a.w2 + ((int64_t)ps.expert(pass) * a.H + r0 + from) * a.F;
-                Rows<16> r;
+    const int rows = r1 - r0, row_tiles = (rows + 15) / 16, pairs = a.T * kTopK;
+    Cut cut = a.cut;
+    // few tiles: parts of their columns, so that each warp has some, while there is room for the parts' sums
+    while (cut.parts < kWarps && row_tiles * ps.count * cut.parts < 3 * kWarps &&
+           cut.steps >= 4 * cut.parts && 2 * cut.parts * pairs <= a.sum_rows)
+        cut.parts *= 2;
+    const int64_t n_act = (int64_t)pairs * a.F;
+    run_tiles<16, kDownStages, false>(
+        smem, nullptr, cut, row_tiles * ps.count,
+        [&](int i) {
+            const int pass = i / row_tiles, rt = i - pass * row_tiles;
+            const int from = rows * rt / row_tiles, n = rows * (rt + 1) / row_tiles - from;
+            const uint16_t *w = a.w2 + ((int64_t)ps.expert(pass) * a.H + r0 + from) * a.F;
+            Rows<16> r;
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const int row = (lane >> 3) + 4 * j;
-                    r.w[j] = row < n ? w + (int64_t)row * a.F : nullptr;
-                }
+            for (int j = 0; j < 4; ++j) {
+                const int row = (lane >> 3) + 4 * j;
+                r.w[j] = row < n ? w + (int64_t)row * a.F : nullptr;
+            }
 #pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    const int row = (lane >> 3) + 4 * j;
-                    r.x[j] = r.x[j + 2] = nullptr;
-                    if (row < ps.tokens(pass)) {
-                        r.x[j] = a.act + (int64_t)ps.pair(pass, row) * a.F;
-                        r.x[j + 2] = r.x[j] + n_act;
-                    }
+            for (int j = 0; j < 2; ++j) {
+                const int row = (lane >> 3) + 4 * j;
+                r.x[j] = r.x[j + 2] = nullptr;
+                if (row < ps.tokens(pass)) {
+                    r.x[j] = a.act + (int64_t)ps.pair(pass, row) * a.F;
+                    r.x[j + 2] = r.x[j] + n_act;
                 }
-                return r;
-            },
-            [&](int round, const float *part_sums) {
-                const int parts = a.cut.parts, at_once = kWarps / parts;
-                // a thread owns a row of each tile and the tokens of its class: sums grow in the order of the
-                // tiles
-                const int r = threadIdx.x & 15, mine = threadIdx.x >> 4;
-                const int end = min(tiles, (round + 1) * at_once);
-                int rt = round * at_once / ps.count, pass = round * at_once - rt * ps.count;
-                for (int i = round * at_once; i < end; ++i) {
-                    const int from = rows * rt / row_tiles, n = rows * (rt + 1) / row_tiles - from;
-                    const uint4 pairs = ps.pairs[pass];
-                    const int tokens = ps.tokens(pass);
-                    const float *v0 = part_sums + (i - round * at_once) * parts * 128 + r * 8;
+            }
+            return r;
+        },
+        [&](int i, int part, const float (&acc)[4]) {
+            const int pass = i / row_tiles, rt = i - pass * row_tiles;
+            const int from = rows * rt / row_tiles, n = rows * (rt + 1) / row_tiles - from;
+            float *to = a.sums + (int64_t)part * pairs * a.H + r0 + from + g;
 #pragma unroll
-                    for (int j = 0; j < kPassTokens; ++j) {
-                        if (j >= tokens)
-                            break;
-                        const int pair = (word(pairs, j / 2) >> (16 * (j & 1))) & 0xffff, t = pair / kTopK;
-                        if ((t & 15) != mine || r >= n)
-                            continue;
-                        float v = 0.0f;
-                        for (int w = 0; w < parts; ++w)
-                            v += v0[w * 128 + j];
-                        float *s = sums + t * rows + from + r;
-                        *s = __fmaf_rn(weight[pair], v, *s);
-                    }
-                    if (++pass == ps.count) {
-                        pass = 0;
-                        ++rt;
-                    }
+            for (int j = 0; j < 2; ++j)
+                if (t2 + j < ps.tokens(pass)) {
+                    float *y = to + (int64_t)ps.pair(pass, t2 + j) * a.H;
+                    if (g < n)
+                        y[0] = acc[j];
+                    if (g + 8 < n)
+                        y[8] = acc[2 + j];
                 }
-            },
-            []() {});
-        __syncthreads();
-        for (int i = threadIdx.x; i < a.T * rows; i += kThreads) {
-            const int t = i / rows, r = i - t * rows;
-            a.out[t * a.out_stride + r0 + r] = (uint16_t)pack_bf16x2(sums[i], 0.0f);
+        },
+        [&]() {
+            // with the last copies under way: the pairs' weights
+#pragma unroll 1
+            for (int i = threadIdx.x; i < pairs; i += kThreads) {
+                const int e = a.ids[i] - a.first;
+                weight[i] = a.scaling * a.weights[i];
+                if (e < 0 || e >= a.local)
+                    weight[i] = __uint_as_float(kAbsent);
+            }
+        });
+    __syncthreads();
+    for (int i = threadIdx.x; i < a.T * rows; i += kThreads) {
+        const int t = i / rows, r = i - t * rows;
+        const float *y = a.sums + (int64_t)t * kTopK * a.H + r0 + r;
+        float sum = 0.0f;
+        float v[kTopK];
+#pragma unroll
+        for (int k = 0; k < kTopK; ++k) {
+            v[k] = 0.0f;
+            if (__float_as_uint(weight[t * kTopK + k]) != kAbsent)
+                for (int p = 0; p < cut.parts; ++p)
+                    v[k] += y[(int64_t)(p * pairs + k) * a.H];
         }
-        __syncthreads();
+#pragma unroll
+        for (int k = 0; k < kTopK; ++k)
+            if (__float_as_uint(weight[t * kTopK + k]) != kAbsent)
+                sum = __fmaf_rn(weight[t * kTopK + k], v[k], sum);
+        a.out[t * a.out_stride + r0 + r] = (uint16_t)pack_bf16x2(sum, 0.0f);
     }
 }
 
@@ -701,7 +716,9 @@ MoePlan moe_plan(int64_t T, int32_t H, int32_t F)
     p.weights = p.ids + T * kTopK * 4;
     p.passes = p.weights + T * kTopK * 4;
     p.act = p.passes + (int64_t)sizeof(Passes);
-    p.bytes = p.act + 2 * T * kTopK * F * 2;
+    p.sums = p.act + 2 * T * kTopK * F * 2;
+    p.sum_rows = T * kTopK > kSumRows ? T * kTopK : kSumRows;
+    p.bytes = p.sums + p.sum_rows * H * 4;
     return p;
 }
 
@@ -721,6 +738,8 @@ cudaError_t launch_moe_layer(const MoeArgs &a, const MoePlan &p, cudaStream_t st
     s.ids = a.ids ? a.ids : (int32_t *)(a.workspace + p.ids);
     s.weights = a.weights ? a.weights : (float *)(a.workspace + p.weights);
     s.passes = (Passes *)(a.workspace + p.passes);
+    s.sums = (float *)(a.workspace + p.sums);
+    s.sum_rows = (int32_t)p.sum_rows;
     s.first = a.first;
     s.local = a.local;
     s.T = a.T;
@@ -747,13 +766,8 @@ cudaError_t launch_moe_layer(const MoeArgs &a, const MoePlan &p, cudaStream_t st
     }
     if (e == cudaSuccess) {
         s.cut = make_cut(a.F);
-        const int own = (a.H + down - 1) / down, most = kMaxSums / (a.T * 4);
-        const int slabs = (own + most - 1) / most;
-        s.slab = (own + slabs - 1) / slabs;
-        e = launch_share<moe_down_kernel>(s, down,
-                                          kWarps * kDownStages * stage_bytes(16) + kAreaBytes +
-                                              a.T * (s.slab + kTopK) * 4,
-                                          stream);
+        s.cut.parts = 1;
+        e = launch_share<moe_down_kernel>(s, down, kWarps * kDownStages * stage_bytes(16), stream);
     }
     return e != cudaSuccess ? e : cudaGetLastError();
 }
