@@ -63,7 +63,7 @@ BEAM_API int beam_kv4_write_fwd(void *k_cache, void *v_cache, void *k_scales, vo
  * sums; products q c are exact: the query row is taken in FP16 after an exact scaling by a power of two (at
  * most 2^60) to [2^14, 2^15), so that only elements 2^-27 below the row's largest (or below 2^-74) lose
  * bits.  Maxima, sums and outputs are FP32.  The products exp(s_j - max) * scale that multiply the values'
- * codes are rounded to FP16, scaled up by a power of two: an error of at most 2^-11 of each and of 2^-40 of
+ * codes are rounded to FP16, scaled up by a power of two: an error of at most 2^-11 of each and of 2^-32 of
  * the largest scale that the row has seen; minima are added in FP32.
  * Results do not depend on the order in which blocks run.
  *
@@ -74,7 +74,7 @@ BEAM_API int beam_kv4_write_fwd(void *k_cache, void *v_cache, void *k_scales, vo
  *   workspace: at least beam_attn_kv4_workspace(...) bytes, 16-byte aligned
  * num_slots in [0, 2^31); n_q_heads a multiple of n_kv_heads, at most 1024; head_dim must be 128 and group
  * 32, 64 or 128; sm_scale finite; B*q_len*n_q_heads < 2^31; table_width in [0, 2^30); q_len >= 1;
- * window, n_sink >= 0.  B == 0 returns BEAM_OK without launching.  No output may overlap anything. */
+ * window, n_sink >= 0; B * n_kv_heads * table_width * ceil(query rows of a KV head / 24) / 32 below 2^31.  B == 0 returns BEAM_OK without launching.  No output may overlap anything. */
 BEAM_API int beam_attn_kv4_fwd(void *out, int64_t out_row_stride, float *lse_out, const void *q,
                                int64_t q_row_stride, const void *k_cache, const void *v_cache,
                                const void *k_scales, const void *v_scales, int64_t num_slots,

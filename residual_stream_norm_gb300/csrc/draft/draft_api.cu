@@ -29,6 +29,9 @@ int check_attn_sizes(int32_t B, int32_t q_len, int32_t n_q, int32_t n_kv, int64_
         return BEAM_ERR_INVALID_ARG;
     if ((int64_t)B * q_len >= kMost || (int64_t)B * q_len * n_q >= kMost)
         return BEAM_ERR_INVALID_ARG;
+    // the kernel counts tiles of keys in 31 bits
+    if (beam::kv4_attn_plan(B, q_len, n_q, n_kv, width, window, n_sink).most_tiles >= (double)kMost)
+        return BEAM_ERR_INVALID_ARG;
     return BEAM_OK;
 }
 

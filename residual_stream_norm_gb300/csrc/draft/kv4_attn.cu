@@ -7,15 +7,18 @@
 //    register pairs that a matrix instruction takes, exactly.  The factor 16 of every second pair goes into
 //    the query (scaled by 1/16 there) and out of the result's rows.
 //  - Codes multiply first and scales after: s = scale <q, c> + minimum sum q, with FP32 sums of exact
-//    products, and out = sum (p scale) c + sum p minimum.
+//    products, and out = sum (p scale) c + sum p minimum.  The products' sums over 32 keys are added to the
+//    output outside the matrix instruction, which cuts off where FP32 rounds: codes are all positive, and what it cuts
+//    off over 100,000 keys showed beside values that average out (error 0.0026 instead of 0.0017).
 // Both products take the cache as the left operand, whose rows are keys (Q K^T) or columns (V^T P^T), and up
 // to 24 query rows of a KV head as the right one, so that few rows waste little: ldmatrix hands out the keys'
 // words, and with a transpose the values' (a 16-bit unit is four columns of a key).
 //
-// Every warp works alone: it owns an even share of all units' tiles of 64 keys, one after the other, copies
-// them with cp.async a few tiles ahead into its own part of shared memory, and carries the running maximum,
-// sum and output of the unit at hand.  A unit is a sequence, a KV head and a tile of query rows; one that is
-// cut between warps leaves parts (FP32 maximum, sum, output) that a second kernel joins in order.
+// Every warp works alone: it owns an even share of all units' tiles of 32 keys, one after the other, copies
+// them with cp.async a few tiles ahead into its own part of shared memory, each with a note of where it stands, and
+// carries the running maximum, sum and output of the unit at hand.  A unit is a sequence, a KV head and a tile of
+// query rows; one that is cut between warps leaves parts (FP32 maximum, sum, output) that a second kernel joins in
+// order.
 
 #include <cuda_fp16.h>
 
@@ -29,28 +32,40 @@ namespace {
 constexpr int kSms = 152;
 constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
-constexpr int kTile = 64;  // keys
+constexpr int kTile = 32;  // keys
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr int kMinExp = -100;
 
 struct Sizes {
     int32_t heads, R, rtiles;
-    int32_t warps;          // of the first kernel
+    uint32_t warps;         // of the first kernel
+    uint32_t per;           // sequences that a thread counts
     float *part_o;          // [warps][2][8 * NT][128]
     float *part_ml;         // [warps][2][8 * NT][2]
 };
 
-__host__ __device__ constexpr int stages_of(int NG) { return NG == 4 ? 2 : 3; }
-__host__ __device__ constexpr int stage_bytes(int NG) { return 2 * kTile * 64 + 2 * kTile * 4 * NG + 16; }
+// What stands behind a tile's codes and scales: where it is from.
+struct Note {
+    uint32_t valid;          // keys to be seen
+    int b, hr;               // sequence; KV head * rtiles + row tile
+    int tile, tiles;         // of the unit
+    int n, ns, skip;         // keys of the sequence; see Keys
+};
+
+__host__ __device__ constexpr int stages_of(int NG) { return NG == 4 ? 5 : 6; }
+__host__ __device__ constexpr int scales_at() { return 2 * kTile * 64; }
+__host__ __device__ constexpr int note_at(int NG) { return scales_at() + 2 * kTile * 4 * NG; }
+__host__ __device__ constexpr int stage_bytes(int NG) { return note_at(NG) + (int)sizeof(Note); }
 
 // The keys that any row of a sequence sees, in a list of its own: first the `ns` sinks, then those from
 // ns + skip on.
 struct Keys {
     int n, ns, skip, count;
+    __device__ __forceinline__ int tiles() const { return (count + kTile - 1) / kTile; }
 };
 
-__device__ __forceinline__ Keys keys_of(const Kv4AttnArgs &a, int64_t b)
+__device__ __forceinline__ Keys keys_of(const Kv4AttnArgs &a, uint32_t b)
 {
     Keys k;
     const int w = (int)a.width;
@@ -64,28 +79,29 @@ __device__ __forceinline__ Keys keys_of(const Kv4AttnArgs &a, int64_t b)
     return k;
 }
 
-__device__ __forceinline__ int64_t tiles_of(const Keys &k) { return (k.count + (int64_t)kTile - 1) / kTile; }
-
-// Tiles of all units in front of each thread's run of sequences, and of all.  `per` sequences a thread.
-__device__ __forceinline__ int64_t scan_tiles(const Kv4AttnArgs &a, const Sizes &z, int64_t *s_before,
-                                              int64_t *s_warp, int64_t per)
+// Tiles of all units in front of each thread's run of sequences (s_before), and of all.  Fewer than 2^31 in all
+// (the entry point's checks).
+__device__ __forceinline__ uint32_t scan_tiles(const Kv4AttnArgs &a, const Sizes &z, uint32_t *s_before,
+                                               uint32_t *s_warp)
 {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    int64_t own = 0;
-    for (int64_t b = threadIdx.x * per; b < (threadIdx.x + 1) * per && b < a.B; ++b)
-        own += tiles_of(keys_of(a, b));
-    own *= (int64_t)a.n_kv * z.rtiles;
-    int64_t s = own;
+    uint32_t own = 0;
+    const uint32_t first = threadIdx.x * z.per;
+    for (uint32_t b = first; b < first + z.per && b < (uint32_t)a.B; ++b)
+        own += (uint32_t)keys_of(a, b).tiles();
+    own *= (uint32_t)(a.n_kv * z.rtiles);
+    uint32_t s = own;
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
-        const int64_t o = __shfl_up_sync(0xffffffffu, s, off);
+        const uint32_t o = __shfl_up_sync(0xffffffffu, s, off);
         if (lane >= off)
             s += o;
     }
     if (lane == 31)
         s_warp[warp] = s;
     __syncthreads();
-    int64_t total = 0, before = s - own;
+    uint32_t total = 0, before = s - own;
+#pragma unroll
     for (int i = 0; i < kWarps; ++i) {
         before += i < warp ? s_warp[i] : 0;
         total += s_warp[i];
@@ -93,30 +109,6 @@ __device__ __forceinline__ int64_t scan_tiles(const Kv4AttnArgs &a, const Sizes 
     s_before[threadIdx.x] = before;
     __syncthreads();
     return total;
-}
-
-// Where a warp stands: a tile of a unit.
-struct At {
-    int64_t b;
-    int hr;    // KV head * rtiles + row tile
-    int tile, tiles;
-    Keys k;
-};
-
-__device__ __forceinline__ void advance(At &p, const Kv4AttnArgs &a, int hrs)
-{
-    if (++p.tile < p.tiles)
-        return;
-    p.tile = 0;
-    if (++p.hr < hrs)
-        return;
-    p.hr = 0;
-    do {
-        if (++p.b >= a.B)
-            return;
-        p.k = keys_of(a, p.b);
-        p.tiles = (int)tiles_of(p.k);
-    } while (p.tiles == 0);
 }
 
 __device__ __forceinline__ void cp_async4(uint32_t dst, const void *src, uint32_t bytes)
@@ -142,67 +134,68 @@ __device__ __forceinline__ void lds_scales(uint32_t (&w)[NG], uint32_t addr)
 // 2^e for -126 <= e <= 127
 __device__ __forceinline__ float pow2i(int e) { return __uint_as_float((uint32_t)(127 + e) << 23); }
 
+// Byte offset of chunk c (16 bytes, 32 columns) of key `key` of a tile: eight keys' chunks take all banks.
+__device__ __forceinline__ uint32_t chunk_at(int key, int c)
+{
+    return (uint32_t)(key * 64 + ((c ^ ((key >> 1) & 3)) << 4));
+}
+
 template <int NT, int NG>
 struct Unit {
     // query, FP16: columns c*32 + t*8 + {j, j + 4} of row g, j = 0..3 (odd j: a sixteenth)
     uint32_t q[NT][4][4];
-    float fac[NT][2];        // rows 2t, 2t+1: what a sum of products is scaled by
-    float qsum[NT][2][NG];   // sums of the query's columns by group, scaled
-    int p[NT][2];            // places of the rows in the sequence (-1: padding)
-    float m[NT][2], l[NT][2], omin[NT][2][NG];
+    // rows 2t, 2t+1: with t = scale (sum of products) + minimum qsum, the scores are fac t in powers of two
+    float fac[NT][2], qsum[NT][2][NG];
+    float m[NT][2], l[NT][2], omin[NT][2][NG];  // of the scaled scores
     int e[NT][2];            // scales seen are below 2^e
+    bool one_e;              // the same one for all rows
     float o[NT][4][2][4];
 };
 
+// Row `row` of a sequence and KV head: its query's index and place in the sequence.
 template <int NT, int NG>
 __device__ __forceinline__ void begin_unit(Unit<NT, NG> &u, const Kv4AttnArgs &a, const Sizes &z,
-                                           const At &at, int lane)
+                                           const Note &at, int lane)
 {
     const int g = lane >> 2, t = lane & 3;
     const int kv = at.hr / z.rtiles, r0 = (at.hr - kv * z.rtiles) * NT * 8;
-    const float sm = a.sm_scale * kLog2e;
+    uint4 v[NT][4];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-        const int r = r0 + nt * 8 + g;
-        const int i = r / z.heads;
-        uint4 v[4];
+        const int r = r0 + nt * 8 + g, i = r / z.heads;
+        const uint16_t *from = (const uint16_t *)a.q + ((int64_t)at.b * a.q_len + i) * a.q_stride +
+                               (kv * z.heads + r - i * z.heads) * 128 + t * 8;
 #pragma unroll
         for (int c = 0; c < 4; ++c)
-            v[c] = r < z.R ? ld_plain((const uint16_t *)a.q + (at.b * a.q_len + i) * a.q_stride +
-                                      (kv * z.heads + r - i * z.heads) * 128 + c * 32 + t * 8)
-                           : make_uint4(0, 0, 0, 0);
-        uint32_t mx = 0u;
-        float sum[4];
+            v[nt][c] = r < z.R ? ld_plain(from + c * 32) : make_uint4(0, 0, 0, 0);
+    }
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-            sum[c] = 0.0f;
-#pragma unroll
-            for (int w = 0; w < 4; ++w) {
-                const float x = bf_lo(word(v[c], w)), y = bf_hi(word(v[c], w));
-                mx = max(mx, max(__float_as_uint(x) & 0x7fffffffu, __float_as_uint(y) & 0x7fffffffu));
-                sum[c] += x + y;
-            }
-        }
-#pragma unroll
-        for (int off = 1; off < 4; off <<= 1) {
-            mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, off));
-#pragma unroll
-            for (int c = 0; c < 4; ++c)
-                sum[c] += __shfl_xor_sync(0xffffffffu, sum[c], off);
-        }
+    for (int nt = 0; nt < NT; ++nt) {
         // the row's power of two: its largest element to [2^14, 2^15)
-        int k = (mx >> 23) == 255u || mx == 0u ? 0 : 141 - (int)(mx >> 23);
+        uint32_t mx = 0u;
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+#pragma unroll
+            for (int w = 0; w < 4; ++w)
+                mx = max(mx, max(word(v[nt][c], w) & 0x7fffu, (word(v[nt][c], w) >> 16) & 0x7fffu));
+        mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+        mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+        int k = mx >= 0x7f80u || mx == 0u ? 0 : 141 - (int)(mx >> 7);
         k = min(k, 60);
-        const float f = pow2i(k);
-        // a sum of products of q 2^k and c 2^-24, back
-        const float inv = pow2i(-k);
+        // a negative scale of the scores turns the query around, none takes it out
+        const float f = a.sm_scale == 0.0f ? 0.0f : (a.sm_scale < 0.0f ? -pow2i(k) : pow2i(k));
+        float gs[NG];
+#pragma unroll
+        for (int j = 0; j < NG; ++j)
+            gs[j] = 0.0f;
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
             float x[8];
 #pragma unroll
             for (int w = 0; w < 4; ++w) {
-                x[2 * w] = bf_lo(word(v[c], w)) * f;
-                x[2 * w + 1] = bf_hi(word(v[c], w)) * f;
+                x[2 * w] = bf_lo(word(v[nt][c], w)) * f;
+                x[2 * w + 1] = bf_hi(word(v[nt][c], w)) * f;
+                gs[c * NG / 4] += x[2 * w] + x[2 * w + 1];
             }
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
@@ -210,59 +203,65 @@ __device__ __forceinline__ void begin_unit(Unit<NT, NG> &u, const Kv4AttnArgs &a
                 u.q[nt][c][j] = pack_f16x2(x[j] * h, x[j + 4] * h);
             }
         }
-        float gs[NG];
 #pragma unroll
         for (int j = 0; j < NG; ++j) {
-            gs[j] = 0.0f;
-#pragma unroll
-            for (int c = 0; c < 4 / NG; ++c)
-                gs[j] += sum[j * (4 / NG) + c];
-            gs[j] *= sm;
+            gs[j] += __shfl_xor_sync(0xffffffffu, gs[j], 1);
+            gs[j] += __shfl_xor_sync(0xffffffffu, gs[j], 2);
+            gs[j] *= 5.9604644775390625e-08f;  // 2^-24, as the codes' products
         }
+        // (not 0, which would make NaN of what is masked)
+        const float fac = a.sm_scale == 0.0f ? 1.0f
+                                             : fmaxf(fabsf(a.sm_scale) * kLog2e * pow2i(-k) * 16777216.0f,
+                                                     1.1754943508222875e-38f);
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
             const int from = (2 * t + e) * 4;  // a lane whose g is this row
-            u.fac[nt][e] = __shfl_sync(0xffffffffu, inv, from) * 16777216.0f * sm;
+            u.fac[nt][e] = __shfl_sync(0xffffffffu, fac, from);
 #pragma unroll
-            for (int j = 0; j < NG; ++j)
+            for (int j = 0; j < NG; ++j) {
                 u.qsum[nt][e][j] = __shfl_sync(0xffffffffu, gs[j], from);
-            const int row = r0 + nt * 8 + 2 * t + e;
-            u.p[nt][e] = row < z.R ? at.k.n - a.q_len + row / z.heads : -1;
+                u.omin[nt][e][j] = 0.0f;
+            }
             u.m[nt][e] = __uint_as_float(0xff800000u);
             u.l[nt][e] = 0.0f;
             u.e[nt][e] = kMinExp;
-#pragma unroll
-            for (int j = 0; j < NG; ++j)
-                u.omin[nt][e][j] = 0.0f;
         }
 #pragma unroll
         for (int c = 0; c < 4; ++c)
 #pragma unroll
             for (int jj = 0; jj < 2; ++jj)
 #pragma unroll
-                for (int i2 = 0; i2 < 4; ++i2)
-                    u.o[nt][c][jj][i2] = 0.0f;
+                for (int i = 0; i < 4; ++i)
+                    u.o[nt][c][jj][i] = 0.0f;
     }
+    u.one_e = true;
 }
 
-// MT times 16 keys of the tile, from key k0 of it on.  Masked: some row may not see some of them.
-template <int NT, int NG, int MT, bool Masked>
-__device__ __forceinline__ void keys_step(Unit<NT, NG> &u, const Kv4AttnArgs &a, const At &at,
-                                          uint32_t base, int k0, uint64_t valid, int lane)
+// A tile of 32 keys.  Thread (g, t) holds scores of keys 16 mt + g (i < 2) and 16 mt + 8 + g (i >= 2) for
+// rows 2t (i even) and 2t + 1.
+template <int NT, int NG>
+__device__ __forceinline__ void take_tile(Unit<NT, NG> &u, const Kv4AttnArgs &a, const Sizes &z, const Note &at,
+                                          uint32_t kb, int lane)
 {
-    const int g = lane >> 2;
-    const uint32_t kb = base, vb = base + kTile * 64, ksb = vb + kTile * 64,
-                   vsb = ksb + kTile * 4 * NG;
+    const int g = lane >> 2, t = lane & 3;
+    const uint32_t vb = kb + kTile * 64, ksb = kb + scales_at(), vsb = ksb + kTile * 4 * NG;
     const float ninf = __uint_as_float(0xff800000u);
-    float s[NT][MT][4];
-    // ---- scores ----------------------------------------------------------------------------------
+    // every row sees every key of the tile: the last key for the first row, the first for the last
+    const int v0 = at.tile * kTile, v1 = v0 + kTile - 1;
+    const int p0 = v0 < at.ns ? v0 : v0 + at.skip, p1 = v1 < at.ns ? v1 : v1 + at.skip;
+    const bool all = at.valid == 0xffffffffu && p1 <= at.n - a.q_len &&
+                     (a.window == 0 || p1 < a.n_sink ||
+                      at.n - 1 - (p0 < a.n_sink ? (int)a.n_sink : p0) < a.window);
+    const bool plain = all && u.one_e;
+    float s[NT][2][4];
+    // ---- scores, but for fac -----------------------------------------------------------------------
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt) {
-        uint32_t lo[4], hi[4];  // words of chunk c (32 columns) of keys g and g + 8
+    for (int mt = 0; mt < 2; ++mt) {
+        uint32_t lo[4], hi[4];  // words of chunk c of keys g and g + 8
         {
-            const int key = k0 + mt * 16 + (lane & 7), c = lane >> 3;
-            ldmatrix_x4(lo, kb + key * 64 + ((c ^ ((key >> 1) & 3)) << 4));
-            ldmatrix_x4(hi, kb + (key + 8) * 64 + ((c ^ ((key >> 1) & 3)) << 4));
+            const uint32_t from = kb + chunk_at(mt * 16 + (lane & 7), lane >> 3);
+            ldmatrix_x4(lo, from);
+            ldmatrix_x4(hi, from + 8 * 64);
         }
         float acc[NT][NG][4];
 #pragma unroll
@@ -284,161 +283,192 @@ __device__ __forceinline__ void keys_step(Unit<NT, NG> &u, const Kv4AttnArgs &a,
                     mma16816<true>(acc[nt][c * NG / 4], f, u.q[nt][c][2 * h], u.q[nt][c][2 * h + 1]);
             }
         uint32_t sc[2][NG];
-        lds_scales<NG>(sc[0], ksb + (k0 + mt * 16 + g) * 4 * NG);
-        lds_scales<NG>(sc[1], ksb + (k0 + mt * 16 + g + 8) * 4 * NG);
+        lds_scales<NG>(sc[0], ksb + (mt * 16 + g) * 4 * NG);
+        lds_scales<NG>(sc[1], ksb + (mt * 16 + g + 8) * 4 * NG);
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                float x = 0.0f;
+                float x = bf_hi(sc[i >> 1][0]) * u.qsum[nt][i & 1][0];
 #pragma unroll
-                for (int j = 0; j < NG; ++j) {
-                    const uint32_t w = sc[i >> 1][j];
-                    x = __fmaf_rn(bf_lo(w) * u.fac[nt][i & 1], acc[nt][j][i],
-                                  __fmaf_rn(bf_hi(w), u.qsum[nt][i & 1][j], x));
-                }
-                if constexpr (Masked) {
-                    const int key = k0 + mt * 16 + g + 8 * (i >> 1);
-                    const int v = at.tile * kTile + key;
-                    const int pos = v < at.k.ns ? v : v + at.k.skip;
-                    const int p = u.p[nt][i & 1];
-                    const bool seen = ((valid >> key) & 1) && pos <= p &&
-                                      (a.window == 0 || p - pos < a.window || pos < a.n_sink);
-                    x = seen ? x : ninf;
-                }
+                for (int j = 1; j < NG; ++j)
+                    x = __fmaf_rn(bf_hi(sc[i >> 1][j]), u.qsum[nt][i & 1][j], x);
+#pragma unroll
+                for (int j = 0; j < NG; ++j)
+                    x = __fmaf_rn(bf_lo(sc[i >> 1][j]), acc[nt][j][i], x);
                 s[nt][mt][i] = x;
             }
     }
-    // ---- maxima: of the scores, and of the values' scales ----------------------------------------
-    int top = 0;  // largest scale's bits (not of NaN and infinite ones, which show in the output)
-    if constexpr (!Masked) {
+    // ---- what a row does not see; the largest of the values' scales --------------------------------
+    // (not of NaN and infinite ones, which show in the output)
+    int e_new[NT][2];
+    if (plain) {
+        uint32_t w[NG];
+        lds_scales<NG>(w, vsb + lane * 4 * NG);
+        int top = 0;
 #pragma unroll
-        for (int i = 0; i < MT / 2; ++i) {
-            uint32_t w[NG];
-            lds_scales<NG>(w, vsb + (k0 + i * 32 + lane) * 4 * NG);
-#pragma unroll
-            for (int j = 0; j < NG; ++j) {
-                const int x = (int)(w[j] & 0x7fffu);
-                top = max(top, x >= 0x7f80 ? 0 : x);
-            }
+        for (int j = 0; j < NG; ++j) {
+            const int x = (int)(w[j] & 0x7fffu);
+            top = max(top, x >= 0x7f80 ? 0 : x);
         }
-        top = __reduce_max_sync(0xffffffffu, top);
+        top = max(u.e[0][0], (__reduce_max_sync(0xffffffffu, top) >> 7) - 126);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+            e_new[nt][0] = e_new[nt][1] = top;
+    } else {
+        const int kv = at.hr / z.rtiles, r0 = (at.hr - kv * z.rtiles) * NT * 8;
+        int highest = kMinExp;
+        bool pad[NT][2];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int row = r0 + nt * 8 + 2 * t + e;
+                const int p = row < z.R ? at.n - a.q_len + row / z.heads : -1;
+                pad[nt][e] = p < 0;
+                int top = 0;
+#pragma unroll
+                for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const int key = mt * 16 + g + 8 * h, v = v0 + key;
+                        const int pos = v < at.ns ? v : v + at.skip;
+                        const bool seen = ((at.valid >> key) & 1) && pos <= p &&
+                                          (a.window == 0 || p - pos < a.window || pos < a.n_sink);
+                        float &x = s[nt][mt][e + 2 * h];
+                        x = seen ? x : ninf;
+                        uint32_t w[NG];
+                        lds_scales<NG>(w, vsb + key * 4 * NG);
+#pragma unroll
+                        for (int j = 0; j < NG; ++j) {
+                            const int b = (int)(w[j] & 0x7fffu);
+                            top = max(top, b >= 0x7f80 || !seen ? 0 : b);
+                        }
+                    }
+#pragma unroll
+                for (int off = 4; off < 32; off <<= 1)
+                    top = max(top, __shfl_xor_sync(0xffffffffu, top, off));
+                e_new[nt][e] = max(u.e[nt][e], (top >> 7) - 126);
+                highest = max(highest, e_new[nt][e]);
+            }
+        // rows whose largest scales are no more than 2^8 apart go by the largest: they have 2^40 in hand
+        highest = __reduce_max_sync(0xffffffffu, highest);
+        bool one = true;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                if (pad[nt][e] || highest - e_new[nt][e] <= 8)
+                    e_new[nt][e] = highest;
+                one = one && e_new[nt][e] == highest;
+            }
+        u.one_e = __all_sync(0xffffffffu, one);
     }
-    bool moved = false;
-    float up[NT][2], mref[NT][2];
+    // ---- maxima and weights -------------------------------------------------------------------------
+    float up[NT][2];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-            float mx = ninf;
-            int tp = top;
+            float mx = fmaxf(fmaxf(s[nt][0][e], s[nt][0][e + 2]), fmaxf(s[nt][1][e], s[nt][1][e + 2]));
 #pragma unroll
-            for (int mt = 0; mt < MT; ++mt)
-                mx = fmaxf(mx, fmaxf(s[nt][mt][e], s[nt][mt][e + 2]));
-            if constexpr (Masked) {
-#pragma unroll
-                for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        uint32_t w[NG];
-                        lds_scales<NG>(w, vsb + (k0 + mt * 16 + g + 8 * h) * 4 * NG);
-#pragma unroll
-                        for (int j = 0; j < NG; ++j) {
-                            const int x = (int)(w[j] & 0x7fffu);
-                            tp = max(tp, x >= 0x7f80 || s[nt][mt][e + 2 * h] == ninf ? 0 : x);
-                        }
-                    }
-            }
-#pragma unroll
-            for (int off = 4; off < 32; off <<= 1) {
+            for (int off = 4; off < 32; off <<= 1)
                 mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
-                if constexpr (Masked)
-                    tp = max(tp, __shfl_xor_sync(0xffffffffu, tp, off));
-            }
-            const float mn = fmaxf(u.m[nt][e], mx);
-            const int en = max(u.e[nt][e], (tp >> 7) - 126);
-            const float alpha = mn == u.m[nt][e] ? 1.0f : exp2_fast(u.m[nt][e] - mn);
-            moved = moved || mn != u.m[nt][e] || en != u.e[nt][e];
-            up[nt][e] = alpha * (en - u.e[nt][e] > 120 ? 0.0f : pow2i(u.e[nt][e] - en));
-            u.l[nt][e] *= alpha;
+            const float mn = fmaxf(u.m[nt][e], mx * u.fac[nt][e]);
+            const float ref = mn == ninf ? 0.0f : mn;
+            const float alpha = exp2_fast(u.m[nt][e] - ref);  // 0 at the first tile
+            up[nt][e] = alpha * pow2i(max(u.e[nt][e] - e_new[nt][e], -126));
+            u.e[nt][e] = e_new[nt][e];
+            u.m[nt][e] = mn;
+            float sum = 0.0f;
+#pragma unroll
+            for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    float &x = s[nt][mt][e + 2 * h];
+                    x = exp2_fast(__fmaf_rn(x, u.fac[nt][e], -ref));
+                    sum += x;
+                }
+            u.l[nt][e] = __fmaf_rn(u.l[nt][e], alpha, sum);
 #pragma unroll
             for (int j = 0; j < NG; ++j)
                 u.omin[nt][e][j] *= alpha;
-            u.m[nt][e] = mn;
-            u.e[nt][e] = en;
-            mref[nt][e] = mn == ninf ? 0.0f : mn;
         }
-    if (__any_sync(0xffffffffu, moved)) {
+    uint32_t b[NT][2][NG][2];
+    const float vinv = pow2i(15 - u.e[0][0]);
+#pragma unroll
+    for (int mt = 0; mt < 2; ++mt) {
+        uint32_t sc[2][NG];
+        lds_scales<NG>(sc[0], vsb + (mt * 16 + g) * 4 * NG);
+        lds_scales<NG>(sc[1], vsb + (mt * 16 + g + 8) * 4 * NG);
+#pragma unroll
+        for (int j = 0; j < NG; ++j) {
+            const float vs[2] = {bf_lo(sc[0][j]) * vinv, bf_lo(sc[1][j]) * vinv};
+            const float vm[2] = {bf_hi(sc[0][j]), bf_hi(sc[1][j])};
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                float w[4];
+                const float(&p)[4] = s[nt][mt];
+                if (plain) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        w[i] = p[i] * vs[i >> 1];
+                        u.omin[nt][i & 1][j] = __fmaf_rn(p[i], vm[i >> 1], u.omin[nt][i & 1][j]);
+                    }
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {  // a key that is not seen leaves nothing, whatever it holds
+                        w[i] = p[i] == 0.0f
+                                   ? 0.0f
+                                   : p[i] * (bf_lo(sc[i >> 1][j]) * pow2i(15 - u.e[nt][i & 1]));
+                        u.omin[nt][i & 1][j] = p[i] == 0.0f ? u.omin[nt][i & 1][j]
+                                                            : __fmaf_rn(p[i], vm[i >> 1],
+                                                                        u.omin[nt][i & 1][j]);
+                    }
+                }
+                b[nt][mt][j][0] = movmatrix_trans(pack_f16x2(w[0], w[1]));
+                b[nt][mt][j][1] = movmatrix_trans(pack_f16x2(w[2], w[3]));
+            }
+        }
+    }
+    // ---- output ------------------------------------------------------------------------------------
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+        uint32_t v[4];  // units of chunk c: keys 0-7, 8-15, 16-23, 24-31
+        ldmatrix_x4_trans(v, vb + chunk_at(lane, c));
+        float acc[NT][2][4];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int c = 0; c < 4; ++c)
+            for (int jj = 0; jj < 2; ++jj)
 #pragma unroll
-                for (int jj = 0; jj < 2; ++jj)
+                for (int i = 0; i < 4; ++i)
+                    acc[nt][jj][i] = 0.0f;
 #pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        u.o[nt][c][jj][i] *= up[nt][i & 1];
-    }
-    // ---- weights and the values' product -----------------------------------------------------------
+        for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt) {
-        uint32_t sc[2][NG];
-        lds_scales<NG>(sc[0], vsb + (k0 + mt * 16 + g) * 4 * NG);
-        lds_scales<NG>(sc[1], vsb + (k0 + mt * 16 + g + 8) * 4 * NG);
-        uint32_t b[NT][NG][2];
+            for (int jj = 0; jj < 2; ++jj) {
+                const uint32_t wl = v[2 * mt] >> (8 * jj), wh = v[2 * mt + 1] >> (8 * jj);
+                const uint32_t f[4] = {wl & 0x000f000fu, wl & 0x00f000f0u, wh & 0x000f000fu,
+                                       wh & 0x00f000f0u};
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-            float p[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                p[i] = exp2_fast(s[nt][mt][i] - mref[nt][i & 1]);
-                u.l[nt][i & 1] += p[i];
+                for (int nt = 0; nt < NT; ++nt)
+                    mma16816<true>(acc[nt][jj], f, b[nt][mt][c * NG / 4][0], b[nt][mt][c * NG / 4][1]);
             }
 #pragma unroll
-            for (int j = 0; j < NG; ++j) {
-                float w[4];
+        for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const uint32_t x = sc[i >> 1][j];
-                    const bool none = Masked && p[i] == 0.0f;
-                    // two factors, each in range: the scale up to FP16's, then the weight
-                    w[i] = none ? 0.0f : p[i] * (bf_lo(x) * pow2i(15 - u.e[nt][i & 1]));
-                    u.omin[nt][i & 1][j] =
-                        none ? u.omin[nt][i & 1][j] : __fmaf_rn(p[i], bf_hi(x), u.omin[nt][i & 1][j]);
-                }
-                b[nt][j][0] = movmatrix_trans(pack_f16x2(w[0], w[1]));
-                b[nt][j][1] = movmatrix_trans(pack_f16x2(w[2], w[3]));
-            }
-        }
+            for (int jj = 0; jj < 2; ++jj)
 #pragma unroll
-        for (int c2 = 0; c2 < 2; ++c2) {
-            uint32_t v[4];  // chunk 2 c2: keys 0-7, 8-15; chunk 2 c2 + 1: the same
-            {
-                const int key = k0 + mt * 16 + ((lane >> 3) & 1) * 8 + (lane & 7);
-                const int c = 2 * c2 + (lane >> 4);
-                ldmatrix_x4_trans(v, vb + key * 64 + ((c ^ ((key >> 1) & 3)) << 4));
-            }
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const int c = 2 * c2 + h;
-#pragma unroll
-                for (int jj = 0; jj < 2; ++jj) {
-                    const uint32_t wl = v[2 * h] >> (8 * jj), wh = v[2 * h + 1] >> (8 * jj);
-                    const uint32_t f[4] = {wl & 0x000f000fu, wl & 0x00f000f0u, wh & 0x000f000fu,
-                                           wh & 0x00f000f0u};
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
-                        mma16816<true>(u.o[nt][c][jj], f, b[nt][c * NG / 4][0], b[nt][c * NG / 4][1]);
-                }
-            }
-        }
+                for (int i = 0; i < 4; ++i)
+                    u.o[nt][c][jj][i] = __fmaf_rn(u.o[nt][c][jj][i], up[nt][i & 1], acc[nt][jj][i]);
     }
 }
 
 // Results of a whole unit, or the part of a cut one.
 template <int NT, int NG>
 __device__ __forceinline__ void end_unit(Unit<NT, NG> &u, const Kv4AttnArgs &a, const Sizes &z,
-                                         const At &at, bool whole, int64_t part, int lane)
+                                         const Note &at, bool whole, uint32_t part, int lane)
 {
     const int g = lane >> 2, t = lane & 3;
     const int kv = at.hr / z.rtiles, r0 = (at.hr - kv * z.rtiles) * NT * 8;
@@ -458,203 +488,180 @@ __device__ __forceinline__ void end_unit(Unit<NT, NG> &u, const Kv4AttnArgs &a, 
                     om[j] += __shfl_xor_sync(0xffffffffu, om[j], off);
             }
             const int in_tile = nt * 8 + 2 * t + e, r = r0 + in_tile;
-            if (r >= z.R)
-                continue;
+            const bool none = l == 0.0f;
+            const float inv = whole ? __fdiv_rn(1.0f, l) : 1.0f;
             const float back = pow2i(u.e[nt][e]);  // and 2^(24 - 15): codes' unit over weights' scaling
-            const float m = u.m[nt][e];
-            if (whole) {
-                const int i = r / z.heads, head = kv * z.heads + r - i * z.heads;
-                const int64_t row = at.b * a.q_len + i;
-                const float inv = __fdiv_rn(1.0f, l);
-                uint16_t *out = (uint16_t *)a.out + row * a.out_stride + head * 128;
+            const int i = r / z.heads, head = kv * z.heads + r - i * z.heads;
+            const int64_t row = (int64_t)at.b * a.q_len + i;
+            uint16_t *out = (uint16_t *)a.out + row * a.out_stride + head * 128 + 4 * g;
+            float *po = z.part_o + ((int64_t)part * NT * 8 + in_tile) * 128 + 4 * g;
+            if (r < z.R) {
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
                     float d[4];
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
                         const float x = u.o[nt][c][j >> 1][e + 2 * (j & 1)] * (j & 1 ? 32.0f : 512.0f);
-                        d[j] = l == 0.0f ? 0.0f : __fmaf_rn(x, back, om[c * NG / 4]) * inv;
+                        d[j] = none ? 0.0f : __fmaf_rn(x, back, om[c * NG / 4]) * inv;
                     }
-                    st_global_v2(out + c * 32 + 4 * g, pack_bf16x2(d[0], d[1]),
-                                 pack_bf16x2(d[2], d[3]));
+                    if (whole)
+                        st_global_v2(out + c * 32, pack_bf16x2(d[0], d[1]), pack_bf16x2(d[2], d[3]));
+                    else
+                        *reinterpret_cast<float4 *>(po + c * 32) = make_float4(d[0], d[1], d[2], d[3]);
                 }
-                if (a.lse && g == 0)
-                    a.lse[row * a.n_q + head] =
-                        l == 0.0f ? __uint_as_float(0xff800000u) : (m + log2f(l)) * kLn2;
-            } else {
-                float *out = z.part_o + (part * NT * 8 + in_tile) * 128;
-#pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    float d[4];
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const float x = u.o[nt][c][j >> 1][e + 2 * (j & 1)] * (j & 1 ? 32.0f : 512.0f);
-                        d[j] = __fmaf_rn(x, back, om[c * NG / 4]);
-                    }
-                    *reinterpret_cast<float4 *>(out + c * 32 + 4 * g) =
-                        make_float4(d[0], d[1], d[2], d[3]);
+                if (g == 0) {
+                    if (!whole)
+                        *reinterpret_cast<float2 *>(z.part_ml + ((int64_t)part * NT * 8 + in_tile) * 2) =
+                            make_float2(u.m[nt][e], l);
+                    else if (a.lse)
+                        a.lse[row * a.n_q + head] =
+                            none ? __uint_as_float(0xff800000u) : (u.m[nt][e] + log2f(l)) * kLn2;
                 }
-                if (g == 0)
-                    *reinterpret_cast<float2 *>(z.part_ml + (part * NT * 8 + in_tile) * 2) =
-                        make_float2(m, l);
             }
+            __syncwarp();
         }
-}
-
-// Slots of keys `lane` and `lane + 32` of a tile; -1: not to be seen.
-__device__ __forceinline__ void load_slots(int (&slot)[2], const Kv4AttnArgs &a, const At &p, int lane)
-{
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const int v = p.tile * kTile + i * 32 + lane;
-        slot[i] = -1;
-        if (v < p.k.count) {
-            const int64_t s = a.table[p.b * a.table_stride + (v < p.k.ns ? v : v + p.k.skip)];
-            slot[i] = s >= 0 && s < a.num_slots ? (int)s : -1;
-        }
-    }
-}
-
-template <int NG>
-__device__ __forceinline__ void copy_tile(uint32_t base, const int (&slot)[2], const Kv4AttnArgs &a, int kv,
-                                          int lane)
-{
-    const uint64_t valid = (uint64_t)__ballot_sync(0xffffffffu, slot[0] >= 0) |
-                           (uint64_t)__ballot_sync(0xffffffffu, slot[1] >= 0) << 32;
-#pragma unroll
-    for (int i = 0; i < kTile / 8; ++i) {
-        const int key = i * 8 + (lane >> 2), c = lane & 3;
-        const int s = __shfl_sync(0xffffffffu, slot[i / 4], key & 31);
-        const int64_t off = s >= 0 ? ((int64_t)s * a.n_kv + kv) * 64 + c * 16 : 0;
-        const uint32_t at = base + key * 64 + ((c ^ ((key >> 1) & 3)) << 4);
-        cp_async16(at, a.cache[0] + off, s >= 0 ? 16u : 0u);
-        cp_async16(at + kTile * 64, a.cache[1] + off, s >= 0 ? 16u : 0u);
-    }
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const int64_t off = slot[i] >= 0 ? ((int64_t)slot[i] * a.n_kv + kv) * 4 * NG : 0;
-        const uint32_t n = slot[i] >= 0 ? 4u * NG : 0u;
-        const uint32_t at = base + kTile * 128 + (i * 32 + lane) * 4 * NG;
-#pragma unroll
-        for (int x = 0; x < 2; ++x) {
-            const char *src = (const char *)a.scales[x] + off;
-            if constexpr (NG == 1)
-                cp_async4(at + x * kTile * 4 * NG, src, n);
-            else if constexpr (NG == 2)
-                cp_async8(at + x * kTile * 4 * NG, src, n);
-            else
-                cp_async16(at + x * kTile * 4 * NG, src, n);
-        }
-    }
-    if (lane == 0)
-        asm volatile("st.shared.u64 [%0], %1;" ::"r"(base + kTile * 128 + 2 * kTile * 4 * NG), "l"(valid)
-                     : "memory");
 }
 
 template <int NT, int NG>
-__global__ void __launch_bounds__(kThreads, 1)
-    kv4_attn_kernel(const Kv4AttnArgs a, const Sizes z, int64_t per)
+__global__ void __launch_bounds__(kThreads, 1) kv4_attn_kernel(const Kv4AttnArgs a, const Sizes z)
 {
     extern __shared__ __align__(128) char smem[];
-    __shared__ int64_t s_before[kThreads];
-    __shared__ int64_t s_warp[kWarps];
+    __shared__ uint32_t s_before[kThreads];
+    __shared__ uint32_t s_warp[kWarps];
     constexpr int kStages = stages_of(NG);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     pdl_launch_dependents();
     pdl_wait();
-    const int64_t total = scan_tiles(a, z, s_before, s_warp, per);
+    const uint32_t total = scan_tiles(a, z, s_before, s_warp);
     // neighbouring shares go to different blocks, so that few shares are spread over all SMs
-    const int64_t me = (int64_t)warp * gridDim.x + blockIdx.x;
-    const int64_t share = (total + z.warps - 1) / z.warps;
-    const int64_t start = me * share, end = start + share < total ? start + share : total;
+    const uint32_t me = (uint32_t)warp * gridDim.x + blockIdx.x;
+    const uint32_t share = (total + z.warps - 1) / z.warps;
+    const uint32_t start = me * share, end = min(start + share, total);
     if (start >= end)
         return;
+    // ---- where the share starts ---------------------------------------------------------------------
     const int hrs = a.n_kv * z.rtiles;
-    At ld;
+    Note ld;
     {
-        int lo = 0, hi = kThreads - 1;  // the last thread's run that starts at or before `start`
-        while (lo < hi) {
-            const int mid = (lo + hi + 1) / 2;
-            if (s_before[mid] <= start)
-                lo = mid;
-            else
-                hi = mid - 1;
-        }
-        int64_t cum = s_before[lo];
-        for (ld.b = lo * per;; ++ld.b) {
-            ld.k = keys_of(a, ld.b);
-            const int64_t n = tiles_of(ld.k) * hrs;
+        int lo = 0;  // the last thread's run that starts at or before `start`
+#pragma unroll 1
+        for (int step = kThreads / 2; step > 0; step /= 2)
+            if (s_before[lo + step] <= start)
+                lo += step;
+        uint32_t cum = s_before[lo];
+#pragma unroll 1
+        for (uint32_t b = (uint32_t)lo * z.per;; ++b) {
+            const Keys k = keys_of(a, b);
+            const uint32_t n = (uint32_t)k.tiles() * hrs;
             if (start < cum + n) {
-                ld.tiles = (int)tiles_of(ld.k);
-                ld.hr = (int)((start - cum) / ld.tiles);
-                ld.tile = (int)((start - cum) - (int64_t)ld.hr * ld.tiles);
+                ld.b = (int)b;
+                ld.n = k.n;
+                ld.ns = k.ns;
+                ld.skip = k.skip;
+                ld.tiles = k.tiles();
+                ld.hr = (int)((start - cum) / (uint32_t)ld.tiles);
+                ld.tile = (int)((start - cum) - (uint32_t)ld.hr * ld.tiles);
                 break;
             }
             cum += n;
         }
     }
-    At cp = ld;
     const uint32_t base =
         (uint32_t)__cvta_generic_to_shared(smem) + warp * kStages * stage_bytes(NG);
-    int64_t to_load = end - start;
-    int slot[2];
-    load_slots(slot, a, ld, lane);
-    auto load_next = [&](int stage) {
+    // ---- copies --------------------------------------------------------------------------------------
+    uint32_t to_load = end - start;
+    int slot, put = 0;
+    auto load_slot = [&]() {  // of key `lane` of the tile; -1: not to be seen
+        const int v = ld.tile * kTile + lane;
+        slot = -1;
+        if (v < ld.n - ld.skip) {
+            const int64_t s = a.table[ld.b * a.table_stride + (v < ld.ns ? v : v + ld.skip)];
+            slot = s >= 0 && s < a.num_slots ? (int)s : -1;
+        }
+    };
+    load_slot();
+    auto load_next = [&]() {
         if (to_load > 0) {
-            copy_tile<NG>(base + stage * stage_bytes(NG), slot, a, ld.hr / z.rtiles, lane);
+            const uint32_t to = base + put * stage_bytes(NG);
+            const int kv = ld.hr / z.rtiles;
+            ld.valid = __ballot_sync(0xffffffffu, slot >= 0);
+#pragma unroll
+            for (int i = 0; i < kTile / 8; ++i) {
+                const int key = i * 8 + (lane >> 2);
+                const int s = __shfl_sync(0xffffffffu, slot, key);
+                const int64_t off = ((int64_t)max(s, 0) * a.n_kv + kv) * 64 + (lane & 3) * 16;
+                const uint32_t at = to + chunk_at(key, lane & 3), n = s >= 0 ? 16u : 0u;
+                cp_async16(at, a.cache[0] + off, n);
+                cp_async16(at + kTile * 64, a.cache[1] + off, n);
+            }
+            const int64_t off = ((int64_t)max(slot, 0) * a.n_kv + kv) * 4 * NG;
+            const uint32_t at = to + scales_at() + lane * 4 * NG, n = slot >= 0 ? 4u * NG : 0u;
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                const char *src = (const char *)a.scales[x] + off;
+                if constexpr (NG == 1)
+                    cp_async4(at + x * kTile * 4, src, n);
+                else if constexpr (NG == 2)
+                    cp_async8(at + x * kTile * 8, src, n);
+                else
+                    cp_async16(at + x * kTile * 16, src, n);
+            }
+            if (lane == 0) {
+                sts128(to + note_at(NG), make_uint4(ld.valid, (uint32_t)ld.b, (uint32_t)ld.hr,
+                                                    (uint32_t)ld.tile));
+                sts128(to + note_at(NG) + 16, make_uint4((uint32_t)ld.tiles, (uint32_t)ld.n,
+                                                         (uint32_t)ld.ns, (uint32_t)ld.skip));
+            }
+            put = put + 1 == kStages ? 0 : put + 1;
             if (--to_load > 0) {
-                advance(ld, a, hrs);
-                load_slots(slot, a, ld, lane);
+                if (++ld.tile == ld.tiles) {
+                    ld.tile = 0;
+                    if (++ld.hr == hrs) {
+                        ld.hr = 0;
+                        Keys k;
+                        do
+                            k = keys_of(a, (uint32_t)++ld.b);
+                        while (k.count == 0);  // tiles are left, so keys are
+                        ld.n = k.n;
+                        ld.ns = k.ns;
+                        ld.skip = k.skip;
+                        ld.tiles = k.tiles();
+                    }
+                }
+                load_slot();
             }
         }
         cp_async_commit();
     };
-#pragma unroll
+#pragma unroll 1
     for (int s = 0; s < kStages - 1; ++s)
-        load_next(s);
-
+        load_next();
+    // ---- tiles ----------------------------------------------------------------------------------------
     Unit<NT, NG> u;
     bool fresh = true, from_start = false;
-    int stage = 0;
-    for (int64_t j = start; j < end; ++j) {
+    int get = 0;
+#pragma unroll 1
+    for (uint32_t j = start; j < end; ++j) {
         cp_async_wait<kStages - 2>();
         __syncwarp();
-        load_next(stage == 0 ? kStages - 1 : stage - 1);
+        load_next();
+        const uint32_t from = base + get * stage_bytes(NG);
+        const uint4 n0 = lds128(from + note_at(NG)), n1 = lds128(from + note_at(NG) + 16);
+        const Note at{n0.x, (int)n0.y, (int)n0.z, (int)n0.w, (int)n1.x, (int)n1.y, (int)n1.z, (int)n1.w};
         if (fresh) {
-            begin_unit(u, a, z, cp, lane);
-            from_start = cp.tile == 0;
+            begin_unit(u, a, z, at, lane);
+            from_start = at.tile == 0;
             fresh = false;
         }
-        const uint32_t at = base + stage * stage_bytes(NG);
-        uint64_t valid;
-        asm volatile("ld.shared.u64 %0, [%1];"
-                     : "=l"(valid)
-                     : "r"(at + kTile * 128 + 2 * kTile * 4 * NG)
-                     : "memory");
-        // every row sees every key of the tile: the last key for the first row, the first for the last
-        const int v0 = cp.tile * kTile, v1 = v0 + kTile - 1;
-        const int64_t p0 = v0 < cp.k.ns ? v0 : v0 + cp.k.skip, p1 = v1 < cp.k.ns ? v1 : v1 + cp.k.skip;
-        const bool all = valid == ~0ull && p1 <= cp.k.n - a.q_len &&
-                         (a.window == 0 || p1 < a.n_sink ||
-                          cp.k.n - 1 - (p0 < a.n_sink ? a.n_sink : p0) < a.window);
-        constexpr int MT = NT == 1 ? 4 : 2;
-#pragma unroll 1
-        for (int k0 = 0; k0 < kTile; k0 += MT * 16) {
-            if (all)
-                keys_step<NT, NG, MT, false>(u, a, cp, at, k0, valid, lane);
-            else
-                keys_step<NT, NG, MT, true>(u, a, cp, at, k0, valid, lane);
-        }
-        const bool last = cp.tile + 1 == cp.tiles;
+        take_tile(u, a, z, at, from, lane);
+        const bool last = at.tile + 1 == at.tiles;
         if (last || j + 1 == end) {
             // the share's first unit leaves its part in place 0, a later one in place 1
-            const bool first_unit = j - cp.tile <= start;
-            end_unit(u, a, z, cp, from_start && last, me * 2 + (first_unit ? 0 : 1), lane);
+            const bool first_unit = j - start <= (uint32_t)at.tile;
+            end_unit(u, a, z, at, from_start && last, me * 2 + (first_unit ? 0 : 1), lane);
             fresh = true;
         }
-        if (j + 1 < end)
-            advance(cp, a, hrs);
-        stage = stage + 1 == kStages ? 0 : stage + 1;
+        get = get + 1 == kStages ? 0 : get + 1;
     }
     cp_async_wait<0>();
 }
@@ -662,24 +669,23 @@ __global__ void __launch_bounds__(kThreads, 1)
 // Rows of units that were cut, from their parts in order; rows of sequences without keys.  A warp takes a row.
 template <int NT>
 __global__ void __launch_bounds__(kThreads)
-    kv4_join_kernel(const Kv4AttnArgs a, const Sizes z, int64_t per)
+    kv4_join_kernel(const Kv4AttnArgs a, const Sizes z)
 {
-    __shared__ int64_t s_before[kThreads];
-    __shared__ int64_t s_warp[kWarps];
+    __shared__ uint32_t s_before[kThreads];
+    __shared__ uint32_t s_warp[kWarps];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     pdl_launch_dependents();
     pdl_wait();
-    const int64_t total = scan_tiles(a, z, s_before, s_warp, per);
-    const int64_t share = (total + z.warps - 1) / z.warps;
-    const int64_t rows = (int64_t)a.B * a.q_len * a.n_q;
-    for (int64_t w = (int64_t)blockIdx.x * kWarps + warp; w < rows; w += (int64_t)gridDim.x * kWarps) {
-        const int64_t row = w / a.n_q;
-        const int head = (int)(w - row * a.n_q);
-        const int64_t b = row / a.q_len;
-        const int kv = head / z.heads;
+    const uint32_t total = scan_tiles(a, z, s_before, s_warp);
+    const uint32_t share = (total + z.warps - 1) / z.warps;
+    const uint32_t rows = (uint32_t)a.B * a.q_len * a.n_q;
+#pragma unroll 1
+    for (uint32_t w = blockIdx.x * kWarps + warp; w < rows; w += gridDim.x * kWarps) {
+        const uint32_t row = w / (uint32_t)a.n_q, b = row / (uint32_t)a.q_len;
+        const int head = (int)(w - row * a.n_q), kv = head / z.heads;
         const int r = (int)(row - b * a.q_len) * z.heads + head - kv * z.heads;
         const int rt = r / (NT * 8), in_tile = r - rt * NT * 8;
-        const int64_t tiles = tiles_of(keys_of(a, b));
+        const uint32_t tiles = (uint32_t)keys_of(a, b).tiles();
         uint16_t *out = (uint16_t *)a.out + row * a.out_stride + head * 128 + lane * 4;
         if (tiles == 0) {
             st_global_v2(out, 0u, 0u);
@@ -687,51 +693,67 @@ __global__ void __launch_bounds__(kThreads)
                 a.lse[w] = __uint_as_float(0xff800000u);
             continue;
         }
-        int64_t t0 = s_before[b / per];
-        for (int64_t i = b / per * per; i < b; ++i)
-            t0 += tiles_of(keys_of(a, i)) * a.n_kv * z.rtiles;
-        t0 += ((int64_t)kv * z.rtiles + rt) * tiles;
-        const int64_t w0 = t0 / share, w1 = (t0 + tiles - 1) / share;
+        const uint32_t run = b / z.per;
+        uint32_t t0 = s_before[run], in_run = (uint32_t)(kv * z.rtiles + rt) * tiles;
+#pragma unroll 1
+        for (uint32_t i = run * z.per; i < b; ++i)
+            t0 += (uint32_t)keys_of(a, i).tiles() * (uint32_t)(a.n_kv * z.rtiles);
+        t0 += in_run;
+        const uint32_t w0 = t0 / share, w1 = (t0 + tiles - 1) / share;
         if (w0 == w1)
             continue;  // written whole
-        // part of share i: its place 0 if the unit is the share's first
-        auto part = [&](int64_t i) { return (i * 2 + (i * share >= t0 ? 0 : 1)) * NT * 8 + in_tile; };
-        // a share that starts inside the unit holds it as its first; only share w0 may start before it
-        float m = __uint_as_float(0xff800000u);
-        for (int64_t i = w0 + lane; i <= w1; i += 32)
-            m = fmaxf(m, z.part_ml[part(i) * 2]);
-#pragma unroll
-        for (int off = 16; off > 0; off >>= 1)
-            m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
-        const float mref = m == __uint_as_float(0xff800000u) ? 0.0f : m;
-        float l = 0.0f;
+        // part of share i: its place 0 if the unit is the share's first, which all but share w0 have for sure
+        auto part = [&](uint32_t i) {
+            return (int64_t)(i * 2 + (i * share >= t0 ? 0 : 1)) * NT * 8 + in_tile;
+        };
+        const float ninf = __uint_as_float(0xff800000u);
+        // running maximum over 32 parts at a time
+        float m = ninf, l = 0.0f;
         float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        for (int64_t i0 = w0; i0 <= w1; i0 += 32) {
-            float f = 0.0f, lf = 0.0f;
-            if (i0 + lane <= w1) {
-                const float2 ml = *reinterpret_cast<const float2 *>(z.part_ml + part(i0 + lane) * 2);
-                f = exp2_fast(ml.x - mref);
-                lf = ml.y * f;
-            }
-            const int n = w1 - i0 + 1 < 32 ? (int)(w1 - i0 + 1) : 32;
-#pragma unroll 8
-            for (int i = 0; i < n; ++i) {
-                const float4 x =
-                    *reinterpret_cast<const float4 *>(z.part_o + part(i0 + i) * 128 + lane * 4);
-                const float fi = __shfl_sync(0xffffffffu, f, i);
-                l += __shfl_sync(0xffffffffu, lf, i);
-                o.x = __fmaf_rn(x.x, fi, o.x);
-                o.y = __fmaf_rn(x.y, fi, o.y);
-                o.z = __fmaf_rn(x.z, fi, o.z);
-                o.w = __fmaf_rn(x.w, fi, o.w);
+#pragma unroll 1
+        for (uint32_t i0 = w0; i0 <= w1; i0 += 32) {
+            float2 ml = make_float2(ninf, 0.0f);
+            if (i0 + lane <= w1)
+                ml = *reinterpret_cast<const float2 *>(z.part_ml + part(i0 + lane) * 2);
+            float mx = ml.x;
+#pragma unroll
+            for (int off = 16; off > 0; off >>= 1)
+                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
+            const float mn = fmaxf(m, mx), ref = mn == ninf ? 0.0f : mn, alpha = exp2_fast(m - ref);
+            m = mn;
+            const float f = exp2_fast(ml.x - ref);
+            float lf = ml.y * f;
+#pragma unroll
+            for (int off = 16; off > 0; off >>= 1)
+                lf += __shfl_xor_sync(0xffffffffu, lf, off);
+            l = __fmaf_rn(l, alpha, lf);
+            o.x *= alpha, o.y *= alpha, o.z *= alpha, o.w *= alpha;
+            const int n = (int)min(w1 - i0 + 1, 32u);
+#pragma unroll 1
+            for (int i1 = 0; i1 < n; i1 += 8) {
+                float4 x[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    x[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                    if (i1 + i < n)
+                        x[i] = *reinterpret_cast<const float4 *>(z.part_o + part(i0 + i1 + i) * 128 +
+                                                                 lane * 4);
+                }
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const float fi = __shfl_sync(0xffffffffu, f, i1 + i);
+                    o.x = __fmaf_rn(x[i].x, fi, o.x);
+                    o.y = __fmaf_rn(x[i].y, fi, o.y);
+                    o.z = __fmaf_rn(x[i].z, fi, o.z);
+                    o.w = __fmaf_rn(x[i].w, fi, o.w);
+                }
             }
         }
-        const float inv = __fdiv_rn(1.0f, l);
         const bool none = l == 0.0f;
-        st_global_v2(out, none ? 0u : pack_bf16x2(o.x * inv, o.y * inv),
-                     none ? 0u : pack_bf16x2(o.z * inv, o.w * inv));
+        const float inv = none ? 0.0f : __fdiv_rn(1.0f, l);
+        st_global_v2(out, pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
         if (a.lse && lane == 0)
-            a.lse[w] = none ? __uint_as_float(0xff800000u) : (m + log2f(l)) * kLn2;
+            a.lse[w] = none ? ninf : (m + log2f(l)) * kLn2;
     }
 }
 
@@ -745,11 +767,11 @@ cudaError_t launch(Kv4AttnArgs a, const Kv4AttnPlan &p, cudaStream_t stream)
     z.heads = p.heads;
     z.R = p.R;
     z.rtiles = p.rtiles;
-    z.warps = p.ctas * kWarps;
+    z.warps = (uint32_t)p.ctas * kWarps;
+    z.per = ((uint32_t)a.B + kThreads - 1) / kThreads;
     z.part_o = (float *)a.workspace;
     z.part_ml = z.part_o + (int64_t)z.warps * 2 * NT * 8 * 128;
-    const int64_t per = ((int64_t)a.B + kThreads - 1) / kThreads;
-    const int smem = kWarps * stages_of(NG) * stage_bytes(NG);
+    constexpr int smem = kWarps * stages_of(NG) * stage_bytes(NG);
     static bool done[64] = {};
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -760,12 +782,12 @@ cudaError_t launch(Kv4AttnArgs a, const Kv4AttnPlan &p, cudaStream_t stream)
             done[dev] = true;
     }
     if (e == cudaSuccess)
-        e = launch_pdl(kv4_attn_kernel<NT, NG>, dim3(p.ctas), dim3(kThreads), smem, stream, a, z, per);
+        e = launch_pdl(kv4_attn_kernel<NT, NG>, dim3(p.ctas), dim3(kThreads), smem, stream, a, z);
     if (e == cudaSuccess) {
         const int64_t rows = (int64_t)a.B * a.q_len * a.n_q;
         const int64_t blocks = (rows + kWarps - 1) / kWarps;
         e = launch_pdl(kv4_join_kernel<NT>, dim3((unsigned)(blocks < kSms * 8 ? blocks : kSms * 8)),
-                       dim3(kThreads), 0, stream, a, z, per);
+                       dim3(kThreads), 0, stream, a, z);
     }
     return e != cudaSuccess ? e : cudaGetLastError();
 }
@@ -789,6 +811,7 @@ Kv4AttnPlan kv4_attn_plan(int32_t B, int32_t q_len, int32_t n_q, int32_t n_kv, i
     const int32_t t8 = (p.R + 7) / 8;
     p.nt = t8 < 3 ? t8 : 3;
     p.rtiles = (t8 + p.nt - 1) / p.nt;
+    p.most_tiles = (double)((width + kTile - 1) / kTile) * B * n_kv * p.rtiles;
     // no more warps than tiles there can be
     int64_t most = width;
     if (window > 0 && window + q_len + n_sink < width)

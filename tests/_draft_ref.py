@@ -84,7 +84,7 @@ def kv4_attention(q, k_cache, v_cache, k_scales, v_scales, table, lens, q_len, s
                 out[t, hs] = w @ vv
                 lse[t, hs] = z
                 out_tol[t, hs] = BF16 * out[t, hs].abs() + (FP16 + rel) * (w @ vsc) + rel * (w @ vmin) + \
-                    2.0 ** -39 * float(vsc.max())
+                    15 * 2.0 ** -32 * float(v_scales[at, kv, :, 0].double().max()) * at.numel()
                 lse_tol[t, hs] = ds + 2.0 ** -20 + 2 * (at.numel() + 64) * U32 + 4 * U32 * z.abs()
     return (out, lse), (out_tol, lse_tol)
 
