@@ -74,7 +74,8 @@ BEAM_API int beam_kv4_write_fwd(void *k_cache, void *v_cache, void *k_scales, vo
  *   workspace: at least beam_attn_kv4_workspace(...) bytes, 16-byte aligned
  * num_slots in [0, 2^31); n_q_heads a multiple of n_kv_heads, at most 1024; head_dim must be 128 and group
  * 32, 64 or 128; sm_scale finite; B*q_len*n_q_heads < 2^31; table_width in [0, 2^30); q_len >= 1;
- * window, n_sink >= 0; B * n_kv_heads * table_width * ceil(query rows of a KV head / 24) / 32 below 2^31.  B == 0 returns BEAM_OK without launching.  No output may overlap anything. */
+ * window, n_sink >= 0; B * ceil(table_width / 32) below 2^31.  B == 0 returns BEAM_OK without launching.  No
+ * output may overlap anything. */
 BEAM_API int beam_attn_kv4_fwd(void *out, int64_t out_row_stride, float *lse_out, const void *q,
                                int64_t q_row_stride, const void *k_cache, const void *v_cache,
                                const void *k_scales, const void *v_scales, int64_t num_slots,

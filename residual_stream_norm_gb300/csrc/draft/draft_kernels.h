@@ -51,8 +51,9 @@ struct Kv4AttnPlan {
     int32_t R;         // rows of a sequence and KV head: q_len * heads
     int32_t nt;        // 8-row tiles of a unit: 1, 2 or 3
     int32_t rtiles;    // units of a sequence and KV head
+    int32_t teams;     // of n_kv * rtiles warps
     int32_t ctas;
-    double most_tiles;  // of all units, if every sequence fills its table
+    double most_tiles;  // if every sequence fills its table
     int64_t bytes;     // workspace
 };
 

@@ -14,11 +14,13 @@
 // to 24 query rows of a KV head as the right one, so that few rows waste little: ldmatrix hands out the keys'
 // words, and with a transpose the values' (a 16-bit unit is four columns of a key).
 //
-// Every warp works alone: it owns an even share of all units' tiles of 32 keys, one after the other, copies
-// them with cp.async a few tiles ahead into its own part of shared memory, each with a note of where it stands, and
-// carries the running maximum, sum and output of the unit at hand.  A unit is a sequence, a KV head and a tile of
-// query rows; one that is cut between warps leaves parts (FP32 maximum, sum, output) that a second kernel joins in
-// order.
+// Every warp works alone: it copies tiles of 32 keys with cp.async a few ahead into its own part of shared memory, each
+// with a note of where it stands, and carries the running maximum, sum and output of the unit at hand.  A unit is a
+// sequence, a KV head and a tile of query rows.  All sequences' tiles, one after the other, are cut into even shares,
+// and a share is walked by a team of neighbouring warps, one for each KV head and row tile: the heads' rows of a slot are
+// neighbours in memory, and what one warp's access brings besides is in the L2 cache for the others (with shares of
+// single heads instead, 8 contexts of 100K keys in groups of 32 read 2.6 times their bytes: 355 us, TODO this way).
+// A unit that is cut between teams leaves parts (FP32 maximum, sum, output) that a second kernel joins in order.
 
 #include <cuda_fp16.h>
 
@@ -39,10 +41,10 @@ constexpr int kMinExp = -100;
 
 struct Sizes {
     int32_t heads, R, rtiles;
-    uint32_t warps;         // of the first kernel
+    uint32_t team, teams;   // warps of a team: KV heads * rtiles
     uint32_t per;           // sequences that a thread counts
-    float *part_o;          // [warps][2][8 * NT][128]
-    float *part_ml;         // [warps][2][8 * NT][2]
+    float *part_o;          // [teams][team][2][8 * NT][128]
+    float *part_ml;         // [teams][team][2][8 * NT][2]
 };
 
 // What stands behind a tile's codes and scales: where it is from.
@@ -79,8 +81,8 @@ __device__ __forceinline__ Keys keys_of(const Kv4AttnArgs &a, uint32_t b)
     return k;
 }
 
-// Tiles of all units in front of each thread's run of sequences (s_before), and of all.  Fewer than 2^31 in all
-// (the entry point's checks).
+// Tiles in front of each thread's run of sequences (s_before), and of all sequences.  Fewer than 2^31 in all (the
+// entry point's checks).
 __device__ __forceinline__ uint32_t scan_tiles(const Kv4AttnArgs &a, const Sizes &z, uint32_t *s_before,
                                                uint32_t *s_warp)
 {
@@ -89,7 +91,6 @@ __device__ __forceinline__ uint32_t scan_tiles(const Kv4AttnArgs &a, const Sizes
     const uint32_t first = threadIdx.x * z.per;
     for (uint32_t b = first; b < first + z.per && b < (uint32_t)a.B; ++b)
         own += (uint32_t)keys_of(a, b).tiles();
-    own *= (uint32_t)(a.n_kv * z.rtiles);
     uint32_t s = own;
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
@@ -522,25 +523,13 @@ __device__ __forceinline__ void end_unit(Unit<NT, NG> &u, const Kv4AttnArgs &a, 
         }
 }
 
+// Tiles [start, end) of all sequences, for KV head and row tile hr, by one warp.
 template <int NT, int NG>
-__global__ void __launch_bounds__(kThreads, 1) kv4_attn_kernel(const Kv4AttnArgs a, const Sizes z)
+__device__ __forceinline__ void take_share(const Kv4AttnArgs &a, const Sizes &z, uint32_t base,
+                                           const uint32_t *s_before, uint32_t mine, uint32_t hr,
+                                           uint32_t start, uint32_t end, int lane)
 {
-    extern __shared__ __align__(128) char smem[];
-    __shared__ uint32_t s_before[kThreads];
-    __shared__ uint32_t s_warp[kWarps];
     constexpr int kStages = stages_of(NG);
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    pdl_launch_dependents();
-    pdl_wait();
-    const uint32_t total = scan_tiles(a, z, s_before, s_warp);
-    // neighbouring shares go to different blocks, so that few shares are spread over all SMs
-    const uint32_t me = (uint32_t)warp * gridDim.x + blockIdx.x;
-    const uint32_t share = (total + z.warps - 1) / z.warps;
-    const uint32_t start = me * share, end = min(start + share, total);
-    if (start >= end)
-        return;
-    // ---- where the share starts ---------------------------------------------------------------------
-    const int hrs = a.n_kv * z.rtiles;
     Note ld;
     {
         int lo = 0;  // the last thread's run that starts at or before `start`
@@ -552,22 +541,20 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_kernel(const Kv4AttnArgs
 #pragma unroll 1
         for (uint32_t b = (uint32_t)lo * z.per;; ++b) {
             const Keys k = keys_of(a, b);
-            const uint32_t n = (uint32_t)k.tiles() * hrs;
-            if (start < cum + n) {
+            if (start < cum + (uint32_t)k.tiles()) {
                 ld.b = (int)b;
+                ld.hr = (int)hr;
                 ld.n = k.n;
                 ld.ns = k.ns;
                 ld.skip = k.skip;
                 ld.tiles = k.tiles();
-                ld.hr = (int)((start - cum) / (uint32_t)ld.tiles);
-                ld.tile = (int)((start - cum) - (uint32_t)ld.hr * ld.tiles);
+                ld.tile = (int)(start - cum);
                 break;
             }
-            cum += n;
+            cum += (uint32_t)k.tiles();
         }
     }
-    const uint32_t base =
-        (uint32_t)__cvta_generic_to_shared(smem) + warp * kStages * stage_bytes(NG);
+    const int kv = (int)hr / z.rtiles;
     // ---- copies --------------------------------------------------------------------------------------
     uint32_t to_load = end - start;
     int slot, put = 0;
@@ -583,7 +570,6 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_kernel(const Kv4AttnArgs
     auto load_next = [&]() {
         if (to_load > 0) {
             const uint32_t to = base + put * stage_bytes(NG);
-            const int kv = ld.hr / z.rtiles;
             ld.valid = __ballot_sync(0xffffffffu, slot >= 0);
 #pragma unroll
             for (int i = 0; i < kTile / 8; ++i) {
@@ -616,17 +602,14 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_kernel(const Kv4AttnArgs
             if (--to_load > 0) {
                 if (++ld.tile == ld.tiles) {
                     ld.tile = 0;
-                    if (++ld.hr == hrs) {
-                        ld.hr = 0;
-                        Keys k;
-                        do
-                            k = keys_of(a, (uint32_t)++ld.b);
-                        while (k.count == 0);  // tiles are left, so keys are
-                        ld.n = k.n;
-                        ld.ns = k.ns;
-                        ld.skip = k.skip;
-                        ld.tiles = k.tiles();
-                    }
+                    Keys k;
+                    do
+                        k = keys_of(a, (uint32_t)++ld.b);
+                    while (k.count == 0);  // tiles are left, so keys are
+                    ld.n = k.n;
+                    ld.ns = k.ns;
+                    ld.skip = k.skip;
+                    ld.tiles = k.tiles();
                 }
                 load_slot();
             }
@@ -658,12 +641,40 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_kernel(const Kv4AttnArgs
         if (last || j + 1 == end) {
             // the share's first unit leaves its part in place 0, a later one in place 1
             const bool first_unit = j - start <= (uint32_t)at.tile;
-            end_unit(u, a, z, at, from_start && last, me * 2 + (first_unit ? 0 : 1), lane);
+            end_unit(u, a, z, at, from_start && last, (mine * z.team + hr) * 2 + (first_unit ? 0 : 1), lane);
             fresh = true;
         }
         get = get + 1 == kStages ? 0 : get + 1;
     }
     cp_async_wait<0>();
+    __syncwarp();
+}
+
+template <int NT, int NG>
+__global__ void __launch_bounds__(kThreads, 1) kv4_attn_kernel(const Kv4AttnArgs a, const Sizes z)
+{
+    extern __shared__ __align__(128) char smem[];
+    __shared__ uint32_t s_before[kThreads];
+    __shared__ uint32_t s_warp[kWarps];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    pdl_launch_dependents();
+    pdl_wait();
+    const uint32_t total = scan_tiles(a, z, s_before, s_warp);
+    const uint32_t share = (total + z.teams - 1) / z.teams;
+    if (total == 0)
+        return;
+    const uint32_t active = (total + share - 1) / share;  // teams that have one
+    // the teams' warps, as many at a time as there are; few teams are spread over all places
+#pragma unroll 1
+    for (uint32_t v = blockIdx.x * kWarps + warp; v < z.teams * z.team; v += gridDim.x * kWarps) {
+        const uint32_t place = v / z.team, hr = v - place * z.team;
+        const uint32_t mine = (place * active + z.teams - 1) / z.teams;
+        if (mine >= active || mine * z.teams / active != place)
+            continue;
+        take_share<NT, NG>(a, z, (uint32_t)__cvta_generic_to_shared(smem) +
+                                     warp * stages_of(NG) * stage_bytes(NG),
+                           s_before, mine, hr, mine * share, min((mine + 1) * share, total), lane);
+    }
 }
 
 // Rows of units that were cut, from their parts in order; rows of sequences without keys.  A warp takes a row.
@@ -677,7 +688,7 @@ __global__ void __launch_bounds__(kThreads)
     pdl_launch_dependents();
     pdl_wait();
     const uint32_t total = scan_tiles(a, z, s_before, s_warp);
-    const uint32_t share = (total + z.warps - 1) / z.warps;
+    const uint32_t share = (total + z.teams - 1) / z.teams;
     const uint32_t rows = (uint32_t)a.B * a.q_len * a.n_q;
 #pragma unroll 1
     for (uint32_t w = blockIdx.x * kWarps + warp; w < rows; w += gridDim.x * kWarps) {
@@ -694,17 +705,17 @@ __global__ void __launch_bounds__(kThreads)
             continue;
         }
         const uint32_t run = b / z.per;
-        uint32_t t0 = s_before[run], in_run = (uint32_t)(kv * z.rtiles + rt) * tiles;
+        uint32_t t0 = s_before[run];
 #pragma unroll 1
         for (uint32_t i = run * z.per; i < b; ++i)
-            t0 += (uint32_t)keys_of(a, i).tiles() * (uint32_t)(a.n_kv * z.rtiles);
-        t0 += in_run;
+            t0 += (uint32_t)keys_of(a, i).tiles();
         const uint32_t w0 = t0 / share, w1 = (t0 + tiles - 1) / share;
         if (w0 == w1)
             continue;  // written whole
         // part of share i: its place 0 if the unit is the share's first, which all but share w0 have for sure
         auto part = [&](uint32_t i) {
-            return (int64_t)(i * 2 + (i * share >= t0 ? 0 : 1)) * NT * 8 + in_tile;
+            return (int64_t)((i * z.team + kv * z.rtiles + rt) * 2 + (i * share >= t0 ? 0 : 1)) * NT * 8 +
+                   in_tile;
         };
         const float ninf = __uint_as_float(0xff800000u);
         // running maximum over 32 parts at a time
@@ -767,10 +778,11 @@ cudaError_t launch(Kv4AttnArgs a, const Kv4AttnPlan &p, cudaStream_t stream)
     z.heads = p.heads;
     z.R = p.R;
     z.rtiles = p.rtiles;
-    z.warps = (uint32_t)p.ctas * kWarps;
+    z.team = (uint32_t)(a.n_kv * p.rtiles);
+    z.teams = (uint32_t)p.teams;
     z.per = ((uint32_t)a.B + kThreads - 1) / kThreads;
     z.part_o = (float *)a.workspace;
-    z.part_ml = z.part_o + (int64_t)z.warps * 2 * NT * 8 * 128;
+    z.part_ml = z.part_o + (int64_t)z.teams * z.team * 2 * NT * 8 * 128;
     constexpr int smem = kWarps * stages_of(NG) * stage_bytes(NG);
     static bool done[64] = {};
     int dev = 0;
@@ -811,14 +823,18 @@ Kv4AttnPlan kv4_attn_plan(int32_t B, int32_t q_len, int32_t n_q, int32_t n_kv, i
     const int32_t t8 = (p.R + 7) / 8;
     p.nt = t8 < 3 ? t8 : 3;
     p.rtiles = (t8 + p.nt - 1) / p.nt;
-    p.most_tiles = (double)((width + kTile - 1) / kTile) * B * n_kv * p.rtiles;
-    // no more warps than tiles there can be
+    p.most_tiles = (double)((width + kTile - 1) / kTile) * B;
+    // as many teams as all SMs' warps make, but no more than there can be tiles
     int64_t most = width;
     if (window > 0 && window + q_len + n_sink < width)
         most = window + q_len + n_sink;
-    const double tiles = (double)((most + kTile - 1) / kTile) * B * n_kv * p.rtiles;
-    p.ctas = tiles < kSms ? (int32_t)(tiles < 1 ? 1 : tiles) : kSms;
-    p.bytes = (int64_t)p.ctas * kWarps * 2 * p.nt * 8 * (128 + 2) * 4;
+    const double tiles = (double)((most + kTile - 1) / kTile) * B;
+    const int32_t team = n_kv * p.rtiles, warps = kSms * kWarps;
+    p.teams = team < warps ? warps / team : 1;
+    p.teams = tiles < p.teams ? (int32_t)(tiles < 1 ? 1 : tiles) : p.teams;
+    const int64_t all = (int64_t)p.teams * team;
+    p.ctas = all < warps ? (int32_t)((all + kWarps - 1) / kWarps) : kSms;
+    p.bytes = all * 2 * p.nt * 8 * (128 + 2) * 4;
     return p;
 }
 
