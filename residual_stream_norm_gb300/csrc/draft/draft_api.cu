@@ -30,7 +30,7 @@ int check_attn_sizes(int32_t B, int32_t q_len, int32_t n_q, int32_t n_kv, int64_
     if ((int64_t)B * q_len >= kMost || (int64_t)B * q_len * n_q >= kMost)
         return BEAM_ERR_INVALID_ARG;
     // the kernel counts tiles of keys in 31 bits
-    if (beam::kv4_attn_plan(B, q_len, n_q, n_kv, width, window, n_sink).most_tiles >= (double)kMost)
+    if (beam::kv4_attn_plan(B, q_len, n_q, n_kv, width, window, n_sink, 128).most_tiles >= (double)kMost)
         return BEAM_ERR_INVALID_ARG;
     return BEAM_OK;
 }
@@ -92,7 +92,15 @@ int64_t beam_attn_kv4_workspace(int32_t B, int32_t q_len, int32_t n_q_heads, int
         check_attn_sizes(B, q_len, n_q_heads, n_kv_heads, table_width, window, n_sink);
     if (st != BEAM_OK || B == 0)
         return st;
-    return beam::kv4_attn_plan(B, q_len, n_q_heads, n_kv_heads, table_width, window, n_sink).bytes;
+    // enough for a cache in any groups
+    int64_t most = 0;
+    for (int32_t group = 32; group <= 128; group *= 2) {
+        const int64_t bytes = beam::kv4_attn_plan(B, q_len, n_q_heads, n_kv_heads, table_width, window,
+                                                  n_sink, group)
+                                  .bytes;
+        most = bytes > most ? bytes : most;
+    }
+    return most;
 }
 
 int beam_attn_kv4_fwd(void *out, int64_t out_row_stride, float *lse_out, const void *q,
@@ -127,8 +135,9 @@ int beam_attn_kv4_fwd(void *out, int64_t out_row_stride, float *lse_out, const v
         !aligned(lse_out, 4) || !aligned(workspace, 16))
         return BEAM_ERR_MISALIGNED;
     const beam::Kv4AttnPlan p =
-        beam::kv4_attn_plan(B, q_len, n_q_heads, n_kv_heads, table_width, window, n_sink);
-    if (workspace_bytes < p.bytes)
+        beam::kv4_attn_plan(B, q_len, n_q_heads, n_kv_heads, table_width, window, n_sink, group);
+    if (workspace_bytes < beam_attn_kv4_workspace(B, q_len, n_q_heads, n_kv_heads, table_width, window,
+                                                  n_sink))
         return BEAM_ERR_INVALID_ARG;
     beam::Kv4AttnArgs a{};
     a.out = out;

@@ -52,13 +52,13 @@ struct Kv4AttnPlan {
     int32_t nt;        // 8-row tiles of a unit: 1, 2 or 3
     int32_t rtiles;    // units of a sequence and KV head
     int32_t teams;     // of n_kv * rtiles warps
-    int32_t ctas;
+    int32_t ctas, warps;  // of a block
     double most_tiles;  // if every sequence fills its table
     int64_t bytes;     // workspace
 };
 
 Kv4AttnPlan kv4_attn_plan(int32_t B, int32_t q_len, int32_t n_q, int32_t n_kv, int64_t width,
-                          int64_t window, int64_t n_sink);
+                          int64_t window, int64_t n_sink, int32_t group);
 cudaError_t launch_kv4_attn(const Kv4AttnArgs &a, const Kv4AttnPlan &p, cudaStream_t stream);
 
 struct MoeArgs {

@@ -19,12 +19,13 @@
 // sequence, a KV head and a tile of query rows.  All sequences' tiles, one after the other, are cut into even shares,
 // and a share is walked by a team of neighbouring warps, one for each KV head and row tile: the heads' rows of a slot are
 // neighbours in memory, and what one warp's access brings besides is in the L2 cache for the others (with shares of
-// single heads instead, 8 contexts of 100K keys in groups of 32 read 2.6 times their bytes: 355 us, TODO this way).
+// single heads instead, 8 contexts of 100K keys in groups of 32 read 2.6 times their bytes: 365 us, and 301 so).
 // A unit that is cut between teams leaves parts (FP32 maximum, sum, output) that a second kernel joins in order.
 
 #include <cuda_fp16.h>
 
 #include "beam_device.cuh"
+#include "beam_f32x2.cuh"
 #include "decode/decode_mma.cuh"
 #include "draft_kernels.h"
 
@@ -32,9 +33,16 @@ namespace beam {
 namespace {
 
 constexpr int kSms = 152;
-constexpr int kWarps = 8;
-constexpr int kThreads = kWarps * 32;
+constexpr int kScan = 256;  // threads that count tiles
 constexpr int kTile = 32;  // keys
+
+// Warps of a block: 16, 12 or 8, as the registers of NT 8-row tiles allow without spilling more than a few (128, 168 or
+// 255 a thread).  Measured: 8 contexts of 100K keys, NT = 1: groups of 128 176 us with 16 and 190 with 12, of 32 240 and
+// 234 (8 warps: 301); 32 sequences of up to 20K, NT = 2: groups of 128 157 us with 8 and 131 with 12, of 32 205 and 215.
+__host__ __device__ constexpr int warps_of(int NT, int NG)
+{
+    return NT == 1 ? (NG == 4 ? 12 : 16) : (NT == 2 && NG == 1 ? 12 : 8);
+}
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr int kMinExp = -100;
@@ -55,10 +63,20 @@ struct Note {
     int n, ns, skip;         // keys of the sequence; see Keys
 };
 
-__host__ __device__ constexpr int stages_of(int NG) { return NG == 4 ? 5 : 6; }
 __host__ __device__ constexpr int scales_at() { return 2 * kTile * 64; }
 __host__ __device__ constexpr int note_at(int NG) { return scales_at() + 2 * kTile * 4 * NG; }
 __host__ __device__ constexpr int stage_bytes(int NG) { return note_at(NG) + (int)sizeof(Note); }
+constexpr int kSmem = 225 * 1024;
+__host__ __device__ constexpr int query_bytes(int NT) { return NT > 1 ? NT * 4 * 32 * 16 : 0; }
+__host__ __device__ constexpr int stages_of(int NT, int NG)
+{
+    const int fit = (kSmem / warps_of(NT, NG) - query_bytes(NT)) / stage_bytes(NG);
+    return fit < 6 ? fit : 6;
+}
+__host__ __device__ constexpr int warp_bytes(int NT, int NG)
+{
+    return stages_of(NT, NG) * stage_bytes(NG) + query_bytes(NT);
+}
 
 // The keys that any row of a sequence sees, in a list of its own: first the `ns` sinks, then those from
 // ns + skip on.
@@ -87,27 +105,31 @@ __device__ __forceinline__ uint32_t scan_tiles(const Kv4AttnArgs &a, const Sizes
                                                uint32_t *s_warp)
 {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    uint32_t own = 0;
-    const uint32_t first = threadIdx.x * z.per;
-    for (uint32_t b = first; b < first + z.per && b < (uint32_t)a.B; ++b)
-        own += (uint32_t)keys_of(a, b).tiles();
-    uint32_t s = own;
+    uint32_t own = 0, s = 0;
+    if (threadIdx.x < kScan) {
+        const uint32_t first = threadIdx.x * z.per;
+#pragma unroll 1
+        for (uint32_t b = first; b < first + z.per && b < (uint32_t)a.B; ++b)
+            own += (uint32_t)keys_of(a, b).tiles();
+        s = own;
 #pragma unroll
-    for (int off = 1; off < 32; off <<= 1) {
-        const uint32_t o = __shfl_up_sync(0xffffffffu, s, off);
-        if (lane >= off)
-            s += o;
+        for (int off = 1; off < 32; off <<= 1) {
+            const uint32_t o = __shfl_up_sync(0xffffffffu, s, off);
+            if (lane >= off)
+                s += o;
+        }
+        if (lane == 31)
+            s_warp[warp] = s;
     }
-    if (lane == 31)
-        s_warp[warp] = s;
     __syncthreads();
     uint32_t total = 0, before = s - own;
 #pragma unroll
-    for (int i = 0; i < kWarps; ++i) {
+    for (int i = 0; i < kScan / 32; ++i) {
         before += i < warp ? s_warp[i] : 0;
         total += s_warp[i];
     }
-    s_before[threadIdx.x] = before;
+    if (threadIdx.x < kScan)
+        s_before[threadIdx.x] = before;
     __syncthreads();
     return total;
 }
@@ -143,8 +165,9 @@ __device__ __forceinline__ uint32_t chunk_at(int key, int c)
 
 template <int NT, int NG>
 struct Unit {
-    // query, FP16: columns c*32 + t*8 + {j, j + 4} of row g, j = 0..3 (odd j: a sixteenth)
-    uint32_t q[NT][4][4];
+    // query, FP16: columns c*32 + t*8 + {j, j + 4} of row g, j = 0..3 (odd j: a sixteenth); of more than one row tile
+    // in shared memory, where it leaves room in the registers
+    uint32_t q[1][4][4];
     // rows 2t, 2t+1: with t = scale (sum of products) + minimum qsum, the scores are fac t in powers of two
     float fac[NT][2], qsum[NT][2][NG];
     float m[NT][2], l[NT][2], omin[NT][2][NG];  // of the scaled scores
@@ -156,7 +179,7 @@ struct Unit {
 // Row `row` of a sequence and KV head: its query's index and place in the sequence.
 template <int NT, int NG>
 __device__ __forceinline__ void begin_unit(Unit<NT, NG> &u, const Kv4AttnArgs &a, const Sizes &z,
-                                           const Note &at, int lane)
+                                           const Note &at, uint32_t qb, int lane)
 {
     const int g = lane >> 2, t = lane & 3;
     const int kv = at.hr / z.rtiles, r0 = (at.hr - kv * z.rtiles) * NT * 8;
@@ -198,11 +221,16 @@ __device__ __forceinline__ void begin_unit(Unit<NT, NG> &u, const Kv4AttnArgs &a
                 x[2 * w + 1] = bf_hi(word(v[nt][c], w)) * f;
                 gs[c * NG / 4] += x[2 * w] + x[2 * w + 1];
             }
+            uint32_t q[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 const float h = j & 1 ? 0.0625f : 1.0f;
-                u.q[nt][c][j] = pack_f16x2(x[j] * h, x[j + 4] * h);
+                q[j] = pack_f16x2(x[j] * h, x[j + 4] * h);
+                if (NT == 1)
+                    u.q[0][c][j] = q[j];
             }
+            if (NT > 1)  // read by this lane alone
+                sts128(qb + ((nt * 4 + c) * 32 + lane) * 16, make_uint4(q[0], q[1], q[2], q[3]));
         }
 #pragma unroll
         for (int j = 0; j < NG; ++j) {
@@ -242,7 +270,7 @@ __device__ __forceinline__ void begin_unit(Unit<NT, NG> &u, const Kv4AttnArgs &a
 // rows 2t (i even) and 2t + 1.
 template <int NT, int NG>
 __device__ __forceinline__ void take_tile(Unit<NT, NG> &u, const Kv4AttnArgs &a, const Sizes &z, const Note &at,
-                                          uint32_t kb, int lane)
+                                          uint32_t kb, uint32_t qb, int lane)
 {
     const int g = lane >> 2, t = lane & 3;
     const uint32_t vb = kb + kTile * 64, ksb = kb + scales_at(), vsb = ksb + kTile * 4 * NG;
@@ -256,49 +284,65 @@ __device__ __forceinline__ void take_tile(Unit<NT, NG> &u, const Kv4AttnArgs &a,
     const bool plain = all && u.one_e;
     float s[NT][2][4];
     // ---- scores, but for fac -----------------------------------------------------------------------
+    {
+        uint32_t sc[2][2][NG], lo[2][4], hi[2][4];  // words of chunk c of keys g and g + 8
 #pragma unroll
-    for (int mt = 0; mt < 2; ++mt) {
-        uint32_t lo[4], hi[4];  // words of chunk c of keys g and g + 8
-        {
+        for (int mt = 0; mt < 2; ++mt) {
             const uint32_t from = kb + chunk_at(mt * 16 + (lane & 7), lane >> 3);
-            ldmatrix_x4(lo, from);
-            ldmatrix_x4(hi, from + 8 * 64);
+            ldmatrix_x4(lo[mt], from);
+            ldmatrix_x4(hi[mt], from + 8 * 64);
+            lds_scales<NG>(sc[mt][0], ksb + (mt * 16 + g) * 4 * NG);
+            lds_scales<NG>(sc[mt][1], ksb + (mt * 16 + g + 8) * 4 * NG);
         }
-        float acc[NT][NG][4];
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
+        for (int j = 0; j < NG; ++j) {
+            float acc[NT][2][4];
 #pragma unroll
-            for (int j = 0; j < NG; ++j)
+            for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    acc[nt][j][i] = 0.0f;
+                for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
-        for (int c = 0; c < 4; ++c)
+                    for (int i = 0; i < 4; ++i)
+                        acc[nt][mt][i] = 0.0f;
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const uint32_t wl = lo[c] >> (8 * h), wh = hi[c] >> (8 * h);
-                const uint32_t f[4] = {wl & 0x000f000fu, wh & 0x000f000fu, wl & 0x00f000f0u,
-                                       wh & 0x00f000f0u};
+            for (int c = j * (4 / NG); c < (j + 1) * (4 / NG); ++c) {
+                uint32_t q[NT][4];
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-                    mma16816<true>(acc[nt][c * NG / 4], f, u.q[nt][c][2 * h], u.q[nt][c][2 * h + 1]);
+                for (int nt = 0; nt < NT; ++nt) {
+                    if constexpr (NT == 1) {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            q[nt][i] = u.q[0][c][i];
+                    } else {
+                        const uint4 w = lds128(qb + ((nt * 4 + c) * 32 + lane) * 16);
+                        q[nt][0] = w.x, q[nt][1] = w.y, q[nt][2] = w.z, q[nt][3] = w.w;
+                    }
+                }
+#pragma unroll
+                for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const uint32_t wl = lo[mt][c] >> (8 * h), wh = hi[mt][c] >> (8 * h);
+                        const uint32_t f[4] = {wl & 0x000f000fu, wh & 0x000f000fu, wl & 0x00f000f0u,
+                                               wh & 0x00f000f0u};
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt)
+                            mma16816<true>(acc[nt][mt], f, q[nt][2 * h], q[nt][2 * h + 1]);
+                    }
             }
-        uint32_t sc[2][NG];
-        lds_scales<NG>(sc[0], ksb + (mt * 16 + g) * 4 * NG);
-        lds_scales<NG>(sc[1], ksb + (mt * 16 + g + 8) * 4 * NG);
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
+            for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                float x = bf_hi(sc[i >> 1][0]) * u.qsum[nt][i & 1][0];
+                for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
-                for (int j = 1; j < NG; ++j)
-                    x = __fmaf_rn(bf_hi(sc[i >> 1][j]), u.qsum[nt][i & 1][j], x);
-#pragma unroll
-                for (int j = 0; j < NG; ++j)
-                    x = __fmaf_rn(bf_lo(sc[i >> 1][j]), acc[nt][j][i], x);
-                s[nt][mt][i] = x;
-            }
+                    for (int i = 0; i < 4; ++i) {
+                        const uint32_t w = sc[mt][i >> 1][j];
+                        float &x = s[nt][mt][i];
+                        const float y = u.qsum[nt][i & 1][j];
+                        x = j == 0 ? __fmul_rn(bf_hi(w), y) : __fmaf_rn(bf_hi(w), y, x);
+                        x = __fmaf_rn(bf_lo(w), acc[nt][mt][i], x);
+                    }
+        }
     }
     // ---- what a row does not see; the largest of the values' scales --------------------------------
     // (not of NaN and infinite ones, which show in the output)
@@ -461,8 +505,13 @@ __device__ __forceinline__ void take_tile(Unit<NT, NG> &u, const Kv4AttnArgs &a,
 #pragma unroll
             for (int jj = 0; jj < 2; ++jj)
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    u.o[nt][c][jj][i] = __fmaf_rn(u.o[nt][c][jj][i], up[nt][i & 1], acc[nt][jj][i]);
+                for (int i = 0; i < 4; i += 2) {
+                    float *o = &u.o[nt][c][jj][i];
+                    const f2 x = fma2(make_f2(o[0], o[1]), make_f2(up[nt][0], up[nt][1]),
+                                      make_f2(acc[nt][jj][i], acc[nt][jj][i + 1]));
+                    o[0] = lo_of(x);
+                    o[1] = hi_of(x);
+                }
     }
 }
 
@@ -529,12 +578,13 @@ __device__ __forceinline__ void take_share(const Kv4AttnArgs &a, const Sizes &z,
                                            const uint32_t *s_before, uint32_t mine, uint32_t hr,
                                            uint32_t start, uint32_t end, int lane)
 {
-    constexpr int kStages = stages_of(NG);
+    constexpr int kStages = stages_of(NT, NG);
+    const uint32_t qb = base + kStages * stage_bytes(NG);
     Note ld;
     {
         int lo = 0;  // the last thread's run that starts at or before `start`
 #pragma unroll 1
-        for (int step = kThreads / 2; step > 0; step /= 2)
+        for (int step = kScan / 2; step > 0; step /= 2)
             if (s_before[lo + step] <= start)
                 lo += step;
         uint32_t cum = s_before[lo];
@@ -567,30 +617,37 @@ __device__ __forceinline__ void take_share(const Kv4AttnArgs &a, const Sizes &z,
         }
     };
     load_slot();
+    // of a slot: the lane's 16 bytes of one of eight rows, and its scales
+    const char *src[2], *src_scales[2];
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+        src[x] = (const char *)a.cache[x] + kv * 64 + (lane & 3) * 16;
+        src_scales[x] = (const char *)a.scales[x] + kv * 4 * NG;
+    }
+    const uint32_t slot_bytes = (uint32_t)a.n_kv * 64u, slot_scales = (uint32_t)a.n_kv * 4u * NG;
+    const uint32_t lane_at = chunk_at(lane >> 2, lane & 3);
     auto load_next = [&]() {
         if (to_load > 0) {
             const uint32_t to = base + put * stage_bytes(NG);
             ld.valid = __ballot_sync(0xffffffffu, slot >= 0);
 #pragma unroll
             for (int i = 0; i < kTile / 8; ++i) {
-                const int key = i * 8 + (lane >> 2);
-                const int s = __shfl_sync(0xffffffffu, slot, key);
-                const int64_t off = ((int64_t)max(s, 0) * a.n_kv + kv) * 64 + (lane & 3) * 16;
-                const uint32_t at = to + chunk_at(key, lane & 3), n = s >= 0 ? 16u : 0u;
-                cp_async16(at, a.cache[0] + off, n);
-                cp_async16(at + kTile * 64, a.cache[1] + off, n);
+                const int at_key = __shfl_sync(0xffffffffu, slot, i * 8 + (lane >> 2));
+                const uint64_t off = (uint64_t)(uint32_t)max(at_key, 0) * slot_bytes;
+                const uint32_t n = at_key >= 0 ? 16u : 0u;
+                cp_async16(to + lane_at + i * 512, src[0] + off, n);
+                cp_async16(to + lane_at + i * 512 + kTile * 64, src[1] + off, n);
             }
-            const int64_t off = ((int64_t)max(slot, 0) * a.n_kv + kv) * 4 * NG;
+            const uint64_t off = (uint64_t)(uint32_t)max(slot, 0) * slot_scales;
             const uint32_t at = to + scales_at() + lane * 4 * NG, n = slot >= 0 ? 4u * NG : 0u;
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
-                const char *src = (const char *)a.scales[x] + off;
                 if constexpr (NG == 1)
-                    cp_async4(at + x * kTile * 4, src, n);
+                    cp_async4(at + x * kTile * 4, src_scales[x] + off, n);
                 else if constexpr (NG == 2)
-                    cp_async8(at + x * kTile * 8, src, n);
+                    cp_async8(at + x * kTile * 8, src_scales[x] + off, n);
                 else
-                    cp_async16(at + x * kTile * 16, src, n);
+                    cp_async16(at + x * kTile * 16, src_scales[x] + off, n);
             }
             if (lane == 0) {
                 sts128(to + note_at(NG), make_uint4(ld.valid, (uint32_t)ld.b, (uint32_t)ld.hr,
@@ -632,11 +689,11 @@ __device__ __forceinline__ void take_share(const Kv4AttnArgs &a, const Sizes &z,
         const uint4 n0 = lds128(from + note_at(NG)), n1 = lds128(from + note_at(NG) + 16);
         const Note at{n0.x, (int)n0.y, (int)n0.z, (int)n0.w, (int)n1.x, (int)n1.y, (int)n1.z, (int)n1.w};
         if (fresh) {
-            begin_unit(u, a, z, at, lane);
+            begin_unit(u, a, z, at, qb, lane);
             from_start = at.tile == 0;
             fresh = false;
         }
-        take_tile(u, a, z, at, from, lane);
+        take_tile(u, a, z, at, from, qb, lane);
         const bool last = at.tile + 1 == at.tiles;
         if (last || j + 1 == end) {
             // the share's first unit leaves its part in place 0, a later one in place 1
@@ -651,11 +708,11 @@ __device__ __forceinline__ void take_share(const Kv4AttnArgs &a, const Sizes &z,
 }
 
 template <int NT, int NG>
-__global__ void __launch_bounds__(kThreads, 1) kv4_attn_kernel(const Kv4AttnArgs a, const Sizes z)
+__global__ void __launch_bounds__(warps_of(NT, NG) * 32, 1) kv4_attn_kernel(const Kv4AttnArgs a, const Sizes z)
 {
     extern __shared__ __align__(128) char smem[];
-    __shared__ uint32_t s_before[kThreads];
-    __shared__ uint32_t s_warp[kWarps];
+    __shared__ uint32_t s_before[kScan];
+    __shared__ uint32_t s_warp[kScan / 32];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     pdl_launch_dependents();
     pdl_wait();
@@ -665,25 +722,26 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_kernel(const Kv4AttnArgs
         return;
     const uint32_t active = (total + share - 1) / share;  // teams that have one
     // the teams' warps, as many at a time as there are; few teams are spread over all places
+    const uint32_t warps = blockDim.x / 32;
 #pragma unroll 1
-    for (uint32_t v = blockIdx.x * kWarps + warp; v < z.teams * z.team; v += gridDim.x * kWarps) {
+    for (uint32_t v = blockIdx.x * warps + warp; v < z.teams * z.team; v += gridDim.x * warps) {
         const uint32_t place = v / z.team, hr = v - place * z.team;
         const uint32_t mine = (place * active + z.teams - 1) / z.teams;
         if (mine >= active || mine * z.teams / active != place)
             continue;
         take_share<NT, NG>(a, z, (uint32_t)__cvta_generic_to_shared(smem) +
-                                     warp * stages_of(NG) * stage_bytes(NG),
+                                     warp * warp_bytes(NT, NG),
                            s_before, mine, hr, mine * share, min((mine + 1) * share, total), lane);
     }
 }
 
 // Rows of units that were cut, from their parts in order; rows of sequences without keys.  A warp takes a row.
 template <int NT>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kScan)
     kv4_join_kernel(const Kv4AttnArgs a, const Sizes z)
 {
-    __shared__ uint32_t s_before[kThreads];
-    __shared__ uint32_t s_warp[kWarps];
+    __shared__ uint32_t s_before[kScan];
+    __shared__ uint32_t s_warp[kScan / 32];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     pdl_launch_dependents();
     pdl_wait();
@@ -691,7 +749,7 @@ __global__ void __launch_bounds__(kThreads)
     const uint32_t share = (total + z.teams - 1) / z.teams;
     const uint32_t rows = (uint32_t)a.B * a.q_len * a.n_q;
 #pragma unroll 1
-    for (uint32_t w = blockIdx.x * kWarps + warp; w < rows; w += gridDim.x * kWarps) {
+    for (uint32_t w = blockIdx.x * (kScan / 32) + warp; w < rows; w += gridDim.x * (kScan / 32)) {
         const uint32_t row = w / (uint32_t)a.n_q, b = row / (uint32_t)a.q_len;
         const int head = (int)(w - row * a.n_q), kv = head / z.heads;
         const int r = (int)(row - b * a.q_len) * z.heads + head - kv * z.heads;
@@ -780,10 +838,10 @@ cudaError_t launch(Kv4AttnArgs a, const Kv4AttnPlan &p, cudaStream_t stream)
     z.rtiles = p.rtiles;
     z.team = (uint32_t)(a.n_kv * p.rtiles);
     z.teams = (uint32_t)p.teams;
-    z.per = ((uint32_t)a.B + kThreads - 1) / kThreads;
+    z.per = ((uint32_t)a.B + kScan - 1) / kScan;
     z.part_o = (float *)a.workspace;
     z.part_ml = z.part_o + (int64_t)z.teams * z.team * 2 * NT * 8 * 128;
-    constexpr int smem = kWarps * stages_of(NG) * stage_bytes(NG);
+    constexpr int smem = warps_of(NT, NG) * warp_bytes(NT, NG);
     static bool done[64] = {};
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -794,12 +852,13 @@ cudaError_t launch(Kv4AttnArgs a, const Kv4AttnPlan &p, cudaStream_t stream)
             done[dev] = true;
     }
     if (e == cudaSuccess)
-        e = launch_pdl(kv4_attn_kernel<NT, NG>, dim3(p.ctas), dim3(kThreads), smem, stream, a, z);
+        e = launch_pdl(kv4_attn_kernel<NT, NG>, dim3(p.ctas), dim3(p.warps * 32),
+                       (size_t)p.warps * warp_bytes(NT, NG), stream, a, z);
     if (e == cudaSuccess) {
         const int64_t rows = (int64_t)a.B * a.q_len * a.n_q;
-        const int64_t blocks = (rows + kWarps - 1) / kWarps;
+        const int64_t blocks = (rows + kScan / 32 - 1) / (kScan / 32);
         e = launch_pdl(kv4_join_kernel<NT>, dim3((unsigned)(blocks < kSms * 8 ? blocks : kSms * 8)),
-                       dim3(kThreads), 0, stream, a, z);
+                       dim3(kScan), 0, stream, a, z);
     }
     return e != cudaSuccess ? e : cudaGetLastError();
 }
@@ -815,7 +874,7 @@ cudaError_t launch_groups(const Kv4AttnArgs &a, const Kv4AttnPlan &p, cudaStream
 }  // namespace
 
 Kv4AttnPlan kv4_attn_plan(int32_t B, int32_t q_len, int32_t n_q, int32_t n_kv, int64_t width,
-                          int64_t window, int64_t n_sink)
+                          int64_t window, int64_t n_sink, int32_t group)
 {
     Kv4AttnPlan p{};
     p.heads = n_q / n_kv;
@@ -829,11 +888,16 @@ Kv4AttnPlan kv4_attn_plan(int32_t B, int32_t q_len, int32_t n_q, int32_t n_kv, i
     if (window > 0 && window + q_len + n_sink < width)
         most = window + q_len + n_sink;
     const double tiles = (double)((most + kTile - 1) / kTile) * B;
-    const int32_t team = n_kv * p.rtiles, warps = kSms * kWarps;
+    const int32_t team = n_kv * p.rtiles, warps = kSms * warps_of(p.nt, 128 / group);
     p.teams = team < warps ? warps / team : 1;
     p.teams = tiles < p.teams ? (int32_t)(tiles < 1 ? 1 : tiles) : p.teams;
+    // few warps are spread over the SMs, but at least those that count the tiles stay together
     const int64_t all = (int64_t)p.teams * team;
-    p.ctas = all < warps ? (int32_t)((all + kWarps - 1) / kWarps) : kSms;
+    p.warps = (int32_t)((all + kSms - 1) / kSms);
+    p.warps = p.warps < kScan / 32 ? kScan / 32 : p.warps;
+    p.warps = p.warps < warps / kSms ? p.warps : warps / kSms;
+    p.ctas = (int32_t)((all + p.warps - 1) / p.warps);
+    p.ctas = p.ctas < kSms ? p.ctas : kSms;
     p.bytes = all * 2 * p.nt * 8 * (128 + 2) * 4;
     return p;
 }
