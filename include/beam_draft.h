@@ -7,7 +7,7 @@
  * The conventions of beam_boundary.h and beam_decode.h hold here too: device pointers on the current
  * device, buffers owned by the caller, no allocation and no synchronisation, every argument checked
  * before anything is launched, calls asynchronous on `stream`, programmatic dependent launch.  The
- * router's weights may be read before the preceding kernel of the stream has ended; everything else is
+ * router's weights and bias may be read before the preceding kernel of the stream has ended; everything else is
  * read, and every output written, only after it.  Calls on different streams need workspaces of their
  * own; a workspace's contents need not be kept or cleared between calls.  No kernel here waits for anything but
  * its own block's or cluster's threads and copies.

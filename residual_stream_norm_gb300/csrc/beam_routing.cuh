@@ -151,6 +151,10 @@ __device__ __forceinline__ bool route_token(const float (&s)[kPerLane],
     return all_finite && cm < 1.0e30f && __fsub_rn(g4, g5) > 2.0f * dg && mingap > 2.0f * dc;
 }
 
+// One copy of the exact sigmoid's code for all of a kernel's calls: where eight of them stood in line, fetching
+// them took most of the time of the rare token that needs all scores exactly.
+__device__ __noinline__ float sigmoid_exact(float z) { return sigmoid_rounded(z); }
+
 // Expert ids of one token by one warp, from its 8 logits and biases a lane: lanes k < 8 return slot k's.  The
 // ranking runs on fast sigmoids, unless it is not certified: then on exact ones of every score.
 __device__ __forceinline__ int route_ids(const float (&z)[kPerLane], const float (&bias)[kPerLane], int lane)
@@ -164,7 +168,7 @@ __device__ __forceinline__ int route_ids(const float (&z)[kPerLane], const float
     if (!route_token(s, bias, e0, lane, group, true, my_id)) {
 #pragma unroll
         for (int i = 0; i < kPerLane; ++i)
-            s[i] = sigmoid_rounded(z[i]);
+            s[i] = sigmoid_exact(z[i]);
         route_token(s, bias, e0, lane, group, false, my_id);
     }
     return my_id;
@@ -174,7 +178,7 @@ __device__ __forceinline__ int route_ids(const float (&z)[kPerLane], const float
 // their FP32 sum in slot order.
 __device__ __forceinline__ float route_weight(float z)
 {
-    const float s = sigmoid_rounded(z);
+    const float s = sigmoid_exact(z);
     float wsum = __shfl_sync(0xffffffffu, s, 0);
 #pragma unroll
     for (int k = 1; k < kTopK; ++k)

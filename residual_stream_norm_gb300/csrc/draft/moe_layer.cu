@@ -19,6 +19,7 @@
 // with more than 8 tokens is taken in several passes, the later ones out of the L2 cache.
 
 #include "beam_device.cuh"
+#include "beam_f32x2.cuh"
 #include "beam_routing.cuh"
 #include "decode/decode_mma.cuh"
 #include "draft_kernels.h"
@@ -34,8 +35,6 @@ constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
 constexpr int kFusedTokens = 16;   // tokens that the up kernel routes itself
 constexpr int kCols = 64;          // columns of a stage: 128 bytes of a row
-constexpr int kUpStages = 8;
-constexpr int kDownStages = 6;
 constexpr int kSumRows = 512;      // least rows of the down kernel's sums
 
 // ---------------------------------------------------------------------------------------------
@@ -44,9 +43,9 @@ constexpr int kSumRows = 512;      // least rows of the down kernel's sums
 
 // A block takes two experts and up to 8 tokens; a thread the columns 4 i, i = its number modulo 256, of both.
 // A sum starts at a power of two times 1.5 that is larger than twice all of its terms together: each
-// addition rounds to a grid that the running sum never leaves, so that the part taken up, acc' - acc, is exact, and what is left of
-// the product, one fused multiply-add, goes into a second sum: four instructions a product, where pairs by
-// TwoSum take ten.
+// addition rounds to a grid that the running sum never leaves, so that the part taken up, acc' - acc, is exact, and
+// what is left of the product, one fused multiply-add, goes into a second sum: four operations a product, where pairs
+// by TwoSum take ten.  Both experts' go in one packed instruction.
 constexpr int kRouterExperts = 2;
 constexpr int kRouterTokens = 8;
 constexpr int kRouterVecs = 5;    // float4s of an expert's row a thread holds: 5,120 columns at a time
@@ -60,7 +59,7 @@ __device__ __forceinline__ Sum2 merge_across(Sum2 keep, Sum2 give, int off)
     return sum_merge(keep, o);
 }
 
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, 2)
     moe_router_kernel(float *logits, const uint16_t *x, int64_t x_stride, const float *router_w,
                       int T, int H)
 {
@@ -95,6 +94,17 @@ __global__ void __launch_bounds__(kThreads)
             for (int v = 0; v < kRouterVecs; ++v)
                 mw[e] = fmaxf(fmaxf(fmaxf(mw[e], fabsf(w[e][v].x)), fabsf(w[e][v].y)),
                               fmaxf(fabsf(w[e][v].z), fabsf(w[e][v].w)));
+        uint2 ahead[kRouterVecs];  // the next token's columns
+        auto load_token = [&](int t) {
+#pragma unroll
+            for (int v = 0; v < kRouterVecs; ++v) {
+                const int k = k0 + (v * kThreads + threadIdx.x) * 4;
+                ahead[v] = make_uint2(0u, 0u);
+                if (k < H)
+                    ahead[v] = *reinterpret_cast<const uint2 *>(x + (t0 + t) * x_stride + k);
+            }
+        };
+        load_token(0);
 #pragma unroll
         for (int t = 0; t < kRouterTokens; ++t) {
             if (t >= n)
@@ -102,12 +112,10 @@ __global__ void __launch_bounds__(kThreads)
             uint2 xv[kRouterVecs];
             float mx = 0.0f;
 #pragma unroll
-            for (int v = 0; v < kRouterVecs; ++v) {
-                const int k = k0 + (v * kThreads + threadIdx.x) * 4;
-                xv[v] = make_uint2(0u, 0u);
-                if (k < H)
-                    xv[v] = *reinterpret_cast<const uint2 *>(x + (t0 + t) * x_stride + k);
-            }
+            for (int v = 0; v < kRouterVecs; ++v)
+                xv[v] = ahead[v];
+            if (t + 1 < n)
+                load_token(t + 1);
             float xs[kRouterVecs][4];
 #pragma unroll
             for (int v = 0; v < kRouterVecs; ++v) {
@@ -117,27 +125,31 @@ __global__ void __launch_bounds__(kThreads)
                 for (int j = 0; j < 4; ++j)
                     mx = fmaxf(mx, fabsf(xs[v][j]));
             }
+            // 20 terms of at most mx mw each are below 2^(E + 1), E the exponent of 32 mx mw; 1.5 2^(E + 2)
+            float seed[2];
 #pragma unroll
-            for (int e = 0; e < kRouterExperts; ++e) {
-                // 20 terms of at most mx mw each are below 2^(E + 1), E the exponent of 32 mx mw; 1.5 2^(E + 2)
+            for (int e = 0; e < 2; ++e) {
                 const float bound = __fmul_rn(__fmul_rn(mx, 32.0f), mw[e]);
-                const float seed = __fmul_rn(
+                seed[e] = __fmul_rn(
                     __uint_as_float(max(__float_as_uint(bound) & 0x7f800000u, 0x01000000u)), 6.0f);
-                float acc = seed, lo = 0.0f;
-#pragma unroll
-                for (int v = 0; v < kRouterVecs; ++v) {
-                    const float ws[4] = {w[e][v].x, w[e][v].y, w[e][v].z, w[e][v].w};
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const float next = __fmaf_rn(xs[v][j], ws[j], acc);
-                        lo = __fadd_rn(lo, __fmaf_rn(xs[v][j], ws[j], -__fsub_rn(next, acc)));
-                        acc = next;
-                    }
-                }
-                Sum2 &s = total[e * kRouterTokens + t];
-                // a NaN or infinite term: seed or sum is not finite, and the logit is NaN
-                s = sum_merge(s, Sum2{__fsub_rn(acc, seed), lo});
             }
+            const f2 start = make_f2(seed[0], seed[1]);
+            f2 acc = start, lo = splat(0.0f);
+#pragma unroll
+            for (int v = 0; v < kRouterVecs; ++v) {
+                const f2 ws[4] = {make_f2(w[0][v].x, w[1][v].x), make_f2(w[0][v].y, w[1][v].y),
+                                  make_f2(w[0][v].z, w[1][v].z), make_f2(w[0][v].w, w[1][v].w)};
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const f2 x2 = splat(xs[v][j]), next = fma2(x2, ws[j], acc);
+                    lo = add2(lo, fma2(x2, ws[j], sub2(acc, next)));
+                    acc = next;
+                }
+            }
+            acc = sub2(acc, start);
+            // a NaN or infinite term: seed or sum is not finite, and the logit is NaN
+            total[t] = sum_merge(total[t], Sum2{lo_of(acc), lo_of(lo)});
+            total[kRouterTokens + t] = sum_merge(total[kRouterTokens + t], Sum2{hi_of(acc), hi_of(lo)});
         }
     }
     // 16 sums over 32 lanes: each step hands half of the sums to the other half of the lanes
@@ -188,11 +200,56 @@ struct PassScratch {
     int16_t begin[kExperts];                // an expert's first pass
     int16_t fill[kWarps][kExperts];         // its pairs, by the warp that counted them
     int32_t ids[kFusedTokens * kTopK];      // of tokens that this block routed
+    int32_t pass_of[kFusedTokens * kTopK];
 };
 
 __host__ __device__ constexpr int most_passes(int T)
 {
     return T * kTopK < kExperts + T ? T * kTopK : kExperts + T;
+}
+
+// Passes of up to 128 pairs, whose experts stand in ps.ids, by pair: which earlier pairs have the same expert.
+// Passes are in the order of their first pairs.  All threads; every block makes the same ones, since blocks share a
+// pass's places.
+__device__ __forceinline__ void build_few_passes(Passes &list, PassScratch &ps, int n, int first, int local)
+{
+    const int i = threadIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int e = i < n ? ps.ids[i] : -1;
+    const bool in = e >= first && e < first + local;
+    int before = 0, lead = i;  // the pair that opens this one's pass
+    if (in) {
+#pragma unroll 1
+        for (int j = 0; j < i; ++j)
+            if (ps.ids[j] == e) {
+                lead = before % kPassTokens == 0 ? j : lead;
+                ++before;
+            }
+    }
+    const bool opens = in && before % kPassTokens == 0;
+    const uint32_t all = __ballot_sync(0xffffffffu, opens);
+    if (lane == 0)
+        ps.scan[warp] = __popc(all);
+    __syncthreads();
+    int pass = __popc(all & ((1u << lane) - 1u)), total = 0;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+        pass += w < warp ? ps.scan[w] : 0;
+        total += ps.scan[w];
+    }
+    if (opens) {
+        ps.pass_of[i] = pass;
+        list.info[pass] = 0;
+    }
+    if (i == 0)
+        list.count = total;
+    __syncthreads();
+    if (in) {
+        pass = ps.pass_of[opens ? i : lead];
+        reinterpret_cast<int16_t *>(&list.pairs[pass])[before % kPassTokens] = (int16_t)i;
+        // the last pair of the pass has the largest number
+        atomicMax(&list.info[pass], (e - first) | (before % kPassTokens + 1) << 16);
+    }
+    __syncthreads();
 }
 
 // All threads.  Passes are in the order of experts, an expert's pairs in their own: every block makes the same ones,
@@ -266,8 +323,14 @@ __device__ __forceinline__ void build_passes(Passes &list, PassScratch &ps, cons
 }
 
 // ---------------------------------------------------------------------------------------------
-// the warps' streams
+// up and down: one kernel, since code that a kernel runs for the first time on an SM comes from far: the second run
+// finds most of it there
 // ---------------------------------------------------------------------------------------------
+
+constexpr int kStages = 6;
+constexpr int kStageBytes = (16 + 16) * 128;   // 16 rows of weights; 8 tokens, in two parts for down
+constexpr int kAreaBytes = 2 * kWarps * 128 * 4;
+constexpr uint32_t kAbsent = 0xffffffffu;  // a weight (a NaN that no product gives): the expert is not here
 
 // Where the 16 bytes `c` of row `row` of a stage stand: rows that eight neighbouring threads read together, 2r and
 // 2r + 1, take different halves of the 128 bytes that a row has.
@@ -275,13 +338,6 @@ __device__ __forceinline__ uint32_t swizzled(int row, int c)
 {
     return (uint32_t)(row * 128 + ((c ^ (((row & 1) << 2) | ((row >> 1) & 3))) << 4));
 }
-
-// Rows of a tile that a lane copies: rows lane / 8 + 4 i of the weights and of the tokens; nullptr: none.
-template <int XR>
-struct Rows {
-    const uint16_t *w[4];
-    const uint16_t *x[XR / 4];
-};
 
 // How a block's tiles are shared out: `parts` warps take a part of a tile's columns each.
 struct Cut {
@@ -297,117 +353,6 @@ Cut make_cut(int K)
     return c;
 }
 
-__host__ __device__ constexpr int stage_bytes(int XR) { return (16 + XR) * 128; }
-constexpr int kAreaBytes = 2 * kWarps * 128 * 4;
-
-// All tiles of the block.  rows_of(tile) gives the rows that this lane copies; drained() is called once by each
-// warp when its last copy is under way.  Joint: done(round, area) is called by all threads behind a barrier, with the
-// sums [warp][16 rows][8 tokens] of the round's 8 / parts tiles.  Otherwise warps go on by themselves, and a warp calls
-// done(tile, part, its sums).  XR is 8, or 16: the tokens' rows in two parts whose sum they are.
-template <int XR, int D, bool Joint, typename RowsOf, typename Done, typename Drained>
-__device__ __forceinline__ void run_tiles(char *smem, float *area, const Cut &c, int tiles, RowsOf rows_of,
-                                          Done done, Drained drained)
-{
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int g = lane >> 2, t = lane & 3;
-    const int at_once = kWarps / c.parts, rounds = (tiles + at_once - 1) / at_once;
-    const int first = warp / c.parts, part = warp % c.parts;
-    const int s0 = c.steps * part / c.parts, steps = c.steps * (part + 1) / c.parts - s0;
-    const int mine = tiles > first ? (tiles - first + at_once - 1) / at_once : 0;
-    const uint32_t base = smem_addr(smem) + warp * D * stage_bytes(XR);
-
-    // copying
-    Rows<XR> rows;
-    int tile = first, step = 0, left = mine * steps, put = 0;
-    const int chunk = lane & 7, row = lane >> 3;
-    auto open_tile = [&]() {
-        rows = rows_of(tile);
-        // past the last column nothing is read, and zeros take its place; rows that are not there are not
-        // copied: what stands in their places reaches only their own sums, which nobody takes
-        const int k = s0 * kCols + chunk * 8 < c.K ? s0 * kCols + chunk * 8 : 0;
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            rows.w[i] = rows.w[i] ? rows.w[i] + k : nullptr;
-#pragma unroll
-        for (int i = 0; i < XR / 4; ++i)
-            rows.x[i] = rows.x[i] ? rows.x[i] + k : nullptr;
-    };
-    auto copy_next = [&]() {
-        if (left > 0) {
-            if (step == 0)
-                open_tile();
-            const uint32_t to = base + put * stage_bytes(XR);
-            const bool in = (s0 + step) * kCols + chunk * 8 < c.K;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                if (rows.w[i])
-                    cp_async16(to + swizzled(i * 4 + row, chunk), rows.w[i] + (in ? step * kCols : 0),
-                               in ? 16u : 0u);
-            }
-#pragma unroll
-            for (int i = 0; i < XR / 4; ++i) {
-                if (rows.x[i])
-                    cp_async16(to + 2048 + swizzled(i * 4 + row, chunk),
-                               rows.x[i] + (in ? step * kCols : 0), in ? 16u : 0u);
-            }
-            put = put + 1 == D ? 0 : put + 1;
-            if (++step == steps) {
-                step = 0;
-                tile += at_once;
-            }
-            if (--left == 0)
-                drained();
-        }
-        cp_async_commit();
-    };
-    if (mine == 0)
-        drained();
-    // not unrolled: code that runs once is bound by its fetching
-#pragma unroll 1
-    for (int i = 0; i < D - 1; ++i)
-        copy_next();
-
-    int get = 0;
-    for (int round = 0; round < rounds; ++round) {
-        float *sums = area + (round & 1) * kWarps * 128;
-        if (round * at_once + first < tiles) {
-            float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll 1
-            for (int s = 0; s < steps; ++s) {
-                cp_async_wait<D - 2>();
-                __syncwarp();
-                copy_next();
-                const uint32_t from = base + get * stage_bytes(XR);
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const uint32_t a = from + swizzled(g, h * 4 + t);
-                    const uint4 lo = lds128(a), hi = lds128(a + 1024);
-                    const uint32_t f0[4] = {lo.x, hi.x, lo.y, hi.y}, f1[4] = {lo.z, hi.z, lo.w, hi.w};
-#pragma unroll
-                    for (int y = 0; y < XR / 8; ++y) {
-                        const uint4 x = lds128(a + 2048 + y * 1024);
-                        mma16816<false>(acc, f0, x.x, x.y);
-                        mma16816<false>(acc, f1, x.z, x.w);
-                    }
-                }
-                get = get + 1 == D ? 0 : get + 1;
-            }
-            if constexpr (Joint) {
-                float *to = sums + warp * 128;
-                *reinterpret_cast<float2 *>(to + g * 8 + 2 * t) = make_float2(acc[0], acc[1]);
-                *reinterpret_cast<float2 *>(to + (8 + g) * 8 + 2 * t) = make_float2(acc[2], acc[3]);
-            } else {
-                done(round * at_once + first, part, acc);
-            }
-        }
-        if constexpr (Joint) {
-            __syncthreads();
-            done(round, sums);
-        }
-    }
-    cp_async_wait<0>();
-}
-
 struct ShareArgs {
     const uint16_t *x;
     int64_t x_stride;
@@ -419,290 +364,376 @@ struct ShareArgs {
     int32_t *ids;
     float *weights;
     Passes *passes;
-    int32_t first, local, T, H, F;
-    float scaling;
-    Cut cut;
     float *sums;               // [sum_rows][H]: a pair's share of the output, by part and pair
     int32_t sum_rows;
+    int32_t first, local, T, H, F;
+    float scaling;
+    bool down;
+    Cut cut;
 };
 
 // The block's rows of the down projection: [from, to).
 __device__ __forceinline__ void down_rows(const ShareArgs &a, int block, int blocks, int &from, int &to)
 {
-    from = (int)((int64_t)a.H * block / blocks);
-    to = (int)((int64_t)a.H * (block + 1) / blocks);
+    from = (int)((uint32_t)a.H * block / blocks);
+    to = (int)((uint32_t)a.H * (block + 1) / blocks);
 }
 
-// ---------------------------------------------------------------------------------------------
-// up: a = silu(g) u
-// ---------------------------------------------------------------------------------------------
+// A run cut evenly into tiles, so that none is much smaller than the others.
+struct Run {
+    int base, more;
+    __device__ __forceinline__ Run(int n, int tiles) : base(n / tiles), more(n - n / tiles * tiles) {}
+    __device__ __forceinline__ int from(int i) const { return i * base + min(i, more); }
+    __device__ __forceinline__ int size(int i) const { return base + (i < more ? 1 : 0); }
+};
 
-// A block's share of the places (of F) of all passes, in tiles of up to 8 places of one pass: a first run that
-// may start inside a pass, whole passes, a last run.
-struct UpTiles {
-    int64_t at, end;
-    int F, first_pass, first_run, first_tiles, whole_tiles, count;
-    __device__ __forceinline__ UpTiles(int64_t from, int64_t to, int F_) : at(from), end(to), F(F_)
+// Tiles of the block, walked in order.
+//  up:   its share [at, end) of the places (of F) of all passes: runs inside a pass, in tiles of up to 8 places
+//  down: its rows in tiles of up to 16, for all passes
+struct Tiles {
+    int pass, from, n;  // the tile at hand: its pass, first place or row, and their number
+    int i, tiles;       // its number in the run, the run's tiles
+    uint32_t at, end;   // up: behind the run, behind all
+    int start;          // first place or row of the run
+    Run run{0, 1};
+
+    __device__ __forceinline__ void open_run(const ShareArgs &a)
     {
-        count = first_tiles = first_pass = first_run = 0;
-        whole_tiles = (F + 7) / 8;
-        if (from >= to)
-            return;
-        first_pass = (int)(from / F);
-        const int64_t stop = ((int64_t)first_pass + 1) * F;
-        first_run = (int)((stop < to ? stop : to) - from);
-        first_tiles = (first_run + 7) / 8;
-        const int64_t rest = to - from - first_run;
-        count = first_tiles + (int)(rest / F) * whole_tiles + (int)((rest % F + 7) / 8);
-    }
-    // its pass, first place and number of places
-    __device__ __forceinline__ void get(int i, int &pass, int &f, int &n) const
-    {
-        int run = first_run, tiles = first_tiles, f0;
-        pass = first_pass;
-        if (i < first_tiles) {
-            f0 = (int)(at - (int64_t)first_pass * F);
+        if (a.down) {
+            ++pass;
         } else {
-            i -= first_tiles;
-            const int over = i / whole_tiles;
-            i -= over * whole_tiles;
-            pass += 1 + over;
-            f0 = 0;
-            const int64_t rest = end - (int64_t)pass * F;
-            run = rest < F ? (int)rest : F;
-            tiles = (run + 7) / 8;
+            pass = (int)(at / (uint32_t)a.F);
+            start = (int)(at - (uint32_t)pass * a.F);
+            const int size = min((int)(end - at), a.F - start);
+            tiles = (size + 7) >> 3;
+            run = Run(size, tiles);
+            at += size;
         }
-        // even: none much smaller than the others
-        f = run * i / tiles;
-        n = run * (i + 1) / tiles - f;
-        f += f0;
+        i = 0;
+    }
+    // `by` tiles on; in front of the first at the beginning
+    __device__ __forceinline__ void go(const ShareArgs &a, int by)
+    {
+#pragma unroll 1
+        for (; by > 0; --by)
+            if (++i >= tiles)
+                open_run(a);
+        from = start + run.from(i);
+        n = run.size(i);
     }
 };
 
-__global__ void __launch_bounds__(kThreads, 1) moe_up_kernel(const ShareArgs a)
+// Two blocks' registers to an SM, so that one starts beside the router's.
+__global__ void __launch_bounds__(kThreads, 2) moe_share_kernel(const ShareArgs a)
 {
     extern __shared__ __align__(128) char smem[];
     __shared__ Passes ps;
     __shared__ PassScratch scratch;
-    float *area = reinterpret_cast<float *>(smem + kWarps * kUpStages * stage_bytes(8));
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    float *area = reinterpret_cast<float *>(smem + kWarps * kStages * kStageBytes);
+    float *weight = area;  // down: a pair's weight times the scaling, or kAbsent
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
+    const bool fused = !a.down && a.T <= kFusedTokens;
+    const int pairs = a.T * kTopK;
     pdl_launch_dependents();
-    pdl_wait();
-    const bool fused = a.T <= kFusedTokens;
-    if (fused) {
+    // Twice: first without a pair and without touching memory, while the kernel before still runs, which fetches the
+    // code; then in earnest.  The up kernel finds room beside the router's blocks; the down kernel, which starts as
+    // the up kernel's blocks end, has its code from them.
 #pragma unroll 1
-        for (int t = warp; t < a.T; t += kWarps) {
-            const float4 z0 = ld_stream_f4(a.logits + t * kExperts + lane * kPerLane);
-            const float4 z1 = ld_stream_f4(a.logits + t * kExperts + lane * kPerLane + 4);
-            const float4 b0 = *reinterpret_cast<const float4 *>(a.bias + lane * kPerLane);
-            const float4 b1 = *reinterpret_cast<const float4 *>(a.bias + lane * kPerLane + 4);
-            const float z[kPerLane] = {z0.x, z0.y, z0.z, z0.w, z1.x, z1.y, z1.z, z1.w};
-            const float bias[kPerLane] = {b0.x, b0.y, b0.z, b0.w, b1.x, b1.y, b1.z, b1.w};
-            const int id = route_ids(z, bias, lane);
-            if (lane < kTopK)
-                scratch.ids[t * kTopK + lane] = id;
-        }
-        __syncthreads();
-    }
-    build_passes(ps, scratch, fused ? scratch.ids : a.ids, a.T, a.first, a.local);
-    if (blockIdx.x == 0) {  // for the next kernel
-        for (int i = threadIdx.x; i < ps.count; i += kThreads) {
-            a.passes->info[i] = ps.info[i];
-            a.passes->pairs[i] = ps.pairs[i];
-        }
-        if (threadIdx.x == 0)
-            a.passes->count = ps.count;
-    }
-    const int64_t places = (int64_t)ps.count * a.F;
-    const UpTiles tiles(places * blockIdx.x / gridDim.x, places * (blockIdx.x + 1) / gridDim.x, a.F);
-    const int64_t n_act = (int64_t)a.T * kTopK * a.F;
-    run_tiles<8, kUpStages, true>(
-        smem, area, a.cut, tiles.count,
-        [&](int i) {
-            int pass, f, n;
-            tiles.get(i, pass, f, n);
-            const uint16_t *w = a.w13 + ((int64_t)ps.expert(pass) * 2 * a.F + f) * a.H;
-            Rows<8> r;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {  // rows 0-7: gate; 8-15: up
-                const int row = (lane >> 3) + 4 * j;
-                r.w[j] = (row & 7) < n ? w + ((row & 7) + (row < 8 ? 0 : (int64_t)a.F)) * a.H : nullptr;
+    for (int dry = a.down ? 0 : 1; dry >= 0; --dry) {
+        if (!dry)
+            pdl_wait();
+        // ---- routing and passes --------------------------------------------------------------------------
+        if (a.down) {
+            const int most = most_passes(a.T);
+#pragma unroll 1
+            for (int i = threadIdx.x; i < most; i += kThreads) {
+                ps.info[i] = a.passes->info[i];
+                ps.pairs[i] = ld_plain(&a.passes->pairs[i]);
             }
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                const int row = (lane >> 3) + 4 * j;
-                r.x[j] = row < ps.tokens(pass) ? a.x + (ps.pair(pass, row) / kTopK) * a.x_stride : nullptr;
-            }
-            return r;
-        },
-        [&](int round, const float *sums) {
-            const int parts = a.cut.parts, at_once = kWarps / parts;
-            // places run fastest: neighbouring threads write neighbouring values
-            for (int i = threadIdx.x; i < at_once * 64; i += kThreads) {
-                const int tile = round * at_once + (i >> 6), r = i & 7, j = (i >> 3) & 7;
-                if (tile >= tiles.count)
-                    break;
-                int pass, f, n;
-                tiles.get(tile, pass, f, n);
-                if (r >= n || j >= ps.tokens(pass))
-                    continue;
-                const float *from = sums + (i >> 6) * parts * 128 + r * 8 + j;
-                float g = 0.0f, u = 0.0f;
-                for (int w = 0; w < parts; ++w) {
-                    g += from[w * 128];
-                    u += from[w * 128 + 64];
+            if (threadIdx.x == 0)
+                ps.count = a.passes->count;
+            __syncthreads();
+        } else if (fused) {
+#pragma unroll 1
+            for (int tok = warp; tok < (dry ? kWarps : a.T); tok += kWarps) {
+                float4 z0 = make_float4(lane, 0.0f, 1.0f, 2.0f), z1 = z0;
+                if (!dry) {
+                    z0 = ld_stream_f4(a.logits + tok * kExperts + lane * kPerLane);
+                    z1 = ld_stream_f4(a.logits + tok * kExperts + lane * kPerLane + 4);
                 }
-                const float v = __fdiv_rn(g, 1.0f + expf(-g)) * u;
-                const uint32_t hi = pack_bf16x2(v, 0.0f);
-                uint16_t *to = a.act + (int64_t)ps.pair(pass, j) * a.F + f + r;
-                to[0] = (uint16_t)hi;
-                to[n_act] = (uint16_t)pack_bf16x2(__fsub_rn(v, bf_lo(hi)), 0.0f);
+                const float4 b0 = *reinterpret_cast<const float4 *>(a.bias + lane * kPerLane);
+                const float4 b1 = *reinterpret_cast<const float4 *>(a.bias + lane * kPerLane + 4);
+                const float z[kPerLane] = {z0.x, z0.y, z0.z, z0.w, z1.x, z1.y, z1.z, z1.w};
+                const float bias[kPerLane] = {b0.x, b0.y, b0.z, b0.w, b1.x, b1.y, b1.z, b1.w};
+                const int id = route_ids(z, bias, lane);
+                if (lane < kTopK)
+                    scratch.ids[tok * kTopK + lane] = id;
             }
-        },
-        [&]() {
-            // This warp's last weights are on their way.  The choice's own weights are of use to the next kernel only.
-            if (fused && blockIdx.x == 0) {
+            __syncthreads();
+            build_few_passes(ps, scratch, dry ? kTopK : pairs, dry ? 0 : a.first, dry ? kExperts : a.local);
+        } else {
+            build_passes(ps, scratch, a.ids, dry ? 0 : a.T, a.first, a.local);
+        }
+        if (!dry && !a.down && blockIdx.x == 0) {  // for the down kernel
 #pragma unroll 1
-                for (int t = warp; t < a.T; t += kWarps) {
-                    const int id = lane < kTopK ? scratch.ids[t * kTopK + lane] : 0;
-                    const float w = route_weight(lane < kTopK ? a.logits[t * kExperts + id] : 0.0f);
+            for (int i = threadIdx.x; i < ps.count; i += kThreads) {
+                a.passes->info[i] = ps.info[i];
+                a.passes->pairs[i] = ps.pairs[i];
+            }
+            if (threadIdx.x == 0)
+                a.passes->count = ps.count;
+        }
+        // ---- the block's tiles ------------------------------------------------------------------------------
+        Cut cut = a.cut;
+        Tiles ld;
+        int count, r0 = 0, rows = 0;
+        ld.i = ld.tiles = 0;
+        if (a.down) {
+            int r1;
+            down_rows(a, blockIdx.x, gridDim.x, r0, r1);
+            rows = r1 - r0;
+            ld.tiles = (rows + 15) >> 4;
+            ld.i = ld.tiles - 1;
+            ld.pass = -1;
+            ld.start = r0;
+            ld.run = Run(rows, ld.tiles);
+            count = ld.tiles * ps.count;
+            // few tiles: parts of their columns, so that each warp has some, while there is room for the parts' sums
+            while (cut.parts < kWarps && count * cut.parts < 3 * kWarps && cut.steps >= 4 * cut.parts &&
+                   2 * cut.parts * pairs <= a.sum_rows)
+                cut.parts *= 2;
+        } else {
+            // block 0, which also finishes the routing of few tokens, takes half a share then
+            const uint64_t places = (uint64_t)(ps.count * a.F);
+            const uint32_t b = 2 * blockIdx.x;
+            constexpr uint32_t kWhole = 2 * kSms;  // the grid's blocks, in halves
+            ld.at = (uint32_t)(fused ? places * (b > 0 ? b - 1 : 0) / (kWhole - 1) : places * b / kWhole);
+            ld.end = (uint32_t)(fused ? places * (b + 1) / (kWhole - 1) : places * (b + 2) / kWhole);
+            if (dry) {
+                ld.at = 0;
+                ld.end = 1;
+                cut.steps = cut.parts;
+            }
+            const uint32_t f0 = ld.at % (uint32_t)a.F, n = ld.end - ld.at;
+            const uint32_t n0 = min(n, a.F - f0), rest = n - n0;  // the first run, and what is behind it
+            count = (int)((n0 + 7) / 8 + rest / a.F * (((uint32_t)a.F + 7) / 8) + (rest % a.F + 7) / 8);
+        }
+        Tiles cp = ld;
+        // ---- the warps' streams ------------------------------------------------------------------------------
+        // Up: `parts` warps take a part of a tile's columns each, and their sums meet behind a barrier, a round of
+        // 8 / parts tiles at a time.  Down: warps go on by themselves.
+        const int at_once = kWarps / cut.parts, rounds = (count + at_once - 1) / at_once;
+        const int first = warp / cut.parts, part = warp - first * cut.parts;
+        const int s0 = cut.steps * part / cut.parts, steps = cut.steps * (part + 1) / cut.parts - s0;
+        const int mine = count > first ? (count - first + at_once - 1) / at_once : 0;
+        const uint32_t base = smem_addr(smem) + warp * kStages * kStageBytes;
+        const int chunk = lane & 7, row = lane >> 3;
+        const int64_t n_act = (int64_t)pairs * a.F;
+
+        const uint16_t *w[4], *x[4];  // rows lane / 8 + 4 i of the weights, and of the tokens (down: i >= 2 their
+                                      // second parts); nullptr: none
+        int step = 0, left = mine * steps, put = 0, by = first + 1;
+        auto open_tile = [&]() {
+            ld.go(a, by);
+            by = at_once;
+            // past the last column nothing is read, and zeros take its place; rows that are not there are not
+            // copied: what stands in their places reaches only their own sums, which nobody takes
+            const int k = s0 * kCols + chunk * 8 < cut.K ? s0 * kCols + chunk * 8 : 0;
+            const int e = ps.info[ld.pass] & 0xffff, tokens = dry ? 0 : ps.tokens(ld.pass), n = dry ? 0 : ld.n;
+            const int64_t pitch = a.down ? a.F : a.H;
+            const uint16_t *from =
+                (a.down ? a.w2 + ((int64_t)e * a.H + ld.from) * a.F
+                        : a.w13 + ((int64_t)e * 2 * a.F + ld.from) * a.H) + k;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int r = row + 4 * i;  // up: 0-7 gate, 8-15 up
+                const int64_t at = a.down ? r : (r & 7) + (r < 8 ? 0 : a.F);
+                w[i] = (a.down ? r : r & 7) < n ? from + at * pitch : nullptr;
+            }
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int r = row + 4 * i;
+                x[i] = x[i + 2] = nullptr;
+                if (r < tokens) {
+                    const int pair = ps.pair(ld.pass, r);
+                    x[i] = (a.down ? a.act + (int64_t)pair * a.F : a.x + (pair / kTopK) * a.x_stride) + k;
+                    if (a.down)
+                        x[i + 2] = x[i] + n_act;
+                }
+            }
+        };
+        auto copy_next = [&]() {
+            if (left > 0) {
+                if (step == 0)
+                    open_tile();
+                const uint32_t to = base + put * kStageBytes;
+                const bool in = (s0 + step) * kCols + chunk * 8 < cut.K;
+                const int64_t off = in ? step * kCols : 0;
+                const uint32_t bytes = in ? 16u : 0u;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    if (w[i])
+                        cp_async16(to + swizzled(i * 4 + row, chunk), w[i] + off, bytes);
+                    if (x[i])
+                        cp_async16(to + 2048 + swizzled(i * 4 + row, chunk), x[i] + off, bytes);
+                }
+                put = put + 1 == kStages ? 0 : put + 1;
+                step = step + 1 == steps ? 0 : step + 1;
+                --left;
+            }
+            cp_async_commit();
+        };
+#pragma unroll 1
+        for (int i = 0; i < kStages - 1; ++i)
+            copy_next();
+
+        int get = 0;
+        bool drained = false;
+#pragma unroll 1
+        for (int round = 0; round < rounds; ++round) {
+            float *meet = area + (round & 1) * kWarps * 128;
+            const bool busy = round * at_once + first < count;
+            float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+            if (busy) {
+#pragma unroll 1
+                for (int s = 0; s < steps; ++s) {
+                    cp_async_wait<kStages - 2>();
+                    __syncwarp();
+                    copy_next();
+                    const uint32_t from = base + get * kStageBytes;
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const uint32_t at = from + swizzled(g, h * 4 + t);
+                        const uint4 lo = lds128(at), hi = lds128(at + 1024), y = lds128(at + 2048);
+                        const uint32_t f0[4] = {lo.x, hi.x, lo.y, hi.y}, f1[4] = {lo.z, hi.z, lo.w, hi.w};
+                        mma16816<false>(acc, f0, y.x, y.y);
+                        mma16816<false>(acc, f1, y.z, y.w);
+                        if (a.down) {
+                            const uint4 y2 = lds128(at + 3072);
+                            mma16816<false>(acc, f0, y2.x, y2.y);
+                            mma16816<false>(acc, f1, y2.z, y2.w);
+                        }
+                    }
+                    get = get + 1 == kStages ? 0 : get + 1;
+                }
+            }
+            if (a.down) {
+                if (busy) {  // this warp's rows of the pairs' sums
+                    cp.go(a, round == 0 ? first + 1 : at_once);
+                    const int tokens = ps.tokens(cp.pass);
+                    float *to = a.sums + (int64_t)part * pairs * a.H + cp.from + g;
+#pragma unroll
+                    for (int j = 0; j < 2; ++j)
+                        if (2 * t + j < tokens) {
+                            float *y = to + (int64_t)ps.pair(cp.pass, 2 * t + j) * a.H;
+                            if (g < cp.n)
+                                y[0] = acc[j];
+                            if (g + 8 < cp.n)
+                                y[8] = acc[2 + j];
+                        }
+                }
+            } else {
+                float *to = meet + warp * 128;
+                *reinterpret_cast<float2 *>(to + g * 8 + 2 * t) = make_float2(acc[0], acc[1]);
+                *reinterpret_cast<float2 *>(to + (8 + g) * 8 + 2 * t) = make_float2(acc[2], acc[3]);
+                __syncthreads();
+#pragma unroll 1
+                for (int k = 0; k < at_once && round * at_once + k < count; ++k) {
+                    cp.go(a, 1);
+                    // places run fastest: neighbouring threads write neighbouring values
+                    const int r = threadIdx.x & 7, j = (threadIdx.x >> 3) & 7;
+                    if (threadIdx.x >> 6 != (k & 3) || r >= cp.n || j >= ps.tokens(cp.pass) || dry)
+                        continue;
+                    const float *from = meet + k * cut.parts * 128 + r * 8 + j;
+                    float gate = 0.0f, up = 0.0f;
+#pragma unroll 1
+                    for (int i = 0; i < cut.parts; ++i) {
+                        gate += from[i * 128];
+                        up += from[i * 128 + 64];
+                    }
+                    const float v = __fdiv_rn(gate, 1.0f + expf(-gate)) * up;
+                    const uint32_t hi = pack_bf16x2(v, 0.0f);
+                    uint16_t *y = a.act + (int64_t)ps.pair(cp.pass, j) * a.F + cp.from + r;
+                    y[0] = (uint16_t)hi;
+                    y[n_act] = (uint16_t)pack_bf16x2(__fsub_rn(v, bf_lo(hi)), 0.0f);
+                }
+            }
+            if (!drained && left == 0 && !dry && !a.down && warp == 0) {
+                // The last weights are on their way.  The first ones that the down kernel's block here reads, up to
+                // 192 KB of them, are brought to the L2 cache while that kernel starts.
+                drained = true;
+                int from, to;
+                down_rows(a, blockIdx.x, gridDim.x, from, to);
+                const uint32_t bytes = (uint32_t)(to - from) * (uint32_t)a.F * 2u;
+#pragma unroll 1
+                for (int p = lane; p < ps.count && bytes > 0 && (p + 1) * (int64_t)bytes <= 192 * 1024; p += 32)
+                    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(
+                                     a.w2 + ((int64_t)ps.expert(p) * a.H + from) * a.F),
+                                 "r"(bytes)
+                                 : "memory");
+            }
+        }
+        cp_async_wait<0>();
+        __syncthreads();
+        // ---- the ends -------------------------------------------------------------------------------------------
+        if (!a.down) {
+            if (fused && blockIdx.x == 0 && !dry) {
+                // the choice's weights are of use to the down kernel only
+#pragma unroll 1
+                for (int tok = warp; tok < a.T; tok += kWarps) {
+                    const int id = lane < kTopK ? scratch.ids[tok * kTopK + lane] : 0;
+                    const float v = route_weight(lane < kTopK ? a.logits[tok * kExperts + id] : 0.0f);
                     if (lane < kTopK) {
-                        a.ids[t * kTopK + lane] = id;
-                        a.weights[t * kTopK + lane] = w;
+                        a.ids[tok * kTopK + lane] = id;
+                        a.weights[tok * kTopK + lane] = v;
                     }
                 }
             }
-            // The first weights that the next kernel's block here reads, up to 192 KB of them, are brought to the L2
-            // cache while that kernel starts.
-            if (warp != 0)
-                return;
-            int from, to;
-            down_rows(a, blockIdx.x, gridDim.x, from, to);
-            const uint32_t bytes = (uint32_t)(to - from) * (uint32_t)a.F * 2u;
-            for (int p = lane; p < ps.count && bytes > 0 && (p + 1) * (int64_t)bytes <= 192 * 1024; p += 32)
-                asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(
-                                 a.w2 + ((int64_t)ps.expert(p) * a.H + from) * a.F),
-                             "r"(bytes)
-                             : "memory");
-        });
-}
-
-// ---------------------------------------------------------------------------------------------
-// down: out = sum over the pairs of scaling * weight * w2 a
-// ---------------------------------------------------------------------------------------------
-
-constexpr uint32_t kAbsent = 0xffffffffu;  // a NaN that no product gives
-
-// A block owns some output columns, so it can add up by itself what its warps leave for each pair: warps never
-// wait for one another until then.  Adding round by round in shared memory instead, in order behind barriers, took
-// half of the kernel's instructions (64 tokens of an eighth: 308 us, TODO).
-__global__ void __launch_bounds__(kThreads, 1) moe_down_kernel(const ShareArgs a)
-{
-    extern __shared__ __align__(128) char smem[];
-    __shared__ Passes ps;
-    __shared__ float weight[kMaxTokens * kTopK];  // scaled; kAbsent: the expert is not here
-    const int lane = threadIdx.x & 31, g = lane >> 2, t2 = 2 * (lane & 3);
-    pdl_launch_dependents();
-    pdl_wait();
-    const int most = most_passes(a.T);
-#pragma unroll 1
-    for (int i = threadIdx.x; i < most; i += kThreads) {
-        ps.info[i] = a.passes->info[i];
-        ps.pairs[i] = ld_plain(&a.passes->pairs[i]);
-    }
-    if (threadIdx.x == 0)
-        ps.count = a.passes->count;
-    __syncthreads();
-    int r0, r1;
-    down_rows(a, blockIdx.x, gridDim.x, r0, r1);
-    const int rows = r1 - r0, row_tiles = (rows + 15) / 16, pairs = a.T * kTopK;
-    Cut cut = a.cut;
-    // few tiles: parts of their columns, so that each warp has some, while there is room for the parts' sums
-    while (cut.parts < kWarps && row_tiles * ps.count * cut.parts < 3 * kWarps &&
-           cut.steps >= 4 * cut.parts && 2 * cut.parts * pairs <= a.sum_rows)
-        cut.parts *= 2;
-    const int64_t n_act = (int64_t)pairs * a.F;
-    run_tiles<16, kDownStages, false>(
-        smem, nullptr, cut, row_tiles * ps.count,
-        [&](int i) {
-            const int pass = i / row_tiles, rt = i - pass * row_tiles;
-            const int from = rows * rt / row_tiles, n = rows * (rt + 1) / row_tiles - from;
-            const uint16_t *w = a.w2 + ((int64_t)ps.expert(pass) * a.H + r0 + from) * a.F;
-            Rows<16> r;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int row = (lane >> 3) + 4 * j;
-                r.w[j] = row < n ? w + (int64_t)row * a.F : nullptr;
-            }
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                const int row = (lane >> 3) + 4 * j;
-                r.x[j] = r.x[j + 2] = nullptr;
-                if (row < ps.tokens(pass)) {
-                    r.x[j] = a.act + (int64_t)ps.pair(pass, row) * a.F;
-                    r.x[j + 2] = r.x[j] + n_act;
-                }
-            }
-            return r;
-        },
-        [&](int i, int part, const float (&acc)[4]) {
-            const int pass = i / row_tiles, rt = i - pass * row_tiles;
-            const int from = rows * rt / row_tiles, n = rows * (rt + 1) / row_tiles - from;
-            float *to = a.sums + (int64_t)part * pairs * a.H + r0 + from + g;
-#pragma unroll
-            for (int j = 0; j < 2; ++j)
-                if (t2 + j < ps.tokens(pass)) {
-                    float *y = to + (int64_t)ps.pair(pass, t2 + j) * a.H;
-                    if (g < n)
-                        y[0] = acc[j];
-                    if (g + 8 < n)
-                        y[8] = acc[2 + j];
-                }
-        },
-        [&]() {
-            // with the last copies under way: the pairs' weights
-#pragma unroll 1
-            for (int i = threadIdx.x; i < pairs; i += kThreads) {
-                const int e = a.ids[i] - a.first;
-                weight[i] = a.scaling * a.weights[i];
-                if (e < 0 || e >= a.local)
-                    weight[i] = __uint_as_float(kAbsent);
-            }
-        });
-    __syncthreads();
-    for (int i = threadIdx.x; i < a.T * rows; i += kThreads) {
-        const int t = i / rows, r = i - t * rows;
-        const float *y = a.sums + (int64_t)t * kTopK * a.H + r0 + r;
-        float sum = 0.0f;
-        float v[kTopK];
-#pragma unroll
-        for (int k = 0; k < kTopK; ++k) {
-            v[k] = 0.0f;
-            if (__float_as_uint(weight[t * kTopK + k]) != kAbsent)
-                for (int p = 0; p < cut.parts; ++p)
-                    v[k] += y[(int64_t)(p * pairs + k) * a.H];
+            continue;
         }
+        // A block owns some output columns, so it adds up by itself what its warps left for each pair.  (Adding round
+        // by round in shared memory, in order behind barriers, took half of the kernel's instructions: 308 us for 64
+        // tokens of an eighth, 186 this way.)
+#pragma unroll 1
+        for (int i = threadIdx.x; i < pairs; i += kThreads) {
+            const int e = a.ids[i] - a.first;
+            weight[i] = e >= 0 && e < a.local ? a.scaling * a.weights[i] : __uint_as_float(kAbsent);
+        }
+        __syncthreads();
+#pragma unroll 1
+        for (int i = threadIdx.x; i < a.T * rows; i += kThreads) {
+            const int tok = i / rows, r = i - tok * rows;
+            const float *y = a.sums + (int64_t)tok * kTopK * a.H + r0 + r;
+            float v[kTopK], sum = 0.0f;
 #pragma unroll
-        for (int k = 0; k < kTopK; ++k)
-            if (__float_as_uint(weight[t * kTopK + k]) != kAbsent)
-                sum = __fmaf_rn(weight[t * kTopK + k], v[k], sum);
-        a.out[t * a.out_stride + r0 + r] = (uint16_t)pack_bf16x2(sum, 0.0f);
+            for (int k = 0; k < kTopK; ++k) {
+                v[k] = 0.0f;
+                if (__float_as_uint(weight[tok * kTopK + k]) != kAbsent)
+                    for (int p = 0; p < cut.parts; ++p)
+                        v[k] += y[(int64_t)(p * pairs + k) * a.H];
+            }
+#pragma unroll
+            for (int k = 0; k < kTopK; ++k)
+                if (__float_as_uint(weight[tok * kTopK + k]) != kAbsent)
+                    sum = __fmaf_rn(weight[tok * kTopK + k], v[k], sum);
+            a.out[tok * a.out_stride + r0 + r] = (uint16_t)pack_bf16x2(sum, 0.0f);
+        }
     }
 }
 
-template <auto Kernel>
-cudaError_t launch_share(const ShareArgs &s, int grid, int smem, cudaStream_t stream)
+cudaError_t launch_share(const ShareArgs &s, int grid, cudaStream_t stream)
 {
-    static int done[64] = {};  // the most shared memory that was asked for
+    constexpr int smem = kWarps * kStages * kStageBytes + kAreaBytes;
+    static bool done[64] = {};
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
-    if (e == cudaSuccess && (dev >= 64 || done[dev] < smem)) {
-        e = cudaFuncSetAttribute(Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e == cudaSuccess && (dev >= 64 || !done[dev])) {
+        e = cudaFuncSetAttribute(moe_share_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
         if (e == cudaSuccess && dev < 64)
-            done[dev] = smem;
+            done[dev] = true;
     }
     return e == cudaSuccess
-               ? launch_pdl(Kernel, dim3((unsigned)grid), dim3(kThreads), (size_t)smem, stream, s)
+               ? launch_pdl(moe_share_kernel, dim3((unsigned)grid), dim3(kThreads), smem, stream, s)
                : e;
 }
 
@@ -758,16 +789,16 @@ cudaError_t launch_moe_layer(const MoeArgs &a, const MoePlan &p, cudaStream_t st
         r.T = a.T;
         e = launch_grouped_topk(r, stream);
     }
-    // both kernels have a block an SM: a block of the second finds its first weights in the L2 cache
-    const int down = a.H < kSms ? a.H : kSms;
     if (e == cudaSuccess) {
         s.cut = make_cut(a.H);
-        e = launch_share<moe_up_kernel>(s, kSms, kWarps * kUpStages * stage_bytes(8) + kAreaBytes, stream);
+        e = launch_share(s, kSms, stream);
     }
     if (e == cudaSuccess) {
         s.cut = make_cut(a.F);
         s.cut.parts = 1;
-        e = launch_share<moe_down_kernel>(s, down, kWarps * kDownStages * stage_bytes(16), stream);
+        s.down = true;
+        // a block an SM, as above: a block finds its first weights in the L2 cache
+        e = launch_share(s, a.H < kSms ? a.H : kSms, stream);
     }
     return e != cudaSuccess ? e : cudaGetLastError();
 }
