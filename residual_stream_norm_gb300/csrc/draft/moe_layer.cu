@@ -34,7 +34,7 @@ constexpr int kPassTokens = 8;
 constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
 constexpr int kFusedTokens = 16;   // tokens that the up kernel routes itself
-constexpr int kCols = 64;          // columns of a stage: 128 bytes of a row
+constexpr int kCols = 128;         // columns of a stage
 constexpr int kSumRows = 512;      // least rows of the down kernel's sums
 
 // ---------------------------------------------------------------------------------------------
@@ -182,6 +182,10 @@ __global__ void __launch_bounds__(kThreads, 2)
 // passes: an expert of this rank with up to 8 of its pairs
 // ---------------------------------------------------------------------------------------------
 
+// For down a pass has up to 4 tokens, whose activations' two BF16 parts fill the 8 columns of its products.
+constexpr int kDownTokens = 4;
+constexpr int kMaxDownPasses = kExperts + 2 * kMaxTokens;  // sum over experts of ceil(pairs / 4)
+
 struct Passes {
     int count;
     int info[kMaxPasses];                   // expert, and the number of its tokens times 2^16
@@ -203,9 +207,41 @@ struct PassScratch {
     int32_t pass_of[kFusedTokens * kTopK];
 };
 
-__host__ __device__ constexpr int most_passes(int T)
+struct DownPasses {
+    int count;
+    int info[kMaxDownPasses];               // expert, and the number of its tokens times 2^16
+    uint2 pairs[kMaxDownPasses];            // 4 16-bit numbers
+};
+
+__host__ __device__ constexpr int most_down_passes(int T)
 {
-    return T * kTopK < kExperts + T ? T * kTopK : kExperts + T;
+    return T * kTopK < kExperts + 2 * T ? T * kTopK : kExperts + 2 * T;
+}
+
+// Passes of up to 8 tokens as passes of up to 4, by one warp.
+__device__ __forceinline__ void split_passes(DownPasses &to, const Passes &ps, int lane)
+{
+    int at = 0;
+#pragma unroll 1
+    for (int p0 = 0; p0 < ps.count; p0 += 32) {
+        const int p = p0 + lane;
+        const bool on = p < ps.count;
+        const int tokens = on ? ps.tokens(p) : 0;
+        const uint32_t two = __ballot_sync(0xffffffffu, tokens > kDownTokens), below = (1u << lane) - 1u;
+        if (on) {
+            const int i = at + lane + __popc(two & below);
+            const uint4 pairs = ps.pairs[p];
+            to.info[i] = ps.expert(p) | min(tokens, kDownTokens) << 16;
+            to.pairs[i] = make_uint2(pairs.x, pairs.y);
+            if (tokens > kDownTokens) {
+                to.info[i + 1] = ps.expert(p) | (tokens - kDownTokens) << 16;
+                to.pairs[i + 1] = make_uint2(pairs.z, pairs.w);
+            }
+        }
+        at += min(ps.count - p0, 32) + __popc(two);
+    }
+    if (lane == 0)
+        to.count = at;
 }
 
 // Passes of up to 128 pairs, whose experts stand in ps.ids, by pair: which earlier pairs have the same expert.
@@ -327,8 +363,9 @@ __device__ __forceinline__ void build_passes(Passes &list, PassScratch &ps, cons
 // finds most of it there
 // ---------------------------------------------------------------------------------------------
 
-constexpr int kStages = 6;
-constexpr int kStageBytes = (16 + 16) * 128;   // 16 rows of weights; 8 tokens, in two parts for down
+constexpr int kStages = 4;
+constexpr int kRowBytes = kCols * 2;
+constexpr int kStageBytes = (16 + 8) * kRowBytes;  // 16 rows of weights and 8 of tokens
 constexpr int kAreaBytes = 2 * kWarps * 128 * 4;
 constexpr uint32_t kAbsent = 0xffffffffu;  // a weight (a NaN that no product gives): the expert is not here
 
@@ -336,7 +373,7 @@ constexpr uint32_t kAbsent = 0xffffffffu;  // a weight (a NaN that no product gi
 // 2r + 1, take different halves of the 128 bytes that a row has.
 __device__ __forceinline__ uint32_t swizzled(int row, int c)
 {
-    return (uint32_t)(row * 128 + ((c ^ (((row & 1) << 2) | ((row >> 1) & 3))) << 4));
+    return (uint32_t)(row * kRowBytes + ((c ^ (((row & 1) << 2) | ((row >> 1) & 3))) << 4));
 }
 
 // How a block's tiles are shared out: `parts` warps take a part of a tile's columns each.
@@ -349,7 +386,7 @@ Cut make_cut(int K)
     Cut c;
     c.K = K;
     c.steps = (K + kCols - 1) / kCols;
-    c.parts = c.steps >= 32 ? 8 : (c.steps >= 16 ? 4 : (c.steps >= 8 ? 2 : 1));
+    c.parts = c.steps >= 16 ? 8 : (c.steps >= 8 ? 4 : (c.steps >= 4 ? 2 : 1));
     return c;
 }
 
@@ -363,7 +400,7 @@ struct ShareArgs {
     const float *logits, *bias;
     int32_t *ids;
     float *weights;
-    Passes *passes;
+    DownPasses *passes;
     float *sums;               // [sum_rows][H]: a pair's share of the output, by part and pair
     int32_t sum_rows;
     int32_t first, local, T, H, F;
@@ -427,8 +464,17 @@ struct Tiles {
 __global__ void __launch_bounds__(kThreads, 2) moe_share_kernel(const ShareArgs a)
 {
     extern __shared__ __align__(128) char smem[];
-    __shared__ Passes ps;
     __shared__ PassScratch scratch;
+    __shared__ __align__(16) char lists[sizeof(Passes)];
+    static_assert(sizeof(DownPasses) <= sizeof(Passes), "one place for either list");
+    Passes &ps = *reinterpret_cast<Passes *>(lists);
+    DownPasses &ds = *reinterpret_cast<DownPasses *>(lists);
+    // the list at hand: count, info, and the pairs of pass p, token j
+    const int &passes = a.down ? ds.count : ps.count;
+    const int *info = a.down ? ds.info : ps.info;
+    const int16_t *pair_of = a.down ? reinterpret_cast<const int16_t *>(ds.pairs)
+                                    : reinterpret_cast<const int16_t *>(ps.pairs);
+    const int per_pass = a.down ? kDownTokens : kPassTokens;
     float *area = reinterpret_cast<float *>(smem + kWarps * kStages * kStageBytes);
     float *weight = area;  // down: a pair's weight times the scaling, or kAbsent
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
@@ -444,14 +490,19 @@ __global__ void __launch_bounds__(kThreads, 2) moe_share_kernel(const ShareArgs 
             pdl_wait();
         // ---- routing and passes --------------------------------------------------------------------------
         if (a.down) {
-            const int most = most_passes(a.T);
+            const int most = most_down_passes(a.T);
 #pragma unroll 1
             for (int i = threadIdx.x; i < most; i += kThreads) {
-                ps.info[i] = a.passes->info[i];
-                ps.pairs[i] = ld_plain(&a.passes->pairs[i]);
+                ds.info[i] = a.passes->info[i];
+                ds.pairs[i] = a.passes->pairs[i];
             }
             if (threadIdx.x == 0)
-                ps.count = a.passes->count;
+                ds.count = a.passes->count;
+#pragma unroll 1
+            for (int i = threadIdx.x; i < pairs; i += kThreads) {
+                const int e = a.ids[i] - a.first;
+                weight[i] = e >= 0 && e < a.local ? a.scaling * a.weights[i] : __uint_as_float(kAbsent);
+            }
             __syncthreads();
         } else if (fused) {
 #pragma unroll 1
@@ -474,15 +525,8 @@ __global__ void __launch_bounds__(kThreads, 2) moe_share_kernel(const ShareArgs 
         } else {
             build_passes(ps, scratch, a.ids, dry ? 0 : a.T, a.first, a.local);
         }
-        if (!dry && !a.down && blockIdx.x == 0) {  // for the down kernel
-#pragma unroll 1
-            for (int i = threadIdx.x; i < ps.count; i += kThreads) {
-                a.passes->info[i] = ps.info[i];
-                a.passes->pairs[i] = ps.pairs[i];
-            }
-            if (threadIdx.x == 0)
-                a.passes->count = ps.count;
-        }
+        if (!dry && !a.down && blockIdx.x == 0 && warp == kWarps - 1)
+            split_passes(*a.passes, ps, lane);
         // ---- the block's tiles ------------------------------------------------------------------------------
         Cut cut = a.cut;
         Tiles ld;
@@ -497,14 +541,14 @@ __global__ void __launch_bounds__(kThreads, 2) moe_share_kernel(const ShareArgs 
             ld.pass = -1;
             ld.start = r0;
             ld.run = Run(rows, ld.tiles);
-            count = ld.tiles * ps.count;
+            count = ld.tiles * passes;
             // few tiles: parts of their columns, so that each warp has some, while there is room for the parts' sums
-            while (cut.parts < kWarps && count * cut.parts < 3 * kWarps && cut.steps >= 4 * cut.parts &&
+            while (cut.parts < kWarps && count * cut.parts < 3 * kWarps && cut.steps >= 2 * cut.parts &&
                    2 * cut.parts * pairs <= a.sum_rows)
                 cut.parts *= 2;
         } else {
             // block 0, which also finishes the routing of few tokens, takes half a share then
-            const uint64_t places = (uint64_t)(ps.count * a.F);
+            const uint64_t places = (uint64_t)(passes * a.F);
             const uint32_t b = 2 * blockIdx.x;
             constexpr uint32_t kWhole = 2 * kSms;  // the grid's blocks, in halves
             ld.at = (uint32_t)(fused ? places * (b > 0 ? b - 1 : 0) / (kWhole - 1) : places * b / kWhole);
@@ -530,8 +574,7 @@ __global__ void __launch_bounds__(kThreads, 2) moe_share_kernel(const ShareArgs 
         const int chunk = lane & 7, row = lane >> 3;
         const int64_t n_act = (int64_t)pairs * a.F;
 
-        const uint16_t *w[4], *x[4];  // rows lane / 8 + 4 i of the weights, and of the tokens (down: i >= 2 their
-                                      // second parts); nullptr: none
+        const uint16_t *w[4], *x[2];  // rows lane / 8 + 4 i of the weights and of the tokens; nullptr: none
         int step = 0, left = mine * steps, put = 0, by = first + 1;
         auto open_tile = [&]() {
             ld.go(a, by);
@@ -539,7 +582,8 @@ __global__ void __launch_bounds__(kThreads, 2) moe_share_kernel(const ShareArgs 
             // past the last column nothing is read, and zeros take its place; rows that are not there are not
             // copied: what stands in their places reaches only their own sums, which nobody takes
             const int k = s0 * kCols + chunk * 8 < cut.K ? s0 * kCols + chunk * 8 : 0;
-            const int e = ps.info[ld.pass] & 0xffff, tokens = dry ? 0 : ps.tokens(ld.pass), n = dry ? 0 : ld.n;
+            const int what = info[ld.pass], e = what & 0xffff;
+            const int tokens = dry ? 0 : what >> 16, n = dry ? 0 : ld.n;
             const int64_t pitch = a.down ? a.F : a.H;
             const uint16_t *from =
                 (a.down ? a.w2 + ((int64_t)e * a.H + ld.from) * a.F
@@ -551,14 +595,13 @@ __global__ void __launch_bounds__(kThreads, 2) moe_share_kernel(const ShareArgs 
                 w[i] = (a.down ? r : r & 7) < n ? from + at * pitch : nullptr;
             }
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const int r = row + 4 * i;
-                x[i] = x[i + 2] = nullptr;
-                if (r < tokens) {
-                    const int pair = ps.pair(ld.pass, r);
-                    x[i] = (a.down ? a.act + (int64_t)pair * a.F : a.x + (pair / kTopK) * a.x_stride) + k;
-                    if (a.down)
-                        x[i + 2] = x[i] + n_act;
+            for (int i = 0; i < 2; ++i) {  // up: tokens 0-3, 4-7; down: the first and second parts of tokens 0-3
+                const int j = row + (a.down ? 0 : 4 * i);
+                x[i] = nullptr;
+                if (j < tokens) {
+                    const int pair = pair_of[ld.pass * per_pass + j];
+                    x[i] = (a.down ? a.act + i * n_act + (int64_t)pair * a.F
+                                   : a.x + (pair / kTopK) * a.x_stride) + k;
                 }
             }
         };
@@ -567,16 +610,23 @@ __global__ void __launch_bounds__(kThreads, 2) moe_share_kernel(const ShareArgs 
                 if (step == 0)
                     open_tile();
                 const uint32_t to = base + put * kStageBytes;
-                const bool in = (s0 + step) * kCols + chunk * 8 < cut.K;
-                const int64_t off = in ? step * kCols : 0;
-                const uint32_t bytes = in ? 16u : 0u;
+                // the two halves of the stage's columns
+                const int k = (s0 + step) * kCols + chunk * 8;
+                const int64_t off = k < cut.K ? step * kCols : 0;
+                const int64_t off2 = k + 64 < cut.K ? step * kCols + 64 : 0;
+                const uint32_t n1 = k < cut.K ? 16u : 0u, n2 = k + 64 < cut.K ? 16u : 0u;
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    if (w[i])
-                        cp_async16(to + swizzled(i * 4 + row, chunk), w[i] + off, bytes);
-                    if (x[i])
-                        cp_async16(to + 2048 + swizzled(i * 4 + row, chunk), x[i] + off, bytes);
-                }
+                for (int i = 0; i < 4; ++i)
+                    if (w[i]) {
+                        cp_async16(to + swizzled(i * 4 + row, chunk), w[i] + off, n1);
+                        cp_async16(to + swizzled(i * 4 + row, chunk + 8), w[i] + off2, n2);
+                    }
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+                    if (x[i]) {
+                        cp_async16(to + swizzled(16 + i * 4 + row, chunk), x[i] + off, n1);
+                        cp_async16(to + swizzled(16 + i * 4 + row, chunk + 8), x[i] + off2, n2);
+                    }
                 put = put + 1 == kStages ? 0 : put + 1;
                 step = step + 1 == steps ? 0 : step + 1;
                 --left;
@@ -602,17 +652,13 @@ __global__ void __launch_bounds__(kThreads, 2) moe_share_kernel(const ShareArgs 
                     copy_next();
                     const uint32_t from = base + get * kStageBytes;
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
+                    for (int h = 0; h < kCols / 32; ++h) {
                         const uint32_t at = from + swizzled(g, h * 4 + t);
-                        const uint4 lo = lds128(at), hi = lds128(at + 1024), y = lds128(at + 2048);
+                        const uint4 lo = lds128(at), hi = lds128(at + 8 * kRowBytes);
+                        const uint4 y = lds128(at + 16 * kRowBytes);
                         const uint32_t f0[4] = {lo.x, hi.x, lo.y, hi.y}, f1[4] = {lo.z, hi.z, lo.w, hi.w};
                         mma16816<false>(acc, f0, y.x, y.y);
                         mma16816<false>(acc, f1, y.z, y.w);
-                        if (a.down) {
-                            const uint4 y2 = lds128(at + 3072);
-                            mma16816<false>(acc, f0, y2.x, y2.y);
-                            mma16816<false>(acc, f1, y2.z, y2.w);
-                        }
                     }
                     get = get + 1 == kStages ? 0 : get + 1;
                 }
@@ -620,12 +666,15 @@ __global__ void __launch_bounds__(kThreads, 2) moe_share_kernel(const ShareArgs 
             if (a.down) {
                 if (busy) {  // this warp's rows of the pairs' sums
                     cp.go(a, round == 0 ? first + 1 : at_once);
-                    const int tokens = ps.tokens(cp.pass);
+                    const int tokens = info[cp.pass] >> 16;
                     float *to = a.sums + (int64_t)part * pairs * a.H + cp.from + g;
 #pragma unroll
+                    for (int i = 0; i < 4; ++i)  // both parts' products
+                        acc[i] += __shfl_xor_sync(0xffffffffu, acc[i], 2);
+#pragma unroll
                     for (int j = 0; j < 2; ++j)
-                        if (2 * t + j < tokens) {
-                            float *y = to + (int64_t)ps.pair(cp.pass, 2 * t + j) * a.H;
+                        if (t < 2 && 2 * t + j < tokens) {
+                            float *y = to + (int64_t)pair_of[cp.pass * kDownTokens + 2 * t + j] * a.H;
                             if (g < cp.n)
                                 y[0] = acc[j];
                             if (g + 8 < cp.n)
@@ -694,28 +743,26 @@ __global__ void __launch_bounds__(kThreads, 2) moe_share_kernel(const ShareArgs 
         // A block owns some output columns, so it adds up by itself what its warps left for each pair.  (Adding round
         // by round in shared memory, in order behind barriers, took half of the kernel's instructions: 308 us for 64
         // tokens of an eighth, 186 this way.)
-#pragma unroll 1
-        for (int i = threadIdx.x; i < pairs; i += kThreads) {
-            const int e = a.ids[i] - a.first;
-            weight[i] = e >= 0 && e < a.local ? a.scaling * a.weights[i] : __uint_as_float(kAbsent);
-        }
-        __syncthreads();
-#pragma unroll 1
+#pragma unroll 2
         for (int i = threadIdx.x; i < a.T * rows; i += kThreads) {
             const int tok = i / rows, r = i - tok * rows;
             const float *y = a.sums + (int64_t)tok * kTopK * a.H + r0 + r;
-            float v[kTopK], sum = 0.0f;
+            float v[kTopK], c[kTopK], sum = 0.0f;
 #pragma unroll
             for (int k = 0; k < kTopK; ++k) {
                 v[k] = 0.0f;
-                if (__float_as_uint(weight[tok * kTopK + k]) != kAbsent)
-                    for (int p = 0; p < cut.parts; ++p)
-                        v[k] += y[(int64_t)(p * pairs + k) * a.H];
+                c[k] = weight[tok * kTopK + k];
             }
+#pragma unroll 1
+            for (int p = 0; p < cut.parts; ++p)  // eight loads at a time
+#pragma unroll
+                for (int k = 0; k < kTopK; ++k)
+                    if (__float_as_uint(c[k]) != kAbsent)
+                        v[k] += y[(int64_t)(p * pairs + k) * a.H];
 #pragma unroll
             for (int k = 0; k < kTopK; ++k)
-                if (__float_as_uint(weight[tok * kTopK + k]) != kAbsent)
-                    sum = __fmaf_rn(weight[tok * kTopK + k], v[k], sum);
+                if (__float_as_uint(c[k]) != kAbsent)
+                    sum = __fmaf_rn(c[k], v[k], sum);
             a.out[tok * a.out_stride + r0 + r] = (uint16_t)pack_bf16x2(sum, 0.0f);
         }
     }
@@ -746,7 +793,7 @@ MoePlan moe_plan(int64_t T, int32_t H, int32_t F)
     p.ids = T * kExperts * 4;
     p.weights = p.ids + T * kTopK * 4;
     p.passes = p.weights + T * kTopK * 4;
-    p.act = p.passes + (int64_t)sizeof(Passes);
+    p.act = p.passes + (int64_t)(sizeof(DownPasses) + 15) / 16 * 16;
     p.sums = p.act + 2 * T * kTopK * F * 2;
     p.sum_rows = T * kTopK > kSumRows ? T * kTopK : kSumRows;
     p.bytes = p.sums + p.sum_rows * H * 4;
@@ -768,7 +815,7 @@ cudaError_t launch_moe_layer(const MoeArgs &a, const MoePlan &p, cudaStream_t st
     s.bias = a.router_bias;
     s.ids = a.ids ? a.ids : (int32_t *)(a.workspace + p.ids);
     s.weights = a.weights ? a.weights : (float *)(a.workspace + p.weights);
-    s.passes = (Passes *)(a.workspace + p.passes);
+    s.passes = (DownPasses *)(a.workspace + p.passes);
     s.sums = (float *)(a.workspace + p.sums);
     s.sum_rows = (int32_t)p.sum_rows;
     s.first = a.first;
