@@ -6,7 +6,8 @@
 //  2. the grouped top-k of beam_grouped_topk_fwd: for up to 16 tokens in every block of the next kernel, two
 //     tokens a warp at most, else as that kernel;
 //  3. up: g, u and a = silu(g) u for each (token, expert) pair;
-//  4. down: each block owns some of the H output columns and adds up all experts' shares of them.
+//  4. down: each pair's share of the output, in FP32;
+//  5. the weighted sum of each token's pairs.
 //
 // Kernels 3 and 4 give each of a block's eight warps a stream of its own: 16 rows of weights by 64 columns at a
 // time, copied with cp.async some stages ahead into the warp's part of shared memory together with the tokens'
@@ -367,7 +368,6 @@ constexpr int kStages = 4;
 constexpr int kRowBytes = kCols * 2;
 constexpr int kStageBytes = (16 + 8) * kRowBytes;  // 16 rows of weights and 8 of tokens
 constexpr int kAreaBytes = 2 * kWarps * 128 * 4;
-constexpr uint32_t kAbsent = 0xffffffffu;  // a weight (a NaN that no product gives): the expert is not here
 
 // Where the 16 bytes `c` of row `row` of a stage stand: rows that eight neighbouring threads read together, 2r and
 // 2r + 1, take different halves of the 128 bytes that a row has.
@@ -409,54 +409,59 @@ struct ShareArgs {
     Cut cut;
 };
 
-// The block's rows of the down projection: [from, to).
-__device__ __forceinline__ void down_rows(const ShareArgs &a, int block, int blocks, int &from, int &to)
+// What is cut: up, the F places of each pass, in tiles of up to 8 (two rows of weights each); down, the H rows of each
+// pass, in tiles of up to 16.
+__device__ __forceinline__ uint32_t unit_of(const ShareArgs &a) { return (uint32_t)(a.down ? a.H : a.F); }
+__device__ __forceinline__ int tile_shift(const ShareArgs &a) { return a.down ? 4 : 3; }
+
+// Parts of a tile's columns for the down kernel: where blocks have few tiles, each warp gets some, while there is room
+// for the parts' sums.
+__device__ __forceinline__ int down_parts(const ShareArgs &a, int passes)
 {
-    from = (int)((uint32_t)a.H * block / blocks);
-    to = (int)((uint32_t)a.H * (block + 1) / blocks);
+    const uint32_t tiles = ((uint32_t)passes * a.H + kSms * 16 - 1) / (kSms * 16);  // of a block
+    int parts = 1;
+    while (parts < kWarps && tiles * parts < 3 * kWarps && a.cut.steps >= 2 * parts &&
+           2 * parts * a.T * kTopK <= a.sum_rows)
+        parts *= 2;
+    return parts;
 }
 
-// A run cut evenly into tiles, so that none is much smaller than the others.
-struct Run {
-    int base, more;
-    __device__ __forceinline__ Run(int n, int tiles) : base(n / tiles), more(n - n / tiles * tiles) {}
-    __device__ __forceinline__ int from(int i) const { return i * base + min(i, more); }
-    __device__ __forceinline__ int size(int i) const { return base + (i < more ? 1 : 0); }
-};
-
-// Tiles of the block, walked in order.
-//  up:   its share [at, end) of the places (of F) of all passes: runs inside a pass, in tiles of up to 8 places
-//  down: its rows in tiles of up to 16, for all passes
+// The tiles of a block's share [at, end) of all passes' places (rows), in order: runs inside a pass, each cut evenly, so
+// that no tile is much smaller than the others.  A share is one stretch of memory but where it passes from expert to
+// expert.
 struct Tiles {
-    int pass, from, n;  // the tile at hand: its pass, first place or row, and their number
+    int pass, from, n;  // the tile at hand: its pass, first place, and their number
     int i, tiles;       // its number in the run, the run's tiles
-    uint32_t at, end;   // up: behind the run, behind all
-    int start;          // first place or row of the run
-    Run run{0, 1};
+    uint32_t at, end;   // behind the run, behind all
+    int start;          // first place of the run
+    int base, more;     // tiles have base places, the first `more` of them one more
 
-    __device__ __forceinline__ void open_run(const ShareArgs &a)
+    __device__ __forceinline__ void open_run(uint32_t unit, int shift)
     {
-        if (a.down) {
-            ++pass;
-        } else {
-            pass = (int)(at / (uint32_t)a.F);
-            start = (int)(at - (uint32_t)pass * a.F);
-            const int size = min((int)(end - at), a.F - start);
-            tiles = (size + 7) >> 3;
-            run = Run(size, tiles);
-            at += size;
-        }
+        pass = (int)(at / unit);
+        start = (int)(at - (uint32_t)pass * unit);
+        const int size = min((int)(end - at), (int)unit - start);
+        tiles = (size + (1 << shift) - 1) >> shift;
+        base = size / tiles;
+        more = size - base * tiles;
+        at += size;
         i = 0;
     }
     // `by` tiles on; in front of the first at the beginning
-    __device__ __forceinline__ void go(const ShareArgs &a, int by)
+    __device__ __forceinline__ void go(uint32_t unit, int shift, int by)
     {
 #pragma unroll 1
         for (; by > 0; --by)
             if (++i >= tiles)
-                open_run(a);
-        from = start + run.from(i);
-        n = run.size(i);
+                open_run(unit, shift);
+        from = start + i * base + min(i, more);
+        n = base + (i < more ? 1 : 0);
+    }
+    __device__ __forceinline__ int count(uint32_t unit, int shift) const
+    {
+        const uint32_t t = (1u << shift) - 1, f0 = at % unit, all = end - at;
+        const uint32_t n0 = min(all, unit - f0), rest = all - n0;  // the first run, and what is behind it
+        return (int)(((n0 + t) >> shift) + rest / unit * ((unit + t) >> shift) + ((rest % unit + t) >> shift));
     }
 };
 
@@ -476,7 +481,6 @@ __global__ void __launch_bounds__(kThreads, 2) moe_share_kernel(const ShareArgs 
                                     : reinterpret_cast<const int16_t *>(ps.pairs);
     const int per_pass = a.down ? kDownTokens : kPassTokens;
     float *area = reinterpret_cast<float *>(smem + kWarps * kStages * kStageBytes);
-    float *weight = area;  // down: a pair's weight times the scaling, or kAbsent
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
     const bool fused = !a.down && a.T <= kFusedTokens;
     const int pairs = a.T * kTopK;
@@ -498,11 +502,6 @@ __global__ void __launch_bounds__(kThreads, 2) moe_share_kernel(const ShareArgs 
             }
             if (threadIdx.x == 0)
                 ds.count = a.passes->count;
-#pragma unroll 1
-            for (int i = threadIdx.x; i < pairs; i += kThreads) {
-                const int e = a.ids[i] - a.first;
-                weight[i] = e >= 0 && e < a.local ? a.scaling * a.weights[i] : __uint_as_float(kAbsent);
-            }
             __syncthreads();
         } else if (fused) {
 #pragma unroll 1
@@ -528,40 +527,27 @@ __global__ void __launch_bounds__(kThreads, 2) moe_share_kernel(const ShareArgs 
         if (!dry && !a.down && blockIdx.x == 0 && warp == kWarps - 1)
             split_passes(*a.passes, ps, lane);
         // ---- the block's tiles ------------------------------------------------------------------------------
+        // block 0 of up, which also finishes the routing of few tokens, takes half a share then
         Cut cut = a.cut;
         Tiles ld;
-        int count, r0 = 0, rows = 0;
-        ld.i = ld.tiles = 0;
-        if (a.down) {
-            int r1;
-            down_rows(a, blockIdx.x, gridDim.x, r0, r1);
-            rows = r1 - r0;
-            ld.tiles = (rows + 15) >> 4;
-            ld.i = ld.tiles - 1;
-            ld.pass = -1;
-            ld.start = r0;
-            ld.run = Run(rows, ld.tiles);
-            count = ld.tiles * passes;
-            // few tiles: parts of their columns, so that each warp has some, while there is room for the parts' sums
-            while (cut.parts < kWarps && count * cut.parts < 3 * kWarps && cut.steps >= 2 * cut.parts &&
-                   2 * cut.parts * pairs <= a.sum_rows)
-                cut.parts *= 2;
-        } else {
-            // block 0, which also finishes the routing of few tokens, takes half a share then
-            const uint64_t places = (uint64_t)(passes * a.F);
+        const uint32_t unit = unit_of(a);
+        const int shift = tile_shift(a);
+        {
+            const uint64_t places = (uint64_t)((uint32_t)passes * unit);
             const uint32_t b = 2 * blockIdx.x;
             constexpr uint32_t kWhole = 2 * kSms;  // the grid's blocks, in halves
             ld.at = (uint32_t)(fused ? places * (b > 0 ? b - 1 : 0) / (kWhole - 1) : places * b / kWhole);
             ld.end = (uint32_t)(fused ? places * (b + 1) / (kWhole - 1) : places * (b + 2) / kWhole);
-            if (dry) {
-                ld.at = 0;
-                ld.end = 1;
-                cut.steps = cut.parts;
-            }
-            const uint32_t f0 = ld.at % (uint32_t)a.F, n = ld.end - ld.at;
-            const uint32_t n0 = min(n, a.F - f0), rest = n - n0;  // the first run, and what is behind it
-            count = (int)((n0 + 7) / 8 + rest / a.F * (((uint32_t)a.F + 7) / 8) + (rest % a.F + 7) / 8);
+            ld.i = ld.tiles = 0;
         }
+        if (a.down)
+            cut.parts = down_parts(a, passes);
+        if (dry) {
+            ld.at = 0;
+            ld.end = 1;
+            cut.steps = cut.parts;
+        }
+        const int count = ld.count(unit, shift);
         Tiles cp = ld;
         // ---- the warps' streams ------------------------------------------------------------------------------
         // Up: `parts` warps take a part of a tile's columns each, and their sums meet behind a barrier, a round of
@@ -577,7 +563,7 @@ __global__ void __launch_bounds__(kThreads, 2) moe_share_kernel(const ShareArgs 
         const uint16_t *w[4], *x[2];  // rows lane / 8 + 4 i of the weights and of the tokens; nullptr: none
         int step = 0, left = mine * steps, put = 0, by = first + 1;
         auto open_tile = [&]() {
-            ld.go(a, by);
+            ld.go(unit, shift, by);
             by = at_once;
             // past the last column nothing is read, and zeros take its place; rows that are not there are not
             // copied: what stands in their places reaches only their own sums, which nobody takes
@@ -665,7 +651,7 @@ __global__ void __launch_bounds__(kThreads, 2) moe_share_kernel(const ShareArgs 
             }
             if (a.down) {
                 if (busy) {  // this warp's rows of the pairs' sums
-                    cp.go(a, round == 0 ? first + 1 : at_once);
+                    cp.go(unit, shift, round == 0 ? first + 1 : at_once);
                     const int tokens = info[cp.pass] >> 16;
                     float *to = a.sums + (int64_t)part * pairs * a.H + cp.from + g;
 #pragma unroll
@@ -688,7 +674,7 @@ __global__ void __launch_bounds__(kThreads, 2) moe_share_kernel(const ShareArgs 
                 __syncthreads();
 #pragma unroll 1
                 for (int k = 0; k < at_once && round * at_once + k < count; ++k) {
-                    cp.go(a, 1);
+                    cp.go(unit, shift, 1);
                     // places run fastest: neighbouring threads write neighbouring values
                     const int r = threadIdx.x & 7, j = (threadIdx.x >> 3) & 7;
                     if (threadIdx.x >> 6 != (k & 3) || r >= cp.n || j >= ps.tokens(cp.pass) || dry)
@@ -711,60 +697,75 @@ __global__ void __launch_bounds__(kThreads, 2) moe_share_kernel(const ShareArgs 
                 // The last weights are on their way.  The first ones that the down kernel's block here reads, up to
                 // 192 KB of them, are brought to the L2 cache while that kernel starts.
                 drained = true;
-                int from, to;
-                down_rows(a, blockIdx.x, gridDim.x, from, to);
-                const uint32_t bytes = (uint32_t)(to - from) * (uint32_t)a.F * 2u;
-#pragma unroll 1
-                for (int p = lane; p < ps.count && bytes > 0 && (p + 1) * (int64_t)bytes <= 192 * 1024; p += 32)
+                const uint32_t at = (uint32_t)((uint64_t)((uint32_t)passes * a.H) * blockIdx.x / kSms);
+                const uint32_t p = at / a.H, r = at - p * a.H;
+                const int64_t rest = (int64_t)(a.H - r) * a.F * 2;  // of the pass
+                const uint32_t bytes = (uint32_t)(rest < 192 * 1024 ? rest : 192 * 1024) / 32 / 16 * 16;
+                if (bytes > 0 && passes > 0)
                     asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(
-                                     a.w2 + ((int64_t)ps.expert(p) * a.H + from) * a.F),
+                                     (const char *)(a.w2 + ((int64_t)ps.expert(p) * a.H + r) * a.F) +
+                                     lane * bytes),
                                  "r"(bytes)
                                  : "memory");
             }
         }
         cp_async_wait<0>();
         __syncthreads();
-        // ---- the ends -------------------------------------------------------------------------------------------
-        if (!a.down) {
-            if (fused && blockIdx.x == 0 && !dry) {
-                // the choice's weights are of use to the down kernel only
+        if (fused && blockIdx.x == 0 && !dry) {
+            // the choice's weights are of use to the last kernel only
 #pragma unroll 1
-                for (int tok = warp; tok < a.T; tok += kWarps) {
-                    const int id = lane < kTopK ? scratch.ids[tok * kTopK + lane] : 0;
-                    const float v = route_weight(lane < kTopK ? a.logits[tok * kExperts + id] : 0.0f);
-                    if (lane < kTopK) {
-                        a.ids[tok * kTopK + lane] = id;
-                        a.weights[tok * kTopK + lane] = v;
-                    }
+            for (int tok = warp; tok < a.T; tok += kWarps) {
+                const int id = lane < kTopK ? scratch.ids[tok * kTopK + lane] : 0;
+                const float v = route_weight(lane < kTopK ? a.logits[tok * kExperts + id] : 0.0f);
+                if (lane < kTopK) {
+                    a.ids[tok * kTopK + lane] = id;
+                    a.weights[tok * kTopK + lane] = v;
                 }
             }
-            continue;
         }
-        // A block owns some output columns, so it adds up by itself what its warps left for each pair.  (Adding round
-        // by round in shared memory, in order behind barriers, took half of the kernel's instructions: 308 us for 64
-        // tokens of an eighth, 186 this way.)
-#pragma unroll 2
-        for (int i = threadIdx.x; i < a.T * rows; i += kThreads) {
-            const int tok = i / rows, r = i - tok * rows;
-            const float *y = a.sums + (int64_t)tok * kTopK * a.H + r0 + r;
-            float v[kTopK], c[kTopK], sum = 0.0f;
+    }
+}
+
+// out = sum over a token's pairs of scaling * weight * its share, in the order of k.  A thread takes four columns.
+__global__ void __launch_bounds__(kThreads) moe_sum_kernel(const ShareArgs a)
+{
+    pdl_launch_dependents();
+    pdl_wait();
+    const int parts = down_parts(a, a.passes->count), pairs = a.T * kTopK, quads = a.H / 4;
+    for (int i = blockIdx.x * kThreads + threadIdx.x; i < a.T * quads; i += gridDim.x * kThreads) {
+        const int tok = i / quads, col = (i - tok * quads) * 4;
+        float c[kTopK];
+        bool here[kTopK];
 #pragma unroll
-            for (int k = 0; k < kTopK; ++k) {
-                v[k] = 0.0f;
-                c[k] = weight[tok * kTopK + k];
-            }
+        for (int k = 0; k < kTopK; ++k) {
+            const int e = a.ids[tok * kTopK + k] - a.first;
+            here[k] = e >= 0 && e < a.local;
+            c[k] = a.scaling * a.weights[tok * kTopK + k];
+        }
+        float4 v[kTopK];
+#pragma unroll
+        for (int k = 0; k < kTopK; ++k)
+            v[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll 1
-            for (int p = 0; p < cut.parts; ++p)  // eight loads at a time
-#pragma unroll
-                for (int k = 0; k < kTopK; ++k)
-                    if (__float_as_uint(c[k]) != kAbsent)
-                        v[k] += y[(int64_t)(p * pairs + k) * a.H];
+        for (int p = 0; p < parts; ++p)
 #pragma unroll
             for (int k = 0; k < kTopK; ++k)
-                if (__float_as_uint(c[k]) != kAbsent)
-                    sum = __fmaf_rn(c[k], v[k], sum);
-            a.out[tok * a.out_stride + r0 + r] = (uint16_t)pack_bf16x2(sum, 0.0f);
-        }
+                if (here[k]) {
+                    const float4 y = *reinterpret_cast<const float4 *>(
+                        a.sums + (int64_t)(p * pairs + tok * kTopK + k) * a.H + col);
+                    v[k].x += y.x, v[k].y += y.y, v[k].z += y.z, v[k].w += y.w;
+                }
+        float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+        for (int k = 0; k < kTopK; ++k)
+            if (here[k]) {
+                sum.x = __fmaf_rn(c[k], v[k].x, sum.x);
+                sum.y = __fmaf_rn(c[k], v[k].y, sum.y);
+                sum.z = __fmaf_rn(c[k], v[k].z, sum.z);
+                sum.w = __fmaf_rn(c[k], v[k].w, sum.w);
+            }
+        st_global_v2(a.out + tok * a.out_stride + col, pack_bf16x2(sum.x, sum.y),
+                     pack_bf16x2(sum.z, sum.w));
     }
 }
 
@@ -842,10 +843,13 @@ cudaError_t launch_moe_layer(const MoeArgs &a, const MoePlan &p, cudaStream_t st
     }
     if (e == cudaSuccess) {
         s.cut = make_cut(a.F);
-        s.cut.parts = 1;
         s.down = true;
-        // a block an SM, as above: a block finds its first weights in the L2 cache
-        e = launch_share(s, a.H < kSms ? a.H : kSms, stream);
+        e = launch_share(s, kSms, stream);
+    }
+    if (e == cudaSuccess) {
+        const int64_t blocks = ((int64_t)a.T * (a.H / 4) + kThreads - 1) / kThreads;
+        e = launch_pdl(moe_sum_kernel, dim3((unsigned)(blocks < 8 * kSms ? blocks : 8 * kSms)),
+                       dim3(kThreads), 0, stream, s);
     }
     return e != cudaSuccess ? e : cudaGetLastError();
 }
