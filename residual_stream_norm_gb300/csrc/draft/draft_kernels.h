@@ -53,6 +53,7 @@ struct Kv4AttnPlan {
     int32_t rtiles;    // units of a sequence and KV head
     int32_t teams;     // of n_kv * rtiles warps
     int32_t ctas, warps;  // of a block
+    int32_t gang;      // 0: even shares of all keys; else the warps that take a unit whole
     double most_tiles;  // if every sequence fills its table
     int64_t bytes;     // workspace
 };

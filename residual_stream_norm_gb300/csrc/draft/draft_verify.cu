@@ -99,29 +99,38 @@ __device__ __forceinline__ void unpack(float (&p)[BF16 ? 8 : 4], const uint4 &v)
     }
 }
 
-// Sum of the weights of tokens [v0, v1), one lane's share, but for a spike.  Rows that start on 16 bytes are
-// read 16 bytes a lane (v0 and v1 are multiples of 8, but for the row's end), others token by token.
+// Sum of the weights of tokens [v0, v1), one lane's share, but for a spike.  Rows that stand the same way to 16 bytes
+// (or one row) are read 16 bytes a lane between the first and the last such places, others token by token.
 template <bool BF16, bool Draft>
 __device__ __forceinline__ uint64_t sum_stretch(const Rows &r, int v0, int v1, int lane)
 {
+    constexpr int kSize = BF16 ? 2 : 4, kVec = 16 / kSize;
     uint64_t sum = 0;
     int v = v0;
-    if (((uintptr_t)r.target | (uintptr_t)r.draft) % 16 == 0) {
-        constexpr int kVec = BF16 ? 8 : 4, kAhead = 4;
-        const uint4 *tp = reinterpret_cast<const uint4 *>(r.target);
-        const uint4 *dp = reinterpret_cast<const uint4 *>(r.draft);
-        const int end = v1 / kVec;
+    if (!Draft || ((uintptr_t)r.target - (uintptr_t)r.draft) % 16 == 0) {
+        constexpr int kAhead = 4;
+        const int lead = (int)((16 - ((uintptr_t)r.target + (uintptr_t)v0 * kSize) % 16) % 16) / kSize;
+        const int first = min(v0 + lead, v1), vecs = (v1 - first) / kVec;
+        // in front and behind: less than a vector each, a token a lane
+        const int edge = lane < 16 ? v0 + lane : first + vecs * kVec + lane - 16;
+        if (lane < 16 ? edge < first : edge < v1) {
+            const Units w = weight_of<Draft>(prob<BF16>(r.target, edge),
+                                             Draft ? prob<BF16>(r.draft, edge) : 0.0f);
+            sum += whole(w.hi, w.lo);
+        }
+        const char *tp = (const char *)r.target + (int64_t)first * kSize;
+        const char *dp = (const char *)r.draft + (int64_t)first * kSize;
 #pragma unroll 1
-        for (int i0 = v0 / kVec; i0 < end; i0 += 32 * kAhead) {
+        for (int i0 = 0; i0 < vecs; i0 += 32 * kAhead) {
             uint4 p[kAhead], q[kAhead];
 #pragma unroll
             for (int k = 0; k < kAhead; ++k) {
                 const int i = i0 + k * 32 + lane;
                 p[k] = q[k] = make_uint4(0, 0, 0, 0);
-                if (i < end) {
-                    p[k] = ld_cached(tp + i);
+                if (i < vecs) {
+                    p[k] = ld_cached(tp + i * 16);
                     if (Draft)
-                        q[k] = ld_cached(dp + i);
+                        q[k] = ld_cached(dp + i * 16);
                 }
             }
             int32_t hi = 0, lo = 0;  // of at most 32 tokens: within 32 bits
@@ -139,7 +148,7 @@ __device__ __forceinline__ uint64_t sum_stretch(const Rows &r, int v0, int v1, i
             }
             sum += whole(hi, lo);
         }
-        v = max(v0, end * kVec);  // the row's end
+        return sum;
     }
     constexpr int kAhead = 8;
 #pragma unroll 1

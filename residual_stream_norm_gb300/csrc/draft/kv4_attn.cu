@@ -26,6 +26,7 @@
 
 #include "beam_device.cuh"
 #include "beam_f32x2.cuh"
+#include "beam_tma.cuh"
 #include "decode/decode_mma.cuh"
 #include "draft_kernels.h"
 
@@ -46,10 +47,13 @@ __host__ __device__ constexpr int warps_of(int NT, int NG)
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr int kMinExp = -100;
+constexpr double kGangExtra = 24;  // tiles of 8 rows
 
 struct Sizes {
     int32_t heads, R, rtiles;
     uint32_t team, teams;   // warps of a team: KV heads * rtiles
+    uint32_t gang;          // 0: shares; else the warps that take a unit whole
+    uint32_t crew;          // warps that join a row
     uint32_t per;           // sequences that a thread counts
     float *part_o;          // [teams][team][2][8 * NT][128]
     float *part_ml;         // [teams][team][2][8 * NT][2]
@@ -518,7 +522,7 @@ __device__ __forceinline__ void take_tile(Unit<NT, NG> &u, const Kv4AttnArgs &a,
 // Results of a whole unit, or the part of a cut one.
 template <int NT, int NG>
 __device__ __forceinline__ void end_unit(Unit<NT, NG> &u, const Kv4AttnArgs &a, const Sizes &z,
-                                         const Note &at, bool whole, uint32_t part, int lane)
+                                         const Note &at, bool whole, float *part_o, float *part_ml, int lane)
 {
     const int g = lane >> 2, t = lane & 3;
     const int kv = at.hr / z.rtiles, r0 = (at.hr - kv * z.rtiles) * NT * 8;
@@ -544,7 +548,7 @@ __device__ __forceinline__ void end_unit(Unit<NT, NG> &u, const Kv4AttnArgs &a, 
             const int i = r / z.heads, head = kv * z.heads + r - i * z.heads;
             const int64_t row = (int64_t)at.b * a.q_len + i;
             uint16_t *out = (uint16_t *)a.out + row * a.out_stride + head * 128 + 4 * g;
-            float *po = z.part_o + ((int64_t)part * NT * 8 + in_tile) * 128 + 4 * g;
+            float *po = part_o + in_tile * 128 + 4 * g;
             if (r < z.R) {
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
@@ -561,7 +565,7 @@ __device__ __forceinline__ void end_unit(Unit<NT, NG> &u, const Kv4AttnArgs &a, 
                 }
                 if (g == 0) {
                     if (!whole)
-                        *reinterpret_cast<float2 *>(z.part_ml + ((int64_t)part * NT * 8 + in_tile) * 2) =
+                        *reinterpret_cast<float2 *>(part_ml + in_tile * 2) =
                             make_float2(u.m[nt][e], l);
                     else if (a.lse)
                         a.lse[row * a.n_q + head] =
@@ -572,41 +576,17 @@ __device__ __forceinline__ void end_unit(Unit<NT, NG> &u, const Kv4AttnArgs &a, 
         }
 }
 
-// Tiles [start, end) of all sequences, for KV head and row tile hr, by one warp.
+// One warp's tiles: `todo` of them from the note `ld` on, every `stride`-th.  Shares: the team's `mine`-th one, units one
+// after the other.  A gang (z.gang): some tiles of one unit, left as a part at the warp's own place in shared memory.
 template <int NT, int NG>
-__device__ __forceinline__ void take_share(const Kv4AttnArgs &a, const Sizes &z, uint32_t base,
-                                           const uint32_t *s_before, uint32_t mine, uint32_t hr,
-                                           uint32_t start, uint32_t end, int lane)
+__device__ __forceinline__ void take_tiles(const Kv4AttnArgs &a, const Sizes &z, uint32_t base, char *own,
+                                           Note ld, uint32_t todo, int stride, uint32_t mine, int lane)
 {
     constexpr int kStages = stages_of(NT, NG);
-    const uint32_t qb = base + kStages * stage_bytes(NG);
-    Note ld;
-    {
-        int lo = 0;  // the last thread's run that starts at or before `start`
-#pragma unroll 1
-        for (int step = kScan / 2; step > 0; step /= 2)
-            if (s_before[lo + step] <= start)
-                lo += step;
-        uint32_t cum = s_before[lo];
-#pragma unroll 1
-        for (uint32_t b = (uint32_t)lo * z.per;; ++b) {
-            const Keys k = keys_of(a, b);
-            if (start < cum + (uint32_t)k.tiles()) {
-                ld.b = (int)b;
-                ld.hr = (int)hr;
-                ld.n = k.n;
-                ld.ns = k.ns;
-                ld.skip = k.skip;
-                ld.tiles = k.tiles();
-                ld.tile = (int)(start - cum);
-                break;
-            }
-            cum += (uint32_t)k.tiles();
-        }
-    }
+    const uint32_t qb = base + kStages * stage_bytes(NG), hr = (uint32_t)ld.hr;
     const int kv = (int)hr / z.rtiles;
     // ---- copies --------------------------------------------------------------------------------------
-    uint32_t to_load = end - start;
+    uint32_t to_load = todo;
     int slot, put = 0;
     auto load_slot = [&]() {  // of key `lane` of the tile; -1: not to be seen
         const int v = ld.tile * kTile + lane;
@@ -616,7 +596,8 @@ __device__ __forceinline__ void take_share(const Kv4AttnArgs &a, const Sizes &z,
             slot = s >= 0 && s < a.num_slots ? (int)s : -1;
         }
     };
-    load_slot();
+    if (todo > 0)
+        load_slot();
     // of a slot: the lane's 16 bytes of one of eight rows, and its scales
     const char *src[2], *src_scales[2];
 #pragma unroll
@@ -657,7 +638,8 @@ __device__ __forceinline__ void take_share(const Kv4AttnArgs &a, const Sizes &z,
             }
             put = put + 1 == kStages ? 0 : put + 1;
             if (--to_load > 0) {
-                if (++ld.tile == ld.tiles) {
+                ld.tile += stride;
+                if (ld.tile >= ld.tiles) {
                     ld.tile = 0;
                     Keys k;
                     do
@@ -681,7 +663,7 @@ __device__ __forceinline__ void take_share(const Kv4AttnArgs &a, const Sizes &z,
     bool fresh = true, from_start = false;
     int get = 0;
 #pragma unroll 1
-    for (uint32_t j = start; j < end; ++j) {
+    for (uint32_t j = 0; j < todo; ++j) {
         cp_async_wait<kStages - 2>();
         __syncwarp();
         load_next();
@@ -695,16 +677,37 @@ __device__ __forceinline__ void take_share(const Kv4AttnArgs &a, const Sizes &z,
         }
         take_tile(u, a, z, at, from, qb, lane);
         const bool last = at.tile + 1 == at.tiles;
-        if (last || j + 1 == end) {
+        if (j + 1 == todo || (last && !z.gang)) {
             // the share's first unit leaves its part in place 0, a later one in place 1
-            const bool first_unit = j - start <= (uint32_t)at.tile;
-            end_unit(u, a, z, at, from_start && last, (mine * z.team + hr) * 2 + (first_unit ? 0 : 1), lane);
+            const bool first_unit = j <= (uint32_t)at.tile;
+            const int64_t part = (int64_t)((mine * z.team + hr) * 2 + (first_unit ? 0 : 1)) * NT * 8;
+            float *po = z.gang ? reinterpret_cast<float *>(own) : z.part_o + part * 128;
+            float *pm = z.gang ? reinterpret_cast<float *>(own + NT * 8 * 512) : z.part_ml + part * 2;
+            if (z.gang) {  // the part takes the place of the tiles
+                cp_async_wait<0>();
+                __syncwarp();
+            }
+            end_unit(u, a, z, at, from_start && last && z.gang < 2, po, pm, lane);
             fresh = true;
         }
         get = get + 1 == kStages ? 0 : get + 1;
     }
     cp_async_wait<0>();
     __syncwarp();
+}
+
+// A joined row: row r of sequence b and KV head kv, its lane's four columns of the sum o, reference m, sum l.
+__device__ __forceinline__ void write_row(const Kv4AttnArgs &a, const Sizes &z, int b, int kv, int r, float m,
+                                          float l, const float4 &o, int lane)
+{
+    const int i = r / z.heads, head = kv * z.heads + r - i * z.heads;
+    const int64_t row = (int64_t)b * a.q_len + i;
+    const bool none = l == 0.0f;
+    const float inv = none ? 0.0f : __fdiv_rn(1.0f, l);
+    st_global_v2((uint16_t *)a.out + row * a.out_stride + head * 128 + lane * 4,
+                 pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
+    if (a.lse && lane == 0)
+        a.lse[row * a.n_q + head] = none ? __uint_as_float(0xff800000u) : (m + log2f(l)) * kLn2;
 }
 
 template <int NT, int NG>
@@ -716,74 +719,169 @@ __global__ void __launch_bounds__(warps_of(NT, NG) * 32, 1) kv4_attn_kernel(cons
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     pdl_launch_dependents();
     pdl_wait();
+    const uint32_t warps = blockDim.x / 32;
+    char *own = smem + warp * warp_bytes(NT, NG);
+    const uint32_t base = (uint32_t)__cvta_generic_to_shared(own);
+    if (z.gang) {
+        // ---- units whole: the warps of a gang take every gang-th tile, and join their parts in shared memory ------
+        const uint32_t in_block = warp / z.gang, i = warp - in_block * z.gang;
+        const uint32_t units = (uint32_t)a.B * z.team, gangs = warps / z.gang;
+        auto meet = [&]() {
+            if (z.gang > 1)
+                named_sync(1 + (int)in_block, (int)z.gang * 32);
+            else
+                __syncwarp();
+        };
+#pragma unroll 1
+        for (uint32_t unit = blockIdx.x * gangs + in_block; unit < units; unit += gridDim.x * gangs) {
+            Note ld;
+            ld.b = (int)(unit / z.team);
+            ld.hr = (int)(unit - (uint32_t)ld.b * z.team);
+            const Keys k = keys_of(a, (uint32_t)ld.b);
+            ld.n = k.n;
+            ld.ns = k.ns;
+            ld.skip = k.skip;
+            ld.tiles = k.tiles();
+            ld.tile = (int)i;
+            const uint32_t todo = (uint32_t)ld.tiles > i ? ((uint32_t)ld.tiles - i + z.gang - 1) / z.gang : 0;
+            const bool alone = z.gang == 1 && todo > 0;  // written by end_unit
+            take_tiles<NT, NG>(a, z, base, own, ld, todo, (int)z.gang, 0, lane);
+            if (alone)
+                continue;
+            // a warp without tiles leaves an empty part
+            float *ml = reinterpret_cast<float *>(own + NT * 8 * 512);
+            if (todo == 0)
+                for (int r = lane; r < NT * 8; r += 32)
+                    *reinterpret_cast<float2 *>(ml + r * 2) = make_float2(__uint_as_float(0xff800000u), 0.0f);
+            meet();
+            const int kv = ld.hr / z.rtiles, r0 = (ld.hr - kv * z.rtiles) * NT * 8;
+            const char *first = own - i * warp_bytes(NT, NG);
+#pragma unroll 1
+            for (int r = (int)i; r < NT * 8 && r0 + r < z.R; r += (int)z.gang) {
+                const float ninf = __uint_as_float(0xff800000u);
+                float2 part = make_float2(ninf, 0.0f);
+                if (lane < (int)z.gang)
+                    part = *reinterpret_cast<const float2 *>(first + lane * warp_bytes(NT, NG) + NT * 8 * 512 +
+                                                             r * 8);
+                float m = part.x;
+#pragma unroll
+                for (int off = 16; off > 0; off >>= 1)
+                    m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
+                const float f = part.y == 0.0f ? 0.0f : exp2_fast(part.x - (m == ninf ? 0.0f : m));
+                float l = part.y * f;
+#pragma unroll
+                for (int off = 16; off > 0; off >>= 1)
+                    l += __shfl_xor_sync(0xffffffffu, l, off);
+                float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 1
+                for (int p = 0; p < (int)z.gang; ++p) {
+                    const float fp = __shfl_sync(0xffffffffu, f, p);
+                    if (fp == 0.0f)
+                        continue;
+                    const float4 x = *reinterpret_cast<const float4 *>(first + p * warp_bytes(NT, NG) +
+                                                                       r * 512 + lane * 16);
+                    o.x = __fmaf_rn(x.x, fp, o.x);
+                    o.y = __fmaf_rn(x.y, fp, o.y);
+                    o.z = __fmaf_rn(x.z, fp, o.z);
+                    o.w = __fmaf_rn(x.w, fp, o.w);
+                }
+                write_row(a, z, ld.b, kv, r0 + r, m, l, o, lane);
+            }
+            meet();  // the parts have been read
+        }
+        return;
+    }
+    // ---- even shares of all tiles ------------------------------------------------------------------------
     const uint32_t total = scan_tiles(a, z, s_before, s_warp);
     const uint32_t share = (total + z.teams - 1) / z.teams;
     if (total == 0)
         return;
     const uint32_t active = (total + share - 1) / share;  // teams that have one
     // the teams' warps, as many at a time as there are; few teams are spread over all places
-    const uint32_t warps = blockDim.x / 32;
 #pragma unroll 1
     for (uint32_t v = blockIdx.x * warps + warp; v < z.teams * z.team; v += gridDim.x * warps) {
-        const uint32_t place = v / z.team, hr = v - place * z.team;
+        const uint32_t place = v / z.team;
         const uint32_t mine = (place * active + z.teams - 1) / z.teams;
         if (mine >= active || mine * z.teams / active != place)
             continue;
-        take_share<NT, NG>(a, z, (uint32_t)__cvta_generic_to_shared(smem) +
-                                     warp * warp_bytes(NT, NG),
-                           s_before, mine, hr, mine * share, min((mine + 1) * share, total), lane);
+        const uint32_t start = mine * share;
+        Note ld;
+        int lo = 0;  // the last thread's run that starts at or before `start`
+#pragma unroll 1
+        for (int step = kScan / 2; step > 0; step /= 2)
+            if (s_before[lo + step] <= start)
+                lo += step;
+        uint32_t cum = s_before[lo];
+#pragma unroll 1
+        for (uint32_t b = (uint32_t)lo * z.per;; ++b) {
+            const Keys k = keys_of(a, b);
+            if (start < cum + (uint32_t)k.tiles()) {
+                ld.b = (int)b;
+                ld.hr = (int)(v - place * z.team);
+                ld.n = k.n;
+                ld.ns = k.ns;
+                ld.skip = k.skip;
+                ld.tiles = k.tiles();
+                ld.tile = (int)(start - cum);
+                break;
+            }
+            cum += (uint32_t)k.tiles();
+        }
+        take_tiles<NT, NG>(a, z, base, own, ld, min(share, total - start), 1, mine, lane);
     }
 }
 
-// Rows of units that were cut, from their parts in order; rows of sequences without keys.  A warp takes a row.
+// Rows of units that were cut, from their parts; rows of sequences without keys.  z.crew warps (a power of two, up to the
+// block's 8) take a row: each every crew-th part, in order, and the crew's sums meet in shared memory, in order.
 template <int NT>
 __global__ void __launch_bounds__(kScan)
     kv4_join_kernel(const Kv4AttnArgs a, const Sizes z)
 {
     __shared__ uint32_t s_before[kScan];
     __shared__ uint32_t s_warp[kScan / 32];
+    __shared__ float4 s_o[kScan];
+    __shared__ float2 s_ml[kScan / 32];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const uint32_t crew = z.crew, at_once = kScan / 32 / crew, i_row = warp / crew, i = warp - i_row * crew;
+    const float ninf = __uint_as_float(0xff800000u);
     pdl_launch_dependents();
     pdl_wait();
     const uint32_t total = scan_tiles(a, z, s_before, s_warp);
     const uint32_t share = (total + z.teams - 1) / z.teams;
     const uint32_t rows = (uint32_t)a.B * a.q_len * a.n_q;
 #pragma unroll 1
-    for (uint32_t w = blockIdx.x * (kScan / 32) + warp; w < rows; w += gridDim.x * (kScan / 32)) {
-        const uint32_t row = w / (uint32_t)a.n_q, b = row / (uint32_t)a.q_len;
-        const int head = (int)(w - row * a.n_q), kv = head / z.heads;
+    for (uint32_t w = blockIdx.x * at_once; w < rows; w += gridDim.x * at_once) {
+        const uint32_t me = w + i_row, row = me / (uint32_t)a.n_q, b = row / (uint32_t)a.q_len;
+        const int head = (int)(me - row * a.n_q), kv = head / z.heads;
         const int r = (int)(row - b * a.q_len) * z.heads + head - kv * z.heads;
         const int rt = r / (NT * 8), in_tile = r - rt * NT * 8;
-        const uint32_t tiles = (uint32_t)keys_of(a, b).tiles();
-        uint16_t *out = (uint16_t *)a.out + row * a.out_stride + head * 128 + lane * 4;
-        if (tiles == 0) {
-            st_global_v2(out, 0u, 0u);
-            if (a.lse && lane == 0)
-                a.lse[w] = __uint_as_float(0xff800000u);
-            continue;
-        }
-        const uint32_t run = b / z.per;
-        uint32_t t0 = s_before[run];
+        uint32_t tiles = 0, t0 = 0, w0 = 0, w1 = 0;
+        if (me < rows) {
+            tiles = (uint32_t)keys_of(a, b).tiles();
+            const uint32_t run = b / z.per;
+            t0 = s_before[run];
 #pragma unroll 1
-        for (uint32_t i = run * z.per; i < b; ++i)
-            t0 += (uint32_t)keys_of(a, i).tiles();
-        const uint32_t w0 = t0 / share, w1 = (t0 + tiles - 1) / share;
-        if (w0 == w1)
-            continue;  // written whole
-        // part of share i: its place 0 if the unit is the share's first, which all but share w0 have for sure
-        auto part = [&](uint32_t i) {
-            return (int64_t)((i * z.team + kv * z.rtiles + rt) * 2 + (i * share >= t0 ? 0 : 1)) * NT * 8 +
+            for (uint32_t j = run * z.per; j < b; ++j)
+                t0 += (uint32_t)keys_of(a, j).tiles();
+            if (tiles > 0) {
+                w0 = t0 / share;
+                w1 = (t0 + tiles - 1) / share;
+            }
+        }
+        const bool cut = w0 != w1;  // the others were written whole, or have no keys
+        // part of share n: its place 0 if the unit is the share's first, which all but share w0 have for sure
+        auto part = [&](uint32_t n) {
+            return (int64_t)((n * z.team + kv * z.rtiles + rt) * 2 + (n * share >= t0 ? 0 : 1)) * NT * 8 +
                    in_tile;
         };
-        const float ninf = __uint_as_float(0xff800000u);
         // running maximum over 32 parts at a time
         float m = ninf, l = 0.0f;
         float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll 1
-        for (uint32_t i0 = w0; i0 <= w1; i0 += 32) {
+        for (uint32_t n0 = w0 + i; cut && n0 <= w1; n0 += 32 * crew) {
             float2 ml = make_float2(ninf, 0.0f);
-            if (i0 + lane <= w1)
-                ml = *reinterpret_cast<const float2 *>(z.part_ml + part(i0 + lane) * 2);
+            if (n0 + lane * crew <= w1)
+                ml = *reinterpret_cast<const float2 *>(z.part_ml + part(n0 + lane * crew) * 2);
             float mx = ml.x;
 #pragma unroll
             for (int off = 16; off > 0; off >>= 1)
@@ -797,32 +895,51 @@ __global__ void __launch_bounds__(kScan)
                 lf += __shfl_xor_sync(0xffffffffu, lf, off);
             l = __fmaf_rn(l, alpha, lf);
             o.x *= alpha, o.y *= alpha, o.z *= alpha, o.w *= alpha;
-            const int n = (int)min(w1 - i0 + 1, 32u);
+            const int n = (int)min((w1 - n0) / crew + 1, 32u);
 #pragma unroll 1
             for (int i1 = 0; i1 < n; i1 += 8) {
                 float4 x[8];
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    x[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                    if (i1 + i < n)
-                        x[i] = *reinterpret_cast<const float4 *>(z.part_o + part(i0 + i1 + i) * 128 +
+                for (int j = 0; j < 8; ++j) {
+                    x[j] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                    if (i1 + j < n)
+                        x[j] = *reinterpret_cast<const float4 *>(z.part_o + part(n0 + (i1 + j) * crew) * 128 +
                                                                  lane * 4);
                 }
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const float fi = __shfl_sync(0xffffffffu, f, i1 + i);
-                    o.x = __fmaf_rn(x[i].x, fi, o.x);
-                    o.y = __fmaf_rn(x[i].y, fi, o.y);
-                    o.z = __fmaf_rn(x[i].z, fi, o.z);
-                    o.w = __fmaf_rn(x[i].w, fi, o.w);
+                for (int j = 0; j < 8; ++j) {
+                    const float fj = __shfl_sync(0xffffffffu, f, i1 + j);
+                    o.x = __fmaf_rn(x[j].x, fj, o.x);
+                    o.y = __fmaf_rn(x[j].y, fj, o.y);
+                    o.z = __fmaf_rn(x[j].z, fj, o.z);
+                    o.w = __fmaf_rn(x[j].w, fj, o.w);
                 }
             }
         }
-        const bool none = l == 0.0f;
-        const float inv = none ? 0.0f : __fdiv_rn(1.0f, l);
-        st_global_v2(out, pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
-        if (a.lse && lane == 0)
-            a.lse[w] = none ? ninf : (m + log2f(l)) * kLn2;
+        if (crew > 1) {
+            s_o[threadIdx.x] = o;
+            if (lane == 0)
+                s_ml[warp] = make_float2(m, l);
+            __syncthreads();
+            if (i == 0) {
+#pragma unroll 1
+                for (uint32_t j = 1; j < crew; ++j) {
+                    const float2 ml = s_ml[warp + j];
+                    const float4 x = s_o[threadIdx.x + 32 * j];
+                    const float mn = fmaxf(m, ml.x), ref = mn == ninf ? 0.0f : mn;
+                    const float fa = exp2_fast(m - ref), fb = exp2_fast(ml.x - ref);
+                    m = mn;
+                    l = __fmaf_rn(l, fa, ml.y * fb);
+                    o.x = __fmaf_rn(o.x, fa, x.x * fb);
+                    o.y = __fmaf_rn(o.y, fa, x.y * fb);
+                    o.z = __fmaf_rn(o.z, fa, x.z * fb);
+                    o.w = __fmaf_rn(o.w, fa, x.w * fb);
+                }
+            }
+            __syncthreads();
+        }
+        if (i == 0 && me < rows && (cut || tiles == 0))
+            write_row(a, z, (int)b, kv, r, m, l, o, lane);
     }
 }
 
@@ -838,6 +955,7 @@ cudaError_t launch(Kv4AttnArgs a, const Kv4AttnPlan &p, cudaStream_t stream)
     z.rtiles = p.rtiles;
     z.team = (uint32_t)(a.n_kv * p.rtiles);
     z.teams = (uint32_t)p.teams;
+    z.gang = (uint32_t)p.gang;
     z.per = ((uint32_t)a.B + kScan - 1) / kScan;
     z.part_o = (float *)a.workspace;
     z.part_ml = z.part_o + (int64_t)z.teams * z.team * 2 * NT * 8 * 128;
@@ -854,9 +972,11 @@ cudaError_t launch(Kv4AttnArgs a, const Kv4AttnPlan &p, cudaStream_t stream)
     if (e == cudaSuccess)
         e = launch_pdl(kv4_attn_kernel<NT, NG>, dim3(p.ctas), dim3(p.warps * 32),
                        (size_t)p.warps * warp_bytes(NT, NG), stream, a, z);
-    if (e == cudaSuccess) {
+    if (e == cudaSuccess && p.gang == 0) {
+        // few rows, which may have many parts: a block each
         const int64_t rows = (int64_t)a.B * a.q_len * a.n_q;
-        const int64_t blocks = (rows + kScan / 32 - 1) / (kScan / 32);
+        z.crew = rows <= 4 * kSms ? 8 : (rows <= 16 * kSms ? 2 : 1);
+        const int64_t at_once = kScan / 32 / z.crew, blocks = (rows + at_once - 1) / at_once;
         e = launch_pdl(kv4_join_kernel<NT>, dim3((unsigned)(blocks < kSms * 8 ? blocks : kSms * 8)),
                        dim3(kScan), 0, stream, a, z);
     }
@@ -899,6 +1019,25 @@ Kv4AttnPlan kv4_attn_plan(int32_t B, int32_t q_len, int32_t n_q, int32_t n_kv, i
     p.ctas = (int32_t)((all + p.warps - 1) / p.warps);
     p.ctas = p.ctas < kSms ? p.ctas : kSms;
     p.bytes = all * 2 * p.nt * 8 * (128 + 2) * 4;
+    // Units whole, by gangs of up to 16 warps that join in shared memory: that saves the second kernel.  An SM takes some
+    // 0.15 us a tile and 8 rows, so a few tiles more than its even share make up for it.  Measured, whole and shares:
+    // one sequence of 500 keys 8.9 and 10.3 us, of 1000 11.4 and 10.1; 8 of 1000 11.7 and 12.4, of 4000 25.4 and 22.8;
+    // 64 of up to 3000 64.7 and 43.5; 128 behind a window of 512 34.0 and 38.3.
+    const double units = (double)B * team;
+    const int32_t gang_warps = warps_of(p.nt, 128 / group) == 16 ? 16 : 8;
+    const int64_t unit_tiles = (most + kTile - 1) / kTile;
+    int32_t gang = gang_warps;
+    while (gang > 1 && units * gang > (double)kSms * gang_warps)
+        gang /= 2;
+    const double even = units * (double)unit_tiles / kSms;
+    const double whole = (double)unit_tiles * (double)(int64_t)((units + kSms - 1) / kSms);
+    if (units < 1.0e9 && (whole - even) * p.nt <= kGangExtra) {
+        p.gang = gang;
+        p.warps = gang_warps;
+        const double blocks = units * gang / gang_warps;
+        p.ctas = blocks < (double)kSms * 64 ? (int32_t)(blocks + 0.999) : kSms * 64;
+        p.ctas = p.ctas < 1 ? 1 : p.ctas;
+    }
     return p;
 }
 

@@ -726,33 +726,35 @@ __global__ void __launch_bounds__(kThreads, 2) moe_share_kernel(const ShareArgs 
     }
 }
 
-// out = sum over a token's pairs of scaling * weight * its share, in the order of k.  A thread takes four columns.
+// out = sum over a token's pairs of scaling * weight * its share, in the order of k.  A thread takes four columns.  Its
+// loads do not wait for one another: shares of pairs that are not here are read too (what the workspace holds there)
+// and not taken.
 __global__ void __launch_bounds__(kThreads) moe_sum_kernel(const ShareArgs a)
 {
+    const int pairs = a.T * kTopK, quads = a.H / 4;
     pdl_launch_dependents();
     pdl_wait();
-    const int parts = down_parts(a, a.passes->count), pairs = a.T * kTopK, quads = a.H / 4;
     for (int i = blockIdx.x * kThreads + threadIdx.x; i < a.T * quads; i += gridDim.x * kThreads) {
         const int tok = i / quads, col = (i - tok * quads) * 4;
+        float4 v[kTopK];
         float c[kTopK];
         bool here[kTopK];
+        const int passes = a.passes->count;
 #pragma unroll
         for (int k = 0; k < kTopK; ++k) {
+            v[k] = *reinterpret_cast<const float4 *>(a.sums + ((int64_t)tok * kTopK + k) * a.H + col);
             const int e = a.ids[tok * kTopK + k] - a.first;
             here[k] = e >= 0 && e < a.local;
             c[k] = a.scaling * a.weights[tok * kTopK + k];
         }
-        float4 v[kTopK];
-#pragma unroll
-        for (int k = 0; k < kTopK; ++k)
-            v[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        const int parts = down_parts(a, passes);
 #pragma unroll 1
-        for (int p = 0; p < parts; ++p)
+        for (int p = 1; p < parts; ++p)
 #pragma unroll
             for (int k = 0; k < kTopK; ++k)
                 if (here[k]) {
                     const float4 y = *reinterpret_cast<const float4 *>(
-                        a.sums + (int64_t)(p * pairs + tok * kTopK + k) * a.H + col);
+                        a.sums + ((int64_t)p * pairs + tok * kTopK + k) * a.H + col);
                     v[k].x += y.x, v[k].y += y.y, v[k].z += y.z, v[k].w += y.w;
                 }
         float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
