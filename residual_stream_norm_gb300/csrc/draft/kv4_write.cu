@@ -7,6 +7,7 @@
 // once, and codes are rounded and packed with FP32 additions and fused multiply-adds.
 
 #include "beam_device.cuh"
+#include "beam_f32x2.cuh"
 #include "draft_kernels.h"
 
 namespace beam {
@@ -14,7 +15,6 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kHalves = kThreads / 16;
-constexpr int kAhead = 4;  // rows that a half-warp has in hand at a time
 
 __device__ __forceinline__ uint32_t min_nan_bf16x2(uint32_t a, uint32_t b)
 {
@@ -23,19 +23,34 @@ __device__ __forceinline__ uint32_t min_nan_bf16x2(uint32_t a, uint32_t b)
     return d;
 }
 
-// The codes rint(d / scale) of 8 values x of one group, d = x - lo.  d times the reciprocal is within 2^-19 of
-// the quotient (which is at most 15.06: scale is span / 15 but for its rounding), so a code is the quotient's own
-// rounding unless the product stands nearer than 2^-18 to a half: then IEEE division decides.
+// x / 15, rounded as by IEEE division: the rounded product with the rounded reciprocal, and Markstein's correction by
+// the exact remainder (which is exact above 2^-100).
+__device__ __forceinline__ float fifteenth(float x)
+{
+    constexpr float kInv = 0.06666667014360428f;  // RN(1 / 15)
+    const float q = __fmul_rn(x, kInv);
+    const float y = __fmaf_rn(__fmaf_rn(-q, 15.0f, x), kInv, q);
+    return x < 7.888609052210118e-31f || x > 1.0e38f ? __fdiv_rn(x, 15.0f) : y;
+}
+
+// The codes rint(d / scale) of 8 values x of one group, d = x - lo.  d times the approximate reciprocal is within
+// 15.06 * 1.5 * 2^-23 < 2^-18 of the quotient (which is at most 15.06: scale is span / 15 but for its rounding), so a
+// code is the quotient's own rounding unless the product stands nearer than 2^-18 to a half: then IEEE division decides.
 __device__ __forceinline__ uint32_t codes_of(const uint4 &v, float lo, float scale)
 {
     constexpr float kMagic = 12582912.0f;  // 1.5 2^23: a sum with it is rounded to a whole number
-    const float inv = __frcp_rn(scale);
+    float inv;
+    asm("rcp.approx.f32 %0, %1;" : "=f"(inv) : "f"(scale));
+    const f2 lo2 = splat(lo), inv2 = splat(inv), magic = splat(kMagic);
     float n[8], off = 0.0f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const float d = __fsub_rn(i & 1 ? bf_hi(word(v, i / 2)) : bf_lo(word(v, i / 2)), lo);
-        n[i] = __fsub_rn(__fmaf_rn(d, inv, kMagic), kMagic);
-        off = fmaxf(off, fabsf(__fmaf_rn(d, inv, -n[i])));
+    for (int i = 0; i < 4; ++i) {
+        const f2 d = sub2(widen(word(v, i)), lo2);
+        const f2 x = sub2(fma2(d, inv2, magic), magic);
+        const f2 r = fma2(d, inv2, x ^ 0x8000000080000000ull);
+        n[2 * i] = lo_of(x);
+        n[2 * i + 1] = hi_of(x);
+        off = fmaxf(off, fmaxf(fabsf(lo_of(r)), fabsf(hi_of(r))));
     }
     // a subnormal scale may be far from span / 15, and its reciprocal overflow
     if (off > 0.5f - 3.814697265625e-06f || scale < 1.1754943508222875e-38f) {
@@ -75,45 +90,45 @@ __global__ void __launch_bounds__(kThreads) kv4_write_kernel(const Kv4WriteArgs 
         uint32_t *codes = reinterpret_cast<uint32_t *>(value ? a.cache[1] : a.cache[0]) + head * 16 + lane;
         uint32_t *scales = reinterpret_cast<uint32_t *>(value ? a.scales[1] : a.scales[0]) +
                            head * kGroups + lane / kLanes;
-        for (int64_t t0 = (int64_t)blockIdx.x * at_once; t0 < a.T; t0 += step * kAhead) {
-            uint4 v[kAhead];
-            int64_t slot[kAhead];
+        // the row after this one, and the slot after that, are on their way
+        int64_t slot = -1, next_slot;
+        uint4 next = make_uint4(0, 0, 0, 0);
+        auto load_slot = [&](int64_t t) { next_slot = on && t < a.T ? a.slot[t] : -1; };
+        auto load_row = [&](int64_t t) {
+            slot = next_slot < a.num_slots ? next_slot : -1;
+            if (slot >= 0)
+                next = ld_stream(src + t * stride);
+        };
+        int64_t t0 = (int64_t)blockIdx.x * at_once;
+        load_slot(t0 + tt);
+        load_row(t0 + tt);
+        load_slot(t0 + step + tt);
+        for (; t0 < a.T; t0 += step) {
+            const uint4 v = next;
+            const int64_t at = slot;
+            load_row(t0 + step + tt);
+            load_slot(t0 + 2 * step + tt);
+            constexpr uint32_t kSign = 0x80008000u;
+            const uint32_t lo2 = min_nan_bf16x2(min_nan_bf16x2(v.x, v.y),
+                                                min_nan_bf16x2(v.z, v.w));
+            const uint32_t hi2 = min_nan_bf16x2(
+                min_nan_bf16x2(v.x ^ kSign, v.y ^ kSign),
+                min_nan_bf16x2(v.z ^ kSign, v.w ^ kSign));
+            // (minimum, -maximum)
+            uint32_t ends = min_nan_bf16x2(__byte_perm(lo2, hi2, 0x5410), __byte_perm(lo2, hi2, 0x7632));
 #pragma unroll
-            for (int i = 0; i < kAhead; ++i) {
-                const int64_t t = t0 + i * step + tt;
-                slot[i] = on && t < a.T ? a.slot[t] : -1;
-                if (slot[i] >= a.num_slots)
-                    slot[i] = -1;
-                v[i] = make_uint4(0, 0, 0, 0);
-                if (slot[i] >= 0)
-                    v[i] = ld_stream(src + t * stride);
-            }
-#pragma unroll
-            for (int i = 0; i < kAhead; ++i) {
-                if (i > 0 && t0 + i * step >= a.T)
-                    break;
-                constexpr uint32_t kSign = 0x80008000u;
-                const uint32_t lo2 = min_nan_bf16x2(min_nan_bf16x2(v[i].x, v[i].y),
-                                                    min_nan_bf16x2(v[i].z, v[i].w));
-                const uint32_t hi2 = min_nan_bf16x2(
-                    min_nan_bf16x2(v[i].x ^ kSign, v[i].y ^ kSign),
-                    min_nan_bf16x2(v[i].z ^ kSign, v[i].w ^ kSign));
-                // (minimum, -maximum)
-                uint32_t ends = min_nan_bf16x2(__byte_perm(lo2, hi2, 0x5410), __byte_perm(lo2, hi2, 0x7632));
-#pragma unroll
-                for (int off = 1; off < kLanes; off <<= 1)
-                    ends = min_nan_bf16x2(ends, __shfl_xor_sync(0xffffffffu, ends, off));
-                const float lo = bf_lo(ends);
-                const float span = -__fadd_rn(bf_hi(ends), lo);  // NaN or infinite: as the values are
-                const uint32_t held = pack_bf16x2(__fdiv_rn(span, 15.0f), lo);
-                const float scale = bf_lo(held);
-                const bool bad = !isfinite(span) || !isfinite(lo);
-                const uint32_t code = bad || !(scale > 0.0f) ? 0u : codes_of(v[i], lo, scale);
-                if (slot[i] >= 0) {
-                    codes[slot[i] * a.n_kv * 16] = code;
-                    if (lane % kLanes == 0)
-                        scales[slot[i] * a.n_kv * kGroups] = bad ? 0x7fc0u : held;
-                }
+            for (int off = 1; off < kLanes; off <<= 1)
+                ends = min_nan_bf16x2(ends, __shfl_xor_sync(0xffffffffu, ends, off));
+            const float lo = bf_lo(ends);
+            const float span = -__fadd_rn(bf_hi(ends), lo);  // NaN or infinite: as the values are
+            const uint32_t held = pack_bf16x2(fifteenth(span), lo);
+            const float scale = bf_lo(held);
+            const bool bad = !isfinite(span) || !isfinite(lo);
+            const uint32_t code = bad || !(scale > 0.0f) ? 0u : codes_of(v, lo, scale);
+            if (at >= 0) {
+                codes[at * a.n_kv * 16] = code;
+                if (lane % kLanes == 0)
+                    scales[at * a.n_kv * kGroups] = bad ? 0x7fc0u : held;
             }
         }
     }
