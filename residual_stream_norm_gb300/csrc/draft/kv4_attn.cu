@@ -722,112 +722,100 @@ __global__ void __launch_bounds__(warps_of(NT, NG) * 32, 1) kv4_attn_kernel(cons
     const uint32_t warps = blockDim.x / 32;
     char *own = smem + warp * warp_bytes(NT, NG);
     const uint32_t base = (uint32_t)__cvta_generic_to_shared(own);
-    if (z.gang) {
-        // ---- units whole: the warps of a gang take every gang-th tile, and join their parts in shared memory ------
-        const uint32_t in_block = warp / z.gang, i = warp - in_block * z.gang;
-        const uint32_t units = (uint32_t)a.B * z.team, gangs = warps / z.gang;
-        auto meet = [&]() {
-            if (z.gang > 1)
-                named_sync(1 + (int)in_block, (int)z.gang * 32);
-            else
-                __syncwarp();
-        };
-#pragma unroll 1
-        for (uint32_t unit = blockIdx.x * gangs + in_block; unit < units; unit += gridDim.x * gangs) {
-            Note ld;
-            ld.b = (int)(unit / z.team);
-            ld.hr = (int)(unit - (uint32_t)ld.b * z.team);
-            const Keys k = keys_of(a, (uint32_t)ld.b);
-            ld.n = k.n;
-            ld.ns = k.ns;
-            ld.skip = k.skip;
-            ld.tiles = k.tiles();
-            ld.tile = (int)i;
-            const uint32_t todo = (uint32_t)ld.tiles > i ? ((uint32_t)ld.tiles - i + z.gang - 1) / z.gang : 0;
-            const bool alone = z.gang == 1 && todo > 0;  // written by end_unit
-            take_tiles<NT, NG>(a, z, base, own, ld, todo, (int)z.gang, 0, lane);
-            if (alone)
-                continue;
-            // a warp without tiles leaves an empty part
-            float *ml = reinterpret_cast<float *>(own + NT * 8 * 512);
-            if (todo == 0)
-                for (int r = lane; r < NT * 8; r += 32)
-                    *reinterpret_cast<float2 *>(ml + r * 2) = make_float2(__uint_as_float(0xff800000u), 0.0f);
-            meet();
-            const int kv = ld.hr / z.rtiles, r0 = (ld.hr - kv * z.rtiles) * NT * 8;
-            const char *first = own - i * warp_bytes(NT, NG);
-#pragma unroll 1
-            for (int r = (int)i; r < NT * 8 && r0 + r < z.R; r += (int)z.gang) {
-                const float ninf = __uint_as_float(0xff800000u);
-                float2 part = make_float2(ninf, 0.0f);
-                if (lane < (int)z.gang)
-                    part = *reinterpret_cast<const float2 *>(first + lane * warp_bytes(NT, NG) + NT * 8 * 512 +
-                                                             r * 8);
-                float m = part.x;
-#pragma unroll
-                for (int off = 16; off > 0; off >>= 1)
-                    m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
-                const float f = part.y == 0.0f ? 0.0f : exp2_fast(part.x - (m == ninf ? 0.0f : m));
-                float l = part.y * f;
-#pragma unroll
-                for (int off = 16; off > 0; off >>= 1)
-                    l += __shfl_xor_sync(0xffffffffu, l, off);
-                float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 1
-                for (int p = 0; p < (int)z.gang; ++p) {
-                    const float fp = __shfl_sync(0xffffffffu, f, p);
-                    if (fp == 0.0f)
-                        continue;
-                    const float4 x = *reinterpret_cast<const float4 *>(first + p * warp_bytes(NT, NG) +
-                                                                       r * 512 + lane * 16);
-                    o.x = __fmaf_rn(x.x, fp, o.x);
-                    o.y = __fmaf_rn(x.y, fp, o.y);
-                    o.z = __fmaf_rn(x.z, fp, o.z);
-                    o.w = __fmaf_rn(x.w, fp, o.w);
-                }
-                write_row(a, z, ld.b, kv, r0 + r, m, l, o, lane);
-            }
-            meet();  // the parts have been read
-        }
-        return;
+    // Gangs: each `gang` warps of a block take a unit whole, every gang-th tile a warp.  Shares: `active` of the teams
+    // have one, and as many teams' warps work at a time as there are; few teams are spread over all places.
+    uint32_t total = 0, share = 1, active = 0;
+    if (!z.gang) {
+        total = scan_tiles(a, z, s_before, s_warp);
+        share = (total + z.teams - 1) / z.teams;
+        if (total == 0)
+            return;
+        active = (total + share - 1) / share;
     }
-    // ---- even shares of all tiles ------------------------------------------------------------------------
-    const uint32_t total = scan_tiles(a, z, s_before, s_warp);
-    const uint32_t share = (total + z.teams - 1) / z.teams;
-    if (total == 0)
-        return;
-    const uint32_t active = (total + share - 1) / share;  // teams that have one
-    // the teams' warps, as many at a time as there are; few teams are spread over all places
+    const uint32_t gang = z.gang ? z.gang : 1, in_block = warp / gang, i = warp - in_block * gang;
+    const uint32_t at_once = warps / gang, all = z.gang ? (uint32_t)a.B * z.team : z.teams * z.team;
+    auto meet = [&]() {
+        if (gang > 1)
+            named_sync(1 + (int)in_block, (int)gang * 32);
+        else
+            __syncwarp();
+    };
 #pragma unroll 1
-    for (uint32_t v = blockIdx.x * warps + warp; v < z.teams * z.team; v += gridDim.x * warps) {
+    for (uint32_t v = blockIdx.x * at_once + in_block; v < all; v += gridDim.x * at_once) {
         const uint32_t place = v / z.team;
-        const uint32_t mine = (place * active + z.teams - 1) / z.teams;
-        if (mine >= active || mine * z.teams / active != place)
-            continue;
-        const uint32_t start = mine * share;
         Note ld;
-        int lo = 0;  // the last thread's run that starts at or before `start`
+        ld.hr = (int)(v - place * z.team);
+        uint32_t b = place, mine = 0, start = 0, cum = 0, todo = 0;
+        if (!z.gang) {
+            mine = (place * active + z.teams - 1) / z.teams;
+            if (mine >= active || mine * z.teams / active != place)
+                continue;
+            start = mine * share;
+            todo = min(share, total - start);
+            uint32_t lo = 0;  // the last thread's run that starts at or before `start`
 #pragma unroll 1
-        for (int step = kScan / 2; step > 0; step /= 2)
-            if (s_before[lo + step] <= start)
-                lo += step;
-        uint32_t cum = s_before[lo];
-#pragma unroll 1
-        for (uint32_t b = (uint32_t)lo * z.per;; ++b) {
-            const Keys k = keys_of(a, b);
-            if (start < cum + (uint32_t)k.tiles()) {
-                ld.b = (int)b;
-                ld.hr = (int)(v - place * z.team);
-                ld.n = k.n;
-                ld.ns = k.ns;
-                ld.skip = k.skip;
-                ld.tiles = k.tiles();
-                ld.tile = (int)(start - cum);
-                break;
-            }
-            cum += (uint32_t)k.tiles();
+            for (int step = kScan / 2; step > 0; step /= 2)
+                if (s_before[lo + step] <= start)
+                    lo += step;
+            cum = s_before[lo];
+            b = lo * z.per;
         }
-        take_tiles<NT, NG>(a, z, base, own, ld, min(share, total - start), 1, mine, lane);
+        Keys k = keys_of(a, b);
+#pragma unroll 1
+        while (!z.gang && start >= cum + (uint32_t)k.tiles()) {
+            cum += (uint32_t)k.tiles();
+            k = keys_of(a, ++b);
+        }
+        ld.b = (int)b;
+        ld.n = k.n;
+        ld.ns = k.ns;
+        ld.skip = k.skip;
+        ld.tiles = k.tiles();
+        ld.tile = z.gang ? (int)i : (int)(start - cum);
+        if (z.gang)
+            todo = (uint32_t)ld.tiles > i ? ((uint32_t)ld.tiles - i + gang - 1) / gang : 0;
+        take_tiles<NT, NG>(a, z, base, own, ld, todo, (int)gang, mine, lane);
+        if (!z.gang || (gang == 1 && todo > 0))
+            continue;  // written, as a whole or as parts
+        // ---- a gang's parts; a warp without tiles leaves an empty one ------------------------------------------
+        float *ml = reinterpret_cast<float *>(own + NT * 8 * 512);
+        if (todo == 0)
+            for (int r = lane; r < NT * 8; r += 32)
+                *reinterpret_cast<float2 *>(ml + r * 2) = make_float2(__uint_as_float(0xff800000u), 0.0f);
+        meet();
+        const int kv = ld.hr / z.rtiles, r0 = (ld.hr - kv * z.rtiles) * NT * 8;
+        const char *first = own - i * warp_bytes(NT, NG);
+#pragma unroll 1
+        for (int r = (int)i; r < NT * 8 && r0 + r < z.R; r += (int)gang) {
+            const float ninf = __uint_as_float(0xff800000u);
+            float2 part = make_float2(ninf, 0.0f);
+            if (lane < (int)gang)
+                part = *reinterpret_cast<const float2 *>(first + lane * warp_bytes(NT, NG) + NT * 8 * 512 + r * 8);
+            float m = part.x;
+#pragma unroll
+            for (int off = 16; off > 0; off >>= 1)
+                m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
+            const float f = part.y == 0.0f ? 0.0f : exp2_fast(part.x - (m == ninf ? 0.0f : m));
+            float l = part.y * f;
+#pragma unroll
+            for (int off = 16; off > 0; off >>= 1)
+                l += __shfl_xor_sync(0xffffffffu, l, off);
+            float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 1
+            for (int p = 0; p < (int)gang; ++p) {
+                const float fp = __shfl_sync(0xffffffffu, f, p);
+                if (fp == 0.0f)
+                    continue;
+                const float4 x = *reinterpret_cast<const float4 *>(first + p * warp_bytes(NT, NG) + r * 512 +
+                                                                   lane * 16);
+                o.x = __fmaf_rn(x.x, fp, o.x);
+                o.y = __fmaf_rn(x.y, fp, o.y);
+                o.z = __fmaf_rn(x.z, fp, o.z);
+                o.w = __fmaf_rn(x.w, fp, o.w);
+            }
+            write_row(a, z, ld.b, kv, r0 + r, m, l, o, lane);
+        }
+        meet();  // the parts have been read
     }
 }
 
