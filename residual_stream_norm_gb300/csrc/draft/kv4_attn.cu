@@ -38,11 +38,12 @@ constexpr int kScan = 256;  // threads that count tiles
 constexpr int kTile = 32;  // keys
 
 // Warps of a block: 16, 12 or 8, as the registers of NT 8-row tiles allow without spilling more than a few (128, 168 or
-// 255 a thread).  Measured: 8 contexts of 100K keys, NT = 1: groups of 128 176 us with 16 and 190 with 12, of 32 240 and
-// 234 (8 warps: 301); 32 sequences of up to 20K, NT = 2: groups of 128 157 us with 8 and 131 with 12, of 32 205 and 215.
+// 255 a thread).  Measured, NT = 1, 8 contexts of 100K keys: groups of 128 176 us with 16 and 190 with 12, of 32 240 and
+// 234 (8 warps: 301).  32 sequences of up to 20K: NT = 2, groups of 64 147 us with 12 and 169 with 8, of 32 189 and 207;
+// NT = 3, groups of 64 269 with 12 and 217 with 8.
 __host__ __device__ constexpr int warps_of(int NT, int NG)
 {
-    return NT == 1 ? (NG == 4 ? 12 : 16) : (NT == 2 && NG == 1 ? 12 : 8);
+    return NT == 1 ? (NG == 4 ? 12 : 16) : (NT == 2 ? 12 : 8);
 }
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
@@ -71,7 +72,8 @@ __host__ __device__ constexpr int scales_at() { return 2 * kTile * 64; }
 __host__ __device__ constexpr int note_at(int NG) { return scales_at() + 2 * kTile * 4 * NG; }
 __host__ __device__ constexpr int stage_bytes(int NG) { return note_at(NG) + (int)sizeof(Note); }
 constexpr int kSmem = 225 * 1024;
-__host__ __device__ constexpr int query_bytes(int NT) { return NT > 1 ? NT * 4 * 32 * 16 : 0; }
+__host__ __device__ constexpr int rows_at(int NT) { return NT * 4 * 32 * 16; }  // behind a query
+__host__ __device__ constexpr int query_bytes(int NT) { return NT > 1 ? rows_at(NT) + NT * 8 * 4 * 5 : 0; }
 __host__ __device__ constexpr int stages_of(int NT, int NG)
 {
     const int fit = (kSmem / warps_of(NT, NG) - query_bytes(NT)) / stage_bytes(NG);
@@ -167,13 +169,25 @@ __device__ __forceinline__ uint32_t chunk_at(int key, int c)
     return (uint32_t)(key * 64 + ((c ^ ((key >> 1) & 3)) << 4));
 }
 
+__device__ __forceinline__ void sts_f32(uint32_t at, float x)
+{
+    asm volatile("st.shared.f32 [%0], %1;" ::"r"(at), "f"(x) : "memory");
+}
+__device__ __forceinline__ float2 lds_f32x2(uint32_t at)
+{
+    float2 x;
+    asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(x.x), "=f"(x.y) : "r"(at) : "memory");
+    return x;
+}
+
 template <int NT, int NG>
 struct Unit {
     // query, FP16: columns c*32 + t*8 + {j, j + 4} of row g, j = 0..3 (odd j: a sixteenth); of more than one row tile
     // in shared memory, where it leaves room in the registers
     uint32_t q[1][4][4];
     // rows 2t, 2t+1: with t = scale (sum of products) + minimum qsum, the scores are fac t in powers of two
-    float fac[NT][2], qsum[NT][2][NG];
+    // (of more than one row tile in shared memory too, behind the query: [1 + NG][NT * 8])
+    float fac[2], qsum[2][NG];
     float m[NT][2], l[NT][2], omin[NT][2][NG];  // of the scaled scores
     int e[NT][2];            // scales seen are below 2^e
     bool one_e;              // the same one for all rows
@@ -249,10 +263,19 @@ __device__ __forceinline__ void begin_unit(Unit<NT, NG> &u, const Kv4AttnArgs &a
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
             const int from = (2 * t + e) * 4;  // a lane whose g is this row
-            u.fac[nt][e] = __shfl_sync(0xffffffffu, fac, from);
+            const uint32_t at_row = qb + rows_at(NT) + (nt * 8 + 2 * t + e) * 4;
+            const float row_fac = __shfl_sync(0xffffffffu, fac, from);
+            if (NT == 1)
+                u.fac[e] = row_fac;
+            else if (g == 0)
+                sts_f32(at_row, row_fac);
 #pragma unroll
             for (int j = 0; j < NG; ++j) {
-                u.qsum[nt][e][j] = __shfl_sync(0xffffffffu, gs[j], from);
+                const float row_sum = __shfl_sync(0xffffffffu, gs[j], from);
+                if (NT == 1)
+                    u.qsum[e][j] = row_sum;
+                else if (g == 0)
+                    sts_f32(at_row + (j + 1) * NT * 32, row_sum);
                 u.omin[nt][e][j] = 0.0f;
             }
             u.m[nt][e] = __uint_as_float(0xff800000u);
@@ -268,6 +291,7 @@ __device__ __forceinline__ void begin_unit(Unit<NT, NG> &u, const Kv4AttnArgs &a
                     u.o[nt][c][jj][i] = 0.0f;
     }
     u.one_e = true;
+    __syncwarp();
 }
 
 // A tile of 32 keys.  Thread (g, t) holds scores of keys 16 mt + g (i < 2) and 16 mt + 8 + g (i >= 2) for
@@ -335,17 +359,21 @@ __device__ __forceinline__ void take_tile(Unit<NT, NG> &u, const Kv4AttnArgs &a,
                     }
             }
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
+            for (int nt = 0; nt < NT; ++nt) {
+                float2 qs = make_float2(u.qsum[0][j], u.qsum[1][j]);
+                if (NT > 1)
+                    qs = lds_f32x2(qb + rows_at(NT) + (((j + 1) * NT + nt) * 8 + 2 * t) * 4);
 #pragma unroll
                 for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         const uint32_t w = sc[mt][i >> 1][j];
                         float &x = s[nt][mt][i];
-                        const float y = u.qsum[nt][i & 1][j];
+                        const float y = i & 1 ? qs.y : qs.x;
                         x = j == 0 ? __fmul_rn(bf_hi(w), y) : __fmaf_rn(bf_hi(w), y, x);
                         x = __fmaf_rn(bf_lo(w), acc[nt][mt][i], x);
                     }
+            }
         }
     }
     // ---- what a row does not see; the largest of the values' scales --------------------------------
@@ -416,14 +444,18 @@ __device__ __forceinline__ void take_tile(Unit<NT, NG> &u, const Kv4AttnArgs &a,
     // ---- maxima and weights -------------------------------------------------------------------------
     float up[NT][2];
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
+    for (int nt = 0; nt < NT; ++nt) {
+        float2 facs = make_float2(u.fac[0], u.fac[1]);
+        if (NT > 1)
+            facs = lds_f32x2(qb + rows_at(NT) + (nt * 8 + 2 * t) * 4);
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
+            const float fac = e ? facs.y : facs.x;
             float mx = fmaxf(fmaxf(s[nt][0][e], s[nt][0][e + 2]), fmaxf(s[nt][1][e], s[nt][1][e + 2]));
 #pragma unroll
             for (int off = 4; off < 32; off <<= 1)
                 mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
-            const float mn = fmaxf(u.m[nt][e], mx * u.fac[nt][e]);
+            const float mn = fmaxf(u.m[nt][e], mx * fac);
             const float ref = mn == ninf ? 0.0f : mn;
             const float alpha = exp2_fast(u.m[nt][e] - ref);  // 0 at the first tile
             up[nt][e] = alpha * pow2i(max(u.e[nt][e] - e_new[nt][e], -126));
@@ -435,7 +467,7 @@ __device__ __forceinline__ void take_tile(Unit<NT, NG> &u, const Kv4AttnArgs &a,
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     float &x = s[nt][mt][e + 2 * h];
-                    x = exp2_fast(__fmaf_rn(x, u.fac[nt][e], -ref));
+                    x = exp2_fast(__fmaf_rn(x, fac, -ref));
                     sum += x;
                 }
             u.l[nt][e] = __fmaf_rn(u.l[nt][e], alpha, sum);
@@ -443,6 +475,7 @@ __device__ __forceinline__ void take_tile(Unit<NT, NG> &u, const Kv4AttnArgs &a,
             for (int j = 0; j < NG; ++j)
                 u.omin[nt][e][j] *= alpha;
         }
+    }
     uint32_t b[NT][2][NG][2];
     const float vinv = pow2i(15 - u.e[0][0]);
 #pragma unroll
