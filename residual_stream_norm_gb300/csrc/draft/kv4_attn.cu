@@ -616,52 +616,46 @@ __device__ __forceinline__ void take_tiles(const Kv4AttnArgs &a, const Sizes &z,
                                            Note ld, uint32_t todo, int stride, uint32_t mine, int lane)
 {
     constexpr int kStages = stages_of(NT, NG);
-    const uint32_t qb = base + kStages * stage_bytes(NG), hr = (uint32_t)ld.hr;
-    const int kv = (int)hr / z.rtiles;
+    const uint32_t qb = base + kStages * stage_bytes(NG);
+    const int kv = ld.hr / z.rtiles;
     // ---- copies --------------------------------------------------------------------------------------
-    uint32_t to_load = todo;
-    int slot, put = 0;
-    auto load_slot = [&]() {  // of key `lane` of the tile; -1: not to be seen
+    int64_t entry;
+    // table entry of key `lane` of the tile; -1: none.  Nothing is done with it before the tile's copies, a tile later.
+    auto load_slot = [&]() {
         const int v = ld.tile * kTile + lane;
-        slot = -1;
-        if (v < ld.n - ld.skip) {
-            const int64_t s = a.table[ld.b * a.table_stride + (v < ld.ns ? v : v + ld.skip)];
-            slot = s >= 0 && s < a.num_slots ? (int)s : -1;
-        }
+        entry = -1;
+        if (v < ld.n - ld.skip)
+            entry = a.table[ld.b * a.table_stride + (v < ld.ns ? v : v + ld.skip)];
     };
     if (todo > 0)
         load_slot();
     // of a slot: the lane's 16 bytes of one of eight rows, and its scales
-    const char *src[2], *src_scales[2];
-#pragma unroll
-    for (int x = 0; x < 2; ++x) {
-        src[x] = (const char *)a.cache[x] + kv * 64 + (lane & 3) * 16;
-        src_scales[x] = (const char *)a.scales[x] + kv * 4 * NG;
-    }
     const uint32_t slot_bytes = (uint32_t)a.n_kv * 64u, slot_scales = (uint32_t)a.n_kv * 4u * NG;
+    const uint64_t own_bytes = (uint32_t)(kv * 64 + (lane & 3) * 16), own_scales = (uint32_t)(kv * 4 * NG);
     const uint32_t lane_at = chunk_at(lane >> 2, lane & 3);
-    auto load_next = [&]() {
-        if (to_load > 0) {
+    auto load_tile = [&](uint32_t j, int put) {  // tile number j
+        if (j < todo) {
             const uint32_t to = base + put * stage_bytes(NG);
+            const int slot = entry >= 0 && entry < a.num_slots ? (int)entry : -1;  // -1: not to be seen
             ld.valid = __ballot_sync(0xffffffffu, slot >= 0);
 #pragma unroll
             for (int i = 0; i < kTile / 8; ++i) {
                 const int at_key = __shfl_sync(0xffffffffu, slot, i * 8 + (lane >> 2));
-                const uint64_t off = (uint64_t)(uint32_t)max(at_key, 0) * slot_bytes;
+                const uint64_t off = (uint64_t)(uint32_t)max(at_key, 0) * slot_bytes + own_bytes;
                 const uint32_t n = at_key >= 0 ? 16u : 0u;
-                cp_async16(to + lane_at + i * 512, src[0] + off, n);
-                cp_async16(to + lane_at + i * 512 + kTile * 64, src[1] + off, n);
+                cp_async16(to + lane_at + i * 512, (const char *)a.cache[0] + off, n);
+                cp_async16(to + lane_at + i * 512 + kTile * 64, (const char *)a.cache[1] + off, n);
             }
-            const uint64_t off = (uint64_t)(uint32_t)max(slot, 0) * slot_scales;
+            const uint64_t off = (uint64_t)(uint32_t)max(slot, 0) * slot_scales + own_scales;
             const uint32_t at = to + scales_at() + lane * 4 * NG, n = slot >= 0 ? 4u * NG : 0u;
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
                 if constexpr (NG == 1)
-                    cp_async4(at + x * kTile * 4, src_scales[x] + off, n);
+                    cp_async4(at + x * kTile * 4, (const char *)a.scales[x] + off, n);
                 else if constexpr (NG == 2)
-                    cp_async8(at + x * kTile * 8, src_scales[x] + off, n);
+                    cp_async8(at + x * kTile * 8, (const char *)a.scales[x] + off, n);
                 else
-                    cp_async16(at + x * kTile * 16, src_scales[x] + off, n);
+                    cp_async16(at + x * kTile * 16, (const char *)a.scales[x] + off, n);
             }
             if (lane == 0) {
                 sts128(to + note_at(NG), make_uint4(ld.valid, (uint32_t)ld.b, (uint32_t)ld.hr,
@@ -669,8 +663,7 @@ __device__ __forceinline__ void take_tiles(const Kv4AttnArgs &a, const Sizes &z,
                 sts128(to + note_at(NG) + 16, make_uint4((uint32_t)ld.tiles, (uint32_t)ld.n,
                                                          (uint32_t)ld.ns, (uint32_t)ld.skip));
             }
-            put = put + 1 == kStages ? 0 : put + 1;
-            if (--to_load > 0) {
+            if (j + 1 < todo) {
                 ld.tile += stride;
                 if (ld.tile >= ld.tiles) {
                     ld.tile = 0;
@@ -690,7 +683,7 @@ __device__ __forceinline__ void take_tiles(const Kv4AttnArgs &a, const Sizes &z,
     };
 #pragma unroll 1
     for (int s = 0; s < kStages - 1; ++s)
-        load_next();
+        load_tile((uint32_t)s, s);
     // ---- tiles ----------------------------------------------------------------------------------------
     Unit<NT, NG> u;
     bool fresh = true, from_start = false;
@@ -699,7 +692,7 @@ __device__ __forceinline__ void take_tiles(const Kv4AttnArgs &a, const Sizes &z,
     for (uint32_t j = 0; j < todo; ++j) {
         cp_async_wait<kStages - 2>();
         __syncwarp();
-        load_next();
+        load_tile(j + kStages - 1, get == 0 ? kStages - 1 : get - 1);
         const uint32_t from = base + get * stage_bytes(NG);
         const uint4 n0 = lds128(from + note_at(NG)), n1 = lds128(from + note_at(NG) + 16);
         const Note at{n0.x, (int)n0.y, (int)n0.z, (int)n0.w, (int)n1.x, (int)n1.y, (int)n1.z, (int)n1.w};
@@ -713,7 +706,7 @@ __device__ __forceinline__ void take_tiles(const Kv4AttnArgs &a, const Sizes &z,
         if (j + 1 == todo || (last && !z.gang)) {
             // the share's first unit leaves its part in place 0, a later one in place 1
             const bool first_unit = j <= (uint32_t)at.tile;
-            const int64_t part = (int64_t)((mine * z.team + hr) * 2 + (first_unit ? 0 : 1)) * NT * 8;
+            const int64_t part = (int64_t)((mine * z.team + (uint32_t)at.hr) * 2 + (first_unit ? 0 : 1)) * NT * 8;
             float *po = z.gang ? reinterpret_cast<float *>(own) : z.part_o + part * 128;
             float *pm = z.gang ? reinterpret_cast<float *>(own + NT * 8 * 512) : z.part_ml + part * 2;
             if (z.gang) {  // the part takes the place of the tiles
