@@ -1019,7 +1019,7 @@ Kv4AttnPlan kv4_attn_plan(int32_t B, int32_t q_len, int32_t n_q, int32_t n_kv, i
     p.most_tiles = (double)((width + kTile - 1) / kTile) * B;
     // as many teams as all SMs' warps make, but no more than there can be tiles
     int64_t most = width;
-    if (window > 0 && window + q_len + n_sink < width)
+    if (window > 0 && window < width && n_sink < width && window + q_len + n_sink < width)
         most = window + q_len + n_sink;
     const double tiles = (double)((most + kTile - 1) / kTile) * B;
     const int32_t team = n_kv * p.rtiles, warps = kSms * warps_of(p.nt, 128 / group);

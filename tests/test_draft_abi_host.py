@@ -91,6 +91,10 @@ def test_attention_workspace(lib):
     assert f(0, 1, 48, 8, 10, 0, 0) == 0
     n = f(8, 1, 48, 8, 5000, 0, 0)
     assert n > 0 and attn(lib, nb=8, width=5000, t_stride=5000, ws_bytes=n - 1) == INVALID
+    # any window from the table's width on is none, and any number of sinks all keys
+    most = (1 << 63) - 1
+    for window, n_sink in ((most, 0), (most, most), (3, most), (5000, 4)):
+        assert f(8, 1, 48, 8, 5000, window, n_sink) == n
     with pytest.raises(rsn.BeamError):
         rsn.beam_attn_kv4_workspace(1, 0, 48, 8, 10)
 

@@ -353,6 +353,46 @@ def test_same_bits_every_time_and_in_a_graph():
     assert torch.equal(out.cpu(), run(c)[0])
 
 
+def test_more_query_rows_than_warps():
+    # more KV heads and row tiles than an SM's, and than all SMs' warps (whole units, and one cut by its rows alone)
+    lib()
+    check(make(2, 150, 16, 2, [200, 40], 64, seed=18))
+    check(make(1, 500, 64, 8, [1500], 128, seed=19))
+
+
+def test_windows_past_the_table():
+    lib()
+    c = make(3, 2, 12, 2, [2, 70, 300], 64, seed=20)
+    plain = run(c)
+    for window, n_sink in ((1 << 62, 0), (300, 5), (7, 1 << 62)):
+        assert all(torch.equal(a, b) for a, b in zip(run(c, window, n_sink), plain))
+
+
+def test_no_table_at_all():
+    lib()
+    c = make(2, 3, 6, 1, [0, 0], 128, width=1)
+    c["table"] = c["table"][:, :0]
+    check(c)
+
+
+def test_two_streams_at_once():
+    # calls that run side by side, each with its own workspace and output
+    lib()
+    cs = [make(4, 1, 12, 2, [700, 3, 90, 4000], 32, seed=21 + i) for i in range(2)]
+    want = [run(c)[0] for c in cs]
+    ds = [{x: c[x].cuda() for x in ("q", "k_cache", "v_cache", "k_scales", "v_scales", "table", "lens")} for c in cs]
+    ws = [torch.empty(rsn.beam_attn_kv4_workspace(4, 1, 12, 2, 4000), dtype=torch.uint8, device="cuda") for _ in cs]
+    outs = [torch.zeros_like(d["q"]) for d in ds]
+    streams = [torch.cuda.Stream() for _ in cs]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for s, d, w, o in zip(streams, ds, ws, outs):
+            rsn.beam_attn_kv4_fwd(o, d["q"], d["k_cache"], d["v_cache"], d["k_scales"], d["v_scales"], d["table"],
+                                  d["lens"], w, group=32, stream=s)
+    torch.cuda.synchronize()
+    assert all(torch.equal(o.cpu(), w) for o, w in zip(outs, want))
+
+
 def test_write_then_read():
     # the step as a server runs it: the new tokens' rows go in, and attention sees them
     lib()

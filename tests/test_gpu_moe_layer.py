@@ -192,6 +192,31 @@ def test_same_bits_every_time_and_in_a_graph():
         assert torch.equal(out.cpu(), first)
 
 
+def test_two_streams_at_once():
+    lib()
+    cs = [make(T, 256, 104, seed=13 + T) for T in (5, 40)]
+    want = [run(c)[0] for c in cs]
+    xs = [c["x"].cuda() for c in cs]
+    ws = [torch.empty(rsn.beam_moe_layer_workspace(len(x), 256, 104), dtype=torch.uint8, device="cuda") for x in xs]
+    outs = [torch.zeros_like(x) for x in xs]
+    streams = [torch.cuda.Stream() for _ in cs]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for s, c, x, w, o in zip(streams, cs, xs, ws, outs):
+            d = c["dev"]
+            rsn.beam_moe_layer_fwd(o, x, d["rw"], d["rb"], d["w13"], d["w2"], w, stream=s)
+    torch.cuda.synchronize()
+    assert all(torch.equal(o.cpu(), w) for o, w in zip(outs, want))
+
+
+@pytest.mark.parametrize("T,H,F", [(256, 16384, 8), (256, 8, 32768)])
+def test_largest_sizes(T, H, F):
+    lib()
+    c = make(T, H, F, 40, 2, seed=T + F)
+    c["rb"][40:42] += 50  # every token comes here
+    check(c)
+
+
 def test_no_tokens():
     lib()
     c = make(1, 64, 16, seed=12)
