@@ -363,15 +363,19 @@ __device__ __forceinline__ void take_tile(Unit<NT, NG> &u, const Kv4AttnArgs &a,
                 float2 qs = make_float2(u.qsum[0][j], u.qsum[1][j]);
                 if (NT > 1)
                     qs = lds_f32x2(qb + rows_at(NT) + (((j + 1) * NT + nt) * 8 + 2 * t) * 4);
+                const f2 sum = make_f2(qs.x, qs.y);  // of a key's two rows
 #pragma unroll
                 for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const uint32_t w = sc[mt][i >> 1][j];
-                        float &x = s[nt][mt][i];
-                        const float y = i & 1 ? qs.y : qs.x;
-                        x = j == 0 ? __fmul_rn(bf_hi(w), y) : __fmaf_rn(bf_hi(w), y, x);
-                        x = __fmaf_rn(bf_lo(w), acc[nt][mt][i], x);
+                    for (int h = 0; h < 2; ++h) {
+                        const uint32_t w = sc[mt][h][j];
+                        float *x = &s[nt][mt][2 * h];
+                        const float *y = &acc[nt][mt][2 * h];
+                        const f2 m = splat(bf_hi(w));
+                        const f2 z2 = j == 0 ? mul2(m, sum) : fma2(m, sum, make_f2(x[0], x[1]));
+                        const f2 r = fma2(splat(bf_lo(w)), make_f2(y[0], y[1]), z2);
+                        x[0] = lo_of(r);
+                        x[1] = hi_of(r);
                     }
             }
         }
@@ -445,35 +449,45 @@ __device__ __forceinline__ void take_tile(Unit<NT, NG> &u, const Kv4AttnArgs &a,
     float up[NT][2];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-        float2 facs = make_float2(u.fac[0], u.fac[1]);
+        float2 fac = make_float2(u.fac[0], u.fac[1]);
         if (NT > 1)
-            facs = lds_f32x2(qb + rows_at(NT) + (nt * 8 + 2 * t) * 4);
+            fac = lds_f32x2(qb + rows_at(NT) + (nt * 8 + 2 * t) * 4);
+        float ref[2], alpha[2];
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-            const float fac = e ? facs.y : facs.x;
             float mx = fmaxf(fmaxf(s[nt][0][e], s[nt][0][e + 2]), fmaxf(s[nt][1][e], s[nt][1][e + 2]));
 #pragma unroll
             for (int off = 4; off < 32; off <<= 1)
                 mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
-            const float mn = fmaxf(u.m[nt][e], mx * fac);
-            const float ref = mn == ninf ? 0.0f : mn;
-            const float alpha = exp2_fast(u.m[nt][e] - ref);  // 0 at the first tile
-            up[nt][e] = alpha * pow2i(max(u.e[nt][e] - e_new[nt][e], -126));
+            const float mn = fmaxf(u.m[nt][e], mx * (e ? fac.y : fac.x));
+            ref[e] = mn == ninf ? 0.0f : mn;
+            alpha[e] = exp2_fast(u.m[nt][e] - ref[e]);  // 0 at the first tile
+            up[nt][e] = alpha[e] * pow2i(max(u.e[nt][e] - e_new[nt][e], -126));
             u.e[nt][e] = e_new[nt][e];
             u.m[nt][e] = mn;
-            float sum = 0.0f;
+        }
+        const f2 fac2 = make_f2(fac.x, fac.y), ref2 = make_f2(-ref[0], -ref[1]);
+        const f2 alpha2 = make_f2(alpha[0], alpha[1]);
+        f2 sum = splat(0.0f);
 #pragma unroll
-            for (int mt = 0; mt < 2; ++mt)
+        for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    float &x = s[nt][mt][e + 2 * h];
-                    x = exp2_fast(__fmaf_rn(x, fac, -ref));
-                    sum += x;
-                }
-            u.l[nt][e] = __fmaf_rn(u.l[nt][e], alpha, sum);
+            for (int h = 0; h < 2; ++h) {
+                float *x = &s[nt][mt][2 * h];
+                const f2 y = fma2(make_f2(x[0], x[1]), fac2, ref2);
+                x[0] = exp2_fast(lo_of(y));
+                x[1] = exp2_fast(hi_of(y));
+                const f2 p = make_f2(x[0], x[1]);
+                sum = mt + h == 0 ? p : add2(sum, p);
+            }
+        sum = fma2(make_f2(u.l[nt][0], u.l[nt][1]), alpha2, sum);
+        u.l[nt][0] = lo_of(sum);
+        u.l[nt][1] = hi_of(sum);
 #pragma unroll
-            for (int j = 0; j < NG; ++j)
-                u.omin[nt][e][j] *= alpha;
+        for (int j = 0; j < NG; ++j) {
+            const f2 x = mul2(make_f2(u.omin[nt][0][j], u.omin[nt][1][j]), alpha2);
+            u.omin[nt][0][j] = lo_of(x);
+            u.omin[nt][1][j] = hi_of(x);
         }
     }
     uint32_t b[NT][2][NG][2];
@@ -493,9 +507,14 @@ __device__ __forceinline__ void take_tile(Unit<NT, NG> &u, const Kv4AttnArgs &a,
                 const float(&p)[4] = s[nt][mt];
                 if (plain) {
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        w[i] = p[i] * vs[i >> 1];
-                        u.omin[nt][i & 1][j] = __fmaf_rn(p[i], vm[i >> 1], u.omin[nt][i & 1][j]);
+                    for (int h = 0; h < 2; ++h) {
+                        const f2 p2 = make_f2(p[2 * h], p[2 * h + 1]), x = mul2(p2, splat(vs[h]));
+                        const f2 y = fma2(p2, splat(vm[h]),
+                                          make_f2(u.omin[nt][0][j], u.omin[nt][1][j]));
+                        w[2 * h] = lo_of(x);
+                        w[2 * h + 1] = hi_of(x);
+                        u.omin[nt][0][j] = lo_of(y);
+                        u.omin[nt][1][j] = hi_of(y);
                     }
                 } else {
 #pragma unroll

@@ -16,7 +16,7 @@
 // - The ranking decisions are those of the correctly rounded FP32 sigmoids (beam_exp.cuh), the
 //   oracle's (see below for how most of them are made on cheaper values).
 // - A group's score is the FP32 sum of its two best choice scores.  The quad finds them with two
-//   shuffle steps on (key, index) pairs.
+//   shuffle steps on their keys.
 // - Every lane ranks the eight group scores.
 // - Then eight rounds pick the experts: each lane keeps its eligible experts sorted.  A round
 //   takes the warp's best head with two `redux.sync` reductions (the largest key, then the
@@ -38,9 +38,9 @@ namespace {
 
 constexpr int kRouteThreads = 256;      // 8 tokens per CTA pass
 
-// 3 CTAs per SM: more warps to cover the ranking's dependent-instruction latency.  At the 80
-// registers this allows the kernel spills a little, and is still faster than at 2 CTAs and 124
-// registers without spills (46.4 against 49.4 us at T = 16384; 4 CTAs gave 46.5).
+// At least 3 CTAs per SM: more warps to cover the ranking's dependent-instruction latency.  The kernel takes 63
+// registers, so four fit: 37.7 us at T = 16384, 2.6 us for one token (51.6 and 4.4 with index pairs in the group
+// scores and the exact sigmoid's code in several places, at 80 registers).
 __global__ void __launch_bounds__(kRouteThreads, 3)
     grouped_topk_kernel(const RouteArgs a)
 {
