@@ -28,6 +28,7 @@
 #include "beam_f32x2.cuh"
 #include "beam_tma.cuh"
 #include "decode/decode_mma.cuh"
+#include "decode/decode_tc.cuh"
 #include "draft_kernels.h"
 
 namespace beam {
@@ -37,13 +38,14 @@ constexpr int kSms = 152;
 constexpr int kScan = 256;  // threads that count tiles
 constexpr int kTile = 32;  // keys
 
-// Warps of a block: 16, 12 or 8, as the registers of NT 8-row tiles allow without spilling more than a few (128, 168 or
-// 255 a thread).  Measured, NT = 1, 8 contexts of 100K keys: groups of 128 176 us with 16 and 190 with 12, of 32 240 and
-// 234 (8 warps: 301).  32 sequences of up to 20K: NT = 2, groups of 64 147 us with 12 and 169 with 8, of 32 189 and 207;
-// NT = 3, groups of 64 269 with 12 and 217 with 8.
+// Warps of a block, as the registers of NT 8-row tiles allow without spilling more than a few (128 or 168 a thread).
+// Between tiles a unit's output is kept in tensor memory, 32 columns of a warp's own lanes for each row tile: with the
+// outputs in registers 8 contexts of 100K keys (NT = 1, groups of 32) took 197 us with 12 warps, 184 so with 16; 32
+// sequences of up to 20K keys in groups of 64 with NT = 2 145 us with 12 warps, 119 so with 12 (and with 16), with NT = 3
+// 180 with 8, 160 so with 12.  (NT = 1 with 20 warps, which spill: groups of 128 152 us, with 16 137.)
 __host__ __device__ constexpr int warps_of(int NT, int NG)
 {
-    return NT == 1 ? (NG == 4 ? 12 : 16) : (NT == 2 ? 12 : 8);
+    return NT == 1 || (NT == 2 && NG == 1) ? 16 : 12;
 }
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
@@ -160,6 +162,51 @@ __device__ __forceinline__ void lds_scales(uint32_t (&w)[NG], uint32_t addr)
                      : "memory");
 }
 
+// Columns that hold n: a power of two from 32 on.
+__device__ __forceinline__ uint32_t tmem_columns(uint32_t n) { return n <= 32 ? 32 : 1u << (32 - __clz(n - 1)); }
+
+// By one whole warp.
+__device__ __forceinline__ void tmem_alloc(uint32_t *dst, uint32_t columns)
+{
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(dst)),
+                 "r"(columns)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+}
+
+__device__ __forceinline__ void tmem_free(uint32_t base, uint32_t columns)
+{
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(base), "r"(columns) : "memory");
+}
+
+// 8 columns of tensor memory, of this thread's lane.  A load's values may be used behind the wait below.
+__device__ __forceinline__ void tmem_ld8(uint32_t addr, float (&x)[8])
+{
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=f"(x[0]), "=f"(x[1]), "=f"(x[2]), "=f"(x[3]), "=f"(x[4]), "=f"(x[5]), "=f"(x[6]), "=f"(x[7])
+                 : "r"(addr)
+                 : "memory");
+}
+
+__device__ __forceinline__ void tmem_st8(uint32_t addr, const float (&x)[8])
+{
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%8], {%0, %1, %2, %3, %4, %5, %6, %7};" ::"f"(x[0]),
+                 "f"(x[1]), "f"(x[2]), "f"(x[3]), "f"(x[4]), "f"(x[5]), "f"(x[6]), "f"(x[7]), "r"(addr)
+                 : "memory");
+}
+
+// Waits for all loads; the values named are behind it for the compiler too.
+template <int N>
+__device__ __forceinline__ void tmem_loaded(float (&x)[N][8])
+{
+    tmem_wait_ld();
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+        asm volatile(""
+                     : "+f"(x[i][0]), "+f"(x[i][1]), "+f"(x[i][2]), "+f"(x[i][3]), "+f"(x[i][4]), "+f"(x[i][5]),
+                       "+f"(x[i][6]), "+f"(x[i][7]));
+}
+
 // 2^e for -126 <= e <= 127
 __device__ __forceinline__ float pow2i(int e) { return __uint_as_float((uint32_t)(127 + e) << 23); }
 
@@ -191,7 +238,7 @@ struct Unit {
     float m[NT][2], l[NT][2], omin[NT][2][NG];  // of the scaled scores
     int e[NT][2];            // scales seen are below 2^e
     bool one_e;              // the same one for all rows
-    float o[NT][4][2][4];
+    uint32_t tmem;           // the output: 8 columns for each (chunk, row tile), [2][4] of a product's places
 };
 
 // Row `row` of a sequence and KV head: its query's index and place in the sequence.
@@ -282,16 +329,16 @@ __device__ __forceinline__ void begin_unit(Unit<NT, NG> &u, const Kv4AttnArgs &a
             u.l[nt][e] = 0.0f;
             u.e[nt][e] = kMinExp;
         }
-#pragma unroll
-        for (int c = 0; c < 4; ++c)
-#pragma unroll
-            for (int jj = 0; jj < 2; ++jj)
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    u.o[nt][c][jj][i] = 0.0f;
     }
     u.one_e = true;
     __syncwarp();
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+            const float zero[8] = {};
+            tmem_st8(u.tmem + (c * NT + nt) * 8, zero);
+        }
 }
 
 // A tile of 32 keys.  Thread (g, t) holds scores of keys 16 mt + g (i < 2) and 16 mt + 8 + g (i >= 2) for
@@ -533,8 +580,13 @@ __device__ __forceinline__ void take_tile(Unit<NT, NG> &u, const Kv4AttnArgs &a,
         }
     }
     // ---- output ------------------------------------------------------------------------------------
+    tmem_wait_st();
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
+        float o[NT][8];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+            tmem_ld8(u.tmem + (c * NT + nt) * 8, o[nt]);
         uint32_t v[4];  // units of chunk c: keys 0-7, 8-15, 16-23, 24-31
         ldmatrix_x4_trans(v, vb + chunk_at(lane, c));
         float acc[NT][2][4];
@@ -556,18 +608,19 @@ __device__ __forceinline__ void take_tile(Unit<NT, NG> &u, const Kv4AttnArgs &a,
                 for (int nt = 0; nt < NT; ++nt)
                     mma16816<true>(acc[nt][jj], f, b[nt][mt][c * NG / 4][0], b[nt][mt][c * NG / 4][1]);
             }
+        tmem_loaded(o);
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
+        for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
-            for (int jj = 0; jj < 2; ++jj)
-#pragma unroll
-                for (int i = 0; i < 4; i += 2) {
-                    float *o = &u.o[nt][c][jj][i];
-                    const f2 x = fma2(make_f2(o[0], o[1]), make_f2(up[nt][0], up[nt][1]),
-                                      make_f2(acc[nt][jj][i], acc[nt][jj][i + 1]));
-                    o[0] = lo_of(x);
-                    o[1] = hi_of(x);
-                }
+            for (int i = 0; i < 8; i += 2) {
+                const float *x = &acc[nt][i >> 2][i & 3];
+                const f2 y = fma2(make_f2(o[nt][i], o[nt][i + 1]), make_f2(up[nt][0], up[nt][1]),
+                                  make_f2(x[0], x[1]));
+                o[nt][i] = lo_of(y);
+                o[nt][i + 1] = hi_of(y);
+            }
+            tmem_st8(u.tmem + (c * NT + nt) * 8, o[nt]);
+        }
     }
 }
 
@@ -578,8 +631,14 @@ __device__ __forceinline__ void end_unit(Unit<NT, NG> &u, const Kv4AttnArgs &a, 
 {
     const int g = lane >> 2, t = lane & 3;
     const int kv = at.hr / z.rtiles, r0 = (at.hr - kv * z.rtiles) * NT * 8;
+    tmem_wait_st();
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
+    for (int nt = 0; nt < NT; ++nt) {
+        float o[4][8];
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+            tmem_ld8(u.tmem + (c * NT + nt) * 8, o[c]);
+        tmem_loaded(o);
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
             float l = u.l[nt][e], om[NG];
@@ -607,7 +666,7 @@ __device__ __forceinline__ void end_unit(Unit<NT, NG> &u, const Kv4AttnArgs &a, 
                     float d[4];
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
-                        const float x = u.o[nt][c][j >> 1][e + 2 * (j & 1)] * (j & 1 ? 32.0f : 512.0f);
+                        const float x = o[c][(j >> 1) * 4 + e + 2 * (j & 1)] * (j & 1 ? 32.0f : 512.0f);
                         d[j] = none ? 0.0f : __fmaf_rn(x, back, om[c * NG / 4]) * inv;
                     }
                     if (whole)
@@ -626,13 +685,14 @@ __device__ __forceinline__ void end_unit(Unit<NT, NG> &u, const Kv4AttnArgs &a, 
             }
             __syncwarp();
         }
+    }
 }
 
 // One warp's tiles: `todo` of them from the note `ld` on, every `stride`-th.  Shares: the team's `mine`-th one, units one
 // after the other.  A gang (z.gang): some tiles of one unit, left as a part at the warp's own place in shared memory.
 template <int NT, int NG>
 __device__ __forceinline__ void take_tiles(const Kv4AttnArgs &a, const Sizes &z, uint32_t base, char *own,
-                                           Note ld, uint32_t todo, int stride, uint32_t mine, int lane)
+                                           Note ld, uint32_t todo, int stride, uint32_t mine, uint32_t tmem, int lane)
 {
     constexpr int kStages = stages_of(NT, NG);
     const uint32_t qb = base + kStages * stage_bytes(NG);
@@ -705,6 +765,7 @@ __device__ __forceinline__ void take_tiles(const Kv4AttnArgs &a, const Sizes &z,
         load_tile((uint32_t)s, s);
     // ---- tiles ----------------------------------------------------------------------------------------
     Unit<NT, NG> u;
+    u.tmem = tmem;
     bool fresh = true, from_start = false;
     int get = 0;
 #pragma unroll 1
@@ -761,8 +822,18 @@ __global__ void __launch_bounds__(warps_of(NT, NG) * 32, 1) kv4_attn_kernel(cons
     extern __shared__ __align__(128) char smem[];
     __shared__ uint32_t s_before[kScan];
     __shared__ uint32_t s_warp[kScan / 32];
+    __shared__ uint32_t s_tmem;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     pdl_launch_dependents();
+    // no more than the warps use: blocks of few warps, and those of the next call, may share an SM
+    const uint32_t columns = tmem_columns((blockDim.x / 32 + 3) / 4 * NT * 32);
+    if (warp == 0)
+        tmem_alloc(&s_tmem, columns);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    // a warp reaches 32 lanes, by its number; those with the same lanes have columns next to each other
+    const uint32_t tmem = s_tmem + ((uint32_t)(warp & 3) << 21) + (uint32_t)(warp >> 2) * NT * 32;
     pdl_wait();
     const uint32_t warps = blockDim.x / 32;
     char *own = smem + warp * warp_bytes(NT, NG);
@@ -773,9 +844,7 @@ __global__ void __launch_bounds__(warps_of(NT, NG) * 32, 1) kv4_attn_kernel(cons
     if (!z.gang) {
         total = scan_tiles(a, z, s_before, s_warp);
         share = (total + z.teams - 1) / z.teams;
-        if (total == 0)
-            return;
-        active = (total + share - 1) / share;
+        active = total > 0 ? (total + share - 1) / share : 0;
     }
     const uint32_t gang = z.gang ? z.gang : 1, in_block = warp / gang, i = warp - in_block * gang;
     const uint32_t at_once = warps / gang, all = z.gang ? (uint32_t)a.B * z.team : z.teams * z.team;
@@ -819,7 +888,7 @@ __global__ void __launch_bounds__(warps_of(NT, NG) * 32, 1) kv4_attn_kernel(cons
         ld.tile = z.gang ? (int)i : (int)(start - cum);
         if (z.gang)
             todo = (uint32_t)ld.tiles > i ? ((uint32_t)ld.tiles - i + gang - 1) / gang : 0;
-        take_tiles<NT, NG>(a, z, base, own, ld, todo, (int)gang, mine, lane);
+        take_tiles<NT, NG>(a, z, base, own, ld, todo, (int)gang, mine, tmem, lane);
         if (!z.gang || (gang == 1 && todo > 0))
             continue;  // written, as a whole or as parts
         // ---- a gang's parts; a warp without tiles leaves an empty one ------------------------------------------
@@ -862,6 +931,13 @@ __global__ void __launch_bounds__(warps_of(NT, NG) * 32, 1) kv4_attn_kernel(cons
         }
         meet();  // the parts have been read
     }
+    __syncwarp();
+    tmem_wait_st();
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 0)
+        tmem_free(s_tmem, columns);
 }
 
 // Rows of units that were cut, from their parts; rows of sequences without keys.  z.crew warps (a power of two, up to the
