@@ -14,13 +14,18 @@
 // to 24 query rows of a KV head as the right one, so that few rows waste little: ldmatrix hands out the keys'
 // words, and with a transpose the values' (a 16-bit unit is four columns of a key).
 //
-// Every warp works alone: it copies tiles of 32 keys with cp.async a few ahead into its own part of shared memory, each
-// with a note of where it stands, and carries the running maximum, sum and output of the unit at hand.  A unit is a
-// sequence, a KV head and a tile of query rows.  All sequences' tiles, one after the other, are cut into even shares,
-// and a share is walked by a team of neighbouring warps, one for each KV head and row tile: the heads' rows of a slot are
-// neighbours in memory, and what one warp's access brings besides is in the L2 cache for the others (with shares of
-// single heads instead, 8 contexts of 100K keys in groups of 32 read 2.6 times their bytes: 365 us, and 301 so).
-// A unit that is cut between teams leaves parts (FP32 maximum, sum, output) that a second kernel joins in order.
+// Every warp works alone: it copies tiles of 32 keys with cp.async one or two ahead into its own part of shared memory,
+// each with a note of where it stands, and carries the running maximum and sum of the unit at hand in registers, its
+// output in tensor memory.  A unit is a sequence, a KV head and a tile of query rows.  All sequences' tiles, one after the
+// other, are cut into even shares, and a share is walked by a team of neighbouring warps, one for each KV head and row
+// tile: the heads' rows of a slot are neighbours in memory, and what one warp's access brings besides is in the L2 cache
+// for the others (with shares of single heads instead, at that step, 8 contexts of 100K keys in groups of 32 read 2.6
+// times their bytes: 365 us, and 301 so).  A unit that is cut between teams leaves parts (FP32 maximum, sum, output) that
+// a second kernel joins in order; short ones are taken whole (see the plan at the end of this file).
+//
+// What bounds it: instructions and their latency (8 contexts of 100K keys in groups of 128: 137 us for 720 MB, 0.78 of
+// the measured copy rate, in groups of 32 184 us for 847 MB; 24 rows of 32 sequences in groups of 64 161 us for 371 MB at
+// about 1,100 instructions a tile).
 
 #include <cuda_fp16.h>
 
@@ -50,7 +55,7 @@ __host__ __device__ constexpr int warps_of(int NT, int NG)
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr int kMinExp = -100;
-constexpr double kGangExtra = 24;  // tiles of 8 rows
+constexpr double kGangExtra = 40;  // tiles of 8 rows
 
 struct Sizes {
     int32_t heads, R, rtiles;
@@ -1129,9 +1134,9 @@ Kv4AttnPlan kv4_attn_plan(int32_t B, int32_t q_len, int32_t n_q, int32_t n_kv, i
     p.ctas = p.ctas < kSms ? p.ctas : kSms;
     p.bytes = all * 2 * p.nt * 8 * (128 + 2) * 4;
     // Units whole, by gangs of up to 16 warps that join in shared memory: that saves the second kernel.  An SM takes some
-    // 0.15 us a tile and 8 rows, so a few tiles more than its even share make up for it.  Measured, whole and shares:
-    // one sequence of 500 keys 8.9 and 10.3 us, of 1000 11.4 and 10.1; 8 of 1000 11.7 and 12.4, of 4000 25.4 and 22.8;
-    // 64 of up to 3000 64.7 and 43.5; 128 behind a window of 512 34.0 and 38.3.
+    // 0.1 us a tile and 8 rows, so some tiles more than its even share make up for it.  Measured, whole and shares:
+    // one sequence of 100 keys 6.8 and 10.1 us, of 500 8.9 and 10.3, of 1000 11.1 and 11.2; 8 of 1000 11.4 and 12.7, of
+    // 2000 15.4 and 16.9, of 4000 24.0 and 22.6; 64 of up to 3000 53 and 40; 128 behind a window of 512 30 and 36.
     const double units = (double)B * team;
     const int32_t gang_warps = warps_of(p.nt, 128 / group) == 16 ? 16 : 8;
     const int64_t unit_tiles = (most + kTile - 1) / kTile;

@@ -3,21 +3,28 @@
 // With up to 256 tokens and 8 of 256 experts each, an expert has a handful of tokens: the layer is bound by
 // reading the chosen experts' weights, each once.  Kernels:
 //  1. router: z = x router_w^T in FP32 pairs;
-//  2. the grouped top-k of beam_grouped_topk_fwd: for up to 16 tokens in every block of the next kernel, two
-//     tokens a warp at most, else as that kernel;
+//  2. the grouped top-k of beam_grouped_topk_fwd: for up to 16 tokens in every block of the next kernel (a chain
+//     shorter by a kernel), a warp to a token, else as that kernel;
 //  3. up: g, u and a = silu(g) u for each (token, expert) pair;
-//  4. down: each pair's share of the output, in FP32;
-//  5. the weighted sum of each token's pairs.
+//  4. down: each pair's share of the output, in FP32, by the same code;
+//  5. the weighted sum of each token's pairs, in order.
 //
-// Kernels 3 and 4 give each of a block's eight warps a stream of its own: 16 rows of weights by 64 columns at a
-// time, copied with cp.async some stages ahead into the warp's part of shared memory together with the tokens'
-// rows that they meet (bulk copies of a row's kilobyte, one instruction each, ran at 1.9 TB/s: 1.17 ms for 64 tokens of a
-// tensor-parallel eighth, 0.55 this way).  They are multiplied with m16n8k16 instructions whose left operand is
-// the weights (for up: 8 rows of the gate and the same 8 of the up projection, so that one thread holds g and u of the
-// same place) and whose right one is up to 8 tokens.  Both operands are read 16 bytes a thread: the
-// instruction's columns are the row's in another order, the same for both.  Warps take parts of the columns of
-// the same tile, or where rows are short tiles of their own; their sums meet in shared memory, in order.  An expert
-// with more than 8 tokens is taken in several passes, the later ones out of the L2 cache.
+// An expert's tokens are taken in passes of up to 8 (up) or 4 (down); all passes' rows of weights, one after the other,
+// are cut into equal shares for the blocks, so that a block reads one stretch of memory but where it passes from expert to
+// expert (a block that owned columns of the output instead, for all experts: the layer of 64 tokens of a tensor-parallel
+// eighth 404 us, 358 this way).  Each of a block's eight warps has a stream of its own: 16 rows of weights by 128 columns
+// at a time, copied with cp.async some stages ahead into the warp's part of shared memory together with the tokens'
+// rows that they meet (bulk copies of a row's kilobyte, one instruction each, ran at 1.9 TB/s).  They are multiplied
+// with m16n8k16 instructions whose left operand is the weights (for up: 8 rows of the gate and the same 8 of the up
+// projection, so that one thread holds g and u of the same place) and whose right one is 8 tokens' rows, or for down
+// both BF16 parts of 4 tokens' activations.  Both operands are read 16 bytes a thread: the instruction's columns are the
+// row's in another order, the same for both.  Up: warps take parts of a tile's columns, and their sums meet in shared
+// memory, in order.  Down: a warp's sums go to memory (FP32, one place for each pair, row and part of the columns).
+// Later passes of an expert find its weights in the L2 cache.
+//
+// What bounds it: memory for many tokens (64 of a tensor-parallel eighth, 2.2 GB: 355 us, 0.91 of the measured copy rate;
+// kernels 33, 11, 185, 133 and 6 us one at a time, caches cold), the chain of four kernels for one (84 MB: 33 us; 7, 23, 14
+// and 9 cold, each a few us of launch, first instructions and first loads).
 
 #include "beam_device.cuh"
 #include "beam_f32x2.cuh"
