@@ -1138,19 +1138,23 @@ Kv4AttnPlan kv4_attn_plan(int32_t B, int32_t q_len, int32_t n_q, int32_t n_kv, i
     // one sequence of 100 keys 6.8 and 10.1 us, of 500 8.9 and 10.3, of 1000 11.1 and 11.2; 8 of 1000 11.4 and 12.7, of
     // 2000 15.4 and 16.9, of 4000 24.0 and 22.6; 64 of up to 3000 53 and 40; 128 behind a window of 512 30 and 36.
     const double units = (double)B * team;
-    const int32_t gang_warps = warps_of(p.nt, 128 / group) == 16 ? 16 : 8;
     const int64_t unit_tiles = (most + kTile - 1) / kTile;
-    int32_t gang = gang_warps;
-    while (gang > 1 && units * gang > (double)kSms * gang_warps)
-        gang /= 2;
     const double even = units * (double)unit_tiles / kSms;
-    const double whole = (double)unit_tiles * (double)(int64_t)((units + kSms - 1) / kSms);
-    if (units < 1.0e9 && (whole - even) * p.nt <= kGangExtra) {
+    const double each = (double)(int64_t)((units + kSms - 1) / kSms);  // units that some SM has to take
+    if (units < 1.0e9 && ((double)unit_tiles * each - even) * p.nt <= kGangExtra) {
+        // as many warps to a unit as there are for `each` units at a time, and no more units to a block than that (128
+        // sequences behind a window of 512, 1024 units: 147 blocks of 7 units 29.4 us, 128 of 8 30.2; 100 sequences
+        // 25.7 and 29.6)
+        const int32_t fit = warps_of(p.nt, 128 / group);
+        int32_t gang = fit == 16 ? 16 : 8;
+        while (gang > 1 && each > fit / gang)
+            gang /= 2;
+        const int64_t count = (int64_t)units;
+        const int32_t in_block = each < 1 ? 1 : (each < fit / gang ? (int32_t)each : fit / gang);
+        const int64_t blocks = (count + in_block - 1) / in_block;
         p.gang = gang;
-        p.warps = gang_warps;
-        const double blocks = units * gang / gang_warps;
-        p.ctas = blocks < (double)kSms * 64 ? (int32_t)(blocks + 0.999) : kSms * 64;
-        p.ctas = p.ctas < 1 ? 1 : p.ctas;
+        p.warps = in_block * gang;
+        p.ctas = (int32_t)(blocks < kSms * 64 ? (blocks < 1 ? 1 : blocks) : kSms * 64);
     }
     return p;
 }
