@@ -1146,11 +1146,8 @@ Kv4AttnPlan kv4_attn_plan(int32_t B, int32_t q_len, int32_t n_q, int32_t n_kv, i
         // sequences behind a window of 512, 1024 units: 147 blocks of 7 units 29.4 us, 128 of 8 30.2; 100 sequences
         // 25.7 and 29.6)
         const int32_t fit = warps_of(p.nt, 128 / group);
-        int32_t gang = fit == 16 ? 16 : 8;
-        while (gang > 1 && each > fit / gang)
-            gang /= 2;
+        const int32_t in_block = each < 1 ? 1 : (each < fit ? (int32_t)each : fit), gang = fit / in_block;
         const int64_t count = (int64_t)units;
-        const int32_t in_block = each < 1 ? 1 : (each < fit / gang ? (int32_t)each : fit / gang);
         const int64_t blocks = (count + in_block - 1) / in_block;
         p.gang = gang;
         p.warps = in_block * gang;
