@@ -12,6 +12,7 @@
 #include <cooperative_groups.h>
 
 #include "beam_device.cuh"
+#include "beam_f32x2.cuh"
 #include "draft_kernels.h"
 
 namespace cg = cooperative_groups;
@@ -32,23 +33,31 @@ __device__ __forceinline__ float prob(const void *row, int v)
         return ((const float *)row)[v];
 }
 
-// rint(2^44 p) = 2^22 hi + lo, p limited to [0, 1]; NaN: 0.  A conversion to 64 bits goes through the FP64
-// pipe, which is narrow here: two FP32 additions to 2^23 do it, which leave a whole number in the
-// mantissa's bits, the first one cut off, the second rounded to nearest even.  What the first cuts off is exact, and
-// the lower part's ties are those of the whole.  Both parts come with the bits of 2^23 on top.
+// rint(2^44 p) = 2^22 hi + lo of a pair of values p in [0, 1].  A conversion to 64 bits goes through the FP64 pipe, which
+// is narrow here: two FP32 additions do it, which leave a whole number in the mantissa's bits, x = 2^22 p rounded to hi by
+// an addition to 2^23, what is left of it, exact and at most a half, to lo by one to 1.5 2^23.  2^22 hi is even, so
+// lo's ties are those of the whole.  Both parts come with the constants' bits on top.
 struct Units {
-    int32_t hi, lo;
+    uint32_t hi, lo;
 };
-constexpr int32_t kNone = 0x4b000000;  // either part of 0
+constexpr Units kNone = {0x4b000000u, 0x4b400000u};  // the parts of 0
 
-__device__ __forceinline__ Units units(float p)
+struct Units2 {
+    f2 hi, lo;
+};
+
+__device__ __forceinline__ Units2 units(f2 p)
 {
-    constexpr float k22 = 4194304.0f, k23 = 8388608.0f;
-    const float x = __fmul_rn(fminf(fmaxf(p, 0.0f), 1.0f), k22);
-    const float h = __fadd_rz(x, k23);
-    const float l = __fadd_rn(__fmul_rn(__fsub_rn(x, __fsub_rn(h, k23)), k22), k23);
-    return Units{(int32_t)__float_as_uint(h), (int32_t)__float_as_uint(l)};
+    const f2 k22 = splat(4194304.0f), k23 = splat(8388608.0f);
+    Units2 u;
+    u.hi = fma2(p, k22, k23);
+    const f2 rest = fma2(p, k22, fma2(u.hi, splat(-1.0f), k23));
+    u.lo = fma2(rest, k22, splat(12582912.0f));
+    return u;
 }
+
+// p limited to [0, 1]; NaN: 0.
+__device__ __forceinline__ float limited(float p) { return __saturatef(p); }
 
 __device__ __forceinline__ uint64_t whole(int32_t hi, int32_t lo)
 {
@@ -62,16 +71,37 @@ struct Rows {
     int32_t spike;      // the draft is all on this token (-1: not so)
 };
 
-// Weight of a token, 2^22 hi + lo.
+// Adds the weights of two tokens, P or max(P - Q, 0), to 2^22 hi + lo (all modulo 2^32, without a draft with what kNone
+// adds).  P grows with p: where q > p, P - Q is at most 0, and P less the units of min(p, q) is 0.
 template <bool Draft>
-__device__ __forceinline__ Units weight_of(float p, float q)
+__device__ __forceinline__ void add_weights(uint32_t &hi, uint32_t &lo, float p0, float p1, float q0, float q1)
 {
-    const Units a = units(p), b = Draft ? units(q) : Units{kNone, kNone};
-    Units w{a.hi - b.hi, a.lo - b.lo};
-    // its sign is that of hi unless hi is 0, since |lo| <= 2^22
-    if (Draft && (w.hi < 0 || (w.hi == 0 && w.lo < 0)))
-        w.hi = w.lo = 0;
-    return w;
+    p0 = limited(p0);
+    p1 = limited(p1);
+    const Units2 a = units(make_f2(p0, p1));
+    hi += __float_as_uint(lo_of(a.hi)) + __float_as_uint(hi_of(a.hi));
+    lo += __float_as_uint(lo_of(a.lo)) + __float_as_uint(hi_of(a.lo));
+    if (Draft) {
+        const Units2 b = units(make_f2(fminf(limited(q0), p0), fminf(limited(q1), p1)));
+        hi -= __float_as_uint(lo_of(b.hi)) + __float_as_uint(hi_of(b.hi));
+        lo -= __float_as_uint(lo_of(b.lo)) + __float_as_uint(hi_of(b.lo));
+    }
+}
+
+// What `pairs` calls of it added up.
+template <bool Draft>
+__device__ __forceinline__ uint64_t sum_of(uint32_t hi, uint32_t lo, int pairs)
+{
+    const uint32_t n = Draft ? 0u : 2u * (uint32_t)pairs;
+    return whole((int32_t)(hi - n * kNone.hi), (int32_t)(lo - n * kNone.lo));
+}
+
+template <bool Draft>
+__device__ __forceinline__ uint64_t weight_of(float p, float q)
+{
+    uint32_t hi = 0, lo = 0;
+    add_weights<Draft>(hi, lo, p, 0.0f, q, 0.0f);
+    return sum_of<Draft>(hi, lo, 1);
 }
 
 template <bool BF16>
@@ -79,9 +109,8 @@ __device__ __forceinline__ uint64_t weight_at(const Rows &r, int v)
 {
     if (v == r.spike)
         return 0;
-    const Units w = r.draft ? weight_of<true>(prob<BF16>(r.target, v), prob<BF16>(r.draft, v))
-                            : weight_of<false>(prob<BF16>(r.target, v), 0.0f);
-    return whole(w.hi, w.lo);
+    return r.draft ? weight_of<true>(prob<BF16>(r.target, v), prob<BF16>(r.draft, v))
+                   : weight_of<false>(prob<BF16>(r.target, v), 0.0f);
 }
 
 // 16 bytes of probabilities.
@@ -114,9 +143,7 @@ __device__ __forceinline__ uint64_t sum_stretch(const Rows &r, int v0, int v1, i
         // in front and behind: less than a vector each, a token a lane
         const int edge = lane < 16 ? v0 + lane : first + vecs * kVec + lane - 16;
         if (lane < 16 ? edge < first : edge < v1) {
-            const Units w = weight_of<Draft>(prob<BF16>(r.target, edge),
-                                             Draft ? prob<BF16>(r.draft, edge) : 0.0f);
-            sum += whole(w.hi, w.lo);
+            sum += weight_of<Draft>(prob<BF16>(r.target, edge), Draft ? prob<BF16>(r.draft, edge) : 0.0f);
         }
         const char *tp = (const char *)r.target + (int64_t)first * kSize;
         const char *dp = (const char *)r.draft + (int64_t)first * kSize;
@@ -133,20 +160,17 @@ __device__ __forceinline__ uint64_t sum_stretch(const Rows &r, int v0, int v1, i
                         q[k] = ld_cached(dp + i * 16);
                 }
             }
-            int32_t hi = 0, lo = 0;  // of at most 32 tokens: within 32 bits
+            uint32_t hi = 0, lo = 0;  // of at most 32 tokens: within 31 bits
 #pragma unroll
             for (int k = 0; k < kAhead; ++k) {
                 float x[kVec], y[kVec];
                 unpack<BF16>(x, p[k]);
                 unpack<BF16>(y, q[k]);
 #pragma unroll
-                for (int j = 0; j < kVec; ++j) {
-                    const Units w = weight_of<Draft>(x[j], y[j]);
-                    hi += w.hi;
-                    lo += w.lo;
-                }
+                for (int j = 0; j < kVec; j += 2)
+                    add_weights<Draft>(hi, lo, x[j], x[j + 1], y[j], y[j + 1]);
             }
-            sum += whole(hi, lo);
+            sum += sum_of<Draft>(hi, lo, kAhead * kVec / 2);
         }
         return sum;
     }
@@ -160,14 +184,11 @@ __device__ __forceinline__ uint64_t sum_stretch(const Rows &r, int v0, int v1, i
             p[k] = i < v1 ? prob<BF16>(r.target, i) : 0.0f;
             q[k] = Draft && i < v1 ? prob<BF16>(r.draft, i) : 0.0f;
         }
-        int32_t hi = 0, lo = 0;
+        uint32_t hi = 0, lo = 0;
 #pragma unroll
-        for (int k = 0; k < kAhead; ++k) {
-            const Units w = weight_of<Draft>(p[k], q[k]);
-            hi += w.hi;
-            lo += w.lo;
-        }
-        sum += whole(hi, lo);
+        for (int k = 0; k < kAhead; k += 2)
+            add_weights<Draft>(hi, lo, p[k], p[k + 1], q[k], q[k + 1]);
+        sum += sum_of<Draft>(hi, lo, kAhead / 2);
     }
     return sum;
 }
@@ -208,28 +229,31 @@ __global__ void __launch_bounds__(kThreads, 4) draft_verify_kernel(const VerifyA
     pdl_wait();
 
     // ---- accepted tokens: every warp by itself ----------------------------------------------------
+    // (the draft's length and the last random number are loaded beside the rest, not in front of and behind it)
     const int k = a.k;
+    const float u_last = a.u_sample[b];
     int n = a.len ? a.len[b] : k;
-    n = n < 0 ? 0 : (n > k ? k : n);
     const char *target = (const char *)a.target + b * a.target_seq * (BF16 ? 2 : 4);
     const char *draft = (const char *)a.draft + b * a.draft_seq * (BF16 ? 2 : 4);
     int acc = 0;
-    while (acc < n) {
+    while (true) {
         const int i = acc + lane;
-        bool ok = false;
-        if (i < n) {
+        float p = 0.0f, q = 1.0f, u = 1.0f;  // not accepted
+        if (i < k) {
             const int64_t x = a.tokens[b * k + i];
             if (x >= 0 && x < a.V) {
-                const float p = prob<BF16>(target + i * a.target_pos * (BF16 ? 2 : 4), (int)x);
-                const float q =
-                    a.draft ? prob<BF16>(draft + i * a.draft_pos * (BF16 ? 2 : 4), (int)x) : 1.0f;
-                // the FP32 factors' product is exact in 64 bits
-                ok = (double)a.u_accept[b * k + i] * (double)q < (double)p;
+                p = prob<BF16>(target + i * a.target_pos * (BF16 ? 2 : 4), (int)x);
+                if (a.draft)
+                    q = prob<BF16>(draft + i * a.draft_pos * (BF16 ? 2 : 4), (int)x);
+                u = a.u_accept[b * k + i];
             }
         }
+        n = n < 0 ? 0 : (n > k ? k : n);
+        // the FP32 factors' product is exact in 64 bits
+        const bool ok = i < n && (double)u * (double)q < (double)p;
         const uint32_t no = ~__ballot_sync(0xffffffffu, ok);
         acc += no ? __ffs((int)no) - 1 : 32;
-        if (no)
+        if (no || acc >= n)
             break;
     }
     Rows r;
@@ -256,8 +280,7 @@ __global__ void __launch_bounds__(kThreads, 4) draft_verify_kernel(const VerifyA
                                           : sum_stretch<BF16, false>(r, v0, v1, lane));
         if (lane == 0) {
             if (r.spike >= v0 && r.spike < v1) {
-                const Units x = weight_of<false>(prob<BF16>(r.target, r.spike), 0.0f);
-                sum -= whole(x.hi, x.lo);
+                sum -= weight_of<false>(prob<BF16>(r.target, r.spike), 0.0f);
             }
             s_w[again][warp] = sum;
         }
@@ -280,8 +303,7 @@ __global__ void __launch_bounds__(kThreads, 4) draft_verify_kernel(const VerifyA
     }
     cluster.sync();  // all have read their peers' shared memory: the others need not stay for the search
     {
-        float u = a.u_sample[b];
-        u = fminf(fmaxf(u, 0.0f), 0.99999994f);  // NaN: 0
+        const float u = fminf(fmaxf(u_last, 0.0f), 0.99999994f);  // NaN: 0
         // floor(floor(2^24 u) S / 2^24)
         const uint64_t border = __umul64hi((uint64_t)(u * 16777216.0f) << 40, total);
         int at = -1;
@@ -306,8 +328,21 @@ __global__ void __launch_bounds__(kThreads, 4) draft_verify_kernel(const VerifyA
             const int few = (each + kThreads - 1) / kThreads;
             const int t0 = f0 + threadIdx.x * few, t1 = min(t0 + few, f1);
             uint64_t own = 0;
-            for (int v = t0; v < t1; ++v)
-                own += weight_at<BF16>(r, v);
+#pragma unroll 1
+            for (int v = t0; v < t1; v += 8) {
+                float p[8], q[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const bool on = v + i < t1 && v + i != r.spike;
+                    p[i] = on ? prob<BF16>(r.target, v + i) : 0.0f;
+                    q[i] = on && r.draft ? prob<BF16>(r.draft, v + i) : 0.0f;
+                }
+                uint32_t hi = 0, lo = 0;
+#pragma unroll
+                for (int i = 0; i < 8; i += 2)
+                    add_weights<true>(hi, lo, p[i], p[i + 1], q[i], q[i + 1]);
+                own += sum_of<true>(hi, lo, 4);
+            }
             uint64_t all;
             uint64_t run = warp_below64(own, lane, all);
             if (lane == 0)
@@ -344,12 +379,14 @@ __global__ void __launch_bounds__(kThreads, 4) draft_verify_kernel(const VerifyA
 template <bool BF16>
 cudaError_t launch(const VerifyArgs &a, cudaStream_t stream)
 {
-    // Blocks of a sequence: 8 while each warp's stretch has 128 tokens, and while all blocks have room at a time
-    // (4 an SM; 128 rows of 160,000: 40 us with 8, 37 with 4).
+    // Blocks of a sequence: 8 while each warp's stretch has 128 tokens, and fewer where not all blocks have room at a time
+    // (4 an SM; 128 rows of 160,000: 35.8 us with 8, 34.9 with 4, 53 with 2), but then no block gets more than 16,000
+    // tokens (400 of 160,000: 73 us with 4, 105 with 1; 1000 of 32,000: 46 us with 2, 57 with 4, 49 with 1; of 8000: 20
+    // with 1, 44 with 4).
     int ranks = kMaxCluster;
     while (ranks > 1 && a.V < (int64_t)ranks * kWarps * 128)
         ranks /= 2;
-    while (ranks > 1 && a.B * ranks > 152 * 4)
+    while (ranks > 1 && a.B * ranks > 152 * 4 && (ranks == kMaxCluster || a.V < (int64_t)ranks * 16000))
         ranks /= 2;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(a.B * ranks));

@@ -3,7 +3,7 @@
 // A group of 32, 64 or 128 columns is held as codes 0..15 on the line minimum + scale * code.  Half a warp
 // takes one row of a KV head: each lane 8 columns (16 bytes in, 4 bytes of codes out), the group's smallest
 // and largest value by shuffles of a BF16 pair (minimum, -maximum) among its 4, 8 or 16 lanes.  For a prefill
-// chunk the kernel is bound by its instructions rather than by memory (16,384 tokens of 8 heads 21 us, 67 MB read and 37
+// chunk the kernel is bound by its instructions rather than by memory (16,384 tokens of 8 heads 21 us, 67 MB read and 19
 // written in 13 at the measured copy rate), so a half-warp's place in a token is worked out once, codes are rounded with
 // packed FP32 additions, whose bits are packed with whole-number multiply-adds.
 

@@ -62,6 +62,12 @@ def test_large_vocabularies():
         check(make(2, 2, V, seed=V, sharp=3.0))
 
 
+@pytest.mark.parametrize("V", [300, 40_000, 70_000])
+def test_more_blocks_than_have_room_at_a_time(V):
+    lib()
+    check(make(160, 1, V, seed=V, sharp=3.0))
+
+
 def test_more_tokens_than_a_warp_has_lanes():
     # all accepted, or the first refusal at each place around a warp's end
     lib()
