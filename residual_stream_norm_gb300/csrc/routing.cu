@@ -36,7 +36,7 @@
 namespace beam {
 namespace {
 
-constexpr int kRouteThreads = 256;      // 8 tokens per CTA pass
+constexpr int kRouteThreads = 256;      // up to 8 tokens per CTA pass
 
 // At least 3 CTAs per SM: more warps to cover the ranking's dependent-instruction latency.  The kernel takes 63
 // registers, so four fit: 37.7 us at T = 16384, 2.6 us for one token (51.6 and 4.4 with index pairs in the group
@@ -56,8 +56,9 @@ __global__ void __launch_bounds__(kRouteThreads, 3)
         bias[4] = b1.x, bias[5] = b1.y, bias[6] = b1.z, bias[7] = b1.w;
     }
     pdl_wait();
-    const int64_t warps = (int64_t)gridDim.x * (kRouteThreads / 32);
-    for (int64_t t = (int64_t)blockIdx.x * (kRouteThreads / 32) + warp; t < a.T; t += warps) {
+    const int per = blockDim.x / 32;
+    const int64_t warps = (int64_t)gridDim.x * per;
+    for (int64_t t = (int64_t)blockIdx.x * per + warp; t < a.T; t += warps) {
         const float *zp = a.logits + t * kExperts + e0;
         const float4 z0 = ld_stream_f4(zp), z1 = ld_stream_f4(zp + 4);
         const float z[kPerLane] = {z0.x, z0.y, z0.z, z0.w, z1.x, z1.y, z1.z, z1.w};
@@ -74,10 +75,14 @@ __global__ void __launch_bounds__(kRouteThreads, 3)
 
 cudaError_t launch_grouped_topk(const RouteArgs &a, cudaStream_t stream)
 {
-    const int64_t ctas = (a.T + kRouteThreads / 32 - 1) / (kRouteThreads / 32);
+    // few tokens are spread over the SMs, a warp for each of their schedulers first (1024 tokens 6.9 us, 13.0 with 8 warps
+    // to a block)
+    const int64_t even = (a.T + 4 * 152 - 1) / (4 * 152);
+    const int per = even < 1 ? 1 : (even < kRouteThreads / 32 ? (int)even : kRouteThreads / 32);
+    const int64_t ctas = (a.T + per - 1) / per;
     const unsigned grid = (unsigned)(ctas < (1 << 20) ? ctas : (1 << 20));
     const cudaError_t e =
-        launch_pdl(grouped_topk_kernel, dim3(grid), dim3(kRouteThreads), 0, stream, a);
+        launch_pdl(grouped_topk_kernel, dim3(grid), dim3(32 * per), 0, stream, a);
     return e != cudaSuccess ? e : cudaGetLastError();
 }
 
