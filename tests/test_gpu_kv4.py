@@ -375,6 +375,28 @@ def test_no_table_at_all():
     check(c)
 
 
+def test_calls_of_all_sizes_one_behind_the_other():
+    # blocks of 1 to 16 warps, which take tensor memory while blocks of the call before may still hold theirs
+    lib()
+    cs = [make(170, 3, 64, 8, [64] * 170, 64, seed=30, S=400), make(1, 1, 8, 8, [9], 128, seed=31),
+          make(40, 3, 64, 8, [300] * 40, 32, seed=32, S=900), make(2, 2, 12, 2, [2000, 50], 64, seed=33),
+          make(70, 1, 12, 2, [90] * 70, 128, seed=34, S=700), make(1, 4, 6, 1, [3], 32, seed=35)]
+    want = [run(c)[0] for c in cs]
+    names = ("q", "k_cache", "v_cache", "k_scales", "v_scales", "table", "lens")
+    ds = [{x: c[x].cuda() for x in names} for c in cs]
+    n = max(rsn.beam_attn_kv4_workspace(c["table"].shape[0], c["q_len"], c["q"].shape[1], c["k_cache"].shape[1],
+                                        c["table"].shape[1]) for c in cs)
+    ws = torch.empty(n, dtype=torch.uint8, device="cuda")
+    outs = [torch.zeros_like(d["q"]) for d in ds]
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for c, d, o in zip(cs, ds, outs):
+            rsn.beam_attn_kv4_fwd(o, d["q"], d["k_cache"], d["v_cache"], d["k_scales"], d["v_scales"], d["table"],
+                                  d["lens"], ws, group=c["group"])
+    torch.cuda.synchronize()
+    assert all(torch.equal(o.cpu(), w) for o, w in zip(outs, want))
+
+
 def test_two_streams_at_once():
     # calls that run side by side, each with its own workspace and output
     lib()
