@@ -9,9 +9,10 @@
  * is launched, calls asynchronous on `stream`, programmatic dependent launch.  Model parameters
  * (4-bit weights, scales, zeros) may be read before the preceding kernel of the stream has ended;
  * everything else is read, and every output written, only after it.  Calls on different streams
- * need workspaces of their own.  Waits inside the kernels are bounded; beam_device_faults() also
- * reports one that ran out, or a block that found its shared memory not aligned as its copies need,
- * after which the call's outputs are not to be used.
+ * need workspaces of their own.  Waits inside the kernels are bounded, but for attention's for tensor
+ * memory (asked for behind the earlier kernels of the stream, and never held while a kernel waits for
+ * another); beam_device_faults() also reports one that ran out, or a block that found its shared
+ * memory not aligned as its copies need, after which the call's outputs are not to be used.
  */
 #ifndef BEAM_DECODE_H
 #define BEAM_DECODE_H

@@ -9,8 +9,9 @@
  * before anything is launched, calls asynchronous on `stream`, programmatic dependent launch.  The
  * router's weights and bias may be read before the preceding kernel of the stream has ended; everything else is
  * read, and every output written, only after it.  Calls on different streams need workspaces of their
- * own; a workspace's contents need not be kept or cleared between calls.  No kernel here waits for anything but
- * its own block's or cluster's threads and copies.
+ * own; a workspace's contents need not be kept or cleared between calls.  A kernel here waits for its own block's or
+ * cluster's threads and copies, and attention's, behind the earlier kernels of its stream, for tensor memory, until other
+ * streams' kernels on its SM give theirs back.  None holds tensor memory while it waits for another kernel.
  */
 #ifndef BEAM_DRAFT_H
 #define BEAM_DRAFT_H

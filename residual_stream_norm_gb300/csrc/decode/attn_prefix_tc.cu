@@ -218,6 +218,9 @@ __global__ void __launch_bounds__(TcConfig<FP8, SPLIT>::kThreads, 1)
         }
         fence_mbar_init();
     }
+    // Tensor memory is asked for behind the kernels before, and the next one may start only when every block here has it:
+    // a block that held columns while it waits for another kernel's end could keep that kernel's blocks from theirs.
+    pdl_wait();
     if (warp == 8)
         tmem_alloc_all(s_tmem);
     tc_fence_before();
@@ -225,7 +228,6 @@ __global__ void __launch_bounds__(TcConfig<FP8, SPLIT>::kThreads, 1)
     tc_fence_after();
     const uint32_t tmem = *s_tmem;
     pdl_launch_dependents();
-    pdl_wait();
 
     if (warp < 8 && !*s_fail) {
         // ---- softmax: a row a thread -------------------------------------------------------------

@@ -829,9 +829,11 @@ __global__ void __launch_bounds__(warps_of(NT, NG) * 32, 1) kv4_attn_kernel(cons
     __shared__ uint32_t s_warp[kScan / 32];
     __shared__ uint32_t s_tmem;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    // No more than the warps use: blocks of few warps, and those of the next call, may share an SM.  The next kernel may
-    // start only when every block here has its columns: one of its blocks that took them first would wait for this
-    // kernel's end, and this kernel for the columns.
+    // Tensor memory is asked for behind the kernels before: a block that held columns while it waits for their end could
+    // keep one of their blocks from its own, and both would wait for ever.  The next kernel may start only when every
+    // block here has its columns, for the same reason.  No more than the warps use, since blocks of few warps, and those
+    // of the next call, may share an SM.
+    pdl_wait();
     const uint32_t columns = tmem_columns((blockDim.x / 32 + 3) / 4 * NT * 32);
     if (warp == 0)
         tmem_alloc(&s_tmem, columns);
@@ -841,7 +843,6 @@ __global__ void __launch_bounds__(warps_of(NT, NG) * 32, 1) kv4_attn_kernel(cons
     // a warp reaches 32 lanes, by its number; those with the same lanes have columns next to each other
     const uint32_t tmem = s_tmem + ((uint32_t)(warp & 3) << 21) + (uint32_t)(warp >> 2) * NT * 32;
     pdl_launch_dependents();
-    pdl_wait();
     const uint32_t warps = blockDim.x / 32;
     char *own = smem + warp * warp_bytes(NT, NG);
     const uint32_t base = (uint32_t)__cvta_generic_to_shared(own);
