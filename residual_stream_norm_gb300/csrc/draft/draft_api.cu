@@ -27,10 +27,11 @@ int check_attn_sizes(int32_t B, int32_t q_len, int32_t n_q, int32_t n_kv, int64_
     if (B < 0 || q_len < 1 || n_kv < 1 || n_q < n_kv || n_q > kMaxHeads || n_q % n_kv != 0 ||
         width < 0 || width >= kMost / 2 || window < 0 || n_sink < 0)
         return BEAM_ERR_INVALID_ARG;
-    if ((int64_t)B * q_len >= kMost || (int64_t)B * q_len * n_q >= kMost)
-        return BEAM_ERR_INVALID_ARG;
-    // the kernel counts tiles of keys in 31 bits
-    if (beam::kv4_attn_plan(B, q_len, n_q, n_kv, width, window, n_sink, 128).most_tiles >= (double)kMost)
+    if (B == 0)
+        return BEAM_OK;  // nothing is planned: the bounds below, which are the plan's, hold for any other sizes
+    // (and the kernel counts tiles of 32 keys in 31 bits)
+    if ((int64_t)B * q_len >= kMost || (int64_t)B * q_len * n_q >= kMost ||
+        (width + 31) / 32 * B >= kMost)
         return BEAM_ERR_INVALID_ARG;
     return BEAM_OK;
 }

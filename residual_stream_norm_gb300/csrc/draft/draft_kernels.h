@@ -45,7 +45,7 @@ struct Kv4AttnArgs {
     char *workspace;
 };
 
-// How one call is divided; a function of its sizes alone.
+// How one call is divided; a function of its sizes alone, for B * q_len * n_q < 2^31 and B > 0.
 struct Kv4AttnPlan {
     int32_t heads;     // query heads of a KV head
     int32_t R;         // rows of a sequence and KV head: q_len * heads
@@ -54,7 +54,6 @@ struct Kv4AttnPlan {
     int32_t teams;     // of n_kv * rtiles warps
     int32_t ctas, warps;  // of a block
     int32_t gang;      // 0: even shares of all keys; else the warps that take a unit whole
-    double most_tiles;  // if every sequence fills its table
     int64_t bytes;     // workspace
 };
 

@@ -1116,10 +1116,9 @@ Kv4AttnPlan kv4_attn_plan(int32_t B, int32_t q_len, int32_t n_q, int32_t n_kv, i
     Kv4AttnPlan p{};
     p.heads = n_q / n_kv;
     p.R = q_len * p.heads;
-    const int32_t t8 = (p.R + 7) / 8;
-    p.nt = t8 < 3 ? t8 : 3;
-    p.rtiles = (t8 + p.nt - 1) / p.nt;
-    p.most_tiles = (double)((width + kTile - 1) / kTile) * B;
+    const int64_t t8 = ((int64_t)p.R + 7) / 8;  // R: up to 2^31 - 1
+    p.nt = t8 < 3 ? (int32_t)t8 : 3;
+    p.rtiles = (int32_t)((t8 + p.nt - 1) / p.nt);
     // as many teams as all SMs' warps make, but no more than there can be tiles
     int64_t most = width;
     if (window > 0 && window < width && n_sink < width && window + q_len + n_sink < width)

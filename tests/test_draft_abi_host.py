@@ -3,6 +3,8 @@ argument is rejected before any CUDA call, so fake device addresses are never de
 import ctypes
 import os
 import re
+import subprocess
+import sys
 
 import pytest
 import torch
@@ -97,6 +99,30 @@ def test_attention_workspace(lib):
         assert f(8, 1, 48, 8, 5000, window, n_sink) == n
     with pytest.raises(rsn.BeamError):
         rsn.beam_attn_kv4_workspace(1, 0, 48, 8, 10)
+
+
+PLANS = """
+import sys
+import residual_stream_norm_gb300 as rsn
+lib = rsn.lib()
+f = lib.beam_attn_kv4_workspace
+# no sequences: any number of query rows, with and without a launch to plan
+for q_len, n_q in ((4194304, 1024), (2147483647, 1024), (1 << 30, 1)):
+    assert f(0, q_len, n_q, 1, 100, 0, 0) == 0
+    assert lib.beam_attn_kv4_fwd(None, 0, None, None, 0, None, None, None, None, 0, 128, None, 0, 100, None, 0,
+                                 q_len, n_q, 1, 128, 0.1, 0, 0, None, 0, None) == 0
+# the most query rows: parts of 24 rows, 130 floats a row, two a unit
+rows = 2147483647
+assert f(1, rows, 1, 1, 100, 0, 0) == -(-rows // 24) * 2 * 24 * 130 * 4
+assert f(1, rows - 7, 1, 1, 100, 0, 0) == -(-(rows - 7) // 24) * 2 * 24 * 130 * 4
+assert f(2, rows, 1, 1, 100, 0, 0) == -1 and f(1, 1 << 21, 1024, 1, 100, 0, 0) == -1
+"""
+
+
+def test_attention_plans_of_the_most_query_rows(lib):
+    # in a process of its own, which a division by a row count that wrapped to zero would end
+    r = subprocess.run([sys.executable, "-c", PLANS], cwd=ROOT, capture_output=True, text=True)
+    assert r.returncode == 0, (r.returncode, r.stderr[-500:])
 
 
 def moe(lib, out=A, out_stride=512, ids=A, w=A, x=A, x_stride=512, rw=A, rb=A, w13=A, w2=A, first=0,
