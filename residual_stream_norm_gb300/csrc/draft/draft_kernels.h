@@ -7,6 +7,7 @@
 #include <cuda_runtime.h>
 
 #include "beam_kernels.h"
+#include "draft_plan.h"
 
 namespace beam {
 
@@ -45,20 +46,6 @@ struct Kv4AttnArgs {
     char *workspace;
 };
 
-// How one call is divided; a function of its sizes alone, for B * q_len * n_q < 2^31 and B > 0.
-struct Kv4AttnPlan {
-    int32_t heads;     // query heads of a KV head
-    int32_t R;         // rows of a sequence and KV head: q_len * heads
-    int32_t nt;        // 8-row tiles of a unit: 1, 2 or 3
-    int32_t rtiles;    // units of a sequence and KV head
-    int32_t teams;     // of n_kv * rtiles warps
-    int32_t ctas, warps;  // of a block
-    int32_t gang;      // 0: even shares of all keys; else the warps that take a unit whole
-    int64_t bytes;     // workspace
-};
-
-Kv4AttnPlan kv4_attn_plan(int32_t B, int32_t q_len, int32_t n_q, int32_t n_kv, int64_t width,
-                          int64_t window, int64_t n_sink, int32_t group);
 cudaError_t launch_kv4_attn(const Kv4AttnArgs &a, const Kv4AttnPlan &p, cudaStream_t stream);
 
 struct MoeArgs {

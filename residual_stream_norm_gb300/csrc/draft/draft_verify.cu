@@ -20,9 +20,8 @@ namespace cg = cooperative_groups;
 namespace beam {
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kWarps = kThreads / 32;
-constexpr int kMaxCluster = 8;
+constexpr int kWarps = kVerifyWarps;
+constexpr int kThreads = kWarps * 32;
 
 template <bool BF16>
 __device__ __forceinline__ float prob(const void *row, int v)
@@ -379,15 +378,7 @@ __global__ void __launch_bounds__(kThreads, 4) draft_verify_kernel(const VerifyA
 template <bool BF16>
 cudaError_t launch(const VerifyArgs &a, cudaStream_t stream)
 {
-    // Blocks of a sequence: 8 while each warp's stretch has 128 tokens, and fewer where not all blocks have room at a time
-    // (4 an SM; 128 rows of 160,000: 35.8 us with 8, 34.9 with 4, 53 with 2), but then no block gets more than 16,000
-    // tokens (400 of 160,000: 73 us with 4, 105 with 1; 1000 of 32,000: 46 us with 2, 57 with 4, 49 with 1; of 8000: 20
-    // with 1, 44 with 4).
-    int ranks = kMaxCluster;
-    while (ranks > 1 && a.V < (int64_t)ranks * kWarps * 128)
-        ranks /= 2;
-    while (ranks > 1 && a.B * ranks > 152 * 4 && (ranks == kMaxCluster || a.V < (int64_t)ranks * 16000))
-        ranks /= 2;
+    const int ranks = verify_ranks(a.B, a.V);
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(a.B * ranks));
     cfg.blockDim = dim3(kThreads);

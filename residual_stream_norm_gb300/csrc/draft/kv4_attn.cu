@@ -21,7 +21,7 @@
 // tile: the heads' rows of a slot are neighbours in memory, and what one warp's access brings besides is in the L2 cache
 // for the others (with shares of single heads instead, at that step, 8 contexts of 100K keys in groups of 32 read 2.6
 // times their bytes: 365 us, and 301 so).  A unit that is cut between teams leaves parts (FP32 maximum, sum, output) that
-// a second kernel joins in order; short ones are taken whole (see the plan at the end of this file).
+// a second kernel joins in order; short ones are taken whole (see draft_plan.h).
 //
 // What bounds it: instructions and their latency (8 contexts of 100K keys in groups of 128: 137 us for 720 MB, 0.78 of
 // the measured copy rate, in groups of 32 184 us for 847 MB; 24 rows of 32 sequences in groups of 64 161 us for 371 MB at
@@ -39,23 +39,14 @@
 namespace beam {
 namespace {
 
-constexpr int kSms = 152;
-constexpr int kScan = 256;  // threads that count tiles
-constexpr int kTile = 32;  // keys
+using kv4::kScan;
+using kv4::kSms;
+using kv4::kTile;
+using kv4::warps_of;
 
-// Warps of a block, as the registers of NT 8-row tiles allow without spilling more than a few (128 or 168 a thread).
-// Between tiles a unit's output is kept in tensor memory, 32 columns of a warp's own lanes for each row tile: with the
-// outputs in registers 8 contexts of 100K keys (NT = 1, groups of 32) took 197 us with 12 warps, 184 so with 16; 32
-// sequences of up to 20K keys in groups of 64 with NT = 2 145 us with 12 warps, 119 so with 12 (and with 16), with NT = 3
-// 180 with 8, 160 so with 12.  (NT = 1 with 20 warps, which spill: groups of 128 152 us, with 16 137.)
-__host__ __device__ constexpr int warps_of(int NT, int NG)
-{
-    return NT == 1 || (NT == 2 && NG == 1) ? 16 : 12;
-}
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr int kMinExp = -100;
-constexpr double kGangExtra = 40;  // tiles of 8 rows
 
 struct Sizes {
     int32_t heads, R, rtiles;
@@ -1109,54 +1100,6 @@ cudaError_t launch_groups(const Kv4AttnArgs &a, const Kv4AttnPlan &p, cudaStream
 }
 
 }  // namespace
-
-Kv4AttnPlan kv4_attn_plan(int32_t B, int32_t q_len, int32_t n_q, int32_t n_kv, int64_t width,
-                          int64_t window, int64_t n_sink, int32_t group)
-{
-    Kv4AttnPlan p{};
-    p.heads = n_q / n_kv;
-    p.R = q_len * p.heads;
-    const int64_t t8 = ((int64_t)p.R + 7) / 8;  // R: up to 2^31 - 1
-    p.nt = t8 < 3 ? (int32_t)t8 : 3;
-    p.rtiles = (int32_t)((t8 + p.nt - 1) / p.nt);
-    // as many teams as all SMs' warps make, but no more than there can be tiles
-    int64_t most = width;
-    if (window > 0 && window < width && n_sink < width && window + q_len + n_sink < width)
-        most = window + q_len + n_sink;
-    const double tiles = (double)((most + kTile - 1) / kTile) * B;
-    const int32_t team = n_kv * p.rtiles, warps = kSms * warps_of(p.nt, 128 / group);
-    p.teams = team < warps ? warps / team : 1;
-    p.teams = tiles < p.teams ? (int32_t)(tiles < 1 ? 1 : tiles) : p.teams;
-    // few warps are spread over the SMs, but at least those that count the tiles stay together
-    const int64_t all = (int64_t)p.teams * team;
-    p.warps = (int32_t)((all + kSms - 1) / kSms);
-    p.warps = p.warps < kScan / 32 ? kScan / 32 : p.warps;
-    p.warps = p.warps < warps / kSms ? p.warps : warps / kSms;
-    p.ctas = (int32_t)((all + p.warps - 1) / p.warps);
-    p.ctas = p.ctas < kSms ? p.ctas : kSms;
-    p.bytes = all * 2 * p.nt * 8 * (128 + 2) * 4;
-    // Units whole, by gangs of up to 16 warps that join in shared memory: that saves the second kernel.  An SM takes some
-    // 0.1 us a tile and 8 rows, so some tiles more than its even share make up for it.  Measured, whole and shares:
-    // one sequence of 100 keys 6.8 and 10.1 us, of 500 8.9 and 10.3, of 1000 11.1 and 11.2; 8 of 1000 11.4 and 12.7, of
-    // 2000 15.4 and 16.9, of 4000 24.0 and 22.6; 64 of up to 3000 53 and 40; 128 behind a window of 512 30 and 36.
-    const double units = (double)B * team;
-    const int64_t unit_tiles = (most + kTile - 1) / kTile;
-    const double even = units * (double)unit_tiles / kSms;
-    const double each = (double)(int64_t)((units + kSms - 1) / kSms);  // units that some SM has to take
-    if (units < 1.0e9 && ((double)unit_tiles * each - even) * p.nt <= kGangExtra) {
-        // as many warps to a unit as there are for `each` units at a time, and no more units to a block than that (128
-        // sequences behind a window of 512, 1024 units: 147 blocks of 7 units 29.4 us, 128 of 8 30.2; 100 sequences
-        // 25.7 and 29.6)
-        const int32_t fit = warps_of(p.nt, 128 / group);
-        const int32_t in_block = each < 1 ? 1 : (each < fit ? (int32_t)each : fit), gang = fit / in_block;
-        const int64_t count = (int64_t)units;
-        const int64_t blocks = (count + in_block - 1) / in_block;
-        p.gang = gang;
-        p.warps = in_block * gang;
-        p.ctas = (int32_t)(blocks < kSms * 64 ? (blocks < 1 ? 1 : blocks) : kSms * 64);
-    }
-    return p;
-}
 
 cudaError_t launch_kv4_attn(const Kv4AttnArgs &a, const Kv4AttnPlan &p, cudaStream_t stream)
 {
