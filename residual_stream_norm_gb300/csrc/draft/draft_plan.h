@@ -73,24 +73,36 @@ inline Kv4AttnPlan kv4_attn_plan(int32_t B, int32_t q_len, int32_t n_q, int32_t 
     p.ctas = (int32_t)((all + p.warps - 1) / p.warps);
     p.ctas = p.ctas < kSms ? p.ctas : kSms;
     p.bytes = all * 2 * p.nt * 8 * (128 + 2) * 4;
-    // Units whole, by gangs of up to 16 warps that join in shared memory: that saves the second kernel.  An SM takes some
-    // 0.1 us a tile and 8 rows, so some tiles more than its even share make up for it.  Measured, whole and shares:
-    // one sequence of 100 keys 6.8 and 10.1 us, of 500 8.9 and 10.3, of 1000 11.1 and 11.2; 8 of 1000 11.4 and 12.7, of
-    // 2000 15.4 and 16.9, of 4000 24.0 and 22.6; 64 of up to 3000 53 and 40; 128 behind a window of 512 30 and 36.
+    // Units whole, by gangs of up to 16 warps that join in shared memory, save the second kernel.  Two things have to hold.
+    // No SM gets much more than its even share where all sequences are as long as they can be: it takes some 0.1 us a tile
+    // and 8 rows.  And the longest unit is short, because a table says how long sequences may be, not how long they are:
+    // one long sequence among short ones is left to its own gangs, at some 0.1 us a tile for each unit that a block has
+    // in hand.  A window makes most units equally long, so more is allowed behind one.  Measured, whole and shares, us,
+    // for tables that are filled; filled to a random length each; one of them filled and the others to a hundredth:
+    //   19 sequences, 2000 keys   17.5 23.2; 15.9 20.3; 15.4 15.5     4000   27.4 31.8; 25.0 25.3; 22.2 21.0
+    //                 8000        42.8 46.3; -; 36.2 30.8             100K   -; -; 354 59
+    //   57 sequences, 1000 keys   23.3 28.1; 20.1 24.0; 19.7 15.1     2000   34.4 39.8; 32.2 30.0; 30.4 19.1
+    //   128 sequences, 500 keys   26.3 33.5; 23.2 29.3; 22.6 13.2     1000   40.3 46.7; 38.9 36.4; 36.5 16.0
+    //   1000 sequences, 200 keys  85.8 91.3; 60.3 76.1; 31.0 42.4
+    //   19 of 4 tokens, 2000 keys 29.4 38.7; 29.8 34.3; 27.1 23.5     4000   44.7 52.9; 47.0 41.7; 40.8 32.7
+    // and of one sequence of 100 keys 6.8 10.1, of 500 8.9 10.3, of 1000 11.1 11.2; 8 of 1000 11.4 12.7, of 2000 15.4
+    // 16.9, of 4000 24.0 22.6; behind a window of 512 128 sequences 29.6 35.8, of 1024 300 sequences 72 89, of 2048 50
+    // sequences 34.9 39.5, 100 62 57, 128 72.8 67.0.
     const double units = (double)B * team;
     const int64_t unit_tiles = (most + kTile - 1) / kTile;
     const double even = units * (double)unit_tiles / kSms;
     const double each = (double)(int64_t)((units + kSms - 1) / kSms);  // units that some SM has to take
-    if (units < 1.0e9 && ((double)unit_tiles * each - even) * p.nt <= kGangExtra) {
+    const int32_t fit = warps_of(p.nt, 128 / group);
+    const int32_t in_block = each < 1 ? 1 : (each < fit ? (int32_t)each : fit);
+    const bool windowed = most < width;
+    const bool brief = unit_tiles <= (windowed ? 40 : 17) || unit_tiles * in_block <= (windowed ? 200 : 128);
+    if (brief && units < 1.0e9 && ((double)unit_tiles * each - even) * p.nt <= kGangExtra) {
         // as many warps to a unit as there are for `each` units at a time, and no more units to a block than that (128
         // sequences behind a window of 512, 1024 units: 147 blocks of 7 units 29.4 us, 128 of 8 30.2; 100 sequences
         // 25.7 and 29.6)
-        const int32_t fit = warps_of(p.nt, 128 / group);
-        const int32_t in_block = each < 1 ? 1 : (each < fit ? (int32_t)each : fit), gang = fit / in_block;
-        const int64_t count = (int64_t)units;
-        const int64_t blocks = (count + in_block - 1) / in_block;
-        p.gang = gang;
-        p.warps = in_block * gang;
+        const int64_t count = (int64_t)units, blocks = (count + in_block - 1) / in_block;
+        p.gang = fit / in_block;
+        p.warps = in_block * p.gang;
         p.ctas = (int32_t)(blocks < kSms * 64 ? (blocks < 1 ? 1 : blocks) : kSms * 64);
     }
     return p;

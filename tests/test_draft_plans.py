@@ -62,6 +62,26 @@ def test_attention_plans_hold_together(so):
         assert p["bytes"] == p["teams"] * n_kv * p["rtiles"] * 2 * p["nt"] * 8 * 130 * 4, args
 
 
+@pytest.mark.parametrize("group", [32, 64, 128])
+def test_one_long_sequence_is_shared_out(so, group):
+    # however evenly the units divide over the SMs: a unit that its gang alone would take for long is cut
+    for n_kv, n_q in ((1, 6), (2, 12), (8, 48), (8, 8)):
+        for B in (1, 2, 8, 16, 17, 18, 19, 37, 38, 57, 76, 95, 114, 128, 150, 152, 190, 304, 700):
+            for q_len in (1, 2, 4):
+                for width in (5000, 8100, 12_160, 24_320, 100_000, 1 << 20):
+                    p = plan(so, B=B, q_len=q_len, n_q=n_q, n_kv=n_kv, width=width, group=group)
+                    assert p["gang"] == 0, (B, q_len, n_q, width)
+                p = plan(so, B=B, q_len=q_len, n_q=n_q, n_kv=n_kv, width=100_000, window=8000, group=group)
+                assert p["gang"] == 0
+
+
+def test_short_sequences_are_taken_whole(so):
+    for B, q_len, width, window in ((1, 1, 500, 0), (8, 1, 2000, 0), (19, 1, 4000, 0), (19, 4, 2000, 0), (128, 1, 500, 0),
+                                    (1000, 1, 200, 0), (128, 1, 8192, 512), (50, 1, 8192, 512), (300, 1, 8192, 1024),
+                                    (128, 4, 8192, 1024)):
+        assert plan(so, B=B, q_len=q_len, width=width, window=window)["gang"] > 0, (B, q_len, width, window)
+
+
 def test_verification_takes_no_more_blocks_than_a_vocabulary_has_work_for(so):
     for V in (1, 500, 2047, 2048, 8192, 160_000, (1 << 20) - 1):
         for B in (1, 16, 76, 77, 152, 153, 400, 5000):
