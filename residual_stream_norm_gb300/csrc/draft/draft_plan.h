@@ -114,16 +114,18 @@ inline Kv4AttnPlan kv4_attn_plan(int32_t B, int32_t q_len, int32_t n_q, int32_t 
 
 constexpr int kVerifyWarps = 8;  // of a block
 
-// Blocks of a sequence: 8 while each warp's stretch has 128 tokens, and fewer where not all blocks have room at a time
-// (4 an SM; 128 rows of 160,000: 35.8 us with 8, 34.9 with 4, 53 with 2), but then no block gets more than 16,000
-// tokens (400 of 160,000: 73 us with 4, 105 with 1; 1000 of 32,000: 46 us with 2, 57 with 4, 49 with 1; of 8000: 20
-// with 1, 44 with 4).
+// Blocks of a sequence: 8 while each warp's stretch has 128 tokens.  Where not all blocks have room at a time (4 an SM)
+// at most 4, and fewer while a block has less than 16,000 tokens, so that none gets more than 32,000 for it (128 rows of
+// 160,000: 35.8 us with 8, 34.9 with 4, 53 with 2; 400 of 160,000: 73 with 4, 105 with 1; 1000 of 32,000: 57 with 4, 46
+// with 2, 49 with 1; of 8000: 44 with 4, 20 with 1).  And as many as a grid holds.
 inline int verify_ranks(int64_t B, int64_t V)
 {
     int ranks = 8;
     while (ranks > 1 && V < (int64_t)ranks * kVerifyWarps * 128)
         ranks /= 2;
     while (ranks > 1 && B * ranks > 152 * 4 && (ranks == 8 || V < (int64_t)ranks * 16000))
+        ranks /= 2;
+    while (ranks > 1 && B * ranks > 0x7fffffff)
         ranks /= 2;
     return ranks;
 }

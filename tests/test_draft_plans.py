@@ -87,3 +87,10 @@ def test_verification_takes_no_more_blocks_than_a_vocabulary_has_work_for(so):
         for B in (1, 16, 76, 77, 152, 153, 400, 5000):
             r = so.ranks(B, V)
             assert r in (1, 2, 4, 8) and (r == 1 or V >= r * 8 * 128)
+
+
+def test_verification_of_the_most_sequences_fits_a_grid(so):
+    # sequences may share their distributions (strides of 0), so there may be as many as the check lets through
+    for V in (1, 2048, 9000, 64_000, (1 << 20) - 1):
+        for B in ((1 << 28) + 1, 1 << 29, (1 << 30) + 152, (1 << 31) - 1):
+            assert B * so.ranks(B, V) <= (1 << 31) - 1, (B, V)
