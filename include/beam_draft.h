@@ -105,8 +105,8 @@ BEAM_API int64_t beam_attn_kv4_workspace(int32_t B, int32_t q_len, int32_t n_q_h
  * (the others are another rank's), with F their intermediate columns on this rank: for expert- and
  * tensor-parallel shares `out` is a partial sum for beam_allreduce_boundary_fwd, for the whole layer it
  * goes to beam_boundary_fwd.  A token none of whose experts is in the range gives a row of zeros.
- * A token with a NaN in x, or whose largest |x| times the largest |router_w| of an expert reaches 2^120, may give any
- * experts and NaN, and does not touch the other tokens' rows.
+ * A token with a NaN in x, or whose largest |x| times the largest |router_w| of an expert reaches 2^113 (the sum may pass
+ * FP32's range), may give any experts and NaN, and does not touch the other tokens' rows.
  *
  *   x, out [T, H] bf16, rows *_row_stride elements apart (>= H, multiples of 8; 16-byte aligned)
  *   router_w [256, H] fp32 (16-byte aligned), router_bias [256] fp32 (16-byte aligned)

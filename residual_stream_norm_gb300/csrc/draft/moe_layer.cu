@@ -137,7 +137,7 @@ __global__ void __launch_bounds__(kThreads, 2)
             float seed[2];
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                const float bound = __fmul_rn(__fmul_rn(mx, 32.0f), mw[e]);
+                const float bound = __fmul_rn(__fmul_rn(mx, mw[e]), 32.0f);  // (mx may be near FP32's end)
                 seed[e] = __fmul_rn(
                     __uint_as_float(max(__float_as_uint(bound) & 0x7f800000u, 0x01000000u)), 6.0f);
             }
