@@ -60,7 +60,7 @@ BEAM_API int beam_kv4_write_fwd(void *k_cache, void *v_cache, void *k_scales, vo
  * h / (n_q_heads / n_kv_heads) and the keys and values k_j, v_j that the codes stand for:
  *   s_j = sm_scale * <q, k_j>    lse = log(sum_j exp(s_j))    out = bf16(sum_j exp(s_j - lse) v_j)
  * A row that sees nothing gives out = 0 and lse = -inf.  Nothing of a key reaches a row that does not
- * see it, whatever it holds.  <q, k_j> is formed per group as scale * sum q c + minimum * sum q with FP32
+ * see it, whatever it holds; NaN in a key that it sees shows, whatever its weight.  <q, k_j> is formed per group as scale * sum q c + minimum * sum q with FP32
  * sums; products q c are exact: the query row is taken in FP16 after an exact scaling by a power of two (at
  * most 2^60) to [2^14, 2^15), so that only elements 2^-27 below the row's largest (or below 2^-74) lose
  * bits.  Maxima, sums and outputs are FP32.  The products exp(s_j - max) * scale that multiply the values'

@@ -426,6 +426,7 @@ __device__ __forceinline__ void take_tile(Unit<NT, NG> &u, const Kv4AttnArgs &a,
     // ---- what a row does not see; the largest of the values' scales --------------------------------
     // (not of NaN and infinite ones, which show in the output)
     int e_new[NT][2];
+    uint32_t sees = 0u;  // of this thread's scores; not used where all are seen
     if (plain) {
         uint32_t w[NG];
         lds_scales<NG>(w, vsb + lane * 4 * NG);
@@ -461,6 +462,7 @@ __device__ __forceinline__ void take_tile(Unit<NT, NG> &u, const Kv4AttnArgs &a,
                                           (a.window == 0 || p - pos < a.window || pos < a.n_sink);
                         float &x = s[nt][mt][e + 2 * h];
                         x = seen ? x : ninf;
+                        sees |= seen ? 1u << (nt * 8 + mt * 4 + e + 2 * h) : 0u;
                         uint32_t w[NG];
                         lds_scales<NG>(w, vsb + key * 4 * NG);
 #pragma unroll
@@ -561,13 +563,13 @@ __device__ __forceinline__ void take_tile(Unit<NT, NG> &u, const Kv4AttnArgs &a,
                     }
                 } else {
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {  // a key that is not seen leaves nothing, whatever it holds
-                        w[i] = p[i] == 0.0f
-                                   ? 0.0f
-                                   : p[i] * (bf_lo(sc[i >> 1][j]) * pow2i(15 - u.e[nt][i & 1]));
-                        u.omin[nt][i & 1][j] = p[i] == 0.0f ? u.omin[nt][i & 1][j]
-                                                            : __fmaf_rn(p[i], vm[i >> 1],
-                                                                        u.omin[nt][i & 1][j]);
+                    for (int i = 0; i < 4; ++i) {
+                        // a key that is not seen leaves nothing, whatever it holds; NaN in one that is seen shows, also
+                        // where its weight is 0 in FP32
+                        const bool seen = (sees >> (nt * 8 + mt * 4 + i)) & 1u;
+                        w[i] = seen ? p[i] * (bf_lo(sc[i >> 1][j]) * pow2i(15 - u.e[nt][i & 1])) : 0.0f;
+                        u.omin[nt][i & 1][j] = seen ? __fmaf_rn(p[i], vm[i >> 1], u.omin[nt][i & 1][j])
+                                                    : u.omin[nt][i & 1][j];
                     }
                 }
                 b[nt][mt][j][0] = movmatrix_trans(pack_f16x2(w[0], w[1]));
@@ -917,7 +919,7 @@ __global__ void __launch_bounds__(warps_of(NT, NG) * 32, 1) kv4_attn_kernel(cons
 #pragma unroll 1
             for (int p = 0; p < (int)gang; ++p) {
                 const float fp = __shfl_sync(0xffffffffu, f, p);
-                if (fp == 0.0f)
+                if (__shfl_sync(0xffffffffu, part.y, p) == 0.0f)  // an empty part, whose sums need not be there
                     continue;
                 const float4 x = *reinterpret_cast<const float4 *>(first + p * warp_bytes(NT, NG) + r * 512 +
                                                                    lane * 16);
