@@ -47,6 +47,7 @@ using kv4::warps_of;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr int kMinExp = -100;
+constexpr int kReach = 7;
 
 struct Sizes {
     int32_t heads, R, rtiles;
@@ -232,7 +233,8 @@ struct Unit {
     // (of more than one row tile in shared memory too, behind the query: [1 + NG][NT * 8])
     float fac[2], qsum[2][NG];
     float m[NT][2], l[NT][2], omin[NT][2][NG];  // of the scaled scores
-    int e[NT][2];            // scales seen are below 2^e
+    int e[NT][2];            // scales seen are below 2^e, the largest of them by no more than 2^(kReach + 1)
+    uint32_t raised;         // a bit for each row whose e may be more than its own scales ask for
     bool one_e;              // the same one for all rows
     uint32_t tmem;           // the output: 8 columns for each (chunk, row tile), [2][4] of a product's places
 };
@@ -326,6 +328,7 @@ __device__ __forceinline__ void begin_unit(Unit<NT, NG> &u, const Kv4AttnArgs &a
             u.e[nt][e] = kMinExp;
         }
     }
+    u.raised = 0u;
     u.one_e = true;
     __syncwarp();
 #pragma unroll
@@ -474,18 +477,23 @@ __device__ __forceinline__ void take_tile(Unit<NT, NG> &u, const Kv4AttnArgs &a,
 #pragma unroll
                 for (int off = 4; off < 32; off <<= 1)
                     top = max(top, __shfl_xor_sync(0xffffffffu, top, off));
-                e_new[nt][e] = max(u.e[nt][e], (top >> 7) - 126);
-                highest = max(highest, e_new[nt][e]);
+                // what the row's own scales ask for, at least
+                e_new[nt][e] = max(u.e[nt][e] - ((u.raised >> (nt * 2 + e)) & 1u ? kReach : 0), (top >> 7) - 126);
+                highest = max(highest, max(u.e[nt][e], e_new[nt][e]));
             }
-        // rows whose largest scales are no more than 2^8 apart go by the largest: they have 2^40 in hand
+        // Rows go by the largest of all rows' where that is no more than kReach above what their own scales ask for: a
+        // weight has 2^40 in hand, half a step of FP16's smallest being 2^-25 and weights scaled up to 2^15.  (By
+        // another row's scales alone an e could rise tile by tile.)
         highest = __reduce_max_sync(0xffffffffu, highest);
         bool one = true;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                if (pad[nt][e] || highest - e_new[nt][e] <= 8)
-                    e_new[nt][e] = highest;
+                const int least = e_new[nt][e];
+                e_new[nt][e] = pad[nt][e] || highest - least <= kReach ? highest : max(u.e[nt][e], least);
+                const uint32_t bit = 1u << (nt * 2 + e);
+                u.raised = e_new[nt][e] > least ? u.raised | bit : u.raised & ~bit;
                 one = one && e_new[nt][e] == highest;
             }
         u.one_e = __all_sync(0xffffffffu, one);

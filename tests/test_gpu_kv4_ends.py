@@ -3,6 +3,7 @@
 import pytest
 import torch
 
+from tests import _draft_ref as ref
 from tests._gpu import lib
 from tests.test_gpu_kv4 import check, make, run
 
@@ -36,3 +37,27 @@ def test_a_seen_key_that_holds_nan_shows_whatever_its_weight(n, what):
         got, z = run(d, sm_scale=1.0)
         assert bool(torch.isnan(got).all()), place
         assert torch.equal(z, lse)
+
+
+@pytest.mark.parametrize("n", [1000, 2000])
+@pytest.mark.parametrize("group", [32, 128])
+def test_scales_that_other_rows_see_do_not_cost_bits(n, group):
+    # 24 query tokens behind a window: the first ones see 23 keys that the last does not, whose values' scales rise from
+    # tile to tile (2^7 and 2^15 beside 1), and share tiles with keys that all see.  The last row's weights of all keys but
+    # one are 2^-25, and that one's value is 0: what they add up to is all of the output.  The batch is so large that a
+    # warp takes all of a sequence's tiles in turn.
+    lib()
+    B, q_len, n_sink, window = 1800, 24, 16, n - 50
+    c = make(B, q_len, 1, 1, [n] * B, group, seed=n, S=n)
+    c["table"][0] = torch.randperm(n, generator=torch.Generator().manual_seed(n))
+    scores(c, 0, [n - 1 - window // 2], 17.34)
+    at, lo = c["table"][0], n - q_len + 1 - window          # lo: first key behind the sinks that the first row sees
+    c["v_scales"][at] = torch.tensor([1.0, 0.0]).bfloat16()
+    c["v_scales"][at[lo:lo + 16], :, :, 0] = 2.0 ** 7
+    c["v_scales"][at[lo + 16:lo + 23], :, :, 0] = 2.0 ** 15
+    c["v_cache"][at[n - 1 - window // 2]] = 0
+    out, _ = run(c, window, n_sink, sm_scale=1.0)
+    (want, _), (tol, _) = ref.kv4_attention(c["q"][:q_len], c["k_cache"], c["v_cache"], c["k_scales"], c["v_scales"],
+                                            c["table"][:1], c["lens"][:1], q_len, 1.0, window, n_sink)
+    d = (out[:q_len].double() - want).abs()
+    assert bool((d <= tol).all()), f"worst {float((d / tol).max()):.3g} of the bound"
