@@ -65,7 +65,9 @@ BEAM_API int beam_kv4_write_fwd(void *k_cache, void *v_cache, void *k_scales, vo
  * most 2^60) to [2^14, 2^15), so that only elements 2^-27 below the row's largest (or below 2^-74) lose
  * bits.  Maxima, sums and outputs are FP32.  The products exp(s_j - max) * scale that multiply the values'
  * codes are rounded to FP16, scaled up by a power of two: an error of at most 2^-11 of each and of 2^-32 of
- * the largest scale that the row has seen; minima are added in FP32.
+ * the largest scale that the row has seen (of 2^-100 if that is less); minima are added in FP32.
+ * A row whose largest |q| times |sm_scale| reaches 2^117, or whose keys' |v_j| add up to more than FP32 holds (sums are
+ * formed before their division), may give infinities and NaN; other rows are as they are.
  * Results do not depend on the order in which blocks run.
  *
  *   out, q [B*q_len, n_q_heads, 128] bf16, rows *_row_stride elements apart (>= n_q_heads*128, multiples

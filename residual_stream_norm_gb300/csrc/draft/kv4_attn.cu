@@ -661,7 +661,7 @@ __device__ __forceinline__ void end_unit(Unit<NT, NG> &u, const Kv4AttnArgs &a, 
             const int in_tile = nt * 8 + 2 * t + e, r = r0 + in_tile;
             const bool none = l == 0.0f;
             const float inv = whole ? __fdiv_rn(1.0f, l) : 1.0f;
-            const float back = pow2i(u.e[nt][e]);  // and 2^(24 - 15): codes' unit over weights' scaling
+            const float back = pow2i(u.e[nt][e] - 1);  // (e: up to 128) and 2^(1 + 24 - 15): codes' unit over weights'
             const int i = r / z.heads, head = kv * z.heads + r - i * z.heads;
             const int64_t row = (int64_t)at.b * a.q_len + i;
             uint16_t *out = (uint16_t *)a.out + row * a.out_stride + head * 128 + 4 * g;
@@ -672,7 +672,7 @@ __device__ __forceinline__ void end_unit(Unit<NT, NG> &u, const Kv4AttnArgs &a, 
                     float d[4];
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
-                        const float x = o[c][(j >> 1) * 4 + e + 2 * (j & 1)] * (j & 1 ? 32.0f : 512.0f);
+                        const float x = o[c][(j >> 1) * 4 + e + 2 * (j & 1)] * (j & 1 ? 64.0f : 1024.0f);
                         d[j] = none ? 0.0f : __fmaf_rn(x, back, om[c * NG / 4]) * inv;
                     }
                     if (whole)

@@ -61,3 +61,33 @@ def test_scales_that_other_rows_see_do_not_cost_bits(n, group):
                                             c["table"][:1], c["lens"][:1], q_len, 1.0, window, n_sink)
     d = (out[:q_len].double() - want).abs()
     assert bool((d <= tol).all()), f"worst {float((d / tol).max()):.3g} of the bound"
+
+
+@pytest.mark.parametrize("n", [1, 64, 3000])
+@pytest.mark.parametrize("group", [32, 64, 128])
+def test_largest_scales_of_values(n, group):
+    # one key with scales from 2^127 on, whose exponent is FP32's last, codes 0 and 1 beside a minimum of -2^126
+    lib()
+    c = make(1, 1, 6, 1, [n], group, seed=n + group)
+    c["v_cache"] &= 0x11
+    big = c["table"][0, n // 2]
+    for far, score in ((2.0 ** 127 * 1.25, 30.0), (2.0 ** 127, 0.0)):
+        scores(c, 0, [n // 2], score)
+        c["v_scales"][..., 0], c["v_scales"][..., 1] = 1.0, 0.5
+        c["v_scales"][big, ..., 0], c["v_scales"][big, ..., 1] = far, -(2.0 ** 126)
+        check(c, sm_scale=1.0)
+
+
+def test_largest_queries():
+    # |q| |sm_scale| just below 2^117 beside keys so small that scores are ordinary; the other row has NaN from infinite ones
+    lib()
+    c = make(2, 2, 6, 1, [70, 150], 64, seed=1)
+    c["q"] = (c["q"].float().clamp(-3.9, 3.9) * 2.0 ** 115).bfloat16()
+    c["k_scales"] = (c["k_scales"].float() * 2.0 ** -118).bfloat16()
+    clean, lse = check(c, sm_scale=0.5)
+    c["q"][1, 2, 5] = float("inf")
+    out, z = run(c, sm_scale=0.5)
+    assert bool(torch.isnan(out[1, 2]).all()) and bool(torch.isnan(z[1, 2]))
+    keep = torch.ones((4, 6), dtype=torch.bool)
+    keep[1, 2] = False
+    assert torch.equal(out[keep], clean[keep]) and torch.equal(z[keep], lse[keep])
