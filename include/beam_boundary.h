@@ -30,7 +30,9 @@
  *    parameters (norm weights w_post / w_pre / wq / wk, the gate bias) before waiting for that
  *    kernel; every other input is read, and every output written, only after the preceding
  *    kernel has completed.  So the norm weights and the gate bias must not be written by the
- *    kernel launched immediately before on the same stream.
+ *    kernel launched immediately before on the same stream, nor by one further ahead that lets its
+ *    successor start before its writes, if only kernels of this library stand between: they let
+ *    their own successors start before they wait.
  */
 #ifndef BEAM_BOUNDARY_H
 #define BEAM_BOUNDARY_H

@@ -7,8 +7,8 @@
  * The conventions of beam_boundary.h hold here too: device pointers on the current device, buffers
  * owned by the caller, no allocation and no synchronisation, every argument checked before anything
  * is launched, calls asynchronous on `stream`, programmatic dependent launch.  Model parameters
- * (4-bit weights, scales, zeros) may be read before the preceding kernel of the stream has ended;
- * everything else is read, and every output written, only after it.  Calls on different streams
+ * (4-bit weights, scales, zeros) may be read before earlier kernels of the stream have ended (see
+ * beam_boundary.h); everything else is read, and every output written, only after them.  Calls on different streams
  * need workspaces of their own.  Waits inside the kernels are bounded, but for attention's for tensor
  * memory (asked for behind the earlier kernels of the stream, and never held while a kernel waits for
  * another); beam_device_faults() also reports one that ran out, or a block that found its shared

@@ -7,8 +7,9 @@
  * The conventions of beam_boundary.h and beam_decode.h hold here too: device pointers on the current
  * device, buffers owned by the caller, no allocation and no synchronisation, every argument checked
  * before anything is launched, calls asynchronous on `stream`, programmatic dependent launch.  The
- * router's weights and bias may be read before the preceding kernel of the stream has ended; everything else is
- * read, and every output written, only after it.  Calls on different streams need workspaces of their
+ * router's weights and bias may be read before earlier kernels of the stream have ended (more than one of them:
+ * kernels here let the next one start before they wait themselves); everything else is read, and every output
+ * written, only after them.  Calls on different streams need workspaces of their
  * own; a workspace's contents need not be kept or cleared between calls.  A kernel here waits for its own block's or
  * cluster's threads and copies, and attention's, behind the earlier kernels of its stream, for tensor memory, until other
  * streams' kernels on its SM give theirs back.  None holds tensor memory while it waits for another kernel.
@@ -108,7 +109,8 @@ BEAM_API int64_t beam_attn_kv4_workspace(int32_t B, int32_t q_len, int32_t n_q_h
  * tensor-parallel shares `out` is a partial sum for beam_allreduce_boundary_fwd, for the whole layer it
  * goes to beam_boundary_fwd.  A token none of whose experts is in the range gives a row of zeros.
  * A token with a NaN in x, or whose largest |x| times the largest |router_w| of an expert reaches 2^113 (the sum may pass
- * FP32's range), may give any experts and NaN, and does not touch the other tokens' rows.
+ * FP32's range), may give any experts and NaN, and does not touch the other tokens' rows; so does one
+ * with an activation a beyond BF16's range, which gives NaN.
  *
  *   x, out [T, H] bf16, rows *_row_stride elements apart (>= H, multiples of 8; 16-byte aligned)
  *   router_w [256, H] fp32 (16-byte aligned), router_bias [256] fp32 (16-byte aligned)
