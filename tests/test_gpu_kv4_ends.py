@@ -5,7 +5,7 @@ import torch
 
 from tests import _draft_ref as ref
 from tests._gpu import lib
-from tests.test_gpu_kv4 import check, make, run
+from tests.test_gpu_kv4 import check, check_write, make, run
 
 pytestmark = pytest.mark.gpu
 NAN = float("nan")
@@ -91,3 +91,14 @@ def test_largest_queries():
     keep = torch.ones((4, 6), dtype=torch.bool)
     keep[1, 2] = False
     assert torch.equal(out[keep], clean[keep]) and torch.equal(z[keep], lse[keep])
+
+
+@pytest.mark.parametrize("group", [32, 64, 128])
+def test_write_of_any_bits(group):
+    # all exponents in one group, and groups whose values are close to one another
+    lib()
+    g = torch.Generator().manual_seed(group)
+    k = torch.randint(-1 << 15, 1 << 15, (150, 2, 128), generator=g, dtype=torch.int16)
+    v = torch.randint(0, 1 << 15, (150, 2, 1), generator=g, dtype=torch.int16)
+    v = v + torch.randint(0, 40, (150, 2, 128), generator=g, dtype=torch.int16)
+    check_write(k.view(torch.bfloat16), v.view(torch.bfloat16), torch.randperm(200, generator=g)[:150], 200, group)
