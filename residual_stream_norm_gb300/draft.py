@@ -36,6 +36,11 @@ def declare(so: ctypes.CDLL) -> None:
     so.beam_draft_verify_fwd.restype = ctypes.c_int
 
 
+def _int(x, bits: int = 32):
+    """x, or -1, which every size here refuses, where the C type cannot hold it (ctypes would cut it off)."""
+    return x if -1 << bits - 1 <= x < 1 << bits - 1 else -1
+
+
 # As in decode.py: good arguments cost one expression; only when it fails do the checks find out what to say.
 
 def _cache_good(k_cache, v_cache, k_scales, v_scales, dev, groups):
@@ -95,7 +100,8 @@ def beam_attn_kv4_workspace(B: int, q_len: int, n_q_heads: int, n_kv_heads: int,
                             window: int = 0, n_sink: int = 0) -> int:
     """Bytes of workspace ``beam_attn_kv4_fwd`` needs for these sizes (host only)."""
     from . import BeamError, lib
-    n = lib().beam_attn_kv4_workspace(B, q_len, n_q_heads, n_kv_heads, table_width, window, n_sink)
+    n = lib().beam_attn_kv4_workspace(_int(B), _int(q_len), _int(n_q_heads), _int(n_kv_heads), _int(table_width, 64),
+                                      _int(window, 64), _int(n_sink, 64))
     if n < 0:
         raise BeamError("beam_attn_kv4_workspace", n)
     return n
@@ -144,14 +150,14 @@ def beam_attn_kv4_fwd(out, q, k_cache, v_cache, k_scales, v_scales, slot_table, 
          None if lse_out is None else lse_out.data_ptr(), q.data_ptr(), q_stride, k_cache.data_ptr(),
          v_cache.data_ptr(), k_scales.data_ptr(), v_scales.data_ptr(), S, group, slot_table.data_ptr(),
          slot_table.stride(0) if B > 1 else N, N, seq_len.data_ptr(), B, T // B if B else 1, nq, n_kv,
-         HEAD_DIM, _SM_SCALE if sm_scale is None else sm_scale, window, n_sink, workspace.data_ptr(),
-         workspace.nbytes)
+         HEAD_DIM, _SM_SCALE if sm_scale is None else sm_scale, _int(window, 64), _int(n_sink, 64),
+         workspace.data_ptr(), workspace.nbytes)
 
 
 def beam_moe_layer_workspace(T: int, H: int, F: int, n_local: int = EXPERTS) -> int:
     """Bytes of workspace ``beam_moe_layer_fwd`` needs for these sizes (host only)."""
     from . import BeamError, lib
-    n = lib().beam_moe_layer_workspace(T, H, F, n_local)
+    n = lib().beam_moe_layer_workspace(_int(T, 64), _int(H), _int(F), _int(n_local))
     if n < 0:
         raise BeamError("beam_moe_layer_workspace", n)
     return n
@@ -213,7 +219,7 @@ def beam_moe_layer_fwd(out, x, router_w, router_bias, w_gate_up, w_down, workspa
          None if topk_ids_out is None else topk_ids_out.data_ptr(),
          None if topk_w_out is None else topk_w_out.data_ptr(), x.data_ptr(),
          x.stride(0) if T > 1 else H, router_w.data_ptr(), router_bias.data_ptr(), w_gate_up.data_ptr(),
-         w_down.data_ptr(), first_expert, n_local, routed_scaling, T, H, F, workspace.data_ptr(),
+         w_down.data_ptr(), _int(first_expert), n_local, routed_scaling, T, H, F, workspace.data_ptr(),
          workspace.nbytes)
 
 

@@ -195,3 +195,21 @@ def test_python_refuses_what_does_not_fit(lib):
                                bf(256, 64, 16), u8(100))
     with pytest.raises(TypeError):
         rsn.beam_draft_verify_fwd(i64, n, i64[:, :3], torch.zeros(1, 4, 9), None, f32[:, :3], f32[0, :1])
+
+
+@pytest.mark.parametrize("bad", [1 << 32, (1 << 32) + 1, -(1 << 32) + 1, (1 << 64) + 1])
+def test_sizes_that_the_c_types_cannot_hold(lib, bad):
+    # ctypes would cut them off to 0 or 1
+    for i in range(4):
+        sizes = [1, 1, 8, 8, 10]
+        sizes[i] = bad
+        with pytest.raises(rsn.BeamError):
+            rsn.beam_attn_kv4_workspace(*sizes)
+    for kw in (dict(window=(1 << 64) + 5), dict(n_sink=1 << 64), dict(table_width=(1 << 64) + 3)):
+        with pytest.raises(rsn.BeamError):
+            rsn.beam_attn_kv4_workspace(**{**dict(B=1, q_len=1, n_q_heads=8, n_kv_heads=8, table_width=10), **kw})
+    for i in range(1, 4):
+        sizes = [4, 64, 16, 256]
+        sizes[i] = bad * 8
+        with pytest.raises(rsn.BeamError):
+            rsn.beam_moe_layer_workspace(*sizes)

@@ -3,6 +3,7 @@ GB300)."""
 import pytest
 import torch
 
+import residual_stream_norm_gb300 as rsn
 from tests._gpu import lib
 from tests.test_gpu_moe_layer import check, make, run
 
@@ -77,3 +78,11 @@ def test_activations_past_the_range_of_bf16(T):
     got, _, _ = run(c)
     assert torch.equal(got[[0, 1] + list(range(3, T))], plain[[0, 1] + list(range(3, T))])
     assert bool(torch.isnan(got[2]).all())
+
+
+def test_first_experts_that_the_c_type_cannot_hold():
+    lib()
+    c = make(3, 64, 16, 0, 8, seed=1)
+    for first in (1 << 32, (1 << 32) + 5, -(1 << 32), 1 << 64):
+        with pytest.raises(rsn.BeamError):
+            run({**c, "first": first})
