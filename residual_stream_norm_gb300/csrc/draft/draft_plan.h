@@ -85,8 +85,8 @@ inline Kv4AttnPlan kv4_attn_plan(int32_t B, int32_t q_len, int32_t n_q, int32_t 
     //   128 sequences, 500 keys   26.3 33.5; 23.2 29.3; 22.6 13.2     1000   40.3 46.7; 38.9 36.4; 36.5 16.0
     //   1000 sequences, 200 keys  85.8 91.3; 60.3 76.1; 31.0 42.4
     //   19 of 4 tokens, 2000 keys 29.4 38.7; 29.8 34.3; 27.1 23.5     4000   44.7 52.9; 47.0 41.7; 40.8 32.7
-    // and of one sequence of 100 keys 6.8 10.1, of 500 8.9 10.3, of 1000 11.1 11.2; 8 of 1000 11.4 12.7, of 2000 15.4
-    // 16.9, of 4000 24.0 22.6; behind a window of 512 128 sequences 29.6 35.8, of 1024 300 sequences 72 89, of 2048 50
+    // and of one sequence of 500 keys 9.3 10.8, of 1000 11.4 10.6, of 2000 15.2 10.9; 8 of 1000 11.9 13.3, of 2000 15.9
+    // 17.1, of 4000 22.6 20.7; behind a window of 512 128 sequences 29.6 35.8, of 1024 300 sequences 72 89, of 2048 50
     // sequences 34.9 39.5, 100 62 57, 128 72.8 67.0.
     const double units = (double)B * team;
     const int64_t unit_tiles = (most + kTile - 1) / kTile;

@@ -23,8 +23,8 @@
 // times their bytes: 365 us, and 301 so).  A unit that is cut between teams leaves parts (FP32 maximum, sum, output) that
 // a second kernel joins in order; short ones are taken whole (see draft_plan.h).
 //
-// What bounds it: instructions and their latency (8 contexts of 100K keys in groups of 128: 137 us for 720 MB, 0.78 of
-// the measured copy rate, in groups of 32 184 us for 847 MB; 24 rows of 32 sequences in groups of 64 161 us for 371 MB at
+// What bounds it: instructions and their latency (8 contexts of 100K keys in groups of 128: 138 us for 720 MB, 0.77 of
+// the measured copy rate, in groups of 32 186 us for 847 MB; 24 rows of 32 sequences in groups of 64 163 us for 371 MB at
 // about 1,100 instructions a tile).
 
 #include <cuda_fp16.h>
