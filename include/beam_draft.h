@@ -109,8 +109,8 @@ BEAM_API int64_t beam_attn_kv4_workspace(int32_t B, int32_t q_len, int32_t n_q_h
  * tensor-parallel shares `out` is a partial sum for beam_allreduce_boundary_fwd, for the whole layer it
  * goes to beam_boundary_fwd.  A token none of whose experts is in the range gives a row of zeros.
  * A token with a NaN in x, or whose largest |x| times the largest |router_w| of an expert reaches 2^113 (the sum may pass
- * FP32's range), may give any experts and NaN, and does not touch the other tokens' rows; so does one
- * with an activation a beyond BF16's range, which gives NaN.
+ * FP32's range), may give any experts and NaN, and does not touch the other tokens' rows.  The
+ * same holds for a token with an activation a beyond BF16's range, which gives NaN.
  *
  *   x, out [T, H] bf16, rows *_row_stride elements apart (>= H, multiples of 8; 16-byte aligned)
  *   router_w [256, H] fp32 (16-byte aligned), router_bias [256] fp32 (16-byte aligned)
